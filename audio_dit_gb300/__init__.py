@@ -22,7 +22,9 @@ __all__ = [
     "MAX_SEGMENTS", "library_path", "load_library", "h3fp4_codes_bytes", "h3fp4_sf_bytes",
     "h3fp4_workspace_bytes", "h3fp4_quantize_weight", "h3fp4_quantize_act", "h3fp4_linear",
     "h3fp4_check", "h3fp4_act_amax", "h3fp4_gscale_from_amax", "h3fp4_selftest_timeout", "h3fp4_measure_fp4_peak", "h3fp4_measure_fp4_pair_peak", "h3fp4_measure_fp4_form", "MMA_FORMS", "h3fp4_quantize_act_noalloc",
-    "h3fp4_linear_swiglu_nvfp4", "h3fp4_set_wait_limit_ns", "h3fp4_status_string", "alloc_nvfp4", "alloc_workspace",
+    "h3fp4_linear_swiglu_nvfp4", "h3fp4_qk_norm_rope", "h3fp4_cross_attn", "h3fp4_shared_attn",
+    "h3fp4_attn_workspace_bytes", "alloc_attn_workspace", "ROPE_PAIRS", "ATTN_MAX_SEGMENTS",
+    "h3fp4_set_wait_limit_ns", "h3fp4_status_string", "alloc_nvfp4", "alloc_workspace",
 ]
 
 PROLOGUE_MOD = 1
@@ -33,7 +35,9 @@ A_PREQUANT = 32
 EPI_SWIGLU = 64
 EPI_AMAX = 128
 FUSED_QUANT = 256
+ROPE_PAIRS = 512
 MAX_SEGMENTS = 8
+ATTN_MAX_SEGMENTS = 256
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 _lib = None
@@ -43,6 +47,11 @@ class H3FP4Error(RuntimeError):
     def __init__(self, status: int, what: str):
         self.status = status
         super().__init__(f"{what}: h3fp4 status {status} ({h3fp4_status_string(status)})")
+
+
+class _Heads(C.Structure):
+    """h3fp4_heads: a strided bf16 [rows][heads][D] tensor."""
+    _fields_ = [("ptr", C.c_void_p), ("row_stride", C.c_int64), ("head_stride", C.c_int64)]
 
 
 def library_path() -> str:
@@ -58,7 +67,7 @@ def load_library():
     if not os.path.exists(path):
         raise ImportError(f"libh3fp4.so not built ({path}); run `python -m audio_dit_gb300.build`")
     L = C.CDLL(path)
-    i64, vp, i32, sz = C.c_int64, C.c_void_p, C.c_int, C.c_size_t
+    i64, vp, i32, sz, hp = C.c_int64, C.c_void_p, C.c_int, C.c_size_t, C.POINTER(_Heads)
     sig = {
         "h3fp4_codes_bytes": (sz, [i64, i64]),
         "h3fp4_sf_bytes": (sz, [i64, i64]),
@@ -78,6 +87,13 @@ def load_library():
         "h3fp4_measure_fp4_pair_peak": (i32, [i32, vp, vp]),
         "h3fp4_measure_fp4_form": (i32, [i32, i32, vp, vp]),
         "h3fp4_quantize_act_noalloc": (i32, [vp, i64, i64, vp, vp, vp, i32, vp, vp, vp, i32, vp]),
+        "h3fp4_qk_norm_rope": (i32, [hp, hp, i64, i32, i32, i32, vp, vp, vp, vp, i32, vp, i32, C.c_float, hp, hp, i32,
+                                     vp]),
+        "h3fp4_cross_attn": (i32, [hp, hp, hp, i64, i64, i32, i32, i32, vp, vp, i32, vp, C.c_float, hp, vp, vp, sz,
+                                   vp]),
+        "h3fp4_shared_attn": (i32, [hp, hp, hp, hp, hp, i64, i64, i64, i32, i32, i32, vp, vp, i32, vp, vp, C.c_float,
+                                    hp, vp, vp, sz, vp]),
+        "h3fp4_attn_workspace_bytes": (sz, [i64, i64, i64, i32, i32, i32, vp, vp, i32]),
         "h3fp4_check": (i32, [vp, vp]),
         "h3fp4_set_wait_limit_ns": (None, [C.c_uint64]),
         "h3fp4_status_string": (C.c_char_p, [i32]),
@@ -104,6 +120,56 @@ def _ptr(t: Optional[torch.Tensor], what: str, dtype=None):
     if dtype is not None and t.dtype != dtype:
         raise TypeError(f"{what} must be {dtype}, got {t.dtype}")
     return t.data_ptr()
+
+
+def _heads(t: Optional[torch.Tensor], what: str, shape):
+    """(h3fp4_heads of a bf16 [rows, heads, D] view, or None).  Any row and head
+    strides; the elements of a head are contiguous."""
+    if t is None:
+        return None
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{what} must be a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{what} must be a CUDA tensor")
+    if t.dtype != torch.bfloat16:
+        raise TypeError(f"{what} must be {torch.bfloat16}, got {t.dtype}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{what} must be {list(shape)}, got {list(t.shape)}")
+    rows, heads, d = t.shape
+    if d > 1 and t.stride(2) != 1:
+        raise ValueError(f"{what}: the last dimension must be contiguous")
+    # the stride of a dimension of one element says nothing about the memory
+    head = t.stride(1) if heads > 1 else d
+    row = t.stride(0) if rows > 1 else heads * head
+    return C.byref(_Heads(t.data_ptr(), row, head))
+
+
+def _mask(t: Optional[torch.Tensor], what: str, n: int):
+    if t is None:
+        return None
+    if isinstance(t, torch.Tensor) and t.dtype == torch.bool:
+        t = t.view(torch.uint8)
+    p = _ptr(t, what, torch.uint8)
+    if t.numel() != n:
+        raise ValueError(f"{what} must have {n} elements, got {t.numel()}")
+    return p
+
+
+def _f32(t: Optional[torch.Tensor], what: str, shape):
+    p = _ptr(t, what, torch.float32)
+    if t is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{what} must be {list(shape)}, got {list(t.shape)}")
+    return p
+
+
+def _seg_pair(q_off, kv_off):
+    if (q_off is None) != (kv_off is None):
+        raise ValueError("q_off and kv_off go together")
+    if q_off is not None and len(q_off) != len(kv_off):
+        raise ValueError(f"q_off and kv_off must have the same length, got {len(q_off)} and {len(kv_off)}")
+    qp, nseg, keep_q = _segs(q_off)
+    kp, _, keep_k = _segs(kv_off)
+    return qp, kp, nseg, (keep_q, keep_k)
 
 
 def _stream(stream) -> Optional[int]:
@@ -315,6 +381,77 @@ def h3fp4_measure_fp4_form(ws: torch.Tensor, form: int, iters: int = 20000) -> f
     return float(out.value)
 
 
+def h3fp4_qk_norm_rope(q: torch.Tensor, k: Optional[torch.Tensor], q_out: torch.Tensor,
+                       k_out: Optional[torch.Tensor], *, q_weight: Optional[torch.Tensor] = None,
+                       k_weight: Optional[torch.Tensor] = None, cos: Optional[torch.Tensor] = None,
+                       sin: Optional[torch.Tensor] = None, interleaved: bool = False,
+                       seg_off: Optional[Sequence[int]] = None, eps: float = 1e-6, stream=None) -> None:
+    """Per-head RMS norm and rotation of Q [M, Hq, D] and K [M, Hk, D] (bf16, any
+    row and head strides; ``k`` and ``k_out`` may be None) in one pass.
+
+    ``q_weight`` / ``k_weight``: fp32 [nseg, D]; ``cos`` / ``sin``: fp32
+    [M, rot/2].  The rotated pairs are (i, i + rot/2), or (2i, 2i + 1) with
+    ``interleaved``.  An output may be its own input."""
+    M, Hq, D = q.shape
+    if (k is None) != (k_out is None):
+        raise ValueError("k and k_out go together")
+    Hk = k.shape[1] if k is not None else 0
+    sp, nseg, _keep = _segs(seg_off)
+    half = cos.shape[-1] if cos is not None else 0
+    _check(load_library().h3fp4_qk_norm_rope(
+        _heads(q, "q", (M, Hq, D)), _heads(k, "k", (M, Hk, D)), M, Hq, Hk, D,
+        _f32(q_weight, "q_weight", (nseg, D)), _f32(k_weight, "k_weight", (nseg, D)),
+        _f32(cos, "cos", (M, half)), _f32(sin, "sin", (M, half)), 2 * half, sp, nseg, float(eps),
+        _heads(q_out, "q_out", (M, Hq, D)), _heads(k_out, "k_out", (M, Hk, D)),
+        ROPE_PAIRS if interleaved else 0, _stream(stream)), "h3fp4_qk_norm_rope")
+
+
+def h3fp4_cross_attn(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, out: torch.Tensor, ws: torch.Tensor, *,
+                     q_off: Optional[Sequence[int]] = None, kv_off: Optional[Sequence[int]] = None,
+                     key_mask: Optional[torch.Tensor] = None, scale: Optional[float] = None,
+                     lse: Optional[torch.Tensor] = None, stream=None) -> None:
+    """out [M, Hq, D] = attention of q [M, Hq, D] to k, v [T, Hkv, D] (bf16, any
+    row and head strides), segment by segment of ``q_off`` / ``kv_off``.
+
+    ``key_mask``: bool or uint8 [T], False / 0 leaves a key out; ``scale``
+    defaults to 1/sqrt(D); ``lse``: fp32 [M, Hq], also written.  ``ws`` from
+    :func:`alloc_attn_workspace`."""
+    M, Hq, D = q.shape
+    T, Hkv, _ = k.shape
+    qp, kp, nseg, _keep = _seg_pair(q_off, kv_off)
+    _check(load_library().h3fp4_cross_attn(
+        _heads(q, "q", (M, Hq, D)), _heads(k, "k", (T, Hkv, D)), _heads(v, "v", (T, Hkv, D)), M, T, Hq, Hkv, D,
+        qp, kp, nseg, _mask(key_mask, "key_mask", T), D ** -0.5 if scale is None else float(scale),
+        _heads(out, "out", (M, Hq, D)), _f32(lse, "lse", (M, Hq)), _ptr(ws, "ws", torch.uint8), ws.numel(),
+        _stream(stream)), "h3fp4_cross_attn")
+
+
+def h3fp4_shared_attn(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, k_ctx: torch.Tensor, v_ctx: torch.Tensor,
+                      out: torch.Tensor, ws: torch.Tensor, *, q_off: Optional[Sequence[int]] = None,
+                      kv_off: Optional[Sequence[int]] = None, key_mask: Optional[torch.Tensor] = None,
+                      ctx_mask: Optional[torch.Tensor] = None, scale: Optional[float] = None,
+                      lse: Optional[torch.Tensor] = None, stream=None) -> None:
+    """:func:`h3fp4_cross_attn` with a context ``k_ctx``, ``v_ctx`` [C, Hkv, D]
+    that the rows of every segment attend to beside their own keys, in one
+    softmax; ``ctx_mask``: bool or uint8 [C]."""
+    M, Hq, D = q.shape
+    T, Hkv, _ = k.shape
+    ctx = k_ctx.shape[0]
+    qp, kp, nseg, _keep = _seg_pair(q_off, kv_off)
+    _check(load_library().h3fp4_shared_attn(
+        _heads(q, "q", (M, Hq, D)), _heads(k, "k", (T, Hkv, D)), _heads(v, "v", (T, Hkv, D)),
+        _heads(k_ctx, "k_ctx", (ctx, Hkv, D)), _heads(v_ctx, "v_ctx", (ctx, Hkv, D)), M, T, ctx, Hq, Hkv, D,
+        qp, kp, nseg, _mask(key_mask, "key_mask", T), _mask(ctx_mask, "ctx_mask", ctx),
+        D ** -0.5 if scale is None else float(scale), _heads(out, "out", (M, Hq, D)), _f32(lse, "lse", (M, Hq)),
+        _ptr(ws, "ws", torch.uint8), ws.numel(), _stream(stream)), "h3fp4_shared_attn")
+
+
+def h3fp4_attn_workspace_bytes(M: int, T: int, Hq: int, Hkv: int, D: int, q_off: Optional[Sequence[int]] = None,
+                               kv_off: Optional[Sequence[int]] = None, ctx: int = 0) -> int:
+    qp, kp, nseg, _keep = _seg_pair(q_off, kv_off)
+    return int(load_library().h3fp4_attn_workspace_bytes(M, T, ctx, Hq, Hkv, D, qp, kp, nseg))
+
+
 def h3fp4_check(ws: torch.Tensor, stream=None) -> None:
     """Synchronise and raise H3FP4Error if a device wait timed out."""
     _check(load_library().h3fp4_check(_ptr(ws, "ws", torch.uint8), _stream(stream)), "h3fp4_check")
@@ -331,3 +468,12 @@ def alloc_nvfp4(rows: int, K: int, device="cuda"):
 
 def alloc_workspace(M: int, N: int, K: int, flags: int = 0, device="cuda") -> torch.Tensor:
     return torch.zeros(h3fp4_workspace_bytes(M, N, K, flags), dtype=torch.uint8, device=device)
+
+
+def alloc_attn_workspace(M: int, T: int, Hq: int, Hkv: int, D: int, q_off: Optional[Sequence[int]] = None,
+                         kv_off: Optional[Sequence[int]] = None, ctx: int = 0, device="cuda") -> torch.Tensor:
+    """Workspace of the attention calls for these sizes (``ctx``: rows of the shared context)."""
+    n = h3fp4_attn_workspace_bytes(M, T, Hq, Hkv, D, q_off, kv_off, ctx)
+    if n == 0:
+        raise ValueError("sizes or segment tables that the attention calls refuse")
+    return torch.zeros(n, dtype=torch.uint8, device=device)

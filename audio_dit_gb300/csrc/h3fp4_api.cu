@@ -6,6 +6,7 @@
 #include <cstring>
 #include <mutex>
 
+#include "h3fp4_heads.h"
 #include "h3fp4_internal.h"
 
 namespace h3fp4 {
@@ -23,6 +24,8 @@ size_t round256(size_t x) { return (x + 255) / 256 * 256; }
 h3fp4_status from_cuda(cudaError_t e) { return e == cudaSuccess ? H3FP4_OK : H3FP4_ERR_CUDA; }
 
 }  // namespace
+
+uint64_t wait_limit_ns() { return g_wait_limit_ns.load(); }
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 

@@ -101,10 +101,12 @@ enum {
     H3FP4_A_PREQUANT = 32,     /* x is already NVFP4: codes + a_sf + a_gscale                     */
     H3FP4_EPI_SWIGLU = 64,     /* out[M][N/2] = bf16(silu(g) * u), see h3fp4_linear                */
     H3FP4_EPI_AMAX = 128,      /* also write max|out| to h3fp4_ws_out_amax(ws)                    */
-    H3FP4_FUSED_QUANT = 256    /* quantise x inside the GEMM kernel, see h3fp4_linear              */
+    H3FP4_FUSED_QUANT = 256,   /* quantise x inside the GEMM kernel, see h3fp4_linear              */
+    H3FP4_ROPE_PAIRS = 512     /* rotate adjacent pairs (2i, 2i+1), see h3fp4_qk_norm_rope         */
 };
 
 #define H3FP4_MAX_SEGMENTS 8
+#define H3FP4_ATTN_MAX_SEGMENTS 256
 
 /* Bytes of the E2M1 codes of a [rows, K] operand: rows * K / 2. */
 H3FP4_API size_t h3fp4_codes_bytes(int64_t rows, int64_t K);
@@ -333,6 +335,87 @@ typedef enum {
  * resident on chip; flops counted as 2 * 128 * 256 * 64 per CTA per K step.
  * Entry point for roofline evidence only; no counterpart on the pages. */
 H3FP4_API h3fp4_status h3fp4_measure_fp4_form(int form, int iters, float* tflops, void* ws);
+
+/* A bf16 tensor [rows][heads][D] in device memory, element (r, h, d) at
+ * ptr + r * row_stride + h * head_stride + d (strides in ELEMENTS, positive
+ * multiples of 8; ptr 16-byte aligned).  Q, K and V may so be read where the
+ * QKV projection left them, interleaved by token ("H3 Runtime Current State",
+ * "Owned Performance Kernels": strided NHD views of the projection output). */
+typedef struct {
+    void* ptr;
+    int64_t row_stride;
+    int64_t head_stride;
+} h3fp4_heads;
+
+/* Per-head RMS norm and rotation of the queries and keys, one pass over both
+ * (the block's step between the QKV projection and attention; "H3 Blackwell
+ * Runtime Plan": norms and RoPE stay BF16, 3-axis RoPE).  For each row r, head h:
+ *     y = x * rsqrt(mean_d(x^2) + eps) * w[seg(r)]                    (fp32)
+ *     (a, b) -> (a cos - b sin, b cos + a sin)   for the rot / 2 pairs of the
+ *               first rot elements; the rest of the head is not rotated
+ *     out = bf16(y)                                       (rounded once)
+ * The pairs are elements (i, i + rot/2), with H3FP4_ROPE_PAIRS (2i, 2i + 1).
+ *   q, k: [M][Hq][D] and [M][Hk][D]; k (with k_out) may be NULL.  D % 8 == 0,
+ *      8 <= D <= 256.  M >= 0; with no row nothing is launched.
+ *   q_weight, k_weight: fp32 [nseg][D], 16-byte aligned; NULL means all ones.
+ *   cos, sin: fp32 [M][rot/2], 16-byte aligned, any angles per row (one, two or
+ *      three position axes alike); both NULL with rot = 0.  rot % 16 == 0,
+ *      rot <= D.
+ *   seg_off, nseg: as in h3fp4_quantize_act (weights per modality).
+ *   eps >= 0.  A row of zeros with eps = 0 gives NaN, as the formula does.
+ *   q_out, k_out: outputs; either may be the very tensor it is computed from
+ *      (same ptr and strides), otherwise no output may overlap an input. */
+H3FP4_API h3fp4_status h3fp4_qk_norm_rope(const h3fp4_heads* q, const h3fp4_heads* k, int64_t M, int Hq, int Hk,
+                                          int D, const float* q_weight, const float* k_weight, const float* cos,
+                                          const float* sin, int rot, const int64_t* seg_off, int nseg, float eps,
+                                          const h3fp4_heads* q_out, const h3fp4_heads* k_out, int flags,
+                                          cudaStream_t stream);
+
+/* Attention of packed query rows to an encoder's states of another length,
+ * segment by segment (a segment is a sample of the batch, or a modality):
+ *     out[r][h] = sum_j p_j v_j / sum_j p_j,   p_j = exp(scale * q_r . k_j - m_r)
+ * over the keys j of r's segment that the mask keeps, with kv head
+ * h / (Hq / Hkv) for query head h (grouped heads).  Scores, statistics and sums
+ * are fp32; the p_j are rounded to bf16 for their product with V.
+ *   q: [M][Hq][D]; k, v: [T][Hkv][D]; out: [M][Hq][D].  Hq % Hkv == 0,
+ *      D % 8 == 0, 8 <= D <= 128, M, T < 2^31.
+ *   q_off, kv_off: HOST arrays of nseg + 1 row offsets (0 first, non-decreasing,
+ *      M and T last); segment i of the rows attends to segment i of the keys.
+ *      Segments may be empty.  Both NULL: one segment.
+ *      1 <= nseg <= H3FP4_ATTN_MAX_SEGMENTS.
+ *   key_mask: T bytes (device), 0 = the key is left out; NULL keeps all.  What
+ *      K and V hold at a key that is left out does not matter (NaN, infinities).
+ *   scale > 0, finite.
+ *   A row without a key (an empty segment, a mask that leaves nothing, or only
+ *   scores of -inf) gives out = 0 and lse = -inf.
+ *   lse: fp32 [M][Hq], 4-byte aligned, log(sum_j exp(scale q_r . k_j)); may be NULL.
+ *   out may not overlap q, k or v.
+ *   ws: device workspace of at least h3fp4_attn_workspace_bytes(...) bytes
+ *      (ws_bytes is checked), first 256 bytes zeroed once before first use;
+ *      h3fp4_check(ws) reports device waits that timed out.  Concurrent calls
+ *      must not share one workspace. */
+H3FP4_API h3fp4_status h3fp4_cross_attn(const h3fp4_heads* q, const h3fp4_heads* k, const h3fp4_heads* v, int64_t M,
+                                        int64_t T, int Hq, int Hkv, int D, const int64_t* q_off,
+                                        const int64_t* kv_off, int nseg, const uint8_t* key_mask, float scale,
+                                        const h3fp4_heads* out, float* lse, void* ws, size_t ws_bytes,
+                                        cudaStream_t stream);
+
+/* The same for a batch that shares a context: every row attends to the C keys
+ * of k_ctx / v_ctx ([C][Hkv][D]; a prompt's and keyframes' states, stored and
+ * read once for all samples) and to the keys of its own segment, in one
+ * softmax over both.  ctx_mask: C bytes, as key_mask.  C = 0 is
+ * h3fp4_cross_attn; T = 0 leaves the context alone. */
+H3FP4_API h3fp4_status h3fp4_shared_attn(const h3fp4_heads* q, const h3fp4_heads* k, const h3fp4_heads* v,
+                                         const h3fp4_heads* k_ctx, const h3fp4_heads* v_ctx, int64_t M, int64_t T,
+                                         int64_t C, int Hq, int Hkv, int D, const int64_t* q_off,
+                                         const int64_t* kv_off, int nseg, const uint8_t* key_mask,
+                                         const uint8_t* ctx_mask, float scale, const h3fp4_heads* out, float* lse,
+                                         void* ws, size_t ws_bytes, cudaStream_t stream);
+
+/* Workspace bytes of h3fp4_cross_attn (C = 0) and h3fp4_shared_attn for these
+ * sizes; 0 for sizes and tables those calls refuse.  No device access. */
+H3FP4_API size_t h3fp4_attn_workspace_bytes(int64_t M, int64_t T, int64_t C, int Hq, int Hkv, int D,
+                                            const int64_t* q_off, const int64_t* kv_off, int nseg);
 
 /* Synchronises `stream`, reads and clears the workspace status word.
  * Returns H3FP4_OK, or H3FP4_ERR_TIMEOUT when a kernel gave up early (a
