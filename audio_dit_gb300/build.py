@@ -18,7 +18,8 @@ OUT_DIR = os.path.join(HERE, "_build")
 LIB = os.path.join(OUT_DIR, "libh3fp4.so")
 SOURCES = ["h3fp4_api.cu", "h3fp4_quant.cu", "h3fp4_gemm.cu", "h3fp4_peak.cu", "h3fp4_noalloc.cu",
            "h3fp4_heads_api.cu", "h3fp4_norm_rope.cu", "h3fp4_attn.cu"]
-HEADERS = ["h3fp4_internal.h", "ptx_sm103.cuh", "nvfp4_encode.cuh", "act_prologue.cuh", "h3fp4_heads.h"]
+HEADERS = ["h3fp4_internal.h", "ptx_sm103.cuh", "nvfp4_encode.cuh", "act_prologue.cuh", "h3fp4_heads.h", "tensor_map.h",
+           "attn_plan.h"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

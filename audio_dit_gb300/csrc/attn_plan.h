@@ -1,0 +1,308 @@
+// How an attention call's work is cut into units, steps and pieces; plain
+// arithmetic shared by the host (planning, workspace size) and the kernels.
+//
+// A tile of queries is 128 rows: `pack` query heads of one kv head times
+// tok = 128 / pack tokens, so that all of them use the same K and V.  A unit is
+// what one CTA works on at a time: two tiles of queries against the same keys
+// (pair plan), or one tile whose even and odd key tiles go to the CTA's two
+// softmax warpgroups (solo plan, for few rows).  Its steps are the 128-key tiles
+// it walks: first the shared context's, then its own segment's.
+//
+// An entry is a segment; with the separate plan (many short segments over a long
+// context) the segments walk their own keys only, and one more entry walks the
+// context for the rows of all segments together.
+//
+// Units are dealt out in two parts.  Of each entry, whole waves of `ctas` units
+// go to the CTAs one by one; consecutive CTAs then read the same keys at the
+// same time.  What is left over (the pool) is laid out as one row of steps and
+// cut into equal stretches, one per CTA: a unit that is cut leaves partial sums
+// that a second kernel joins.  A cut within kSnap steps of a unit's edge moves
+// there, since a partial costs about as much as that many steps.
+#pragma once
+#include <cstddef>
+#include <cstdint>
+
+#include "../../include/h3fp4.h"
+
+namespace h3fp4 {
+
+constexpr int kKeyTile = 128;
+constexpr int kAttnCtas = 152;   // one per SM of the GB300
+constexpr int kSnap = 4;
+constexpr int kAttnEntries = H3FP4_ATTN_MAX_SEGMENTS + 1;
+
+struct AttnTable {
+    int nseg, entries;     // entries = nseg (+ 1: the context's, separate plan)
+    int ctas;
+    int pack, tok;         // heads and tokens of a tile
+    int unit_tok;          // tokens of a unit: 2 tok (pair) or tok (solo)
+    int head_blocks;       // Hq / pack
+    int ctx_tiles;         // key tiles of the context
+    int separate;
+    int any_full;          // some entry has whole waves
+    int pool_steps, pool_units;
+    int M;
+    int q_off[H3FP4_ATTN_MAX_SEGMENTS + 1];
+    int kv_off[H3FP4_ATTN_MAX_SEGMENTS + 1];
+    int pool_step[kAttnEntries + 1];   // steps of the pool before each entry
+    int pool_unit[kAttnEntries + 1];   // units of the pool before each entry
+
+    __host__ __device__ int q_begin(int e) const { return e < nseg ? q_off[e] : 0; }
+    __host__ __device__ int q_end(int e) const { return e < nseg ? q_off[e + 1] : M; }
+    // Key tiles of an entry: the context's share and all of them.
+    __host__ __device__ int tiles_ctx(int e) const { return separate && e < nseg ? 0 : ctx_tiles; }
+    __host__ __device__ int tiles_own(int e) const
+    {
+        return e < nseg ? (kv_off[e + 1] - kv_off[e] + kKeyTile - 1) / kKeyTile : 0;
+    }
+    __host__ __device__ int tiles(int e) const { return tiles_ctx(e) + tiles_own(e); }
+    // A unit without keys still takes a step (it writes zeros).
+    __host__ __device__ int steps(int e) const
+    {
+        const int n = tiles(e);
+        return n > 0 ? n : 1;
+    }
+    __host__ __device__ int row_blocks(int e) const { return (q_end(e) - q_begin(e) + unit_tok - 1) / unit_tok; }
+    __host__ __device__ int units(int e) const { return head_blocks * row_blocks(e); }
+    __host__ __device__ int full(int e) const { return any_full ? units(e) / ctas * ctas : 0; }
+
+    // Largest i in [0, entries) with start[i] <= x.
+    __host__ __device__ int find(const int* start, int x) const
+    {
+        int lo = 0, hi = entries;
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (start[mid] <= x) lo = mid;
+            else hi = mid;
+        }
+        return lo;
+    }
+    // Where CTA c's stretch of the pool begins.
+    __host__ __device__ int bound(int c) const
+    {
+        const int x = (int)((long long)c * pool_steps / ctas);
+        if (c <= 0 || c >= ctas || x <= 0 || x >= pool_steps) return x;
+        const int e = find(pool_step, x), n = steps(e), t = (x - pool_step[e]) % n;
+        if (t <= kSnap && t <= n - t) return x - t;
+        if (n - t <= kSnap) return x + n - t;
+        return x;
+    }
+    // The CTA whose stretch holds step x of the pool.
+    __host__ __device__ int cta_of(int x) const
+    {
+        int c = (int)((long long)x * ctas / pool_steps);
+        if (c > ctas - 1) c = ctas - 1;
+        while (c > 0 && bound(c) > x) --c;
+        while (c + 1 < ctas && bound(c + 1) <= x) ++c;
+        return c;
+    }
+};
+
+__host__ __device__ inline int lesser(int a, int b) { return a < b ? a : b; }
+
+// A stretch of the pool has at most two cut units: its first, begun by another
+// CTA, and its last, which it begins itself.
+__host__ __device__ inline int cut_slot(int cta, bool begins_unit) { return 2 * cta + (begins_unit ? 1 : 0); }
+
+// A piece of a unit: key tiles [t0, t0 + nt) of it, for tokens [tok0, tok0 + ntok).
+struct Piece {
+    int e, head0, tok0, ntok;
+    int t0, nt;
+    int ctx_tiles;          // tiles below this index are the context's
+    int own_tiles, kv0, kv_len;
+    bool whole;             // all steps of the unit
+    int slot;               // of the partial sums, if not whole (or separate plan)
+};
+
+// The pieces of this CTA, in order; every role walks them by itself.
+struct Walk {
+    const AttnTable& t;
+    int cta, e, unit, pos, end;
+
+    __host__ __device__ Walk(const AttnTable& table, int c) : t(table), cta(c)
+    {
+        e = 0;
+        unit = cta;
+        pos = t.pool_steps ? t.bound(cta) : 0;
+        end = t.pool_steps ? t.bound(cta + 1) : 0;
+    }
+    __host__ __device__ void fill(Piece& p, int entry, int u) const
+    {
+        const int rb = t.row_blocks(entry), hb = u / rb;
+        p.e = entry;
+        p.head0 = hb * t.pack;
+        p.tok0 = t.q_begin(entry) + (u - hb * rb) * t.unit_tok;
+        p.ntok = lesser(t.unit_tok, t.q_end(entry) - p.tok0);
+        p.ctx_tiles = t.tiles_ctx(entry);
+        p.own_tiles = t.tiles_own(entry);
+        p.kv0 = entry < t.nseg ? t.kv_off[entry] : 0;
+        p.kv_len = entry < t.nseg ? t.kv_off[entry + 1] - p.kv0 : 0;
+    }
+    __host__ __device__ bool next(Piece& p)
+    {
+        while (t.any_full && e < t.entries) {
+            if (unit < t.full(e)) {
+                fill(p, e, unit);
+                unit += t.ctas;
+                p.t0 = 0;
+                p.nt = p.ctx_tiles + p.own_tiles;
+                p.whole = true;
+                p.slot = 0;
+                return true;
+            }
+            ++e;
+            unit = cta;
+        }
+        if (pos >= end) return false;
+        const int entry = t.find(t.pool_step, pos), n = t.steps(entry);
+        const int local = pos - t.pool_step[entry], u = local / n, t0 = local - u * n;
+        const int take = lesser(n - t0, end - pos);
+        fill(p, entry, t.full(entry) + u);
+        p.t0 = t0;
+        p.nt = lesser(t0 + take, p.ctx_tiles + p.own_tiles) - t0;
+        p.whole = take == n && !t.separate;
+        // A stretch has at most two cut units, its first and its last; with the
+        // separate plan every piece leaves partials, numbered along the pool.
+        p.slot = t.separate ? (entry < t.nseg ? t.pool_unit[entry] + u : u) + cta
+                            : cut_slot(cta, t0 == 0);
+        pos += take;
+        return true;
+    }
+    // The same without the units that have no key (only the epilogue sees those).
+    __host__ __device__ bool next_with_keys(Piece& p)
+    {
+        while (next(p))
+            if (p.nt > 0) return true;
+        return false;
+    }
+};
+
+struct AttnPlan {
+    AttnTable t;
+    bool solo;
+    bool join;           // partial sums exist: the second kernel runs
+    int dp;              // D padded to 64 or 128
+    int slot_rows[2];    // rows of a partial: segments' units, the context entry's
+    long long slots[2];  // partials of each kind
+    size_t slot_off[2];  // byte offsets in the workspace
+    size_t bytes;        // workspace; 0: more steps than 32 bits count
+};
+
+// Units, steps and the pool for one choice of pack, solo and separate.
+template <class Job>
+inline void lay_out(const Job& job, int pack, bool solo, bool separate, AttnTable& t)
+{
+    t.nseg = job.nseg;
+    t.entries = job.nseg + (separate ? 1 : 0);
+    t.pack = pack;
+    t.tok = 128 / pack;
+    t.unit_tok = solo ? t.tok : 2 * t.tok;
+    t.head_blocks = job.Hq / pack;
+    t.ctx_tiles = (int)((job.C + kKeyTile - 1) / kKeyTile);
+    t.separate = separate ? 1 : 0;
+    t.M = (int)job.M;
+    t.ctas = kAttnCtas;
+}
+
+// Steps of all units.
+inline double total_steps(const AttnTable& t)
+{
+    double s = 0;
+    for (int e = 0; e < t.entries; ++e) s += (double)t.units(e) * t.steps(e);
+    return s;
+}
+
+template <class Job>
+inline AttnPlan make_plan(const Job& job)
+{
+    AttnPlan pl{};
+    AttnTable& t = pl.t;
+    pl.dp = job.D <= 64 ? 64 : 128;
+    for (int i = 0; i <= job.nseg; ++i) {
+        t.q_off[i] = (int)job.q_off[i];
+        t.kv_off[i] = (int)job.kv_off[i];
+    }
+    // Heads of a kv group share a tile's keys; the largest pack with the fewest steps.
+    const int group = job.Hq / job.Hkv;
+    int pack = 1;
+    double best = 0;
+    for (int g = 1; g <= group && g <= 128; ++g) {
+        if (group % g) continue;
+        lay_out(job, g, true, false, t);
+        const double s = total_steps(t);
+        if (g == 1 || s <= best) {
+            best = s;
+            pack = g;
+        }
+    }
+    // A pair's step takes about 1.5 of a solo step (which reads K and V for one
+    // tile of queries only); the separate plan pays a step per unit for its partials.
+    double cost[2][2];
+    for (int sep = 0; sep < 2; ++sep)
+        for (int solo = 0; solo < 2; ++solo) {
+            lay_out(job, pack, solo != 0, sep != 0, t);
+            double units = 0;
+            for (int e = 0; e < t.entries; ++e) units += t.units(e);
+            cost[sep][solo] = (total_steps(t) + (sep ? 2 * units : 0)) * (solo ? 1.0 : 1.5);
+        }
+    const bool can_separate = job.nseg > 1 && job.C > 0;
+    const double whole = cost[0][0] < cost[0][1] ? cost[0][0] : cost[0][1];
+    const double apart = cost[1][0] < cost[1][1] ? cost[1][0] : cost[1][1];
+    const bool sep = can_separate && apart + 2 * kAttnCtas < whole;
+    pl.solo = cost[sep][1] <= cost[sep][0];
+    lay_out(job, pack, pl.solo, sep, t);
+
+    // CTAs: one per SM where there is work for all of them.
+    const double steps = total_steps(t);
+    if (steps >= 2147483648.0) return pl;  // steps are counted in 32 bits; bytes = 0
+    long long units = 0;
+    for (int e = 0; e < t.entries; ++e) units += t.units(e);
+    long long ctas = (long long)(steps / kSnap);
+    if (ctas < units) ctas = units;
+    t.ctas = ctas > kAttnCtas ? kAttnCtas : ctas < 1 ? 1 : (int)ctas;
+    t.any_full = 0;
+    if (!sep && t.ctas == kAttnCtas)
+        for (int e = 0; e < t.entries; ++e)
+            if (t.units(e) >= t.ctas) t.any_full = 1;
+    for (int e = 0; e < t.entries; ++e) {
+        const int rest = t.units(e) - t.full(e);
+        t.pool_unit[e + 1] = t.pool_unit[e] + rest;
+        t.pool_step[e + 1] = t.pool_step[e] + rest * t.steps(e);
+    }
+    t.pool_units = t.pool_unit[t.entries];
+    t.pool_steps = t.pool_step[t.entries];
+
+    // Partials: rows of the largest unit of each kind, an even number so that
+    // every slot of rows * (dp + 2) floats begins on 16 bytes.
+    int most = 0;
+    for (int e = 0; e < t.nseg; ++e) {
+        const int rows = t.q_end(e) - t.q_begin(e);
+        if (rows > most) most = rows;
+    }
+    pl.slot_rows[0] = (most < t.unit_tok ? most : t.unit_tok) * pack;
+    pl.slot_rows[1] = (t.M < t.unit_tok ? t.M : t.unit_tok) * pack;
+    for (int& rows : pl.slot_rows) rows += rows & 1;
+    if (sep) {
+        pl.join = true;
+        pl.slots[0] = t.pool_unit[t.nseg] + t.ctas;
+        pl.slots[1] = t.units(t.nseg) + t.ctas;
+    } else {
+        for (int c = 1; c < t.ctas && t.pool_steps > 0 && !pl.join; ++c) {
+            const int x = t.bound(c);
+            if (x <= 0 || x >= t.pool_steps) continue;
+            const int e = t.find(t.pool_step, x);
+            if ((x - t.pool_step[e]) % t.steps(e) != 0) pl.join = true;
+        }
+        pl.slots[0] = pl.join ? 2 * t.ctas : 0;
+    }
+    size_t at = 256;
+    for (int k = 0; k < 2; ++k) {
+        pl.slot_off[k] = at;
+        at += (size_t)pl.slots[k] * pl.slot_rows[k] * (pl.dp + 2) * 4;
+        at = (at + 255) / 256 * 256;
+    }
+    pl.bytes = at;
+    return pl;
+}
+
+}  // namespace h3fp4

@@ -1,162 +1,828 @@
 // Attention of packed query rows to an encoder's states and to a shared context.
 //
 //     out[r][h] = sum_j p_j v_j / l,  p_j = exp(scale q_r.k_j - m),  l = sum_j p_j
-// over the context's keys and the keys of r's own segment, in one pass with a
-// running maximum m: when m grows, the sums so far are scaled by exp(m_old - m).
+// over the context's keys and the keys of r's own segment, in one pass over the
+// keys with a running maximum: scores S = Q K^T of 128 queries x 128 keys and
+// the products P V run on the tensor cores (tcgen05, bf16 operands, fp32
+// accumulators in TMEM); the softmax between them runs in registers, one thread
+// per query row.
 //
-// A CTA takes 64 query rows of one head and walks its keys 32 at a time
-// through shared memory; four threads share a row (eight scores each, then a
-// quarter of the output's columns each).  All arithmetic is fp32.
+// The maximum in use, m, only follows the true one when that is more than 2^8
+// above it (in exp's base 2): the p_j stay below 2^8, l and the sums lose
+// nothing in fp32, and the accumulator is rescaled a few times per row instead
+// of once per tile.  The p_j are rounded to bf16 for their product with V (the
+// tensor cores' 16-bit input with fp32's range); l sums them unrounded.
+//
+// How units, steps and pieces are cut: attn_plan.h.
+//
+// Roles (512 threads, one CTA per SM):
+//   warp 0       loads: Q tiles (two buffers) and a ring of K and V tiles by TMA,
+//                128-byte swizzled 64-column chunks; columns past D are zero-filled
+//   warp 1       issues the MMAs.  Per query tile X and key tile: S_X = Q_X K^T,
+//                then, once the softmax stored P_X over S_X's first columns,
+//                O_X += P_X V.  The two tiles alternate, so that one tile's MMAs
+//                run under the other's softmax.
+//   warp 2       keys that are left out (a mask, the end of a segment inside a
+//                tile): their bits for the softmax, and zeros over their rows of
+//                the V tile, since 0 * NaN is not 0
+//   warp 3       allocates TMEM
+//   warps 4-11   softmax of tile A, of tile B (a warpgroup each)
+//   warps 12-15  epilogue: divides by l, rounds, stores; or stores partial sums
+// The epilogue of a unit overlaps the next unit's first MMAs and softmax.
+//
+// Every wait is bounded; a role that gives up records it in the status word and
+// leaves, and so do the roles that depend on it.
 #include <cmath>
 #include <cstdint>
 
+#include <cuda.h>
 #include <cuda_bf16.h>
 
+#include "attn_plan.h"
 #include "h3fp4_heads.h"
 #include "ptx_sm103.cuh"
+#include "tensor_map.h"
 
 namespace h3fp4 {
 namespace {
 
-constexpr int kRows = 64, kKeys = 32, kThreads = 256;
+constexpr int kThreads = 512;
+constexpr float kGrowth = 8.0f;      // log2 of how far the true maximum may pass the one in use
+constexpr int kMaskSlots = 16;
+constexpr uint32_t kTmemCols = 512;
+constexpr uint32_t kRegsControl = 56, kRegsSoftmax = 184, kRegsEpilogue = 88;
+static_assert(kRegsControl + 2 * kRegsSoftmax + kRegsEpilogue <= 512, "setmaxnreg shares exceed the launch budget");
 
-struct AttnParams {
-    HeadsIn q, k, v, kc, vc;
-    __nv_bfloat16* out;
-    long long out_row, out_head;
-    float* lse;
-    int C, Hq, group, D, nseg;
-    const uint8_t* key_mask;
-    const uint8_t* ctx_mask;
-    float scale_log2;
-    int q_off[H3FP4_ATTN_MAX_SEGMENTS + 1];
-    int kv_off[H3FP4_ATTN_MAX_SEGMENTS + 1];
-    int tiles[H3FP4_ATTN_MAX_SEGMENTS + 1];  // row tiles before each segment
+constexpr unsigned int kStatusTimeoutAttnLoad = 64u, kStatusTimeoutAttnMma = 128u, kStatusTimeoutAttnSoftmax = 256u,
+                       kStatusTimeoutAttnEpilogue = 512u, kStatusTimeoutAttnMask = 1024u;
+
+template <int DP, bool kSolo>
+struct Layout {
+    static constexpr uint32_t kTile = 128 * DP * 2;   // bytes of a 128-row tile
+    static constexpr int kQTiles = kSolo ? 1 : 2;     // per buffer
+    static constexpr int kStages = (7 - 2 * kQTiles) * (128 / DP);
+    static constexpr uint32_t kKvOff = 2 * kQTiles * kTile;
+    static constexpr uint32_t kBarOff = kKvOff + kStages * kTile;
+    // barriers: q_full, q_empty (2 each), kv_full, kv_empty (per stage), s_full, p_full, o_full, o_empty,
+    // stat_full, stat_empty (2 each), gap_load, mask_full (per slot), done
+    static constexpr int kBars = 4 + 2 * kStages + 12 + 2 * kMaskSlots + 1;
+    static constexpr uint32_t kMaskOff = kBarOff + (kBars * 8 + 8 + 15) / 16 * 16;
+    static constexpr uint32_t kStatOff = kMaskOff + kMaskSlots * 16;
+    static constexpr uint32_t kBytes = kStatOff + 2 * 128 * 8;
+    static_assert(kBytes <= 232448, "shared memory budget");
 };
 
-__global__ void __launch_bounds__(kThreads) attn_kernel(const __grid_constant__ AttnParams p)
-{
-    griddep_wait();
-    __shared__ __nv_bfloat16 sq[kRows][kAttnMaxD + 2];
-    __shared__ __nv_bfloat16 sk[kKeys][kAttnMaxD + 2];
-    __shared__ __nv_bfloat16 sv[kKeys][kAttnMaxD];
-    __shared__ uint8_t keep[kKeys];
-    __shared__ float sp[kRows][kKeys + 1];
-    const int tid = threadIdx.x, row = tid >> 2, c = tid & 3;
-    const int h = blockIdx.y, hk = h / p.group;
-    int seg = 0;
-    while (seg + 1 < p.nseg && (int)blockIdx.x >= p.tiles[seg + 1]) ++seg;
-    const int r0 = p.q_off[seg] + ((int)blockIdx.x - p.tiles[seg]) * kRows;
-    const int rows = min(kRows, p.q_off[seg + 1] - r0);
-    for (int i = tid; i < kRows * p.D; i += kThreads) {
-        const int r = i / p.D, d = i - r * p.D;
-        sq[r][d] = r < rows ? p.q.p[(r0 + r) * p.q.row + h * p.q.head + d] : __float2bfloat16(0.0f);
-    }
-    float m = -INFINITY, l = 0.0f, acc[kAttnMaxD / 4];
-#pragma unroll
-    for (int i = 0; i < kAttnMaxD / 4; ++i) acc[i] = 0.0f;
+struct AttnParams {
+    AttnTable t;
+    int Hq, group, D, C;
+    const uint8_t* key_mask;
+    const uint8_t* ctx_mask;
+    float scale_log2, growth;      // growth: kGrowth in units of the raw scores
+    __nv_bfloat16* out;
+    long long out_row, out_head;
+    int wide_out;                  // output rows 32-byte aligned, D % 16 == 0
+    float* lse;
+    float* part[2];                // partial sums: segments' units, the context entry's
+    int slot_rows[2];
+    uint32_t q_bytes;              // bytes a Q tile's copies deliver
+    unsigned int* status;
+    unsigned long long wait_ns;
+    int stall;                     // self-test: the loads are left out, so every wait runs out
+};
 
-    for (int part = 0; part < 2; ++part) {  // the context, then the segment's own keys
-        const HeadsIn& K = part ? p.k : p.kc;
-        const HeadsIn& V = part ? p.v : p.vc;
-        const uint8_t* mask = part ? p.key_mask : p.ctx_mask;
-        const int k0 = part ? p.kv_off[seg] : 0, k1 = part ? p.kv_off[seg + 1] : p.C;
-        for (int t = k0; t < k1; t += kKeys) {
-            __syncthreads();
-            if (tid < kKeys) keep[tid] = t + tid < k1 && (!mask || mask[t + tid]);
-            __syncthreads();
-            for (int i = tid; i < kKeys * p.D; i += kThreads) {
-                const int j = i / p.D, d = i - j * p.D;
-                const long long at = (long long)(t + j);
-                sk[j][d] = keep[j] ? K.p[at * K.row + hk * K.head + d] : __float2bfloat16(0.0f);
-                sv[j][d] = keep[j] ? V.p[at * V.row + hk * V.head + d] : __float2bfloat16(0.0f);
+// Whether key tile t (of the unit) has keys that are left out, and how many such
+// tiles a piece has before it.
+__device__ __forceinline__ bool has_gaps(const AttnParams& p, const Piece& u, int t)
+{
+    if (t < u.ctx_tiles) return p.ctx_mask != nullptr || (t == u.ctx_tiles - 1 && (p.C & 127) != 0);
+    return p.key_mask != nullptr || (t == u.ctx_tiles + u.own_tiles - 1 && (u.kv_len & 127) != 0);
+}
+
+// Tiles of a piece for query tile X: how many, and which is the i-th (relative to t0).
+template <bool kSolo>
+__device__ __forceinline__ int tiles_for(const Piece& u, int X, int tok)
+{
+    if (kSolo) return X == 0 ? (u.nt + 1) >> 1 : u.nt >> 1;
+    return X == 0 || u.ntok > tok ? u.nt : 0;
+}
+template <bool kSolo>
+__device__ __forceinline__ int tile_at(int X, int i)
+{
+    return kSolo ? 2 * i + X : i;
+}
+// Places of K and V tile i of nt in the ring's order of loads.
+template <bool kSolo>
+__device__ __forceinline__ int k_place(int i)
+{
+    return kSolo ? (i == 0 ? 0 : 2 * i - 1) : 2 * i;
+}
+template <bool kSolo>
+__device__ __forceinline__ int v_place(int i, int nt)
+{
+    return kSolo ? (i == nt - 1 ? 2 * nt - 1 : 2 * i + 2) : 2 * i + 1;
+}
+
+__device__ __forceinline__ void store_row(__nv_bfloat16* o, const uint32_t (&w)[16], int cols, bool wide)
+{
+    if (wide) {
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+            if (16 * j < cols)
+                asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(o + 16 * j),
+                             "r"(w[8 * j]), "r"(w[8 * j + 1]), "r"(w[8 * j + 2]), "r"(w[8 * j + 3]),
+                             "r"(w[8 * j + 4]), "r"(w[8 * j + 5]), "r"(w[8 * j + 6]), "r"(w[8 * j + 7])
+                             : "memory");
+    } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            if (8 * j < cols)
+                *reinterpret_cast<uint4*>(o + 8 * j) =
+                    make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
+    }
+}
+
+template <int DP, bool kSolo>
+__global__ void __launch_bounds__(kThreads, 1)
+    attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+                const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmKc,
+                const __grid_constant__ CUtensorMap tmVc, const __grid_constant__ AttnParams p)
+{
+    extern __shared__ __align__(1024) uint8_t smem[];
+    using L = Layout<DP, kSolo>;
+    constexpr int kStages = L::kStages;
+    constexpr int kChunks = DP / 64;
+    constexpr uint32_t kTmS = 0, kTmO = 256;  // S_A, S_B at 0 and 128; O_A, O_B from 256, DP columns each
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+    // Swizzled TMA tiles need 1024-byte alignment; refuse to run otherwise.
+    if ((smem_u32(smem) & 1023u) != 0) {
+        if (threadIdx.x == 0) atomicOr(p.status, kStatusBadSmemAlign);
+        griddep_wait();
+        return;
+    }
+    uint64_t* q_full = reinterpret_cast<uint64_t*>(smem + L::kBarOff);  // per Q buffer: its tiles landed
+    uint64_t* q_empty = q_full + 2;                 // the unit's last S was computed
+    uint64_t* kv_full = q_empty + 2;                // per stage: the K or V tile landed
+    uint64_t* kv_empty = kv_full + kStages;         // its MMAs are done
+    uint64_t* s_full = kv_empty + kStages;          // per query tile: S computed (and the MMAs before it done)
+    uint64_t* p_full = s_full + 2;                  // P stored, O rescaled where it had to be
+    uint64_t* o_full = p_full + 2;                  // O complete
+    uint64_t* o_empty = o_full + 2;                 // O read by the epilogue
+    uint64_t* stat_full = o_empty + 2;              // maximum and sum of each row stored
+    uint64_t* stat_empty = stat_full + 2;           // and read
+    uint64_t* gap_load = stat_empty + 2;            // per slot: the load of a V tile with gaps was issued
+    uint64_t* mask_full = gap_load + kMaskSlots;    // per slot: bits stored, V rows zeroed
+    uint64_t* done = mask_full + kMaskSlots;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done + 1);
+    uint4* mask_bits = reinterpret_cast<uint4*>(smem + L::kMaskOff);
+    float2* stat = reinterpret_cast<float2*>(smem + L::kStatOff);  // [2][128]: (maximum, sum)
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&q_full[i], 1);
+            mbar_init(&q_empty[i], 1);
+            mbar_init(&s_full[i], 1);
+            mbar_init(&p_full[i], 4);
+            mbar_init(&o_full[i], 1);
+            mbar_init(&o_empty[i], 4);
+            mbar_init(&stat_full[i], 4);
+            mbar_init(&stat_empty[i], 4);
+        }
+        for (int i = 0; i < kStages; ++i) {
+            mbar_init(&kv_full[i], 1);
+            mbar_init(&kv_empty[i], 1);
+        }
+        for (int i = 0; i < kMaskSlots; ++i) {
+            mbar_init(&gap_load[i], 1);
+            mbar_init(&mask_full[i], 1);
+        }
+        mbar_init(done, 1);
+        fence_mbarrier_init();
+        prefetch_tensormap(&tmQ);
+        prefetch_tensormap(&tmK);
+        prefetch_tensormap(&tmV);
+        if (p.C > 0) {
+            prefetch_tensormap(&tmKc);
+            prefetch_tensormap(&tmVc);
+        }
+    }
+    if (warp == 3) {
+        tmem_alloc(tmem_slot, kTmemCols);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    // Everything above overlaps the previous kernel's tail (programmatic
+    // dependent launch); its outputs are read only after this.
+    griddep_wait();
+    const uint32_t tmem = *tmem_slot;
+    const int tok = p.t.tok;
+
+    if (warp < 4) {
+        setmaxnreg_dec<kRegsControl>();
+        Walk walk(p.t, blockIdx.x);
+        if (warp == 0) {
+            // ------------------------------------------------------------ loads
+            Piece u;
+            uint32_t unit = 0, place = 0, gaps = 0;
+            bool ok = p.stall == 0;
+            while (ok && walk.next_with_keys(u)) {
+                const uint32_t buf = unit & 1u;
+                const bool two = !kSolo && u.ntok > tok;
+                ok = mbar_wait(&q_empty[buf], ((unit >> 1) & 1u) ^ 1u, p.wait_ns, p.status, kStatusTimeoutAttnLoad);
+                if (!__all_sync(0xffffffffu, ok)) {
+                    ok = false;
+                    break;
+                }
+                if (elect_one()) {
+                    uint8_t* q = smem + buf * L::kQTiles * L::kTile;
+                    mbar_arrive_expect_tx(&q_full[buf], p.q_bytes * (two ? 2u : 1u));
+                    for (int X = 0; X < (two ? 2 : 1); ++X)
+                        for (int c = 0; c < kChunks; ++c)
+                            tma_load_3d(q + X * L::kTile + c * 16384, &tmQ, &q_full[buf], 64 * c, u.head0,
+                                        u.tok0 + X * tok);
+                }
+                ++unit;
+                const int hk = u.head0 / p.group;
+                for (int i = 0; i < 2 * u.nt; ++i, ++place) {
+                    // which tile the ring's next place takes
+                    bool is_v;
+                    int t;
+                    if (kSolo) {
+                        is_v = i == 2 * u.nt - 1 || (i > 0 && (i & 1) == 0);
+                        t = i == 0 ? 0 : i == 2 * u.nt - 1 ? u.nt - 1 : is_v ? i / 2 - 1 : (i + 1) / 2;
+                    } else {
+                        is_v = (i & 1) != 0;
+                        t = i >> 1;
+                    }
+                    t += u.t0;
+                    const uint32_t st = place % kStages;
+                    ok = mbar_wait(&kv_empty[st], ((place / kStages) & 1u) ^ 1u, p.wait_ns, p.status,
+                                   kStatusTimeoutAttnLoad);
+                    if (!__all_sync(0xffffffffu, ok)) {
+                        ok = false;
+                        break;
+                    }
+                    if (elect_one()) {
+                        const bool ctx = t < u.ctx_tiles;
+                        const CUtensorMap* map = is_v ? (ctx ? &tmVc : &tmV) : (ctx ? &tmKc : &tmK);
+                        const int row = ctx ? t * kKeyTile : u.kv0 + (t - u.ctx_tiles) * kKeyTile;
+                        uint8_t* d = smem + L::kKvOff + st * L::kTile;
+                        mbar_arrive_expect_tx(&kv_full[st], L::kTile);
+                        for (int c = 0; c < kChunks; ++c) tma_load_3d(d + c * 16384, map, &kv_full[st], 64 * c, hk, row);
+                        if (is_v && has_gaps(p, u, t)) mbar_arrive(&gap_load[gaps % kMaskSlots]);
+                    }
+                    gaps += is_v && has_gaps(p, u, t);
+                }
             }
-            __syncthreads();
-            float z[kKeys / 4], top = -INFINITY;
-#pragma unroll
-            for (int i = 0; i < kKeys / 4; ++i) z[i] = 0.0f;
-            for (int d = 0; d < p.D; ++d) {
-                const float x = __bfloat162float(sq[row][d]);
-#pragma unroll
-                for (int i = 0; i < kKeys / 4; ++i) z[i] = fmaf(x, __bfloat162float(sk[c + 4 * i][d]), z[i]);
+            // No copy may be in flight when the CTA leaves (all have landed unless a role gave up).
+            for (uint32_t b = 0; b < 2 && b < unit; ++b) {
+                const uint32_t last = unit - 1 - ((unit - 1 - b) & 1u);  // last fill of buffer b
+                (void)mbar_wait(&q_full[b], (last >> 1) & 1u, p.wait_ns, p.status, kStatusTimeoutAttnLoad);
             }
-#pragma unroll
-            for (int i = 0; i < kKeys / 4; ++i) {
-                if (!keep[c + 4 * i]) z[i] = -INFINITY;
-                top = fmaxf(top, z[i]);
+            for (uint32_t st = 0; st < kStages && st < place; ++st) {
+                const uint32_t fills = (place - 1 - st) / kStages;       // index of the stage's last fill
+                (void)mbar_wait(&kv_full[st], fills & 1u, p.wait_ns, p.status, kStatusTimeoutAttnLoad);
             }
-            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-            const float m_new = fmaxf(m, top);
-            const float base = m_new == -INFINITY ? 0.0f : m_new * p.scale_log2;
-            const float f = exp2f(fmaf(m, p.scale_log2, -base));
-            l *= f;
+        } else if (warp == 1) {
+            // ------------------------------------------------------------ MMAs
+            constexpr uint32_t kIdescS = (1u << 4) | (1u << 7) | (1u << 10) | ((128u >> 3) << 17) | ((128u >> 4) << 24);
+            constexpr uint32_t kIdescO =
+                (1u << 4) | (1u << 7) | (1u << 10) | (1u << 16) | (((uint32_t)DP >> 3) << 17) | ((128u >> 4) << 24);
+            Piece cur, nxt;
+            uint32_t unit = 0, place = 0, gaps = 0;    // of cur: Q buffer count, first ring place, gap tiles before it
+            uint32_t p_count[2] = {0, 0}, o_count[2] = {0, 0};
+            int s_left = 0, s_left_next = 0;           // S products still to be issued
+            bool ok = true;
+            auto wait = [&](uint64_t* bar, uint32_t parity) {
+                ok = mbar_wait(bar, parity, p.wait_ns, p.status, kStatusTimeoutAttnMma);
+                ok = __all_sync(0xffffffffu, ok);
+                return ok;
+            };
+            auto s_total = [&](const Piece& u) { return tiles_for<kSolo>(u, 0, tok) + tiles_for<kSolo>(u, 1, tok); };
+            // S_X = Q_X K_i^T of unit u
+            auto issue_s = [&](const Piece& u, uint32_t un, uint32_t pl, int X, int i, int& left) {
+                const uint32_t at = pl + (uint32_t)k_place<kSolo>(tile_at<kSolo>(X, i)), st = at % kStages;
+                const uint32_t buf = un & 1u;
+                if (!wait(&q_full[buf], (un >> 1) & 1u) || !wait(&kv_full[st], (at / kStages) & 1u)) return;
+                tc_fence_after();
+                --left;
+                if (elect_one()) {
+                    const uint32_t q = smem_u32(smem) + (buf * L::kQTiles + (kSolo ? 0 : X)) * L::kTile;
+                    const uint32_t k = smem_u32(smem) + L::kKvOff + st * L::kTile;
 #pragma unroll
-            for (int i = 0; i < kKeys / 4; ++i) {
-                const float e = exp2f(fmaf(z[i], p.scale_log2, -base));
-                l += e;
-                sp[row][c + 4 * i] = e;
+                    for (int c = 0; c < DP / 16; ++c) {
+                        const uint32_t o = (c >> 2) * 16384 + (c & 3) * 32;
+                        mma_f16_ss(tmem + kTmS + 128 * X, smem_desc(q + o, 16, 1024, 2), smem_desc(k + o, 16, 1024, 2),
+                                   kIdescS, c > 0);
+                    }
+                    tc_commit(&s_full[X]);
+                    // the K tile's last use: always (solo); the second query tile, or the only one
+                    if (kSolo || X == 1 || u.ntok <= tok) tc_commit(&kv_empty[st]);
+                    if (left == 0) tc_commit(&q_empty[buf]);
+                }
+                __syncwarp();
+            };
+            bool have = walk.next_with_keys(cur);
+            if (have) {
+                s_left = s_total(cur);
+                issue_s(cur, 0, 0, 0, 0, s_left);
+                if (ok && tiles_for<kSolo>(cur, 1, tok) > 0) issue_s(cur, 0, 0, 1, 0, s_left);
             }
+            while (ok && have) {
+                const bool more = walk.next_with_keys(nxt);
+                if (more) s_left_next = s_total(nxt);
+                const uint32_t next_place = place + 2 * (uint32_t)cur.nt;
+                const int na = tiles_for<kSolo>(cur, 0, tok), nb = tiles_for<kSolo>(cur, 1, tok);
+                const uint32_t unit_gaps = gaps;
+                int seen = 0;  // tiles of the unit whose gaps are counted
+                for (int i = 0; i < na && ok; ++i) {
+                    for (int X = 0; X < 2 && ok; ++X) {
+                        const int n = X ? nb : na;
+                        if (i < n) {
+                            const int t = tile_at<kSolo>(X, i);
+                            const uint32_t at = place + (uint32_t)v_place<kSolo>(t, cur.nt), st = at % kStages;
+                            if (!wait(&p_full[X], p_count[X] & 1u)) break;
+                            ++p_count[X];
+                            if (i == 0 && !wait(&o_empty[X], (o_count[X] & 1u) ^ 1u)) break;
+                            if (!wait(&kv_full[st], (at / kStages) & 1u)) break;
+                            for (; seen < t; ++seen) gaps += has_gaps(p, cur, cur.t0 + seen);
+                            if (has_gaps(p, cur, cur.t0 + t) &&
+                                !wait(&mask_full[gaps % kMaskSlots], (gaps / kMaskSlots) & 1u))
+                                break;
+                            tc_fence_after();
+                            if (elect_one()) {
+                                const uint32_t v = smem_u32(smem) + L::kKvOff + st * L::kTile;
 #pragma unroll
-            for (int i = 0; i < kAttnMaxD / 4; ++i) acc[i] *= f;
-            m = m_new;
+                                for (int c = 0; c < 8; ++c)
+                                    mma_f16_ts(tmem + kTmO + DP * X, tmem + kTmS + 128 * X + 8 * c,
+                                               smem_desc(v + c * 2048, 16384, 1024, 2), kIdescO, i > 0 || c > 0);
+                                if (kSolo || X == 1 || nb == 0) tc_commit(&kv_empty[st]);
+                                if (i == n - 1) tc_commit(&o_full[X]);
+                            }
+                            __syncwarp();
+                            if (i == n - 1) ++o_count[X];
+                        }
+                        if (i + 1 < n)
+                            issue_s(cur, unit, place, X, i + 1, s_left);
+                        else if ((i + 1 == n || (n == 0 && i == na - 1)) && more && tiles_for<kSolo>(nxt, X, tok) > 0)
+                            issue_s(nxt, unit + 1, next_place, X, 0, s_left_next);
+                    }
+                }
+                if (!ok) break;
+                gaps = unit_gaps;
+                for (int t = 0; t < cur.nt; ++t) gaps += has_gaps(p, cur, cur.t0 + t);
+                ++unit;
+                place = next_place;
+                cur = nxt;
+                s_left = s_left_next;
+                have = more;
+            }
+            // All MMAs are done before TMEM and shared memory go.
+            if (elect_one()) tc_commit(done);
             __syncwarp();
-            for (int j = 0; j < kKeys; ++j) {
-                const float e = sp[row][j];
+            (void)mbar_wait(done, 0, p.wait_ns, p.status, kStatusTimeoutAttnMma);
+        } else if (warp == 2) {
+            // ------------------------------------------------------------ keys that are left out
+            Piece u;
+            uint32_t place = 0, gaps = 0;
+            bool ok = true;
+            while (ok && walk.next_with_keys(u)) {
+                for (int i = 0; i < u.nt && ok; ++i) {
+                    const int t = u.t0 + i;
+                    if (!has_gaps(p, u, t)) continue;
+                    const uint32_t at = place + (uint32_t)v_place<kSolo>(i, u.nt), st = at % kStages;
+                    // A parity tells a stage's fill from the one before it only once that one is done with,
+                    // so first the load has to be issued.  The V tile's arrival also says that the mask
+                    // slot's last reader is through: the ring holds fewer tiles than there are slots.
+                    const uint32_t slot = gaps % kMaskSlots;
+                    ok = mbar_wait(&gap_load[slot], (gaps / kMaskSlots) & 1u, p.wait_ns, p.status,
+                                   kStatusTimeoutAttnMask) &&
+                         mbar_wait(&kv_full[st], (at / kStages) & 1u, p.wait_ns, p.status, kStatusTimeoutAttnMask);
+                    ok = __all_sync(0xffffffffu, ok);
+                    if (!ok) break;
+                    const bool ctx = t < u.ctx_tiles;
+                    const uint8_t* mask = ctx ? p.ctx_mask : p.key_mask;
+                    const long long row = ctx ? t * kKeyTile : u.kv0 + (long long)(t - u.ctx_tiles) * kKeyTile;
+                    const int n = min(kKeyTile, ctx ? p.C - t * kKeyTile : u.kv_len - (t - u.ctx_tiles) * kKeyTile);
+                    uint32_t w[4];
+                    uint8_t* v = smem + L::kKvOff + st * L::kTile;
 #pragma unroll
-                for (int i = 0; i < kAttnMaxD / 4; ++i)
-                    if (c + 4 * i < p.D) acc[i] = fmaf(e, __bfloat162float(sv[j][c + 4 * i]), acc[i]);
+                    for (int j = 0; j < 4; ++j) {
+                        const int k = 32 * j + lane;
+                        const bool on = k < n && (mask == nullptr || mask[row + k] != 0);
+                        w[j] = __ballot_sync(0xffffffffu, on);
+                        if (!on)
+                            for (int c = 0; c < kChunks; ++c) {
+                                uint4* d = reinterpret_cast<uint4*>(v + c * 16384 + k * 128);
+#pragma unroll
+                                for (int x = 0; x < 8; ++x) d[x] = make_uint4(0, 0, 0, 0);
+                            }
+                    }
+                    if (lane == 0) mask_bits[slot] = make_uint4(w[0], w[1], w[2], w[3]);
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&mask_full[slot]);
+                    ++gaps;
+                }
+                place += 2 * (uint32_t)u.nt;
+            }
+        }
+    } else if (warp < 12) {
+        // ---------------------------------------------------------------- softmax of tile X
+        setmaxnreg_inc<kRegsSoftmax>();
+        const int X = (warp - 4) >> 2, quarter = warp & 3;
+        const int row = 32 * quarter + lane;
+        const uint32_t lanes = (uint32_t)(32 * quarter) << 16;
+        const uint32_t tS = tmem + kTmS + 128 * X + lanes, tO = tmem + kTmO + DP * X + lanes;
+        const uint64_t sl2 = f2(p.scale_log2, p.scale_log2);
+        Walk walk(p.t, blockIdx.x);
+        Piece u;
+        uint32_t s_count = 0, units = 0, gaps = 0;
+        bool ok = true;
+        while (ok && walk.next_with_keys(u)) {
+            const int n = tiles_for<kSolo>(u, X, tok);
+            const int rows = min(tok, u.ntok - (kSolo ? 0 : X * tok)) * p.t.pack;
+            const bool work = 32 * quarter < rows;   // some row of this warp is a query
+            float m = -INFINITY, l = 0.0f;
+            int seen = 0;
+            for (int i = 0; i < n; ++i) {
+                ok = mbar_wait(&s_full[X], s_count & 1u, p.wait_ns, p.status, kStatusTimeoutAttnSoftmax);
+                if (!__all_sync(0xffffffffu, ok)) {
+                    ok = false;
+                    break;
+                }
+                ++s_count;
+                const int t = tile_at<kSolo>(X, i);
+                for (; seen < t; ++seen) gaps += has_gaps(p, u, u.t0 + seen);
+                const bool gap = has_gaps(p, u, u.t0 + t);
+                tc_fence_after();
+                if (work) {
+                    uint32_t s[4][32];
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) tc_ld_32x32b_x32(tS + 32 * c, s[c]);
+                    tc_wait_ld();
+                    if (gap) {
+                        ok = mbar_wait(&mask_full[gaps % kMaskSlots], (gaps / kMaskSlots) & 1u, p.wait_ns, p.status,
+                                       kStatusTimeoutAttnSoftmax);
+                        if (!__all_sync(0xffffffffu, ok)) {
+                            ok = false;
+                            break;
+                        }
+                        const uint4 b = mask_bits[gaps % kMaskSlots];
+                        const uint32_t w[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+                        for (int c = 0; c < 4; ++c)
+#pragma unroll
+                            for (int j = 0; j < 32; ++j)
+                                if (!((w[c] >> j) & 1u)) s[c][j] = 0xFF800000u;  // -inf
+                    }
+                    float top[4];
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        top[c] = fmaxf(__uint_as_float(s[c][0]), __uint_as_float(s[c][1]));
+#pragma unroll
+                        for (int j = 2; j < 32; j += 2)
+                            top[c] = max3(top[c], __uint_as_float(s[c][j]), __uint_as_float(s[c][j + 1]));
+                    }
+                    const float m_new = fmaxf(m, fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])));
+                    if (__any_sync(0xffffffffu, row < rows && m_new > m + p.growth)) {
+                        const float f = m_new == m ? 1.0f : ex2_approx((m - m_new) * p.scale_log2);
+                        l *= f;
+                        m = m_new;
+                        if (i > 0) {  // S_X(i) is computed, so the MMAs into O_X before it are done
+                            const uint64_t ff = f2(f, f);
+#pragma unroll
+                            for (int c = 0; c < DP / 16; ++c) {
+                                uint32_t o[16];
+                                tc_ld_32x32b_x16(tO + 16 * c, o);
+                                tc_wait_ld();
+#pragma unroll
+                                for (int j = 0; j < 16; j += 2) {
+                                    float a, b;
+                                    unf2(mul2(f2(__uint_as_float(o[j]), __uint_as_float(o[j + 1])), ff), a, b);
+                                    o[j] = __float_as_uint(a);
+                                    o[j + 1] = __float_as_uint(b);
+                                }
+                                tc_st_32x32b_x16(tO + 16 * c, o);
+                            }
+                        }
+                    }
+                    const float base = m == -INFINITY ? 0.0f : -m * p.scale_log2;
+                    const uint64_t base2 = f2(base, base);
+                    uint64_t sum[4] = {0, 0, 0, 0};
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        uint32_t w[16];
+#pragma unroll
+                        for (int j = 0; j < 32; j += 2) {
+                            float a, b;
+                            unf2(fma2(f2(__uint_as_float(s[c][j]), __uint_as_float(s[c][j + 1])), sl2, base2), a, b);
+                            const uint64_t e = f2(ex2_approx(a), ex2_approx(b));
+                            sum[(j >> 1) & 3] = add2(sum[(j >> 1) & 3], e);
+                            w[j >> 1] = cvt_bf16x2(e);
+                        }
+                        tc_st_32x32b_x16(tS + 16 * c, w);
+                    }
+                    float a, b;
+                    unf2(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])), a, b);
+                    l += a + b;
+                    tc_wait_st();
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&p_full[X]);
+            }
+            if (!ok) break;
+            for (; seen < u.nt; ++seen) gaps += has_gaps(p, u, u.t0 + seen);
+            if (n > 0) {
+                ok = mbar_wait(&stat_empty[X], (units & 1u) ^ 1u, p.wait_ns, p.status, kStatusTimeoutAttnSoftmax);
+                if (!__all_sync(0xffffffffu, ok)) break;
+                stat[128 * X + row] = make_float2(m, l);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&stat_full[X]);
+                ++units;
+            }
+        }
+    } else {
+        // ---------------------------------------------------------------- epilogue
+        setmaxnreg_dec<kRegsEpilogue>();
+        const int quarter = warp & 3, row = 32 * quarter + lane;
+        const uint32_t lanes = (uint32_t)(32 * quarter) << 16;
+        const int row_tok = row / p.t.pack, row_head = row - row_tok * p.t.pack;
+        Walk walk(p.t, blockIdx.x);
+        Piece u;
+        uint32_t units[2] = {0, 0};
+        bool ok = true;
+        while (ok && walk.next(u)) {
+            const bool direct = u.whole;
+            const int kind = u.e < p.t.nseg ? 0 : 1;
+            const int tiles = kSolo ? 1 : (u.ntok > tok ? 2 : 1);
+            for (int Y = 0; Y < tiles && ok; ++Y) {  // a tile of queries
+                const int tokens = min(tok, u.ntok - Y * tok);
+                const bool on = row < tokens * p.t.pack;
+                const long long r = u.tok0 + Y * tok + row_tok;
+                const int h = u.head0 + row_head;
+                // parts of the tile: A and B (solo: the even and the odd key tiles)
+                const int nA = kSolo ? tiles_for<kSolo>(u, 0, tok) : u.nt, nB = kSolo ? tiles_for<kSolo>(u, 1, tok) : 0;
+                float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
+#pragma unroll
+                for (int x = 0; x < (kSolo ? 2 : 1); ++x) {
+                    if ((x ? nB : nA) == 0) continue;
+                    const int X = kSolo ? x : Y;
+                    ok = mbar_wait(&stat_full[X], units[X] & 1u, p.wait_ns, p.status, kStatusTimeoutAttnEpilogue) &&
+                         mbar_wait(&o_full[X], units[X] & 1u, p.wait_ns, p.status, kStatusTimeoutAttnEpilogue);
+                    ok = __all_sync(0xffffffffu, ok);
+                    if (!ok) break;
+                    const float2 st = stat[128 * X + row];
+                    m[x] = st.x;
+                    l[x] = st.y;
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&stat_empty[X]);
+                    ++units[X];
+                }
+                if (!ok) break;
+                tc_fence_after();
+                const float top = fmaxf(m[0], m[1]), top2 = top * p.scale_log2;
+                // weights of the two parts against the common maximum
+                float f0 = 1.0f, f1 = 0.0f, sum = l[0];
+                if (kSolo && nB > 0) {
+                    f0 = m[0] == top ? 1.0f : ex2_approx((m[0] - top) * p.scale_log2);
+                    f1 = m[1] == top ? 1.0f : ex2_approx((m[1] - top) * p.scale_log2);
+                    sum = l[0] * f0 + l[1] * f1;
+                }
+                float* slot = nullptr;
+                if (direct) {
+                    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;  // a row without a key: zeros
+                    f0 *= inv;
+                    f1 *= inv;
+                    if (on && p.lse)
+                        p.lse[r * p.Hq + h] =
+                            sum == 0.0f ? -INFINITY : (top2 + log2f(sum)) * 0.69314718055994531f;
+                } else {
+                    const int rows = p.slot_rows[kind];
+                    float* base = p.part[kind] + (long long)u.slot * rows * (DP + 2);
+                    const int at = Y * tok * p.t.pack + row;
+                    slot = base + (long long)at * DP;
+                    if (on) *reinterpret_cast<float2*>(base + (long long)rows * DP + 2 * at) = make_float2(
+                        sum == 0.0f ? -INFINITY : top2, sum);
+                }
+                __nv_bfloat16* o = p.out + r * p.out_row + (long long)h * p.out_head;
+#pragma unroll
+                for (int c = 0; c < DP / 32; ++c) {
+                    float v[32];
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) v[j] = 0.0f;
+                    if (nA > 0) {
+                        uint32_t a[32];
+                        tc_ld_32x32b_x32(tmem + kTmO + (kSolo ? 0 : DP * Y) + lanes + 32 * c, a);
+                        tc_wait_ld();
+                        // sums that are zero in place of what a row without a key has in TMEM
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) v[j] = f0 == 0.0f ? 0.0f : __uint_as_float(a[j]) * f0;
+                    }
+                    if (kSolo && nB > 0) {
+                        uint32_t a[32];
+                        tc_ld_32x32b_x32(tmem + kTmO + DP + lanes + 32 * c, a);
+                        tc_wait_ld();
+#pragma unroll
+                        for (int j = 0; j < 32; ++j)
+                            v[j] = f1 == 0.0f ? v[j] : fmaf(__uint_as_float(a[j]), f1, v[j]);
+                    }
+                    if (on && direct) {
+                        uint32_t w[16];
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) w[j] = cvt_bf16x2(f2(v[2 * j], v[2 * j + 1]));
+                        if (32 * c < p.D) store_row(o + 32 * c, w, p.D - 32 * c, p.wide_out != 0);
+                    } else if (on) {
+#pragma unroll
+                        for (int j = 0; j < 8; ++j)
+                            *reinterpret_cast<float4*>(slot + 32 * c + 4 * j) =
+                                make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+                    }
+                    __syncwarp();
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) {
+                    if (nA > 0) mbar_arrive(&o_empty[kSolo ? 0 : Y]);
+                    if (kSolo && nB > 0) mbar_arrive(&o_empty[1]);
+                }
             }
         }
     }
-    l += __shfl_xor_sync(0xffffffffu, l, 1);
-    l += __shfl_xor_sync(0xffffffffu, l, 2);
-    if (row >= rows) return;
-    const float inv = l == 0.0f ? 0.0f : 1.0f / l;  // a row without a key: zeros
-    __nv_bfloat16* o = p.out + (long long)(r0 + row) * p.out_row + h * p.out_head;
+    griddep_launch_dependents();
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 3) {
+        tc_fence_after();
+        tmem_dealloc(tmem, kTmemCols);
+    }
+}
+
+// ------------------------------------------------------------------ joining partial sums
+//
+// One warp per row of a unit of the pool: its partials, each with its maximum
+// (in base 2) and sum, joined as exp2(m_i - m) weights.  Reads each partial once.
+constexpr int kJoinThreads = 256;
+constexpr int kJoinRows = 16;
+
+template <int DP>
+__global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const __grid_constant__ AttnParams p)
+{
+    griddep_wait();
+    const AttnTable& t = p.t;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    // the unit (of the segments') and its partials
+    const int pu = blockIdx.x;
+    int e = 0;
+    {
+        int lo = 0, hi = t.nseg;
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (t.pool_unit[mid] <= pu) lo = mid;
+            else hi = mid;
+        }
+        e = lo;
+    }
+    const int n = t.steps(e), ul = pu - t.pool_unit[e], a = t.pool_step[e] + ul * n;
+    const int c0 = t.cta_of(a), c1 = t.cta_of(a + n - 1);
+    if (c0 == c1 && !t.separate) return;  // not cut: written by the first kernel
+    const int u = t.full(e) + ul, rb = t.row_blocks(e), hb = u / rb;
+    const int tok0 = t.q_begin(e) + (u - hb * rb) * t.unit_tok;
+    const int rows = min(t.unit_tok, t.q_end(e) - tok0) * t.pack;
+    constexpr int kV = DP / 32;  // columns per lane
+    for (int at = blockIdx.y * kJoinRows + warp; at < min(rows, (int)(blockIdx.y + 1) * kJoinRows);
+         at += kJoinThreads / 32) {
+        const int tk = at / t.pack, r = tok0 + tk, h = hb * t.pack + at - tk * t.pack;
+        float acc[kV], m = -INFINITY, l = 0.0f;
 #pragma unroll
-    for (int i = 0; i < kAttnMaxD / 4; ++i)
-        if (c + 4 * i < p.D) o[c + 4 * i] = __float2bfloat16_rn(acc[i] * inv);
-    if (p.lse && c == 0)
-        p.lse[(long long)(r0 + row) * p.Hq + h] =
-            l == 0.0f ? -INFINITY : (m * p.scale_log2 + log2f(l)) * 0.69314718055994531f;
+        for (int j = 0; j < kV; ++j) acc[j] = 0.0f;
+        // partials first, first + step, ... (n of them) of one kind, for row `in` of its unit
+        auto join = [&](int kind, int first, int last_cta, int first_cta, int in, bool numbered) {
+            const long long stride = (long long)p.slot_rows[kind] * (DP + 2);
+            for (int c = first_cta; c <= last_cta; ++c) {
+                const int slot = numbered ? first + c : cut_slot(c, c == first_cta);
+                const float* base = p.part[kind] + slot * stride;
+                const float2 ml = __ldg(reinterpret_cast<const float2*>(base + (long long)p.slot_rows[kind] * DP) + in);
+                if (ml.y == 0.0f) continue;
+                const float m_new = fmaxf(m, ml.x);
+                const float f = m == m_new ? 1.0f : ex2_approx(m - m_new);
+                const float g = ml.x == m_new ? 1.0f : ex2_approx(ml.x - m_new);
+                const float* src = base + (long long)in * DP + lane * kV;
+#pragma unroll
+                for (int j = 0; j < kV; ++j) acc[j] = acc[j] * f + __ldg(src + j) * g;
+                l = l * f + ml.y * g;
+                m = m_new;
+            }
+        };
+        if (!t.separate) {
+            // the first partial begins its unit; it is the last piece of its CTA unless the stretch
+            // begins with the unit (then too: a piece that starts its unit takes the second slot)
+            join(0, 0, c1, c0, at, false);
+        } else {
+            join(0, pu, c1, c0, at, true);
+            if (t.ctx_tiles > 0) {
+                const int ce = t.nseg, cn = t.steps(ce), crb = t.row_blocks(ce);
+                const int ub = r / t.unit_tok, cu = hb * crb + ub, ca = t.pool_step[ce] + cu * cn;
+                const int in = (r - ub * t.unit_tok) * t.pack + at - tk * t.pack;
+                join(1, cu, t.cta_of(ca + cn - 1), t.cta_of(ca), in, true);
+            }
+        }
+        const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+        __nv_bfloat16* o = p.out + (long long)r * p.out_row + (long long)h * p.out_head + lane * kV;
+#pragma unroll
+        for (int j = 0; j < kV; j += 2)
+            if (lane * kV + j < p.D) *reinterpret_cast<uint32_t*>(o + j) = cvt_bf16x2(f2(acc[j] * inv, acc[j + 1] * inv));
+        if (p.lse && lane == 0)
+            p.lse[(long long)r * p.Hq + h] = l == 0.0f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
+    }
+}
+
+// ------------------------------------------------------------------ host side
+
+// bf16 [rows][heads][D] as a tensor map with boxes of 64 columns x `heads_box` x `rows_box`.
+bool make_heads_map(CUtensorMap* map, const HeadsIn& x, int64_t rows, int heads, int D, int heads_box, int rows_box)
+{
+    EncodeTiledFn fn = get_encode_fn();
+    if (!fn) return false;
+    const cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)heads, (cuuint64_t)rows};
+    const cuuint64_t strides[2] = {(cuuint64_t)x.head * 2, (cuuint64_t)x.row * 2};
+    const cuuint32_t box[3] = {64, (cuuint32_t)heads_box, (cuuint32_t)rows_box};
+    const cuuint32_t es[3] = {1, 1, 1};
+    return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<__nv_bfloat16*>(x.p), dims, strides, box, es,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int DP, bool kSolo>
+cudaError_t run(const AttnPlan& pl, const CUtensorMap (&m)[5], const AttnParams& p, cudaStream_t s)
+{
+    auto kernel = attn_kernel<DP, kSolo>;
+    constexpr uint32_t bytes = Layout<DP, kSolo>::kBytes;
+    cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void*>(kernel), (int)bytes);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.gridDim = dim3((unsigned)pl.t.ctas);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = bytes;
+    cfg.stream = s;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    e = cudaLaunchKernelEx(&cfg, kernel, m[0], m[1], m[2], m[3], m[4], p);
+    if (e != cudaSuccess || !pl.join) return e;
+    cfg.gridDim = dim3((unsigned)pl.t.pool_unit[pl.t.nseg], (unsigned)((pl.slot_rows[0] + kJoinRows - 1) / kJoinRows));
+    cfg.blockDim = dim3(kJoinThreads);
+    cfg.dynamicSmemBytes = 0;
+    return cudaLaunchKernelEx(&cfg, attn_join_kernel<DP>, p);
 }
 
 }  // namespace
 
-size_t attn_workspace_bytes(const AttnJob& job)
-{
-    (void)job;
-    return 256;  // the status word
-}
+size_t attn_workspace_bytes(const AttnJob& job) { return make_plan(job).bytes; }
 
 cudaError_t launch_attn(const AttnJob& job, cudaStream_t s)
 {
+    const AttnPlan pl = make_plan(job);
     AttnParams p{};
-    p.q = job.q;
-    p.k = job.k;
-    p.v = job.v;
-    p.kc = job.kc;
-    p.vc = job.vc;
-    p.out = job.out;
-    p.out_row = job.out_row;
-    p.out_head = job.out_head;
-    p.lse = job.lse;
-    p.C = (int)job.C;
+    p.t = pl.t;
     p.Hq = job.Hq;
     p.group = job.Hq / job.Hkv;
     p.D = job.D;
-    p.nseg = job.nseg;
+    p.C = (int)job.C;
     p.key_mask = job.key_mask;
     p.ctx_mask = job.ctx_mask;
     p.scale_log2 = job.scale * 1.4426950408889634f;
-    for (int i = 0; i <= job.nseg; ++i) {
-        p.q_off[i] = (int)job.q_off[i];
-        p.kv_off[i] = (int)job.kv_off[i];
-        if (i < job.nseg) p.tiles[i + 1] = p.tiles[i] + (int)((job.q_off[i + 1] - job.q_off[i] + kRows - 1) / kRows);
+    p.growth = fminf(kGrowth / p.scale_log2, 1e38f);  // finite: -inf plus it stays -inf
+    p.out = job.out;
+    p.out_row = job.out_row;
+    p.out_head = job.out_head;
+    p.wide_out = job.D % 16 == 0 && job.out_row % 16 == 0 && job.out_head % 16 == 0 &&
+                 (reinterpret_cast<uintptr_t>(job.out) & 31u) == 0;
+    p.lse = job.lse;
+    for (int k = 0; k < 2; ++k) {
+        p.part[k] = reinterpret_cast<float*>(job.ws + pl.slot_off[k]);
+        p.slot_rows[k] = pl.slot_rows[k];
     }
-    attn_kernel<<<dim3((unsigned)p.tiles[job.nseg], (unsigned)job.Hq), kThreads, 0, s>>>(p);
-    return cudaGetLastError();
+    p.status = reinterpret_cast<unsigned int*>(job.ws + kWsStatus);
+    p.wait_ns = job.wait_limit_ns;
+    p.stall = job.stall;
+    const int chunks = pl.dp / 64;
+    p.q_bytes = (uint32_t)(chunks * 128 * pl.t.pack * pl.t.tok);
+    CUtensorMap m[5] = {};
+    if (!make_heads_map(&m[0], job.q, job.M, job.Hq, job.D, pl.t.pack, pl.t.tok)) return cudaErrorInvalidValue;
+    if (job.T > 0 && (!make_heads_map(&m[1], job.k, job.T, job.Hkv, job.D, 1, kKeyTile) ||
+                      !make_heads_map(&m[2], job.v, job.T, job.Hkv, job.D, 1, kKeyTile)))
+        return cudaErrorInvalidValue;
+    if (job.C > 0 && (!make_heads_map(&m[3], job.kc, job.C, job.Hkv, job.D, 1, kKeyTile) ||
+                      !make_heads_map(&m[4], job.vc, job.C, job.Hkv, job.D, 1, kKeyTile)))
+        return cudaErrorInvalidValue;
+    if (pl.dp == 64) return pl.solo ? run<64, true>(pl, m, p, s) : run<64, false>(pl, m, p, s);
+    return pl.solo ? run<128, true>(pl, m, p, s) : run<128, false>(pl, m, p, s);
 }
 
 }  // namespace h3fp4

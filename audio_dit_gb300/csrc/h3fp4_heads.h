@@ -53,10 +53,11 @@ struct AttnJob {
     const uint8_t* ctx_mask;   // device, C bytes or null
     float scale;
     uint8_t* ws;
+    int stall;                 // self-test: no loads, so every wait runs out
     uint64_t wait_limit_ns;
 };
 
-// Workspace bytes launch_attn needs for the sizes and tables of `job` (pointers unread).
+// Workspace bytes launch_attn needs for the sizes and tables of `job` (pointers unread); 0: more work than it counts.
 size_t attn_workspace_bytes(const AttnJob& job);
 
 cudaError_t launch_attn(const AttnJob& job, cudaStream_t s);

@@ -11,6 +11,8 @@ namespace {
 
 constexpr int64_t kMaxStride = (int64_t)1 << 38;  // elements: row pitches below the 2^40 bytes a TMA map holds
 
+constexpr int64_t kMaxRows = INT32_MAX - 255;  // rows are counted in 32 bits, up to two tiles past the last
+
 // Strides are positive multiples of 8 elements (16 bytes).
 bool good_strides(const h3fp4_heads& t)
 {
@@ -65,7 +67,7 @@ bool good_table(const int64_t* off, int nseg, int64_t rows)
 h3fp4_status attn_sizes(int64_t M, int64_t T, int64_t C, int Hq, int Hkv, int D, const int64_t* q_off,
                         const int64_t* kv_off, int nseg, int64_t* one_q, int64_t* one_kv, AttnJob* job)
 {
-    if (M < 0 || T < 0 || C < 0 || M > INT32_MAX || T > INT32_MAX || C > INT32_MAX) return H3FP4_ERR_SHAPE;
+    if (M < 0 || T < 0 || C < 0 || M > kMaxRows || T > kMaxRows || C > kMaxRows) return H3FP4_ERR_SHAPE;
     if (Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || D < 8 || D > kAttnMaxD || D % 8 != 0) return H3FP4_ERR_SHAPE;
     if (M * (int64_t)Hq > INT32_MAX) return H3FP4_ERR_SHAPE;
     if ((q_off == nullptr) != (kv_off == nullptr)) return H3FP4_ERR_INVALID;
@@ -107,7 +109,9 @@ h3fp4_status attn(const h3fp4_heads* q, const h3fp4_heads* k, const h3fp4_heads*
         (st = check_in(kc, C)) != H3FP4_OK || (st = check_in(vc, C)) != H3FP4_OK ||
         (st = check_out(out, M, Hq, D)) != H3FP4_OK)
         return st;
-    if (!ws || ws_bytes < attn_workspace_bytes(job)) return H3FP4_ERR_INVALID;
+    const size_t need = attn_workspace_bytes(job);
+    if (need == 0) return H3FP4_ERR_SHAPE;
+    if (!ws || ws_bytes < need) return H3FP4_ERR_INVALID;
     if (!aligned16(ws) || (reinterpret_cast<uintptr_t>(lse) & 3u)) return H3FP4_ERR_ALIGN;
     if (M > 0 && (out->ptr == q->ptr || (T > 0 && (out->ptr == k->ptr || out->ptr == v->ptr)) ||
                   (C > 0 && (out->ptr == kc->ptr || out->ptr == vc->ptr))))

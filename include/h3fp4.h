@@ -378,7 +378,8 @@ H3FP4_API h3fp4_status h3fp4_qk_norm_rope(const h3fp4_heads* q, const h3fp4_head
  * h / (Hq / Hkv) for query head h (grouped heads).  Scores, statistics and sums
  * are fp32; the p_j are rounded to bf16 for their product with V.
  *   q: [M][Hq][D]; k, v: [T][Hkv][D]; out: [M][Hq][D].  Hq % Hkv == 0,
- *      D % 8 == 0, 8 <= D <= 128, M, T < 2^31.
+ *      D % 8 == 0, 8 <= D <= 128, M, T <= 2^31 - 256, M * Hq < 2^31; at most
+ *      2^31 - 1 products of a 128-row query tile with a 128-key tile.
  *   q_off, kv_off: HOST arrays of nseg + 1 row offsets (0 first, non-decreasing,
  *      M and T last); segment i of the rows attends to segment i of the keys.
  *      Segments may be empty.  Both NULL: one segment.

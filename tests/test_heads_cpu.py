@@ -63,7 +63,8 @@ def attn(lib, q=None, k=None, v=None, kc=None, vc=None, M=4, T=9, ctx=0, Hq=2, H
 
 def test_attention_refusals(lib):
     for kw in (dict(D=4), dict(D=20), dict(D=136), dict(Hq=3), dict(Hq=0), dict(Hkv=0), dict(M=-1), dict(T=-1),
-               dict(M=1 << 31), dict(T=1 << 31), dict(q_off=[0] * 257 + [4], kv_off=[0] * 257 + [9], nseg=257),
+               dict(M=1 << 31), dict(T=1 << 31), dict(T=(1 << 31) - 255), dict(M=1 << 30, Hq=2),
+               dict(M=1 << 26, T=(1 << 31) - 256), dict(q_off=[0] * 257 + [4], kv_off=[0] * 257 + [9], nseg=257),
                dict(q_off=[0, 4], kv_off=[0, 9], nseg=0)):
         assert attn(lib, **kw) == SHAPE, kw
     for kw in (dict(q_off=[0, 4]), dict(kv_off=[0, 9]), dict(nseg=2), dict(q_off=[0, 3], kv_off=[0, 9]),
