@@ -40,6 +40,7 @@ struct AttnTable {
     int ctx_tiles;         // key tiles of the context
     int separate;
     int any_full;          // some entry has whole waves
+    int ctx_masked, own_masked, ctx_ragged;  // masks are given; the context's length is no multiple of a tile
     int pool_steps, pool_units;
     int M;
     int q_off[H3FP4_ATTN_MAX_SEGMENTS + 1];
@@ -110,8 +111,16 @@ struct Piece {
     int t0, nt;
     int ctx_tiles;          // tiles below this index are the context's
     int own_tiles, kv0, kv_len;
+    bool gaps_ctx, gaps_own;  // every tile of that source has keys that may be left out (a mask)
+    int gap_ctx, gap_own;     // else the tile whose end lies past the source's last key, or -1
     bool whole;             // all steps of the unit
     int slot;               // of the partial sums, if not whole (or separate plan)
+
+    // Whether tile t of the unit has keys that are left out.
+    __host__ __device__ bool has_gaps(int t) const
+    {
+        return t < ctx_tiles ? gaps_ctx || t == gap_ctx : gaps_own || t == gap_own;
+    }
 };
 
 // The pieces of this CTA, in order; every role walks them by itself.
@@ -137,6 +146,10 @@ struct Walk {
         p.own_tiles = t.tiles_own(entry);
         p.kv0 = entry < t.nseg ? t.kv_off[entry] : 0;
         p.kv_len = entry < t.nseg ? t.kv_off[entry + 1] - p.kv0 : 0;
+        p.gaps_ctx = t.ctx_masked != 0;
+        p.gaps_own = t.own_masked != 0;
+        p.gap_ctx = t.ctx_ragged && p.ctx_tiles > 0 ? p.ctx_tiles - 1 : -1;
+        p.gap_own = (p.kv_len & (kKeyTile - 1)) ? p.ctx_tiles + p.own_tiles - 1 : -1;
     }
     __host__ __device__ bool next(Piece& p)
     {
@@ -200,6 +213,7 @@ inline void lay_out(const Job& job, int pack, bool solo, bool separate, AttnTabl
     t.head_blocks = job.Hq / pack;
     t.ctx_tiles = (int)((job.C + kKeyTile - 1) / kKeyTile);
     t.separate = separate ? 1 : 0;
+    t.ctx_ragged = job.C % kKeyTile != 0;
     t.M = (int)job.M;
     t.ctas = kAttnCtas;
 }

@@ -90,14 +90,6 @@ struct AttnParams {
     int stall;                     // self-test: the loads are left out, so every wait runs out
 };
 
-// Whether key tile t (of the unit) has keys that are left out, and how many such
-// tiles a piece has before it.
-__device__ __forceinline__ bool has_gaps(const AttnParams& p, const Piece& u, int t)
-{
-    if (t < u.ctx_tiles) return p.ctx_mask != nullptr || (t == u.ctx_tiles - 1 && (p.C & 127) != 0);
-    return p.key_mask != nullptr || (t == u.ctx_tiles + u.own_tiles - 1 && (u.kv_len & 127) != 0);
-}
-
 // Tiles of a piece for query tile X: how many, and which is the i-th (relative to t0).
 template <bool kSolo>
 __device__ __forceinline__ int tiles_for(const Piece& u, int X, int tok)
@@ -271,9 +263,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                         uint8_t* d = smem + L::kKvOff + st * L::kTile;
                         mbar_arrive_expect_tx(&kv_full[st], L::kTile);
                         for (int c = 0; c < kChunks; ++c) tma_load_3d(d + c * 16384, map, &kv_full[st], 64 * c, hk, row);
-                        if (is_v && has_gaps(p, u, t)) mbar_arrive(&gap_load[gaps % kMaskSlots]);
+                        if (is_v && u.has_gaps(t)) mbar_arrive(&gap_load[gaps % kMaskSlots]);
                     }
-                    gaps += is_v && has_gaps(p, u, t);
+                    gaps += is_v && u.has_gaps(t);
                 }
             }
             // No copy may be in flight when the CTA leaves (all have landed unless a role gave up).
@@ -290,36 +282,44 @@ __global__ void __launch_bounds__(kThreads, 1)
             constexpr uint32_t kIdescS = (1u << 4) | (1u << 7) | (1u << 10) | ((128u >> 3) << 17) | ((128u >> 4) << 24);
             constexpr uint32_t kIdescO =
                 (1u << 4) | (1u << 7) | (1u << 10) | (1u << 16) | (((uint32_t)DP >> 3) << 17) | ((128u >> 4) << 24);
+            // Descriptors without their addresses; offsets inside a tile are added
+            // in their units of 16 bytes.
+            constexpr uint64_t kDescK = (1ull << 16) | (64ull << 32) | (1ull << 46) | (2ull << 61);
+            constexpr uint64_t kDescV = (1024ull << 16) | (64ull << 32) | (1ull << 46) | (2ull << 61);
+            const uint32_t sbase = uniform(smem_u32(smem) >> 4);
+            const uint32_t tm = uniform(tmem);
             Piece cur, nxt;
             uint32_t unit = 0, place = 0, gaps = 0;    // of cur: Q buffer count, first ring place, gap tiles before it
-            uint32_t p_count[2] = {0, 0}, o_count[2] = {0, 0};
+            uint32_t p_phase = 0, o_phase = 0;         // bit X: parity of the next P, of the units O_X has held
             int s_left = 0, s_left_next = 0;           // S products still to be issued
             bool ok = true;
             auto wait = [&](uint64_t* bar, uint32_t parity) {
-                ok = mbar_wait(bar, parity, p.wait_ns, p.status, kStatusTimeoutAttnMma);
-                ok = __all_sync(0xffffffffu, ok);
+                ok = __all_sync(0xffffffffu, mbar_wait(bar, parity, p.wait_ns, p.status, kStatusTimeoutAttnMma));
                 return ok;
             };
             auto s_total = [&](const Piece& u) { return tiles_for<kSolo>(u, 0, tok) + tiles_for<kSolo>(u, 1, tok); };
-            // S_X = Q_X K_i^T of unit u
+            // S_X = Q_X K_i^T of unit u.  The pair's second query tile finds the waits done by the first.
             auto issue_s = [&](const Piece& u, uint32_t un, uint32_t pl, int X, int i, int& left) {
                 const uint32_t at = pl + (uint32_t)k_place<kSolo>(tile_at<kSolo>(X, i)), st = at % kStages;
                 const uint32_t buf = un & 1u;
-                if (!wait(&q_full[buf], (un >> 1) & 1u) || !wait(&kv_full[st], (at / kStages) & 1u)) return;
-                tc_fence_after();
+                if (kSolo || X == 0) {
+                    if (i == 0 && !wait(&q_full[buf], (un >> 1) & 1u)) return;
+                    if (!wait(&kv_full[st], (at / kStages) & 1u)) return;
+                    tc_fence_after();
+                }
                 --left;
+                const uint64_t q = kDescK + (sbase + (buf * L::kQTiles + (kSolo ? 0 : X)) * (L::kTile >> 4));
+                const uint64_t k = kDescK + (sbase + ((L::kKvOff + st * L::kTile) >> 4));
+                const bool last_k = kSolo || X == 1 || u.ntok <= tok;
                 if (elect_one()) {
-                    const uint32_t q = smem_u32(smem) + (buf * L::kQTiles + (kSolo ? 0 : X)) * L::kTile;
-                    const uint32_t k = smem_u32(smem) + L::kKvOff + st * L::kTile;
 #pragma unroll
                     for (int c = 0; c < DP / 16; ++c) {
-                        const uint32_t o = (c >> 2) * 16384 + (c & 3) * 32;
-                        mma_f16_ss(tmem + kTmS + 128 * X, smem_desc(q + o, 16, 1024, 2), smem_desc(k + o, 16, 1024, 2),
-                                   kIdescS, c > 0);
+                        const uint32_t o = (c >> 2) * 1024 + (c & 3) * 2;
+                        mma_f16_ss(tm + kTmS + 128 * X, q + o, k + o, kIdescS, c > 0);
                     }
                     tc_commit(&s_full[X]);
                     // the K tile's last use: always (solo); the second query tile, or the only one
-                    if (kSolo || X == 1 || u.ntok <= tok) tc_commit(&kv_empty[st]);
+                    if (last_k) tc_commit(&kv_empty[st]);
                     if (left == 0) tc_commit(&q_empty[buf]);
                 }
                 __syncwarp();
@@ -335,35 +335,37 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (more) s_left_next = s_total(nxt);
                 const uint32_t next_place = place + 2 * (uint32_t)cur.nt;
                 const int na = tiles_for<kSolo>(cur, 0, tok), nb = tiles_for<kSolo>(cur, 1, tok);
-                const uint32_t unit_gaps = gaps;
-                int seen = 0;  // tiles of the unit whose gaps are counted
                 for (int i = 0; i < na && ok; ++i) {
-                    for (int X = 0; X < 2 && ok; ++X) {
+#pragma unroll
+                    for (int X = 0; X < 2; ++X) {
                         const int n = X ? nb : na;
-                        if (i < n) {
+                        if (ok && i < n) {
                             const int t = tile_at<kSolo>(X, i);
                             const uint32_t at = place + (uint32_t)v_place<kSolo>(t, cur.nt), st = at % kStages;
-                            if (!wait(&p_full[X], p_count[X] & 1u)) break;
-                            ++p_count[X];
-                            if (i == 0 && !wait(&o_empty[X], (o_count[X] & 1u) ^ 1u)) break;
-                            if (!wait(&kv_full[st], (at / kStages) & 1u)) break;
-                            for (; seen < t; ++seen) gaps += has_gaps(p, cur, cur.t0 + seen);
-                            if (has_gaps(p, cur, cur.t0 + t) &&
-                                !wait(&mask_full[gaps % kMaskSlots], (gaps / kMaskSlots) & 1u))
-                                break;
+                            if (!wait(&p_full[X], (p_phase >> X) & 1u)) break;
+                            p_phase ^= 1u << X;
+                            if (i == 0 && !wait(&o_empty[X], ((o_phase >> X) & 1u) ^ 1u)) break;
+                            const bool gap = cur.has_gaps(cur.t0 + t);
+                            if (kSolo || X == 0) {
+                                if (!wait(&kv_full[st], (at / kStages) & 1u)) break;
+                                if (gap && !wait(&mask_full[gaps % kMaskSlots], (gaps / kMaskSlots) & 1u)) break;
+                            }
+                            const bool last_v = kSolo || X == 1 || nb == 0;
+                            if (last_v) gaps += gap;
                             tc_fence_after();
+                            const uint64_t v = kDescV + (sbase + ((L::kKvOff + st * L::kTile) >> 4));
                             if (elect_one()) {
-                                const uint32_t v = smem_u32(smem) + L::kKvOff + st * L::kTile;
 #pragma unroll
                                 for (int c = 0; c < 8; ++c)
-                                    mma_f16_ts(tmem + kTmO + DP * X, tmem + kTmS + 128 * X + 8 * c,
-                                               smem_desc(v + c * 2048, 16384, 1024, 2), kIdescO, i > 0 || c > 0);
-                                if (kSolo || X == 1 || nb == 0) tc_commit(&kv_empty[st]);
+                                    mma_f16_ts(tm + kTmO + DP * X, tm + kTmS + 128 * X + 8 * c, v + c * 128, kIdescO,
+                                               i > 0 || c > 0);
+                                if (last_v) tc_commit(&kv_empty[st]);
                                 if (i == n - 1) tc_commit(&o_full[X]);
                             }
                             __syncwarp();
-                            if (i == n - 1) ++o_count[X];
+                            if (i == n - 1) o_phase ^= 1u << X;
                         }
+                        if (!ok) break;
                         if (i + 1 < n)
                             issue_s(cur, unit, place, X, i + 1, s_left);
                         else if ((i + 1 == n || (n == 0 && i == na - 1)) && more && tiles_for<kSolo>(nxt, X, tok) > 0)
@@ -371,8 +373,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
                 if (!ok) break;
-                gaps = unit_gaps;
-                for (int t = 0; t < cur.nt; ++t) gaps += has_gaps(p, cur, cur.t0 + t);
                 ++unit;
                 place = next_place;
                 cur = nxt;
@@ -391,7 +391,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             while (ok && walk.next_with_keys(u)) {
                 for (int i = 0; i < u.nt && ok; ++i) {
                     const int t = u.t0 + i;
-                    if (!has_gaps(p, u, t)) continue;
+                    if (!u.has_gaps(t)) continue;
                     const uint32_t at = place + (uint32_t)v_place<kSolo>(i, u.nt), st = at % kStages;
                     // A parity tells a stage's fill from the one before it only once that one is done with,
                     // so first the load has to be issued.  The V tile's arrival also says that the mask
@@ -455,8 +455,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 ++s_count;
                 const int t = tile_at<kSolo>(X, i);
-                for (; seen < t; ++seen) gaps += has_gaps(p, u, u.t0 + seen);
-                const bool gap = has_gaps(p, u, u.t0 + t);
+                for (; seen < t; ++seen) gaps += u.has_gaps(u.t0 + seen);
+                const bool gap = u.has_gaps(u.t0 + t);
                 tc_fence_after();
                 if (work) {
                     uint32_t s[4][32];
@@ -488,7 +488,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     const float m_new = fmaxf(m, fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])));
                     if (__any_sync(0xffffffffu, row < rows && m_new > m + p.growth)) {
-                        const float f = m_new == m ? 1.0f : ex2_approx((m - m_new) * p.scale_log2);
+                        const float f = m_new == m ? 1.0f : ex2_approx_ftz((m - m_new) * p.scale_log2);
                         l *= f;
                         m = m_new;
                         if (i > 0) {  // S_X(i) is computed, so the MMAs into O_X before it are done
@@ -519,7 +519,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         for (int j = 0; j < 32; j += 2) {
                             float a, b;
                             unf2(fma2(f2(__uint_as_float(s[c][j]), __uint_as_float(s[c][j + 1])), sl2, base2), a, b);
-                            const uint64_t e = f2(ex2_approx(a), ex2_approx(b));
+                            const uint64_t e = f2(ex2_approx_ftz(a), ex2_approx_ftz(b));
                             sum[(j >> 1) & 3] = add2(sum[(j >> 1) & 3], e);
                             w[j >> 1] = cvt_bf16x2(e);
                         }
@@ -535,7 +535,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (lane == 0) mbar_arrive(&p_full[X]);
             }
             if (!ok) break;
-            for (; seen < u.nt; ++seen) gaps += has_gaps(p, u, u.t0 + seen);
+            for (; seen < u.nt; ++seen) gaps += u.has_gaps(u.t0 + seen);
             if (n > 0) {
                 ok = mbar_wait(&stat_empty[X], (units & 1u) ^ 1u, p.wait_ns, p.status, kStatusTimeoutAttnSoftmax);
                 if (!__all_sync(0xffffffffu, ok)) break;
@@ -588,8 +588,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // weights of the two parts against the common maximum
                 float f0 = 1.0f, f1 = 0.0f, sum = l[0];
                 if (kSolo && nB > 0) {
-                    f0 = m[0] == top ? 1.0f : ex2_approx((m[0] - top) * p.scale_log2);
-                    f1 = m[1] == top ? 1.0f : ex2_approx((m[1] - top) * p.scale_log2);
+                    f0 = m[0] == top ? 1.0f : ex2_approx_ftz((m[0] - top) * p.scale_log2);
+                    f1 = m[1] == top ? 1.0f : ex2_approx_ftz((m[1] - top) * p.scale_log2);
                     sum = l[0] * f0 + l[1] * f1;
                 }
                 float* slot = nullptr;
@@ -708,8 +708,8 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const __grid_co
                 const float2 ml = __ldg(reinterpret_cast<const float2*>(base + (long long)p.slot_rows[kind] * DP) + in);
                 if (ml.y == 0.0f) continue;
                 const float m_new = fmaxf(m, ml.x);
-                const float f = m == m_new ? 1.0f : ex2_approx(m - m_new);
-                const float g = ml.x == m_new ? 1.0f : ex2_approx(ml.x - m_new);
+                const float f = m == m_new ? 1.0f : ex2_approx_ftz(m - m_new);
+                const float g = ml.x == m_new ? 1.0f : ex2_approx_ftz(ml.x - m_new);
                 const float* src = base + (long long)in * DP + lane * kV;
 #pragma unroll
                 for (int j = 0; j < kV; ++j) acc[j] = acc[j] * f + __ldg(src + j) * g;
@@ -790,6 +790,8 @@ cudaError_t launch_attn(const AttnJob& job, cudaStream_t s)
     const AttnPlan pl = make_plan(job);
     AttnParams p{};
     p.t = pl.t;
+    p.t.own_masked = job.key_mask != nullptr;
+    p.t.ctx_masked = job.ctx_mask != nullptr;
     p.Hq = job.Hq;
     p.group = job.Hq / job.Hkv;
     p.D = job.D;

@@ -283,6 +283,10 @@ __device__ __forceinline__ void tc_ld_32x32b_x16(uint32_t taddr, uint32_t (&v)[1
         : "memory");
 }
 
+// A value that is the same in all lanes, in a form the compiler can keep in a
+// uniform register (where the MMA instructions want theirs).
+__device__ __forceinline__ uint32_t uniform(uint32_t v) { return __shfl_sync(0xffffffffu, v, 0); }
+
 // ------------------------------------------------------------------ narrow converts
 
 // fp32 -> E4M3 code (round to nearest even, saturating to 448).
@@ -536,6 +540,15 @@ __device__ __forceinline__ float ex2_approx(float x)
 {
     float y;
     asm("ex2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// The same with subnormal arguments and results flushed to zero: one instruction,
+// where the form above scales its argument and result.
+__device__ __forceinline__ float ex2_approx_ftz(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
 
