@@ -31,6 +31,8 @@ constexpr int kAttnCtas = 152;   // one per SM of the GB300
 constexpr int kSnap = 4;
 constexpr int kAttnEntries = H3FP4_ATTN_MAX_SEGMENTS + 1;
 
+__host__ __device__ inline int lesser(int a, int b) { return a < b ? a : b; }
+
 struct AttnTable {
     int nseg, entries;     // entries = nseg (+ 1: the context's, separate plan)
     int ctas;
@@ -99,8 +101,6 @@ struct AttnTable {
     }
 };
 
-__host__ __device__ inline int lesser(int a, int b) { return a < b ? a : b; }
-
 // A stretch of the pool has at most two cut units: its first, begun by another
 // CTA, and its last, which it begins itself.
 __host__ __device__ inline int cut_slot(int cta, bool begins_unit) { return 2 * cta + (begins_unit ? 1 : 0); }
@@ -120,6 +120,12 @@ struct Piece {
     __host__ __device__ bool has_gaps(int t) const
     {
         return t < ctx_tiles ? gaps_ctx || t == gap_ctx : gaps_own || t == gap_own;
+    }
+    // How many such tiles there are among [t0, t).
+    __host__ __device__ int gaps_before(int t) const
+    {
+        const int c = lesser(t, ctx_tiles) - lesser(t0, ctx_tiles), o = t - t0 - c;
+        return (gaps_ctx ? c : (int)(t0 <= gap_ctx && gap_ctx < t)) + (gaps_own ? o : (int)(t0 <= gap_own && gap_own < t));
     }
 };
 

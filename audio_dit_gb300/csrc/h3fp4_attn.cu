@@ -18,14 +18,15 @@
 // Roles (512 threads, one CTA per SM):
 //   warp 0       loads: Q tiles (two buffers) and a ring of K and V tiles by TMA,
 //                128-byte swizzled 64-column chunks; columns past D are zero-filled
-//   warp 1       issues the MMAs.  Per query tile X and key tile: S_X = Q_X K^T,
-//                then, once the softmax stored P_X over S_X's first columns,
-//                O_X += P_X V.  The two tiles alternate, so that one tile's MMAs
-//                run under the other's softmax.
-//   warp 2       keys that are left out (a mask, the end of a segment inside a
-//                tile): their bits for the softmax, and zeros over their rows of
-//                the V tile, since 0 * NaN is not 0
-//   warp 3       allocates TMEM
+//   warps 1, 3   issue the MMAs of query tile A, of tile B.  Per key tile: S_X =
+//                Q_X K^T, then, once the softmax stored P_X over S_X's first
+//                columns (in two halves), O_X += P_X V.  One tile's MMAs run under
+//                the other's softmax.  A warp of its own per tile, since the
+//                waits and bookkeeping around a tile's sixteen MMAs take one warp
+//                about as long as the MMAs themselves.
+//   warp 2       allocates TMEM; keys that are left out (a mask, the end of a
+//                segment inside a tile): their bits for the softmax, and zeros
+//                over their rows of the V tile, since 0 * NaN is not 0
 //   warps 4-11   softmax of tile A, of tile B (a warpgroup each)
 //   warps 12-15  epilogue: divides by l, rounds, stores; or stores partial sums
 // The epilogue of a unit overlaps the next unit's first MMAs and softmax.
@@ -50,7 +51,7 @@ constexpr int kThreads = 512;
 constexpr float kGrowth = 8.0f;      // log2 of how far the true maximum may pass the one in use
 constexpr int kMaskSlots = 16;
 constexpr uint32_t kTmemCols = 512;
-constexpr uint32_t kRegsControl = 56, kRegsSoftmax = 184, kRegsEpilogue = 88;
+constexpr uint32_t kRegsControl = 80, kRegsSoftmax = 176, kRegsEpilogue = 80;
 static_assert(kRegsControl + 2 * kRegsSoftmax + kRegsEpilogue <= 512, "setmaxnreg shares exceed the launch budget");
 
 constexpr unsigned int kStatusTimeoutAttnLoad = 64u, kStatusTimeoutAttnMma = 128u, kStatusTimeoutAttnSoftmax = 256u,
@@ -59,13 +60,15 @@ constexpr unsigned int kStatusTimeoutAttnLoad = 64u, kStatusTimeoutAttnMma = 128
 template <int DP, bool kSolo>
 struct Layout {
     static constexpr uint32_t kTile = 128 * DP * 2;   // bytes of a 128-row tile
-    static constexpr int kQTiles = kSolo ? 1 : 2;     // per buffer
-    static constexpr int kStages = (7 - 2 * kQTiles) * (128 / DP);
-    static constexpr uint32_t kKvOff = 2 * kQTiles * kTile;
+    // Q tiles: one more than a unit has, so that the next unit's first tile is there
+    // when this unit's last products are issued; the rest holds K and V tiles.
+    static constexpr int kQ = kSolo ? 2 : 3;
+    static constexpr int kStages = (7 - kQ) * (128 / DP);
+    static constexpr uint32_t kKvOff = kQ * kTile;
     static constexpr uint32_t kBarOff = kKvOff + kStages * kTile;
-    // barriers: q_full, q_empty (2 each), kv_full, kv_empty (per stage), s_full, p_full, o_full, o_empty,
-    // stat_full, stat_empty (2 each), gap_load, mask_full (per slot), done
-    static constexpr int kBars = 4 + 2 * kStages + 12 + 2 * kMaskSlots + 1;
+    // barriers: q_full, q_empty (per Q tile), kv_full, kv_empty (per stage), s_full, p_half, p_full, o_full,
+    // o_empty, stat_full, stat_empty (2 each), gap_load, mask_full (per slot), done
+    static constexpr int kBars = 2 * kQ + 2 * kStages + 14 + 2 * kMaskSlots + 2;
     static constexpr uint32_t kMaskOff = kBarOff + (kBars * 8 + 8 + 15) / 16 * 16;
     static constexpr uint32_t kStatOff = kMaskOff + kMaskSlots * 16;
     static constexpr uint32_t kBytes = kStatOff + 2 * 128 * 8;
@@ -152,12 +155,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         griddep_wait();
         return;
     }
-    uint64_t* q_full = reinterpret_cast<uint64_t*>(smem + L::kBarOff);  // per Q buffer: its tiles landed
-    uint64_t* q_empty = q_full + 2;                 // the unit's last S was computed
-    uint64_t* kv_full = q_empty + 2;                // per stage: the K or V tile landed
+    uint64_t* q_full = reinterpret_cast<uint64_t*>(smem + L::kBarOff);  // per Q place: the tile landed
+    uint64_t* q_empty = q_full + L::kQ;             // its last S was computed
+    uint64_t* kv_full = q_empty + L::kQ;               // per stage: the K or V tile landed
     uint64_t* kv_empty = kv_full + kStages;         // its MMAs are done
     uint64_t* s_full = kv_empty + kStages;          // per query tile: S computed (and the MMAs before it done)
-    uint64_t* p_full = s_full + 2;                  // P stored, O rescaled where it had to be
+    uint64_t* p_half = s_full + 2;                  // P's first 64 keys stored, O rescaled where it had to be
+    uint64_t* p_full = p_half + 2;                  // all of P stored
     uint64_t* o_full = p_full + 2;                  // O complete
     uint64_t* o_empty = o_full + 2;                 // O read by the epilogue
     uint64_t* stat_full = o_empty + 2;              // maximum and sum of each row stored
@@ -165,30 +169,33 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint64_t* gap_load = stat_empty + 2;            // per slot: the load of a V tile with gaps was issued
     uint64_t* mask_full = gap_load + kMaskSlots;    // per slot: bits stored, V rows zeroed
     uint64_t* done = mask_full + kMaskSlots;
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done + 1);
-    uint4* mask_bits = reinterpret_cast<uint4*>(smem + L::kMaskOff);
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done + 2);
+    uint32_t* mask_bits = reinterpret_cast<uint32_t*>(smem + L::kMaskOff);
     float2* stat = reinterpret_cast<float2*>(smem + L::kStatOff);  // [2][128]: (maximum, sum)
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < 2; ++i) {
-            mbar_init(&q_full[i], 1);
-            mbar_init(&q_empty[i], 1);
+            mbar_init(&done[i], 1);
             mbar_init(&s_full[i], 1);
+            mbar_init(&p_half[i], 4);
             mbar_init(&p_full[i], 4);
             mbar_init(&o_full[i], 1);
             mbar_init(&o_empty[i], 4);
             mbar_init(&stat_full[i], 4);
             mbar_init(&stat_empty[i], 4);
         }
+        for (int i = 0; i < L::kQ; ++i) {
+            mbar_init(&q_full[i], 1);
+            mbar_init(&q_empty[i], kSolo ? 2 : 1);
+        }
         for (int i = 0; i < kStages; ++i) {
             mbar_init(&kv_full[i], 1);
-            mbar_init(&kv_empty[i], 1);
+            mbar_init(&kv_empty[i], kSolo ? 1 : 2);
         }
         for (int i = 0; i < kMaskSlots; ++i) {
             mbar_init(&gap_load[i], 1);
             mbar_init(&mask_full[i], 1);
         }
-        mbar_init(done, 1);
         fence_mbarrier_init();
         prefetch_tensormap(&tmQ);
         prefetch_tensormap(&tmK);
@@ -198,7 +205,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             prefetch_tensormap(&tmVc);
         }
     }
-    if (warp == 3) {
+    if (warp == 2) {
         tmem_alloc(tmem_slot, kTmemCols);
         tmem_relinquish();
     }
@@ -217,25 +224,26 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (warp == 0) {
             // ------------------------------------------------------------ loads
             Piece u;
-            uint32_t unit = 0, place = 0, gaps = 0;
+            uint32_t q_place = 0, place = 0, gaps = 0;
             bool ok = p.stall == 0;
             while (ok && walk.next_with_keys(u)) {
-                const uint32_t buf = unit & 1u;
-                const bool two = !kSolo && u.ntok > tok;
-                ok = mbar_wait(&q_empty[buf], ((unit >> 1) & 1u) ^ 1u, p.wait_ns, p.status, kStatusTimeoutAttnLoad);
-                if (!__all_sync(0xffffffffu, ok)) {
-                    ok = false;
-                    break;
-                }
-                if (elect_one()) {
-                    uint8_t* q = smem + buf * L::kQTiles * L::kTile;
-                    mbar_arrive_expect_tx(&q_full[buf], p.q_bytes * (two ? 2u : 1u));
-                    for (int X = 0; X < (two ? 2 : 1); ++X)
+                const int tiles = !kSolo && u.ntok > tok ? 2 : 1;
+                for (int X = 0; X < tiles; ++X, ++q_place) {
+                    const uint32_t st = q_place % L::kQ;
+                    ok = mbar_wait(&q_empty[st], ((q_place / L::kQ) & 1u) ^ 1u, p.wait_ns, p.status,
+                                   kStatusTimeoutAttnLoad);
+                    if (!__all_sync(0xffffffffu, ok)) {
+                        ok = false;
+                        break;
+                    }
+                    if (elect_one()) {
+                        mbar_arrive_expect_tx(&q_full[st], p.q_bytes);
                         for (int c = 0; c < kChunks; ++c)
-                            tma_load_3d(q + X * L::kTile + c * 16384, &tmQ, &q_full[buf], 64 * c, u.head0,
+                            tma_load_3d(smem + st * L::kTile + c * 16384, &tmQ, &q_full[st], 64 * c, u.head0,
                                         u.tok0 + X * tok);
+                    }
                 }
-                ++unit;
+                if (!ok) break;
                 const int hk = u.head0 / p.group;
                 for (int i = 0; i < 2 * u.nt; ++i, ++place) {
                     // which tile the ring's next place takes
@@ -269,16 +277,17 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             }
             // No copy may be in flight when the CTA leaves (all have landed unless a role gave up).
-            for (uint32_t b = 0; b < 2 && b < unit; ++b) {
-                const uint32_t last = unit - 1 - ((unit - 1 - b) & 1u);  // last fill of buffer b
-                (void)mbar_wait(&q_full[b], (last >> 1) & 1u, p.wait_ns, p.status, kStatusTimeoutAttnLoad);
+            for (uint32_t st = 0; st < L::kQ && st < q_place; ++st) {
+                const uint32_t fills = (q_place - 1 - st) / L::kQ;       // index of the place's last fill
+                (void)mbar_wait(&q_full[st], fills & 1u, p.wait_ns, p.status, kStatusTimeoutAttnLoad);
             }
             for (uint32_t st = 0; st < kStages && st < place; ++st) {
                 const uint32_t fills = (place - 1 - st) / kStages;       // index of the stage's last fill
                 (void)mbar_wait(&kv_full[st], fills & 1u, p.wait_ns, p.status, kStatusTimeoutAttnLoad);
             }
-        } else if (warp == 1) {
-            // ------------------------------------------------------------ MMAs
+        } else if (warp == 1 || warp == 3) {
+            // ------------------------------------------------------------ MMAs of query tile X
+            const uint32_t X = uniform((uint32_t)warp >> 1);
             constexpr uint32_t kIdescS = (1u << 4) | (1u << 7) | (1u << 10) | ((128u >> 3) << 17) | ((128u >> 4) << 24);
             constexpr uint32_t kIdescO =
                 (1u << 4) | (1u << 7) | (1u << 10) | (1u << 16) | (((uint32_t)DP >> 3) << 17) | ((128u >> 4) << 24);
@@ -286,103 +295,99 @@ __global__ void __launch_bounds__(kThreads, 1)
             // in their units of 16 bytes.
             constexpr uint64_t kDescK = (1ull << 16) | (64ull << 32) | (1ull << 46) | (2ull << 61);
             constexpr uint64_t kDescV = (1024ull << 16) | (64ull << 32) | (1ull << 46) | (2ull << 61);
-            const uint32_t sbase = uniform(smem_u32(smem) >> 4);
-            const uint32_t tm = uniform(tmem);
+            constexpr uint32_t kTile16 = L::kTile >> 4;
+            const uint32_t sq = uniform(smem_u32(smem) >> 4), skv = sq + (L::kKvOff >> 4);
+            const uint32_t tmS = uniform(tmem) + kTmS + 128 * X, tmO = uniform(tmem) + kTmO + DP * X;
+            // Each branch costs a lone warp some 25 cycles, so what belongs to a tile has few:
+            // instructions of the elected lane are predicated, a wait that ran out is looked
+            // at once per tile.
+            const uint32_t on = elect_one() ? 1u : 0u;
             Piece cur, nxt;
-            uint32_t unit = 0, place = 0, gaps = 0;    // of cur: Q buffer count, first ring place, gap tiles before it
-            uint32_t p_phase = 0, o_phase = 0;         // bit X: parity of the next P, of the units O_X has held
-            int s_left = 0, s_left_next = 0;           // S products still to be issued
+            uint32_t q_place = 0, place = 0, gaps = 0;  // of cur: first places of Q, of K and V; gap tiles before it
+            uint32_t p_phase = 0, o_phase = 1;
             bool ok = true;
             auto wait = [&](uint64_t* bar, uint32_t parity) {
-                ok = __all_sync(0xffffffffu, mbar_wait(bar, parity, p.wait_ns, p.status, kStatusTimeoutAttnMma));
-                return ok;
+                ok &= mbar_wait(bar, parity, p.wait_ns, p.status, kStatusTimeoutAttnMma);
             };
-            auto s_total = [&](const Piece& u) { return tiles_for<kSolo>(u, 0, tok) + tiles_for<kSolo>(u, 1, tok); };
-            // S_X = Q_X K_i^T of unit u.  The pair's second query tile finds the waits done by the first.
-            auto issue_s = [&](const Piece& u, uint32_t un, uint32_t pl, int X, int i, int& left) {
+            // S = Q K_i^T of unit u, whose places begin at qp and pl; `last`: the unit's last for X
+            auto issue_s = [&](uint32_t qp, uint32_t pl, int i, bool last) {
                 const uint32_t at = pl + (uint32_t)k_place<kSolo>(tile_at<kSolo>(X, i)), st = at % kStages;
-                const uint32_t buf = un & 1u;
-                if (kSolo || X == 0) {
-                    if (i == 0 && !wait(&q_full[buf], (un >> 1) & 1u)) return;
-                    if (!wait(&kv_full[st], (at / kStages) & 1u)) return;
-                    tc_fence_after();
-                }
-                --left;
-                const uint64_t q = kDescK + (sbase + (buf * L::kQTiles + (kSolo ? 0 : X)) * (L::kTile >> 4));
-                const uint64_t k = kDescK + (sbase + ((L::kKvOff + st * L::kTile) >> 4));
-                const bool last_k = kSolo || X == 1 || u.ntok <= tok;
-                if (elect_one()) {
+                const uint32_t qa = qp + (kSolo ? 0u : X), qs = qa % L::kQ;
+                if (i == 0) wait(&q_full[qs], (qa / L::kQ) & 1u);
+                wait(&kv_full[st], (at / kStages) & 1u);
+                tc_fence_after();
+                const uint64_t q = kDescK + (sq + qs * kTile16), k = kDescK + (skv + st * kTile16);
 #pragma unroll
-                    for (int c = 0; c < DP / 16; ++c) {
-                        const uint32_t o = (c >> 2) * 1024 + (c & 3) * 2;
-                        mma_f16_ss(tm + kTmS + 128 * X, q + o, k + o, kIdescS, c > 0);
-                    }
-                    tc_commit(&s_full[X]);
-                    // the K tile's last use: always (solo); the second query tile, or the only one
-                    if (last_k) tc_commit(&kv_empty[st]);
-                    if (left == 0) tc_commit(&q_empty[buf]);
+                for (int c = 0; c < DP / 16; ++c) {
+                    const uint32_t o = (c >> 2) * 1024 + (c & 3) * 2;
+                    mma_f16_ss(on, tmS, q + o, k + o, kIdescS, c > 0);
                 }
-                __syncwarp();
+                tc_commit_if(on, &s_full[X]);
+                tc_commit_if(on, &kv_empty[st]);
+                tc_commit_if(on & (uint32_t)last, &q_empty[qs]);
             };
-            bool have = walk.next_with_keys(cur);
-            if (have) {
-                s_left = s_total(cur);
-                issue_s(cur, 0, 0, 0, 0, s_left);
-                if (ok && tiles_for<kSolo>(cur, 1, tok) > 0) issue_s(cur, 0, 0, 1, 0, s_left);
-            }
-            while (ok && have) {
-                const bool more = walk.next_with_keys(nxt);
-                if (more) s_left_next = s_total(nxt);
-                const uint32_t next_place = place + 2 * (uint32_t)cur.nt;
-                const int na = tiles_for<kSolo>(cur, 0, tok), nb = tiles_for<kSolo>(cur, 1, tok);
-                for (int i = 0; i < na && ok; ++i) {
-#pragma unroll
-                    for (int X = 0; X < 2; ++X) {
-                        const int n = X ? nb : na;
-                        if (ok && i < n) {
-                            const int t = tile_at<kSolo>(X, i);
-                            const uint32_t at = place + (uint32_t)v_place<kSolo>(t, cur.nt), st = at % kStages;
-                            if (!wait(&p_full[X], (p_phase >> X) & 1u)) break;
-                            p_phase ^= 1u << X;
-                            if (i == 0 && !wait(&o_empty[X], ((o_phase >> X) & 1u) ^ 1u)) break;
-                            const bool gap = cur.has_gaps(cur.t0 + t);
-                            if (kSolo || X == 0) {
-                                if (!wait(&kv_full[st], (at / kStages) & 1u)) break;
-                                if (gap && !wait(&mask_full[gaps % kMaskSlots], (gaps / kMaskSlots) & 1u)) break;
-                            }
-                            const bool last_v = kSolo || X == 1 || nb == 0;
-                            if (last_v) gaps += gap;
-                            tc_fence_after();
-                            const uint64_t v = kDescV + (sbase + ((L::kKvOff + st * L::kTile) >> 4));
-                            if (elect_one()) {
-#pragma unroll
-                                for (int c = 0; c < 8; ++c)
-                                    mma_f16_ts(tm + kTmO + DP * X, tm + kTmS + 128 * X + 8 * c, v + c * 128, kIdescO,
-                                               i > 0 || c > 0);
-                                if (last_v) tc_commit(&kv_empty[st]);
-                                if (i == n - 1) tc_commit(&o_full[X]);
-                            }
-                            __syncwarp();
-                            if (i == n - 1) o_phase ^= 1u << X;
-                        }
-                        if (!ok) break;
-                        if (i + 1 < n)
-                            issue_s(cur, unit, place, X, i + 1, s_left);
-                        else if ((i + 1 == n || (n == 0 && i == na - 1)) && more && tiles_for<kSolo>(nxt, X, tok) > 0)
-                            issue_s(nxt, unit + 1, next_place, X, 0, s_left_next);
+            // A unit that has nothing for X: its places are given back as they fill.
+            auto pass = [&](const Piece& u) {
+                if (kSolo) {  // Q is the other warp's alone
+                    const uint32_t qs = q_place % L::kQ;
+                    wait(&q_full[qs], (q_place / L::kQ) & 1u);
+                    mbar_arrive_if(on, &q_empty[qs]);
+                } else {
+                    for (uint32_t at = place; __all_sync(0xffffffffu, ok) && at < place + 2 * (uint32_t)u.nt; ++at) {
+                        const uint32_t st = at % kStages;
+                        wait(&kv_full[st], (at / kStages) & 1u);
+                        mbar_arrive_if(on, &kv_empty[st]);
                     }
                 }
-                if (!ok) break;
-                ++unit;
+            };
+            bool have = walk.next_with_keys(cur), begun = false;
+            while (have && __all_sync(0xffffffffu, ok)) {
+                const int n = tiles_for<kSolo>(cur, X, tok);
+                if (n > 0 && !begun) issue_s(q_place, place, 0, n == 1);
+                const uint32_t next_place = place + 2 * (uint32_t)cur.nt;
+                const uint32_t next_q = q_place + (!kSolo && cur.ntok > tok ? 2u : 1u);
+                have = walk.next_with_keys(nxt);
+                const int n_next = have ? tiles_for<kSolo>(nxt, X, tok) : 0;
+                begun = n > 0 && n_next > 0;
+                for (int i = 0; i < n && __all_sync(0xffffffffu, ok); ++i) {
+                    const int t = tile_at<kSolo>(X, i);
+                    const uint32_t at = place + (uint32_t)v_place<kSolo>(t, cur.nt), st = at % kStages;
+                    const bool last = i == n - 1;
+                    wait(&p_half[X], p_phase);
+                    if (i == 0) {
+                        wait(&o_empty[X], o_phase);
+                        o_phase ^= 1u;
+                    }
+                    wait(&kv_full[st], (at / kStages) & 1u);
+                    if (cur.has_gaps(cur.t0 + t)) {
+                        const uint32_t g = gaps + cur.gaps_before(cur.t0 + t);
+                        wait(&mask_full[g % kMaskSlots], (g / kMaskSlots) & 1u);
+                    }
+                    tc_fence_after();
+                    const uint64_t v = kDescV + (skv + st * kTile16);
+#pragma unroll
+                    for (int c = 0; c < 4; ++c)
+                        mma_f16_ts(on, tmO, tmS + 8 * c, v + c * 128, kIdescO, c > 0 ? 1u : (uint32_t)(i > 0));
+                    wait(&p_full[X], p_phase);
+                    p_phase ^= 1u;
+                    tc_fence_after();
+#pragma unroll
+                    for (int c = 4; c < 8; ++c) mma_f16_ts(on, tmO, tmS + 8 * c, v + c * 128, kIdescO, 1u);
+                    tc_commit_if(on, &kv_empty[st]);
+                    tc_commit_if(on & (uint32_t)last, &o_full[X]);
+                    if (!last || n_next > 0)
+                        issue_s(last ? next_q : q_place, last ? next_place : place, last ? 0 : i + 1,
+                                last ? n_next == 1 : i + 2 == n);
+                }
+                if (n == 0) pass(cur);
+                gaps += cur.gaps_before(cur.t0 + cur.nt);
+                q_place = next_q;
                 place = next_place;
                 cur = nxt;
-                s_left = s_left_next;
-                have = more;
             }
             // All MMAs are done before TMEM and shared memory go.
-            if (elect_one()) tc_commit(done);
-            __syncwarp();
-            (void)mbar_wait(done, 0, p.wait_ns, p.status, kStatusTimeoutAttnMma);
+            tc_commit_if(on, &done[X]);
+            (void)mbar_wait(&done[X], 0, p.wait_ns, p.status, kStatusTimeoutAttnMma);
         } else if (warp == 2) {
             // ------------------------------------------------------------ keys that are left out
             Piece u;
@@ -420,7 +425,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 for (int x = 0; x < 8; ++x) d[x] = make_uint4(0, 0, 0, 0);
                             }
                     }
-                    if (lane == 0) mask_bits[slot] = make_uint4(w[0], w[1], w[2], w[3]);
+                    if (lane == 0) *reinterpret_cast<uint4*>(mask_bits + 4 * slot) = make_uint4(w[0], w[1], w[2], w[3]);
                     fence_proxy_async_smem();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&mask_full[slot]);
@@ -439,45 +444,44 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint64_t sl2 = f2(p.scale_log2, p.scale_log2);
         Walk walk(p.t, blockIdx.x);
         Piece u;
-        uint32_t s_count = 0, units = 0, gaps = 0;
+        uint32_t s_phase = 0, stat_phase = 1, gaps = 0;
         bool ok = true;
-        while (ok && walk.next_with_keys(u)) {
+        while (__all_sync(0xffffffffu, ok) && walk.next_with_keys(u)) {
             const int n = tiles_for<kSolo>(u, X, tok);
             const int rows = min(tok, u.ntok - (kSolo ? 0 : X * tok)) * p.t.pack;
             const bool work = 32 * quarter < rows;   // some row of this warp is a query
             float m = -INFINITY, l = 0.0f;
-            int seen = 0;
-            for (int i = 0; i < n; ++i) {
-                ok = mbar_wait(&s_full[X], s_count & 1u, p.wait_ns, p.status, kStatusTimeoutAttnSoftmax);
-                if (!__all_sync(0xffffffffu, ok)) {
-                    ok = false;
-                    break;
-                }
-                ++s_count;
-                const int t = tile_at<kSolo>(X, i);
-                for (; seen < t; ++seen) gaps += u.has_gaps(u.t0 + seen);
-                const bool gap = u.has_gaps(u.t0 + t);
+            for (int i = 0; i < n && __all_sync(0xffffffffu, ok); ++i) {
+                ok &= mbar_wait(&s_full[X], s_phase, p.wait_ns, p.status, kStatusTimeoutAttnSoftmax);
+                s_phase ^= 1u;
                 tc_fence_after();
                 if (work) {
+                    const int t = u.t0 + tile_at<kSolo>(X, i);
+                    if (u.has_gaps(t)) {
+                        // -inf over the scores of the keys that are left out
+                        const uint32_t g = gaps + u.gaps_before(t);
+                        ok &= mbar_wait(&mask_full[g % kMaskSlots], (g / kMaskSlots) & 1u, p.wait_ns, p.status,
+                                        kStatusTimeoutAttnSoftmax);
+                        __syncwarp();
+#pragma unroll 1
+                        for (int c = 0; c < 4; ++c) {
+                            const uint32_t w = mask_bits[4 * (g % kMaskSlots) + c];
+                            if (w == 0xffffffffu) continue;
+                            uint32_t s[32];
+                            tc_ld_32x32b_x32(tS + 32 * c, s);
+                            tc_wait_ld_x32(s);
+#pragma unroll
+                            for (int j = 0; j < 32; ++j)
+                                if (!((w >> j) & 1u)) s[j] = 0xFF800000u;
+                            tc_st_32x32b_x32(tS + 32 * c, s);
+                        }
+                        tc_wait_st();
+                    }
                     uint32_t s[4][32];
 #pragma unroll
                     for (int c = 0; c < 4; ++c) tc_ld_32x32b_x32(tS + 32 * c, s[c]);
-                    tc_wait_ld();
-                    if (gap) {
-                        ok = mbar_wait(&mask_full[gaps % kMaskSlots], (gaps / kMaskSlots) & 1u, p.wait_ns, p.status,
-                                       kStatusTimeoutAttnSoftmax);
-                        if (!__all_sync(0xffffffffu, ok)) {
-                            ok = false;
-                            break;
-                        }
-                        const uint4 b = mask_bits[gaps % kMaskSlots];
-                        const uint32_t w[4] = {b.x, b.y, b.z, b.w};
 #pragma unroll
-                        for (int c = 0; c < 4; ++c)
-#pragma unroll
-                            for (int j = 0; j < 32; ++j)
-                                if (!((w[c] >> j) & 1u)) s[c][j] = 0xFF800000u;  // -inf
-                    }
+                    for (int c = 0; c < 4; ++c) tc_wait_ld_x32(s[c]);
                     float top[4];
 #pragma unroll
                     for (int c = 0; c < 4; ++c) {
@@ -524,25 +528,31 @@ __global__ void __launch_bounds__(kThreads, 1)
                             w[j >> 1] = cvt_bf16x2(e);
                         }
                         tc_st_32x32b_x16(tS + 16 * c, w);
+                        if (c == 1) {
+                            tc_wait_st();
+                            tc_fence_before();
+                            __syncwarp();
+                            mbar_arrive_if(lane == 0, &p_half[X]);
+                        }
                     }
                     float a, b;
                     unf2(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])), a, b);
                     l += a + b;
                     tc_wait_st();
+                } else {
+                    mbar_arrive_if(lane == 0, &p_half[X]);
                 }
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&p_full[X]);
+                mbar_arrive_if(lane == 0, &p_full[X]);
             }
-            if (!ok) break;
-            for (; seen < u.nt; ++seen) gaps += u.has_gaps(u.t0 + seen);
+            gaps += u.gaps_before(u.t0 + u.nt);
             if (n > 0) {
-                ok = mbar_wait(&stat_empty[X], (units & 1u) ^ 1u, p.wait_ns, p.status, kStatusTimeoutAttnSoftmax);
-                if (!__all_sync(0xffffffffu, ok)) break;
+                ok &= mbar_wait(&stat_empty[X], stat_phase, p.wait_ns, p.status, kStatusTimeoutAttnSoftmax);
+                stat_phase ^= 1u;
                 stat[128 * X + row] = make_float2(m, l);
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&stat_full[X]);
-                ++units;
+                mbar_arrive_if(lane == 0, &stat_full[X]);
             }
         }
     } else {
@@ -655,7 +665,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     griddep_launch_dependents();
     tc_fence_before();
     __syncthreads();
-    if (warp == 3) {
+    if (warp == 2) {
         tc_fence_after();
         tmem_dealloc(tmem, kTmemCols);
     }
