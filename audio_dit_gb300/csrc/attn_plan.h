@@ -129,29 +129,67 @@ struct Piece {
     }
 };
 
-// The pieces of this CTA, in order; every role walks them by itself.
+// The pieces of this CTA, in order; every role walks them by itself.  Divisions
+// are done where an entry begins; from piece to piece the state is counted up.
 struct Walk {
     const AttnTable& t;
-    int cta, e, unit, pos, end;
+    int cta;
+    int e, hb, rb, blocks;     // entry, head block and row block of the next unit; row blocks of the entry
+    int step_hb, step_rb;      // whole waves: what `ctas` units further is, and the units in them
+    int wave_end;
+    int tile, left;            // pool: first tile of the next piece, steps left of the stretch
+    bool waves;
 
     __host__ __device__ Walk(const AttnTable& table, int c) : t(table), cta(c)
     {
-        e = 0;
-        unit = cta;
-        pos = t.pool_steps ? t.bound(cta) : 0;
-        end = t.pool_steps ? t.bound(cta + 1) : 0;
+        left = 0;
+        tile = 0;
+        step_hb = step_rb = wave_end = 0;
+        waves = t.any_full != 0;
+        if (waves) begin_waves(0);
+        else begin_pool();
     }
-    __host__ __device__ void fill(Piece& p, int entry, int u) const
+    __host__ __device__ void begin_waves(int entry)
     {
-        const int rb = t.row_blocks(entry), hb = u / rb;
-        p.e = entry;
+        for (; entry < t.entries; ++entry) {
+            wave_end = t.full(entry);
+            if (wave_end == 0) continue;
+            e = entry;
+            blocks = t.row_blocks(e);
+            step_hb = t.ctas / blocks;
+            step_rb = t.ctas - step_hb * blocks;
+            hb = cta / blocks;
+            rb = cta - hb * blocks;
+            return;
+        }
+        waves = false;
+        begin_pool();
+    }
+    __host__ __device__ void begin_pool()
+    {
+        hb = rb = e = 0;
+        blocks = 1;
+        if (t.pool_steps == 0) return;
+        const int pos = t.bound(cta);
+        left = t.bound(cta + 1) - pos;
+        if (left <= 0) return;
+        e = t.find(t.pool_step, pos);
+        const int n = t.steps(e), local = pos - t.pool_step[e], u = local / n;
+        tile = local - u * n;
+        blocks = t.row_blocks(e);
+        hb = (t.full(e) + u) / blocks;
+        rb = t.full(e) + u - hb * blocks;
+    }
+    __host__ __device__ void fill(Piece& p) const
+    {
+        p.e = e;
         p.head0 = hb * t.pack;
-        p.tok0 = t.q_begin(entry) + (u - hb * rb) * t.unit_tok;
-        p.ntok = lesser(t.unit_tok, t.q_end(entry) - p.tok0);
-        p.ctx_tiles = t.tiles_ctx(entry);
-        p.own_tiles = t.tiles_own(entry);
-        p.kv0 = entry < t.nseg ? t.kv_off[entry] : 0;
-        p.kv_len = entry < t.nseg ? t.kv_off[entry + 1] - p.kv0 : 0;
+        p.tok0 = t.q_begin(e) + rb * t.unit_tok;
+        p.ntok = lesser(t.unit_tok, t.q_end(e) - p.tok0);
+        p.ctx_tiles = t.tiles_ctx(e);
+        p.own_tiles = t.tiles_own(e);
+        p.kv0 = e < t.nseg ? t.kv_off[e] : 0;
+        p.kv_len = e < t.nseg ? t.kv_off[e + 1] - p.kv0 : 0;
         p.gaps_ctx = t.ctx_masked != 0;
         p.gaps_own = t.own_masked != 0;
         p.gap_ctx = t.ctx_ragged && p.ctx_tiles > 0 ? p.ctx_tiles - 1 : -1;
@@ -159,32 +197,44 @@ struct Walk {
     }
     __host__ __device__ bool next(Piece& p)
     {
-        while (t.any_full && e < t.entries) {
-            if (unit < t.full(e)) {
-                fill(p, e, unit);
-                unit += t.ctas;
-                p.t0 = 0;
-                p.nt = p.ctx_tiles + p.own_tiles;
-                p.whole = true;
-                p.slot = 0;
-                return true;
+        if (waves) {
+            fill(p);
+            p.t0 = 0;
+            p.nt = p.ctx_tiles + p.own_tiles;
+            p.whole = true;
+            p.slot = 0;
+            // the last whole wave of an entry ends where fewer than ctas units are left
+            rb += step_rb;
+            hb += step_hb;
+            if (rb >= blocks) {
+                rb -= blocks;
+                ++hb;
             }
-            ++e;
-            unit = cta;
+            if (hb * blocks + rb >= wave_end) begin_waves(e + 1);
+            return true;
         }
-        if (pos >= end) return false;
-        const int entry = t.find(t.pool_step, pos), n = t.steps(entry);
-        const int local = pos - t.pool_step[entry], u = local / n, t0 = local - u * n;
-        const int take = lesser(n - t0, end - pos);
-        fill(p, entry, t.full(entry) + u);
-        p.t0 = t0;
-        p.nt = lesser(t0 + take, p.ctx_tiles + p.own_tiles) - t0;
+        if (left <= 0) return false;
+        fill(p);
+        const int tiles = p.ctx_tiles + p.own_tiles, n = tiles > 0 ? tiles : 1;
+        const int take = lesser(n - tile, left);
+        p.t0 = tile;
+        p.nt = lesser(tile + take, tiles) - tile;
         p.whole = take == n && !t.separate;
-        // A stretch has at most two cut units, its first and its last; with the
-        // separate plan every piece leaves partials, numbered along the pool.
-        p.slot = t.separate ? (entry < t.nseg ? t.pool_unit[entry] + u : u) + cta
-                            : cut_slot(cta, t0 == 0);
-        pos += take;
+        // With the separate plan every piece leaves partials, numbered along the pool.
+        p.slot = t.separate ? (e < t.nseg ? t.pool_unit[e] : 0) + hb * blocks + rb + cta : cut_slot(cta, tile == 0);
+        left -= take;
+        tile = 0;
+        if (++rb == blocks) {
+            rb = 0;
+            if (++hb == t.head_blocks && left > 0) {
+                do ++e;
+                while (t.pool_step[e + 1] == t.pool_step[e]);
+                blocks = t.row_blocks(e);
+                const int u = t.full(e);
+                hb = u / blocks;
+                rb = u - hb * blocks;
+            }
+        }
         return true;
     }
     // The same without the units that have no key (only the epilogue sees those).

@@ -51,7 +51,7 @@ constexpr int kThreads = 512;
 constexpr float kGrowth = 8.0f;      // log2 of how far the true maximum may pass the one in use
 constexpr int kMaskSlots = 16;
 constexpr uint32_t kTmemCols = 512;
-constexpr uint32_t kRegsControl = 80, kRegsSoftmax = 176, kRegsEpilogue = 80;
+constexpr uint32_t kRegsControl = 64, kRegsSoftmax = 184, kRegsEpilogue = 80;
 static_assert(kRegsControl + 2 * kRegsSoftmax + kRegsEpilogue <= 512, "setmaxnreg shares exceed the launch budget");
 
 constexpr unsigned int kStatusTimeoutAttnLoad = 64u, kStatusTimeoutAttnMma = 128u, kStatusTimeoutAttnSoftmax = 256u,
@@ -66,9 +66,9 @@ struct Layout {
     static constexpr int kStages = (7 - kQ) * (128 / DP);
     static constexpr uint32_t kKvOff = kQ * kTile;
     static constexpr uint32_t kBarOff = kKvOff + kStages * kTile;
-    // barriers: q_full, q_empty (per Q tile), kv_full, kv_empty (per stage), s_full, p_half, p_full, o_full,
-    // o_empty, stat_full, stat_empty (2 each), gap_load, mask_full (per slot), done
-    static constexpr int kBars = 2 * kQ + 2 * kStages + 14 + 2 * kMaskSlots + 2;
+    // barriers: q_full (two per Q tile), q_empty, kv_full (two per stage), kv_empty, s_full, p_half, p_full,
+    // o_full, o_empty, stat_full, stat_empty, done, turn (2 each), gap_load, mask_full (per slot)
+    static constexpr int kBars = 3 * kQ + 3 * kStages + 18 + 2 * kMaskSlots;
     static constexpr uint32_t kMaskOff = kBarOff + (kBars * 8 + 8 + 15) / 16 * 16;
     static constexpr uint32_t kStatOff = kMaskOff + kMaskSlots * 16;
     static constexpr uint32_t kBytes = kStatOff + 2 * 128 * 8;
@@ -77,7 +77,7 @@ struct Layout {
 
 struct AttnParams {
     AttnTable t;
-    int Hq, group, D, C;
+    int Hq, group, D, T, C;
     const uint8_t* key_mask;
     const uint8_t* ctx_mask;
     float scale_log2, growth;      // growth: kGrowth in units of the raw scores
@@ -117,22 +117,20 @@ __device__ __forceinline__ int v_place(int i, int nt)
     return kSolo ? (i == nt - 1 ? 2 * nt - 1 : 2 * i + 2) : 2 * i + 1;
 }
 
-__device__ __forceinline__ void store_row(__nv_bfloat16* o, const uint32_t (&w)[16], int cols, bool wide)
+// One row's 32 sums v (columns c0...) as bf16, by the lanes whose `on` is set.
+__device__ __forceinline__ void store_bf16(uint32_t on, __nv_bfloat16* o, const uint32_t (&v)[32], uint64_t f, int cols,
+                                           bool wide)
 {
+    uint32_t w[16];
+#pragma unroll
+    for (int j = 0; j < 16; ++j)
+        w[j] = cvt_bf16x2(mul2(f2(__uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1])), f));
     if (wide) {
 #pragma unroll
-        for (int j = 0; j < 2; ++j)
-            if (16 * j < cols)
-                asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(o + 16 * j),
-                             "r"(w[8 * j]), "r"(w[8 * j + 1]), "r"(w[8 * j + 2]), "r"(w[8 * j + 3]),
-                             "r"(w[8 * j + 4]), "r"(w[8 * j + 5]), "r"(w[8 * j + 6]), "r"(w[8 * j + 7])
-                             : "memory");
+        for (int j = 0; j < 2; ++j) st_global_v8_if(on & (uint32_t)(16 * j < cols), o + 16 * j, w + 8 * j);
     } else {
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-            if (8 * j < cols)
-                *reinterpret_cast<uint4*>(o + 8 * j) =
-                    make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
+        for (int j = 0; j < 4; ++j) st_global_v4_if(on & (uint32_t)(8 * j < cols), o + 8 * j, w + 4 * j);
     }
 }
 
@@ -155,10 +153,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         griddep_wait();
         return;
     }
-    uint64_t* q_full = reinterpret_cast<uint64_t*>(smem + L::kBarOff);  // per Q place: the tile landed
-    uint64_t* q_empty = q_full + L::kQ;             // its last S was computed
-    uint64_t* kv_full = q_empty + L::kQ;               // per stage: the K or V tile landed
-    uint64_t* kv_empty = kv_full + kStages;         // its MMAs are done
+    // A wait tells a barrier's phase from the one before it by a parity, so it is
+    // right only once the phase before has completed.  Copies may land out of
+    // order, and a role that waits for some of the ring's places only can ask for
+    // a fill before the previous one of its stage has landed (for another role).
+    // So the "full" barriers alternate between two per stage: the fill before the
+    // previous one is over when this one can be asked for, as the loads of what
+    // the role used last have been issued since.
+    uint64_t* q_full = reinterpret_cast<uint64_t*>(smem + L::kBarOff);  // the Q tile landed, two per tile
+    uint64_t* q_empty = q_full + 2 * L::kQ;         // its last S was computed
+    uint64_t* kv_full = q_empty + L::kQ;            // the K or V tile landed, two per stage
+    uint64_t* kv_empty = kv_full + 2 * kStages;     // its MMAs are done
     uint64_t* s_full = kv_empty + kStages;          // per query tile: S computed (and the MMAs before it done)
     uint64_t* p_half = s_full + 2;                  // P's first 64 keys stored, O rescaled where it had to be
     uint64_t* p_full = p_half + 2;                  // all of P stored
@@ -168,14 +173,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint64_t* stat_empty = stat_full + 2;           // and read
     uint64_t* gap_load = stat_empty + 2;            // per slot: the load of a V tile with gaps was issued
     uint64_t* mask_full = gap_load + kMaskSlots;    // per slot: bits stored, V rows zeroed
-    uint64_t* done = mask_full + kMaskSlots;
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done + 2);
+    uint64_t* done = mask_full + kMaskSlots;        // a warp's MMAs are done
+    uint64_t* turn = done + 2;                      // a warp may issue its next tile's MMAs
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(turn + 2);
     uint32_t* mask_bits = reinterpret_cast<uint32_t*>(smem + L::kMaskOff);
     float2* stat = reinterpret_cast<float2*>(smem + L::kStatOff);  // [2][128]: (maximum, sum)
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < 2; ++i) {
             mbar_init(&done[i], 1);
+            mbar_init(&turn[i], 1);
             mbar_init(&s_full[i], 1);
             mbar_init(&p_half[i], 4);
             mbar_init(&p_full[i], 4);
@@ -184,22 +191,20 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(&stat_full[i], 4);
             mbar_init(&stat_empty[i], 4);
         }
-        for (int i = 0; i < L::kQ; ++i) {
-            mbar_init(&q_full[i], 1);
-            mbar_init(&q_empty[i], kSolo ? 2 : 1);
-        }
-        for (int i = 0; i < kStages; ++i) {
-            mbar_init(&kv_full[i], 1);
-            mbar_init(&kv_empty[i], kSolo ? 1 : 2);
-        }
+        for (int i = 0; i < 2 * L::kQ; ++i) mbar_init(&q_full[i], 1);
+        for (int i = 0; i < L::kQ; ++i) mbar_init(&q_empty[i], kSolo ? 2 : 1);
+        for (int i = 0; i < 2 * kStages; ++i) mbar_init(&kv_full[i], 1);
+        for (int i = 0; i < kStages; ++i) mbar_init(&kv_empty[i], kSolo ? 1 : 2);
         for (int i = 0; i < kMaskSlots; ++i) {
             mbar_init(&gap_load[i], 1);
             mbar_init(&mask_full[i], 1);
         }
         fence_mbarrier_init();
         prefetch_tensormap(&tmQ);
-        prefetch_tensormap(&tmK);
-        prefetch_tensormap(&tmV);
+        if (p.T > 0) {
+            prefetch_tensormap(&tmK);
+            prefetch_tensormap(&tmV);
+        }
         if (p.C > 0) {
             prefetch_tensormap(&tmKc);
             prefetch_tensormap(&tmVc);
@@ -217,6 +222,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     griddep_wait();
     const uint32_t tmem = *tmem_slot;
     const int tok = p.t.tok;
+    // the "full" barrier of a place, and its parity
+    auto q_bar = [&](uint32_t place) { return &q_full[place % (2 * L::kQ)]; };
+    auto q_par = [&](uint32_t place) { return (place / (2 * L::kQ)) & 1u; };
+    auto kv_bar = [&](uint32_t place) { return &kv_full[place % (2 * kStages)]; };
+    auto kv_par = [&](uint32_t place) { return (place / (2 * kStages)) & 1u; };
 
     if (warp < 4) {
         setmaxnreg_dec<kRegsControl>();
@@ -237,9 +247,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                         break;
                     }
                     if (elect_one()) {
-                        mbar_arrive_expect_tx(&q_full[st], p.q_bytes);
+                        mbar_arrive_expect_tx(q_bar(q_place), p.q_bytes);
                         for (int c = 0; c < kChunks; ++c)
-                            tma_load_3d(smem + st * L::kTile + c * 16384, &tmQ, &q_full[st], 64 * c, u.head0,
+                            tma_load_3d(smem + st * L::kTile + c * 16384, &tmQ, q_bar(q_place), 64 * c, u.head0,
                                         u.tok0 + X * tok);
                     }
                 }
@@ -269,73 +279,73 @@ __global__ void __launch_bounds__(kThreads, 1)
                         const CUtensorMap* map = is_v ? (ctx ? &tmVc : &tmV) : (ctx ? &tmKc : &tmK);
                         const int row = ctx ? t * kKeyTile : u.kv0 + (t - u.ctx_tiles) * kKeyTile;
                         uint8_t* d = smem + L::kKvOff + st * L::kTile;
-                        mbar_arrive_expect_tx(&kv_full[st], L::kTile);
-                        for (int c = 0; c < kChunks; ++c) tma_load_3d(d + c * 16384, map, &kv_full[st], 64 * c, hk, row);
+                        mbar_arrive_expect_tx(kv_bar(place), L::kTile);
+                        for (int c = 0; c < kChunks; ++c)
+                            tma_load_3d(d + c * 16384, map, kv_bar(place), 64 * c, hk, row);
                         if (is_v && u.has_gaps(t)) mbar_arrive(&gap_load[gaps % kMaskSlots]);
                     }
                     gaps += is_v && u.has_gaps(t);
                 }
             }
             // No copy may be in flight when the CTA leaves (all have landed unless a role gave up).
-            for (uint32_t st = 0; st < L::kQ && st < q_place; ++st) {
-                const uint32_t fills = (q_place - 1 - st) / L::kQ;       // index of the place's last fill
-                (void)mbar_wait(&q_full[st], fills & 1u, p.wait_ns, p.status, kStatusTimeoutAttnLoad);
-            }
-            for (uint32_t st = 0; st < kStages && st < place; ++st) {
-                const uint32_t fills = (place - 1 - st) / kStages;       // index of the stage's last fill
-                (void)mbar_wait(&kv_full[st], fills & 1u, p.wait_ns, p.status, kStatusTimeoutAttnLoad);
-            }
+            for (uint32_t b = 1; b <= L::kQ && b <= q_place; ++b)
+                (void)mbar_wait(q_bar(q_place - b), q_par(q_place - b), p.wait_ns, p.status, kStatusTimeoutAttnLoad);
+            for (uint32_t b = 1; b <= kStages && b <= place; ++b)
+                (void)mbar_wait(kv_bar(place - b), kv_par(place - b), p.wait_ns, p.status, kStatusTimeoutAttnLoad);
         } else if (warp == 1 || warp == 3) {
             // ------------------------------------------------------------ MMAs of query tile X
             const uint32_t X = uniform((uint32_t)warp >> 1);
             constexpr uint32_t kIdescS = (1u << 4) | (1u << 7) | (1u << 10) | ((128u >> 3) << 17) | ((128u >> 4) << 24);
             constexpr uint32_t kIdescO =
                 (1u << 4) | (1u << 7) | (1u << 10) | (1u << 16) | (((uint32_t)DP >> 3) << 17) | ((128u >> 4) << 24);
-            // Descriptors without their addresses; offsets inside a tile are added
-            // in their units of 16 bytes.
-            constexpr uint64_t kDescK = (1ull << 16) | (64ull << 32) | (1ull << 46) | (2ull << 61);
-            constexpr uint64_t kDescV = (1024ull << 16) | (64ull << 32) | (1ull << 46) | (2ull << 61);
+            // Descriptors: the low word holds the address and the leading offset in units of 16
+            // bytes, the high word is the same for all (stride 1024, 128-byte swizzle).
+            constexpr uint32_t kDescHi = 64u | (1u << 14) | (2u << 29), kDescK = 1u << 16, kDescV = 1024u << 16;
+            auto desc = [](uint32_t lo) { return ((uint64_t)kDescHi << 32) | lo; };
             constexpr uint32_t kTile16 = L::kTile >> 4;
-            const uint32_t sq = uniform(smem_u32(smem) >> 4), skv = sq + (L::kKvOff >> 4);
-            const uint32_t tmS = uniform(tmem) + kTmS + 128 * X, tmO = uniform(tmem) + kTmO + DP * X;
+            const uint32_t sq = smem_u32(smem) >> 4, skv = sq + (L::kKvOff >> 4);
+            const uint32_t tmS = uniform(tmem + kTmS + 128 * X), tmO = uniform(tmem + kTmO + DP * X);
             // Each branch costs a lone warp some 25 cycles, so what belongs to a tile has few:
             // instructions of the elected lane are predicated, a wait that ran out is looked
             // at once per tile.
             const uint32_t on = elect_one() ? 1u : 0u;
             Piece cur, nxt;
             uint32_t q_place = 0, place = 0, gaps = 0;  // of cur: first places of Q, of K and V; gap tiles before it
-            uint32_t p_phase = 0, o_phase = 1;
+            uint32_t p_phase = 0, o_phase = 1, t_phase = X ^ 1u;
             bool ok = true;
             auto wait = [&](uint64_t* bar, uint32_t parity) {
                 ok &= mbar_wait(bar, parity, p.wait_ns, p.status, kStatusTimeoutAttnMma);
             };
-            // S = Q K_i^T of unit u, whose places begin at qp and pl; `last`: the unit's last for X
-            auto issue_s = [&](uint32_t qp, uint32_t pl, int i, bool last) {
-                const uint32_t at = pl + (uint32_t)k_place<kSolo>(tile_at<kSolo>(X, i)), st = at % kStages;
-                const uint32_t qa = qp + (kSolo ? 0u : X), qs = qa % L::kQ;
-                if (i == 0) wait(&q_full[qs], (qa / L::kQ) & 1u);
-                wait(&kv_full[st], (at / kStages) & 1u);
-                tc_fence_after();
-                const uint64_t q = kDescK + (sq + qs * kTile16), k = kDescK + (skv + st * kTile16);
+            // S = Q K_i^T of a unit whose places begin at qp and pl, in two steps: what it waits
+            // for, and the products.  `last`: the unit's last for X.
+            auto wait_s = [&](uint32_t qp, uint32_t pl, int i) {
+                const uint32_t at = pl + (uint32_t)k_place<kSolo>(tile_at<kSolo>(X, i));
+                if (i == 0) wait(q_bar(qp + (kSolo ? 0u : X)), q_par(qp + (kSolo ? 0u : X)));
+                wait(kv_bar(at), kv_par(at));
+            };
+            auto issue_s = [&](uint32_t go, uint32_t qp, uint32_t pl, int i, bool last) {
+                const uint32_t st = (pl + (uint32_t)k_place<kSolo>(tile_at<kSolo>(X, i))) % kStages;
+                const uint32_t qs = (qp + (kSolo ? 0u : X)) % L::kQ;
+                const uint32_t q = uniform(kDescK + sq + qs * kTile16), k = uniform(kDescK + skv + st * kTile16);
 #pragma unroll
                 for (int c = 0; c < DP / 16; ++c) {
                     const uint32_t o = (c >> 2) * 1024 + (c & 3) * 2;
-                    mma_f16_ss(on, tmS, q + o, k + o, kIdescS, c > 0);
+                    mma_f16_ss(go, tmS, desc(q + o), desc(k + o), kIdescS, c > 0);
                 }
-                tc_commit_if(on, &s_full[X]);
-                tc_commit_if(on, &kv_empty[st]);
-                tc_commit_if(on & (uint32_t)last, &q_empty[qs]);
+                tc_commit_if(go, &s_full[X]);
+                tc_commit_if(go, &kv_empty[st]);
+                tc_commit_if(go & (uint32_t)last, &q_empty[qs]);
             };
             // A unit that has nothing for X: its places are given back as they fill.
             auto pass = [&](const Piece& u) {
                 if (kSolo) {  // Q is the other warp's alone
                     const uint32_t qs = q_place % L::kQ;
-                    wait(&q_full[qs], (q_place / L::kQ) & 1u);
+                    wait(q_bar(q_place), q_par(q_place));
                     mbar_arrive_if(on, &q_empty[qs]);
                 } else {
                     for (uint32_t at = place; __all_sync(0xffffffffu, ok) && at < place + 2 * (uint32_t)u.nt; ++at) {
                         const uint32_t st = at % kStages;
-                        wait(&kv_full[st], (at / kStages) & 1u);
+                        wait(kv_bar(at), kv_par(at));
                         mbar_arrive_if(on, &kv_empty[st]);
                     }
                 }
@@ -343,43 +353,61 @@ __global__ void __launch_bounds__(kThreads, 1)
             bool have = walk.next_with_keys(cur), begun = false;
             while (have && __all_sync(0xffffffffu, ok)) {
                 const int n = tiles_for<kSolo>(cur, X, tok);
-                if (n > 0 && !begun) issue_s(q_place, place, 0, n == 1);
+                // turns of a unit: none where B has no tile, else A's (B passes on what it has not)
+                const int turns = tiles_for<kSolo>(cur, 1, tok) > 0 ? tiles_for<kSolo>(cur, 0, tok) : 0;
+                if (n > 0 && !begun) {
+                    wait_s(q_place, place, 0);
+                    tc_fence_after();
+                    issue_s(on, q_place, place, 0, n == 1);
+                }
                 const uint32_t next_place = place + 2 * (uint32_t)cur.nt;
                 const uint32_t next_q = q_place + (!kSolo && cur.ntok > tok ? 2u : 1u);
                 have = walk.next_with_keys(nxt);
                 const int n_next = have ? tiles_for<kSolo>(nxt, X, tok) : 0;
                 begun = n > 0 && n_next > 0;
+                if (n > 0) wait(&o_empty[X], o_phase);
+                o_phase ^= (uint32_t)(n > 0);
                 for (int i = 0; i < n && __all_sync(0xffffffffu, ok); ++i) {
+                    // Everything but P is waited for while the softmax works on it.
                     const int t = tile_at<kSolo>(X, i);
                     const uint32_t at = place + (uint32_t)v_place<kSolo>(t, cur.nt), st = at % kStages;
-                    const bool last = i == n - 1;
-                    wait(&p_half[X], p_phase);
-                    if (i == 0) {
-                        wait(&o_empty[X], o_phase);
-                        o_phase ^= 1u;
-                    }
-                    wait(&kv_full[st], (at / kStages) & 1u);
+                    const bool last = i == n - 1, more = !last || n_next > 0;
+                    const uint32_t s_q = last ? next_q : q_place, s_place = last ? next_place : place;
+                    const int s_i = last ? 0 : i + 1;
+                    const uint32_t v = uniform(kDescV + skv + st * kTile16);
+                    wait(kv_bar(at), kv_par(at));
                     if (cur.has_gaps(cur.t0 + t)) {
                         const uint32_t g = gaps + cur.gaps_before(cur.t0 + t);
                         wait(&mask_full[g % kMaskSlots], (g / kMaskSlots) & 1u);
                     }
+                    if (more) wait_s(s_q, s_place, s_i);
+                    wait(&p_half[X], p_phase);
+                    // The two warps take turns: were their MMAs mixed, both tiles' would end at the
+                    // same time and both softmaxes run while the tensor cores stand idle.
+                    if (turns > 0) {
+                        wait(&turn[X], t_phase);
+                        t_phase ^= 1u;
+                    }
                     tc_fence_after();
-                    const uint64_t v = kDescV + (skv + st * kTile16);
 #pragma unroll
                     for (int c = 0; c < 4; ++c)
-                        mma_f16_ts(on, tmO, tmS + 8 * c, v + c * 128, kIdescO, c > 0 ? 1u : (uint32_t)(i > 0));
+                        mma_f16_ts(on, tmO, tmS + 8 * c, desc(v + c * 128), kIdescO, c > 0 ? 1u : (uint32_t)(i > 0));
                     wait(&p_full[X], p_phase);
                     p_phase ^= 1u;
                     tc_fence_after();
 #pragma unroll
-                    for (int c = 4; c < 8; ++c) mma_f16_ts(on, tmO, tmS + 8 * c, v + c * 128, kIdescO, 1u);
+                    for (int c = 4; c < 8; ++c) mma_f16_ts(on, tmO, tmS + 8 * c, desc(v + c * 128), kIdescO, 1u);
                     tc_commit_if(on, &kv_empty[st]);
                     tc_commit_if(on & (uint32_t)last, &o_full[X]);
-                    if (!last || n_next > 0)
-                        issue_s(last ? next_q : q_place, last ? next_place : place, last ? 0 : i + 1,
-                                last ? n_next == 1 : i + 2 == n);
+                    issue_s(on & (uint32_t)more, s_q, s_place, s_i, last ? n_next == 1 : i + 2 == n);
+                    mbar_arrive_if(on & (uint32_t)(turns > 0), &turn[X ^ 1u]);
                 }
                 if (n == 0) pass(cur);
+                for (int i = n; i < turns && __all_sync(0xffffffffu, ok); ++i) {
+                    wait(&turn[X], t_phase);
+                    t_phase ^= 1u;
+                    mbar_arrive_if(on, &turn[X ^ 1u]);
+                }
                 gaps += cur.gaps_before(cur.t0 + cur.nt);
                 q_place = next_q;
                 place = next_place;
@@ -404,7 +432,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const uint32_t slot = gaps % kMaskSlots;
                     ok = mbar_wait(&gap_load[slot], (gaps / kMaskSlots) & 1u, p.wait_ns, p.status,
                                    kStatusTimeoutAttnMask) &&
-                         mbar_wait(&kv_full[st], (at / kStages) & 1u, p.wait_ns, p.status, kStatusTimeoutAttnMask);
+                         mbar_wait(kv_bar(at), kv_par(at), p.wait_ns, p.status, kStatusTimeoutAttnMask);
                     ok = __all_sync(0xffffffffu, ok);
                     if (!ok) break;
                     const bool ctx = t < u.ctx_tiles;
@@ -563,102 +591,107 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int row_tok = row / p.t.pack, row_head = row - row_tok * p.t.pack;
         Walk walk(p.t, blockIdx.x);
         Piece u;
-        uint32_t units[2] = {0, 0};
+        uint32_t phase = 0;  // bit X: parity of the next O_X
         bool ok = true;
-        while (ok && walk.next(u)) {
-            const bool direct = u.whole;
-            const int kind = u.e < p.t.nseg ? 0 : 1;
-            const int tiles = kSolo ? 1 : (u.ntok > tok ? 2 : 1);
-            for (int Y = 0; Y < tiles && ok; ++Y) {  // a tile of queries
-                const int tokens = min(tok, u.ntok - Y * tok);
-                const bool on = row < tokens * p.t.pack;
+        auto wait = [&](uint64_t* bar, uint32_t parity) {
+            ok &= mbar_wait(bar, parity, p.wait_ns, p.status, kStatusTimeoutAttnEpilogue);
+        };
+        while (__all_sync(0xffffffffu, ok) && walk.next(u)) {
+            const int tiles = !kSolo && u.ntok > tok ? 2 : 1;
+            for (int Y = 0; Y < tiles; ++Y) {  // a tile of queries
+                const uint32_t on = row < min(tok, u.ntok - Y * tok) * p.t.pack;
                 const long long r = u.tok0 + Y * tok + row_tok;
                 const int h = u.head0 + row_head;
-                // parts of the tile: A and B (solo: the even and the odd key tiles)
-                const int nA = kSolo ? tiles_for<kSolo>(u, 0, tok) : u.nt, nB = kSolo ? tiles_for<kSolo>(u, 1, tok) : 0;
-                float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
-#pragma unroll
-                for (int x = 0; x < (kSolo ? 2 : 1); ++x) {
-                    if ((x ? nB : nA) == 0) continue;
-                    const int X = kSolo ? x : Y;
-                    ok = mbar_wait(&stat_full[X], units[X] & 1u, p.wait_ns, p.status, kStatusTimeoutAttnEpilogue) &&
-                         mbar_wait(&o_full[X], units[X] & 1u, p.wait_ns, p.status, kStatusTimeoutAttnEpilogue);
-                    ok = __all_sync(0xffffffffu, ok);
-                    if (!ok) break;
-                    const float2 st = stat[128 * X + row];
-                    m[x] = st.x;
-                    l[x] = st.y;
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&stat_empty[X]);
-                    ++units[X];
+                // Sums and statistics: O_Y; solo: O_A and O_B, of the even and the odd key tiles.
+                const int nA = u.nt, nB = kSolo ? u.nt >> 1 : 0;
+                const int X = kSolo ? 0 : Y;
+                float2 a = make_float2(-INFINITY, 0.0f), b = a;
+                if (nA > 0) {
+                    wait(&stat_full[X], (phase >> X) & 1u);
+                    wait(&o_full[X], (phase >> X) & 1u);
+                    phase ^= 1u << X;
+                    a = stat[128 * X + row];
                 }
-                if (!ok) break;
-                tc_fence_after();
-                const float top = fmaxf(m[0], m[1]), top2 = top * p.scale_log2;
-                // weights of the two parts against the common maximum
-                float f0 = 1.0f, f1 = 0.0f, sum = l[0];
                 if (kSolo && nB > 0) {
-                    f0 = m[0] == top ? 1.0f : ex2_approx_ftz((m[0] - top) * p.scale_log2);
-                    f1 = m[1] == top ? 1.0f : ex2_approx_ftz((m[1] - top) * p.scale_log2);
-                    sum = l[0] * f0 + l[1] * f1;
+                    wait(&stat_full[1], (phase >> 1) & 1u);
+                    wait(&o_full[1], (phase >> 1) & 1u);
+                    phase ^= 2u;
+                    b = stat[128 + row];
                 }
-                float* slot = nullptr;
-                if (direct) {
+                __syncwarp();
+                mbar_arrive_if(lane == 0 && nA > 0, &stat_empty[X]);
+                if (kSolo) mbar_arrive_if(lane == 0 && nB > 0, &stat_empty[1]);
+                tc_fence_after();
+                const float top = fmaxf(a.x, b.x), top2 = top * p.scale_log2;
+                // weights of the two parts against the common maximum
+                float f0 = 1.0f, f1 = 0.0f, sum = a.y;
+                if (kSolo && nB > 0) {
+                    f0 = a.x == top ? 1.0f : ex2_approx_ftz((a.x - top) * p.scale_log2);
+                    f1 = b.x == top ? 1.0f : ex2_approx_ftz((b.x - top) * p.scale_log2);
+                    sum = a.y * f0 + b.y * f1;
+                }
+                // Where a part has no key (or only scores of -inf), its sums may be anything.
+                const bool clear = __any_sync(0xffffffffu, a.y == 0.0f || (kSolo && nB > 0 && b.y == 0.0f));
+                const uint32_t tA = tmem + kTmO + DP * X + lanes, tB = tmem + kTmO + DP + lanes;
+                // the sums of columns 32 c...; solo: of both parts, weighted
+                auto load = [&](int c, uint32_t (&v)[32]) {
+                    if (nA > 0) {
+                        tc_ld_32x32b_x32(tA + 32 * c, v);
+                        tc_wait_ld_x32(v);
+                        if (clear) {
+#pragma unroll
+                            for (int j = 0; j < 32; ++j) v[j] = a.y == 0.0f ? 0u : v[j];
+                        }
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) v[j] = 0u;
+                    }
+                    if (kSolo && nB > 0) {
+#pragma unroll
+                        for (int k = 0; k < 2; ++k) {
+                            uint32_t w[16];
+                            tc_ld_32x32b_x16(tB + 32 * c + 16 * k, w);
+                            tc_wait_ld_x16(w);
+#pragma unroll
+                            for (int j = 0; j < 16; ++j) {
+                                const float x = clear && b.y == 0.0f ? 0.0f : __uint_as_float(w[j]);
+                                v[16 * k + j] = __float_as_uint(fmaf(x, f1, __uint_as_float(v[16 * k + j]) * f0));
+                            }
+                        }
+                    }
+                };
+                if (u.whole) {
                     const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;  // a row without a key: zeros
-                    f0 *= inv;
-                    f1 *= inv;
+                    const uint64_t f = f2(inv, inv);
                     if (on && p.lse)
                         p.lse[r * p.Hq + h] =
                             sum == 0.0f ? -INFINITY : (top2 + log2f(sum)) * 0.69314718055994531f;
+                    __nv_bfloat16* o = p.out + r * p.out_row + (long long)h * p.out_head;
+#pragma unroll
+                    for (int c = 0; c < DP / 32; ++c) {
+                        uint32_t v[32];
+                        load(c, v);
+                        store_bf16(on, o + 32 * c, v, f, p.D - 32 * c, p.wide_out != 0);
+                    }
                 } else {
-                    const int rows = p.slot_rows[kind];
+                    const int kind = u.e < p.t.nseg ? 0 : 1, rows = p.slot_rows[kind];
                     float* base = p.part[kind] + (long long)u.slot * rows * (DP + 2);
                     const int at = Y * tok * p.t.pack + row;
-                    slot = base + (long long)at * DP;
                     if (on) *reinterpret_cast<float2*>(base + (long long)rows * DP + 2 * at) = make_float2(
                         sum == 0.0f ? -INFINITY : top2, sum);
-                }
-                __nv_bfloat16* o = p.out + r * p.out_row + (long long)h * p.out_head;
 #pragma unroll
-                for (int c = 0; c < DP / 32; ++c) {
-                    float v[32];
-#pragma unroll
-                    for (int j = 0; j < 32; ++j) v[j] = 0.0f;
-                    if (nA > 0) {
-                        uint32_t a[32];
-                        tc_ld_32x32b_x32(tmem + kTmO + (kSolo ? 0 : DP * Y) + lanes + 32 * c, a);
-                        tc_wait_ld();
-                        // sums that are zero in place of what a row without a key has in TMEM
-#pragma unroll
-                        for (int j = 0; j < 32; ++j) v[j] = f0 == 0.0f ? 0.0f : __uint_as_float(a[j]) * f0;
-                    }
-                    if (kSolo && nB > 0) {
-                        uint32_t a[32];
-                        tc_ld_32x32b_x32(tmem + kTmO + DP + lanes + 32 * c, a);
-                        tc_wait_ld();
-#pragma unroll
-                        for (int j = 0; j < 32; ++j)
-                            v[j] = f1 == 0.0f ? v[j] : fmaf(__uint_as_float(a[j]), f1, v[j]);
-                    }
-                    if (on && direct) {
-                        uint32_t w[16];
-#pragma unroll
-                        for (int j = 0; j < 16; ++j) w[j] = cvt_bf16x2(f2(v[2 * j], v[2 * j + 1]));
-                        if (32 * c < p.D) store_row(o + 32 * c, w, p.D - 32 * c, p.wide_out != 0);
-                    } else if (on) {
+                    for (int c = 0; c < DP / 32; ++c) {
+                        uint32_t v[32];
+                        load(c, v);
 #pragma unroll
                         for (int j = 0; j < 8; ++j)
-                            *reinterpret_cast<float4*>(slot + 32 * c + 4 * j) =
-                                make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+                            st_global_v4_if(on, base + (long long)at * DP + 32 * c + 4 * j, v + 4 * j);
                     }
-                    __syncwarp();
                 }
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) {
-                    if (nA > 0) mbar_arrive(&o_empty[kSolo ? 0 : Y]);
-                    if (kSolo && nB > 0) mbar_arrive(&o_empty[1]);
-                }
+                mbar_arrive_if(lane == 0 && nA > 0, &o_empty[X]);
+                if (kSolo) mbar_arrive_if(lane == 0 && nB > 0, &o_empty[1]);
             }
         }
     }
@@ -805,6 +838,7 @@ cudaError_t launch_attn(const AttnJob& job, cudaStream_t s)
     p.Hq = job.Hq;
     p.group = job.Hq / job.Hkv;
     p.D = job.D;
+    p.T = (int)job.T;
     p.C = (int)job.C;
     p.key_mask = job.key_mask;
     p.ctx_mask = job.ctx_mask;

@@ -227,6 +227,14 @@ __device__ __forceinline__ void tc_wait_ld_x32(uint32_t (&v)[32])
                    "+r"(v[29]), "+r"(v[30]), "+r"(v[31])::"memory");
 }
 
+__device__ __forceinline__ void tc_wait_ld_x16(uint32_t (&v)[16])
+{
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]), "+r"(v[6]), "+r"(v[7]),
+                   "+r"(v[8]), "+r"(v[9]), "+r"(v[10]), "+r"(v[11]), "+r"(v[12]), "+r"(v[13]), "+r"(v[14]),
+                   "+r"(v[15])::"memory");
+}
+
 __device__ __forceinline__ void tc_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 
 // 32 lanes x 32 consecutive fp32 columns: thread i receives lane (base + i).
@@ -284,6 +292,25 @@ __device__ __forceinline__ void mma_f16_ts(uint32_t on, uint32_t d_tmem, uint32_
                  "setp.ne.b32 q, %5, 0;\n\t"
                  "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
                  "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(on)
+                 : "memory");
+}
+
+// Stores of 32 and 16 bytes by the lanes whose `on` is set.
+__device__ __forceinline__ void st_global_v8_if(uint32_t on, void* dst, const uint32_t* w)
+{
+    asm volatile("{\n\t.reg .pred q;\n\t"
+                 "setp.ne.b32 q, %9, 0;\n\t"
+                 "@q st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};\n\t}" ::"l"(dst),
+                 "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7]), "r"(on)
+                 : "memory");
+}
+
+__device__ __forceinline__ void st_global_v4_if(uint32_t on, void* dst, const uint32_t* w)
+{
+    asm volatile("{\n\t.reg .pred q;\n\t"
+                 "setp.ne.b32 q, %5, 0;\n\t"
+                 "@q st.global.v4.b32 [%0], {%1, %2, %3, %4};\n\t}" ::"l"(dst),
+                 "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(on)
                  : "memory");
 }
 

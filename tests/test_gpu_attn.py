@@ -307,3 +307,25 @@ def test_no_rows_and_no_keys():
     A.h3fp4_shared_attn(q, none, none, none, none, out.fill_(3.0), ws, lse=lse.zero_())
     A.h3fp4_check(ws)
     assert not bool(out.any()) and bool((lse == -math.inf).all())
+
+
+def test_cold_caches_and_repeats():
+    """Copies that take long and land out of order: the same bits as with everything in L2, many times over."""
+    import audio_dit_gb300 as A
+    flush = torch.empty(256 << 20, dtype=torch.uint8, device="cuda")
+    for c in (Case(111, 32, 8, 128, [0, 1], [0, 9000]), Case(112, 4, 4, 64, [0, 40, 700], [0, 3000, 5000], ctx=2000),
+              Case(113, 2, 2, 128, [0, 300, 600, 1300], [0, 100, 230, 231], ctx=128)):
+        q, k, v = c.q.cuda(), c.k.cuda(), c.v.cuda()
+        kc, vc = (c.kc.cuda(), c.vc.cuda()) if c.C else (k[:0], v[:0])
+        out, lse = torch.empty_like(q), torch.empty(c.M, c.Hq, device="cuda")
+        ws = A.alloc_attn_workspace(c.M, c.T, c.Hq, c.Hkv, c.D, c.q_off, c.kv_off, ctx=c.C)
+        first = None
+        for i in range(30):
+            if i % 3:
+                flush.zero_()
+            A.h3fp4_shared_attn(q, k, v, kc, vc, out.zero_(), ws, q_off=c.q_off, kv_off=c.kv_off, lse=lse)
+            A.h3fp4_check(ws)
+            if first is None:
+                first = out.clone(), lse.clone()
+                c.check(out.cpu(), lse.cpu())
+            assert torch.equal(out.view(torch.int16), first[0].view(torch.int16)) and torch.equal(lse, first[1]), i
