@@ -323,12 +323,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (i == 0) wait(q_bar(qp + (kSolo ? 0u : X)), q_par(qp + (kSolo ? 0u : X)));
                 wait(kv_bar(at), kv_par(at));
             };
-            auto issue_s = [&](uint32_t go, uint32_t qp, uint32_t pl, int i, bool last) {
+            auto issue_s = [&](uint32_t go, uint32_t qp, uint32_t pl, int i, bool last, uint32_t pass_turn) {
                 const uint32_t st = (pl + (uint32_t)k_place<kSolo>(tile_at<kSolo>(X, i))) % kStages;
                 const uint32_t qs = (qp + (kSolo ? 0u : X)) % L::kQ;
                 const uint32_t q = uniform(kDescK + sq + qs * kTile16), k = uniform(kDescK + skv + st * kTile16);
 #pragma unroll
                 for (int c = 0; c < DP / 16; ++c) {
+                    // the other warp's products queue up behind the rest of these
+                    if (c == DP / 32) mbar_arrive_if(pass_turn, &turn[X ^ 1u]);
                     const uint32_t o = (c >> 2) * 1024 + (c & 3) * 2;
                     mma_f16_ss(go, tmS, desc(q + o), desc(k + o), kIdescS, c > 0);
                 }
@@ -358,7 +360,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (n > 0 && !begun) {
                     wait_s(q_place, place, 0);
                     tc_fence_after();
-                    issue_s(on, q_place, place, 0, n == 1);
+                    issue_s(on, q_place, place, 0, n == 1, 0);
                 }
                 const uint32_t next_place = place + 2 * (uint32_t)cur.nt;
                 const uint32_t next_q = q_place + (!kSolo && cur.ntok > tok ? 2u : 1u);
@@ -399,8 +401,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int c = 4; c < 8; ++c) mma_f16_ts(on, tmO, tmS + 8 * c, desc(v + c * 128), kIdescO, 1u);
                     tc_commit_if(on, &kv_empty[st]);
                     tc_commit_if(on & (uint32_t)last, &o_full[X]);
-                    issue_s(on & (uint32_t)more, s_q, s_place, s_i, last ? n_next == 1 : i + 2 == n);
-                    mbar_arrive_if(on & (uint32_t)(turns > 0), &turn[X ^ 1u]);
+                    issue_s(on & (uint32_t)more, s_q, s_place, s_i, last ? n_next == 1 : i + 2 == n,
+                            on & (uint32_t)(turns > 0));
                 }
                 if (n == 0) pass(cur);
                 for (int i = n; i < turns && __all_sync(0xffffffffu, ok); ++i) {
