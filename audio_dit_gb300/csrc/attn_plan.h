@@ -107,7 +107,7 @@ __host__ __device__ inline int cut_slot(int cta, bool begins_unit) { return 2 * 
 
 // A piece of a unit: key tiles [t0, t0 + nt) of it, for tokens [tok0, tok0 + ntok).
 struct Piece {
-    int e, head0, tok0, ntok;
+    int e, head0, tok0, ntok;   // e: entry
     int t0, nt;
     int ctx_tiles;          // tiles below this index are the context's
     int own_tiles, kv0, kv_len;

@@ -24,7 +24,7 @@
 //                the other's softmax.  A warp of its own per tile, since the
 //                waits and bookkeeping around a tile's sixteen MMAs take one warp
 //                about as long as the MMAs themselves.
-//   warp 2       allocates TMEM; keys that are left out (a mask, the end of a
+//   warp 2       allocates TMEM; walks the CTA's pieces for all roles; keys that are left out (a mask, the end of a
 //                segment inside a tile): their bits for the softmax, and zeros
 //                over their rows of the V tile, since 0 * NaN is not 0
 //   warps 4-11   softmax of tile A, of tile B (a warpgroup each)
@@ -49,9 +49,10 @@ namespace {
 
 constexpr int kThreads = 512;
 constexpr float kGrowth = 8.0f;      // log2 of how far the true maximum may pass the one in use
-constexpr int kMaskSlots = 16;
+constexpr int kMaskSlots = 8;       // more than the ring's V tiles
+constexpr int kPieceSlots = 4;
 constexpr uint32_t kTmemCols = 512;
-constexpr uint32_t kRegsControl = 64, kRegsSoftmax = 184, kRegsEpilogue = 80;
+constexpr uint32_t kRegsControl = 80, kRegsSoftmax = 176, kRegsEpilogue = 80;
 static_assert(kRegsControl + 2 * kRegsSoftmax + kRegsEpilogue <= 512, "setmaxnreg shares exceed the launch budget");
 
 constexpr unsigned int kStatusTimeoutAttnLoad = 64u, kStatusTimeoutAttnMma = 128u, kStatusTimeoutAttnSoftmax = 256u,
@@ -67,10 +68,13 @@ struct Layout {
     static constexpr uint32_t kKvOff = kQ * kTile;
     static constexpr uint32_t kBarOff = kKvOff + kStages * kTile;
     // barriers: q_full (two per Q tile), q_empty, kv_full (two per stage), kv_empty, s_full, p_half, p_full,
-    // o_full, o_empty, stat_full, stat_empty, done, turn (2 each), gap_load, mask_full (per slot)
-    static constexpr int kBars = 3 * kQ + 3 * kStages + 18 + 2 * kMaskSlots;
+    // o_full, o_empty, stat_full, stat_empty, done, turn (2 each), gap_load, mask_full (per slot),
+    // piece_full, piece_empty (per slot)
+    static constexpr int kBars = 3 * kQ + 3 * kStages + 18 + 2 * kMaskSlots + 2 * kPieceSlots;
+    static_assert(kStages / 2 + 1 < kMaskSlots, "a mask slot's readers are through when its next V tile lands");
     static constexpr uint32_t kMaskOff = kBarOff + (kBars * 8 + 8 + 15) / 16 * 16;
-    static constexpr uint32_t kStatOff = kMaskOff + kMaskSlots * 16;
+    static constexpr uint32_t kPieceOff = kMaskOff + kMaskSlots * 16;
+    static constexpr uint32_t kStatOff = kPieceOff + kPieceSlots * 48;
     static constexpr uint32_t kBytes = kStatOff + 2 * 128 * 8;
     static_assert(kBytes <= 232448, "shared memory budget");
 };
@@ -175,7 +179,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint64_t* mask_full = gap_load + kMaskSlots;    // per slot: bits stored, V rows zeroed
     uint64_t* done = mask_full + kMaskSlots;        // a warp's MMAs are done
     uint64_t* turn = done + 2;                      // a warp may issue its next tile's MMAs
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(turn + 2);
+    uint64_t* piece_full = turn + 2;                // per slot: a piece is described
+    uint64_t* piece_empty = piece_full + kPieceSlots;  // and read by all that work on it
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(piece_empty + kPieceSlots);
     uint32_t* mask_bits = reinterpret_cast<uint32_t*>(smem + L::kMaskOff);
     float2* stat = reinterpret_cast<float2*>(smem + L::kStatOff);  // [2][128]: (maximum, sum)
 
@@ -195,6 +201,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int i = 0; i < L::kQ; ++i) mbar_init(&q_empty[i], kSolo ? 2 : 1);
         for (int i = 0; i < 2 * kStages; ++i) mbar_init(&kv_full[i], 1);
         for (int i = 0; i < kStages; ++i) mbar_init(&kv_empty[i], kSolo ? 1 : 2);
+        for (int i = 0; i < kPieceSlots; ++i) {
+            mbar_init(&piece_full[i], 1);
+            mbar_init(&piece_empty[i], 16);  // warps: loads, MMAs (2), gaps, softmax (8), epilogue (4)
+        }
         for (int i = 0; i < kMaskSlots; ++i) {
             mbar_init(&gap_load[i], 1);
             mbar_init(&mask_full[i], 1);
@@ -222,6 +232,33 @@ __global__ void __launch_bounds__(kThreads, 1)
     griddep_wait();
     const uint32_t tmem = *tmem_slot;
     const int tok = p.t.tok;
+    // The pieces of this CTA, described by warp 2 a few ahead (a walk costs some hundred cycles of
+    // constant loads; a slot is read in one).
+    uint32_t piece_count = 0;
+    auto next_piece = [&](Piece& u, bool& ok, unsigned int code) {
+        const uint32_t slot = piece_count % kPieceSlots;
+        ok &= mbar_wait(&piece_full[slot], (piece_count / kPieceSlots) & 1u, p.wait_ns, p.status, code);
+        const int4* rec = reinterpret_cast<const int4*>(smem + L::kPieceOff + slot * 48);
+        const int4 a = rec[0], b = rec[1], c = rec[2];
+        ++piece_count;
+        u.t0 = a.x, u.nt = a.y, u.ntok = a.z, u.tok0 = a.w;
+        u.head0 = b.x, u.ctx_tiles = b.y, u.kv0 = b.z, u.kv_len = b.w;
+        u.slot = c.x, u.e = c.y;
+        u.whole = c.x < 0;
+        u.own_tiles = (u.kv_len + kKeyTile - 1) / kKeyTile;
+        u.gaps_ctx = p.t.ctx_masked != 0;
+        u.gaps_own = p.t.own_masked != 0;
+        u.gap_ctx = p.t.ctx_ragged ? u.ctx_tiles - 1 : -1;
+        u.gap_own = (u.kv_len & (kKeyTile - 1)) ? u.ctx_tiles + u.own_tiles - 1 : -1;
+        __syncwarp();
+        mbar_arrive_if(lane == 0, &piece_empty[slot]);
+        return __all_sync(0xffffffffu, ok) && u.nt >= 0;  // -1: no piece is left
+    };
+    auto next_with_keys = [&](Piece& u, bool& ok, unsigned int code) {
+        while (next_piece(u, ok, code))
+            if (u.nt > 0) return true;
+        return false;
+    };
     // the "full" barrier of a place, and its parity
     auto q_bar = [&](uint32_t place) { return &q_full[place % (2 * L::kQ)]; };
     auto q_par = [&](uint32_t place) { return (place / (2 * L::kQ)) & 1u; };
@@ -230,13 +267,12 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     if (warp < 4) {
         setmaxnreg_dec<kRegsControl>();
-        Walk walk(p.t, blockIdx.x);
         if (warp == 0) {
             // ------------------------------------------------------------ loads
             Piece u;
             uint32_t q_place = 0, place = 0, gaps = 0;
             bool ok = p.stall == 0;
-            while (ok && walk.next_with_keys(u)) {
+            while (ok && next_with_keys(u, ok, kStatusTimeoutAttnLoad)) {
                 const int tiles = !kSolo && u.ntok > tok ? 2 : 1;
                 for (int X = 0; X < tiles; ++X, ++q_place) {
                     const uint32_t st = q_place % L::kQ;
@@ -352,7 +388,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
             };
-            bool have = walk.next_with_keys(cur), begun = false;
+            // Only one piece is read ahead, with keys or not: warp 2 may be waiting for this unit's
+            // tiles before it describes more than a few.
+            bool have = next_piece(cur, ok, kStatusTimeoutAttnMma), begun = false;
             while (have && __all_sync(0xffffffffu, ok)) {
                 const int n = tiles_for<kSolo>(cur, X, tok);
                 // turns of a unit: none where B has no tile, else A's (B passes on what it has not)
@@ -363,8 +401,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     issue_s(on, q_place, place, 0, n == 1, 0);
                 }
                 const uint32_t next_place = place + 2 * (uint32_t)cur.nt;
-                const uint32_t next_q = q_place + (!kSolo && cur.ntok > tok ? 2u : 1u);
-                have = walk.next_with_keys(nxt);
+                const uint32_t next_q = q_place + (cur.nt == 0 ? 0u : !kSolo && cur.ntok > tok ? 2u : 1u);
+                have = next_piece(nxt, ok, kStatusTimeoutAttnMma);
                 const int n_next = have ? tiles_for<kSolo>(nxt, X, tok) : 0;
                 begun = n > 0 && n_next > 0;
                 if (n > 0) wait(&o_empty[X], o_phase);
@@ -404,7 +442,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     issue_s(on & (uint32_t)more, s_q, s_place, s_i, last ? n_next == 1 : i + 2 == n,
                             on & (uint32_t)(turns > 0));
                 }
-                if (n == 0) pass(cur);
+                if (n == 0 && cur.nt > 0) pass(cur);
                 for (int i = n; i < turns && __all_sync(0xffffffffu, ok); ++i) {
                     wait(&turn[X], t_phase);
                     t_phase ^= 1u;
@@ -420,10 +458,31 @@ __global__ void __launch_bounds__(kThreads, 1)
             (void)mbar_wait(&done[X], 0, p.wait_ns, p.status, kStatusTimeoutAttnMma);
         } else if (warp == 2) {
             // ------------------------------------------------------------ keys that are left out
+            Walk walk(p.t, blockIdx.x);
+            uint32_t described = 0;
+            bool ok = true, left = true;
+            auto describe = [&]() {  // the next piece, or that there is none
+                if (!left) return;
+                const uint32_t slot = described % kPieceSlots;
+                ok &= mbar_wait(&piece_empty[slot], ((described / kPieceSlots) & 1u) ^ 1u, p.wait_ns, p.status,
+                                kStatusTimeoutAttnMask);
+                Piece n;
+                left = __all_sync(0xffffffffu, ok) && walk.next(n);
+                if (lane == 0) {
+                    int4* rec = reinterpret_cast<int4*>(smem + L::kPieceOff + slot * 48);
+                    rec[0] = make_int4(n.t0, left ? n.nt : -1, n.ntok, n.tok0);
+                    rec[1] = make_int4(n.head0, n.ctx_tiles, n.kv0, n.kv_len);
+                    rec[2] = make_int4(n.whole ? -1 : n.slot, n.e, 0, 0);
+                    mbar_arrive(&piece_full[slot]);
+                }
+                __syncwarp();
+                ++described;
+            };
+            for (int i = 0; i < kPieceSlots - 1; ++i) describe();
             Piece u;
             uint32_t place = 0, gaps = 0;
-            bool ok = true;
-            while (ok && walk.next_with_keys(u)) {
+            while (next_piece(u, ok, kStatusTimeoutAttnMask)) {
+                describe();
                 for (int i = 0; i < u.nt && ok; ++i) {
                     const int t = u.t0 + i;
                     if (!u.has_gaps(t)) continue;
@@ -472,11 +531,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t lanes = (uint32_t)(32 * quarter) << 16;
         const uint32_t tS = tmem + kTmS + 128 * X + lanes, tO = tmem + kTmO + DP * X + lanes;
         const uint64_t sl2 = f2(p.scale_log2, p.scale_log2);
-        Walk walk(p.t, blockIdx.x);
         Piece u;
         uint32_t s_phase = 0, stat_phase = 1, gaps = 0;
         bool ok = true;
-        while (__all_sync(0xffffffffu, ok) && walk.next_with_keys(u)) {
+        while (next_with_keys(u, ok, kStatusTimeoutAttnSoftmax)) {
             const int n = tiles_for<kSolo>(u, X, tok);
             const int rows = min(tok, u.ntok - (kSolo ? 0 : X * tok)) * p.t.pack;
             const bool work = 32 * quarter < rows;   // some row of this warp is a query
@@ -591,14 +649,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int quarter = warp & 3, row = 32 * quarter + lane;
         const uint32_t lanes = (uint32_t)(32 * quarter) << 16;
         const int row_tok = row / p.t.pack, row_head = row - row_tok * p.t.pack;
-        Walk walk(p.t, blockIdx.x);
         Piece u;
         uint32_t phase = 0;  // bit X: parity of the next O_X
         bool ok = true;
         auto wait = [&](uint64_t* bar, uint32_t parity) {
             ok &= mbar_wait(bar, parity, p.wait_ns, p.status, kStatusTimeoutAttnEpilogue);
         };
-        while (__all_sync(0xffffffffu, ok) && walk.next(u)) {
+        while (next_piece(u, ok, kStatusTimeoutAttnEpilogue)) {
             const int tiles = !kSolo && u.ntok > tok ? 2 : 1;
             for (int Y = 0; Y < tiles; ++Y) {  // a tile of queries
                 const uint32_t on = row < min(tok, u.ntok - Y * tok) * p.t.pack;

@@ -329,3 +329,13 @@ def test_cold_caches_and_repeats():
                 first = out.clone(), lse.clone()
                 c.check(out.cpu(), lse.cpu())
             assert torch.equal(out.view(torch.int16), first[0].view(torch.int16)) and torch.equal(lse, first[1]), i
+
+
+def test_many_units_without_keys_between_masked_ones():
+    """Runs of units that only get zeros, between units whose every tile has keys that are left out."""
+    c = Case(121, 24, 8, 96, [0, 900, 2500, 2600, 4000, 4001, 5200], [0, 300, 300, 700, 700, 1011, 1400])
+    c.key_mask = torch.from_numpy(c.rng.random(1400) < 0.7)
+    c.check()
+    c = Case(122, 4, 2, 64, list(range(0, 201)), [i // 7 * 150 for i in range(201)], ctx=0)
+    c.key_mask = torch.from_numpy(c.rng.random(c.T) < 0.7)
+    c.check()
