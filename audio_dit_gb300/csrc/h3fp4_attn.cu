@@ -68,9 +68,9 @@ struct Layout {
     static constexpr uint32_t kKvOff = kQ * kTile;
     static constexpr uint32_t kBarOff = kKvOff + kStages * kTile;
     // barriers: q_full (two per Q tile), q_empty, kv_full (two per stage), kv_empty, s_full, p_half, p_full,
-    // o_full, o_empty, stat_full, stat_empty, done, turn (2 each), gap_load, mask_full (per slot),
+    // o_full, o_empty, stat_full, stat_empty, done, turn (2 each), gap_load, mask_full, zero_full (per slot),
     // piece_full, piece_empty (per slot)
-    static constexpr int kBars = 3 * kQ + 3 * kStages + 18 + 2 * kMaskSlots + 2 * kPieceSlots;
+    static constexpr int kBars = 3 * kQ + 3 * kStages + 18 + 3 * kMaskSlots + 2 * kPieceSlots;
     static_assert(kStages / 2 + 1 < kMaskSlots, "a mask slot's readers are through when its next V tile lands");
     static constexpr uint32_t kMaskOff = kBarOff + (kBars * 8 + 8 + 15) / 16 * 16;
     static constexpr uint32_t kPieceOff = kMaskOff + kMaskSlots * 16;
@@ -176,8 +176,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint64_t* stat_full = o_empty + 2;              // maximum and sum of each row stored
     uint64_t* stat_empty = stat_full + 2;           // and read
     uint64_t* gap_load = stat_empty + 2;            // per slot: the load of a V tile with gaps was issued
-    uint64_t* mask_full = gap_load + kMaskSlots;    // per slot: bits stored, V rows zeroed
-    uint64_t* done = mask_full + kMaskSlots;        // a warp's MMAs are done
+    uint64_t* mask_full = gap_load + kMaskSlots;    // per slot: bits stored
+    uint64_t* zero_full = mask_full + kMaskSlots;   // per slot: V rows zeroed
+    uint64_t* done = zero_full + kMaskSlots;        // a warp's MMAs are done
     uint64_t* turn = done + 2;                      // a warp may issue its next tile's MMAs
     uint64_t* piece_full = turn + 2;                // per slot: a piece is described
     uint64_t* piece_empty = piece_full + kPieceSlots;  // and read by all that work on it
@@ -208,6 +209,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int i = 0; i < kMaskSlots; ++i) {
             mbar_init(&gap_load[i], 1);
             mbar_init(&mask_full[i], 1);
+            mbar_init(&zero_full[i], 1);
         }
         fence_mbarrier_init();
         prefetch_tensormap(&tmQ);
@@ -418,7 +420,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     wait(kv_bar(at), kv_par(at));
                     if (cur.has_gaps(cur.t0 + t)) {
                         const uint32_t g = gaps + cur.gaps_before(cur.t0 + t);
-                        wait(&mask_full[g % kMaskSlots], (g / kMaskSlots) & 1u);
+                        wait(&zero_full[g % kMaskSlots], (g / kMaskSlots) & 1u);
                     }
                     if (more) wait_s(s_q, s_place, s_i);
                     wait(&p_half[X], p_phase);
@@ -478,6 +480,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 __syncwarp();
                 ++described;
             };
+#pragma unroll 1
             for (int i = 0; i < kPieceSlots - 1; ++i) describe();
             Piece u;
             uint32_t place = 0, gaps = 0;
@@ -487,37 +490,47 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const int t = u.t0 + i;
                     if (!u.has_gaps(t)) continue;
                     const uint32_t at = place + (uint32_t)v_place<kSolo>(i, u.nt), st = at % kStages;
-                    // A parity tells a stage's fill from the one before it only once that one is done with,
-                    // so first the load has to be issued.  The V tile's arrival also says that the mask
-                    // slot's last reader is through: the ring holds fewer tiles than there are slots.
-                    const uint32_t slot = gaps % kMaskSlots;
-                    ok = mbar_wait(&gap_load[slot], (gaps / kMaskSlots) & 1u, p.wait_ns, p.status,
-                                   kStatusTimeoutAttnMask) &&
-                         mbar_wait(kv_bar(at), kv_par(at), p.wait_ns, p.status, kStatusTimeoutAttnMask);
+                    const uint32_t slot = gaps % kMaskSlots, par = (gaps / kMaskSlots) & 1u;
+                    // Once the V tile's load is issued, its stage was free, so the mask slot's last
+                    // readers are through too: the ring holds fewer V tiles than there are slots.
+                    ok &= mbar_wait(&gap_load[slot], par, p.wait_ns, p.status, kStatusTimeoutAttnMask);
                     ok = __all_sync(0xffffffffu, ok);
                     if (!ok) break;
                     const bool ctx = t < u.ctx_tiles;
                     const uint8_t* mask = ctx ? p.ctx_mask : p.key_mask;
-                    const long long row = ctx ? t * kKeyTile : u.kv0 + (long long)(t - u.ctx_tiles) * kKeyTile;
+                    const long long first = ctx ? t * kKeyTile : u.kv0 + (long long)(t - u.ctx_tiles) * kKeyTile;
                     const int n = min(kKeyTile, ctx ? p.C - t * kKeyTile : u.kv_len - (t - u.ctx_tiles) * kKeyTile);
+                    bool keep[4];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        keep[j] = 32 * j + lane < n && (mask == nullptr || mask[first + 32 * j + lane] != 0);
                     uint32_t w[4];
-                    uint8_t* v = smem + L::kKvOff + st * L::kTile;
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) w[j] = __ballot_sync(0xffffffffu, keep[j]);
+                    if (lane == 0) {
+                        *reinterpret_cast<uint4*>(mask_bits + 4 * slot) = make_uint4(w[0], w[1], w[2], w[3]);
+                        mbar_arrive(&mask_full[slot]);
+                    }
+                    __syncwarp();
+                    ok = mbar_wait(kv_bar(at), kv_par(at), p.wait_ns, p.status, kStatusTimeoutAttnMask);
+                    ok = __all_sync(0xffffffffu, ok);
+                    if (!ok) break;
+                    // zeros, eight lanes to a row of a chunk and four rows at a time
+                    uint8_t* v = smem + L::kKvOff + st * L::kTile + lane * 16;
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
-                        const int k = 32 * j + lane;
-                        const bool on = k < n && (mask == nullptr || mask[row + k] != 0);
-                        w[j] = __ballot_sync(0xffffffffu, on);
-                        if (!on)
-                            for (int c = 0; c < kChunks; ++c) {
-                                uint4* d = reinterpret_cast<uint4*>(v + c * 16384 + k * 128);
+                        if (w[j] == 0xffffffffu) continue;
 #pragma unroll
-                                for (int x = 0; x < 8; ++x) d[x] = make_uint4(0, 0, 0, 0);
-                            }
+                        for (int k = 0; k < 8; ++k)
+                            if (!((w[j] >> (4 * k + (lane >> 3))) & 1u))
+#pragma unroll
+                                for (int c = 0; c < kChunks; ++c)
+                                    *reinterpret_cast<uint4*>(v + c * 16384 + (8 * j + k) * 512) =
+                                        make_uint4(0, 0, 0, 0);
                     }
-                    if (lane == 0) *reinterpret_cast<uint4*>(mask_bits + 4 * slot) = make_uint4(w[0], w[1], w[2], w[3]);
                     fence_proxy_async_smem();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(&mask_full[slot]);
+                    if (lane == 0) mbar_arrive(&zero_full[slot]);
                     ++gaps;
                 }
                 place += 2 * (uint32_t)u.nt;
@@ -585,7 +598,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         m = m_new;
                         if (i > 0) {  // S_X(i) is computed, so the MMAs into O_X before it are done
                             const uint64_t ff = f2(f, f);
-#pragma unroll
+#pragma unroll 1
                             for (int c = 0; c < DP / 16; ++c) {
                                 uint32_t o[16];
                                 tc_ld_32x32b_x16(tO + 16 * c, o);
@@ -719,32 +732,29 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                     }
                 };
-                if (u.whole) {
-                    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;  // a row without a key: zeros
-                    const uint64_t f = f2(inv, inv);
-                    if (on && p.lse)
-                        p.lse[r * p.Hq + h] =
-                            sum == 0.0f ? -INFINITY : (top2 + log2f(sum)) * 0.69314718055994531f;
-                    __nv_bfloat16* o = p.out + r * p.out_row + (long long)h * p.out_head;
-#pragma unroll
-                    for (int c = 0; c < DP / 32; ++c) {
-                        uint32_t v[32];
-                        load(c, v);
+                const float inv = sum == 0.0f ? 0.0f : rcp_approx(sum);  // a row without a key: zeros
+                const uint64_t f = f2(inv, inv);
+                const int kind = u.e < p.t.nseg ? 0 : 1, rows = p.slot_rows[kind];
+                float* base = p.part[kind] + (long long)u.slot * rows * (DP + 2);
+                const int at = Y * tok * p.t.pack + row;
+                float* part = base + (long long)at * DP;
+                __nv_bfloat16* o = p.out + r * p.out_row + (long long)h * p.out_head;
+                if (on && !u.whole)
+                    *reinterpret_cast<float2*>(base + (long long)rows * DP + 2 * at) =
+                        make_float2(sum == 0.0f ? -INFINITY : top2, sum);
+                if (on && u.whole && p.lse)
+                    p.lse[r * p.Hq + h] = sum == 0.0f ? -INFINITY : (top2 + __log2f(sum)) * 0.69314718055994531f;
+                // A loop and not straight code: it runs once per unit, when its instructions have left
+                // the caches; fetching them costs more than the branches.
+#pragma unroll 1
+                for (int c = 0; c < DP / 32; ++c) {
+                    uint32_t v[32];
+                    load(c, v);
+                    if (u.whole) {
                         store_bf16(on, o + 32 * c, v, f, p.D - 32 * c, p.wide_out != 0);
-                    }
-                } else {
-                    const int kind = u.e < p.t.nseg ? 0 : 1, rows = p.slot_rows[kind];
-                    float* base = p.part[kind] + (long long)u.slot * rows * (DP + 2);
-                    const int at = Y * tok * p.t.pack + row;
-                    if (on) *reinterpret_cast<float2*>(base + (long long)rows * DP + 2 * at) = make_float2(
-                        sum == 0.0f ? -INFINITY : top2, sum);
+                    } else {
 #pragma unroll
-                    for (int c = 0; c < DP / 32; ++c) {
-                        uint32_t v[32];
-                        load(c, v);
-#pragma unroll
-                        for (int j = 0; j < 8; ++j)
-                            st_global_v4_if(on, base + (long long)at * DP + 32 * c + 4 * j, v + 4 * j);
+                        for (int j = 0; j < 8; ++j) st_global_v4_if(on, part + 32 * c + 4 * j, v + 4 * j);
                     }
                 }
                 tc_fence_before();
