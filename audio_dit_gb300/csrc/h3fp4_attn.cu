@@ -744,23 +744,38 @@ __global__ void __launch_bounds__(kThreads, 1)
                         make_float2(sum == 0.0f ? -INFINITY : top2, sum);
                 if (on && u.whole && p.lse)
                     p.lse[r * p.Hq + h] = sum == 0.0f ? -INFINITY : (top2 + __log2f(sum)) * 0.69314718055994531f;
-                // A loop and not straight code: it runs once per unit, when its instructions have left
-                // the caches; fetching them costs more than the branches.
+                auto release = [&]() {
+                    tc_fence_before();
+                    __syncwarp();
+                    mbar_arrive_if(lane == 0 && nA > 0, &o_empty[X]);
+                    if (kSolo) mbar_arrive_if(lane == 0 && nB > 0, &o_empty[1]);
+                };
+                if (!kSolo && u.whole && p.wide_out && nA > 0 && !clear) {
+                    // The usual case of the pair plan, whose next unit waits for these sums to be read.
 #pragma unroll 1
-                for (int c = 0; c < DP / 32; ++c) {
-                    uint32_t v[32];
-                    load(c, v);
-                    if (u.whole) {
-                        store_bf16(on, o + 32 * c, v, f, p.D - 32 * c, p.wide_out != 0);
-                    } else {
-#pragma unroll
-                        for (int j = 0; j < 8; ++j) st_global_v4_if(on, part + 32 * c + 4 * j, v + 4 * j);
+                    for (int c = 0; c < DP / 32; ++c) {
+                        uint32_t v[32];
+                        tc_ld_32x32b_x32(tA + 32 * c, v);
+                        tc_wait_ld_x32(v);
+                        store_bf16(on, o + 32 * c, v, f, p.D - 32 * c, true);
                     }
+                    release();
+                } else {
+                    // A loop and not straight code: it runs once per unit, when its instructions have
+                    // left the caches; fetching them costs more than the branches.
+#pragma unroll 1
+                    for (int c = 0; c < DP / 32; ++c) {
+                        uint32_t v[32];
+                        load(c, v);
+                        if (u.whole) {
+                            store_bf16(on, o + 32 * c, v, f, p.D - 32 * c, p.wide_out != 0);
+                        } else {
+#pragma unroll
+                            for (int j = 0; j < 8; ++j) st_global_v4_if(on, part + 32 * c + 4 * j, v + 4 * j);
+                        }
+                    }
+                    release();
                 }
-                tc_fence_before();
-                __syncwarp();
-                mbar_arrive_if(lane == 0 && nA > 0, &o_empty[X]);
-                if (kSolo) mbar_arrive_if(lane == 0 && nB > 0, &o_empty[1]);
             }
         }
     }
