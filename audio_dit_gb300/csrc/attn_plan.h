@@ -44,6 +44,7 @@ struct AttnTable {
     int any_full;          // some entry has whole waves
     int ctx_masked, own_masked, ctx_ragged;  // masks are given; the context's length is no multiple of a tile
     int pool_steps, pool_units;
+    int share, longer;     // steps of a CTA's stretch of the pool: share + 1 for the first `longer` CTAs
     int M;
     int q_off[H3FP4_ATTN_MAX_SEGMENTS + 1];
     int kv_off[H3FP4_ATTN_MAX_SEGMENTS + 1];
@@ -83,18 +84,20 @@ struct AttnTable {
     // Where CTA c's stretch of the pool begins.
     __host__ __device__ int bound(int c) const
     {
-        const int x = (int)((long long)c * pool_steps / ctas);
+        const int x = c * share + lesser(c, longer);
         if (c <= 0 || c >= ctas || x <= 0 || x >= pool_steps) return x;
         const int e = find(pool_step, x), n = steps(e), t = (x - pool_step[e]) % n;
-        if (t <= kSnap && t <= n - t) return x - t;
-        if (n - t <= kSnap) return x + n - t;
+        // (a segment's unit of the separate plan is never cut)
+        const int snap = separate && e < nseg ? n : kSnap;
+        if (t <= snap && t <= n - t) return x - t;
+        if (n - t <= snap) return x + n - t;
         return x;
     }
     // The CTA whose stretch holds step x of the pool.
     __host__ __device__ int cta_of(int x) const
     {
-        int c = (int)((long long)x * ctas / pool_steps);
-        if (c > ctas - 1) c = ctas - 1;
+        const int head = longer * (share + 1);
+        int c = x < head ? x / (share + 1) : share > 0 ? longer + (x - head) / share : ctas - 1;
         while (c > 0 && bound(c) > x) --c;
         while (c + 1 < ctas && bound(c + 1) <= x) ++c;
         return c;
@@ -220,8 +223,11 @@ struct Walk {
         p.t0 = tile;
         p.nt = lesser(tile + take, tiles) - tile;
         p.whole = take == n && !t.separate;
-        // With the separate plan every piece leaves partials, numbered along the pool.
-        p.slot = t.separate ? (e < t.nseg ? t.pool_unit[e] : 0) + hb * blocks + rb + cta : cut_slot(cta, tile == 0);
+        // With the separate plan every piece leaves partials: one for a segment's unit, those of the
+        // context's numbered along the pool.
+        p.slot = !t.separate ? cut_slot(cta, tile == 0)
+                 : e < t.nseg ? t.pool_unit[e] + hb * blocks + rb
+                              : hb * blocks + rb + cta;
         left -= take;
         tile = 0;
         if (++rb == blocks) {
@@ -246,8 +252,15 @@ struct Walk {
     }
 };
 
+// A unit of the pool that is cut, and the CTAs that hold its pieces.
+struct Cut {
+    int tok0, head0, rows, cta, parts;
+};
+
 struct AttnPlan {
     AttnTable t;
+    Cut cuts[kAttnCtas];
+    int n_cuts;
     bool solo;
     bool join;           // partial sums exist: the second kernel runs
     int dp;              // D padded to 64 or 128
@@ -341,6 +354,8 @@ inline AttnPlan make_plan(const Job& job)
     }
     t.pool_units = t.pool_unit[t.entries];
     t.pool_steps = t.pool_step[t.entries];
+    t.share = t.pool_steps / t.ctas;
+    t.longer = t.pool_steps % t.ctas;
 
     // Partials: rows of the largest unit of each kind, an even number so that
     // every slot of rows * (dp + 2) floats begins on 16 bytes.
@@ -354,15 +369,24 @@ inline AttnPlan make_plan(const Job& job)
     for (int& rows : pl.slot_rows) rows += rows & 1;
     if (sep) {
         pl.join = true;
-        pl.slots[0] = t.pool_unit[t.nseg] + t.ctas;
+        pl.slots[0] = t.pool_unit[t.nseg];
         pl.slots[1] = t.units(t.nseg) + t.ctas;
     } else {
-        for (int c = 1; c < t.ctas && t.pool_steps > 0 && !pl.join; ++c) {
+        for (int c = 1, cut = -1; c < t.ctas && t.pool_steps > 0; ++c) {
             const int x = t.bound(c);
             if (x <= 0 || x >= t.pool_steps) continue;
-            const int e = t.find(t.pool_step, x);
-            if ((x - t.pool_step[e]) % t.steps(e) != 0) pl.join = true;
+            const int e = t.find(t.pool_step, x), n = t.steps(e), local = x - t.pool_step[e], u = local / n;
+            if (local == u * n) continue;
+            const int id = t.pool_unit[e] + u;
+            if (id == cut) {  // cut once more
+                ++pl.cuts[pl.n_cuts - 1].parts;
+                continue;
+            }
+            cut = id;
+            const int rb = t.row_blocks(e), all = t.full(e) + u, hb = all / rb, tok0 = t.q_begin(e) + (all - hb * rb) * t.unit_tok;
+            pl.cuts[pl.n_cuts++] = Cut{tok0, hb * pack, lesser(t.unit_tok, t.q_end(e) - tok0) * pack, c - 1, 2};
         }
+        pl.join = pl.n_cuts > 0;
         pl.slots[0] = pl.join ? 2 * t.ctas : 0;
     }
     size_t at = 256;

@@ -35,6 +35,7 @@
 // leaves, and so do the roles that depend on it.
 #include <cmath>
 #include <cstdint>
+#include <cstring>
 
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -790,80 +791,152 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // ------------------------------------------------------------------ joining partial sums
 //
-// One warp per row of a unit of the pool: its partials, each with its maximum
-// (in base 2) and sum, joined as exp2(m_i - m) weights.  Reads each partial once.
+// One warp per row of a unit of the pool: with m_i (base 2) and l_i of its
+// partials and m the largest m_i, out = sum_i 2^(m_i - m) o_i / sum_i 2^(m_i - m) l_i.
+// Reads each partial once; bound by latency where rows are few, so the
+// statistics of up to 32 partials are read at once, a lane each, then their
+// sums in groups of four.
 constexpr int kJoinThreads = 256;
-constexpr int kJoinRows = 16;
+constexpr int kJoinWarps = kJoinThreads / 32;
+constexpr int kJoinRows = 2 * kJoinWarps;  // rows of a block of the first kernel below
+
+struct JoinOut {
+    __nv_bfloat16* out;
+    long long out_row, out_head;
+    float* lse;
+    const float* part[2];
+    int slot_rows[2];
+    int D, Hq, pack;
+};
+
+// Row r, head h from `all` partials; at(i, row, ml) gives the sums and the
+// statistics of partial i.
+template <int DP, class At>
+__device__ __forceinline__ void join_row(const JoinOut& p, int r, int h, int all, At at)
+{
+    const int lane = threadIdx.x & 31;
+    constexpr int kV = DP / 32;  // columns per lane
+    float acc[kV], m = -INFINITY, l = 0.0f;
+#pragma unroll
+    for (int j = 0; j < kV; ++j) acc[j] = 0.0f;
+    for (int first = 0; first < all; first += 32) {
+        const int here = min(32, all - first);
+        const float* row = nullptr;
+        float2 ml = make_float2(-INFINITY, 0.0f);
+        if (lane < here) {
+            const float2* src;
+            at(first + lane, row, src);
+            ml = __ldg(src);
+        }
+        float top = ml.x;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+        const float m_new = fmaxf(m, top);
+        const float f = m == m_new ? 1.0f : ex2_approx_ftz(m - m_new);
+        const float w = ml.x == -INFINITY ? 0.0f : ml.x == m_new ? 1.0f : ex2_approx_ftz(ml.x - m_new);
+        float add = ml.y * w;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) add += __shfl_xor_sync(0xffffffffu, add, o);
+        l = l * f + add;
+        m = m_new;
+#pragma unroll
+        for (int j = 0; j < kV; ++j) acc[j] *= f;
+        for (int i = 0; i < here; i += 4) {
+            float v[4][kV], g[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const int from = min(i + k, here - 1);
+                const float* src = reinterpret_cast<const float*>(
+                    __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(row), from));
+                g[k] = __shfl_sync(0xffffffffu, w, from);
+                if (i + k >= here) g[k] = 0.0f;
+                if constexpr (kV == 4) {
+                    const float4 x = __ldg(reinterpret_cast<const float4*>(src) + lane);
+                    v[k][0] = x.x, v[k][1] = x.y, v[k][2] = x.z, v[k][3] = x.w;
+                } else {
+                    const float2 x = __ldg(reinterpret_cast<const float2*>(src) + lane);
+                    v[k][0] = x.x, v[k][1] = x.y;
+                }
+            }
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+#pragma unroll
+                for (int j = 0; j < kV; ++j)  // a partial without a key counts nothing, whatever its sums are
+                    acc[j] = g[k] == 0.0f ? acc[j] : fmaf(v[k][j], g[k], acc[j]);
+        }
+    }
+    const float inv = l == 0.0f ? 0.0f : rcp_approx(l);
+    __nv_bfloat16* o = p.out + (long long)r * p.out_row + (long long)h * p.out_head + lane * kV;
+#pragma unroll
+    for (int j = 0; j < kV; j += 2)
+        if (lane * kV + j < p.D) *reinterpret_cast<uint32_t*>(o + j) = cvt_bf16x2(f2(acc[j] * inv, acc[j + 1] * inv));
+    if (p.lse && lane == 0)
+        p.lse[(long long)r * p.Hq + h] = l == 0.0f ? -INFINITY : (m + __log2f(l)) * 0.69314718055994531f;
+}
+
+// Sums and statistics of row `in` of slot `slot`.
+template <int DP>
+__device__ __forceinline__ void slot_row(const JoinOut& p, int kind, int slot, int in, const float*& row,
+                                         const float2*& ml)
+{
+    const float* base = p.part[kind] + (long long)slot * p.slot_rows[kind] * (DP + 2);
+    row = base + (long long)in * DP;
+    ml = reinterpret_cast<const float2*>(base + (long long)p.slot_rows[kind] * DP) + in;
+}
+
+// The cut units of the pool: block (i, y) takes rows 16 y... of cut i.
+struct JoinCuts {
+    JoinOut o;
+    Cut cuts[kAttnCtas];
+};
 
 template <int DP>
-__global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const __grid_constant__ AttnParams p)
+__global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const __grid_constant__ JoinCuts p)
 {
+    const Cut c = p.cuts[blockIdx.x];
     griddep_wait();
-    const AttnTable& t = p.t;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    // the unit (of the segments') and its partials
-    const int pu = blockIdx.x;
-    int e = 0;
-    {
-        int lo = 0, hi = t.nseg;
-        while (hi - lo > 1) {
-            const int mid = (lo + hi) >> 1;
-            if (t.pool_unit[mid] <= pu) lo = mid;
-            else hi = mid;
-        }
-        e = lo;
+    const int end = min(c.rows, (int)(blockIdx.y + 1) * kJoinRows);
+    for (int at = blockIdx.y * kJoinRows + (threadIdx.x >> 5); at < end; at += kJoinWarps) {
+        const int tk = at / p.o.pack;
+        join_row<DP>(p.o, c.tok0 + tk, c.head0 + at - tk * p.o.pack, c.parts,
+                     [&](int i, const float*& row, const float2*& ml) {
+                         slot_row<DP>(p.o, 0, cut_slot(c.cta + i, i == 0), at, row, ml);
+                     });
     }
-    const int n = t.steps(e), ul = pu - t.pool_unit[e], a = t.pool_step[e] + ul * n;
-    const int c0 = t.cta_of(a), c1 = t.cta_of(a + n - 1);
-    if (c0 == c1 && !t.separate) return;  // not cut: written by the first kernel
-    const int u = t.full(e) + ul, rb = t.row_blocks(e), hb = u / rb;
-    const int tok0 = t.q_begin(e) + (u - hb * rb) * t.unit_tok;
-    const int rows = min(t.unit_tok, t.q_end(e) - tok0) * t.pack;
-    constexpr int kV = DP / 32;  // columns per lane
-    for (int at = blockIdx.y * kJoinRows + warp; at < min(rows, (int)(blockIdx.y + 1) * kJoinRows);
-         at += kJoinThreads / 32) {
-        const int tk = at / t.pack, r = tok0 + tk, h = hb * t.pack + at - tk * t.pack;
-        float acc[kV], m = -INFINITY, l = 0.0f;
-#pragma unroll
-        for (int j = 0; j < kV; ++j) acc[j] = 0.0f;
-        // partials first, first + step, ... (n of them) of one kind, for row `in` of its unit
-        auto join = [&](int kind, int first, int last_cta, int first_cta, int in, bool numbered) {
-            const long long stride = (long long)p.slot_rows[kind] * (DP + 2);
-            for (int c = first_cta; c <= last_cta; ++c) {
-                const int slot = numbered ? first + c : cut_slot(c, c == first_cta);
-                const float* base = p.part[kind] + slot * stride;
-                const float2 ml = __ldg(reinterpret_cast<const float2*>(base + (long long)p.slot_rows[kind] * DP) + in);
-                if (ml.y == 0.0f) continue;
-                const float m_new = fmaxf(m, ml.x);
-                const float f = m == m_new ? 1.0f : ex2_approx_ftz(m - m_new);
-                const float g = ml.x == m_new ? 1.0f : ex2_approx_ftz(ml.x - m_new);
-                const float* src = base + (long long)in * DP + lane * kV;
-#pragma unroll
-                for (int j = 0; j < kV; ++j) acc[j] = acc[j] * f + __ldg(src + j) * g;
-                l = l * f + ml.y * g;
-                m = m_new;
-            }
-        };
-        if (!t.separate) {
-            // the first partial begins its unit; it is the last piece of its CTA unless the stretch
-            // begins with the unit (then too: a piece that starts its unit takes the second slot)
-            join(0, 0, c1, c0, at, false);
-        } else {
-            join(0, pu, c1, c0, at, true);
-            if (t.ctx_tiles > 0) {
-                const int ce = t.nseg, cn = t.steps(ce), crb = t.row_blocks(ce);
-                const int ub = r / t.unit_tok, cu = hb * crb + ub, ca = t.pool_step[ce] + cu * cn;
-                const int in = (r - ub * t.unit_tok) * t.pack + at - tk * t.pack;
-                join(1, cu, t.cta_of(ca + cn - 1), t.cta_of(ca), in, true);
-            }
+}
+
+// The separate plan: block x takes the rows of a segment's unit, whose own keys
+// are one partial and the context's as many as its unit was cut into.
+template <int DP>
+__global__ void __launch_bounds__(kJoinThreads)
+    attn_join_separate_kernel(const __grid_constant__ JoinOut o, const __grid_constant__ AttnTable t)
+{
+    const int pu = blockIdx.x;
+    int lo = 0, hi = t.nseg;
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (t.pool_unit[mid] <= pu) lo = mid;
+        else hi = mid;
+    }
+    const int u = pu - t.pool_unit[lo], rb = t.row_blocks(lo), hb = u / rb;
+    const int tok0 = t.q_begin(lo) + (u - hb * rb) * t.unit_tok;
+    const int rows = min(t.unit_tok, t.q_end(lo) - tok0) * t.pack;
+    const int ce = t.nseg, cn = t.steps(ce), crb = t.row_blocks(ce);
+    int block = -1, first = 0, parts = 0;  // of the context's unit of the last row
+    griddep_wait();
+    for (int at = threadIdx.x >> 5; at < rows; at += kJoinWarps) {
+        const int tk = at / t.pack, r = tok0 + tk, head = at - tk * t.pack;
+        if (r / t.unit_tok != block) {
+            block = r / t.unit_tok;
+            const int ca = t.pool_step[ce] + (hb * crb + block) * cn;
+            first = t.cta_of(ca);
+            parts = t.cta_of(ca + cn - 1) - first + 1;
         }
-        const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-        __nv_bfloat16* o = p.out + (long long)r * p.out_row + (long long)h * p.out_head + lane * kV;
-#pragma unroll
-        for (int j = 0; j < kV; j += 2)
-            if (lane * kV + j < p.D) *reinterpret_cast<uint32_t*>(o + j) = cvt_bf16x2(f2(acc[j] * inv, acc[j + 1] * inv));
-        if (p.lse && lane == 0)
-            p.lse[(long long)r * p.Hq + h] = l == 0.0f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
+        const int in = (r - block * t.unit_tok) * t.pack + head;
+        join_row<DP>(o, r, hb * t.pack + head, 1 + parts, [&](int i, const float*& row, const float2*& ml) {
+            if (i == 0) slot_row<DP>(o, 0, pu, at, row, ml);
+            else slot_row<DP>(o, 1, hb * crb + block + first + i - 1, in, row, ml);
+        });
     }
 }
 
@@ -902,10 +975,19 @@ cudaError_t run(const AttnPlan& pl, const CUtensorMap (&m)[5], const AttnParams&
     cfg.numAttrs = 1;
     e = cudaLaunchKernelEx(&cfg, kernel, m[0], m[1], m[2], m[3], m[4], p);
     if (e != cudaSuccess || !pl.join) return e;
-    cfg.gridDim = dim3((unsigned)pl.t.pool_unit[pl.t.nseg], (unsigned)((pl.slot_rows[0] + kJoinRows - 1) / kJoinRows));
+    const JoinOut o{p.out, p.out_row, p.out_head, p.lse, {p.part[0], p.part[1]}, {p.slot_rows[0], p.slot_rows[1]},
+                    p.D, p.Hq, pl.t.pack};
     cfg.blockDim = dim3(kJoinThreads);
     cfg.dynamicSmemBytes = 0;
-    return cudaLaunchKernelEx(&cfg, attn_join_kernel<DP>, p);
+    if (pl.t.separate) {
+        cfg.gridDim = dim3((unsigned)pl.t.pool_unit[pl.t.nseg]);
+        return cudaLaunchKernelEx(&cfg, attn_join_separate_kernel<DP>, o, p.t);
+    }
+    JoinCuts cuts;
+    cuts.o = o;
+    std::memcpy(cuts.cuts, pl.cuts, sizeof(cuts.cuts));
+    cfg.gridDim = dim3((unsigned)pl.n_cuts, (unsigned)((pl.slot_rows[0] + kJoinRows - 1) / kJoinRows));
+    return cudaLaunchKernelEx(&cfg, attn_join_kernel<DP>, cuts);
 }
 
 }  // namespace

@@ -72,20 +72,28 @@ static const char* check(const Job& job)
     if ((int)seen.size() != [&] { int u = 0; for (int e = 0; e < t.entries; ++e) u += t.units(e); return u; }())
         return "units";
     if (!pl.join) return nullptr;
-    // the joining kernel's view
+    // the joining kernels' view
+    if (!t.separate) {
+        std::map<std::vector<int>, std::set<int>> want;
+        for (int i = 0; i < pl.n_cuts; ++i) {
+            const Cut& c = pl.cuts[i];
+            if (c.rows < 1 || c.rows > pl.slot_rows[0]) return "rows of a cut";
+            int e = 0;
+            while (c.tok0 >= t.q_end(e)) ++e;
+            if (c.rows != lesser(t.unit_tok, t.q_end(e) - c.tok0) * t.pack) return "rows of a cut";
+            for (int k = 0; k < c.parts; ++k) want[{e, c.head0, c.tok0}].insert(cut_slot(c.cta + k, k == 0));
+        }
+        return want == slots[0] ? nullptr : "slots joined are not those written";
+    }
     for (int e = 0; e < t.entries; ++e)
-        for (int ul = 0; ul < t.units(e) - t.full(e); ++ul) {
-            const int kind = e < t.nseg ? 0 : 1;
-            const int n = t.steps(e), a = t.pool_step[e] + ul * n, c0 = t.cta_of(a), c1 = t.cta_of(a + n - 1);
-            const int u = t.full(e) + ul, rb = t.row_blocks(e), hb = u / rb;
-            const std::vector<int> key = {e, hb * t.pack, t.q_begin(e) + (u - hb * rb) * t.unit_tok};
+        for (int u = 0; u < t.units(e); ++u) {
+            const int n = t.steps(e), a = t.pool_step[e] + u * n, rb = t.row_blocks(e), hb = u / rb;
             std::set<int> want;
-            if (t.separate)
-                for (int c = c0; c <= c1; ++c) want.insert((kind ? u : t.pool_unit[e] + ul) + c);
-            else if (c0 != c1)
-                for (int c = c0; c <= c1; ++c) want.insert(cut_slot(c, c == c0));
-            const auto it = slots[kind].find(key);
-            if (want != (it == slots[kind].end() ? std::set<int>() : it->second)) return "slots joined are not those written";
+            if (e < t.nseg) want.insert(t.pool_unit[e] + u);
+            else
+                for (int c = t.cta_of(a); c <= t.cta_of(a + n - 1); ++c) want.insert(u + c);
+            if (want != slots[e < t.nseg ? 0 : 1][{e, hb * t.pack, t.q_begin(e) + (u - hb * rb) * t.unit_tok}])
+                return "slots joined are not those written";
         }
     return nullptr;
 }
