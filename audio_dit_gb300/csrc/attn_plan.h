@@ -18,6 +18,11 @@
 // cut into equal stretches, one per CTA: a unit that is cut leaves partial sums
 // that a second kernel joins.  A cut within kSnap steps of a unit's edge moves
 // there, since a partial costs about as much as that many steps.
+//
+// Few units of a head over keys that do not fit in L2: were they cut one after
+// the other, the units of a head would walk the same keys at different times and
+// each read them from memory.  There the pool holds one row of steps per head,
+// and a stretch goes to `lanes` CTAs side by side, one per unit of the head.
 #pragma once
 #include <cstddef>
 #include <cstdint>
@@ -44,7 +49,8 @@ struct AttnTable {
     int any_full;          // some entry has whole waves
     int ctx_masked, own_masked, ctx_ragged;  // masks are given; the context's length is no multiple of a tile
     int pool_steps, pool_units;
-    int share, longer;     // steps of a CTA's stretch of the pool: share + 1 for the first `longer` CTAs
+    int lanes, stretches;  // CTAs side by side on a stretch of the pool, and stretches
+    int share, longer;     // steps of a stretch: share + 1 for the first `longer` of them
     int M;
     int q_off[H3FP4_ATTN_MAX_SEGMENTS + 1];
     int kv_off[H3FP4_ATTN_MAX_SEGMENTS + 1];
@@ -81,11 +87,11 @@ struct AttnTable {
         }
         return lo;
     }
-    // Where CTA c's stretch of the pool begins.
+    // Where stretch c of the pool begins.
     __host__ __device__ int bound(int c) const
     {
         const int x = c * share + lesser(c, longer);
-        if (c <= 0 || c >= ctas || x <= 0 || x >= pool_steps) return x;
+        if (c <= 0 || c >= stretches || x <= 0 || x >= pool_steps) return x;
         const int e = find(pool_step, x), n = steps(e), t = (x - pool_step[e]) % n;
         // (a segment's unit of the separate plan is never cut)
         const int snap = separate && e < nseg ? n : kSnap;
@@ -93,13 +99,13 @@ struct AttnTable {
         if (n - t <= snap) return x + n - t;
         return x;
     }
-    // The CTA whose stretch holds step x of the pool.
-    __host__ __device__ int cta_of(int x) const
+    // The stretch that holds step x of the pool.
+    __host__ __device__ int stretch_of(int x) const
     {
         const int head = longer * (share + 1);
-        int c = x < head ? x / (share + 1) : share > 0 ? longer + (x - head) / share : ctas - 1;
+        int c = x < head ? x / (share + 1) : share > 0 ? longer + (x - head) / share : stretches - 1;
         while (c > 0 && bound(c) > x) --c;
-        while (c + 1 < ctas && bound(c + 1) <= x) ++c;
+        while (c + 1 < stretches && bound(c + 1) <= x) ++c;
         return c;
     }
 };
@@ -173,13 +179,20 @@ struct Walk {
         hb = rb = e = 0;
         blocks = 1;
         if (t.pool_steps == 0) return;
-        const int pos = t.bound(cta);
-        left = t.bound(cta + 1) - pos;
+        const int stretch = cta / t.lanes;
+        if (stretch >= t.stretches) return;
+        const int pos = t.bound(stretch);
+        left = t.bound(stretch + 1) - pos;
         if (left <= 0) return;
         e = t.find(t.pool_step, pos);
         const int n = t.steps(e), local = pos - t.pool_step[e], u = local / n;
         tile = local - u * n;
         blocks = t.row_blocks(e);
+        if (t.lanes > 1) {
+            hb = u;
+            rb = cta - stretch * t.lanes;
+            return;
+        }
         hb = (t.full(e) + u) / blocks;
         rb = t.full(e) + u - hb * blocks;
     }
@@ -230,7 +243,9 @@ struct Walk {
                               : hb * blocks + rb + cta;
         left -= take;
         tile = 0;
-        if (++rb == blocks) {
+        if (t.lanes > 1) {
+            ++hb;
+        } else if (++rb == blocks) {
             rb = 0;
             if (++hb == t.head_blocks && left > 0) {
                 do ++e;
@@ -252,7 +267,8 @@ struct Walk {
     }
 };
 
-// A unit of the pool that is cut, and the CTAs that hold its pieces.
+// A unit of the pool that is cut, the first CTA that holds a piece, and how many do
+// (each `lanes` after the one before).
 struct Cut {
     int tok0, head0, rows, cta, parts;
 };
@@ -347,15 +363,27 @@ inline AttnPlan make_plan(const Job& job)
     if (!sep && t.ctas == kAttnCtas)
         for (int e = 0; e < t.entries; ++e)
             if (t.units(e) >= t.ctas) t.any_full = 1;
+    // Units of a head side by side: one entry, all of it in the pool, keys of more
+    // than 64 MB (half the L2), and at most a twentieth of the CTAs left idle.
+    t.lanes = 1;
+    t.stretches = t.ctas;
+    if (t.entries == 1 && !t.any_full && t.ctas == kAttnCtas) {
+        const int rb = t.row_blocks(0), idle = kAttnCtas % rb;
+        const double key_bytes = 4.0 * job.Hkv * job.D * ((double)job.T + (double)job.C);
+        if (rb > 1 && rb <= kAttnCtas / 2 && idle * 20 <= kAttnCtas && key_bytes > 64.0 * 1024 * 1024) {
+            t.lanes = rb;
+            t.stretches = kAttnCtas / rb;
+        }
+    }
     for (int e = 0; e < t.entries; ++e) {
         const int rest = t.units(e) - t.full(e);
         t.pool_unit[e + 1] = t.pool_unit[e] + rest;
-        t.pool_step[e + 1] = t.pool_step[e] + rest * t.steps(e);
+        t.pool_step[e + 1] = t.pool_step[e] + rest / t.lanes * t.steps(e);
     }
     t.pool_units = t.pool_unit[t.entries];
     t.pool_steps = t.pool_step[t.entries];
-    t.share = t.pool_steps / t.ctas;
-    t.longer = t.pool_steps % t.ctas;
+    t.share = t.pool_steps / t.stretches;
+    t.longer = t.pool_steps % t.stretches;
 
     // Partials: rows of the largest unit of each kind, an even number so that
     // every slot of rows * (dp + 2) floats begins on 16 bytes.
@@ -372,19 +400,23 @@ inline AttnPlan make_plan(const Job& job)
         pl.slots[0] = t.pool_unit[t.nseg];
         pl.slots[1] = t.units(t.nseg) + t.ctas;
     } else {
-        for (int c = 1, cut = -1; c < t.ctas && t.pool_steps > 0; ++c) {
+        for (int c = 1, cut = -1; c < t.stretches && t.pool_steps > 0; ++c) {
             const int x = t.bound(c);
             if (x <= 0 || x >= t.pool_steps) continue;
             const int e = t.find(t.pool_step, x), n = t.steps(e), local = x - t.pool_step[e], u = local / n;
             if (local == u * n) continue;
             const int id = t.pool_unit[e] + u;
             if (id == cut) {  // cut once more
-                ++pl.cuts[pl.n_cuts - 1].parts;
+                for (int k = 1; k <= t.lanes; ++k) ++pl.cuts[pl.n_cuts - k].parts;
                 continue;
             }
             cut = id;
-            const int rb = t.row_blocks(e), all = t.full(e) + u, hb = all / rb, tok0 = t.q_begin(e) + (all - hb * rb) * t.unit_tok;
-            pl.cuts[pl.n_cuts++] = Cut{tok0, hb * pack, lesser(t.unit_tok, t.q_end(e) - tok0) * pack, c - 1, 2};
+            for (int k = 0; k < t.lanes; ++k) {
+                const int rb = t.row_blocks(e), all = t.lanes > 1 ? u * rb + k : t.full(e) + u, hb = all / rb;
+                const int tok0 = t.q_begin(e) + (all - hb * rb) * t.unit_tok;
+                pl.cuts[pl.n_cuts++] = Cut{tok0, hb * pack, lesser(t.unit_tok, t.q_end(e) - tok0) * pack,
+                                           (c - 1) * t.lanes + k, 2};
+            }
         }
         pl.join = pl.n_cuts > 0;
         pl.slots[0] = pl.join ? 2 * t.ctas : 0;

@@ -187,32 +187,19 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t* mask_bits = reinterpret_cast<uint32_t*>(smem + L::kMaskOff);
     float2* stat = reinterpret_cast<float2*>(smem + L::kStatOff);  // [2][128]: (maximum, sum)
 
-    if (threadIdx.x == 0) {
-        for (int i = 0; i < 2; ++i) {
-            mbar_init(&done[i], 1);
-            mbar_init(&turn[i], 1);
-            mbar_init(&s_full[i], 1);
-            mbar_init(&p_half[i], 4);
-            mbar_init(&p_full[i], 4);
-            mbar_init(&o_full[i], 1);
-            mbar_init(&o_empty[i], 4);
-            mbar_init(&stat_full[i], 4);
-            mbar_init(&stat_empty[i], 4);
-        }
-        for (int i = 0; i < 2 * L::kQ; ++i) mbar_init(&q_full[i], 1);
-        for (int i = 0; i < L::kQ; ++i) mbar_init(&q_empty[i], kSolo ? 2 : 1);
-        for (int i = 0; i < 2 * kStages; ++i) mbar_init(&kv_full[i], 1);
-        for (int i = 0; i < kStages; ++i) mbar_init(&kv_empty[i], kSolo ? 1 : 2);
-        for (int i = 0; i < kPieceSlots; ++i) {
-            mbar_init(&piece_full[i], 1);
-            mbar_init(&piece_empty[i], 16);  // warps: loads, MMAs (2), gaps, softmax (8), epilogue (4)
-        }
-        for (int i = 0; i < kMaskSlots; ++i) {
-            mbar_init(&gap_load[i], 1);
-            mbar_init(&mask_full[i], 1);
-            mbar_init(&zero_full[i], 1);
-        }
+    if (threadIdx.x < L::kBars) {
+        // one barrier per thread; the arrivals that complete a phase
+        const uint64_t* b = q_full + threadIdx.x;
+        auto in = [&](const uint64_t* first, int n) { return b >= first && b < first + n; };
+        const uint32_t count = in(q_empty, L::kQ)                             ? (kSolo ? 2 : 1)
+                               : in(kv_empty, kStages)                        ? (kSolo ? 1 : 2)
+                               : in(p_half, 4) || in(o_empty, 6)              ? 4   // warps of a warpgroup
+                               : in(piece_empty, kPieceSlots)                 ? 16  // loads, MMAs (2), gaps, softmax (8), epilogue (4)
+                                                                              : 1;
+        mbar_init(q_full + threadIdx.x, count);
         fence_mbarrier_init();
+    }
+    if (threadIdx.x == 0) {
         prefetch_tensormap(&tmQ);
         if (p.T > 0) {
             prefetch_tensormap(&tmK);
@@ -233,6 +220,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     // Everything above overlaps the previous kernel's tail (programmatic
     // dependent launch); its outputs are read only after this.
     griddep_wait();
+    // The next kernel's blocks (those that join partials) may queue up from here on: they find
+    // room as CTAs leave, and read nothing before all have.
+    griddep_launch_dependents();
     const uint32_t tmem = *tmem_slot;
     const int tok = p.t.tok;
     // The pieces of this CTA, described by warp 2 a few ahead (a walk costs some hundred cycles of
@@ -780,7 +770,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
         }
     }
-    griddep_launch_dependents();
     tc_fence_before();
     __syncthreads();
     if (warp == 2) {
@@ -887,6 +876,7 @@ __device__ __forceinline__ void slot_row(const JoinOut& p, int kind, int slot, i
 // The cut units of the pool: block (i, y) takes rows 16 y... of cut i.
 struct JoinCuts {
     JoinOut o;
+    int lanes;
     Cut cuts[kAttnCtas];
 };
 
@@ -900,13 +890,13 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const __grid_co
         const int tk = at / p.o.pack;
         join_row<DP>(p.o, c.tok0 + tk, c.head0 + at - tk * p.o.pack, c.parts,
                      [&](int i, const float*& row, const float2*& ml) {
-                         slot_row<DP>(p.o, 0, cut_slot(c.cta + i, i == 0), at, row, ml);
+                         slot_row<DP>(p.o, 0, cut_slot(c.cta + i * p.lanes, i == 0), at, row, ml);
                      });
     }
 }
 
-// The separate plan: block x takes the rows of a segment's unit, whose own keys
-// are one partial and the context's as many as its unit was cut into.
+// The separate plan: blocks (x, y) take the rows of segments' unit x, a warp each.
+// Their own keys are one partial, the context's as many as its unit was cut into.
 template <int DP>
 __global__ void __launch_bounds__(kJoinThreads)
     attn_join_separate_kernel(const __grid_constant__ JoinOut o, const __grid_constant__ AttnTable t)
@@ -921,23 +911,24 @@ __global__ void __launch_bounds__(kJoinThreads)
     const int u = pu - t.pool_unit[lo], rb = t.row_blocks(lo), hb = u / rb;
     const int tok0 = t.q_begin(lo) + (u - hb * rb) * t.unit_tok;
     const int rows = min(t.unit_tok, t.q_end(lo) - tok0) * t.pack;
-    const int ce = t.nseg, cn = t.steps(ce), crb = t.row_blocks(ce);
-    int block = -1, first = 0, parts = 0;  // of the context's unit of the last row
-    griddep_wait();
-    for (int at = threadIdx.x >> 5; at < rows; at += kJoinWarps) {
-        const int tk = at / t.pack, r = tok0 + tk, head = at - tk * t.pack;
-        if (r / t.unit_tok != block) {
-            block = r / t.unit_tok;
-            const int ca = t.pool_step[ce] + (hb * crb + block) * cn;
-            first = t.cta_of(ca);
-            parts = t.cta_of(ca + cn - 1) - first + 1;
-        }
-        const int in = (r - block * t.unit_tok) * t.pack + head;
-        join_row<DP>(o, r, hb * t.pack + head, 1 + parts, [&](int i, const float*& row, const float2*& ml) {
-            if (i == 0) slot_row<DP>(o, 0, pu, at, row, ml);
-            else slot_row<DP>(o, 1, hb * crb + block + first + i - 1, in, row, ml);
-        });
+    const int at = blockIdx.y * kJoinWarps + (threadIdx.x >> 5);
+    int r = 0, h = 0, slot = 0, parts = 0, in = 0;
+    if (at < rows) {
+        const int tk = at / t.pack, ce = t.nseg, cn = t.steps(ce);
+        r = tok0 + tk;
+        h = hb * t.pack + at - tk * t.pack;
+        const int block = r / t.unit_tok, cu = hb * t.row_blocks(ce) + block, ca = t.pool_step[ce] + cu * cn;
+        const int first = t.stretch_of(ca);
+        parts = t.stretch_of(ca + cn - 1) - first + 1;
+        slot = cu + first;
+        in = (r - block * t.unit_tok) * t.pack + at - tk * t.pack;
     }
+    griddep_wait();
+    if (at >= rows) return;
+    join_row<DP>(o, r, h, 1 + parts, [&](int i, const float*& row, const float2*& ml) {
+        if (i == 0) slot_row<DP>(o, 0, pu, at, row, ml);
+        else slot_row<DP>(o, 1, slot + i - 1, in, row, ml);
+    });
 }
 
 // ------------------------------------------------------------------ host side
@@ -980,11 +971,13 @@ cudaError_t run(const AttnPlan& pl, const CUtensorMap (&m)[5], const AttnParams&
     cfg.blockDim = dim3(kJoinThreads);
     cfg.dynamicSmemBytes = 0;
     if (pl.t.separate) {
-        cfg.gridDim = dim3((unsigned)pl.t.pool_unit[pl.t.nseg]);
+        cfg.gridDim = dim3((unsigned)pl.t.pool_unit[pl.t.nseg],
+                           (unsigned)((pl.slot_rows[0] + kJoinWarps - 1) / kJoinWarps));
         return cudaLaunchKernelEx(&cfg, attn_join_separate_kernel<DP>, o, p.t);
     }
     JoinCuts cuts;
     cuts.o = o;
+    cuts.lanes = pl.t.lanes;
     std::memcpy(cuts.cuts, pl.cuts, sizeof(cuts.cuts));
     cfg.gridDim = dim3((unsigned)pl.n_cuts, (unsigned)((pl.slot_rows[0] + kJoinRows - 1) / kJoinRows));
     return cudaLaunchKernelEx(&cfg, attn_join_kernel<DP>, cuts);

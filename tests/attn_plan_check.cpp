@@ -2,7 +2,7 @@
 // cover every key tile of every unit exactly once, that partial sums never share
 // a slot or leave the workspace, and that the joining kernel reads just the slots
 // that were written.  Input lines: M T C Hq Hkv D nseg q_off... kv_off...
-// Prints one line per problem: "ok solo separate join ctas" or what is wrong.
+// Prints one line per problem: "ok solo separate join ctas lanes" or what is wrong.
 #define __host__
 #define __device__
 #include <cstdio>
@@ -81,7 +81,7 @@ static const char* check(const Job& job)
             int e = 0;
             while (c.tok0 >= t.q_end(e)) ++e;
             if (c.rows != lesser(t.unit_tok, t.q_end(e) - c.tok0) * t.pack) return "rows of a cut";
-            for (int k = 0; k < c.parts; ++k) want[{e, c.head0, c.tok0}].insert(cut_slot(c.cta + k, k == 0));
+            for (int k = 0; k < c.parts; ++k) want[{e, c.head0, c.tok0}].insert(cut_slot(c.cta + k * t.lanes, k == 0));
         }
         return want == slots[0] ? nullptr : "slots joined are not those written";
     }
@@ -91,7 +91,7 @@ static const char* check(const Job& job)
             std::set<int> want;
             if (e < t.nseg) want.insert(t.pool_unit[e] + u);
             else
-                for (int c = t.cta_of(a); c <= t.cta_of(a + n - 1); ++c) want.insert(u + c);
+                for (int c = t.stretch_of(a); c <= t.stretch_of(a + n - 1); ++c) want.insert(u + c);
             if (want != slots[e < t.nseg ? 0 : 1][{e, hb * t.pack, t.q_begin(e) + (u - hb * rb) * t.unit_tok}])
                 return "slots joined are not those written";
         }
@@ -113,7 +113,7 @@ int main()
         const char* bad = check(job);
         const AttnPlan pl = make_plan(job);
         if (bad) std::printf("%s\n", bad);
-        else std::printf("ok %d %d %d %d\n", (int)pl.solo, pl.t.separate, (int)pl.join, pl.t.ctas);
+        else std::printf("ok %d %d %d %d %d\n", (int)pl.solo, pl.t.separate, (int)pl.join, pl.t.ctas, pl.t.lanes);
     }
     return 0;
 }

@@ -35,10 +35,18 @@ def one(M, T, C, Hq, Hkv, D=128):
 def test_named_sizes(check):
     got = check([one(30720, 512, 0, 24, 24), one(1024, 30720, 0, 24, 24), one(1, 32768, 0, 32, 8), one(1, 1, 0, 1, 1),
                  (16384, 16384, 1024, 24, 24, 128, [0, 8192, 16384], [0, 8192, 16384]),
+                 one(500, 70000, 0, 24, 24), one(130, 70000, 0, 24, 8),
                  (48, 9000, 16384, 32, 8, 128, list(range(49)), [i * 9000 // 48 for i in range(49)])])
     assert [g.split()[:4] for g in got] == [
         ["ok", "0", "0", "0"], ["ok", "0", "0", "1"], ["ok", "1", "0", "1"], ["ok", "1", "0", "0"],
-        ["ok", "0", "0", "1"], ["ok", "1", "1", "1"]], got
+        ["ok", "0", "0", "1"], ["ok", "0", "0", "1"], ["ok", "0", "0", "1"], ["ok", "1", "1", "1"]], got
+    # side by side where the keys of a head's units would be read once for each
+
+
+def test_lanes(check):
+    lanes = [int(g.split()[5]) for g in check([one(1024, 30720, 0, 24, 24), one(500, 70000, 0, 24, 24),
+                                               one(1024, 1024, 0, 24, 24), one(1, 32768, 0, 32, 8)])]
+    assert lanes[0] == 4 and lanes[1] == 2 and lanes[2:] == [1, 1], lanes
 
 
 def test_random_problems(check):
