@@ -12,6 +12,7 @@ from __future__ import annotations
 
 import ctypes as C
 import os
+from array import array
 from typing import Optional, Sequence
 
 import torch
@@ -67,7 +68,7 @@ def load_library():
     if not os.path.exists(path):
         raise ImportError(f"libh3fp4.so not built ({path}); run `python -m audio_dit_gb300.build`")
     L = C.CDLL(path)
-    i64, vp, i32, sz, hp = C.c_int64, C.c_void_p, C.c_int, C.c_size_t, C.POINTER(_Heads)
+    i64, vp, i32, sz, hp = C.c_int64, C.c_void_p, C.c_int, C.c_size_t, C.c_void_p  # hp: h3fp4_heads
     sig = {
         "h3fp4_codes_bytes": (sz, [i64, i64]),
         "h3fp4_sf_bytes": (sz, [i64, i64]),
@@ -122,26 +123,37 @@ def _ptr(t: Optional[torch.Tensor], what: str, dtype=None):
     return t.data_ptr()
 
 
-def _heads(t: Optional[torch.Tensor], what: str, shape):
-    """(h3fp4_heads of a bf16 [rows, heads, D] view, or None).  Any row and head
-    strides; the elements of a head are contiguous."""
-    if t is None:
-        return None
+_BF16 = torch.bfloat16
+
+
+def _heads(t: torch.Tensor, what: str, rows: int, heads: int, d: int):
+    """(address, row stride, head stride) of a bf16 [rows, heads, d] view: any row
+    and head strides, the elements of a head contiguous."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{what} must be a torch.Tensor")
     if not t.is_cuda:
         raise ValueError(f"{what} must be a CUDA tensor")
-    if t.dtype != torch.bfloat16:
-        raise TypeError(f"{what} must be {torch.bfloat16}, got {t.dtype}")
-    if tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{what} must be {list(shape)}, got {list(t.shape)}")
-    rows, heads, d = t.shape
-    if d > 1 and t.stride(2) != 1:
+    if t.dtype is not _BF16:
+        raise TypeError(f"{what} must be {_BF16}, got {t.dtype}")
+    if t.shape != (rows, heads, d):
+        raise ValueError(f"{what} must be {[rows, heads, d]}, got {list(t.shape)}")
+    row, head, one = t.stride()
+    if d > 1 and one != 1:
         raise ValueError(f"{what}: the last dimension must be contiguous")
     # the stride of a dimension of one element says nothing about the memory
-    head = t.stride(1) if heads > 1 else d
-    row = t.stride(0) if rows > 1 else heads * head
-    return C.byref(_Heads(t.data_ptr(), row, head))
+    if heads <= 1:
+        head = d
+    if rows <= 1:
+        row = heads * head
+    return t.data_ptr(), row, head
+
+
+def _table(seq: Optional[Sequence[int]]):
+    """(array of int64 to keep, its address, number of segments) of an offset table."""
+    if seq is None:
+        return None, None, 1
+    a = array("q", seq if isinstance(seq, list) else [int(v) for v in seq])
+    return a, a.buffer_info()[0], len(a) - 1
 
 
 def _mask(t: Optional[torch.Tensor], what: str, n: int):
@@ -167,14 +179,15 @@ def _seg_pair(q_off, kv_off):
         raise ValueError("q_off and kv_off go together")
     if q_off is not None and len(q_off) != len(kv_off):
         raise ValueError(f"q_off and kv_off must have the same length, got {len(q_off)} and {len(kv_off)}")
-    qp, nseg, keep_q = _segs(q_off)
-    kp, _, keep_k = _segs(kv_off)
-    return qp, kp, nseg, (keep_q, keep_k)
+    keep_q, q, nseg = _table(q_off)
+    keep_k, k, _ = _table(kv_off)
+    return q, k, nseg, (keep_q, keep_k)
 
 
 def _stream(stream) -> Optional[int]:
     if stream is None:
-        stream = torch.cuda.current_stream()
+        # the raw handle: torch.cuda.current_stream() builds a Stream object, 3 us per call
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
     return stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
 
 
@@ -396,14 +409,18 @@ def h3fp4_qk_norm_rope(q: torch.Tensor, k: Optional[torch.Tensor], q_out: torch.
     if (k is None) != (k_out is None):
         raise ValueError("k and k_out go together")
     Hk = k.shape[1] if k is not None else 0
-    sp, nseg, _keep = _segs(seg_off)
+    keep, sp, nseg = _table(seg_off)
     half = cos.shape[-1] if cos is not None else 0
+    views = [*_heads(q, "q", M, Hq, D), *_heads(q_out, "q_out", M, Hq, D)]
+    if k is not None:
+        views += (*_heads(k, "k", M, Hk, D), *_heads(k_out, "k_out", M, Hk, D))
+    a = array("q", views)   # h3fp4_heads, one after the other
+    at = a.buffer_info()[0]
     _check(load_library().h3fp4_qk_norm_rope(
-        _heads(q, "q", (M, Hq, D)), _heads(k, "k", (M, Hk, D)), M, Hq, Hk, D,
-        _f32(q_weight, "q_weight", (nseg, D)), _f32(k_weight, "k_weight", (nseg, D)),
-        _f32(cos, "cos", (M, half)), _f32(sin, "sin", (M, half)), 2 * half, sp, nseg, float(eps),
-        _heads(q_out, "q_out", (M, Hq, D)), _heads(k_out, "k_out", (M, Hk, D)),
-        ROPE_PAIRS if interleaved else 0, _stream(stream)), "h3fp4_qk_norm_rope")
+        at, at + 48 if k is not None else None, M, Hq, Hk, D, _f32(q_weight, "q_weight", (nseg, D)),
+        _f32(k_weight, "k_weight", (nseg, D)), _f32(cos, "cos", (M, half)), _f32(sin, "sin", (M, half)), 2 * half,
+        sp, nseg, eps, at + 24, at + 72 if k is not None else None, ROPE_PAIRS if interleaved else 0,
+        _stream(stream)), "h3fp4_qk_norm_rope")
 
 
 def h3fp4_cross_attn(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, out: torch.Tensor, ws: torch.Tensor, *,
@@ -418,12 +435,14 @@ def h3fp4_cross_attn(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, out: tor
     :func:`alloc_attn_workspace`."""
     M, Hq, D = q.shape
     T, Hkv, _ = k.shape
-    qp, kp, nseg, _keep = _seg_pair(q_off, kv_off)
+    qp, kp, nseg, keep = _seg_pair(q_off, kv_off)
+    a = array("q", (*_heads(q, "q", M, Hq, D), *_heads(k, "k", T, Hkv, D), *_heads(v, "v", T, Hkv, D),
+                    *_heads(out, "out", M, Hq, D)))
+    at = a.buffer_info()[0]
     _check(load_library().h3fp4_cross_attn(
-        _heads(q, "q", (M, Hq, D)), _heads(k, "k", (T, Hkv, D)), _heads(v, "v", (T, Hkv, D)), M, T, Hq, Hkv, D,
-        qp, kp, nseg, _mask(key_mask, "key_mask", T), D ** -0.5 if scale is None else float(scale),
-        _heads(out, "out", (M, Hq, D)), _f32(lse, "lse", (M, Hq)), _ptr(ws, "ws", torch.uint8), ws.numel(),
-        _stream(stream)), "h3fp4_cross_attn")
+        at, at + 24, at + 48, M, T, Hq, Hkv, D, qp, kp, nseg, _mask(key_mask, "key_mask", T),
+        D ** -0.5 if scale is None else scale, at + 72, _f32(lse, "lse", (M, Hq)), _ptr(ws, "ws", torch.uint8),
+        ws.numel(), _stream(stream)), "h3fp4_cross_attn")
 
 
 def h3fp4_shared_attn(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, k_ctx: torch.Tensor, v_ctx: torch.Tensor,
@@ -437,13 +456,15 @@ def h3fp4_shared_attn(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, k_ctx: 
     M, Hq, D = q.shape
     T, Hkv, _ = k.shape
     ctx = k_ctx.shape[0]
-    qp, kp, nseg, _keep = _seg_pair(q_off, kv_off)
+    qp, kp, nseg, keep = _seg_pair(q_off, kv_off)
+    a = array("q", (*_heads(q, "q", M, Hq, D), *_heads(k, "k", T, Hkv, D), *_heads(v, "v", T, Hkv, D),
+                    *_heads(k_ctx, "k_ctx", ctx, Hkv, D), *_heads(v_ctx, "v_ctx", ctx, Hkv, D),
+                    *_heads(out, "out", M, Hq, D)))
+    at = a.buffer_info()[0]
     _check(load_library().h3fp4_shared_attn(
-        _heads(q, "q", (M, Hq, D)), _heads(k, "k", (T, Hkv, D)), _heads(v, "v", (T, Hkv, D)),
-        _heads(k_ctx, "k_ctx", (ctx, Hkv, D)), _heads(v_ctx, "v_ctx", (ctx, Hkv, D)), M, T, ctx, Hq, Hkv, D,
-        qp, kp, nseg, _mask(key_mask, "key_mask", T), _mask(ctx_mask, "ctx_mask", ctx),
-        D ** -0.5 if scale is None else float(scale), _heads(out, "out", (M, Hq, D)), _f32(lse, "lse", (M, Hq)),
-        _ptr(ws, "ws", torch.uint8), ws.numel(), _stream(stream)), "h3fp4_shared_attn")
+        at, at + 24, at + 48, at + 72, at + 96, M, T, ctx, Hq, Hkv, D, qp, kp, nseg, _mask(key_mask, "key_mask", T),
+        _mask(ctx_mask, "ctx_mask", ctx), D ** -0.5 if scale is None else scale, at + 120,
+        _f32(lse, "lse", (M, Hq)), _ptr(ws, "ws", torch.uint8), ws.numel(), _stream(stream)), "h3fp4_shared_attn")
 
 
 def h3fp4_attn_workspace_bytes(M: int, T: int, Hq: int, Hkv: int, D: int, q_off: Optional[Sequence[int]] = None,

@@ -286,37 +286,44 @@ struct AttnPlan {
     size_t bytes;        // workspace; 0: more steps than 32 bits count
 };
 
-// Units, steps and the pool for one choice of pack, solo and separate.
-template <class Job>
-inline void lay_out(const Job& job, int pack, bool solo, bool separate, AttnTable& t)
-{
-    t.nseg = job.nseg;
-    t.entries = job.nseg + (separate ? 1 : 0);
-    t.pack = pack;
-    t.tok = 128 / pack;
-    t.unit_tok = solo ? t.tok : 2 * t.tok;
-    t.head_blocks = job.Hq / pack;
-    t.ctx_tiles = (int)((job.C + kKeyTile - 1) / kKeyTile);
-    t.separate = separate ? 1 : 0;
-    t.ctx_ragged = job.C % kKeyTile != 0;
-    t.M = (int)job.M;
-    t.ctas = kAttnCtas;
-}
+// Units and steps of all of them for one choice of pack and of solo or pair units:
+// with the segments' units walking the context too, and with it apart.
+struct Cost {
+    double units, steps, units_apart, steps_apart;
+};
 
-// Steps of all units.
-inline double total_steps(const AttnTable& t)
+template <class Job>
+inline Cost cost_of(const Job& job, const AttnTable& t, int pack, bool solo)
 {
-    double s = 0;
-    for (int e = 0; e < t.entries; ++e) s += (double)t.units(e) * t.steps(e);
-    return s;
+    const int tok = 128 / pack, unit_tok = solo ? tok : 2 * tok;
+    const long long ctx = t.ctx_tiles;
+    long long units = 0, steps = 0, own = 0;
+    for (int e = 0; e < t.nseg; ++e) {
+        const long long rb = (t.q_off[e + 1] - t.q_off[e] + unit_tok - 1) / unit_tok, n = t.tiles_own(e);
+        units += rb;
+        steps += rb * (ctx + n > 0 ? ctx + n : 1);
+        own += rb * (n > 0 ? n : 1);
+    }
+    const long long apart = (job.M + unit_tok - 1) / unit_tok, hb = job.Hq / pack;
+    return Cost{(double)(hb * units), (double)hb * (double)steps, (double)(hb * (units + apart)),
+                (double)hb * (double)(own + apart * (ctx > 0 ? ctx : 1))};
 }
 
 template <class Job>
 inline AttnPlan make_plan(const Job& job)
 {
-    AttnPlan pl{};
+    AttnPlan pl;
     AttnTable& t = pl.t;
+    pl.bytes = 0;
+    pl.join = false;
+    pl.n_cuts = 0;
+    pl.slots[0] = pl.slots[1] = 0;
     pl.dp = job.D <= 64 ? 64 : 128;
+    t.nseg = job.nseg;
+    t.M = (int)job.M;
+    t.ctx_tiles = (int)((job.C + kKeyTile - 1) / kKeyTile);
+    t.ctx_ragged = job.C % kKeyTile != 0;
+    t.ctx_masked = t.own_masked = 0;  // set at launch
     for (int i = 0; i <= job.nseg; ++i) {
         t.q_off[i] = (int)job.q_off[i];
         t.kv_off[i] = (int)job.kv_off[i];
@@ -327,36 +334,33 @@ inline AttnPlan make_plan(const Job& job)
     double best = 0;
     for (int g = 1; g <= group && g <= 128; ++g) {
         if (group % g) continue;
-        lay_out(job, g, true, false, t);
-        const double s = total_steps(t);
+        const double s = group == 1 ? 0 : cost_of(job, t, g, true).steps;
         if (g == 1 || s <= best) {
             best = s;
             pack = g;
         }
     }
     // A pair's step takes about 1.5 of a solo step (which reads K and V for one
-    // tile of queries only); the separate plan pays a step per unit for its partials.
-    double cost[2][2];
-    for (int sep = 0; sep < 2; ++sep)
-        for (int solo = 0; solo < 2; ++solo) {
-            lay_out(job, pack, solo != 0, sep != 0, t);
-            double units = 0;
-            for (int e = 0; e < t.entries; ++e) units += t.units(e);
-            cost[sep][solo] = (total_steps(t) + (sep ? 2 * units : 0)) * (solo ? 1.0 : 1.5);
-        }
-    const bool can_separate = job.nseg > 1 && job.C > 0;
-    const double whole = cost[0][0] < cost[0][1] ? cost[0][0] : cost[0][1];
-    const double apart = cost[1][0] < cost[1][1] ? cost[1][0] : cost[1][1];
-    const bool sep = can_separate && apart + 2 * kAttnCtas < whole;
-    pl.solo = cost[sep][1] <= cost[sep][0];
-    lay_out(job, pack, pl.solo, sep, t);
+    // tile of queries only); the separate plan pays two steps per unit for its partials.
+    const Cost pair = cost_of(job, t, pack, false), single = cost_of(job, t, pack, true);
+    const double whole = single.steps < 1.5 * pair.steps ? single.steps : 1.5 * pair.steps;
+    const double solo_apart = single.steps_apart + 2 * single.units_apart;
+    const double pair_apart = 1.5 * (pair.steps_apart + 2 * pair.units_apart);
+    const double apart = solo_apart < pair_apart ? solo_apart : pair_apart;
+    const bool sep = job.nseg > 1 && job.C > 0 && apart + 2 * kAttnCtas < whole;
+    pl.solo = sep ? solo_apart <= pair_apart : single.steps <= 1.5 * pair.steps;
+    t.entries = job.nseg + (sep ? 1 : 0);
+    t.pack = pack;
+    t.tok = 128 / pack;
+    t.unit_tok = pl.solo ? t.tok : 2 * t.tok;
+    t.head_blocks = job.Hq / pack;
+    t.separate = sep ? 1 : 0;
 
     // CTAs: one per SM where there is work for all of them.
-    const double steps = total_steps(t);
-    if (steps >= 2147483648.0) return pl;  // steps are counted in 32 bits; bytes = 0
-    long long units = 0;
-    for (int e = 0; e < t.entries; ++e) units += t.units(e);
-    long long ctas = (long long)(steps / kSnap);
+    const Cost& cost = pl.solo ? single : pair;
+    const double steps = sep ? cost.steps_apart : cost.steps, units = sep ? cost.units_apart : cost.units;
+    if (steps >= 2147483648.0) return pl;  // steps are counted in 32 bits
+    double ctas = steps / kSnap;
     if (ctas < units) ctas = units;
     t.ctas = ctas > kAttnCtas ? kAttnCtas : ctas < 1 ? 1 : (int)ctas;
     t.any_full = 0;
@@ -375,8 +379,11 @@ inline AttnPlan make_plan(const Job& job)
             t.stretches = kAttnCtas / rb;
         }
     }
+    int longest = 0;  // steps of a unit of the pool
+    t.pool_unit[0] = t.pool_step[0] = 0;
     for (int e = 0; e < t.entries; ++e) {
         const int rest = t.units(e) - t.full(e);
+        if (rest > 0 && t.steps(e) > longest) longest = t.steps(e);
         t.pool_unit[e + 1] = t.pool_unit[e] + rest;
         t.pool_step[e + 1] = t.pool_step[e] + rest / t.lanes * t.steps(e);
     }
@@ -400,7 +407,7 @@ inline AttnPlan make_plan(const Job& job)
         pl.slots[0] = t.pool_unit[t.nseg];
         pl.slots[1] = t.units(t.nseg) + t.ctas;
     } else {
-        for (int c = 1, cut = -1; c < t.stretches && t.pool_steps > 0; ++c) {
+        for (int c = 1, cut = -1; c < t.stretches && longest > 2 * kSnap; ++c) {
             const int x = t.bound(c);
             if (x <= 0 || x >= t.pool_steps) continue;
             const int e = t.find(t.pool_step, x), n = t.steps(e), local = x - t.pool_step[e], u = local / n;

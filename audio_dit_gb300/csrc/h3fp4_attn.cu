@@ -220,9 +220,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     // Everything above overlaps the previous kernel's tail (programmatic
     // dependent launch); its outputs are read only after this.
     griddep_wait();
-    // The next kernel's blocks (those that join partials) may queue up from here on: they find
-    // room as CTAs leave, and read nothing before all have.
-    griddep_launch_dependents();
     const uint32_t tmem = *tmem_slot;
     const int tok = p.t.tok;
     // The pieces of this CTA, described by warp 2 a few ahead (a walk costs some hundred cycles of
@@ -770,6 +767,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
         }
     }
+    griddep_launch_dependents();
     tc_fence_before();
     __syncthreads();
     if (warp == 2) {
@@ -985,11 +983,8 @@ cudaError_t run(const AttnPlan& pl, const CUtensorMap (&m)[5], const AttnParams&
 
 }  // namespace
 
-size_t attn_workspace_bytes(const AttnJob& job) { return make_plan(job).bytes; }
-
-cudaError_t launch_attn(const AttnJob& job, cudaStream_t s)
+cudaError_t launch_attn(const AttnJob& job, const AttnPlan& pl, cudaStream_t s)
 {
-    const AttnPlan pl = make_plan(job);
     AttnParams p{};
     p.t = pl.t;
     p.t.own_masked = job.key_mask != nullptr;

@@ -57,10 +57,9 @@ struct AttnJob {
     uint64_t wait_limit_ns;
 };
 
-// Workspace bytes launch_attn needs for the sizes and tables of `job` (pointers unread); 0: more work than it counts.
-size_t attn_workspace_bytes(const AttnJob& job);
-
-cudaError_t launch_attn(const AttnJob& job, cudaStream_t s);
+// Launches the call as `plan` (attn_plan.h, made from `job`) cuts it.
+struct AttnPlan;
+cudaError_t launch_attn(const AttnJob& job, const AttnPlan& plan, cudaStream_t s);
 
 // The limit set with h3fp4_set_wait_limit_ns.
 uint64_t wait_limit_ns();

@@ -4,6 +4,7 @@
 #include <cmath>
 #include <cstdint>
 
+#include "attn_plan.h"
 #include "h3fp4_heads.h"
 
 namespace h3fp4 {
@@ -109,9 +110,9 @@ h3fp4_status attn(const h3fp4_heads* q, const h3fp4_heads* k, const h3fp4_heads*
         (st = check_in(kc, C)) != H3FP4_OK || (st = check_in(vc, C)) != H3FP4_OK ||
         (st = check_out(out, M, Hq, D)) != H3FP4_OK)
         return st;
-    const size_t need = attn_workspace_bytes(job);
-    if (need == 0) return H3FP4_ERR_SHAPE;
-    if (!ws || ws_bytes < need) return H3FP4_ERR_INVALID;
+    const AttnPlan plan = make_plan(job);
+    if (plan.bytes == 0) return H3FP4_ERR_SHAPE;
+    if (!ws || ws_bytes < plan.bytes) return H3FP4_ERR_INVALID;
     if (!aligned16(ws) || (reinterpret_cast<uintptr_t>(lse) & 3u)) return H3FP4_ERR_ALIGN;
     if (M > 0 && (out->ptr == q->ptr || (T > 0 && (out->ptr == k->ptr || out->ptr == v->ptr)) ||
                   (C > 0 && (out->ptr == kc->ptr || out->ptr == vc->ptr))))
@@ -132,7 +133,7 @@ h3fp4_status attn(const h3fp4_heads* q, const h3fp4_heads* k, const h3fp4_heads*
     job.scale = scale;
     job.ws = static_cast<uint8_t*>(ws);
     job.wait_limit_ns = wait_limit_ns();
-    return launch_attn(job, stream) == cudaSuccess ? H3FP4_OK : H3FP4_ERR_CUDA;
+    return launch_attn(job, plan, stream) == cudaSuccess ? H3FP4_OK : H3FP4_ERR_CUDA;
 }
 
 }  // namespace
@@ -211,7 +212,7 @@ size_t h3fp4_attn_workspace_bytes(int64_t M, int64_t T, int64_t C, int Hq, int H
     AttnJob job{};
     int64_t one_q[2], one_kv[2];
     if (attn_sizes(M, T, C, Hq, Hkv, D, q_off, kv_off, nseg, one_q, one_kv, &job) != H3FP4_OK) return 0;
-    return attn_workspace_bytes(job);
+    return make_plan(job).bytes;
 }
 
 }  // extern "C"
