@@ -13,6 +13,10 @@
 // and c + rot/16, so both halves of its eight pairs are in its own registers
 // and the rotation exchanges nothing; the chunks past rot, and all chunks when
 // adjacent elements form the pairs, are dealt out two by two.
+//
+// A warp takes kUnroll heads per group of one tensor (a part of the row's heads)
+// for every so many rows: its weights stay in registers, and all of a row's loads
+// are issued before the first is used, which is what memory latency asks for.
 #include <cstdint>
 
 #include <cuda_bf16.h>
@@ -26,8 +30,12 @@ namespace {
 
 constexpr int kThreads = 128;
 
+constexpr int kUnroll = 3;  // heads of a group in flight: 24 heads of 128 are two parts
+constexpr int kBlocksPerSm = 5;
+
 struct NormRopeParams {
     NormTensor t[2];
+    int parts[2];       // of a row's heads, per tensor
     long long M;
     int D, rot, half;
     float inv_d, eps;
@@ -62,70 +70,67 @@ __device__ __forceinline__ uint4 pack8(const float (&f)[8])
 
 // kLanes lanes per head (a power of two, at least half the head's chunks).
 template <int kLanes, bool kPairs>
-__global__ void __launch_bounds__(kThreads) norm_rope_kernel(const NormRopeParams p)
+__global__ void __launch_bounds__(kThreads, kBlocksPerSm) norm_rope_kernel(const __grid_constant__ NormRopeParams p)
 {
-    griddep_wait();
     constexpr int kGroups = 32 / kLanes;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int lane = threadIdx.x & 31;
     const int c = lane & (kLanes - 1), g = lane / kLanes;
-    const long long r = (long long)blockIdx.x * (kThreads / 32) + warp;
-    if (r >= p.M) return;
+    // this warp's tensor, part of its heads, first row and step
+    const int all_parts = p.parts[0] + p.parts[1];
+    const int warp = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5), warps = gridDim.x * (kThreads / 32);
+    const int part = warp % all_parts;
+    const bool second = part >= p.parts[0];
+    const NormTensor& t = p.t[second ? 1 : 0];
+    const int h0 = (second ? part - p.parts[0] : part) * (kGroups * kUnroll) + g;
+    const int step = warps / all_parts;  // the grid is a multiple of the parts
     const int n = p.D >> 3, hc = p.rot >> 4;
-    int ca, cb;  // this lane's chunks
-    if (kPairs) {
-        ca = 2 * c;
-        cb = 2 * c + 1;
-    } else if (c < hc) {
+    int ca = 2 * c, cb = 2 * c + 1;  // this lane's chunks
+    if (!kPairs && c < hc) {
         ca = c;
         cb = c + hc;
-    } else {
-        ca = 2 * c;
-        cb = 2 * c + 1;
     }
     const bool has_a = ca < n, has_b = cb < n;
-    const int s = segment_of(p.seg, r);
-
-    // The angles of this lane's pairs: eight for the split halves (shared by
-    // both chunks), four per chunk for adjacent pairs.
-    float co[8], si[8];
-    bool turn_a = false, turn_b = false;
-    if (p.rot > 0) {
-        const float* cr = p.cos + r * p.half;
-        const float* sr = p.sin + r * p.half;
-        if (kPairs) {
-            turn_a = 8 * ca < p.rot;  // rot is a multiple of 16: both chunks of a lane or none
-            turn_b = turn_a;
-            if (turn_a) {
-                load8(cr + 4 * ca, co);
-                load8(sr + 4 * ca, si);
-            }
-        } else if (c < hc) {
-            turn_a = turn_b = true;
-            load8(cr + 8 * c, co);
-            load8(sr + 8 * c, si);
-        }
-    }
-#pragma unroll 1
-    for (int ti = 0; ti < 2; ++ti) {
-        const NormTensor& t = p.t[ti];
-        float wa[8], wb[8];
+    // Pairs of adjacent elements: rot is a multiple of 16, both chunks of a lane turn or none.
+    const bool turn = kPairs ? 8 * ca < p.rot : c < hc;
+    const int angle = kPairs ? 4 * ca : 8 * c;
+    const __nv_bfloat16* xa = t.x + 8 * ca;
+    const __nv_bfloat16* xb = t.x + 8 * cb;
+    __nv_bfloat16* ya = t.y + 8 * ca;
+    __nv_bfloat16* yb = t.y + 8 * cb;
+    griddep_wait();
+    float wa[8], wb[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) wa[i] = wb[i] = 1.0f;
-        if (t.weight) {
-            if (has_a) load8(t.weight + (long long)s * p.D + 8 * ca, wa);
-            if (has_b) load8(t.weight + (long long)s * p.D + 8 * cb, wb);
+    for (int i = 0; i < 8; ++i) wa[i] = wb[i] = 1.0f;
+    long long seg_end = 0;  // the weights are those of the rows before it
+    for (long long r = warp / all_parts; r < p.M; r += step) {
+        uint4 va[kUnroll], vb[kUnroll];
+#pragma unroll
+        for (int k = 0; k < kUnroll; ++k) {
+            const int h = h0 + k * kGroups;
+            const long long at = r * t.x_row + (long long)h * t.x_head;
+            va[k] = vb[k] = make_uint4(0, 0, 0, 0);
+            if (h < t.heads && has_a) va[k] = *reinterpret_cast<const uint4*>(xa + at);
+            if (h < t.heads && has_b) vb[k] = *reinterpret_cast<const uint4*>(xb + at);
         }
-#pragma unroll 1
-        for (int h0 = 0; h0 < t.heads; h0 += kGroups) {
-            const int h = h0 + g;
-            const bool on = h < t.heads;
-            uint4 va = make_uint4(0, 0, 0, 0), vb = va;
-            const __nv_bfloat16* x = t.x + r * t.x_row + (long long)h * t.x_head;
-            if (on && has_a) va = *reinterpret_cast<const uint4*>(x + 8 * ca);
-            if (on && has_b) vb = *reinterpret_cast<const uint4*>(x + 8 * cb);
+        // The angles of this lane's pairs: eight that both chunks share, or four per chunk.
+        float co[8], si[8];
+        if (turn) {
+            load8(p.cos + r * p.half + angle, co);
+            load8(p.sin + r * p.half + angle, si);
+        }
+        if (r >= seg_end) {
+            const int s = segment_of(p.seg, r);
+            seg_end = p.seg.off[s + 1];
+            if (t.weight) {
+                if (has_a) load8(t.weight + (long long)s * p.D + 8 * ca, wa);
+                if (has_b) load8(t.weight + (long long)s * p.D + 8 * cb, wb);
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < kUnroll; ++k) {
             float a[8], b[8];
-            unpack8(va, a);
-            unpack8(vb, b);
+            unpack8(va[k], a);
+            unpack8(vb[k], b);
             float sum = 0.0f;
 #pragma unroll
             for (int i = 0; i < 8; ++i) sum = fmaf(a[i], a[i], fmaf(b[i], b[i], sum));
@@ -137,7 +142,7 @@ __global__ void __launch_bounds__(kThreads) norm_rope_kernel(const NormRopeParam
                 a[i] *= rs * wa[i];
                 b[i] *= rs * wb[i];
             }
-            if (turn_a) {
+            if (turn) {
                 if (kPairs) {
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
@@ -156,22 +161,34 @@ __global__ void __launch_bounds__(kThreads) norm_rope_kernel(const NormRopeParam
                     }
                 }
             }
-            __nv_bfloat16* y = t.y + r * t.y_row + (long long)h * t.y_head;
-            if (on && has_a) *reinterpret_cast<uint4*>(y + 8 * ca) = pack8(a);
-            if (on && has_b) *reinterpret_cast<uint4*>(y + 8 * cb) = pack8(b);
+            const int h = h0 + k * kGroups;
+            const long long at = r * t.y_row + (long long)h * t.y_head;
+            if (h < t.heads && has_a) *reinterpret_cast<uint4*>(ya + at) = pack8(a);
+            if (h < t.heads && has_b) *reinterpret_cast<uint4*>(yb + at) = pack8(b);
         }
     }
 }
 
 template <int kLanes>
-cudaError_t launch_lanes(const NormRopeParams& p, bool pairs, cudaStream_t s)
+cudaError_t launch_lanes(NormRopeParams& p, bool pairs, cudaStream_t s)
 {
-    const unsigned blocks = (unsigned)((p.M + kThreads / 32 - 1) / (kThreads / 32));
+    constexpr int kHeads = 32 / kLanes * kUnroll, kWarps = kThreads / 32;
+    for (int i = 0; i < 2; ++i) p.parts[i] = (p.t[i].heads + kHeads - 1) / kHeads;
+    // Warps for as many rows as are resident at once, which then take the next rows; up to
+    // four times as many where a warp has few rows, so that blocks in waiting even out the
+    // end (4099 rows of 25 heads of 80: 17 against 21 us; 31744 rows of 48 heads of 128:
+    // 128 against 126 us).  Either way a whole number of rows' warps.
+    const long long parts = p.parts[0] + p.parts[1], most = (long long)sm_count_current_device() * kBlocksPerSm * kWarps;
+    long long rows = most / parts;
+    if (p.M <= 16 * rows) rows *= 4;
+    rows = rows < 1 ? 1 : rows < p.M ? rows : p.M;
+    long long blocks = (rows * parts + kWarps - 1) / kWarps;
+    while (blocks * kWarps % parts) ++blocks;
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.gridDim = dim3(blocks);
+    cfg.gridDim = dim3((unsigned)blocks);
     cfg.blockDim = dim3(kThreads);
     cfg.stream = s;
     cfg.attrs = attr;
