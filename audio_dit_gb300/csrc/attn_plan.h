@@ -149,8 +149,10 @@ struct Walk {
     int tile, left;            // pool: first tile of the next piece, steps left of the stretch
     bool waves;
 
-    __host__ __device__ Walk(const AttnTable& table, int c) : t(table), cta(c)
+    __host__ __device__ explicit Walk(const AttnTable& table) : t(table) {}
+    __host__ __device__ void start(int c)
     {
+        cta = c;
         left = 0;
         tile = 0;
         step_hb = step_rb = wave_end = 0;

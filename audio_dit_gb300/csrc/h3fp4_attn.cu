@@ -210,9 +210,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             prefetch_tensormap(&tmVc);
         }
     }
+    Walk walk(p.t);  // warp 2's
     if (warp == 2) {
         tmem_alloc(tmem_slot, kTmemCols);
         tmem_relinquish();
+        walk.start(blockIdx.x);
     }
     tc_fence_before();
     __syncthreads();
@@ -448,9 +450,23 @@ __global__ void __launch_bounds__(kThreads, 1)
             (void)mbar_wait(&done[X], 0, p.wait_ns, p.status, kStatusTimeoutAttnMma);
         } else if (warp == 2) {
             // ------------------------------------------------------------ keys that are left out
-            Walk walk(p.t, blockIdx.x);
             uint32_t described = 0;
             bool ok = true, left = true;
+            int ctx_keep = -1, own_keep = 0, own_entry = -1;
+            // Key tiles up to the last key that a mask of n bytes keeps.
+            auto kept_tiles = [&](const uint8_t* mask, int n) {
+                int tile = (n + kKeyTile - 1) / kKeyTile;
+                for (bool some = false; tile > 0 && !some; tile -= some ? 0 : 1) {
+                    bool on = false;
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const int k = (tile - 1) * kKeyTile + 32 * j + lane;
+                        on |= k < n && mask[k] != 0;
+                    }
+                    some = __any_sync(0xffffffffu, on);
+                }
+                return tile;
+            };
             auto describe = [&]() {  // the next piece, or that there is none
                 if (!left) return;
                 const uint32_t slot = described % kPieceSlots;
@@ -458,6 +474,21 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 kStatusTimeoutAttnMask);
                 Piece n;
                 left = __all_sync(0xffffffffu, ok) && walk.next(n);
+                if (left && (p.ctx_mask != nullptr || p.key_mask != nullptr)) {
+                    // Tiles behind the last key that a mask keeps are left out (padded prompts).
+                    if (p.ctx_mask != nullptr && ctx_keep < 0) ctx_keep = kept_tiles(p.ctx_mask, p.C);
+                    if (p.key_mask != nullptr && n.e < p.t.nseg && n.e != own_entry) {
+                        own_entry = n.e;
+                        own_keep = kept_tiles(p.key_mask + n.kv0, n.kv_len);
+                    }
+                    const int all = n.ctx_tiles, ctx = p.ctx_mask != nullptr ? min(all, ctx_keep) : all;
+                    const int own = p.key_mask != nullptr && n.e < p.t.nseg ? own_keep : n.own_tiles;
+                    auto moved = [&](int t) { return t <= ctx ? t : max(ctx, t - (all - ctx)); };
+                    const int end = moved(min(n.t0 + n.nt, all + own));
+                    n.t0 = moved(n.t0);
+                    n.nt = max(0, end - n.t0);
+                    n.ctx_tiles = ctx;
+                }
                 if (lane == 0) {
                     int4* rec = reinterpret_cast<int4*>(smem + L::kPieceOff + slot * 48);
                     rec[0] = make_int4(n.t0, left ? n.nt : -1, n.ntok, n.tok0);

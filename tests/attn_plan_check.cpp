@@ -32,7 +32,8 @@ static const char* check(const Job& job)
     std::map<std::vector<int>, std::set<int>> slots[2];  // unit -> slots written
     std::set<int> used[2];
     for (int c = 0; c < t.ctas; ++c) {
-        Walk w(t, c);
+        Walk w(t);
+        w.start(c);
         Piece p;
         while (w.next(p)) {
             const int n = p.ctx_tiles + p.own_tiles;

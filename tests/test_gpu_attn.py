@@ -339,3 +339,24 @@ def test_many_units_without_keys_between_masked_ones():
     c = Case(122, 4, 2, 64, list(range(0, 201)), [i // 7 * 150 for i in range(201)], ctx=0)
     c.key_mask = torch.from_numpy(c.rng.random(c.T) < 0.7)
     c.check()
+
+
+def test_padding_behind_the_last_kept_key():
+    """Whole tiles of padding, in the context and behind each segment's keys, beside segments without a kept key."""
+    c = Case(131, 4, 2, 64, [0, 100, 101, 400, 900, 901], [0, 700, 900, 900, 1500, 2200], ctx=1000)
+    keep = np.zeros(2200, bool)
+    for a, n in ((0, 130), (700, 0), (900, 1), (1500, 513)):
+        keep[a:a + n] = True
+    keep[640:642] = False
+    c.key_mask = torch.from_numpy(keep)
+    c.check()
+    for n in (0, 1, 128, 300, 1000):
+        c.ctx_mask = torch.from_numpy(np.arange(1000) < n)
+        c.check()
+    c.key_mask = None
+    c.check()
+    # a long axis that is cut, kept at its beginning, in the middle and at its end
+    d = Case(132, 8, 2, 128, [0, 3], [0, 9000])
+    for a, b in ((0, 100), (4000, 4500), (8990, 9000)):
+        d.key_mask = torch.from_numpy((np.arange(9000) >= a) & (np.arange(9000) < b))
+        d.check()
