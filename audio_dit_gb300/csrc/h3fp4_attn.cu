@@ -266,24 +266,26 @@ __global__ void __launch_bounds__(kThreads, 1)
             bool ok = p.stall == 0;
             while (ok && next_with_keys(u, ok, kStatusTimeoutAttnLoad)) {
                 const int tiles = !kSolo && u.ntok > tok ? 2 : 1;
-                for (int X = 0; X < tiles; ++X, ++q_place) {
-                    const uint32_t st = q_place % L::kQ;
-                    ok = mbar_wait(&q_empty[st], ((q_place / L::kQ) & 1u) ^ 1u, p.wait_ns, p.status,
-                                   kStatusTimeoutAttnLoad);
-                    if (!__all_sync(0xffffffffu, ok)) {
-                        ok = false;
-                        break;
-                    }
-                    if (elect_one()) {
-                        mbar_arrive_expect_tx(q_bar(q_place), p.q_bytes);
-                        for (int c = 0; c < kChunks; ++c)
-                            tma_load_3d(smem + st * L::kTile + c * 16384, &tmQ, q_bar(q_place), 64 * c, u.head0,
-                                        u.tok0 + X * tok);
-                    }
-                }
-                if (!ok) break;
                 const int hk = u.head0 / p.group;
+                // Q_A, K_0, Q_B, then the rest: Q_B's place is this unit's predecessor's Q_A, which is
+                // given back last, and nothing else shall wait for it.
                 for (int i = 0; i < 2 * u.nt; ++i, ++place) {
+                    for (int X = i; X < tiles && i < 2; X += 2, ++q_place) {
+                        const uint32_t st = q_place % L::kQ;
+                        ok = mbar_wait(&q_empty[st], ((q_place / L::kQ) & 1u) ^ 1u, p.wait_ns, p.status,
+                                       kStatusTimeoutAttnLoad);
+                        if (!__all_sync(0xffffffffu, ok)) {
+                            ok = false;
+                            break;
+                        }
+                        if (elect_one()) {
+                            mbar_arrive_expect_tx(q_bar(q_place), p.q_bytes);
+                            for (int c = 0; c < kChunks; ++c)
+                                tma_load_3d(smem + st * L::kTile + c * 16384, &tmQ, q_bar(q_place), 64 * c, u.head0,
+                                            u.tok0 + X * tok);
+                        }
+                    }
+                    if (!ok) break;
                     // which tile the ring's next place takes
                     bool is_v;
                     int t;
@@ -722,7 +724,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     sum = a.y * f0 + b.y * f1;
                 }
                 // Where a part has no key (or only scores of -inf), its sums may be anything.
-                const bool clear = __any_sync(0xffffffffu, a.y == 0.0f || (kSolo && nB > 0 && b.y == 0.0f));
+                const bool clear = __any_sync(0xffffffffu, on && (a.y == 0.0f || (kSolo && nB > 0 && b.y == 0.0f)));
                 const uint32_t tA = tmem + kTmO + DP * X + lanes, tB = tmem + kTmO + DP + lanes;
                 // the sums of columns 32 c...; solo: of both parts, weighted
                 auto load = [&](int c, uint32_t (&v)[32]) {
@@ -769,7 +771,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                     mbar_arrive_if(lane == 0 && nA > 0, &o_empty[X]);
                     if (kSolo) mbar_arrive_if(lane == 0 && nB > 0, &o_empty[1]);
                 };
-                if (!kSolo && u.whole && p.wide_out && nA > 0 && !clear) {
+                if (32 * quarter >= min(tok, u.ntok - Y * tok) * p.t.pack) {
+                    release();  // none of this warp's rows is a query
+                } else if (!kSolo && u.whole && p.wide_out && nA > 0 && !clear) {
                     // The usual case of the pair plan, whose next unit waits for these sums to be read.
 #pragma unroll 1
                     for (int c = 0; c < DP / 32; ++c) {
