@@ -34,6 +34,9 @@ namespace h3fp4 {
 constexpr int kKeyTile = 128;
 constexpr int kAttnCtas = 152;   // one per SM of the GB300
 constexpr int kSnap = 4;
+constexpr int kUnitSteps = 1;    // what a unit costs beside its tiles, in steps
+constexpr int kEmptySteps = 2;   // what a unit without keys costs
+static_assert(kUnitSteps < kSnap && kEmptySteps <= 2 * kSnap, "cuts lie behind a unit's overhead");
 constexpr int kAttnEntries = H3FP4_ATTN_MAX_SEGMENTS + 1;
 
 __host__ __device__ inline int lesser(int a, int b) { return a < b ? a : b; }
@@ -66,12 +69,10 @@ struct AttnTable {
         return e < nseg ? (kv_off[e + 1] - kv_off[e] + kKeyTile - 1) / kKeyTile : 0;
     }
     __host__ __device__ int tiles(int e) const { return tiles_ctx(e) + tiles_own(e); }
-    // A unit without keys still takes a step (it writes zeros).
-    __host__ __device__ int steps(int e) const
-    {
-        const int n = tiles(e);
-        return n > 0 ? n : 1;
-    }
+    // Steps of a unit: its tiles, and what beginning and ending it costs; a unit
+    // without keys still writes zeros.
+    __host__ __device__ static int steps_of(int tiles) { return tiles > 0 ? tiles + kUnitSteps : kEmptySteps; }
+    __host__ __device__ int steps(int e) const { return steps_of(tiles(e)); }
     __host__ __device__ int row_blocks(int e) const { return (q_end(e) - q_begin(e) + unit_tok - 1) / unit_tok; }
     __host__ __device__ int units(int e) const { return head_blocks * row_blocks(e); }
     __host__ __device__ int full(int e) const { return any_full ? units(e) / ctas * ctas : 0; }
@@ -233,10 +234,11 @@ struct Walk {
         }
         if (left <= 0) return false;
         fill(p);
-        const int tiles = p.ctx_tiles + p.own_tiles, n = tiles > 0 ? tiles : 1;
+        const int tiles = p.ctx_tiles + p.own_tiles, n = AttnTable::steps_of(tiles);
         const int take = lesser(n - tile, left);
-        p.t0 = tile;
-        p.nt = lesser(tile + take, tiles) - tile;
+        // a unit's first steps are its overhead; cuts lie behind them
+        p.t0 = tile > kUnitSteps ? tile - kUnitSteps : 0;
+        p.nt = tiles > 0 ? tile + take - kUnitSteps - p.t0 : 0;
         p.whole = take == n && !t.separate;
         // With the separate plan every piece leaves partials: one for a segment's unit, those of the
         // context's numbered along the pool.
@@ -361,7 +363,7 @@ inline AttnPlan make_plan(const Job& job)
     // CTAs: one per SM where there is work for all of them.
     const Cost& cost = pl.solo ? single : pair;
     const double steps = sep ? cost.steps_apart : cost.steps, units = sep ? cost.units_apart : cost.units;
-    if (steps >= 2147483648.0) return pl;  // steps are counted in 32 bits
+    if (steps + 2 * kEmptySteps * units >= 2147483648.0) return pl;  // steps are counted in 32 bits
     double ctas = steps / kSnap;
     if (ctas < units) ctas = units;
     t.ctas = ctas > kAttnCtas ? kAttnCtas : ctas < 1 ? 1 : (int)ctas;
