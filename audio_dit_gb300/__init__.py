@@ -24,7 +24,7 @@ __all__ = [
     "h3fp4_workspace_bytes", "h3fp4_quantize_weight", "h3fp4_quantize_act", "h3fp4_linear",
     "h3fp4_check", "h3fp4_act_amax", "h3fp4_gscale_from_amax", "h3fp4_selftest_timeout", "h3fp4_measure_fp4_peak", "h3fp4_measure_fp4_pair_peak", "h3fp4_measure_fp4_form", "MMA_FORMS", "h3fp4_quantize_act_noalloc",
     "h3fp4_linear_swiglu_nvfp4", "h3fp4_qk_norm_rope", "h3fp4_cross_attn", "h3fp4_shared_attn",
-    "h3fp4_attn_workspace_bytes", "alloc_attn_workspace", "ROPE_PAIRS", "ATTN_MAX_SEGMENTS",
+    "h3fp4_attn_workspace_bytes", "alloc_attn_workspace", "h3fp4_selftest_attn_timeout", "ROPE_PAIRS", "ATTN_MAX_SEGMENTS",
     "h3fp4_set_wait_limit_ns", "h3fp4_status_string", "alloc_nvfp4", "alloc_workspace",
 ]
 
@@ -95,6 +95,7 @@ def load_library():
         "h3fp4_shared_attn": (i32, [hp, hp, hp, hp, hp, i64, i64, i64, i32, i32, i32, vp, vp, i32, vp, vp, C.c_float,
                                     hp, vp, vp, sz, vp]),
         "h3fp4_attn_workspace_bytes": (sz, [i64, i64, i64, i32, i32, i32, vp, vp, i32]),
+        "h3fp4_selftest_attn_timeout": (i32, [vp, C.c_uint64, vp]),
         "h3fp4_check": (i32, [vp, vp]),
         "h3fp4_set_wait_limit_ns": (None, [C.c_uint64]),
         "h3fp4_status_string": (C.c_char_p, [i32]),
@@ -363,6 +364,13 @@ def h3fp4_selftest_pack_timeout(x: torch.Tensor, a_gscale: torch.Tensor, ws: tor
                                                       _ptr(a_gscale, "a_gscale", torch.float32),
                                                       _ptr(ws, "ws", torch.uint8), int(limit_ns), _stream(stream)),
            "h3fp4_selftest_pack_timeout")
+
+
+def h3fp4_selftest_attn_timeout(ws: torch.Tensor, limit_ns: int, stream=None) -> None:
+    if ws.numel() < 2048:
+        raise ValueError("ws must have 2048 bytes")
+    _check(load_library().h3fp4_selftest_attn_timeout(_ptr(ws, "ws", torch.uint8), int(limit_ns), _stream(stream)),
+           "h3fp4_selftest_attn_timeout")
 
 
 def h3fp4_measure_fp4_peak(ws: torch.Tensor, iters: int = 20000) -> float:

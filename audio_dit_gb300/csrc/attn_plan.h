@@ -51,7 +51,7 @@ struct AttnTable {
     int separate;
     int any_full;          // some entry has whole waves
     int ctx_masked, own_masked, ctx_ragged;  // masks are given; the context's length is no multiple of a tile
-    int pool_steps, pool_units;
+    int pool_steps;
     int lanes, stretches;  // CTAs side by side on a stretch of the pool, and stretches
     int share, longer;     // steps of a stretch: share + 1 for the first `longer` of them
     int M;
@@ -391,7 +391,6 @@ inline AttnPlan make_plan(const Job& job)
         t.pool_unit[e + 1] = t.pool_unit[e] + rest;
         t.pool_step[e + 1] = t.pool_step[e] + rest / t.lanes * t.steps(e);
     }
-    t.pool_units = t.pool_unit[t.entries];
     t.pool_steps = t.pool_step[t.entries];
     t.share = t.pool_steps / t.stretches;
     t.longer = t.pool_steps % t.stretches;

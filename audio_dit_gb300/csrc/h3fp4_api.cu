@@ -137,7 +137,7 @@ const char* h3fp4_status_string(h3fp4_status s)
     switch (s) {
     case H3FP4_OK: return "ok";
     case H3FP4_ERR_INVALID: return "invalid argument";
-    case H3FP4_ERR_SHAPE: return "unsupported shape (K % 64, N % 8, rows >= 1, segments)";
+    case H3FP4_ERR_SHAPE: return "unsupported shape (K % 64, N % 8, rows >= 1, segments, heads)";
     case H3FP4_ERR_ALIGN: return "pointer not 16-byte aligned";
     case H3FP4_ERR_CUDA: return "CUDA error";
     case H3FP4_ERR_TIMEOUT: return "device wait timed out";

@@ -206,6 +206,29 @@ h3fp4_status h3fp4_shared_attn(const h3fp4_heads* q, const h3fp4_heads* k, const
                 ws, ws_bytes, stream);
 }
 
+h3fp4_status h3fp4_selftest_attn_timeout(void* ws, uint64_t limit_ns, cudaStream_t stream)
+{
+    if (!ws) return H3FP4_ERR_INVALID;
+    if (!aligned16(ws)) return H3FP4_ERR_ALIGN;
+    const h3fp4_status st = check_device();
+    if (st != H3FP4_OK) return st;
+    // One query and one key of one head of 64, in the workspace behind the status word.
+    int64_t one_q[2], one_kv[2];
+    AttnJob job{};
+    if (attn_sizes(1, 1, 0, 1, 1, 64, nullptr, nullptr, 1, one_q, one_kv, &job) != H3FP4_OK) return H3FP4_ERR_INVALID;
+    __nv_bfloat16* data = reinterpret_cast<__nv_bfloat16*>(static_cast<uint8_t*>(ws) + 256);
+    job.q = HeadsIn{data, 64, 64};
+    job.k = HeadsIn{data + 128, 64, 64};
+    job.v = HeadsIn{data + 256, 64, 64};
+    job.out = data + 384;
+    job.out_row = job.out_head = 64;
+    job.scale = 1.0f;
+    job.ws = static_cast<uint8_t*>(ws);
+    job.stall = 1;
+    job.wait_limit_ns = limit_ns ? limit_ns : 1;
+    return launch_attn(job, make_plan(job), stream) == cudaSuccess ? H3FP4_OK : H3FP4_ERR_CUDA;
+}
+
 size_t h3fp4_attn_workspace_bytes(int64_t M, int64_t T, int64_t C, int Hq, int Hkv, int D, const int64_t* q_off,
                                   const int64_t* kv_off, int nseg)
 {

@@ -48,7 +48,8 @@
  *   - All calls are asynchronous on `stream`; the return value reports host
  *     validation and launch errors only.  Device-side wait timeouts are
  *     recorded in the workspace status word; read them with h3fp4_check().
- *   - Shapes: K % 64 == 0, N % 8 == 0, rows >= 1; 16-byte aligned pointers
+ *   - Shapes: K % 64 == 0, N % 8 == 0, rows >= 1 (the norm and attention calls
+ *     state their own); 16-byte aligned pointers
  *     (codes, sf, bf16 tensors, workspace); violations return
  *     H3FP4_ERR_SHAPE / H3FP4_ERR_ALIGN and launch nothing.
  *   - Only sm_103 devices are accepted (H3FP4_ERR_UNSUPPORTED_DEVICE
@@ -60,6 +61,10 @@
  *   - The GEMM runs as clusters of two CTAs (512 threads, ~228 KB of shared
  *     memory and all 512 TMEM columns each), one CTA per SM, over every SM
  *     pair that can be co-resident.
+ *   - The attention calls run one CTA per SM (512 threads, ~227 KB of shared
+ *     memory, all 512 TMEM columns) and a small second kernel where a row's
+ *     keys were divided over CTAs.  Results do not depend on timing: the same
+ *     call gives the same bits.
  *   - Calls issue only kernel launches and (with H3FP4_EPI_AMAX) one memset
  *     on `stream`, so a fixed sequence of calls can be captured into a CUDA
  *     graph.  Make one eager call per device before the first capture: it
@@ -86,7 +91,7 @@ extern "C" {
 typedef enum {
     H3FP4_OK = 0,
     H3FP4_ERR_INVALID = 1,            /* null pointer, bad flag combination, bad segments */
-    H3FP4_ERR_SHAPE = 2,              /* K % 64, N % 8, rows < 1, too many segments       */
+    H3FP4_ERR_SHAPE = 2,              /* K % 64, N % 8, rows < 1, too many segments, heads */
     H3FP4_ERR_ALIGN = 3,              /* a pointer is not 16-byte aligned                 */
     H3FP4_ERR_CUDA = 4,               /* a CUDA runtime/driver call failed                */
     H3FP4_ERR_TIMEOUT = 5,            /* a bounded device wait ran out (h3fp4_check)      */
@@ -300,6 +305,12 @@ H3FP4_API h3fp4_status h3fp4_selftest_timeout(void* ws, uint64_t limit_ns, cudaS
  * 0) bytes; h3fp4_check(ws) must afterwards report H3FP4_ERR_TIMEOUT. */
 H3FP4_API h3fp4_status h3fp4_selftest_pack_timeout(const void* x_bf16, const float* a_gscale, void* ws,
                                                    uint64_t limit_ns, cudaStream_t stream);
+
+/* The same for the attention kernel: one query and one key with every load left
+ * out, so that its waits run out after limit_ns and it returns.  ws: 2048
+ * bytes (written from byte 256 on); h3fp4_check(ws) must afterwards report
+ * H3FP4_ERR_TIMEOUT. */
+H3FP4_API h3fp4_status h3fp4_selftest_attn_timeout(void* ws, uint64_t limit_ns, cudaStream_t stream);
 
 /* Measured tensor-core ceiling for the GEMM's instruction on the current
  * device: back-to-back tcgen05.mma.kind::mxf4nvf4.block_scale (M=128, N=256,

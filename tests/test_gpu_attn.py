@@ -360,3 +360,29 @@ def test_padding_behind_the_last_kept_key():
     for a, b in ((0, 100), (4000, 4500), (8990, 9000)):
         d.key_mask = torch.from_numpy((np.arange(9000) >= a) & (np.arange(9000) < b))
         d.check()
+
+
+def test_timeout_is_reported_and_the_next_call_is_right():
+    import time
+
+    import audio_dit_gb300 as A
+    ws = torch.zeros(2048, dtype=torch.uint8, device="cuda")
+    torch.cuda.synchronize()
+    t = time.perf_counter()
+    A.h3fp4_selftest_attn_timeout(ws, 2_000_000)                    # 2 ms, and no load is issued
+    with pytest.raises(A.H3FP4Error) as e:
+        A.h3fp4_check(ws)
+    assert e.value.status == 5 and time.perf_counter() - t < 1.0
+    A.h3fp4_check(ws)                                               # cleared
+    Case(141, 2, 2, 128, [0, 300], [0, 300]).check()
+
+
+def test_whole_waves_and_what_is_left_over():
+    """More units of a segment than SMs: dealt out whole, the rest cut."""
+    Case(151, 2, 2, 64, [0, 40001], [0, 40]).check()
+    Case(152, 2, 1, 64, [0, 20001, 21000], [0, 1300, 1500], ctx=200).check()
+
+
+def test_units_of_a_head_side_by_side():
+    """Keys of more than half the L2 and few rows."""
+    Case(161, 2, 2, 128, [0, 601], [0, 70000]).check()

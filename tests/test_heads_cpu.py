@@ -81,6 +81,11 @@ def test_attention_refusals(lib):
         assert attn(lib, **kw) == ALIGN, kw
 
 
+def test_selftest_refusals(lib):
+    assert lib.h3fp4_selftest_attn_timeout(None, 1, None) == INVALID
+    assert lib.h3fp4_selftest_attn_timeout(C.c_void_p(4104), 1, None) == ALIGN
+
+
 def test_workspace_bytes(lib):
     import audio_dit_gb300 as A
     assert A.h3fp4_attn_workspace_bytes(0, 0, 2, 2, 64) >= 256
