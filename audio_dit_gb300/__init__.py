@@ -124,12 +124,25 @@ def _ptr(t: Optional[torch.Tensor], what: str, dtype=None):
     return t.data_ptr()
 
 
-_BF16 = torch.bfloat16
+_BF16, _F32 = torch.bfloat16, torch.float32
 
 
 def _heads(t: torch.Tensor, what: str, rows: int, heads: int, d: int):
     """(address, row stride, head stride) of a bf16 [rows, heads, d] view: any row
     and head strides, the elements of a head contiguous."""
+    if (not isinstance(t, torch.Tensor) or t.dtype is not _BF16 or t.shape != (rows, heads, d) or not t.is_cuda
+            or (d > 1 and t.stride(2) != 1)):
+        _refuse_heads(t, what, rows, heads, d)
+    row, head, _ = t.stride()
+    # the stride of a dimension of one element says nothing about the memory
+    if heads <= 1:
+        head = d
+    if rows <= 1:
+        row = heads * head
+    return t.data_ptr(), row, head
+
+
+def _refuse_heads(t, what: str, rows: int, heads: int, d: int):
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{what} must be a torch.Tensor")
     if not t.is_cuda:
@@ -138,15 +151,7 @@ def _heads(t: torch.Tensor, what: str, rows: int, heads: int, d: int):
         raise TypeError(f"{what} must be {_BF16}, got {t.dtype}")
     if t.shape != (rows, heads, d):
         raise ValueError(f"{what} must be {[rows, heads, d]}, got {list(t.shape)}")
-    row, head, one = t.stride()
-    if d > 1 and one != 1:
-        raise ValueError(f"{what}: the last dimension must be contiguous")
-    # the stride of a dimension of one element says nothing about the memory
-    if heads <= 1:
-        head = d
-    if rows <= 1:
-        row = heads * head
-    return t.data_ptr(), row, head
+    raise ValueError(f"{what}: the last dimension must be contiguous")
 
 
 def _table(seq: Optional[Sequence[int]]):
@@ -169,10 +174,12 @@ def _mask(t: Optional[torch.Tensor], what: str, n: int):
 
 
 def _f32(t: Optional[torch.Tensor], what: str, shape):
-    p = _ptr(t, what, torch.float32)
-    if t is not None and tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{what} must be {list(shape)}, got {list(t.shape)}")
-    return p
+    if t is None:
+        return None
+    if isinstance(t, torch.Tensor) and t.dtype is _F32 and t.shape == shape and t.is_cuda and t.is_contiguous():
+        return t.data_ptr()
+    _ptr(t, what, _F32)
+    raise ValueError(f"{what} must be {list(shape)}, got {list(t.shape)}")
 
 
 def _seg_pair(q_off, kv_off):
@@ -185,10 +192,13 @@ def _seg_pair(q_off, kv_off):
     return q, k, nseg, (keep_q, keep_k)
 
 
+_raw_stream, _device = (getattr(torch._C, n, None) for n in ("_cuda_getCurrentRawStream", "_cuda_getDevice"))
+
+
 def _stream(stream) -> Optional[int]:
     if stream is None:
         # the raw handle: torch.cuda.current_stream() builds a Stream object, 3 us per call
-        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+        return _raw_stream(_device()) if _raw_stream else torch.cuda.current_stream().cuda_stream
     return stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
 
 
@@ -202,6 +212,12 @@ def _segs(seg_off: Optional[Sequence[int]]):
 def _check(status: int, what: str):
     if status != 0:
         raise H3FP4Error(status, what)
+
+
+def _workspace(ws: torch.Tensor) -> int:
+    if isinstance(ws, torch.Tensor) and ws.dtype is torch.uint8 and ws.is_cuda and ws.is_contiguous():
+        return ws.data_ptr()
+    return _ptr(ws, "ws", torch.uint8)
 
 
 # ------------------------------------------------------------------ C-ABI functions
@@ -449,8 +465,8 @@ def h3fp4_cross_attn(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, out: tor
     at = a.buffer_info()[0]
     _check(load_library().h3fp4_cross_attn(
         at, at + 24, at + 48, M, T, Hq, Hkv, D, qp, kp, nseg, _mask(key_mask, "key_mask", T),
-        D ** -0.5 if scale is None else scale, at + 72, _f32(lse, "lse", (M, Hq)), _ptr(ws, "ws", torch.uint8),
-        ws.numel(), _stream(stream)), "h3fp4_cross_attn")
+        D ** -0.5 if scale is None else scale, at + 72, _f32(lse, "lse", (M, Hq)), _workspace(ws), ws.numel(),
+        _stream(stream)), "h3fp4_cross_attn")
 
 
 def h3fp4_shared_attn(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, k_ctx: torch.Tensor, v_ctx: torch.Tensor,
@@ -472,7 +488,7 @@ def h3fp4_shared_attn(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, k_ctx: 
     _check(load_library().h3fp4_shared_attn(
         at, at + 24, at + 48, at + 72, at + 96, M, T, ctx, Hq, Hkv, D, qp, kp, nseg, _mask(key_mask, "key_mask", T),
         _mask(ctx_mask, "ctx_mask", ctx), D ** -0.5 if scale is None else scale, at + 120,
-        _f32(lse, "lse", (M, Hq)), _ptr(ws, "ws", torch.uint8), ws.numel(), _stream(stream)), "h3fp4_shared_attn")
+        _f32(lse, "lse", (M, Hq)), _workspace(ws), ws.numel(), _stream(stream)), "h3fp4_shared_attn")
 
 
 def h3fp4_attn_workspace_bytes(M: int, T: int, Hq: int, Hkv: int, D: int, q_off: Optional[Sequence[int]] = None,
