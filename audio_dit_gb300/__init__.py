@@ -130,10 +130,13 @@ _BF16, _F32 = torch.bfloat16, torch.float32
 def _heads(t: torch.Tensor, what: str, rows: int, heads: int, d: int):
     """(address, row stride, head stride) of a bf16 [rows, heads, d] view: any row
     and head strides, the elements of a head contiguous."""
-    if (not isinstance(t, torch.Tensor) or t.dtype is not _BF16 or t.shape != (rows, heads, d) or not t.is_cuda
-            or (d > 1 and t.stride(2) != 1)):
+    try:
+        row, head, one = t.stride()
+        good = t.dtype is _BF16 and t.shape == (rows, heads, d) and t.is_cuda and (one == 1 or d == 1)
+    except (AttributeError, ValueError):
+        good = False
+    if not good:
         _refuse_heads(t, what, rows, heads, d)
-    row, head, _ = t.stride()
     # the stride of a dimension of one element says nothing about the memory
     if heads <= 1:
         head = d

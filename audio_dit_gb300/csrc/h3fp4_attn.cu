@@ -918,6 +918,7 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const __grid_co
 {
     const Cut c = p.cuts[blockIdx.x];
     griddep_wait();
+    griddep_launch_dependents();
     const int end = min(c.rows, (int)(blockIdx.y + 1) * kJoinRows);
     for (int at = blockIdx.y * kJoinRows + (threadIdx.x >> 5); at < end; at += kJoinWarps) {
         const int tk = at / p.o.pack;
@@ -957,6 +958,7 @@ __global__ void __launch_bounds__(kJoinThreads)
         in = (r - block * t.unit_tok) * t.pack + at - tk * t.pack;
     }
     griddep_wait();
+    griddep_launch_dependents();
     if (at >= rows) return;
     join_row<DP>(o, r, h, 1 + parts, [&](int i, const float*& row, const float2*& ml) {
         if (i == 0) slot_row<DP>(o, 0, pu, at, row, ml);
