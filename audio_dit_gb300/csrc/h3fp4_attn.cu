@@ -817,7 +817,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 // partials and m the largest m_i, out = sum_i 2^(m_i - m) o_i / sum_i 2^(m_i - m) l_i.
 // Reads each partial once; bound by latency where rows are few, so the
 // statistics of up to 32 partials are read at once, a lane each, then their
-// sums in groups of four.
+// sums in groups of four.  Ordinary loads: the attention kernel may still be
+// writing when this one starts, and a read-only load could be moved above the
+// wait for it.
 constexpr int kJoinThreads = 256;
 constexpr int kJoinWarps = kJoinThreads / 32;
 constexpr int kJoinRows = 2 * kJoinWarps;  // rows of a block of the first kernel below
@@ -848,7 +850,7 @@ __device__ __forceinline__ void join_row(const JoinOut& p, int r, int h, int all
         if (lane < here) {
             const float2* src;
             at(first + lane, row, src);
-            ml = __ldg(src);
+            ml = *src;
         }
         float top = ml.x;
 #pragma unroll
@@ -873,10 +875,10 @@ __device__ __forceinline__ void join_row(const JoinOut& p, int r, int h, int all
                 g[k] = __shfl_sync(0xffffffffu, w, from);
                 if (i + k >= here) g[k] = 0.0f;
                 if constexpr (kV == 4) {
-                    const float4 x = __ldg(reinterpret_cast<const float4*>(src) + lane);
+                    const float4 x = reinterpret_cast<const float4*>(src)[lane];
                     v[k][0] = x.x, v[k][1] = x.y, v[k][2] = x.z, v[k][3] = x.w;
                 } else {
-                    const float2 x = __ldg(reinterpret_cast<const float2*>(src) + lane);
+                    const float2 x = reinterpret_cast<const float2*>(src)[lane];
                     v[k][0] = x.x, v[k][1] = x.y;
                 }
             }
