@@ -24,12 +24,23 @@
 //                the other's softmax.  A warp of its own per tile, since the
 //                waits and bookkeeping around a tile's sixteen MMAs take one warp
 //                about as long as the MMAs themselves.
-//   warp 2       allocates TMEM; walks the CTA's pieces for all roles; keys that are left out (a mask, the end of a
-//                segment inside a tile): their bits for the softmax, and zeros
-//                over their rows of the V tile, since 0 * NaN is not 0
+//   warp 2       allocates TMEM; walks the CTA's pieces for all roles; keys that
+//                are left out (a mask, the end of a segment inside a tile): their
+//                bits for the softmax, and zeros over their rows of the V tile,
+//                since 0 * NaN is not 0
 //   warps 4-11   softmax of tile A, of tile B (a warpgroup each)
 //   warps 12-15  epilogue: divides by l, rounds, stores; or stores partial sums
 // The epilogue of a unit overlaps the next unit's first MMAs and softmax.
+//
+// What bounds it: a step (two query tiles, 128 keys, heads of 128) is 2048 cycles
+// of MMAs and takes about 2700, because a tile's softmax (about 1500) and its own
+// MMAs follow one another and the other tile fills the tensor cores only in part.
+// With heads of 64 the softmax warpgroups' latency is what is left (2490 a step,
+// 1024 of them MMAs).  A unit's ends cost about one step more.  Kernel time with
+// flushed caches: 2 x 8192 rows over 1024 shared and 8192 own keys, 24 heads of
+// 128: 1066 us (1.74 PFLOP/s); 30720 rows over 512 keys: 152 us (1.27 PFLOP/s);
+// 1024 rows over 30720 keys: 247 us (1.56 PFLOP/s); one row over 32768 keys, 32
+// heads over 8: 46 us (36 of them this kernel, 3.7 TB/s).
 //
 // Every wait is bounded; a role that gives up records it in the status word and
 // leaves, and so do the roles that depend on it.
@@ -49,10 +60,15 @@ namespace h3fp4 {
 namespace {
 
 constexpr int kThreads = 512;
-constexpr float kGrowth = 8.0f;      // log2 of how far the true maximum may pass the one in use
+// log2 of how far the true maximum may pass the one in use (2 x 8192 rows over 1024
+// shared and 8192 own keys: 1066 us, following every new maximum 1325 us)
+constexpr float kGrowth = 8.0f;
 constexpr int kMaskSlots = 8;       // more than the ring's V tiles
 constexpr int kPieceSlots = 4;
 constexpr uint32_t kTmemCols = 512;
+// The softmax holds 128 scores a thread; with 152 registers it spills. The others' split
+// hardly matters (72/176/80 and 80/176/64: the same within 2 %; 96/168/80: 30720
+// rows over 512 keys 164 us instead of 152, 112/160/80: 185).
 constexpr uint32_t kRegsControl = 80, kRegsSoftmax = 176, kRegsEpilogue = 80;
 static_assert(kRegsControl + 2 * kRegsSoftmax + kRegsEpilogue <= 512, "setmaxnreg shares exceed the launch budget");
 
@@ -815,7 +831,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 //
 // One warp per row of a unit of the pool: with m_i (base 2) and l_i of its
 // partials and m the largest m_i, out = sum_i 2^(m_i - m) o_i / sum_i 2^(m_i - m) l_i.
-// Reads each partial once; bound by latency where rows are few, so the
+// Reads each partial once; bound by latency (8 units of 4 rows, cut into 19 each:
+// 6 us by itself; 96 units of 256 rows: 12 us), so the
 // statistics of up to 32 partials are read at once, a lane each, then their
 // sums in groups of four.  Ordinary loads: the attention kernel may still be
 // writing when this one starts, and a read-only load could be moved above the

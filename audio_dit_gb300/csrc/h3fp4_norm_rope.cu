@@ -17,6 +17,12 @@
 // A warp takes kUnroll heads per group of one tensor (a part of the row's heads)
 // for every so many rows: its weights stay in registers, and all of a row's loads
 // are issued before the first is used, which is what memory latency asks for.
+//
+// Measured (24 + 24 heads of 128, all rotated; calls back to back): 31744 rows
+// 120 us (6.6 TB/s of 6.8 that a copy reaches), 8192 rows 34 us (6.1 TB/s), one
+// row 2 us.  31744 rows with flushed caches: three heads in flight and five
+// blocks per SM 126 us, two and eight 144, six and three 130; a whole row per
+// warp 136.
 #include <cstdint>
 
 #include <cuda_bf16.h>
