@@ -774,7 +774,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int kind = u.e < p.t.nseg ? 0 : 1, rows = p.slot_rows[kind];
                 float* base = p.part[kind] + (long long)u.slot * rows * (DP + 2);
                 const int at = Y * tok * p.t.pack + row;
-                float* part = base + (long long)at * DP;
+                float* part = base + 4 * at;
                 __nv_bfloat16* o = p.out + r * p.out_row + (long long)h * p.out_head;
                 if (on && !u.whole)
                     *reinterpret_cast<float2*>(base + (long long)rows * DP + 2 * at) =
@@ -810,7 +810,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                             store_bf16(on, o + 32 * c, v, f, p.D - 32 * c, p.wide_out != 0);
                         } else {
 #pragma unroll
-                            for (int j = 0; j < 8; ++j) st_global_v4_if(on, part + 32 * c + 4 * j, v + 4 * j);
+                            for (int j = 0; j < 8; ++j) st_global_v4_if(on, part + (long long)(8 * c + j) * 4 * rows, v + 4 * j);
                         }
                     }
                     release();
@@ -829,17 +829,17 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // ------------------------------------------------------------------ joining partial sums
 //
-// One warp per row of a unit of the pool: with m_i (base 2) and l_i of its
-// partials and m the largest m_i, out = sum_i 2^(m_i - m) o_i / sum_i 2^(m_i - m) l_i.
-// Reads each partial once; bound by latency (8 units of 4 rows, cut into 19 each:
-// 6 us by itself; 96 units of 256 rows: 12 us), so the
-// statistics of up to 32 partials are read at once, a lane each, then their
-// sums in groups of four.  Ordinary loads: the attention kernel may still be
+// With m_i (base 2) and l_i of a row's partials and m the largest m_i,
+//     out = sum_i 2^(m_i - m) o_i / sum_i 2^(m_i - m) l_i.
+// A partial holds its sums as [DP / 4][rows][4], so that both the attention's
+// threads, a row each, and those here, a row and eight columns each, read and
+// write whole lines; `shift` rows (log2) are side by side here, fewer than 32
+// where a unit has fewer.  Bound by latency where rows are few: kJoinAtOnce
+// partials are read at once.  Ordinary loads: the attention kernel may still be
 // writing when this one starts, and a read-only load could be moved above the
 // wait for it.
 constexpr int kJoinThreads = 256;
-constexpr int kJoinWarps = kJoinThreads / 32;
-constexpr int kJoinRows = 2 * kJoinWarps;  // rows of a block of the first kernel below
+constexpr int kJoinAtOnce = 4;
 
 struct JoinOut {
     __nv_bfloat16* out;
@@ -848,84 +848,91 @@ struct JoinOut {
     const float* part[2];
     int slot_rows[2];
     int D, Hq, pack;
+    int shift;
 };
 
-// Row r, head h from `all` partials; at(i, row, ml) gives the sums and the
-// statistics of partial i.
-template <int DP, class At>
-__device__ __forceinline__ void join_row(const JoinOut& p, int r, int h, int all, At at)
+// A row's sums from column col on, and its statistics, in one slot.
+template <int DP>
+struct JoinAt {
+    const float4* o;
+    const float2* ml;
+    long long rows;
+    __device__ __forceinline__ JoinAt(const JoinOut& p, int kind, int slot, int row, int col) : rows(p.slot_rows[kind])
+    {
+        const float* base = p.part[kind] + slot * rows * (DP + 2);
+        o = reinterpret_cast<const float4*>(base) + (col >> 2) * rows + row;
+        ml = reinterpret_cast<const float2*>(base + rows * DP) + row;
+    }
+};
+
+// Columns col... of row r, head h: the partial `own`, and `others` more from
+// `rest` on, `apart` slots from one to the next.
+template <int DP>
+__device__ __forceinline__ void join_row(const JoinOut& p, int r, int h, int col, const JoinAt<DP>& own,
+                                         const JoinAt<DP>& rest, int others, int apart)
 {
-    const int lane = threadIdx.x & 31;
-    constexpr int kV = DP / 32;  // columns per lane
-    float acc[kV], m = -INFINITY, l = 0.0f;
+    const long long step = apart * rest.rows * (DP + 2);  // floats, a multiple of 4 (rows are even)
+    const int all = 1 + others;
+    float acc[8], m = -INFINITY, l = 0.0f;
 #pragma unroll
-    for (int j = 0; j < kV; ++j) acc[j] = 0.0f;
-    for (int first = 0; first < all; first += 32) {
-        const int here = min(32, all - first);
-        const float* row = nullptr;
-        float2 ml = make_float2(-INFINITY, 0.0f);
-        if (lane < here) {
-            const float2* src;
-            at(first + lane, row, src);
-            ml = *src;
-        }
-        float top = ml.x;
+    for (int j = 0; j < 8; ++j) acc[j] = 0.0f;
+    for (int first = 0; first < all; first += kJoinAtOnce) {
+        float2 ml[kJoinAtOnce];
+        float4 lo[kJoinAtOnce], hi[kJoinAtOnce];
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-        const float m_new = fmaxf(m, top);
-        const float f = m == m_new ? 1.0f : ex2_approx_ftz(m - m_new);
-        const float w = ml.x == -INFINITY ? 0.0f : ml.x == m_new ? 1.0f : ex2_approx_ftz(ml.x - m_new);
-        float add = ml.y * w;
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) add += __shfl_xor_sync(0xffffffffu, add, o);
-        l = l * f + add;
-        m = m_new;
-#pragma unroll
-        for (int j = 0; j < kV; ++j) acc[j] *= f;
-        for (int i = 0; i < here; i += 4) {
-            float v[4][kV], g[4];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const int from = min(i + k, here - 1);
-                const float* src = reinterpret_cast<const float*>(
-                    __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(row), from));
-                g[k] = __shfl_sync(0xffffffffu, w, from);
-                if (i + k >= here) g[k] = 0.0f;
-                if constexpr (kV == 4) {
-                    const float4 x = reinterpret_cast<const float4*>(src)[lane];
-                    v[k][0] = x.x, v[k][1] = x.y, v[k][2] = x.z, v[k][3] = x.w;
-                } else {
-                    const float2 x = reinterpret_cast<const float2*>(src)[lane];
-                    v[k][0] = x.x, v[k][1] = x.y;
-                }
+        for (int i = 0; i < kJoinAtOnce; ++i) {
+            ml[i] = make_float2(-INFINITY, 0.0f);
+            lo[i] = hi[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            if (i == 0 && first == 0) {
+                ml[i] = *own.ml;
+                lo[i] = own.o[0];
+                hi[i] = own.o[own.rows];
+            } else if (first + i < all) {
+                const long long off = (first + i - 1) * step;
+                const float4* o = rest.o + (off >> 2);
+                ml[i] = rest.ml[off >> 1];
+                lo[i] = o[0];
+                hi[i] = o[rest.rows];
             }
+        }
+        float top = m;
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
+        for (int i = 0; i < kJoinAtOnce; ++i) top = fmaxf(top, ml[i].x);
+        const float f = m == top ? 1.0f : ex2_approx_ftz(m - top);
+        m = top;
+        l *= f;
 #pragma unroll
-                for (int j = 0; j < kV; ++j)  // a partial without a key counts nothing, whatever its sums are
-                    acc[j] = g[k] == 0.0f ? acc[j] : fmaf(v[k][j], g[k], acc[j]);
+        for (int j = 0; j < 8; ++j) acc[j] *= f;
+#pragma unroll
+        for (int i = 0; i < kJoinAtOnce; ++i) {
+            // a partial without a key counts nothing, whatever its sums are
+            const bool some = ml[i].x != -INFINITY;
+            const float w = !some ? 0.0f : ml[i].x == m ? 1.0f : ex2_approx_ftz(ml[i].x - m);
+            const float v[8] = {lo[i].x, lo[i].y, lo[i].z, lo[i].w, hi[i].x, hi[i].y, hi[i].z, hi[i].w};
+            l = fmaf(ml[i].y, w, l);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) acc[j] = some ? fmaf(v[j], w, acc[j]) : acc[j];
         }
     }
     const float inv = l == 0.0f ? 0.0f : rcp_approx(l);
-    __nv_bfloat16* o = p.out + (long long)r * p.out_row + (long long)h * p.out_head + lane * kV;
-#pragma unroll
-    for (int j = 0; j < kV; j += 2)
-        if (lane * kV + j < p.D) *reinterpret_cast<uint32_t*>(o + j) = cvt_bf16x2(f2(acc[j] * inv, acc[j + 1] * inv));
-    if (p.lse && lane == 0)
+    if (col < p.D)  // D is a multiple of 8
+        *reinterpret_cast<uint4*>(p.out + (long long)r * p.out_row + (long long)h * p.out_head + col) =
+            make_uint4(cvt_bf16x2(f2(acc[0] * inv, acc[1] * inv)), cvt_bf16x2(f2(acc[2] * inv, acc[3] * inv)),
+                       cvt_bf16x2(f2(acc[4] * inv, acc[5] * inv)), cvt_bf16x2(f2(acc[6] * inv, acc[7] * inv)));
+    if (p.lse && col == 0)
         p.lse[(long long)r * p.Hq + h] = l == 0.0f ? -INFINITY : (m + __log2f(l)) * 0.69314718055994531f;
 }
 
-// Sums and statistics of row `in` of slot `slot`.
+// This thread's row of the block's unit, and its first column.
 template <int DP>
-__device__ __forceinline__ void slot_row(const JoinOut& p, int kind, int slot, int in, const float*& row,
-                                         const float2*& ml)
+__device__ __forceinline__ int join_place(int shift, int& col)
 {
-    const float* base = p.part[kind] + (long long)slot * p.slot_rows[kind] * (DP + 2);
-    row = base + (long long)in * DP;
-    ml = reinterpret_cast<const float2*>(base + (long long)p.slot_rows[kind] * DP) + in;
+    const int i = blockIdx.y * kJoinThreads + threadIdx.x, group = i >> shift;
+    col = group % (DP / 8) * 8;
+    return (group / (DP / 8) << shift) + (i & ((1 << shift) - 1));
 }
 
-// The cut units of the pool: block (i, y) takes rows 16 y... of cut i.
+// The cut units of the pool: blocks (i, y) take the rows of cut i.
 struct JoinCuts {
     JoinOut o;
     int lanes;
@@ -936,19 +943,17 @@ template <int DP>
 __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const __grid_constant__ JoinCuts p)
 {
     const Cut c = p.cuts[blockIdx.x];
+    int col;
+    const int at = join_place<DP>(p.o.shift, col), tk = at / p.o.pack;
     griddep_wait();
     griddep_launch_dependents();
-    const int end = min(c.rows, (int)(blockIdx.y + 1) * kJoinRows);
-    for (int at = blockIdx.y * kJoinRows + (threadIdx.x >> 5); at < end; at += kJoinWarps) {
-        const int tk = at / p.o.pack;
-        join_row<DP>(p.o, c.tok0 + tk, c.head0 + at - tk * p.o.pack, c.parts,
-                     [&](int i, const float*& row, const float2*& ml) {
-                         slot_row<DP>(p.o, 0, cut_slot(c.cta + i * p.lanes, i == 0), at, row, ml);
-                     });
-    }
+    if (at >= c.rows) return;
+    // (slots: cut_slot() of the CTAs that hold the unit's pieces, of which the first begins it)
+    join_row<DP>(p.o, c.tok0 + tk, c.head0 + at - tk * p.o.pack, col, JoinAt<DP>(p.o, 0, cut_slot(c.cta, true), at, col),
+                 JoinAt<DP>(p.o, 0, cut_slot(c.cta + p.lanes, false), at, col), c.parts - 1, 2 * p.lanes);
 }
 
-// The separate plan: blocks (x, y) take the rows of segments' unit x, a warp each.
+// The separate plan: blocks (x, y) take the rows of segments' unit x.
 // Their own keys are one partial, the context's as many as its unit was cut into.
 template <int DP>
 __global__ void __launch_bounds__(kJoinThreads)
@@ -964,7 +969,8 @@ __global__ void __launch_bounds__(kJoinThreads)
     const int u = pu - t.pool_unit[lo], rb = t.row_blocks(lo), hb = u / rb;
     const int tok0 = t.q_begin(lo) + (u - hb * rb) * t.unit_tok;
     const int rows = min(t.unit_tok, t.q_end(lo) - tok0) * t.pack;
-    const int at = blockIdx.y * kJoinWarps + (threadIdx.x >> 5);
+    int col;
+    const int at = join_place<DP>(o.shift, col);
     int r = 0, h = 0, slot = 0, parts = 0, in = 0;
     if (at < rows) {
         const int tk = at / t.pack, ce = t.nseg, cn = t.steps(ce);
@@ -979,10 +985,7 @@ __global__ void __launch_bounds__(kJoinThreads)
     griddep_wait();
     griddep_launch_dependents();
     if (at >= rows) return;
-    join_row<DP>(o, r, h, 1 + parts, [&](int i, const float*& row, const float2*& ml) {
-        if (i == 0) slot_row<DP>(o, 0, pu, at, row, ml);
-        else slot_row<DP>(o, 1, slot + i - 1, in, row, ml);
-    });
+    join_row<DP>(o, r, h, col, JoinAt<DP>(o, 0, pu, at, col), JoinAt<DP>(o, 1, slot, in, col), parts, 1);
 }
 
 // ------------------------------------------------------------------ host side
@@ -1020,20 +1023,22 @@ cudaError_t run(const AttnPlan& pl, const CUtensorMap (&m)[5], const AttnParams&
     cfg.numAttrs = 1;
     e = cudaLaunchKernelEx(&cfg, kernel, m[0], m[1], m[2], m[3], m[4], p);
     if (e != cudaSuccess || !pl.join) return e;
-    const JoinOut o{p.out, p.out_row, p.out_head, p.lse, {p.part[0], p.part[1]}, {p.slot_rows[0], p.slot_rows[1]},
-                    p.D, p.Hq, pl.t.pack};
+    JoinOut o{p.out, p.out_row, p.out_head, p.lse, {p.part[0], p.part[1]}, {p.slot_rows[0], p.slot_rows[1]},
+              p.D, p.Hq, pl.t.pack, 0};
+    while (o.shift < 5 && (1 << o.shift) < pl.slot_rows[0]) ++o.shift;
+    const int groups = (pl.slot_rows[0] + (1 << o.shift) - 1) >> o.shift;
+    const unsigned blocks = (unsigned)(((groups << o.shift) * (DP / 8) + kJoinThreads - 1) / kJoinThreads);
     cfg.blockDim = dim3(kJoinThreads);
     cfg.dynamicSmemBytes = 0;
     if (pl.t.separate) {
-        cfg.gridDim = dim3((unsigned)pl.t.pool_unit[pl.t.nseg],
-                           (unsigned)((pl.slot_rows[0] + kJoinWarps - 1) / kJoinWarps));
+        cfg.gridDim = dim3((unsigned)pl.t.pool_unit[pl.t.nseg], blocks);
         return cudaLaunchKernelEx(&cfg, attn_join_separate_kernel<DP>, o, p.t);
     }
     JoinCuts cuts;
     cuts.o = o;
     cuts.lanes = pl.t.lanes;
     std::memcpy(cuts.cuts, pl.cuts, sizeof(cuts.cuts));
-    cfg.gridDim = dim3((unsigned)pl.n_cuts, (unsigned)((pl.slot_rows[0] + kJoinRows - 1) / kJoinRows));
+    cfg.gridDim = dim3((unsigned)pl.n_cuts, blocks);
     return cudaLaunchKernelEx(&cfg, attn_join_kernel<DP>, cuts);
 }
 
