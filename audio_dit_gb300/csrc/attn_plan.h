@@ -5,7 +5,7 @@
 // tok = 128 / pack tokens, so that all of them use the same K and V.  A unit is
 // what one CTA works on at a time: two tiles of queries against the same keys
 // (pair plan), or one tile whose even and odd key tiles go to the CTA's two
-// softmax warpgroups (solo plan, for few rows).  Its steps are the 128-key tiles
+// softmax warpgroups (solo plan, for few units).  Its steps are the 128-key tiles
 // it walks: first the shared context's, then its own segment's.
 //
 // An entry is a segment; with the separate plan (many short segments over a long
@@ -17,7 +17,8 @@
 // same time.  What is left over (the pool) is laid out as one row of steps and
 // cut into equal stretches, one per CTA: a unit that is cut leaves partial sums
 // that a second kernel joins.  A cut within kSnap steps of a unit's edge moves
-// there, since a partial costs about as much as that many steps.
+// there, since a partial costs about as much as that many steps.  Where units as
+// they are come out sooner than cut ones and the second kernel, none is cut.
 //
 // Few units of a head over keys that do not fit in L2: were they cut one after
 // the other, the units of a head would walk the same keys at different times and
@@ -35,12 +36,12 @@ namespace h3fp4 {
 constexpr int kKeyTile = 128;
 constexpr int kAttnCtas = 152;   // one per SM of the GB300
 constexpr int kSnap = 4;         // 2 and 8 measured 0 and 1 % slower on 16384 rows over 9216 keys
-// What a unit costs beside its tiles, and a unit without keys, in steps.  9001 masked
-// rows over six prompts, one without keys: 0 and 1 69 us, 0 and 2 72, 1 and 2 62, 1 and
-// 3 68, 2 and 4 64.
-constexpr int kUnitSteps = 1;
-constexpr int kEmptySteps = 2;
-static_assert(kUnitSteps < kSnap && kEmptySteps <= 2 * kSnap, "cuts lie behind a unit's overhead");
+// What a unit costs beside its tiles, in steps: one of the pair plan's, three of the solo
+// plan's, which are about half as long; a unit without keys one more.  9001 masked rows over
+// six prompts, one without keys (pair; unit and empty unit): 0 and 1 69 us, 0 and 2 72, 1 and
+// 2 62, 1 and 3 68, 2 and 4 64.
+constexpr int kPairUnitSteps = 1, kSoloUnitSteps = 3;
+static_assert(kSoloUnitSteps < kSnap && kSoloUnitSteps + 1 <= 2 * kSnap, "cuts lie behind a unit's overhead");
 constexpr int kAttnEntries = H3FP4_ATTN_MAX_SEGMENTS + 1;
 
 __host__ __device__ inline int lesser(int a, int b) { return a < b ? a : b; }
@@ -53,6 +54,8 @@ struct AttnTable {
     int head_blocks;       // Hq / pack
     int ctx_tiles;         // key tiles of the context
     int separate;
+    int uncut;             // no unit of the pool is cut
+    int unit_steps;        // steps a unit counts beside its tiles
     int any_full;          // some entry has whole waves
     int ctx_masked, own_masked, ctx_ragged;  // masks are given; the context's length is no multiple of a tile
     int pool_steps;
@@ -75,7 +78,7 @@ struct AttnTable {
     __host__ __device__ int tiles(int e) const { return tiles_ctx(e) + tiles_own(e); }
     // Steps of a unit: its tiles, and what beginning and ending it costs; a unit
     // without keys still writes zeros.
-    __host__ __device__ static int steps_of(int tiles) { return tiles > 0 ? tiles + kUnitSteps : kEmptySteps; }
+    __host__ __device__ int steps_of(int tiles) const { return (tiles > 0 ? tiles : 1) + unit_steps; }
     __host__ __device__ int steps(int e) const { return steps_of(tiles(e)); }
     __host__ __device__ int row_blocks(int e) const { return (q_end(e) - q_begin(e) + unit_tok - 1) / unit_tok; }
     __host__ __device__ int units(int e) const { return head_blocks * row_blocks(e); }
@@ -97,9 +100,10 @@ struct AttnTable {
     {
         const int x = c * share + lesser(c, longer);
         if (c <= 0 || c >= stretches || x <= 0 || x >= pool_steps) return x;
-        const int e = find(pool_step, x), n = steps(e), t = (x - pool_step[e]) % n;
+        const int last = entries - 1, e = x >= pool_step[last] ? last : find(pool_step, x);
+        const int n = steps(e), t = (x - pool_step[e]) % n;
         // (a segment's unit of the separate plan is never cut)
-        const int snap = separate && e < nseg ? n : kSnap;
+        const int snap = uncut || (separate && e < nseg) ? n : kSnap;
         if (t <= snap && t <= n - t) return x - t;
         if (n - t <= snap) return x + n - t;
         return x;
@@ -238,11 +242,11 @@ struct Walk {
         }
         if (left <= 0) return false;
         fill(p);
-        const int tiles = p.ctx_tiles + p.own_tiles, n = AttnTable::steps_of(tiles);
+        const int tiles = p.ctx_tiles + p.own_tiles, n = t.steps_of(tiles);
         const int take = lesser(n - tile, left);
         // a unit's first steps are its overhead; cuts lie behind them
-        p.t0 = tile > kUnitSteps ? tile - kUnitSteps : 0;
-        p.nt = tiles > 0 ? tile + take - kUnitSteps - p.t0 : 0;
+        p.t0 = tile > t.unit_steps ? tile - t.unit_steps : 0;
+        p.nt = tiles > 0 ? tile + take - t.unit_steps - p.t0 : 0;
         p.whole = take == n && !t.separate;
         // With the separate plan every piece leaves partials: one for a segment's unit, those of the
         // context's numbered along the pool.
@@ -294,10 +298,11 @@ struct AttnPlan {
     size_t bytes;        // workspace; 0: more steps than 32 bits count
 };
 
-// Units and steps of all of them for one choice of pack and of solo or pair units:
-// with the segments' units walking the context too, and with it apart.
+// Units, tiles of all of them and of the longest, for one choice of pack and of solo or
+// pair units: with the segments' units walking the context too, and with it apart;
+// the bytes of the context's keys that its units walk then.
 struct Cost {
-    double units, steps, units_apart, steps_apart;
+    double units, tiles, longest, units_apart, tiles_apart, ctx_bytes;
 };
 
 template <class Job>
@@ -305,16 +310,56 @@ inline Cost cost_of(const Job& job, const AttnTable& t, int pack, bool solo)
 {
     const int tok = 128 / pack, unit_tok = solo ? tok : 2 * tok;
     const long long ctx = t.ctx_tiles;
-    long long units = 0, steps = 0, own = 0;
+    long long units = 0, tiles = 0, longest = 0, own = 0;
     for (int e = 0; e < t.nseg; ++e) {
         const long long rb = (t.q_off[e + 1] - t.q_off[e] + unit_tok - 1) / unit_tok, n = t.tiles_own(e);
         units += rb;
-        steps += rb * (ctx + n > 0 ? ctx + n : 1);
+        tiles += rb * (ctx + n > 0 ? ctx + n : 1);
         own += rb * (n > 0 ? n : 1);
+        if (rb > 0 && ctx + n > longest) longest = ctx + n;
     }
     const long long apart = (job.M + unit_tok - 1) / unit_tok, hb = job.Hq / pack;
-    return Cost{(double)(hb * units), (double)hb * (double)steps, (double)(hb * (units + apart)),
-                (double)hb * (double)(own + apart * (ctx > 0 ? ctx : 1))};
+    return Cost{(double)(hb * units), (double)hb * (double)tiles, (double)longest, (double)(hb * (units + apart)),
+                (double)hb * (double)(own + apart * (ctx > 0 ? ctx : 1)),
+                4.0 * job.D * (double)job.C * (double)(apart * hb)};
+}
+
+// The time of a plan in steps of a pair unit (1.35 us at heads of 128): a tile of a solo
+// unit takes 0.52, its ends 1.45 (a pair's 1); cutting costs a piece's end, the partials'
+// way through memory and a second kernel, 13 us (pair) or 11 us (solo, half the rows).
+// Measured, 24 heads of 128, calls back to back, us (the smallest is what is taken):
+//     rows x keys      pair, cut   pair, whole   solo, cut   solo, whole
+//     256 x 4096            26.9          50.4        22.6          29.9
+//     512 x 2048            27.0          29.0        23.7          19.1
+//     1024 x 2048           36.9          30.1        32.7          34.2
+//     2048 x 2048           49.8          54.7        51.4          48.0
+//     4096 x 512               -          28.7           -          36.7
+//     4096 x 4096          137.5         144.7       147.8         158.7
+//     1024 x 30720         237.5         336.8       247.5         361.6
+// With the context apart (heads, rows a segment; cut):   pair, solo
+//     32 over 8 of 128, 48 x 1 over 16384 keys           38.7, 36.2
+//     24 of 128, 40 x 1 over 16384                       78.8, 63.7
+//     24 of 64, 20 x 20 over 12000                       75.8, 78.9
+//     24 of 128, 20 x 20 over 12000                      93.0, 120.9
+// The last one's keys do not stay in L2 from one of a head's units to the next, and solo
+// units are twice as many: hence the term with the bytes where all heads' keys exceed 96 MB.
+struct PlanTime {
+    double cut, whole, apart;
+};
+
+inline PlanTime time_of(const Cost& c, bool solo, double key_bytes)
+{
+    const double tile = solo ? 0.52 : 1.0, ends = solo ? 1.45 : 1.0, join = solo ? 8.0 : 10.0;
+    const double all = tile * c.tiles + ends * c.units, unit = tile * c.longest + ends;
+    double ctas = c.tiles / kSnap;
+    if (ctas < c.units) ctas = c.units;
+    if (ctas > kAttnCtas) ctas = kAttnCtas;
+    const double waves = (double)(((long long)c.units + kAttnCtas - 1) / kAttnCtas);
+    const double even = all / kAttnCtas + unit, dealt = waves * unit;
+    double apart = tile * c.tiles_apart + (ends + 0.5) * c.units_apart;  // a partial of each unit
+    if (key_bytes > 96.0 * 1024 * 1024) apart += kAttnCtas * c.ctx_bytes / 18e6;
+    return PlanTime{ctas > 0 ? all / ctas + join : 0.0, dealt < even ? dealt : even,
+                    apart / kAttnCtas + join};
 }
 
 template <class Job>
@@ -342,21 +387,23 @@ inline AttnPlan make_plan(const Job& job)
     double best = 0;
     for (int g = 1; g <= group && g <= 128; ++g) {
         if (group % g) continue;
-        const double s = group == 1 ? 0 : cost_of(job, t, g, true).steps;
+        const double s = group == 1 ? 0 : cost_of(job, t, g, true).tiles;
         if (g == 1 || s <= best) {
             best = s;
             pack = g;
         }
     }
-    // A pair's step takes about 1.5 of a solo step (which reads K and V for one
-    // tile of queries only); the separate plan pays two steps per unit for its partials.
     const Cost pair = cost_of(job, t, pack, false), single = cost_of(job, t, pack, true);
-    const double whole = single.steps < 1.5 * pair.steps ? single.steps : 1.5 * pair.steps;
-    const double solo_apart = single.steps_apart + 2 * single.units_apart;
-    const double pair_apart = 1.5 * (pair.steps_apart + 2 * pair.units_apart);
-    const double apart = solo_apart < pair_apart ? solo_apart : pair_apart;
-    const bool sep = job.nseg > 1 && job.C > 0 && apart + 2 * kAttnCtas < whole;
-    pl.solo = sep ? solo_apart <= pair_apart : single.steps <= 1.5 * pair.steps;
+    const double ctx_bytes = 4.0 * job.D * (double)job.C * job.Hkv;
+    const PlanTime of_pair = time_of(pair, false, ctx_bytes), of_solo = time_of(single, true, ctx_bytes);
+    const double best_pair = of_pair.cut < of_pair.whole ? of_pair.cut : of_pair.whole;
+    const double best_solo = of_solo.cut < of_solo.whole ? of_solo.cut : of_solo.whole;
+    const double apart = of_solo.apart < of_pair.apart ? of_solo.apart : of_pair.apart;
+    // 48 tokens over 16384 shared keys: apart 41 us, each token for itself 146 us
+    const bool sep = job.nseg > 1 && job.C > 0 && apart < best_pair && apart < best_solo;
+    pl.solo = sep ? of_solo.apart <= of_pair.apart : best_solo <= best_pair;
+    t.uncut = !sep && (pl.solo ? of_solo.whole <= of_solo.cut : of_pair.whole <= of_pair.cut);
+    t.unit_steps = pl.solo ? kSoloUnitSteps : kPairUnitSteps;
     t.entries = job.nseg + (sep ? 1 : 0);
     t.pack = pack;
     t.tok = 128 / pack;
@@ -366,9 +413,9 @@ inline AttnPlan make_plan(const Job& job)
 
     // CTAs: one per SM where there is work for all of them.
     const Cost& cost = pl.solo ? single : pair;
-    const double steps = sep ? cost.steps_apart : cost.steps, units = sep ? cost.units_apart : cost.units;
-    if (steps + 2 * kEmptySteps * units >= 2147483648.0) return pl;  // steps are counted in 32 bits
-    double ctas = steps / kSnap;
+    const double tiles = sep ? cost.tiles_apart : cost.tiles, units = sep ? cost.units_apart : cost.units;
+    if (tiles + 2 * (kSoloUnitSteps + 1) * units >= 2147483648.0) return pl;  // steps are counted in 32 bits
+    double ctas = t.uncut ? units : tiles / kSnap;
     if (ctas < units) ctas = units;
     t.ctas = ctas > kAttnCtas ? kAttnCtas : ctas < 1 ? 1 : (int)ctas;
     t.any_full = 0;
@@ -379,7 +426,7 @@ inline AttnPlan make_plan(const Job& job)
     // than 64 MB (half the L2), and at most a twentieth of the CTAs left idle.
     t.lanes = 1;
     t.stretches = t.ctas;
-    if (t.entries == 1 && !t.any_full && t.ctas == kAttnCtas) {
+    if (t.entries == 1 && !t.uncut && !t.any_full && t.ctas == kAttnCtas) {
         const int rb = t.row_blocks(0), idle = kAttnCtas % rb;
         const double key_bytes = 4.0 * job.Hkv * job.D * ((double)job.T + (double)job.C);
         if (rb > 1 && rb <= kAttnCtas / 2 && idle * 20 <= kAttnCtas && key_bytes > 64.0 * 1024 * 1024) {
@@ -414,7 +461,7 @@ inline AttnPlan make_plan(const Job& job)
         pl.slots[0] = t.pool_unit[t.nseg];
         pl.slots[1] = t.units(t.nseg) + t.ctas;
     } else {
-        for (int c = 1, cut = -1; c < t.stretches && longest > 2 * kSnap; ++c) {
+        for (int c = 1, cut = -1; c < t.stretches && !t.uncut && longest > 2 * kSnap; ++c) {
             const int x = t.bound(c);
             if (x <= 0 || x >= t.pool_steps) continue;
             const int e = t.find(t.pool_step, x), n = t.steps(e), local = x - t.pool_step[e], u = local / n;

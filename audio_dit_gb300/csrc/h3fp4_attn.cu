@@ -953,39 +953,45 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const __grid_co
                  JoinAt<DP>(p.o, 0, cut_slot(c.cta + p.lanes, false), at, col), c.parts - 1, 2 * p.lanes);
 }
 
-// The separate plan: blocks (x, y) take the rows of segments' unit x.
-// Their own keys are one partial, the context's as many as its unit was cut into.
+// The separate plan: a row's own keys are one partial, the context's as many as its unit
+// was cut into.  Blocks take the rows (pack heads of a token side by side) of a head block
+// one after the other, whatever their segments: a block per segment's unit, each looking
+// for its place in the plan, took 36 us for 2400 units of 400 rows and 12 us for 480.
 template <int DP>
 __global__ void __launch_bounds__(kJoinThreads)
-    attn_join_separate_kernel(const __grid_constant__ JoinOut o, const __grid_constant__ AttnTable t)
+    attn_join_separate_kernel(const __grid_constant__ JoinOut o, const __grid_constant__ AttnTable t, int groups)
 {
-    const int pu = blockIdx.x;
-    int lo = 0, hi = t.nseg;
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (t.pool_unit[mid] <= pu) lo = mid;
-        else hi = mid;
-    }
-    const int u = pu - t.pool_unit[lo], rb = t.row_blocks(lo), hb = u / rb;
-    const int tok0 = t.q_begin(lo) + (u - hb * rb) * t.unit_tok;
-    const int rows = min(t.unit_tok, t.q_end(lo) - tok0) * t.pack;
-    int col;
-    const int at = join_place<DP>(o.shift, col);
-    int r = 0, h = 0, slot = 0, parts = 0, in = 0;
-    if (at < rows) {
-        const int tk = at / t.pack, ce = t.nseg, cn = t.steps(ce);
-        r = tok0 + tk;
-        h = hb * t.pack + at - tk * t.pack;
-        const int block = r / t.unit_tok, cu = hb * t.row_blocks(ce) + block, ca = t.pool_step[ce] + cu * cn;
-        const int first = t.stretch_of(ca);
-        parts = t.stretch_of(ca + cn - 1) - first + 1;
-        slot = cu + first;
-        in = (r - block * t.unit_tok) * t.pack + at - tk * t.pack;
+    constexpr int kRows = kJoinThreads / (DP / 8);
+    __shared__ int q_off[H3FP4_ATTN_MAX_SEGMENTS + 1];
+    for (int i = threadIdx.x; i <= t.nseg; i += kJoinThreads) q_off[i] = t.q_off[i];
+    __syncthreads();
+    const int hb = blockIdx.x / groups;
+    const int col = threadIdx.x / kRows * 8;
+    const long long at = (long long)(blockIdx.x - hb * groups) * kRows + threadIdx.x % kRows;
+    const int r = (int)(at / t.pack), head = (int)(at - (long long)r * t.pack);
+    int own = 0, own_at = 0, first = 0, parts = 0, in = 0;
+    if (r < t.M) {
+        int e = 0, end = t.nseg;
+        while (end - e > 1) {
+            const int mid = (e + end) >> 1;
+            if (q_off[mid] <= r) e = mid;
+            else end = mid;
+        }
+        const int local = r - q_off[e], rb = local / t.unit_tok;
+        own = t.pool_unit[e] + hb * t.row_blocks(e) + rb;
+        own_at = (local - rb * t.unit_tok) * t.pack + head;
+        const int ce = t.nseg, cn = t.steps(ce), block = r / t.unit_tok, cu = hb * t.row_blocks(ce) + block;
+        const int begin = t.pool_step[ce] + cu * cn;
+        first = t.stretch_of(begin);
+        parts = t.stretch_of(begin + cn - 1) - first + 1;
+        first += cu;
+        in = (r - block * t.unit_tok) * t.pack + head;
     }
     griddep_wait();
     griddep_launch_dependents();
-    if (at >= rows) return;
-    join_row<DP>(o, r, h, col, JoinAt<DP>(o, 0, pu, at, col), JoinAt<DP>(o, 1, slot, in, col), parts, 1);
+    if (r >= t.M) return;
+    join_row<DP>(o, r, hb * t.pack + head, col, JoinAt<DP>(o, 0, own, own_at, col), JoinAt<DP>(o, 1, first, in, col),
+                 parts, 1);
 }
 
 // ------------------------------------------------------------------ host side
@@ -1031,8 +1037,10 @@ cudaError_t run(const AttnPlan& pl, const CUtensorMap (&m)[5], const AttnParams&
     cfg.blockDim = dim3(kJoinThreads);
     cfg.dynamicSmemBytes = 0;
     if (pl.t.separate) {
-        cfg.gridDim = dim3((unsigned)pl.t.pool_unit[pl.t.nseg], blocks);
-        return cudaLaunchKernelEx(&cfg, attn_join_separate_kernel<DP>, o, p.t);
+        const int rows = kJoinThreads / (DP / 8);
+        const int per_head = (int)(((long long)pl.t.M * pl.t.pack + rows - 1) / rows);
+        cfg.gridDim = dim3((unsigned)per_head * (unsigned)pl.t.head_blocks);
+        return cudaLaunchKernelEx(&cfg, attn_join_separate_kernel<DP>, o, p.t, per_head);
     }
     JoinCuts cuts;
     cuts.o = o;
