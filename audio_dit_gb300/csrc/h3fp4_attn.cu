@@ -38,9 +38,9 @@
 // With heads of 64 the softmax warpgroups' latency is what is left (2490 a step,
 // 1024 of them MMAs).  A unit's ends cost about one step more.  Kernel time with
 // flushed caches: 2 x 8192 rows over 1024 shared and 8192 own keys, 24 heads of
-// 128: 1066 us (1.74 PFLOP/s); 30720 rows over 512 keys: 152 us (1.27 PFLOP/s);
-// 1024 rows over 30720 keys: 247 us (1.56 PFLOP/s); one row over 32768 keys, 32
-// heads over 8: 46 us (36 of them this kernel, 3.7 TB/s).
+// 128: 1062 us (1.75 PFLOP/s); 30720 rows over 512 keys: 150 us (1.29 PFLOP/s);
+// 1024 rows over 30720 keys: 242 us (1.60 PFLOP/s); one row over 32768 keys, 32
+// heads over 8: 46 us (35 of them this kernel, 3.8 TB/s).
 //
 // Every wait is bounded; a role that gives up records it in the status word and
 // leaves, and so do the roles that depend on it.
@@ -834,10 +834,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 // A partial holds its sums as [DP / 4][rows][4], so that both the attention's
 // threads, a row each, and those here, a row and eight columns each, read and
 // write whole lines; `shift` rows (log2) are side by side here, fewer than 32
-// where a unit has fewer.  Bound by latency where rows are few: kJoinAtOnce
-// partials are read at once.  Ordinary loads: the attention kernel may still be
-// writing when this one starts, and a read-only load could be moved above the
-// wait for it.
+// where a unit has fewer.  Bound by latency (8 units of 4 rows in 19 parts or so:
+// 7 us by itself; 96 units of 256 rows in 2 or 3 parts: 10 us): kJoinAtOnce
+// partials are read at once (8: 1 us slower on 512 to 2048 rows over 2048 keys).
+// Ordinary loads: the attention kernel may still be writing when this one starts,
+// and a read-only load could be moved above the wait for it.
 constexpr int kJoinThreads = 256;
 constexpr int kJoinAtOnce = 4;
 
