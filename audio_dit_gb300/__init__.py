@@ -162,6 +162,8 @@ def _table(seq: Optional[Sequence[int]]):
     if seq is None:
         return None, None, 1
     a = array("q", seq if isinstance(seq, list) else [int(v) for v in seq])
+    if len(a) < 2:
+        raise ValueError(f"an offset table has two entries at least (0 first, the number of rows last), got {len(a)}")
     return a, a.buffer_info()[0], len(a) - 1
 
 

@@ -168,7 +168,7 @@ h3fp4_status h3fp4_qk_norm_rope(const h3fp4_heads* q, const h3fp4_heads* k, int6
          q_out->ptr == k_out->ptr))
         return H3FP4_ERR_INVALID;
     NormRopeJob job{};
-    if ((st = make_segments(seg_off, nseg <= 0 ? 1 : nseg, M, &job.seg)) != H3FP4_OK) return st;
+    if ((st = make_segments(seg_off, seg_off == nullptr && nseg <= 0 ? 1 : nseg, M, &job.seg)) != H3FP4_OK) return st;
     if ((st = check_device()) != H3FP4_OK) return st;
     if (M == 0) return H3FP4_OK;
     auto tensor = [](const h3fp4_heads& x, const h3fp4_heads& y, const float* w, int heads) {
