@@ -157,13 +157,17 @@ def _refuse_heads(t, what: str, rows: int, heads: int, d: int):
     raise ValueError(f"{what}: the last dimension must be contiguous")
 
 
+def _check_table(seq: Sequence[int]):
+    if len(seq) < 2:
+        raise ValueError(f"an offset table has two entries at least (0 first, the number of rows last), got {len(seq)}")
+
+
 def _table(seq: Optional[Sequence[int]]):
     """(array of int64 to keep, its address, number of segments) of an offset table."""
     if seq is None:
         return None, None, 1
+    _check_table(seq)
     a = array("q", seq if isinstance(seq, list) else [int(v) for v in seq])
-    if len(a) < 2:
-        raise ValueError(f"an offset table has two entries at least (0 first, the number of rows last), got {len(a)}")
     return a, a.buffer_info()[0], len(a) - 1
 
 
@@ -210,6 +214,7 @@ def _stream(stream) -> Optional[int]:
 def _segs(seg_off: Optional[Sequence[int]]):
     if seg_off is None:
         return None, 1, None
+    _check_table(seg_off)
     arr = (C.c_int64 * len(seg_off))(*[int(v) for v in seg_off])
     return C.cast(arr, C.c_void_p), len(seg_off) - 1, arr
 
