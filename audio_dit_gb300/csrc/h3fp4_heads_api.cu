@@ -13,6 +13,7 @@ namespace {
 constexpr int64_t kMaxStride = (int64_t)1 << 38;  // elements: row pitches below the 2^40 bytes a TMA map holds
 
 constexpr int64_t kMaxRows = INT32_MAX - 255;  // rows are counted in 32 bits, up to two tiles past the last
+constexpr int kMaxHeads = INT32_MAX - 255;     // the norm's heads too, up to a warp's places past the last
 
 // Strides are positive multiples of 8 elements (16 bytes).
 bool good_strides(const h3fp4_heads& t)
@@ -151,7 +152,7 @@ h3fp4_status h3fp4_qk_norm_rope(const h3fp4_heads* q, const h3fp4_heads* k, int6
     if (M < 0 || M > INT32_MAX || D < 8 || D > kNormMaxD || D % 8 != 0) return H3FP4_ERR_SHAPE;
     if (rot < 0 || rot > D || rot % 16 != 0) return H3FP4_ERR_SHAPE;
     const bool with_k = k != nullptr;
-    if (Hq < 1 || (with_k && Hk < 1)) return H3FP4_ERR_SHAPE;
+    if (Hq < 1 || Hq > kMaxHeads || (with_k && (Hk < 1 || Hk > kMaxHeads))) return H3FP4_ERR_SHAPE;
     if (flags & ~H3FP4_ROPE_PAIRS) return H3FP4_ERR_INVALID;
     if (with_k != (k_out != nullptr) || !q || !q_out) return H3FP4_ERR_INVALID;
     if (!(eps >= 0.0f) || std::isinf(eps)) return H3FP4_ERR_INVALID;

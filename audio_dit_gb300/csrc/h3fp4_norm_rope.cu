@@ -24,6 +24,7 @@
 // blocks per SM 126 us, two and eight 144, six and three 130; a whole row per
 // warp 136.
 #include <cstdint>
+#include <numeric>
 
 #include <cuda_bf16.h>
 
@@ -82,13 +83,13 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) norm_rope_kernel(const
     const int lane = threadIdx.x & 31;
     const int c = lane & (kLanes - 1), g = lane / kLanes;
     // this warp's tensor, part of its heads, first row and step
-    const int all_parts = p.parts[0] + p.parts[1];
-    const int warp = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5), warps = gridDim.x * (kThreads / 32);
+    const unsigned all_parts = p.parts[0] + p.parts[1];
+    const unsigned warp = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5), warps = gridDim.x * (kThreads / 32);
     const int part = warp % all_parts;
     const bool second = part >= p.parts[0];
     const NormTensor& t = p.t[second ? 1 : 0];
     const int h0 = (second ? part - p.parts[0] : part) * (kGroups * kUnroll) + g;
-    const int step = warps / all_parts;  // the grid is a multiple of the parts
+    const unsigned step = warps / all_parts;  // the grid is a multiple of the parts
     const int n = p.D >> 3, hc = p.rot >> 4;
     int ca = 2 * c, cb = 2 * c + 1;  // this lane's chunks
     if (!kPairs && c < hc) {
@@ -188,8 +189,8 @@ cudaError_t launch_lanes(NormRopeParams& p, bool pairs, cudaStream_t s)
     long long rows = most / parts;
     if (p.M <= 16 * rows) rows *= 4;
     rows = rows < 1 ? 1 : rows < p.M ? rows : p.M;
-    long long blocks = (rows * parts + kWarps - 1) / kWarps;
-    while (blocks * kWarps % parts) ++blocks;
+    const long long whole = parts / std::gcd(parts, (long long)kWarps);  // blocks whose warps are whole rows
+    const long long blocks = ((rows * parts + kWarps - 1) / kWarps + whole - 1) / whole * whole;
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

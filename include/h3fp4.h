@@ -367,7 +367,8 @@ typedef struct {
  *     out = bf16(y)                                       (rounded once)
  * The pairs are elements (i, i + rot/2), with H3FP4_ROPE_PAIRS (2i, 2i + 1).
  *   q, k: [M][Hq][D] and [M][Hk][D]; k (with k_out) may be NULL.  D % 8 == 0,
- *      8 <= D <= 256.  M >= 0; with no row nothing is launched.
+ *      8 <= D <= 256.  M >= 0; with no row nothing is launched.  Hq, Hk <=
+ *      2^31 - 256.
  *   q_weight, k_weight: fp32 [nseg][D], 16-byte aligned; NULL means all ones.
  *   cos, sin: fp32 [M][rot/2], 16-byte aligned, any angles per row (one, two or
  *      three position axes alike); both NULL with rot = 0.  rot % 16 == 0,
