@@ -298,6 +298,23 @@ struct AttnPlan {
     size_t bytes;        // workspace; 0: more steps than 32 bits count
 };
 
+// The limit of one device wait of a call with this table, from the limit that is
+// set.  Some waits last as long as their unit does, not a step: the epilogue's for
+// a unit's sums, those of a role that has nothing in it, and of all roles while a
+// mask's end is looked for.  Four units may lie between (the pieces described
+// ahead); a tile takes 1.6 us at most and 0.7 us to look for, so 20 us per tile of
+// the longest unit are twice what they add up to.  A fixed limit ran out at units
+// of 1.2 million tiles with the default of 2 s, and sooner with a lower one.
+constexpr uint64_t kWaitNsPerTile = 20000;
+inline uint64_t attn_wait_ns(const AttnTable& t, uint64_t limit_ns)
+{
+    uint64_t longest = 0;
+    for (int e = 0; e < t.entries; ++e)
+        if (t.row_blocks(e) > 0 && (uint64_t)t.tiles(e) > longest) longest = (uint64_t)t.tiles(e);
+    const uint64_t more = longest * kWaitNsPerTile;
+    return limit_ns > UINT64_MAX - more ? UINT64_MAX : limit_ns + more;
+}
+
 // Units, tiles of all of them and of the longest, for one choice of pack and of solo or
 // pair units: with the segments' units walking the context too, and with it apart;
 // the bytes of the context's keys that its units walk then.

@@ -1079,7 +1079,7 @@ cudaError_t launch_attn(const AttnJob& job, const AttnPlan& pl, cudaStream_t s)
         p.slot_rows[k] = pl.slot_rows[k];
     }
     p.status = reinterpret_cast<unsigned int*>(job.ws + kWsStatus);
-    p.wait_ns = job.wait_limit_ns;
+    p.wait_ns = attn_wait_ns(pl.t, job.wait_limit_ns);
     p.stall = job.stall;
     const int chunks = pl.dp / 64;
     p.q_bytes = (uint32_t)(chunks * 128 * pl.t.pack * pl.t.tok);

@@ -437,7 +437,9 @@ H3FP4_API size_t h3fp4_attn_workspace_bytes(int64_t M, int64_t T, int64_t C, int
 H3FP4_API h3fp4_status h3fp4_check(void* ws, cudaStream_t stream);
 
 /* Maximum wait of every device-side spin in nanoseconds (default 2e9).
- * Process-wide; meant for tests of the timeout path. */
+ * Process-wide; meant for tests of the timeout path.  The attention calls, some
+ * of whose waits last as long as a row's whole key axis, add 20 us per 128 keys
+ * of the longest one. */
 H3FP4_API void h3fp4_set_wait_limit_ns(uint64_t ns);
 
 /* Human-readable status. */
