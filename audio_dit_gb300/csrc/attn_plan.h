@@ -147,7 +147,20 @@ struct Piece {
     }
 };
 
-// The pieces of this CTA, in order; every role walks them by itself.  Divisions
+// Leaves out of a piece the tiles behind the last keys that masks keep: of its
+// unit's ctx_tiles + own_tiles tiles the first ctx_keep and own_keep are walked.
+// Tiles are then counted over what is left.
+__host__ __device__ inline void trim_piece(Piece& p, int ctx_keep, int own_keep)
+{
+    const int all = p.ctx_tiles, gone = all - ctx_keep;
+    auto moved = [&](int t) { return t <= ctx_keep ? t : t - gone > ctx_keep ? t - gone : ctx_keep; };
+    const int end = moved(lesser(p.t0 + p.nt, all + own_keep));
+    p.t0 = moved(p.t0);
+    p.nt = end > p.t0 ? end - p.t0 : 0;
+    p.ctx_tiles = ctx_keep;
+}
+
+// The pieces of this CTA, in order; one warp walks them for all roles.  Divisions
 // are done where an entry begins; from piece to piece the state is counted up.
 struct Walk {
     const AttnTable& t;

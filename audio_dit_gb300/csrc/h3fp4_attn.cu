@@ -499,13 +499,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                         own_entry = n.e;
                         own_keep = kept_tiles(p.key_mask + n.kv0, n.kv_len);
                     }
-                    const int all = n.ctx_tiles, ctx = p.ctx_mask != nullptr ? min(all, ctx_keep) : all;
-                    const int own = p.key_mask != nullptr && n.e < p.t.nseg ? own_keep : n.own_tiles;
-                    auto moved = [&](int t) { return t <= ctx ? t : max(ctx, t - (all - ctx)); };
-                    const int end = moved(min(n.t0 + n.nt, all + own));
-                    n.t0 = moved(n.t0);
-                    n.nt = max(0, end - n.t0);
-                    n.ctx_tiles = ctx;
+                    trim_piece(n, p.ctx_mask != nullptr ? min(n.ctx_tiles, ctx_keep) : n.ctx_tiles,
+                               p.key_mask != nullptr && n.e < p.t.nseg ? own_keep : n.own_tiles);
                 }
                 if (lane == 0) {
                     int4* rec = reinterpret_cast<int4*>(smem + L::kPieceOff + slot * 48);
