@@ -129,10 +129,21 @@ struct Piece {
     int t0, nt;
     int ctx_tiles;          // tiles below this index are the context's
     int own_tiles, kv0, kv_len;
+    // set by find_gaps():
     bool gaps_ctx, gaps_own;  // every tile of that source has keys that may be left out (a mask)
     int gap_ctx, gap_own;     // else the tile whose end lies past the source's last key, or -1
     bool whole;             // all steps of the unit
     int slot;               // of the partial sums, if not whole (or separate plan)
+
+    // own_tiles and the gap fields, from the others (the kernel's roles read a piece without them).
+    __host__ __device__ void find_gaps(const AttnTable& t)
+    {
+        own_tiles = (kv_len + kKeyTile - 1) / kKeyTile;
+        gaps_ctx = t.ctx_masked != 0;
+        gaps_own = t.own_masked != 0;
+        gap_ctx = t.ctx_ragged ? ctx_tiles - 1 : -1;  // -1 too where no tile is the context's
+        gap_own = (kv_len & (kKeyTile - 1)) ? ctx_tiles + own_tiles - 1 : -1;
+    }
 
     // Whether tile t of the unit has keys that are left out.
     __host__ __device__ bool has_gaps(int t) const
@@ -230,10 +241,6 @@ struct Walk {
         p.own_tiles = t.tiles_own(e);
         p.kv0 = e < t.nseg ? t.kv_off[e] : 0;
         p.kv_len = e < t.nseg ? t.kv_off[e + 1] - p.kv0 : 0;
-        p.gaps_ctx = t.ctx_masked != 0;
-        p.gaps_own = t.own_masked != 0;
-        p.gap_ctx = t.ctx_ragged && p.ctx_tiles > 0 ? p.ctx_tiles - 1 : -1;
-        p.gap_own = (p.kv_len & (kKeyTile - 1)) ? p.ctx_tiles + p.own_tiles - 1 : -1;
     }
     __host__ __device__ bool next(Piece& p)
     {
@@ -282,13 +289,6 @@ struct Walk {
             }
         }
         return true;
-    }
-    // The same without the units that have no key (only the epilogue sees those).
-    __host__ __device__ bool next_with_keys(Piece& p)
-    {
-        while (next(p))
-            if (p.nt > 0) return true;
-        return false;
     }
 };
 

@@ -16,8 +16,9 @@
 // How units, steps and pieces are cut: attn_plan.h.
 //
 // Roles (512 threads, one CTA per SM):
-//   warp 0       loads: Q tiles (two buffers) and a ring of K and V tiles by TMA,
-//                128-byte swizzled 64-column chunks; columns past D are zero-filled
+//   warp 0       loads: Q tiles (three places, two with solo units) and a ring of K
+//                and V tiles by TMA, 128-byte swizzled 64-column chunks; columns past
+//                D are zero-filled
 //   warps 1, 3   issue the MMAs of query tile A, of tile B.  Per key tile: S_X =
 //                Q_X K^T, then, once the softmax stored P_X over S_X's first
 //                columns (in two halves), O_X += P_X V.  One tile's MMAs run under
@@ -253,11 +254,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         u.head0 = b.x, u.ctx_tiles = b.y, u.kv0 = b.z, u.kv_len = b.w;
         u.slot = c.x, u.e = c.y;
         u.whole = c.x < 0;
-        u.own_tiles = (u.kv_len + kKeyTile - 1) / kKeyTile;
-        u.gaps_ctx = p.t.ctx_masked != 0;
-        u.gaps_own = p.t.own_masked != 0;
-        u.gap_ctx = p.t.ctx_ragged ? u.ctx_tiles - 1 : -1;
-        u.gap_own = (u.kv_len & (kKeyTile - 1)) ? u.ctx_tiles + u.own_tiles - 1 : -1;
+        u.find_gaps(p.t);
         __syncwarp();
         mbar_arrive_if(lane == 0, &piece_empty[slot]);
         return __all_sync(0xffffffffu, ok) && u.nt >= 0;  // -1: no piece is left

@@ -1,6 +1,7 @@
 // Walks the pieces of an attention plan and trims them to the tiles that masks keep
 // (trim_piece), as the kernel's describing warp does, and checks that each unit's
-// kept tiles are walked exactly once, in the numbering that is left.  Input lines:
+// kept tiles are walked exactly once, in the numbering that is left; and which tiles
+// of an untrimmed piece have keys that are left out (find_gaps).  Input lines:
 // M T C Hq Hkv D nseg q_off... kv_off... ctx_keep own_keep...; prints "ok" or what
 // is wrong.
 #define __host__
@@ -47,6 +48,37 @@ static const char* check(const Job& job, int ctx_keep, const std::vector<int>& o
     return nullptr;
 }
 
+static const char* check_gaps(const Job& job)
+{
+    AttnPlan pl = make_plan(job);
+    for (int masks = 0; masks < 4; ++masks) {
+        pl.t.ctx_masked = masks & 1;
+        pl.t.own_masked = masks >> 1;
+        for (int c = 0; c < pl.t.ctas; ++c) {
+            Walk w(pl.t);
+            w.start(c);
+            Piece p;
+            while (w.next(p)) {
+                p.own_tiles = -1;
+                p.find_gaps(pl.t);
+                const int all = p.ctx_tiles + p.own_tiles;
+                if (p.own_tiles != (p.kv_len + 127) / 128 || p.t0 + p.nt > all) return "own tiles";
+                int n = 0;
+                for (int t = p.t0; t < p.t0 + p.nt; ++t) {
+                    const bool ctx = t < p.ctx_tiles;
+                    const long long end = ctx ? 128LL * (t + 1) : 128LL * (t - p.ctx_tiles + 1);
+                    const bool want = ctx ? (masks & 1) || end > job.C : (masks >> 1) || end > p.kv_len;
+                    if (p.gaps_before(t) != n) return "gaps before a tile";
+                    if (p.has_gaps(t) != want) return "tiles with gaps";
+                    n += want;
+                }
+                if (p.gaps_before(p.t0 + p.nt) != n) return "gaps of a piece";
+            }
+        }
+    }
+    return nullptr;
+}
+
 int main()
 {
     long long M, T, C;
@@ -65,6 +97,7 @@ int main()
         for (int& x : own)
             if (std::scanf("%d", &x) != 1) return 1;
         const char* bad = check(job, ctx, own);
+        if (!bad) bad = check_gaps(job);
         std::printf("%s\n", bad ? bad : "ok");
     }
     return 0;
