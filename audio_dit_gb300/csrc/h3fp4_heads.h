@@ -11,6 +11,7 @@ namespace h3fp4 {
 
 constexpr int kNormMaxD = 256;
 constexpr int kAttnMaxD = 128;
+constexpr float kLog2E = 1.4426950408889634f;
 
 // One of the tensors the norm runs over.
 struct NormTensor {

@@ -106,7 +106,8 @@ h3fp4_status attn(const h3fp4_heads* q, const h3fp4_heads* k, const h3fp4_heads*
     int64_t one_q[2], one_kv[2];
     h3fp4_status st = attn_sizes(M, T, C, Hq, Hkv, D, q_off, kv_off, nseg, one_q, one_kv, &job);
     if (st != H3FP4_OK) return st;
-    if (!(scale > 0.0f) || std::isinf(scale)) return H3FP4_ERR_INVALID;
+    // (the kernel's exponents are in base 2)
+    if (!(scale > 0.0f) || std::isinf(scale * kLog2E)) return H3FP4_ERR_INVALID;
     if ((st = check_in(q, M)) != H3FP4_OK || (st = check_in(k, T)) != H3FP4_OK || (st = check_in(v, T)) != H3FP4_OK ||
         (st = check_in(kc, C)) != H3FP4_OK || (st = check_in(vc, C)) != H3FP4_OK ||
         (st = check_out(out, M, Hq, D)) != H3FP4_OK)

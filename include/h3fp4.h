@@ -398,7 +398,7 @@ H3FP4_API h3fp4_status h3fp4_qk_norm_rope(const h3fp4_heads* q, const h3fp4_head
  *      1 <= nseg <= H3FP4_ATTN_MAX_SEGMENTS.
  *   key_mask: T bytes (device), 0 = the key is left out; NULL keeps all.  What
  *      K and V hold at a key that is left out does not matter (NaN, infinities).
- *   scale > 0, finite.
+ *   scale > 0, scale * log2(e) finite.
  *   A row without a key (an empty segment, a mask that leaves nothing, or only
  *   scores of -inf) gives out = 0 and lse = -inf.
  *   lse: fp32 [M][Hq], 4-byte aligned, log(sum_j exp(scale q_r . k_j)); may be NULL.
