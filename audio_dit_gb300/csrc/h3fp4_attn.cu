@@ -761,7 +761,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                     }
                 };
-                const float inv = sum == 0.0f ? 0.0f : rcp_approx(sum);  // a row without a key: zeros
+                // a row without a key: zeros (scores past fp32's range leave no sum either: NaN)
+                const bool none = sum == 0.0f && top == -INFINITY;
+                const float inv = none ? 0.0f : rcp_approx(sum);
                 const uint64_t f = f2(inv, inv);
                 const int kind = u.e < p.t.nseg ? 0 : 1, rows = p.slot_rows[kind];
                 float* base = p.part[kind] + (long long)u.slot * rows * (DP + 2);
@@ -770,9 +772,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 __nv_bfloat16* o = p.out + r * p.out_row + (long long)h * p.out_head;
                 if (on && !u.whole)
                     *reinterpret_cast<float2*>(base + (long long)rows * DP + 2 * at) =
-                        make_float2(sum == 0.0f ? -INFINITY : top2, sum);
+                        make_float2(none ? -INFINITY : top2, sum);
                 if (on && u.whole && p.lse)
-                    p.lse[r * p.Hq + h] = sum == 0.0f ? -INFINITY : (top2 + __log2f(sum)) * 0.69314718055994531f;
+                    p.lse[r * p.Hq + h] = none ? -INFINITY : (top2 + __log2f(sum)) * 0.69314718055994531f;
                 auto release = [&]() {
                     tc_fence_before();
                     __syncwarp();
@@ -907,13 +909,14 @@ __device__ __forceinline__ void join_row(const JoinOut& p, int r, int h, int col
             for (int j = 0; j < 8; ++j) acc[j] = some ? fmaf(v[j], w, acc[j]) : acc[j];
         }
     }
-    const float inv = l == 0.0f ? 0.0f : rcp_approx(l);
+    const bool none = l == 0.0f && m == -INFINITY;
+    const float inv = none ? 0.0f : rcp_approx(l);
     if (col < p.D)  // D is a multiple of 8
         *reinterpret_cast<uint4*>(p.out + (long long)r * p.out_row + (long long)h * p.out_head + col) =
             make_uint4(cvt_bf16x2(f2(acc[0] * inv, acc[1] * inv)), cvt_bf16x2(f2(acc[2] * inv, acc[3] * inv)),
                        cvt_bf16x2(f2(acc[4] * inv, acc[5] * inv)), cvt_bf16x2(f2(acc[6] * inv, acc[7] * inv)));
     if (p.lse && col == 0)
-        p.lse[(long long)r * p.Hq + h] = l == 0.0f ? -INFINITY : (m + __log2f(l)) * 0.69314718055994531f;
+        p.lse[(long long)r * p.Hq + h] = none ? -INFINITY : (m + __log2f(l)) * 0.69314718055994531f;
 }
 
 // This thread's row of the block's unit, and its first column.
@@ -1058,7 +1061,7 @@ cudaError_t launch_attn(const AttnJob& job, const AttnPlan& pl, cudaStream_t s)
     p.C = (int)job.C;
     p.key_mask = job.key_mask;
     p.ctx_mask = job.ctx_mask;
-    p.scale_log2 = job.scale * 1.4426950408889634f;
+    p.scale_log2 = job.scale * kLog2E;
     p.growth = fminf(kGrowth / p.scale_log2, 1e38f);  // finite: -inf plus it stays -inf
     p.out = job.out;
     p.out_row = job.out_row;

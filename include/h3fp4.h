@@ -398,7 +398,8 @@ H3FP4_API h3fp4_status h3fp4_qk_norm_rope(const h3fp4_heads* q, const h3fp4_head
  *      1 <= nseg <= H3FP4_ATTN_MAX_SEGMENTS.
  *   key_mask: T bytes (device), 0 = the key is left out; NULL keeps all.  What
  *      K and V hold at a key that is left out does not matter (NaN, infinities).
- *   scale > 0, scale * log2(e) finite.
+ *   scale > 0, scale * log2(e) finite.  Where scale * log2(e) * (q_r . k_j) of a
+ *      row's largest score passes fp32's range, the row is NaN.
  *   A row without a key (an empty segment, a mask that leaves nothing, or only
  *   scores of -inf) gives out = 0 and lse = -inf.
  *   lse: fp32 [M][Hq], 4-byte aligned, log(sum_j exp(scale q_r . k_j)); may be NULL.
