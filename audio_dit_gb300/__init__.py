@@ -433,8 +433,9 @@ def h3fp4_qk_norm_rope(q: torch.Tensor, k: Optional[torch.Tensor], q_out: torch.
                        k_weight: Optional[torch.Tensor] = None, cos: Optional[torch.Tensor] = None,
                        sin: Optional[torch.Tensor] = None, interleaved: bool = False,
                        seg_off: Optional[Sequence[int]] = None, eps: float = 1e-6, stream=None) -> None:
-    """Per-head RMS norm and rotation of Q [M, Hq, D] and K [M, Hk, D] (bf16, any
-    row and head strides; ``k`` and ``k_out`` may be None) in one pass.
+    """Per-head RMS norm and rotation of Q [M, Hq, D] and K [M, Hk, D] (bf16, row
+    and head strides positive multiples of 8; ``k`` and ``k_out`` may be None) in
+    one pass.
 
     ``q_weight`` / ``k_weight``: fp32 [nseg, D]; ``cos`` / ``sin``: fp32
     [M, rot/2].  The rotated pairs are (i, i + rot/2), or (2i, 2i + 1) with
@@ -461,8 +462,9 @@ def h3fp4_cross_attn(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, out: tor
                      q_off: Optional[Sequence[int]] = None, kv_off: Optional[Sequence[int]] = None,
                      key_mask: Optional[torch.Tensor] = None, scale: Optional[float] = None,
                      lse: Optional[torch.Tensor] = None, stream=None) -> None:
-    """out [M, Hq, D] = attention of q [M, Hq, D] to k, v [T, Hkv, D] (bf16, any
-    row and head strides), segment by segment of ``q_off`` / ``kv_off``.
+    """out [M, Hq, D] = attention of q [M, Hq, D] to k, v [T, Hkv, D] (bf16; row and
+    head strides are positive multiples of 8, so shared key heads are given once
+    and not expanded), segment by segment of ``q_off`` / ``kv_off``.
 
     ``key_mask``: bool or uint8 [T], False / 0 leaves a key out; ``scale``
     defaults to 1/sqrt(D); ``lse``: fp32 [M, Hq], also written.  ``ws`` from

@@ -24,7 +24,8 @@
 // the other, the units of a head would walk the same keys at different times and
 // each read them from memory.  There the pool holds one row of steps per head,
 // and a stretch goes to `lanes` CTAs side by side, one per unit of the head
-// (1024 rows over 30720 keys, 24 heads: 247 us against 282).
+// (1024 rows over 30720 keys, 24 heads, caches flushed: 247 us against 282 when it
+// came in, 244 now).
 #pragma once
 #include <cstddef>
 #include <cstdint>
@@ -34,8 +35,11 @@
 namespace h3fp4 {
 
 constexpr int kKeyTile = 128;
-constexpr int kAttnCtas = 152;   // one per SM of the GB300
-constexpr int kSnap = 4;         // 2 and 8 measured 0 and 1 % slower on 16384 rows over 9216 keys
+constexpr int kAttnCtas = 152;   // one per SM of the GB300; on a device with fewer the last ones run alone
+// 2 and 8 measured 0 and 1 % slower on 16384 rows over 9216 keys, where a CTA has 728 steps.
+// At few steps a CTA it makes stretches uneven (4500 ragged rows, 19 steps on average: the
+// fullest CTA has 24 with it, 22 with 2); that was not timed.
+constexpr int kSnap = 4;
 // What a unit costs beside its tiles, in steps: one of the pair plan's, three of the solo
 // plan's, which are about half as long; a unit without keys one more.  9001 masked rows over
 // six prompts, one without keys (pair; unit and empty unit): 0 and 1 69 us, 0 and 2 72, 1 and
@@ -354,10 +358,15 @@ inline Cost cost_of(const Job& job, const AttnTable& t, int pack, bool solo)
                 4.0 * job.D * (double)job.C * (double)(apart * hb)};
 }
 
-// The time of a plan in steps of a pair unit (1.35 us at heads of 128): a tile of a solo
-// unit takes 0.52, its ends 1.45 (a pair's 1); cutting costs a piece's end, the partials'
-// way through memory and a second kernel, 13 us (pair) or 11 us (solo, half the rows).
-// Measured, 24 heads of 128, calls back to back, us (the smallest is what is taken):
+// The time of a plan in steps of a pair unit (1.35 us at heads of 128 in short calls, 1.6 in
+// long ones): a tile of a solo unit takes 0.52, its ends 1.45 (a
+// pair's 1); cutting costs a piece's end, the partials' way through memory and a second
+// kernel, 13 us (pair) or 11 us (solo, half the rows).  Two things it leaves out: units of
+// one to three tiles take longer than this counts (9001 rows over six prompts: 26 steps on
+// the fullest CTA, 57 us), and whole units are dealt out by steps, so that where their
+// lengths differ a CTA may hold two and another none (`dealt` counts one a wave): 5 and 4
+// rows over 1647 and 2090 keys 26.5 us, over 2090 each 17.8.
+// Measured, 24 heads of 128, bursts of calls back to back, us (the smallest is what is taken):
 //     rows x keys      pair, cut   pair, whole   solo, cut   solo, whole
 //     256 x 4096            26.9          50.4        22.6          29.9
 //     512 x 2048            27.0          29.0        23.7          19.1
@@ -372,7 +381,8 @@ inline Cost cost_of(const Job& job, const AttnTable& t, int pack, bool solo)
 //     24 of 64, 20 x 20 over 12000                       75.8, 78.9
 //     24 of 128, 20 x 20 over 12000                      93.0, 120.9
 // The last one's keys do not stay in L2 from one of a head's units to the next, and solo
-// units are twice as many: hence the term with the bytes where all heads' keys exceed 96 MB.
+// units are twice as many: hence the term with the bytes where all heads' keys exceed 96 MB
+// (its two constants are fitted to that case alone).
 struct PlanTime {
     double cut, whole, apart;
 };

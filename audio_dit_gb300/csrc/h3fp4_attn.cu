@@ -39,9 +39,10 @@
 // With heads of 64 the softmax warpgroups' latency is what is left (2490 a step,
 // 1024 of them MMAs).  A unit's ends cost about one step more.  Kernel time with
 // flushed caches: 2 x 8192 rows over 1024 shared and 8192 own keys, 24 heads of
-// 128: 1062 us (1.75 PFLOP/s); 30720 rows over 512 keys: 150 us (1.29 PFLOP/s);
-// 1024 rows over 30720 keys: 242 us (1.60 PFLOP/s); one row over 32768 keys, 32
-// heads over 8: 46 us (35 of them this kernel, 3.8 TB/s).
+// 128: 1068 us (1.74 PFLOP/s); 31744 rows over as many keys: 7.36 ms (1.68 PFLOP/s);
+// 30720 rows over 512 keys: 152 us (1.27 PFLOP/s); 1024 rows over 30720 keys: 244 us
+// (1.58 PFLOP/s); one row over 32768 keys, 32 heads over 8: 46 us (35 of them this
+// kernel, 3.8 TB/s).
 //
 // Every wait is bounded; a role that gives up records it in the status word and
 // leaves, and so do the roles that depend on it.
@@ -468,7 +469,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             uint32_t described = 0;
             bool ok = true, left = true;
             int ctx_keep = -1, own_keep = 0, own_entry = -1;
-            // Key tiles up to the last key that a mask of n bytes keeps.
+            // Key tiles up to the last key that a mask of n bytes keeps. One tile after the other,
+            // 0.3 us each, in every CTA: a long tail costs more than its tiles would, spread over
+            // all CTAs (one row over 32768 keys: 32 us without a mask, 34 with all kept, 101 with
+            // 1000 kept; 1024 rows over 4096: 58 with all kept, 51 with half).
             auto kept_tiles = [&](const uint8_t* mask, int n) {
                 int tile = (n + kKeyTile - 1) / kKeyTile;
                 for (bool some = false; tile > 0 && !some; tile -= some ? 0 : 1) {

@@ -1,7 +1,7 @@
 """The attention half of a joint video/audio block, from the modulated rows to the gated residual.
 
 Two samples of one prompt are packed one after the other; every row attends to the prompt's states (stored once, shared
-by the samples) and to all rows of its own sample, then the audio rows attend to a second encoder's states:
+by the samples) and to all rows of its own sample, and its queries to a second encoder's states as well:
 
     qkv   = NVFP4 linear of the modulated rows                    h3fp4_linear
     q, k  = per-head norm and rotation, in place on qkv's views    h3fp4_qk_norm_rope

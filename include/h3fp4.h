@@ -61,9 +61,11 @@
  *   - The GEMM runs as clusters of two CTAs (512 threads, ~228 KB of shared
  *     memory and all 512 TMEM columns each), one CTA per SM, over every SM
  *     pair that can be co-resident.
- *   - The attention calls run one CTA per SM (512 threads, ~227 KB of shared
- *     memory, all 512 TMEM columns) and a small second kernel where a row's
- *     keys were divided over CTAs.  Results do not depend on timing: the same
+ *   - The attention calls run up to 152 CTAs, one per SM of the GB300 (512
+ *     threads, ~227 KB of shared memory, all 512 TMEM columns), and a small second
+ *     kernel where a row's keys were divided over CTAs.  On an sm_103 device with
+ *     another number of SMs they are right, but cut for 152 (fewer SMs run the
+ *     last CTAs alone, more stay idle).  Results do not depend on timing: the same
  *     call gives the same bits.
  *   - Calls issue only kernel launches and (with H3FP4_EPI_AMAX) one memset
  *     on `stream`, so a fixed sequence of calls can be captured into a CUDA
@@ -374,7 +376,9 @@ typedef struct {
  *      three position axes alike); both NULL with rot = 0.  rot % 16 == 0,
  *      rot <= D.
  *   seg_off, nseg: as in h3fp4_quantize_act (weights per modality).
- *   eps >= 0.  A row of zeros with eps = 0 gives NaN, as the formula does.
+ *   eps >= 0.  A row of zeros with eps = 0 gives NaN, as the formula does.  The
+ *      sum of squares is fp32's: heads with elements of 1e18 and more, or, with
+ *      eps = 0, all below 1e-18, leave its range.
  *   q_out, k_out: outputs; either may be the very tensor it is computed from
  *      (same ptr and strides), otherwise no output may overlap an input. */
 H3FP4_API h3fp4_status h3fp4_qk_norm_rope(const h3fp4_heads* q, const h3fp4_heads* k, int64_t M, int Hq, int Hk,
@@ -407,7 +411,9 @@ H3FP4_API h3fp4_status h3fp4_qk_norm_rope(const h3fp4_heads* q, const h3fp4_head
  *   ws: device workspace of at least h3fp4_attn_workspace_bytes(...) bytes
  *      (ws_bytes is checked), first 256 bytes zeroed once before first use;
  *      h3fp4_check(ws) reports device waits that timed out.  Concurrent calls
- *      must not share one workspace. */
+ *      must not share one workspace, nor an attention call one with
+ *      H3FP4_FUSED_QUANT calls (partial sums would lie where these keep their
+ *      ready flags). */
 H3FP4_API h3fp4_status h3fp4_cross_attn(const h3fp4_heads* q, const h3fp4_heads* k, const h3fp4_heads* v, int64_t M,
                                         int64_t T, int Hq, int Hkv, int D, const int64_t* q_off,
                                         const int64_t* kv_off, int nseg, const uint8_t* key_mask, float scale,
