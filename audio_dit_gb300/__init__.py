@@ -26,6 +26,7 @@ __all__ = [
     "h3fp4_linear_swiglu_nvfp4", "h3fp4_qk_norm_rope", "h3fp4_cross_attn", "h3fp4_shared_attn",
     "h3fp4_attn_workspace_bytes", "alloc_attn_workspace", "h3fp4_selftest_attn_timeout", "ROPE_PAIRS", "ATTN_MAX_SEGMENTS",
     "h3fp4_set_wait_limit_ns", "h3fp4_status_string", "alloc_nvfp4", "alloc_workspace",
+    "h3fp4_block_norm", "NORM_POST", "NORM_LAYER", "CAUSAL",
 ]
 
 PROLOGUE_MOD = 1
@@ -37,6 +38,9 @@ EPI_SWIGLU = 64
 EPI_AMAX = 128
 FUSED_QUANT = 256
 ROPE_PAIRS = 512
+NORM_POST = 1024
+NORM_LAYER = 2048
+CAUSAL = 4096
 MAX_SEGMENTS = 8
 ATTN_MAX_SEGMENTS = 256
 
@@ -96,6 +100,8 @@ def load_library():
                                     hp, vp, vp, sz, vp]),
         "h3fp4_attn_workspace_bytes": (sz, [i64, i64, i64, i32, i32, i32, vp, vp, i32]),
         "h3fp4_selftest_attn_timeout": (i32, [vp, C.c_uint64, vp]),
+        "h3fp4_block_norm": (i32, [vp, vp, i64, i64, vp, vp, C.c_float, vp, vp, vp, vp, i32, C.c_float, vp, vp, vp, i32,
+                                   vp]),
         "h3fp4_check": (i32, [vp, vp]),
         "h3fp4_set_wait_limit_ns": (None, [C.c_uint64]),
         "h3fp4_status_string": (C.c_char_p, [i32]),
@@ -188,6 +194,15 @@ def _f32(t: Optional[torch.Tensor], what: str, shape):
     if isinstance(t, torch.Tensor) and t.dtype is _F32 and t.shape == shape and t.is_cuda and t.is_contiguous():
         return t.data_ptr()
     _ptr(t, what, _F32)
+    raise ValueError(f"{what} must be {list(shape)}, got {list(t.shape)}")
+
+
+def _bf16(t: Optional[torch.Tensor], what: str, shape):
+    if t is None:
+        return None
+    if isinstance(t, torch.Tensor) and t.dtype is _BF16 and t.shape == shape and t.is_cuda and t.is_contiguous():
+        return t.data_ptr()
+    _ptr(t, what, _BF16)
     raise ValueError(f"{what} must be {list(shape)}, got {list(t.shape)}")
 
 
@@ -507,6 +522,29 @@ def h3fp4_attn_workspace_bytes(M: int, T: int, Hq: int, Hkv: int, D: int, q_off:
                                kv_off: Optional[Sequence[int]] = None, ctx: int = 0) -> int:
     qp, kp, nseg, _keep = _seg_pair(q_off, kv_off)
     return int(load_library().h3fp4_attn_workspace_bytes(M, T, ctx, Hq, Hkv, D, qp, kp, nseg))
+
+
+def h3fp4_block_norm(x: torch.Tensor, out: Optional[torch.Tensor] = None, *, y: Optional[torch.Tensor] = None,
+                     x_out: Optional[torch.Tensor] = None, gate: Optional[torch.Tensor] = None,
+                     y_weight: Optional[torch.Tensor] = None, x_scale: float = 1.0,
+                     weight: Optional[torch.Tensor] = None, shift: Optional[torch.Tensor] = None,
+                     scale: Optional[torch.Tensor] = None, seg_off: Optional[Sequence[int]] = None,
+                     eps: float = 1e-6, post_norm: bool = False, layer_norm: bool = False,
+                     out_amax: Optional[torch.Tensor] = None, stream=None) -> None:
+    """The norms around a block with its gate and residual, one pass over the rows of bf16 [M, K]:
+
+    ``r = x_scale * x + gate * y'`` into ``x_out``, with ``y' = y`` or (``post_norm``) its RMS norm times
+    ``y_weight``; the RMS norm of r (``layer_norm``: its layer norm) times ``weight``, modulated by ``1 + scale`` and
+    ``shift``, into ``out``.  The vectors are fp32 [nseg, K], each may be None; without ``y`` r is x.  ``out_amax``:
+    fp32 [1], receives max|out|.  An output may be its own input."""
+    M, K = shape = x.shape
+    keep, sp, nseg = _table(seg_off)
+    vec = (nseg, K)
+    _check(load_library().h3fp4_block_norm(
+        _bf16(x, "x", shape), _bf16(y, "y", shape), M, K, _f32(y_weight, "y_weight", vec), _f32(gate, "gate", vec),
+        x_scale, _f32(weight, "weight", vec), _f32(shift, "shift", vec), _f32(scale, "scale", vec), sp, nseg, eps,
+        _bf16(x_out, "x_out", shape), _bf16(out, "out", shape), _f32(out_amax, "out_amax", (1,)),
+        (NORM_POST if post_norm else 0) | (NORM_LAYER if layer_norm else 0), _stream(stream)), "h3fp4_block_norm")
 
 
 def h3fp4_check(ws: torch.Tensor, stream=None) -> None:

@@ -109,7 +109,10 @@ enum {
     H3FP4_EPI_SWIGLU = 64,     /* out[M][N/2] = bf16(silu(g) * u), see h3fp4_linear                */
     H3FP4_EPI_AMAX = 128,      /* also write max|out| to h3fp4_ws_out_amax(ws)                    */
     H3FP4_FUSED_QUANT = 256,   /* quantise x inside the GEMM kernel, see h3fp4_linear              */
-    H3FP4_ROPE_PAIRS = 512     /* rotate adjacent pairs (2i, 2i+1), see h3fp4_qk_norm_rope         */
+    H3FP4_ROPE_PAIRS = 512,    /* rotate adjacent pairs (2i, 2i+1), see h3fp4_qk_norm_rope         */
+    H3FP4_NORM_POST = 1024,    /* RMS norm of a block's output, see h3fp4_block_norm                */
+    H3FP4_NORM_LAYER = 2048,   /* layer norm instead of RMS norm, see h3fp4_block_norm              */
+    H3FP4_CAUSAL = 4096        /* a row attends up to its own position, see h3fp4_cache_attn        */
 };
 
 #define H3FP4_MAX_SEGMENTS 8
@@ -436,6 +439,35 @@ H3FP4_API h3fp4_status h3fp4_shared_attn(const h3fp4_heads* q, const h3fp4_heads
  * sizes; 0 for sizes and tables those calls refuse.  No device access. */
 H3FP4_API size_t h3fp4_attn_workspace_bytes(int64_t M, int64_t T, int64_t C, int Hq, int Hkv, int D,
                                             const int64_t* q_off, const int64_t* kv_off, int nseg);
+
+/* The norms around a block with its gate and residual, one pass over the rows
+ * ("H3 Runtime Current State", "Implemented And Validated": fused modulation and
+ * residual gates; "H3 Blackwell Runtime Plan": residual, norms, modulation and adds
+ * stay BF16).  For each row, in fp32:
+ *     y' = y * rsqrt(mean(y^2) + eps) * y_weight[seg]      with H3FP4_NORM_POST, else y' = y
+ *     r  = x_scale * x + gate[seg] * y'                     x_out = bf16(r)
+ *     z  = r * rsqrt(mean(r^2) + eps), with H3FP4_NORM_LAYER
+ *          (r - mean(r)) * rsqrt(mean((r - mean(r))^2) + eps)
+ *     out = bf16(z * weight[seg] * (1 + scale[seg]) + shift[seg])
+ * Each output is rounded once (the norm goes over r, not over x_out).
+ *   x, y, x_out, out: bf16 [M][K], M >= 0, K % 8 == 0, 8 <= K <= 32768.
+ *      Without y (NULL), r = x: no x_out, gate, y_weight or H3FP4_NORM_POST then, and
+ *      x_scale means nothing.  x_out may be NULL; out may be NULL, with no
+ *      weight, shift, scale, out_amax or H3FP4_NORM_LAYER then.  An output may be
+ *      one of the inputs itself (in place); otherwise nothing may overlap.
+ *   y_weight, gate, weight, shift, scale: fp32 [nseg][K], 16-byte aligned, each may
+ *      be NULL (ones, ones, ones, zeros, zeros).
+ *   seg_off, nseg: as in h3fp4_quantize_act.
+ *   eps >= 0.  A row of zeros with eps = 0 gives NaN, as the formula does.  Sums of
+ *      squares are fp32's: rows with elements of 1e17 and more leave its range.
+ *   out_amax: device fp32 or NULL, receives max |out| (0 without rows): with
+ *      h3fp4_gscale_from_amax and H3FP4_GSCALE_GIVEN the linear that follows
+ *      quantises out in one pass. */
+H3FP4_API h3fp4_status h3fp4_block_norm(const void* x_bf16, const void* y_bf16, int64_t M, int64_t K,
+                                        const float* y_weight, const float* gate, float x_scale, const float* weight,
+                                        const float* shift, const float* scale, const int64_t* seg_off, int nseg,
+                                        float eps, void* x_out_bf16, void* out_bf16, float* out_amax, int flags,
+                                        cudaStream_t stream);
 
 /* Synchronises `stream`, reads and clears the workspace status word.
  * Returns H3FP4_OK, or H3FP4_ERR_TIMEOUT when a kernel gave up early (a
