@@ -26,7 +26,9 @@ __all__ = [
     "h3fp4_linear_swiglu_nvfp4", "h3fp4_qk_norm_rope", "h3fp4_cross_attn", "h3fp4_shared_attn",
     "h3fp4_attn_workspace_bytes", "alloc_attn_workspace", "h3fp4_selftest_attn_timeout", "ROPE_PAIRS", "ATTN_MAX_SEGMENTS",
     "h3fp4_set_wait_limit_ns", "h3fp4_status_string", "alloc_nvfp4", "alloc_workspace",
-    "h3fp4_block_norm", "NORM_POST", "NORM_LAYER", "CAUSAL",
+    "h3fp4_block_norm", "NORM_POST", "NORM_LAYER", "CAUSAL", "h3fp4_cache_append", "h3fp4_cache_read",
+    "h3fp4_cache_attn", "h3fp4_cache_page_bytes", "h3fp4_cache_attn_workspace_bytes", "alloc_kv_cache",
+    "alloc_cache_attn_workspace", "h3fp4_selftest_cache_attn_timeout",
 ]
 
 PROLOGUE_MOD = 1
@@ -102,6 +104,12 @@ def load_library():
         "h3fp4_selftest_attn_timeout": (i32, [vp, C.c_uint64, vp]),
         "h3fp4_block_norm": (i32, [vp, vp, i64, i64, vp, vp, C.c_float, vp, vp, vp, vp, i32, C.c_float, vp, vp, vp, i32,
                                    vp]),
+        "h3fp4_cache_page_bytes": (sz, [i32, i32, i32]),
+        "h3fp4_cache_append": (i32, [hp, hp, i64, vp, vp]),
+        "h3fp4_cache_read": (i32, [hp, hp, i64, vp, vp]),
+        "h3fp4_cache_attn": (i32, [hp, i64, i32, vp, C.c_float, hp, vp, i32, vp, sz, vp]),
+        "h3fp4_cache_attn_workspace_bytes": (sz, [i32]),
+        "h3fp4_selftest_cache_attn_timeout": (i32, [vp, C.c_uint64, vp]),
         "h3fp4_check": (i32, [vp, vp]),
         "h3fp4_set_wait_limit_ns": (None, [C.c_uint64]),
         "h3fp4_status_string": (C.c_char_p, [i32]),
@@ -547,6 +555,101 @@ def h3fp4_block_norm(x: torch.Tensor, out: Optional[torch.Tensor] = None, *, y: 
         (NORM_POST if post_norm else 0) | (NORM_LAYER if layer_norm else 0), _stream(stream)), "h3fp4_block_norm")
 
 
+def _i32(t: Optional[torch.Tensor], what: str, shape):
+    if t is None:
+        return 0
+    if isinstance(t, torch.Tensor) and t.dtype is torch.int32 and t.shape == shape and t.is_cuda and t.is_contiguous():
+        return t.data_ptr()
+    _ptr(t, what, torch.int32)
+    raise ValueError(f"{what} must be {list(shape)}, got {list(t.shape)}")
+
+
+def _cache_width(D: int) -> int:
+    return 64 if D <= 64 else 128 if D <= 128 else 256
+
+
+def _cache(cache: torch.Tensor, table: torch.Tensor, length: torch.Tensor, row_off: Optional[torch.Tensor], M: int,
+           D: int, k_gscale: Optional[torch.Tensor], v_gscale: Optional[torch.Tensor]):
+    """The fields of an h3fp4_cache, and its number of heads."""
+    at = _ptr(cache, "cache", torch.uint8)
+    if cache.dim() != 4 or cache.shape[3] != _cache_width(D) * 9 // 8:
+        raise ValueError(f"cache must be [pages, heads, page, {_cache_width(D) * 9 // 8}] for heads of {D}, got "
+                         f"{list(cache.shape)}")
+    n_pages, heads, page, _ = cache.shape
+    if not isinstance(table, torch.Tensor) or table.dim() != 2:
+        raise ValueError("table must be an int32 tensor [nseq, max_pages]")
+    nseq, max_pages = table.shape
+    if row_off is None and nseq != M:
+        raise ValueError(f"without row_off there is one row per sequence: {M} rows, {nseq} sequences")
+    return (at, n_pages, page, heads, D, _i32(table, "table", (nseq, max_pages)), max_pages,
+            _i32(length, "length", (nseq,)), _i32(row_off, "row_off", (nseq + 1,)), nseq,
+            _f32(k_gscale, "k_gscale", (heads,)) or 0, _f32(v_gscale, "v_gscale", (heads,)) or 0), heads
+
+
+def _cache_rows(name: str, k, v, cache, table, length, row_off, k_gscale, v_gscale, stream):
+    M, heads, D = k.shape
+    fields, held = _cache(cache, table, length, row_off, M, D, k_gscale, v_gscale)
+    if heads != held:
+        raise ValueError(f"cache holds {held} heads, the rows have {heads}")
+    a = array("q", (*_heads(k, "k", M, heads, D), *_heads(v, "v", M, heads, D), *fields))
+    at = a.buffer_info()[0]
+    _check(getattr(load_library(), name)(at, at + 24, M, at + 48, _stream(stream)), name)
+
+
+def h3fp4_cache_append(k: torch.Tensor, v: torch.Tensor, cache: torch.Tensor, table: torch.Tensor,
+                       length: torch.Tensor, row_off: Optional[torch.Tensor] = None, *,
+                       k_gscale: Optional[torch.Tensor] = None, v_gscale: Optional[torch.Tensor] = None,
+                       stream=None) -> None:
+    """Write the rows ``k``, ``v`` [M, heads, D] (bf16 views) to their places in a paged 4-bit ``cache`` of
+    :func:`alloc_kv_cache`.
+
+    ``table`` int32 [nseq, max_pages]: the pages of each sequence; ``length`` int32 [nseq]: its tokens, with the new
+    ones; ``row_off`` int32 [nseq + 1]: which rows are its last ones (None: row s is sequence s's).  All on the device,
+    read when the call runs.  ``k_gscale`` / ``v_gscale``: fp32 [heads]."""
+    _cache_rows("h3fp4_cache_append", k, v, cache, table, length, row_off, k_gscale, v_gscale, stream)
+
+
+def h3fp4_cache_read(k: torch.Tensor, v: torch.Tensor, cache: torch.Tensor, table: torch.Tensor, length: torch.Tensor,
+                     row_off: Optional[torch.Tensor] = None, *, k_gscale: Optional[torch.Tensor] = None,
+                     v_gscale: Optional[torch.Tensor] = None, stream=None) -> None:
+    """The way back of :func:`h3fp4_cache_append`: the rows' places as bf16 into ``k``, ``v``."""
+    _cache_rows("h3fp4_cache_read", k, v, cache, table, length, row_off, k_gscale, v_gscale, stream)
+
+
+def h3fp4_cache_attn(q: torch.Tensor, cache: torch.Tensor, table: torch.Tensor, length: torch.Tensor, out: torch.Tensor,
+                     ws: torch.Tensor, *, row_off: Optional[torch.Tensor] = None,
+                     k_gscale: Optional[torch.Tensor] = None, v_gscale: Optional[torch.Tensor] = None,
+                     causal: bool = True, scale: Optional[float] = None, lse: Optional[torch.Tensor] = None,
+                     stream=None) -> None:
+    """out [M, Hq, D] = attention of the rows q [M, Hq, D] to the cached keys and values of their sequences
+    (arguments as in :func:`h3fp4_cache_append`), up to each row's own position with ``causal``, else to all.
+
+    ``scale`` defaults to 1/sqrt(D); ``lse``: fp32 [M, Hq], also written.  ``ws`` from
+    :func:`alloc_cache_attn_workspace`."""
+    M, Hq, D = q.shape
+    fields, _ = _cache(cache, table, length, row_off, M, D, k_gscale, v_gscale)
+    a = array("q", (*_heads(q, "q", M, Hq, D), *_heads(out, "out", M, Hq, D), *fields))
+    at = a.buffer_info()[0]
+    _check(load_library().h3fp4_cache_attn(
+        at, M, Hq, at + 48, D ** -0.5 if scale is None else scale, at + 24, _f32(lse, "lse", (M, Hq)),
+        CAUSAL if causal else 0, _workspace(ws), ws.numel(), _stream(stream)), "h3fp4_cache_attn")
+
+
+def h3fp4_cache_page_bytes(heads: int, D: int, page: int) -> int:
+    return int(load_library().h3fp4_cache_page_bytes(heads, D, page))
+
+
+def h3fp4_cache_attn_workspace_bytes(D: int) -> int:
+    return int(load_library().h3fp4_cache_attn_workspace_bytes(D))
+
+
+def h3fp4_selftest_cache_attn_timeout(ws: torch.Tensor, limit_ns: int, stream=None) -> None:
+    if ws.numel() < h3fp4_cache_attn_workspace_bytes(64):
+        raise ValueError("ws must be a workspace for heads of 64")
+    _check(load_library().h3fp4_selftest_cache_attn_timeout(_ptr(ws, "ws", torch.uint8), int(limit_ns),
+                                                            _stream(stream)), "h3fp4_selftest_cache_attn_timeout")
+
+
 def h3fp4_check(ws: torch.Tensor, stream=None) -> None:
     """Synchronise and raise H3FP4Error if a device wait timed out."""
     _check(load_library().h3fp4_check(_ptr(ws, "ws", torch.uint8), _stream(stream)), "h3fp4_check")
@@ -571,4 +674,19 @@ def alloc_attn_workspace(M: int, T: int, Hq: int, Hkv: int, D: int, q_off: Optio
     n = h3fp4_attn_workspace_bytes(M, T, Hq, Hkv, D, q_off, kv_off, ctx)
     if n == 0:
         raise ValueError("sizes or segment tables that the attention calls refuse")
+    return torch.zeros(n, dtype=torch.uint8, device=device)
+
+
+def alloc_kv_cache(pages: int, heads: int, D: int, page: int = 64, device="cuda") -> torch.Tensor:
+    """uint8 [pages, heads, page, bytes of a token and head]: a paged 4-bit cache of ``pages`` pages of ``page`` tokens."""
+    if h3fp4_cache_page_bytes(heads, D, page) == 0:
+        raise ValueError("sizes that the cache calls refuse")
+    return torch.zeros(pages, heads, page, _cache_width(D) * 9 // 8, dtype=torch.uint8, device=device)
+
+
+def alloc_cache_attn_workspace(rows: int, seqs: int, Hq: int, heads: int, D: int, device="cuda") -> torch.Tensor:
+    """Workspace of :func:`h3fp4_cache_attn` (its size depends on D alone)."""
+    n = h3fp4_cache_attn_workspace_bytes(D)
+    if n == 0 or heads < 1 or Hq % heads or seqs < 1 or rows < 0:
+        raise ValueError("sizes that the cache attention refuses")
     return torch.zeros(n, dtype=torch.uint8, device=device)

@@ -1,0 +1,781 @@
+// Attention of a few rows of each sequence to a paged cache held in four bits.
+//
+//     out[r][h] = sum_j p_j v_j / sum_j p_j,  p_j = exp(scale * q_r . k_j - m_r),  k = e2m1 * S * s_k, v likewise
+//
+// What it has to read is the cache, 9/8 bytes per element pair of K and V, each element for
+// up to 16 query columns (rows x query heads of a kv head): bound by HBM where the lanes can
+// unpack that fast.  An element costs half a conversion (two codes to f16x2), half a
+// multiplication by its block scale (exact in f16: six significant bits) and its share of the
+// matrix products, about 1 instruction in all; the 47 G (token, head) pairs a second that HBM
+// delivers at heads of 128 leave 1.5.
+//
+// A unit of work is (sequence, kv head, 16 columns); its keys come in tiles of 64, four warps
+// taking a group of 16 each.  All units' tiles are one row of work that is cut evenly over the
+// CTAs, from the lengths on the device: the same launch serves any lengths, so it can be
+// captured.  Every warp has a ring of groups that bulk copies fill, its own running maximum,
+// sum and output; the four are joined at a unit's end.  A unit that was cut leaves partial sums
+// in the workspace, which a second kernel joins.  All orders are fixed: the same call gives
+// the same bits.
+//
+// S = Q K^T: m16n8k16 with the columns as rows of A and the tokens as columns of B; what a lane
+// unpacks of a token is its B fragment.  O = P V: P stays where S was (the accumulator layout
+// is A's), V's fragment pairs two tokens, interleaved as nibbles before they are converted.
+// Q is scaled per column by a power of two to f16's range (exact for elements within 2^31 of
+// the column's largest).  The reference of the exponent follows the true maximum only when
+// that passed it by 2^14: p lies in f16's upper range, and those below 2^-30 of the largest
+// vanish.  Scores, sums and O are fp32.
+#include <cstdint>
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "h3fp4_token.h"
+#include "kv_cache.cuh"
+#include "ptx_sm103.cuh"
+
+namespace h3fp4 {
+namespace {
+
+constexpr int kWarps = 4;
+constexpr int kThreads = 32 * kWarps;
+constexpr int kTile = kCacheGroup * kWarps;   // tokens of a tile
+constexpr int kCols = 16;                     // query columns of a unit
+constexpr int kMaxCtas = 608;                 // of a launch: the workspace is made for as many
+constexpr float kRaise = 14.0f, kStart = 6.0f;  // in powers of two: see above
+// No key yet; and the lowest score that counts: where a column's largest is there, it left fp32's range.
+constexpr float kNone = -3.4e38f, kLowest = -3.0e38f;
+
+// What a CTA leaves for the joining kernel about the cut at its first tile.
+struct Cut {
+    int seq, head, tile, count;   // the unit, and of how many CTAs it takes partials (0: no first cut)
+};
+
+// Partial sums: per CTA one of a unit that began before it, one of a unit that goes on after it.
+template <int W>
+struct Part {
+    static constexpr long long kFloats = kCols * (W + 2);
+};
+
+constexpr size_t kCutOff = 256;
+constexpr size_t kPartOff = kCutOff + kMaxCtas * sizeof(Cut);
+
+template <int W>
+struct Config {
+    static constexpr int kSlots = W == 256 ? 3 : W == 128 ? 4 : 6;     // groups in flight per warp
+    static constexpr int kCtasPerSm = W == 256 ? 2 : 3;
+    static constexpr int kMergeRegs = W / 2 + 4;                       // a lane's state: O, two maxima, two sums
+    static constexpr uint32_t kRing = kWarps * kSlots * CacheLayout<W>::kGroupBytes;
+    static constexpr uint32_t kMerge = 2 * kMergeRegs * 32 * 4;
+    static constexpr uint32_t kPrefix = (kCacheMaxSeqs + 1) * 8;
+    static constexpr uint32_t kBars = kWarps * kSlots * 8;
+    static constexpr uint32_t kSmem = kRing + kMerge + kPrefix + kBars;
+};
+
+struct AttnParams {
+    CacheView c;
+    HeadsIn q;
+    __nv_bfloat16* out;
+    long long out_row, out_head;
+    float* lse;
+    long long M;
+    int Hq, group, causal, stall;
+    float scale_log2;
+    uint8_t* ws;
+    unsigned long long wait_ns;
+};
+
+// The rows of sequence s and its units.  Row offsets may hold anything: they are kept inside
+// the M rows that there are.
+struct Seq {
+    long long first, rows, len;   // packed rows [first, first + rows), tokens that the table has room for
+    long long start;              // position of the first row
+    int coltiles, tiles;
+};
+
+__device__ __forceinline__ Seq sequence(const AttnParams& p, int s)
+{
+    Seq q;
+    long long a = s, b = s + 1;
+    if (p.c.row_off) {
+        a = p.c.row_off[s];
+        b = p.c.row_off[s + 1];
+    }
+    q.start = (long long)p.c.length[s] - (b - a);
+    if (a < 0) {
+        q.start -= a;
+        a = 0;
+    }
+    b = b < p.M ? b : p.M;
+    q.first = a;
+    q.rows = b > a ? b - a : 0;
+    q.len = cache_length(p.c, s);
+    q.coltiles = (int)((q.rows * p.group + kCols - 1) / kCols);
+    q.tiles = (int)((q.len + kTile - 1) / kTile);
+    return q;
+}
+
+__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar)
+{
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                     smem_u32(dst)),
+                 "l"(src), "r"(bytes), "r"(smem_u32(bar))
+                 : "memory");
+}
+
+__device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
+{
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// Four bytes of two E2M1 codes each -> four f16x2 (the low code in the low half).
+__device__ __forceinline__ void e2m1x8_f16(uint32_t w, uint32_t (&o)[4])
+{
+    asm("{\n\t.reg .b8 a, b, c, d;\n\t"
+        "mov.b32 {a, b, c, d}, %4;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %0, a;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %1, b;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %2, c;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %3, d;\n\t}"
+        : "=r"(o[0]), "=r"(o[1]), "=r"(o[2]), "=r"(o[3])
+        : "r"(w));
+}
+
+// Two E4M3 codes -> f16x2 (exact).
+__device__ __forceinline__ uint32_t e4m3x2_f16(uint32_t w)
+{
+    uint32_t o;
+    asm("{\n\t.reg .b16 c;\n\tcvt.u16.u32 c, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, c;\n\t}" : "=r"(o) : "r"(w));
+    return o;
+}
+
+__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b)
+{
+    uint32_t o;
+    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(o) : "r"(a), "r"(b));
+    return o;
+}
+
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi)
+{
+    uint32_t o;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(o) : "f"(hi), "f"(lo));
+    return o;
+}
+
+// The larger one, NaN where either is.
+__device__ __forceinline__ float max_nan(float a, float b)
+{
+    float o;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(o) : "f"(a), "f"(b));
+    return o;
+}
+
+// A column's outputs per unit of O: zero without a key, NaN where the largest score left fp32's range.
+__device__ __forceinline__ float norm(float m, float l, float s)
+{
+    return l == 0.0f ? 0.0f : m < 0.99f * kLowest ? __int_as_float(0x7FFFFFFF) : s / l;
+}
+
+__device__ __forceinline__ float log_sum(float m, float l)
+{
+    return l == 0.0f ? -INFINITY : m < 0.99f * kLowest ? __int_as_float(0x7FFFFFFF) : (m + log2f(l)) * 0.6931471805599453f;
+}
+
+// 2^x for an integer x in the normal range.
+__device__ __forceinline__ float pow2i(int x) { return __uint_as_float((uint32_t)(x + 127) << 23); }
+
+template <int N>
+__device__ __forceinline__ void ld_words(const uint8_t* p, uint32_t (&w)[N])
+{
+    if constexpr (N >= 4) {
+#pragma unroll
+        for (int i = 0; i < N / 4; ++i) {
+            const uint4 v = reinterpret_cast<const uint4*>(p)[i];
+            w[4 * i] = v.x, w[4 * i + 1] = v.y, w[4 * i + 2] = v.z, w[4 * i + 3] = v.w;
+        }
+    } else if constexpr (N == 2) {
+        const uint2 v = *reinterpret_cast<const uint2*>(p);
+        w[0] = v.x, w[1] = v.y;
+    } else {
+        w[0] = *reinterpret_cast<const uint32_t*>(p);
+    }
+}
+
+// The state of a warp over the tokens it has seen, of columns g and g + 8: the exponents'
+// reference, the lane's part of the sums, and O (n tile j holds elements n W/8 + j).
+template <int W>
+struct State {
+    float m[2], l[2];
+    float o[W / 8][4];
+};
+
+template <int W>
+__device__ __forceinline__ void rescale(State<W>& st, int row, float to)
+{
+    const float f = exp2f(st.m[row] - to);
+    st.m[row] = to;
+    st.l[row] *= f;
+#pragma unroll
+    for (int j = 0; j < W / 8; ++j) {
+        st.o[j][2 * row] *= f;
+        st.o[j][2 * row + 1] *= f;
+    }
+}
+
+// One group of 16 tokens.  `left`: how many of its tokens hold anything; lim: tokens that
+// columns g and g + 8 attend to, counted from the group's first.
+template <int W>
+__device__ __forceinline__ void group_step(State<W>& st, const uint8_t* gp, int lane, const uint32_t (&qa)[W / 16][4],
+                                           const float (&factor)[2], bool masked, int left, const int (&lim)[2])
+{
+    using L = CacheLayout<W>;
+    const int c = lane & 3;
+    float s[2][4];
+    // ------------------------------------------------------------ S = Q K^T, tokens 8 half + g
+    {
+        uint32_t sc[W == 256 ? 2 : 1];   // the lane's scales of both halves
+        if constexpr (W == 256) ld_words<2>(gp + L::kKScale + lane * 8, sc);
+        else if constexpr (W == 128) sc[0] = *reinterpret_cast<const uint32_t*>(gp + L::kKScale + lane * 4);
+        else sc[0] = *reinterpret_cast<const uint16_t*>(gp + L::kKScale + lane * 2);
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+            s[half][0] = s[half][1] = s[half][2] = s[half][3] = 0.0f;
+            constexpr int kRuns = W == 256 ? 2 : 1;
+#pragma unroll
+            for (int run = 0; run < kRuns; ++run) {
+                constexpr int kWords = W == 64 ? 2 : 4;
+                uint32_t w[kWords];
+                ld_words<kWords>(W == 64 ? gp + half * 256 + lane * 8 : gp + run * 1024 + half * 512 + lane * 16, w);
+                uint32_t pair;   // this run's scales of this half, f16x2 (W = 64: one, twice)
+                if constexpr (W == 64) {
+                    const uint32_t b = half ? sc[0] >> 8 : sc[0] & 0xFFu;
+                    pair = e4m3x2_f16(b | (b << 8));
+                } else if constexpr (W == 128) {
+                    pair = e4m3x2_f16(half ? sc[0] >> 16 : sc[0]);
+                } else {
+                    pair = e4m3x2_f16(run ? sc[half] >> 16 : sc[half]);
+                }
+                const uint32_t s0 = __byte_perm(pair, pair, 0x1010), s1 = __byte_perm(pair, pair, 0x3232);
+#pragma unroll
+                for (int i = 0; i < kWords; ++i) {
+                    uint32_t f[4];
+                    e2m1x8_f16(w[i], f);
+                    const uint32_t x = 2 * i < kWords ? s0 : s1;
+                    const int step = run * 8 + 2 * i;
+                    mma_f16(s[half], qa[step], mul_f16x2(f[0], x), mul_f16x2(f[1], x));
+                    mma_f16(s[half], qa[step + 1], mul_f16x2(f[2], x), mul_f16x2(f[3], x));
+                }
+            }
+        }
+    }
+    // ------------------------------------------------------------ exponents, column g (row 0) and g + 8
+#pragma unroll
+    for (int half = 0; half < 2; ++half)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            s[half][i] = max_nan(s[half][i] * factor[i >> 1], kLowest);
+            if (masked && 8 * half + 2 * c + (i & 1) >= lim[i >> 1]) s[half][i] = -INFINITY;
+        }
+    uint32_t pa[4];
+    float top[2];
+#pragma unroll
+    for (int row = 0; row < 2; ++row)
+        top[row] = fmaxf(fmaxf(s[0][2 * row], s[0][2 * row + 1]), fmaxf(s[1][2 * row], s[1][2 * row + 1]));
+    if (__any_sync(0xffffffffu, top[0] > st.m[0] + kRaise || top[1] > st.m[1] + kRaise)) {
+#pragma unroll
+        for (int row = 0; row < 2; ++row) {
+            float t = top[row];
+            t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 1));
+            t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 2));
+            if (t > st.m[row] + kRaise) rescale<W>(st, row, t - kStart);
+        }
+    }
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+        float e[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            e[i] = ex2_approx_ftz(s[half][i] - st.m[i >> 1]);
+            st.l[i >> 1] += e[i];
+        }
+        pa[2 * half] = pack_f16x2(e[0], e[1]);
+        pa[2 * half + 1] = pack_f16x2(e[2], e[3]);
+    }
+    // ------------------------------------------------------------ O += P V, token pairs 8 half + 2 c + (0, 1)
+    constexpr int kVBlocks = W == 256 ? 2 : 1;      // scale blocks of a lane
+    constexpr int kVWords = W == 64 ? 1 : W == 128 ? 2 : 4;  // words of a token
+    uint32_t vs[2][kVBlocks];
+#pragma unroll
+    for (int b = 0; b < kVBlocks; ++b) {
+        const int g = lane >> 2;
+        const int block = W == 64 ? g >> 1 : W == 128 ? g : 2 * g + b;
+        const uint32_t four = *reinterpret_cast<const uint32_t*>(gp + L::kVScale + (block * 4 + c) * 4);
+        vs[0][b] = e4m3x2_f16(four);
+        vs[1][b] = e4m3x2_f16(four >> 16);
+    }
+    if (masked) {
+        // tokens without data: their scales may be anything, NaN too
+#pragma unroll
+        for (int half = 0; half < 2; ++half)
+#pragma unroll
+            for (int b = 0; b < kVBlocks; ++b) {
+                const int t = 8 * half + 2 * c;
+                vs[half][b] &= (t < left ? 0xFFFFu : 0u) | (t + 1 < left ? 0xFFFF0000u : 0u);
+            }
+    }
+    uint32_t w0[2][kVWords], w1[2][kVWords];
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+        if constexpr (W == 256) {
+            ld_words<4>(gp + L::kV + half * 1024 + lane * 16, w0[half]);
+            ld_words<4>(gp + L::kV + half * 1024 + 512 + lane * 16, w1[half]);
+        } else {
+            uint32_t w[2 * kVWords];
+            ld_words<2 * kVWords>(gp + L::kV + half * (32 * 8 * kVWords) + lane * (8 * kVWords), w);
+#pragma unroll
+            for (int i = 0; i < kVWords; ++i) {
+                w0[half][i] = w[i];
+                w1[half][i] = w[kVWords + i];
+            }
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < kVWords; ++i) {
+        uint32_t even[2][4], odd[2][4];
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+            const uint32_t a = w0[half][i], b = w1[half][i];
+            e2m1x8_f16((a & 0x0F0F0F0Fu) | ((b << 4) & 0xF0F0F0F0u), even[half]);
+            e2m1x8_f16(((a >> 4) & 0x0F0F0F0Fu) | (b & 0xF0F0F0F0u), odd[half]);
+        }
+        const int blk = W == 256 ? i >> 1 : 0;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            mma_f16(st.o[8 * i + 2 * j], pa, mul_f16x2(even[0][j], vs[0][blk]), mul_f16x2(even[1][j], vs[1][blk]));
+            mma_f16(st.o[8 * i + 2 * j + 1], pa, mul_f16x2(odd[0][j], vs[0][blk]), mul_f16x2(odd[1][j], vs[1][blk]));
+        }
+    }
+}
+
+// The larger reference of two states, and what their sums are scaled with.
+__device__ __forceinline__ void join_scale(float a, float b, float& m, float& fa, float& fb)
+{
+    m = fmaxf(a, b);
+    fa = exp2f(a - m);
+    fb = exp2f(b - m);
+}
+
+template <int W>
+__global__ void __launch_bounds__(kThreads, Config<W>::kCtasPerSm)
+    cache_attn_kernel(const __grid_constant__ AttnParams p)
+{
+    using L = CacheLayout<W>;
+    using C = Config<W>;
+    extern __shared__ __align__(128) uint8_t smem[];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
+    uint8_t* ring = smem + warp * (C::kSlots * L::kGroupBytes);
+    float* merge = reinterpret_cast<float*>(smem + C::kRing);
+    long long* prefix = reinterpret_cast<long long*>(smem + C::kRing + C::kMerge);
+    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::kRing + C::kMerge + C::kPrefix) + warp * C::kSlots;
+    __shared__ long long warp_sum[kWarps];
+    unsigned int* status = reinterpret_cast<unsigned int*>(p.ws);
+    if (lane == 0) {
+        for (int i = 0; i < C::kSlots; ++i) mbar_init(&bars[i], 1);
+        fence_mbarrier_init();
+    }
+    griddep_wait();
+    const int nseq = p.c.nseq;
+
+    // ------------------------------------------------------------ tiles before each sequence
+    {
+        const int per = (nseq + kThreads - 1) / kThreads, s0 = threadIdx.x * per;
+        long long mine = 0;
+        for (int s = s0; s < s0 + per && s < nseq; ++s) {
+            const Seq q = sequence(p, s);
+            mine += (long long)p.c.Hkv * q.coltiles * q.tiles;
+        }
+        long long upto = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long v = __shfl_up_sync(0xffffffffu, upto, o);
+            if (lane >= o) upto += v;
+        }
+        if (lane == 31) warp_sum[warp] = upto;
+        __syncthreads();
+        for (int w = 0; w < warp; ++w) upto += warp_sum[w];
+        long long before = upto - mine;
+        for (int s = s0; s < s0 + per && s < nseq; ++s) {
+            prefix[s] = before;
+            const Seq q = sequence(p, s);
+            before += (long long)p.c.Hkv * q.coltiles * q.tiles;
+        }
+        if (threadIdx.x == kThreads - 1) prefix[nseq] = upto;
+        __syncthreads();
+    }
+    const long long total = prefix[nseq];
+    const long long chunk = (total + gridDim.x - 1) / gridDim.x;
+    const long long begin = min(total, chunk * blockIdx.x), end = min(total, begin + chunk);
+
+    // rows of sequences that hold nothing
+    for (int s = blockIdx.x; s < nseq; s += gridDim.x) {
+        const Seq q = sequence(p, s);
+        if (q.tiles > 0) continue;
+        const int vecs = p.c.D / 8;
+        for (long long i = threadIdx.x; i < q.rows * p.Hq * vecs; i += kThreads) {
+            const long long r = q.first + i / (p.Hq * vecs);
+            const int h = (int)(i / vecs % p.Hq), v = (int)(i % vecs);
+            *reinterpret_cast<uint4*>(p.out + r * p.out_row + (long long)h * p.out_head + 8 * v) = make_uint4(0, 0, 0, 0);
+            if (p.lse && v == 0) p.lse[r * p.Hq + h] = -INFINITY;
+        }
+    }
+    Cut* cut = reinterpret_cast<Cut*>(p.ws + kCutOff) + blockIdx.x;
+    if (threadIdx.x == 0) *cut = Cut{0, 0, 0, 0};
+
+    // ------------------------------------------------------------ units
+    uint32_t phases = 0;    // of the ring's barriers, one bit each
+    bool lost = false;      // a wait ran out: nothing more is loaded or computed
+    int s = 0;
+    for (long long at = begin; at < end;) {
+        // the sequence whose tiles hold `at`
+        {
+            int lo = s, hi = nseq;
+            while (hi - lo > 1) {
+                const int mid = (lo + hi) / 2;
+                if (prefix[mid] <= at) lo = mid;
+                else hi = mid;
+            }
+            s = lo;
+        }
+        const Seq q = sequence(p, s);
+        const long long unit = (at - prefix[s]) / q.tiles;
+        const int h = (int)(unit / q.coltiles), ct = (int)(unit % q.coltiles);
+        const long long ubegin = prefix[s] + unit * q.tiles, uend = ubegin + q.tiles;
+        const int t0 = (int)(at - ubegin), t1 = (int)(min(end, uend) - ubegin);
+        // what each column attends to
+        const int cols = (int)min((long long)kCols, q.rows * p.group - (long long)ct * kCols);
+        auto limit = [&](int col) -> long long {
+            const long long row = ((long long)ct * kCols + col) / p.group;
+            return p.causal ? max(0ll, min(q.len, q.start + row + 1)) : q.len;
+        };
+        const long long least = limit(0), most = limit(cols - 1);
+        const long long mylim[2] = {g < cols ? limit(g) : most, g + 8 < cols ? limit(g + 8) : most};
+
+        // this warp's groups: tile t's group of 16 tokens is 4 t + warp, up to the last token that any column sees
+        const int groups = (int)((most + kCacheGroup - 1) / kCacheGroup);
+        int n = 0;   // of this warp in [t0, t1)
+        if (groups > kWarps * t0 + warp) n = min(t1 - t0, (groups - (kWarps * t0 + warp) + kWarps - 1) / kWarps);
+        const int per_page = p.c.page / kCacheGroup;
+        const int32_t* table = p.c.table + (long long)s * p.c.max_pages;
+        const long long head_bytes = (long long)per_page * L::kGroupBytes;
+        // page numbers of the next 32 groups, one per lane, and which of them the pool has
+        int page_at = 0, page = 0;
+        auto fetch_pages = [&](int i) {
+            page_at = i;
+            const int gi = kWarps * (t0 + i + lane) + warp;
+            page = -1;
+            if (i + lane < n) {
+                page = table[gi / per_page];
+                if (page < 0 || page >= p.c.n_pages) page = -1;
+            }
+        };
+        uint32_t there = 0;   // slots whose group exists
+        auto load = [&](int i, int slot) {
+            if (i - page_at >= 32) fetch_pages(i);
+            const int pg = __shfl_sync(0xffffffffu, page, i - page_at);
+            const int gi = kWarps * (t0 + i) + warp;
+            there = (there & ~(1u << slot)) | (pg >= 0 ? 1u << slot : 0u);
+            if (lane == 0 && !p.stall) {
+                if (pg < 0) {
+                    mbar_arrive(&bars[slot]);
+                } else {
+                    mbar_arrive_expect_tx(&bars[slot], L::kGroupBytes);
+                    bulk_load(ring + slot * L::kGroupBytes,
+                              p.c.pool + ((long long)pg * p.c.Hkv + h) * head_bytes +
+                                  (long long)(gi % per_page) * L::kGroupBytes,
+                              L::kGroupBytes, &bars[slot]);
+                }
+            }
+        };
+        int loaded = 0;
+        if (n > 0 && !lost) {
+            fetch_pages(0);
+            for (; loaded < min(n, C::kSlots); ++loaded) load(loaded, loaded);
+        }
+
+        // Q's fragments: the lane's elements of columns g and g + 8, scaled to f16's range
+        uint32_t qa[W / 16][4];
+        float factor[2];
+        const float kg = p.c.k_gscale ? p.c.k_gscale[h] : 1.0f;
+#pragma unroll
+        for (int row = 0; row < 2; ++row) {
+            const int col = g + 8 * row;
+            const long long id = (long long)ct * kCols + col;
+            const __nv_bfloat16* src = nullptr;
+            if (col < cols)
+                src = p.q.p + (q.first + id / p.group) * p.q.row + (long long)(h * p.group + (int)(id % p.group)) * p.q.head;
+            uint2 raw[W / 16];
+            uint32_t top = 0;
+#pragma unroll
+            for (int t = 0; t < W / 16; ++t) {
+                const int d = W == 64 ? 16 * c + 4 * t : (t >> 3) * 128 + 32 * c + 4 * (t & 7);
+                raw[t] = make_uint2(0, 0);
+                if (src && d < p.c.D) raw[t] = *reinterpret_cast<const uint2*>(src + d);
+                top = max(top, max(max(raw[t].x & 0x7FFFu, (raw[t].x >> 16) & 0x7FFFu),
+                                   max(raw[t].y & 0x7FFFu, (raw[t].y >> 16) & 0x7FFFu)));
+            }
+            top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+            top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+            // the largest to [2^14, 2^15): by at most 2^127 either way, in two steps where that is subnormal
+            const int e = min(126, max(-126, 14 - ((int)(top >> 7) - 127)));
+            const float up = pow2i(e);
+            factor[row] = p.scale_log2 * kg * pow2i(-e);
+#pragma unroll
+            for (int t = 0; t < W / 16; ++t) {
+                auto f16 = [&](uint32_t w) {
+                    return pack_f16x2(__uint_as_float(w << 16) * up, __uint_as_float(w & 0xFFFF0000u) * up);
+                };
+                qa[t][row] = f16(raw[t].x);
+                qa[t][2 + row] = f16(raw[t].y);
+            }
+        }
+
+        State<W> st;
+        st.m[0] = st.m[1] = kNone;
+        st.l[0] = st.l[1] = 0.0f;
+#pragma unroll
+        for (int j = 0; j < W / 8; ++j) st.o[j][0] = st.o[j][1] = st.o[j][2] = st.o[j][3] = 0.0f;
+        int slot = 0;
+        for (int i = 0; i < n && !lost; ++i) {
+            const bool ok = mbar_wait(&bars[slot], (phases >> slot) & 1u, p.wait_ns, status, kStatusTimeoutMma);
+            if (!__all_sync(0xffffffffu, ok)) {
+                lost = true;
+                // copies in flight land before the CTA may end
+                if (!p.stall)
+                    for (int k = i; k < loaded; ++k) {
+                        (void)mbar_wait(&bars[slot], (phases >> slot) & 1u, p.wait_ns, status, kStatusTimeoutMma);
+                        slot = slot + 1 == C::kSlots ? 0 : slot + 1;
+                    }
+                break;
+            }
+            phases ^= 1u << slot;
+            if ((there >> slot) & 1u) {
+                const long long first = (long long)(kWarps * (t0 + i) + warp) * kCacheGroup;
+                const bool masked = first + kCacheGroup > least;
+                const int lim[2] = {(int)min((long long)kCacheGroup, mylim[0] - first),
+                                    (int)min((long long)kCacheGroup, mylim[1] - first)};
+                group_step<W>(st, ring + slot * L::kGroupBytes, lane, qa, factor, masked,
+                              (int)min((long long)kCacheGroup, most - first), lim);
+            }
+            fence_proxy_async_smem();  // these reads, before the slot's next fill
+            __syncwarp();
+            if (loaded < n) {
+                load(loaded, slot);
+                ++loaded;
+            }
+            slot = slot + 1 == C::kSlots ? 0 : slot + 1;
+        }
+        __syncwarp();
+
+        // ------------------------------------------------------------ the four warps' sums into warp 0
+#pragma unroll
+        for (int row = 0; row < 2; ++row) {
+            st.l[row] += __shfl_xor_sync(0xffffffffu, st.l[row], 1);
+            st.l[row] += __shfl_xor_sync(0xffffffffu, st.l[row], 2);
+        }
+#pragma unroll
+        for (int with = 2; with >= 1; with >>= 1) {
+            float* slot_m = merge + (warp & (with - 1)) * (C::kMergeRegs * 32) + lane;
+            __syncthreads();
+            if (warp >= with && warp < 2 * with) {
+                slot_m[0] = st.m[0], slot_m[32] = st.m[1], slot_m[64] = st.l[0], slot_m[96] = st.l[1];
+#pragma unroll
+                for (int j = 0; j < W / 2; ++j) slot_m[32 * (4 + j)] = st.o[j >> 2][j & 3];
+            }
+            __syncthreads();
+            if (warp < with) {
+                float fa[2], fb[2];
+#pragma unroll
+                for (int row = 0; row < 2; ++row) {
+                    float m;
+                    join_scale(st.m[row], slot_m[32 * row], m, fa[row], fb[row]);
+                    st.m[row] = m;
+                    st.l[row] = st.l[row] * fa[row] + slot_m[32 * (2 + row)] * fb[row];
+                }
+#pragma unroll
+                for (int j = 0; j < W / 2; ++j) {
+                    const int row = (j & 3) >> 1;
+                    st.o[j >> 2][j & 3] = st.o[j >> 2][j & 3] * fa[row] + slot_m[32 * (4 + j)] * fb[row];
+                }
+            }
+        }
+        if (warp == 0) {
+            const bool whole = at == ubegin && uend <= end;
+            if (whole) {
+                const float vg = p.c.v_gscale ? p.c.v_gscale[h] : 1.0f;
+#pragma unroll
+                for (int row = 0; row < 2; ++row) {
+                    const int col = g + 8 * row;
+                    if (col >= cols) continue;
+                    const long long id = (long long)ct * kCols + col;
+                    const long long r = q.first + id / p.group;
+                    const int hq = h * p.group + (int)(id % p.group);
+                    const float f = norm(st.m[row], st.l[row], vg);
+                    __nv_bfloat16* o = p.out + r * p.out_row + (long long)hq * p.out_head;
+                    // elements n W/8 + j of n = 2 c, 2 c + 1
+#pragma unroll
+                    for (int k = 0; k < W / 4; k += 8) {
+                        const int e = k / (W / 8), j = k % (W / 8);
+                        uint32_t w[4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            w[i] = cvt_bf16x2(f2(st.o[j + 2 * i][2 * row + e] * f, st.o[j + 2 * i + 1][2 * row + e] * f));
+                        const int d = (2 * c + e) * (W / 8) + j;
+                        if (d < p.c.D) *reinterpret_cast<uint4*>(o + d) = make_uint4(w[0], w[1], w[2], w[3]);
+                    }
+                    if (p.lse && c == 0)
+                        p.lse[r * p.Hq + hq] = log_sum(st.m[row], st.l[row]);
+                }
+            } else {
+                float* part = reinterpret_cast<float*>(p.ws + kPartOff) +
+                              (2ll * blockIdx.x + (at == ubegin ? 1 : 0)) * Part<W>::kFloats;
+#pragma unroll
+                for (int row = 0; row < 2; ++row) {
+                    const int col = g + 8 * row;
+                    if (c == 0) {
+                        part[col] = st.m[row];
+                        part[kCols + col] = st.l[row];
+                    }
+                    float* o = part + 2 * kCols + col * W;
+#pragma unroll
+                    for (int k = 0; k < W / 4; k += 4) {
+                        const int e = k / (W / 8), j = k % (W / 8);
+                        *reinterpret_cast<float4*>(o + (2 * c + e) * (W / 8) + j) =
+                            make_float4(st.o[j][2 * row + e], st.o[j + 1][2 * row + e], st.o[j + 2][2 * row + e],
+                                        st.o[j + 3][2 * row + e]);
+                    }
+                }
+                // the first cut of a unit stands with the CTA behind it
+                const long long before = ubegin / chunk;
+                if (lane == 0 && at != ubegin && before + 1 == blockIdx.x)
+                    *cut = Cut{s, h, ct, (int)((uend - 1) / chunk - before + 1)};
+            }
+        }
+        at = ubegin + t1;
+    }
+}
+
+// One column of a unit that was cut: block (cut, column).
+template <int W>
+__global__ void __launch_bounds__(128) cache_join_kernel(const __grid_constant__ AttnParams p)
+{
+    constexpr int kLanes = W / 4;                 // threads of a partial, four elements each
+    constexpr int kSplit = 128 / kLanes;          // partials at a time
+    __shared__ float4 sum[128];
+    griddep_wait();
+    const Cut cut = reinterpret_cast<const Cut*>(p.ws + kCutOff)[blockIdx.x];
+    if (cut.count == 0) return;
+    const Seq q = sequence(p, cut.seq);
+    const long long id = (long long)cut.tile * kCols + blockIdx.y;
+    if (id >= q.rows * p.group) return;
+    const int col = blockIdx.y;
+    // partial 0 is the CTA's before this one (its second), the others are the first ones
+    auto part = [&](int i) {
+        return reinterpret_cast<const float*>(p.ws + kPartOff) +
+               (2ll * ((long long)blockIdx.x - 1 + i) + (i == 0 ? 1 : 0)) * Part<W>::kFloats;
+    };
+    // the largest reference, then the sums under it
+    float m = kNone;
+    for (int i = threadIdx.x & 31; i < cut.count; i += 32) m = fmaxf(m, part(i)[col]);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    float l = 0.0f;
+    for (int i = threadIdx.x & 31; i < cut.count; i += 32) l += part(i)[kCols + col] * exp2f(part(i)[col] - m);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+    const int lane = threadIdx.x % kLanes;
+    float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 4
+    for (int i = threadIdx.x / kLanes; i < cut.count; i += kSplit) {
+        const float* a = part(i);
+        const float f = exp2f(a[col] - m);
+        const float4 v = *reinterpret_cast<const float4*>(a + 2 * kCols + col * W + 4 * lane);
+        acc.x = fmaf(v.x, f, acc.x), acc.y = fmaf(v.y, f, acc.y);
+        acc.z = fmaf(v.z, f, acc.z), acc.w = fmaf(v.w, f, acc.w);
+    }
+    sum[threadIdx.x] = acc;
+    __syncthreads();
+    if (threadIdx.x >= kLanes) return;
+    for (int i = 1; i < kSplit; ++i) {
+        const float4 v = sum[threadIdx.x + i * kLanes];
+        acc.x += v.x, acc.y += v.y, acc.z += v.z, acc.w += v.w;
+    }
+    const long long r = q.first + id / p.group;
+    const int hq = cut.head * p.group + (int)(id % p.group);
+    const float f = norm(m, l, p.c.v_gscale ? p.c.v_gscale[cut.head] : 1.0f);
+    if (4 * lane < p.c.D)
+        *reinterpret_cast<uint2*>(p.out + r * p.out_row + (long long)hq * p.out_head + 4 * lane) =
+            make_uint2(cvt_bf16x2(f2(acc.x * f, acc.y * f)), cvt_bf16x2(f2(acc.z * f, acc.w * f)));
+    if (p.lse && lane == 0) p.lse[r * p.Hq + hq] = log_sum(m, l);
+}
+
+template <int W>
+cudaError_t launch(const AttnParams& p, cudaStream_t s)
+{
+    using C = Config<W>;
+    const cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void*>(cache_attn_kernel<W>), (int)C::kSmem);
+    if (e != cudaSuccess) return e;
+    int ctas = sm_count_current_device() * C::kCtasPerSm;
+    if (ctas > kMaxCtas) ctas = kMaxCtas;
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.gridDim = dim3((unsigned)ctas);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = C::kSmem;
+    cfg.stream = s;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    const cudaError_t first = cudaLaunchKernelEx(&cfg, cache_attn_kernel<W>, p);
+    if (first != cudaSuccess) return first;
+    cfg.gridDim = dim3((unsigned)ctas, kCols);
+    cfg.blockDim = dim3(128);
+    cfg.dynamicSmemBytes = 0;
+    return cudaLaunchKernelEx(&cfg, cache_join_kernel<W>, p);
+}
+
+}  // namespace
+
+size_t cache_attn_workspace_bytes(int D)
+{
+    const int w = cache_width(D);
+    return kPartOff + 2 * kMaxCtas * sizeof(float) * (w == 64 ? Part<64>::kFloats : w == 128 ? Part<128>::kFloats : Part<256>::kFloats);
+}
+
+cudaError_t launch_cache_attn(const CacheAttnJob& job, cudaStream_t s)
+{
+    if (job.M == 0) return cudaSuccess;
+    AttnParams p{};
+    p.c = job.c;
+    p.q = job.q;
+    p.out = job.out;
+    p.out_row = job.out_row;
+    p.out_head = job.out_head;
+    p.lse = job.lse;
+    p.M = job.M;
+    p.Hq = job.Hq;
+    p.group = job.Hq / job.c.Hkv;
+    p.causal = job.causal;
+    p.stall = job.stall;
+    p.scale_log2 = job.scale * kLog2E;
+    p.ws = job.ws;
+    p.wait_ns = job.wait_limit_ns;
+    const int w = cache_width(job.c.D);
+    return w == 64 ? launch<64>(p, s) : w == 128 ? launch<128>(p, s) : launch<256>(p, s);
+}
+
+}  // namespace h3fp4

@@ -62,6 +62,12 @@ struct AttnJob {
 struct AttnPlan;
 cudaError_t launch_attn(const AttnJob& job, const AttnPlan& plan, cudaStream_t s);
 
+// Checks of a view (defined in h3fp4_heads_api.cu): an input of `rows` rows, H3FP4_OK or
+// what is wrong with it; an output, whose elements lie in places of their own.
+h3fp4_status check_in(const h3fp4_heads* t, int64_t rows);
+h3fp4_status check_out(const h3fp4_heads* t, int64_t rows, int heads, int D);
+HeadsIn in(const h3fp4_heads* t);
+
 // The limit set with h3fp4_set_wait_limit_ns.
 uint64_t wait_limit_ns();
 

@@ -8,15 +8,13 @@
 #include "h3fp4_heads.h"
 
 namespace h3fp4 {
+
 namespace {
-
 constexpr int64_t kMaxStride = (int64_t)1 << 38;  // elements: row pitches below the 2^40 bytes a TMA map holds
-
-constexpr int64_t kMaxRows = INT32_MAX - 255;  // rows are counted in 32 bits, up to two tiles past the last
-constexpr int kMaxHeads = INT32_MAX - 255;     // the norm's heads too, up to a warp's places past the last
+}  // namespace
 
 // Strides are positive multiples of 8 elements (16 bytes).
-bool good_strides(const h3fp4_heads& t)
+static bool good_strides(const h3fp4_heads& t)
 {
     return t.row_stride > 0 && t.head_stride > 0 && t.row_stride % 8 == 0 && t.head_stride % 8 == 0 &&
            t.row_stride <= kMaxStride && t.head_stride <= kMaxStride;
@@ -45,15 +43,20 @@ h3fp4_status check_out(const h3fp4_heads* t, int64_t rows, int heads, int D)
     return H3FP4_OK;
 }
 
-bool same_view(const h3fp4_heads& a, const h3fp4_heads& b)
-{
-    return a.ptr == b.ptr && a.row_stride == b.row_stride && a.head_stride == b.head_stride;
-}
-
 HeadsIn in(const h3fp4_heads* t)
 {
     if (!t) return HeadsIn{nullptr, 0, 0};
     return HeadsIn{static_cast<const __nv_bfloat16*>(t->ptr), t->row_stride, t->head_stride};
+}
+
+namespace {
+
+constexpr int64_t kMaxRows = INT32_MAX - 255;  // rows are counted in 32 bits, up to two tiles past the last
+constexpr int kMaxHeads = INT32_MAX - 255;     // the norm's heads too, up to a warp's places past the last
+
+bool same_view(const h3fp4_heads& a, const h3fp4_heads& b)
+{
+    return a.ptr == b.ptr && a.row_stride == b.row_stride && a.head_stride == b.head_stride;
 }
 
 bool good_table(const int64_t* off, int nseg, int64_t rows)

@@ -1,5 +1,5 @@
-// C ABI of a token's way through a block (h3fp4_block_norm): argument validation
-// and job set-up.  Nothing here allocates device memory or synchronises.
+// C ABI of a token's way through a block (h3fp4_block_norm, h3fp4_cache_append,
+// h3fp4_cache_read, h3fp4_cache_attn): argument validation and job set-up.  Nothing here allocates device memory or synchronises.
 #include <cmath>
 #include <cstdint>
 
@@ -12,6 +12,58 @@ bool overlap(const void* a, const void* b, int64_t bytes)
 {
     const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
     return a && b && x < y + (uint64_t)bytes && y < x + (uint64_t)bytes;
+}
+
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+// A cache and its sequences, of a call of M rows.
+h3fp4_status cache_view(const h3fp4_cache* c, int64_t M, CacheView* out)
+{
+    if (!c) return H3FP4_ERR_INVALID;
+    if (M < 0 || M > INT32_MAX - 255) return H3FP4_ERR_SHAPE;
+    if (c->dim < 16 || c->dim > kCacheMaxD || c->dim % 16 != 0 || c->heads < 1 || c->heads > 4096 ||
+        c->page < kCacheGroup || c->page > kCacheMaxPage || c->page % kCacheGroup != 0 || c->nseq < 1 ||
+        c->nseq > kCacheMaxSeqs || c->n_pages < 1 || c->n_pages > INT32_MAX || c->max_pages < 1 ||
+        c->max_pages > INT32_MAX)
+        return H3FP4_ERR_SHAPE;
+    if (!c->pool || !c->table || !c->length) return H3FP4_ERR_INVALID;
+    if (!c->row_off && M != c->nseq) return H3FP4_ERR_INVALID;
+    if (!aligned16(c->pool) || !aligned4(c->table) || !aligned4(c->length) || !aligned4(c->row_off) ||
+        !aligned4(c->k_gscale) || !aligned4(c->v_gscale))
+        return H3FP4_ERR_ALIGN;
+    out->pool = static_cast<uint8_t*>(c->pool);
+    out->n_pages = c->n_pages;
+    out->table = c->table;
+    out->length = c->length;
+    out->row_off = c->row_off;
+    out->k_gscale = c->k_gscale;
+    out->v_gscale = c->v_gscale;
+    out->max_pages = c->max_pages;
+    out->page = (int)c->page;
+    out->Hkv = (int)c->heads;
+    out->D = (int)c->dim;
+    out->nseq = (int)c->nseq;
+    return H3FP4_OK;
+}
+
+h3fp4_status cache_rows(const h3fp4_heads* k, const h3fp4_heads* v, int64_t M, const h3fp4_cache* cache, bool read,
+                        cudaStream_t stream)
+{
+    CacheRowsJob job{};
+    h3fp4_status st = cache_view(cache, M, &job.c);
+    if (st != H3FP4_OK) return st;
+    for (const h3fp4_heads* t : {k, v})
+        if ((st = read ? check_out(t, M, job.c.Hkv, job.c.D) : check_in(t, M)) != H3FP4_OK) return st;
+    if (read && M > 0 && k->ptr == v->ptr) return H3FP4_ERR_INVALID;
+    if ((st = check_device()) != H3FP4_OK) return st;
+    if (M == 0) return H3FP4_OK;
+    job.k = in(k);
+    job.v = in(v);
+    job.k_out = static_cast<__nv_bfloat16*>(k->ptr);
+    job.v_out = static_cast<__nv_bfloat16*>(v->ptr);
+    job.M = M;
+    const cudaError_t e = read ? launch_cache_read(job, stream) : launch_cache_append(job, stream);
+    return e == cudaSuccess ? H3FP4_OK : H3FP4_ERR_CUDA;
 }
 
 }  // namespace
@@ -68,6 +120,88 @@ h3fp4_status h3fp4_block_norm(const void* x, const void* y, int64_t M, int64_t K
     job.M = M;
     job.K = (int)K;
     return launch_block_norm(job, stream) == cudaSuccess ? H3FP4_OK : H3FP4_ERR_CUDA;
+}
+
+size_t h3fp4_cache_page_bytes(int heads, int dim, int page)
+{
+    if (heads < 1 || heads > 4096 || dim < 16 || dim > kCacheMaxD || dim % 16 != 0 || page < kCacheGroup ||
+        page > kCacheMaxPage || page % kCacheGroup != 0)
+        return 0;
+    return (size_t)heads * (size_t)page * (size_t)(cache_width(dim) * 9 / 8);
+}
+
+h3fp4_status h3fp4_cache_append(const h3fp4_heads* k, const h3fp4_heads* v, int64_t M, const h3fp4_cache* cache,
+                                cudaStream_t stream)
+{
+    return cache_rows(k, v, M, cache, false, stream);
+}
+
+h3fp4_status h3fp4_cache_read(const h3fp4_heads* k, const h3fp4_heads* v, int64_t M, const h3fp4_cache* cache,
+                              cudaStream_t stream)
+{
+    return cache_rows(k, v, M, cache, true, stream);
+}
+
+size_t h3fp4_cache_attn_workspace_bytes(int dim)
+{
+    return dim < 16 || dim > kCacheMaxD || dim % 16 != 0 ? 0 : cache_attn_workspace_bytes(dim);
+}
+
+h3fp4_status h3fp4_cache_attn(const h3fp4_heads* q, int64_t M, int Hq, const h3fp4_cache* cache, float scale,
+                              const h3fp4_heads* out, float* lse, int flags, void* ws, size_t ws_bytes,
+                              cudaStream_t stream)
+{
+    CacheAttnJob job{};
+    h3fp4_status st = cache_view(cache, M, &job.c);
+    if (st != H3FP4_OK) return st;
+    if (Hq < 1 || Hq % job.c.Hkv != 0 || M * (int64_t)Hq > INT32_MAX) return H3FP4_ERR_SHAPE;
+    if (flags & ~H3FP4_CAUSAL) return H3FP4_ERR_INVALID;
+    if (!(scale > 0.0f) || std::isinf(scale * kLog2E)) return H3FP4_ERR_INVALID;
+    if ((st = check_in(q, M)) != H3FP4_OK || (st = check_out(out, M, Hq, job.c.D)) != H3FP4_OK) return st;
+    if (!ws || ws_bytes < cache_attn_workspace_bytes(job.c.D)) return H3FP4_ERR_INVALID;
+    if (!aligned16(ws) || !aligned4(lse)) return H3FP4_ERR_ALIGN;
+    if (M > 0 && out->ptr == q->ptr) return H3FP4_ERR_INVALID;
+    if ((st = check_device()) != H3FP4_OK) return st;
+    if (M == 0) return H3FP4_OK;
+    job.q = in(q);
+    job.out = static_cast<__nv_bfloat16*>(out->ptr);
+    job.out_row = out->row_stride;
+    job.out_head = out->head_stride;
+    job.lse = lse;
+    job.M = M;
+    job.Hq = Hq;
+    job.causal = (flags & H3FP4_CAUSAL) != 0;
+    job.scale = scale;
+    job.ws = static_cast<uint8_t*>(ws);
+    job.wait_limit_ns = wait_limit_ns();
+    return launch_cache_attn(job, stream) == cudaSuccess ? H3FP4_OK : H3FP4_ERR_CUDA;
+}
+
+h3fp4_status h3fp4_selftest_cache_attn_timeout(void* ws, uint64_t limit_ns, cudaStream_t stream)
+{
+    if (!ws) return H3FP4_ERR_INVALID;
+    if (!aligned16(ws)) return H3FP4_ERR_ALIGN;
+    const h3fp4_status st = check_device();
+    if (st != H3FP4_OK) return st;
+    // One row of one head of 64 over a page of 16 tokens, in the workspace's last bytes: a length and a
+    // page number of 0x01010101, so that the page is full and not one of the pool's.
+    uint8_t* data = static_cast<uint8_t*>(ws) + (cache_attn_workspace_bytes(64) - 1024) / 16 * 16;
+    if (cudaMemsetAsync(data, 1, 512, stream) != cudaSuccess) return H3FP4_ERR_CUDA;
+    CacheAttnJob job{};
+    job.c.pool = data;
+    job.c.n_pages = job.c.max_pages = job.c.Hkv = job.c.nseq = 1;
+    job.c.table = job.c.length = reinterpret_cast<const int32_t*>(data);
+    job.c.page = kCacheGroup;
+    job.c.D = 64;
+    job.q = HeadsIn{reinterpret_cast<const __nv_bfloat16*>(data), 64, 64};
+    job.out = reinterpret_cast<__nv_bfloat16*>(data + 512);
+    job.out_row = job.out_head = 64;
+    job.M = job.Hq = 1;
+    job.scale = 1.0f;
+    job.ws = static_cast<uint8_t*>(ws);
+    job.wait_limit_ns = limit_ns ? limit_ns : 1;
+    job.stall = 1;
+    return launch_cache_attn(job, stream) == cudaSuccess ? H3FP4_OK : H3FP4_ERR_CUDA;
 }
 
 }  // extern "C"

@@ -469,6 +469,85 @@ H3FP4_API h3fp4_status h3fp4_block_norm(const void* x_bf16, const void* y_bf16, 
                                         float eps, void* x_out_bf16, void* out_bf16, float* out_amax, int flags,
                                         cudaStream_t stream);
 
+/* A paged cache of keys and values held in four bits, and the sequences of a call.
+ *   pool: device, 16-byte aligned, n_pages * h3fp4_cache_page_bytes(heads, dim, page)
+ *      bytes.  A page holds `page` tokens (16 to 1024, a multiple of 16) of all heads:
+ *      E2M1 codes with an E4M3 scale per 16 elements of a head, in an order of the
+ *      library's own.  dim: 16 to 256, a multiple of 16; a head takes the room of 64,
+ *      128 or 256 elements.  heads <= 4096.
+ *   table: device int32 [nseq][max_pages]: position t of sequence s lies in page
+ *      table[s][t / page] of the pool.  An entry that is no page of the pool (-1, say)
+ *      holds no tokens: rows that belong there are dropped, keys there are left out.
+ *   length: device int32 [nseq], tokens of each sequence, with the rows of this call.
+ *      What passes max_pages * page is not there.
+ *   row_off: device int32 [nseq + 1] (0 first, non-decreasing): rows
+ *      [row_off[s], row_off[s + 1]) of the call are the last ones of sequence s, so that
+ *      row r lies at position length[s] - row_off[s + 1] + r.  Rows from row_off[nseq] on
+ *      are none's: nothing is read or written for them.  NULL: row s is sequence s's
+ *      last (M = nseq).  1 <= nseq <= 1024.
+ *   k_gscale, v_gscale: device fp32 [heads] > 0, the global scales of the heads (for
+ *      instance amax / (6*448) of calibration, with room above), NULL: ones.  Elements
+ *      of 2688 times the scale and more are held as that (six times 448).
+ * Table, lengths and row offsets are read on the device when the call runs: a captured
+ * call serves whatever they hold then.  No value in them makes a call read or write
+ * outside the pool or the rows. */
+typedef struct {
+    void* pool;
+    int64_t n_pages, page, heads, dim;
+    const int32_t* table;
+    int64_t max_pages;
+    const int32_t* length;
+    const int32_t* row_off;
+    int64_t nseq;
+    const float* k_gscale;
+    const float* v_gscale;
+} h3fp4_cache;
+
+/* Bytes of one page; 0 for sizes that the cache calls refuse. */
+H3FP4_API size_t h3fp4_cache_page_bytes(int heads, int dim, int page);
+
+/* Writes the rows k, v [M][heads][dim] (views as for the attention calls) to their
+ * places in the cache, quantised as h3fp4_quantize_act does with H3FP4_GSCALE_GIVEN
+ * and the head's global scale ("H3 Runtime Current State", "Owned Performance
+ * Kernels": tensor scale/QDATA; the pages have no cache).  Inputs must be finite.
+ * The places of a call's rows must differ.  0 <= M <= 2^31 - 256. */
+H3FP4_API h3fp4_status h3fp4_cache_append(const h3fp4_heads* k, const h3fp4_heads* v, int64_t M,
+                                          const h3fp4_cache* cache, cudaStream_t stream);
+
+/* The way back: k, v [M][heads][dim] (outputs) receive bf16(e2m1 * e4m3 * s) of the
+ * rows' places, for instance a sequence's cached context for h3fp4_cross_attn or
+ * h3fp4_shared_attn.  Rows without a place are left as they are. */
+H3FP4_API h3fp4_status h3fp4_cache_read(const h3fp4_heads* k, const h3fp4_heads* v, int64_t M,
+                                        const h3fp4_cache* cache, cudaStream_t stream);
+
+/* Attention of packed query rows to the cache's keys and values of their sequences:
+ *     out[r][h] = sum_j p_j v_j / sum_j p_j,   p_j = exp(scale * q_r . k_j - m_r)
+ * over all positions j of the row's sequence, with H3FP4_CAUSAL over those up to the
+ * row's own; kv head h / (Hq / heads) for query head h.  q, out: [M][Hq][dim], Hq %
+ * heads == 0, M * Hq < 2^31.  Made for few rows per sequence (single tokens): the cache is
+ * read once per 16 columns (rows * Hq / heads); many rows are right, but h3fp4_cache_read
+ * and h3fp4_cross_attn are faster for them.
+ *   Scores, statistics and sums are fp32; keys and values enter as they are held, q
+ *   unrounded (elements below 2^-31 of the largest of their row and head are rounded),
+ *   the p_j rounded to fp16 for their product with V.
+ *   A row without a key gives out = 0 and lse = -inf; one whose largest score
+ *   scale * log2(e) * (q . k) is beyond 3e38 either way is NaN.
+ *   scale > 0, scale * log2(e) finite.  lse: fp32 [M][Hq], 4-byte aligned, or NULL.
+ *   flags: H3FP4_CAUSAL.  out may not overlap q.
+ *   ws: device workspace of h3fp4_cache_attn_workspace_bytes(dim) bytes (ws_bytes is
+ *      checked), first 256 bytes zeroed once before first use; h3fp4_check(ws) reports
+ *      device waits that timed out.  Concurrent calls must not share one workspace. */
+H3FP4_API h3fp4_status h3fp4_cache_attn(const h3fp4_heads* q, int64_t M, int Hq, const h3fp4_cache* cache, float scale,
+                                        const h3fp4_heads* out, float* lse, int flags, void* ws, size_t ws_bytes,
+                                        cudaStream_t stream);
+
+/* Workspace bytes of h3fp4_cache_attn (for any sequences); 0 for a dim it refuses. */
+H3FP4_API size_t h3fp4_cache_attn_workspace_bytes(int dim);
+
+/* Failure-detection self-test of h3fp4_cache_attn, as h3fp4_selftest_attn_timeout: its
+ * copies are left out.  ws: h3fp4_cache_attn_workspace_bytes(64) bytes. */
+H3FP4_API h3fp4_status h3fp4_selftest_cache_attn_timeout(void* ws, uint64_t limit_ns, cudaStream_t stream);
+
 /* Synchronises `stream`, reads and clears the workspace status word.
  * Returns H3FP4_OK, or H3FP4_ERR_TIMEOUT when a kernel gave up early (a
  * bounded device wait ran out, or shared memory came up misaligned); the

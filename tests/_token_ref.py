@@ -38,3 +38,64 @@ def block_norm(x, y, y_weight, gate, x_scale, weight, shift, scale, off, eps, po
     if shift is not None:
         tol = tol + 2.0 ** -22 * shift.abs()
     return out, x_out, tol, x_tol
+
+
+# E2M1's magnitudes by code, and where one code ends and the next begins (a tie goes to the even code)
+_E2M1 = torch.tensor([0.0, 0.5, 1.0, 1.5, 2.0, 3.0, 4.0, 6.0], dtype=torch.float64)
+
+
+def held(x, gscale):
+    """float64 [..., H, D] of what bf16 rows are held as: blocks of 16 under the heads' global scales (fp32 [H]), each
+    step of the format one fp32 operation, and the bf16 that comes back."""
+    s = gscale[:, None]
+    b = x.float().unflatten(-1, (-1, 16))
+    S = (b.abs().amax(-1) / 6.0 / s).clamp(max=448.0).to(torch.float8_e4m3fn).float()
+    eff = S * s
+    r = torch.where(eff == 0, torch.zeros_like(eff), (1.0 / eff).clamp(max=torch.finfo(torch.float32).max))
+    q = (b * r[..., None]).double()
+    at = q.abs()[..., None]
+    mid = (_E2M1[1:] + _E2M1[:-1]) / 2
+    even_up = torch.tensor([False, True, False, True, False, True, False])   # the upper code is even: it takes the tie
+    code = ((at > mid) | ((at == mid) & even_up)).sum(-1)
+    v = torch.where(torch.signbit(q), -_E2M1[code], _E2M1[code]) * S.double()[..., None]
+    return v.flatten(-2) * gscale.double()[:, None], (v.float() * s[..., None]).flatten(-2).to(torch.bfloat16)
+
+
+def cache_attention(q, k, v, row_off, total, causal, scale, there=None):
+    """float64 (out, lse, size, reach, keys) of rows q [M, Hq, D] over lists of each sequence's held keys and values
+    [len, H, D]; `there`: per sequence a mask of positions whose page exists.  `size`, `reach` as in _heads_ref."""
+    M, Hq, D = q.shape
+    out, size = torch.zeros(M, Hq, D, dtype=torch.float64), torch.zeros(M, Hq, D, dtype=torch.float64)
+    lse = torch.full((M, Hq), -float("inf"), dtype=torch.float64)
+    reach, keys = torch.zeros(M, Hq, dtype=torch.float64), torch.zeros(M, dtype=torch.float64)
+    for s, n in enumerate(total):
+        g = Hq // k[s].shape[1]
+        for r in range(row_off[s], row_off[s + 1]):
+            last = n - (row_off[s + 1] - r) + 1 if causal else n
+            on = torch.arange(len(k[s])) < last
+            if there is not None:
+                on &= there[s]
+            keys[r] = int(on.sum())
+            if not keys[r]:
+                continue
+            ki, vi = k[s][on].repeat_interleave(g, 1), v[s][on].repeat_interleave(g, 1)
+            z = torch.einsum("hd,khd->hk", q[r].double(), ki) * scale
+            lse[r] = torch.logsumexp(z, -1)
+            p = torch.exp(z - lse[r][:, None])
+            out[r] = torch.einsum("hk,khd->hd", p, vi)
+            size[r] = torch.einsum("hk,khd->hd", p, vi.abs())
+            reach[r] = (torch.einsum("hd,khd->hk", q[r].double().abs(), ki.abs()) * scale).amax(-1)
+    return out, lse, size, reach, keys
+
+
+def cache_attention_bounds(out, lse, size, reach, keys, top, D):
+    """Bounds of |out - ref| and |lse - ref|; `top`: the largest |v|.
+
+    A score is a sum of D exact products in fp32, each of at most D + 8 steps off by 2^-23 of the sum of magnitudes; its
+    error goes into p relatively, and once more through the sum.  The p are rounded to fp16 (2^-11) for the product with
+    V; those below 2^-25 vanish where the largest is 2^6 at least, so each key is off by 2^-31 of the largest value.  2^-11
+    covers the 2^x (2^-22), its argument and sums of up to 2^13 fp32 steps (2^-24 each, twice).  bf16 outputs: 2^-8."""
+    z = reach * (D + 8) * 2.0 ** -23
+    tol = 2.0 ** -8 * out.abs() + (2.0 ** -11 + 2.0 ** -11 + 4 * z)[..., None] * size
+    tol = tol + (keys * 2.0 ** -31 * top)[:, None, None] + 1e-38
+    return tol, 2.0 ** -11 + 2 * z + 2.0 ** -22 * lse.abs().nan_to_num(posinf=0.0)

@@ -50,3 +50,74 @@ def test_block_norm_python_checks(lib):
         A._bf16(3, "x", (4, 64))
     with pytest.raises(ValueError, match="two entries"):
         A.h3fp4_block_norm(x, x, seg_off=[4])
+
+
+def cache(pool=MB, n_pages=10, page=64, heads_=2, dim=64, table=2 * MB, max_pages=4, length=3 * MB, row_off=4 * MB,
+          nseq=3, kg=None, vg=None):
+    f = [pool or 0, n_pages, page, heads_, dim, table or 0, max_pages, length or 0, row_off or 0, nseq, kg or 0, vg or 0]
+    return C.byref((C.c_int64 * 12)(*f))
+
+
+def view(ptr=5 * MB, row=256, head=64):
+    from audio_dit_gb300 import _Heads
+    return C.byref(_Heads(ptr, row, head))
+
+
+def rows_call(lib, fn="h3fp4_cache_append", k=None, v=None, M=3, **kw):
+    return getattr(lib, fn)(k or view(), v or view(6 * MB), M, cache(**kw), None)
+
+
+def attend(lib, q=None, M=3, Hq=4, scale=0.1, out=None, lse=None, flags=4096, ws=8 * MB, ws_bytes=1 << 40, **kw):
+    return lib.h3fp4_cache_attn(q or view(), M, Hq, cache(**kw), scale, out or view(7 * MB), lse, flags, ws, ws_bytes, None)
+
+
+def test_cache_refusals(lib):
+    for call in (lambda **k: rows_call(lib, **k), lambda **k: rows_call(lib, "h3fp4_cache_read", **k),
+                 lambda **k: attend(lib, **k)):
+        for kw in (dict(dim=0), dict(dim=8), dict(dim=72), dict(dim=272), dict(heads_=0), dict(heads_=4097), dict(page=8),
+                   dict(page=24), dict(page=1040), dict(nseq=0), dict(nseq=1025), dict(n_pages=0), dict(n_pages=1 << 31),
+                   dict(max_pages=0), dict(max_pages=1 << 31), dict(M=-1), dict(M=(1 << 31) - 255)):
+            assert call(**kw) == SHAPE, kw
+        for kw in (dict(pool=None), dict(table=None), dict(length=None), dict(row_off=None, M=2)):
+            assert call(**kw) == INVALID, kw
+        for kw in (dict(pool=MB + 8), dict(table=MB + 2), dict(length=MB + 1), dict(row_off=MB + 2), dict(kg=MB + 2),
+                   dict(vg=MB + 3)):
+            assert call(**kw) == ALIGN, kw
+    for kw in (dict(k=view(0)), dict(v=view(0)), dict(fn="h3fp4_cache_read", k=view(0)),
+               dict(fn="h3fp4_cache_read", v=view(5 * MB)), dict(fn="h3fp4_cache_read", k=view(row=64))):
+        assert rows_call(lib, **kw) == INVALID, kw
+    for kw in (dict(k=view(5 * MB + 2)), dict(v=view(row=4)), dict(v=view(head=-64))):
+        assert rows_call(lib, **kw) == ALIGN, kw
+    for kw in (dict(Hq=0), dict(Hq=3), dict(M=1 << 29)):
+        assert attend(lib, **kw) == SHAPE, kw
+    for kw in (dict(flags=1), dict(scale=0.0), dict(scale=float("nan")), dict(scale=float("inf")), dict(scale=3e38),
+               dict(q=view(0)), dict(out=view(0)), dict(out=view()), dict(out=view(7 * MB, 64, 64)), dict(ws=None),
+               dict(ws_bytes=1000)):
+        assert attend(lib, **kw) == INVALID, kw
+    for kw in (dict(q=view(5 * MB + 8)), dict(out=view(row=260)), dict(ws=8 * MB + 8), dict(lse=MB + 2)):
+        assert attend(lib, **kw) == ALIGN, kw
+    assert lib.h3fp4_cache_append(view(), view(), 3, None, None) == INVALID
+    assert lib.h3fp4_selftest_cache_attn_timeout(None, 1, None) == INVALID
+    assert lib.h3fp4_selftest_cache_attn_timeout(C.c_void_p(4104), 1, None) == ALIGN
+
+
+def test_cache_sizes(lib):
+    import torch
+
+    import audio_dit_gb300 as A
+    for heads_, D, page, width in ((2, 64, 16, 64), (1, 16, 32, 64), (8, 80, 64, 128), (3, 256, 1024, 256), (1, 144, 16, 256)):
+        assert A.h3fp4_cache_page_bytes(heads_, D, page) == heads_ * page * width * 9 // 8
+        c = A.alloc_kv_cache(5, heads_, D, page, device="cpu")
+        assert c.numel() == 5 * A.h3fp4_cache_page_bytes(heads_, D, page)
+    for bad in ((0, 64, 16), (1, 24, 16), (1, 64, 40), (1, 64, 2048), (1, 512, 16)):
+        assert A.h3fp4_cache_page_bytes(*bad) == 0
+        with pytest.raises(ValueError, match="refuse"):
+            A.alloc_kv_cache(5, *bad, device="cpu")
+    assert A.h3fp4_cache_attn_workspace_bytes(64) < A.h3fp4_cache_attn_workspace_bytes(256)
+    assert A.h3fp4_cache_attn_workspace_bytes(40) == 0
+    for bad in ((1, 1, 3, 2, 64), (1, 0, 2, 2, 64), (1, 1, 2, 2, 60)):
+        with pytest.raises(ValueError, match="refuse"):
+            A.alloc_cache_attn_workspace(*bad, device="cpu")
+    x, t = torch.zeros(3, 2, 64, dtype=torch.bfloat16), torch.zeros(3, 4, dtype=torch.int32)
+    with pytest.raises(ValueError, match="CUDA"):
+        A.h3fp4_cache_append(x, x, A.alloc_kv_cache(5, 2, 64, 16, device="cpu"), t, t[:, 0])
