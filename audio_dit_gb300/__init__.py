@@ -28,7 +28,8 @@ __all__ = [
     "h3fp4_set_wait_limit_ns", "h3fp4_status_string", "alloc_nvfp4", "alloc_workspace",
     "h3fp4_block_norm", "NORM_POST", "NORM_LAYER", "CAUSAL", "h3fp4_cache_append", "h3fp4_cache_read",
     "h3fp4_cache_attn", "h3fp4_cache_page_bytes", "h3fp4_cache_attn_workspace_bytes", "alloc_kv_cache",
-    "alloc_cache_attn_workspace", "h3fp4_selftest_cache_attn_timeout",
+    "alloc_cache_attn_workspace", "h3fp4_linear_rows",
+    "h3fp4_linear_rows_workspace_bytes", "alloc_rows_workspace", "ROWS_MAX", "h3fp4_selftest_cache_attn_timeout",
 ]
 
 PROLOGUE_MOD = 1
@@ -45,6 +46,7 @@ NORM_LAYER = 2048
 CAUSAL = 4096
 MAX_SEGMENTS = 8
 ATTN_MAX_SEGMENTS = 256
+ROWS_MAX = 64
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 _lib = None
@@ -104,6 +106,8 @@ def load_library():
         "h3fp4_selftest_attn_timeout": (i32, [vp, C.c_uint64, vp]),
         "h3fp4_block_norm": (i32, [vp, vp, i64, i64, vp, vp, C.c_float, vp, vp, vp, vp, i32, C.c_float, vp, vp, vp, i32,
                                    vp]),
+        "h3fp4_linear_rows": (i32, [vp, i64, i64, i64, vp, vp, vp, vp, i64, vp, vp, vp, i32, vp, sz, vp]),
+        "h3fp4_linear_rows_workspace_bytes": (sz, [i64, i64, i64]),
         "h3fp4_cache_page_bytes": (sz, [i32, i32, i32]),
         "h3fp4_cache_append": (i32, [hp, hp, i64, vp, vp]),
         "h3fp4_cache_read": (i32, [hp, hp, i64, vp, vp]),
@@ -555,6 +559,39 @@ def h3fp4_block_norm(x: torch.Tensor, out: Optional[torch.Tensor] = None, *, y: 
         (NORM_POST if post_norm else 0) | (NORM_LAYER if layer_norm else 0), _stream(stream)), "h3fp4_block_norm")
 
 
+def h3fp4_linear_rows(x: torch.Tensor, w_codes: torch.Tensor, w_sf: torch.Tensor, w_gscale: torch.Tensor,
+                      out: torch.Tensor, ws: torch.Tensor, *, bias: Optional[torch.Tensor] = None,
+                      gate: Optional[torch.Tensor] = None, resid: Optional[torch.Tensor] = None, swiglu: bool = False,
+                      stream=None) -> None:
+    """out = [resid + gate *](x . W^T [+ bias]) of a few rows x bf16 [M, K] (M <= ROWS_MAX) over NVFP4 weights; x is not
+    quantised.
+
+    ``gate``: fp32 [M, N], or [N] for all rows, with ``resid`` bf16 [M, N] (which may be ``out``).  ``swiglu``: out is
+    [M, N/2] = bf16(silu(g) * u) over the weight's [gate 128 | up 128] row groups.  ``ws`` from
+    :func:`alloc_rows_workspace`."""
+    M, K = x.shape
+    N = out.shape[1] * (2 if swiglu else 1)
+    stride = 0
+    if gate is not None:
+        stride = N if gate.dim() == 2 else 0
+        gate_shape = (M, N) if stride else (N,)
+    if w_codes.shape != (N, K // 2):
+        raise ValueError(f"w_codes must be {[N, K // 2]}, got {list(w_codes.shape)}")
+    if w_sf.numel() != (N + 127) // 128 * 8 * K:
+        raise ValueError(f"w_sf must have {(N + 127) // 128 * 8 * K} elements, got {w_sf.numel()}")
+    flags = ((EPI_BIAS if bias is not None else 0) | (EPI_GATE_RESID if gate is not None else 0)
+             | (EPI_SWIGLU if swiglu else 0))
+    _check(load_library().h3fp4_linear_rows(
+        _bf16(x, "x", x.shape), M, N, K, _ptr(w_codes, "w_codes", torch.uint8), _ptr(w_sf, "w_sf", torch.uint8),
+        _f32(w_gscale, "w_gscale", (1,)), None if gate is None else _f32(gate, "gate", gate_shape), stride,
+        _bf16(bias, "bias", (N,)), _bf16(resid, "resid", (M, N)), _bf16(out, "out", (M, N // 2 if swiglu else N)), flags,
+        _workspace(ws), ws.numel(), _stream(stream)), "h3fp4_linear_rows")
+
+
+def h3fp4_linear_rows_workspace_bytes(M: int, N: int, K: int) -> int:
+    return int(load_library().h3fp4_linear_rows_workspace_bytes(M, N, K))
+
+
 def _i32(t: Optional[torch.Tensor], what: str, shape):
     if t is None:
         return 0
@@ -674,6 +711,14 @@ def alloc_attn_workspace(M: int, T: int, Hq: int, Hkv: int, D: int, q_off: Optio
     n = h3fp4_attn_workspace_bytes(M, T, Hq, Hkv, D, q_off, kv_off, ctx)
     if n == 0:
         raise ValueError("sizes or segment tables that the attention calls refuse")
+    return torch.zeros(n, dtype=torch.uint8, device=device)
+
+
+def alloc_rows_workspace(M: int, N: int, K: int, device="cuda") -> torch.Tensor:
+    """Workspace of :func:`h3fp4_linear_rows` for these sizes."""
+    n = h3fp4_linear_rows_workspace_bytes(M, N, K)
+    if n == 0:
+        raise ValueError("sizes that the linear of a few rows refuses")
     return torch.zeros(n, dtype=torch.uint8, device=device)
 
 

@@ -82,4 +82,26 @@ struct CacheAttnJob {
 size_t cache_attn_workspace_bytes(int D);
 cudaError_t launch_cache_attn(const CacheAttnJob& job, cudaStream_t s);
 
+constexpr int kRowsMax = 64;           // rows of the linear of a few rows
+
+struct LinearRowsJob {
+    const __nv_bfloat16* x;   // [M][K]
+    const uint8_t* w_codes;   // [N][K/2]
+    const uint8_t* w_sf;
+    const float* w_gscale;
+    const float* gate;        // or null: row m at gate + m * gate_stride
+    int64_t gate_stride;
+    const __nv_bfloat16* bias;   // [N] or null
+    const __nv_bfloat16* resid;  // [M][N], with gate
+    __nv_bfloat16* out;       // [M][N], or [M][N/2] with swiglu
+    bool swiglu;
+    int64_t M, N, K;
+    uint8_t* ws;
+    uint64_t wait_limit_ns;
+    int stall;                // self-test: no copies, so every wait runs out
+};
+
+size_t linear_rows_workspace_bytes(int64_t M, int64_t N, int64_t K);
+cudaError_t launch_linear_rows(const LinearRowsJob& job, cudaStream_t s);
+
 }  // namespace h3fp4

@@ -1,5 +1,5 @@
-// C ABI of a token's way through a block (h3fp4_block_norm, h3fp4_cache_append,
-// h3fp4_cache_read, h3fp4_cache_attn): argument validation and job set-up.  Nothing here allocates device memory or synchronises.
+// C ABI of a token's way through a block (h3fp4_block_norm, h3fp4_linear_rows,
+// h3fp4_cache_append, h3fp4_cache_read, h3fp4_cache_attn): argument validation and job set-up.  Nothing here allocates device memory or synchronises.
 #include <cmath>
 #include <cstdint>
 
@@ -66,6 +66,13 @@ h3fp4_status cache_rows(const h3fp4_heads* k, const h3fp4_heads* v, int64_t M, c
     return e == cudaSuccess ? H3FP4_OK : H3FP4_ERR_CUDA;
 }
 
+h3fp4_status rows_shape(int64_t M, int64_t N, int64_t K)
+{
+    if (M < 1 || M > kRowsMax || N < 8 || N % 8 != 0 || N > (1 << 24)) return H3FP4_ERR_SHAPE;
+    if (K < 64 || K % 64 != 0 || K > (1 << 20)) return H3FP4_ERR_SHAPE;
+    return H3FP4_OK;
+}
+
 }  // namespace
 }  // namespace h3fp4
 
@@ -120,6 +127,53 @@ h3fp4_status h3fp4_block_norm(const void* x, const void* y, int64_t M, int64_t K
     job.M = M;
     job.K = (int)K;
     return launch_block_norm(job, stream) == cudaSuccess ? H3FP4_OK : H3FP4_ERR_CUDA;
+}
+
+size_t h3fp4_linear_rows_workspace_bytes(int64_t M, int64_t N, int64_t K)
+{
+    return rows_shape(M, N, K) == H3FP4_OK ? linear_rows_workspace_bytes(M, N, K) : 0;
+}
+
+h3fp4_status h3fp4_linear_rows(const void* x, int64_t M, int64_t N, int64_t K, const void* w_codes, const void* w_sf,
+                               const float* w_gscale, const float* gate, int64_t gate_stride, const void* bias,
+                               const void* resid, void* out, int flags, void* ws, size_t ws_bytes, cudaStream_t stream)
+{
+    h3fp4_status st = rows_shape(M, N, K);
+    if (st != H3FP4_OK) return st;
+    if (flags & ~(H3FP4_EPI_BIAS | H3FP4_EPI_GATE_RESID | H3FP4_EPI_SWIGLU)) return H3FP4_ERR_INVALID;
+    const bool swiglu = (flags & H3FP4_EPI_SWIGLU) != 0, gated = (flags & H3FP4_EPI_GATE_RESID) != 0;
+    if (swiglu && gated) return H3FP4_ERR_INVALID;
+    if (swiglu && N % 256 != 0) return H3FP4_ERR_SHAPE;
+    if (!x || !w_codes || !w_sf || !w_gscale || !out || !ws) return H3FP4_ERR_INVALID;
+    if (((flags & H3FP4_EPI_BIAS) != 0) != (bias != nullptr) || gated != (gate != nullptr) ||
+        gated != (resid != nullptr))
+        return H3FP4_ERR_INVALID;
+    if (gated && gate_stride != 0 && gate_stride < N) return H3FP4_ERR_INVALID;
+    for (const void* p : {x, w_codes, w_sf, bias, resid, static_cast<const void*>(out), static_cast<const void*>(ws)})
+        if (!aligned16(p)) return H3FP4_ERR_ALIGN;
+    if (!aligned4(w_gscale) || !aligned4(gate)) return H3FP4_ERR_ALIGN;
+    if (ws_bytes < linear_rows_workspace_bytes(M, N, K)) return H3FP4_ERR_INVALID;
+    // resid may be out itself; nothing else may overlap it
+    const int64_t outs = M * (swiglu ? N / 2 : N) * 2;
+    if (out == x || (gated && out != resid && overlap(out, resid, outs))) return H3FP4_ERR_INVALID;
+    if ((st = check_device()) != H3FP4_OK) return st;
+    LinearRowsJob job{};
+    job.x = static_cast<const __nv_bfloat16*>(x);
+    job.w_codes = static_cast<const uint8_t*>(w_codes);
+    job.w_sf = static_cast<const uint8_t*>(w_sf);
+    job.w_gscale = w_gscale;
+    job.gate = gate;
+    job.gate_stride = gate_stride;
+    job.bias = static_cast<const __nv_bfloat16*>(bias);
+    job.resid = static_cast<const __nv_bfloat16*>(resid);
+    job.out = static_cast<__nv_bfloat16*>(out);
+    job.swiglu = swiglu;
+    job.M = M;
+    job.N = N;
+    job.K = K;
+    job.ws = static_cast<uint8_t*>(ws);
+    job.wait_limit_ns = wait_limit_ns();
+    return launch_linear_rows(job, stream) == cudaSuccess ? H3FP4_OK : H3FP4_ERR_CUDA;
 }
 
 size_t h3fp4_cache_page_bytes(int heads, int dim, int page)

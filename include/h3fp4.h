@@ -117,6 +117,7 @@ enum {
 
 #define H3FP4_MAX_SEGMENTS 8
 #define H3FP4_ATTN_MAX_SEGMENTS 256
+#define H3FP4_ROWS_MAX 64
 
 /* Bytes of the E2M1 codes of a [rows, K] operand: rows * K / 2. */
 H3FP4_API size_t h3fp4_codes_bytes(int64_t rows, int64_t K);
@@ -468,6 +469,30 @@ H3FP4_API h3fp4_status h3fp4_block_norm(const void* x_bf16, const void* y_bf16, 
                                         const float* shift, const float* scale, const int64_t* seg_off, int nseg,
                                         float eps, void* x_out_bf16, void* out_bf16, float* out_amax, int flags,
                                         cudaStream_t stream);
+
+/* The linear of a few rows (a token of each sequence, say) over NVFP4 weights: as
+ * h3fp4_linear, with the activations as they are instead of quantised
+ *     out = bf16(R + g * (s_w * (x . W_q^T) + b))  or  bf16(s_w * (x . W_q^T) + b)
+ * ("H3 Blackwell Runtime" README, "Checkpoints": pre-quantised weights).  Sums are fp32; x
+ * enters with an error of at most 2^-22 of the largest magnitude of its block of 16.
+ *   x: bf16 [M][K], finite, 1 <= M <= H3FP4_ROWS_MAX; K % 64 == 0, K <= 2^20; N % 8 == 0,
+ *      N <= 2^24.
+ *   w_codes, w_sf, w_gscale: output of h3fp4_quantize_weight.
+ *   flags: H3FP4_EPI_BIAS (bias bf16 [N]); H3FP4_EPI_GATE_RESID (gate fp32, row m's at
+ *      gate + m * gate_stride, gate_stride >= N or 0 for one gate of all rows; resid bf16
+ *      [M][N]); H3FP4_EPI_SWIGLU as in h3fp4_linear (N % 256 == 0, W's [gate 128 | up
+ *      128] row groups, out [M][N/2], not with a gate).
+ *   out: bf16, may be resid itself and overlaps nothing else.
+ *   ws: device workspace of h3fp4_linear_rows_workspace_bytes(M, N, K) bytes (ws_bytes is
+ *      checked), first 256 bytes zeroed once before first use; h3fp4_check(ws) reports
+ *      device waits that timed out.  Concurrent calls must not share one workspace. */
+H3FP4_API h3fp4_status h3fp4_linear_rows(const void* x_bf16, int64_t M, int64_t N, int64_t K, const void* w_codes,
+                                         const void* w_sf, const float* w_gscale, const float* gate,
+                                         int64_t gate_stride, const void* bias_bf16, const void* resid_bf16,
+                                         void* out_bf16, int flags, void* ws, size_t ws_bytes, cudaStream_t stream);
+
+/* Workspace bytes of h3fp4_linear_rows; 0 for sizes it refuses. */
+H3FP4_API size_t h3fp4_linear_rows_workspace_bytes(int64_t M, int64_t N, int64_t K);
 
 /* A paged cache of keys and values held in four bits, and the sequences of a call.
  *   pool: device, 16-byte aligned, n_pages * h3fp4_cache_page_bytes(heads, dim, page)

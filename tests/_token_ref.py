@@ -99,3 +99,40 @@ def cache_attention_bounds(out, lse, size, reach, keys, top, D):
     tol = 2.0 ** -8 * out.abs() + (2.0 ** -11 + 2.0 ** -11 + 4 * z)[..., None] * size
     tol = tol + (keys * 2.0 ** -31 * top)[:, None, None] + 1e-38
     return tol, 2.0 ** -11 + 2 * z + 2.0 ** -22 * lse.abs().nan_to_num(posinf=0.0)
+
+
+def decode_weight(codes, sf, gscale, K):
+    """float64 (W [N, K], the magnitudes) of NVFP4 codes, their 128x4-tiled block scales and the global scale."""
+    N = codes.shape[0]
+    values = torch.cat([_E2M1, -_E2M1])
+    w = values[torch.stack([codes & 15, codes >> 4], -1).flatten(-2).long()]
+    r, c = torch.arange(N)[:, None], torch.arange(K // 16)[None]
+    at = ((r // 128) * (K // 64) + c // 4) * 512 + (r % 32) * 16 + (r % 128) // 32 * 4 + c % 4
+    S = sf.view(torch.float8_e4m3fn).double()[at]
+    return w * S.repeat_interleave(16, 1) * float(gscale)
+
+
+def linear_rows(x, w, bias, gate, resid, swiglu):
+    """float64 (out, tolerance) of the linear of a few rows, with bounds in the manner of the linear's.
+
+    A sum of K exact products is accumulated in fp32 (1e-5 of the sum of magnitudes, the linear's own), x enters with an
+    error of at most 2^-22 of the largest of its block of 16; the output is rounded to bf16 once (2^-8)."""
+    a = x.double()
+    y, size = a @ w.T, a.abs() @ w.abs().T
+    top = a.abs().unflatten(-1, (-1, 16)).amax(-1).repeat_interleave(16, -1)
+    off = 1e-5 * size + 2.0 ** -22 * (top @ w.abs().T)
+    if bias is not None:
+        y = y + bias.double()
+        off = off + 2.0 ** -22 * bias.double().abs()
+    if swiglu:
+        # the bf16 outputs g and u are off by their bounds; |silu'| <= 1.1; the fp32 evaluation 2^-17, h to bf16 2^-8
+        tol = 2.0 ** -8 * y.abs() + off
+        (g, u), (tg, tu) = (t.unflatten(-1, (-1, 2, 128)).unbind(-2) for t in (y, tol))
+        g, u, tg, tu = (t.flatten(-2) if t.dim() > 2 else t for t in (g, u, tg, tu))
+        s = g * torch.sigmoid(g)
+        first = (s.abs() + 1.1 * tg) * tu + 1.1 * tg * u.abs()
+        return s * u, first + (2.0 ** -8 + 2.0 ** -17) * ((s * u).abs() + first) + 1e-38
+    if gate is not None:
+        y, off = resid.double() + gate.double() * y, gate.double().abs() * off
+        off = off + 2.0 ** -22 * (resid.double().abs() + y.abs())
+    return y, 2.0 ** -8 * y.abs() + off + 1e-38

@@ -121,3 +121,42 @@ def test_cache_sizes(lib):
     x, t = torch.zeros(3, 2, 64, dtype=torch.bfloat16), torch.zeros(3, 4, dtype=torch.int32)
     with pytest.raises(ValueError, match="CUDA"):
         A.h3fp4_cache_append(x, x, A.alloc_kv_cache(5, 2, 64, 16, device="cpu"), t, t[:, 0])
+
+
+def rows(lib, x=MB, M=4, N=256, K=128, wc=2 * MB, wsf=3 * MB, wg=4 * MB, gate=None, stride=0, bias=None, resid=None,
+         out=5 * MB, flags=0, ws=6 * MB, ws_bytes=1 << 40):
+    return lib.h3fp4_linear_rows(x, M, N, K, wc, wsf, wg, gate, stride, bias, resid, out, flags, ws, ws_bytes, None)
+
+
+def test_linear_rows_refusals(lib):
+    G = dict(flags=4, gate=7 * MB, resid=8 * MB)
+    for kw in (dict(M=0), dict(M=65), dict(M=-1), dict(N=0), dict(N=12), dict(N=(1 << 24) + 8), dict(K=0), dict(K=96),
+               dict(K=(1 << 20) + 64), dict(flags=64, N=128)):
+        assert rows(lib, **kw) == SHAPE, kw
+    for kw in (dict(x=None), dict(wc=None), dict(wsf=None), dict(wg=None), dict(out=None), dict(ws=None), dict(ws_bytes=0),
+               dict(flags=1), dict(flags=2), dict(bias=7 * MB), dict(gate=7 * MB), dict(flags=4), dict(flags=4, gate=7 * MB),
+               dict(flags=4, resid=7 * MB), {**G, "flags": 68}, {**G, "stride": 255}, {**G, "stride": -1},
+               {**G, "resid": 5 * MB + 16}, dict(out=MB)):
+        assert rows(lib, **kw) == INVALID, kw
+    for kw in (dict(x=MB + 2), dict(wc=2 * MB + 8), dict(wsf=3 * MB + 8), dict(wg=4 * MB + 2), dict(out=5 * MB + 4),
+               dict(ws=6 * MB + 8), dict(flags=2, bias=7 * MB + 2), {**G, "gate": 7 * MB + 2}, {**G, "resid": 8 * MB + 8}):
+        assert rows(lib, **kw) == ALIGN, kw
+
+
+def test_linear_rows_python_checks(lib):
+    import torch
+
+    import audio_dit_gb300 as A
+    assert A.ROWS_MAX == 64 and A.h3fp4_linear_rows_workspace_bytes(1, 8, 64) >= 256
+    for bad in ((65, 8, 64), (0, 8, 64), (1, 4, 64), (1, 8, 32)):
+        assert A.h3fp4_linear_rows_workspace_bytes(*bad) == 0
+        with pytest.raises(ValueError, match="refuse"):
+            A.alloc_rows_workspace(*bad, device="cpu")
+    x, o = torch.zeros(2, 64, dtype=torch.bfloat16), torch.zeros(2, 128, dtype=torch.bfloat16)
+    codes, sf, g = torch.zeros(128, 32, dtype=torch.uint8), torch.zeros(512, dtype=torch.uint8), torch.ones(1)
+    with pytest.raises(ValueError, match="CUDA"):
+        A.h3fp4_linear_rows(x, codes, sf, g, o, sf)
+    with pytest.raises(ValueError, match="w_codes"):
+        A.h3fp4_linear_rows(x, codes[:64], sf, g, o, sf)
+    with pytest.raises(ValueError, match="w_sf"):
+        A.h3fp4_linear_rows(x, codes, sf[:256], g, o, sf)
