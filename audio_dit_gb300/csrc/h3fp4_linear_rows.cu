@@ -2,41 +2,457 @@
 //
 //     out[m][n] = bf16( R[m][n] + g[m][n] * (s_w * sum_k x[m][k] W[n][k] + b[n]) )
 //
-// or the SwiGLU of gate and up rows.  It has to read the weights, 9/16 byte an element.
-// A warp takes a row of W (with SwiGLU its gate and up row), a lane a block of 16 at a time.
+// or the SwiGLU of gate and up rows.  It has to read the weights, 9/16 byte an element: bound by
+// HBM as long as nothing on the way needs an instruction per element.  So the weights go from
+// memory to the FP4 matrix unit as they are (TMA, tcgen05.mma.kind::mxf4nvf4; W's rows are the
+// 128 rows of A), and x comes to them: each row is written as the sum of kDigits = 8 rows of
+// E2M1 digits in base 8,
+//     x[k] = 2^(e_b) sum_t d_t[k] 8^-t,   |d_t| <= 4,  d_t = e2m1(what is left, in units of 8^-t),
+// e_b the exponent of x's block of 16.  Up to 4, E2M1's steps are at most 1, so what is left
+// shrinks by 8 each time: eight digits are exact for elements within 2^-16 of their block's
+// largest and within 2^-23 of it otherwise.  All digits of a block share its scale
+// 2^(e_b - e_row + 8), a power of two that E4M3 holds for 17 binades; e_row is the row's.  The
+// matrix unit multiplies 8 M <= 256 digit rows by each W tile in the time that the tile takes
+// to arrive (M = 32: 128 of 199 cycles); more than 32 rows take two passes over the tile, the
+// second from L2.  The products and the sums of 16 are exact, the accumulators fp32.
+//
+// Three kernels: digits_kernel writes the digits, their scales and the rows' factors;
+// rows_gemm_kernel multiplies.  Its work is one row of (W tile, pass, 256-column K stage), cut
+// evenly over one CTA per SM, and the sums of each (tile, CTA) piece go to the workspace;
+// rows_join_kernel adds the pieces of a tile in order and finishes the outputs.  The same call
+// gives the same bits.  Each starts while the one before it drains; the first W tiles are on
+// their way before the digits are there.
 #include <cstdint>
 
+#include <cuda.h>
 #include <cuda_bf16.h>
 
 #include "act_prologue.cuh"
 #include "h3fp4_token.h"
 #include "nvfp4_encode.cuh"
 #include "ptx_sm103.cuh"
+#include "tensor_map.h"
 
 namespace h3fp4 {
 namespace {
 
-constexpr int kThreads = 128;
-constexpr int kRowsAtOnce = 8;
+constexpr int kDigits = 8;
+constexpr int kPassRows = 32;                          // rows of x per pass: 256 digit rows
+constexpr int BM = 128;                                // rows of W per tile
+constexpr int BK = 256;                                // columns per stage
+constexpr int kMaxCtas = 160;
+constexpr int kThreads = 384;                          // producer, MMA, 2 idle; 4 scale warps; 4 epilogue warps
+constexpr uint32_t kWBytes = BM * BK / 2;
+constexpr uint32_t kSfwBytes = BM * (BK / 16);
+constexpr uint32_t kSfBox = 2048;                      // a stage's scale tiles of 128 rows
+constexpr uint32_t kTmemCols = 512;
 
-struct RowsParams {
-    LinearRowsJob j;
+// Digit rows that a CTA takes at once, and what fits beside them: the ring's stages, the
+// accumulators (two where they fit, so that one drains while the other fills), the scales.
+template <int NB>
+struct Plan {
+    static constexpr int kHalves = (NB + 127) / 128;   // scale tiles of the digits
+    static constexpr int kStages = NB <= 64 ? 7 : NB <= 128 ? 6 : 4;
+    static constexpr int kAccs = NB <= 128 ? 2 : 1;
+    static constexpr uint32_t kDBytes = NB * BK / 2;
+    static constexpr uint32_t kStage = kWBytes + kDBytes + kSfwBytes + kHalves * kSfBox;
+    static constexpr uint32_t kSfTmem = kAccs * NB;
+    static constexpr uint32_t kSfCols = 16 + 16 * kHalves;
+    static constexpr uint32_t kBarOff = kStages * kStage;
+    static constexpr uint32_t kSmem = kBarOff + 8 * (3 * kStages + 2 * kAccs + 1) + 16;
+    static_assert(kStage % 1024 == 0, "stages keep the swizzle's alignment");
+    static_assert(kSfTmem + kStages * kSfCols <= kTmemCols, "TMEM budget");
+    static_assert(kSmem <= 232448, "shared memory budget");
 };
 
-__device__ __forceinline__ float2 e2m1_pair(uint32_t byte)
+// Workspace: status, the rows' factors, digit codes, digit scales, pieces.
+struct Layout {
+    int passes, pass_rows;    // rows of x per pass, the last may have fewer
+    int64_t digit_rows;       // rows of the code matrix: pass p's begin at 256 p
+    int64_t tiles, kb4;
+    size_t codes, scales, parts, bytes;
+};
+
+constexpr size_t kFactors = 256;
+
+inline Layout layout(int64_t M, int64_t N, int64_t K)
 {
-    float lo, hi;
-    asm("{\n\t.reg .b8 a, b, c, d;\n\t.reg .b32 h2;\n\t.reg .b16 l, h;\n\t"
-        "mov.b32 {a, b, c, d}, %2;\n\t"
-        "cvt.rn.f16x2.e2m1x2 h2, a;\n\t"
-        "mov.b32 {l, h}, h2;\n\t"
-        "cvt.f32.f16 %0, l;\n\t"
-        "cvt.f32.f16 %1, h;\n\t}"
-        : "=f"(lo), "=f"(hi)
-        : "r"(byte));
-    return make_float2(lo, hi);
+    Layout l{};
+    l.passes = (int)((M + kPassRows - 1) / kPassRows);
+    l.pass_rows = (int)((M + l.passes - 1) / l.passes);
+    l.digit_rows = 256 * (l.passes - 1) + kDigits * l.pass_rows;
+    l.tiles = (N + BM - 1) / BM;
+    l.kb4 = K / 64;
+    auto round = [](size_t x) { return (x + 255) / 256 * 256; };
+    l.codes = round(kFactors + kRowsMax * sizeof(float));
+    l.scales = l.codes + round((size_t)l.digit_rows * (size_t)(K / 2));
+    l.parts = l.scales + round((size_t)((l.digit_rows + 127) / 128) * (size_t)l.kb4 * 512);
+    l.bytes = l.parts + (size_t)(l.tiles * l.passes + kMaxCtas) * l.pass_rows * BM * sizeof(float);
+    return l;
 }
 
+// 2^x for x in the normal range.
+__device__ __forceinline__ float pow2i(int x) { return __uint_as_float((uint32_t)(x + 127) << 23); }
+
+// ------------------------------------------------------------------ digits
+
+constexpr int kDigitThreads = 128;
+constexpr int kDigitColumns = kDigitThreads * 8;   // of x per CTA
+
+// Block (columns, row): the digits of 1024 columns of a row, two threads a block of 16.
+__global__ void __launch_bounds__(kDigitThreads)
+    digits_kernel(const __nv_bfloat16* x, int K, int pass_rows, int kb4, uint8_t* codes, uint8_t* scales, float* factors)
+{
+    __shared__ uint32_t tops[kDigitThreads / 32];
+    const int m = blockIdx.y, t = threadIdx.x, lane = t & 31;
+    const __nv_bfloat16* row = x + (long long)m * K;
+    griddep_wait();
+    griddep_launch_dependents();   // the weights may be fetched: nothing before this call writes them any more
+    // the row's largest magnitude (non-negative bf16 values order like their bits)
+    auto top2 = [](uint32_t w) { return max(w & 0x7FFFu, (w >> 16) & 0x7FFFu); };
+    auto top8 = [&](const uint4& v) { return max(max(top2(v.x), top2(v.y)), max(top2(v.z), top2(v.w))); };
+    uint32_t top = 0;
+#pragma unroll 4
+    for (int i = t; i < K / 8; i += kDigitThreads) top = max(top, top8(reinterpret_cast<const uint4*>(row)[i]));
+    top = __reduce_max_sync(0xffffffffu, top);
+    if (lane == 0) tops[t >> 5] = top;
+    __syncthreads();
+    top = max(max(tops[0], tops[1]), max(tops[2], tops[3]));
+    const int e_row = max(1, (int)(top >> 7)) - 127 - 1;   // digits of the largest lie in [2, 4)
+    if (blockIdx.x == 0 && t == 0) {
+        // 2^(e_row - 8): the scales are that much larger (in two factors, either may be subnormal together)
+        factors[m] = pow2i(e_row / 2) * pow2i(e_row - e_row / 2 - 8);
+    }
+    const int col = blockIdx.x * kDigitColumns + 8 * t;
+    const bool real = col < K;
+    uint4 v = make_uint4(0, 0, 0, 0);
+    if (real) v = *reinterpret_cast<const uint4*>(row + col);
+    uint32_t btop = top8(v);
+    btop = max(btop, __shfl_xor_sync(0xffffffffu, btop, 1));
+    // binades below the row's largest, as far as E4M3 goes: 2^8 down to 2^-9
+    const int below = min(17, e_row - (max(1, (int)(btop >> 7)) - 127 - 1));
+    const int k = 8 - below;
+    const uint32_t S = k >= -6 ? (uint32_t)(k + 7) << 3 : 1u << (k + 9);
+    const int e = below - e_row;   // what x is scaled with: two factors, as the sum may pass 127
+    const float up0 = pow2i(e / 2), up1 = pow2i(e - e / 2);
+    float r[8];
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        r[2 * i] = bf16_lo(w[i]) * up0 * up1;
+        r[2 * i + 1] = bf16_hi(w[i]) * up0 * up1;
+    }
+    const int pass = m / pass_rows, r0 = 256 * pass + kDigits * (m - pass * pass_rows);
+#pragma unroll
+    for (int d = 0; d < kDigits; ++d) {
+        const uint32_t c = e2m1x8(r);
+        if (real) *reinterpret_cast<uint32_t*>(codes + (long long)(r0 + d) * (K / 2) + col / 2) = c;
+        uint32_t q[4];
+        asm("{\n\t.reg .b8 a, b, c, d;\n\t"
+            "mov.b32 {a, b, c, d}, %4;\n\t"
+            "cvt.rn.f16x2.e2m1x2 %0, a;\n\t"
+            "cvt.rn.f16x2.e2m1x2 %1, b;\n\t"
+            "cvt.rn.f16x2.e2m1x2 %2, c;\n\t"
+            "cvt.rn.f16x2.e2m1x2 %3, d;\n\t}"
+            : "=r"(q[0]), "=r"(q[1]), "=r"(q[2]), "=r"(q[3])
+            : "r"(c));
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            float lo, hi;
+            asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\tcvt.f32.f16 %0, l;\n\tcvt.f32.f16 %1, h;\n\t}"
+                : "=f"(lo), "=f"(hi)
+                : "r"(q[i]));
+            r[2 * i] = (r[2 * i] - lo) * 8.0f;   // (exact)
+            r[2 * i + 1] = (r[2 * i + 1] - hi) * 8.0f;
+        }
+    }
+    // Eight lanes have the four scales of a 64-column group; each writes the word of one digit row.
+    uint32_t word = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) word |= __shfl_sync(0xffffffffu, S, (lane & ~7) + 2 * i) << (8 * i);
+    if (real) {
+        const int rr = r0 + (lane & 7);
+        *reinterpret_cast<uint32_t*>(scales + ((long long)(rr >> 7) * kb4 + (col >> 6)) * 512 + (rr & 31) * 16 +
+                                     ((rr & 127) >> 5) * 4) = word;
+    }
+}
+
+// ------------------------------------------------------------------ products
+
+struct GemmParams {
+    long long units, chunk;   // (tile, pass) pairs; stages per CTA
+    int passes, ks, kb4, nb;  // K stages of a unit, 64-column groups, digit rows of a pass
+    int pass_rows, M;
+    float* parts;
+    unsigned int* status;
+    unsigned long long wait_ns;
+    int stall;
+};
+
+template <int NB>
+__global__ void __launch_bounds__(kThreads, 1)
+    rows_gemm_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmSfw,
+                     const __grid_constant__ CUtensorMap tmD, const __grid_constant__ CUtensorMap tmSfd, const GemmParams p)
+{
+    extern __shared__ __align__(1024) uint8_t smem[];
+    using P = Plan<NB>;
+    constexpr int kStages = P::kStages;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if ((smem_u32(smem) & 1023u) != 0) {
+        if (threadIdx.x == 0) atomicOr(p.status, kStatusBadSmemAlign);
+        return;
+    }
+    uint64_t* full = reinterpret_cast<uint64_t*>(smem + P::kBarOff);   // codes landed and scales stored
+    uint64_t* empty = full + kStages;                                  // the MMAs released the stage
+    uint64_t* sf_full = empty + kStages;                               // scale tiles landed
+    uint64_t* acc_full = sf_full + kStages;
+    uint64_t* acc_empty = acc_full + P::kAccs;
+    uint64_t* done_bar = acc_empty + P::kAccs;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done_bar + 1);
+    volatile int& s_abort = *reinterpret_cast<volatile int*>(tmem_slot + 1);
+    if (threadIdx.x == 0) {
+        s_abort = 0;
+        for (int i = 0; i < kStages; ++i) {
+            mbar_init(&full[i], 1 + 4);   // the producer, four scale warps
+            mbar_init(&empty[i], 1);
+            mbar_init(&sf_full[i], 1);
+        }
+        for (int i = 0; i < P::kAccs; ++i) {
+            mbar_init(&acc_full[i], 1);
+            mbar_init(&acc_empty[i], 4);
+        }
+        mbar_init(done_bar, 1);
+        fence_mbarrier_init();
+        prefetch_tensormap(&tmW);
+        prefetch_tensormap(&tmSfw);
+        prefetch_tensormap(&tmD);
+        prefetch_tensormap(&tmSfd);
+    }
+    if (warp == 1) {
+        tmem_alloc(tmem_slot, kTmemCols);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    griddep_launch_dependents();
+    const long long begin = p.chunk * blockIdx.x;
+    const long long end = min(p.units * p.ks, begin + p.chunk);
+
+    if (warp == 0) {
+        // ------------------------------------------------------------ producer
+        const uint32_t d_bytes = (uint32_t)p.nb * (BK / 2);
+        const uint32_t d_halves = (uint32_t)(p.nb + 127) / 128;
+        auto load_w = [&](long long i, int stage) {
+            const long long u = i / p.ks;
+            const int kb = (int)(i % p.ks), tile = (int)(u / p.passes);
+            uint8_t* st = smem + stage * P::kStage;
+            mbar_arrive_expect_tx(&sf_full[stage], kSfwBytes + d_halves * kSfBox);
+            tma_load_2d(st + kWBytes + P::kDBytes, &tmSfw, &sf_full[stage], 0, (tile * p.kb4 + kb * 4) * 2);
+            mbar_arrive_expect_tx(&full[stage], kWBytes + d_bytes);
+            tma_load_2d(st, &tmW, &full[stage], kb * (BK / 2), tile * BM);
+        };
+        auto load_d = [&](long long i, int stage) {
+            const int kb = (int)(i % p.ks), pass = (int)(i / p.ks % p.passes);
+            uint8_t* st = smem + stage * P::kStage;
+            for (uint32_t h = 0; h < d_halves; ++h)
+                tma_load_2d(st + kWBytes + P::kDBytes + kSfwBytes + h * kSfBox, &tmSfd, &sf_full[stage], 0,
+                            ((2 * pass + (int)h) * p.kb4 + kb * 4) * 2);
+            tma_load_2d(st + kWBytes, &tmD, &full[stage], kb * (BK / 2), 256 * pass);
+        };
+        const int ahead = (int)min((long long)kStages, end - begin);
+        uint32_t fills[kStages] = {};
+        if (!p.stall) {
+            if (elect_one())
+                for (int i = 0; i < ahead; ++i) load_w(begin + i, i);
+            __syncwarp();
+            griddep_wait();
+            if (elect_one())
+                for (int i = 0; i < ahead; ++i) load_d(begin + i, i);
+            __syncwarp();
+#pragma unroll
+            for (int i = 0; i < kStages; ++i) fills[i] = i < ahead ? 1 : 0;
+            int stage = 0;
+            uint32_t phase = 0;
+            for (long long i = begin + ahead; i < end; ++i) {
+                const bool ok = mbar_wait(&empty[stage], phase, p.wait_ns, p.status, kStatusTimeoutProducer);
+                if (!__all_sync(0xffffffffu, ok && s_abort == 0)) {
+                    s_abort = 1;
+                    break;
+                }
+                if (elect_one()) {
+                    load_w(i, stage);
+                    load_d(i, stage);
+                }
+                __syncwarp();
+                ++fills[stage];
+                if (++stage == kStages) {
+                    stage = 0;
+                    phase ^= 1u;
+                }
+            }
+        }
+        // every copy lands before the CTA may end
+        for (int i = 0; i < kStages; ++i)
+            if (fills[i] > 0) {
+                (void)mbar_wait(&sf_full[i], (fills[i] - 1u) & 1u, p.wait_ns, p.status, kStatusTimeoutProducer);
+                (void)mbar_wait(&full[i], (fills[i] - 1u) & 1u, p.wait_ns, p.status, kStatusTimeoutProducer);
+            }
+    } else if (warp == 1) {
+        // ------------------------------------------------------------ MMA
+        // E2M1 operands, K-major, N = nb, M = 128, UE4M3 scales
+        const uint32_t idesc = (1u << 7) | (1u << 10) | ((uint32_t)(p.nb >> 3) << 17) | ((uint32_t)(BM >> 4) << 24);
+        int stage = 0, acc = 0;
+        uint32_t phase = 0, acc_phase = 0;
+        bool ok = true;
+        for (long long i = begin; i < end && ok;) {
+            const long long last = min(end, (i / p.ks + 1) * p.ks);
+            ok = mbar_wait(&acc_empty[acc], acc_phase ^ 1u, p.wait_ns, p.status, kStatusTimeoutMma);
+            ok = __all_sync(0xffffffffu, ok && s_abort == 0);
+            tc_fence_after();
+            const uint32_t d = tmem + (uint32_t)(acc * NB);
+            for (bool first = true; i < last && ok; ++i, first = false) {
+                ok = mbar_wait(&full[stage], phase, p.wait_ns, p.status, kStatusTimeoutMma);
+                ok = __all_sync(0xffffffffu, ok && s_abort == 0);
+                if (!ok) break;
+                tc_fence_after();
+                const int nk = min(4, p.kb4 - (int)(i % p.ks) * 4);
+                const uint32_t st = smem_u32(smem) + (uint32_t)stage * P::kStage;
+                const uint64_t a = smem_desc(st, 16, 1024, 2), b = smem_desc(st + kWBytes, 16, 1024, 2);
+                const uint32_t sfa = tmem + P::kSfTmem + (uint32_t)stage * P::kSfCols, sfb = sfa + 16;
+                if (elect_one()) {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        if (j < nk)
+                            mma_mxf4nvf4(d, a + 2u * j, b + 2u * j, idesc, sfa + 4u * j, sfb + 4u * P::kHalves * j,
+                                         !first || j > 0 ? 1u : 0u);
+                    tc_commit(&empty[stage]);
+                }
+                __syncwarp();
+                if (++stage == kStages) {
+                    stage = 0;
+                    phase ^= 1u;
+                }
+            }
+            if (ok && elect_one()) tc_commit(&acc_full[acc]);
+            __syncwarp();
+            if (++acc == P::kAccs) {
+                acc = 0;
+                acc_phase ^= 1u;
+            }
+        }
+        if (!ok) s_abort = 1;
+        // every MMA ends before TMEM is released
+        if (elect_one()) tc_commit(done_bar);
+        __syncwarp();
+        (void)mbar_wait(done_bar, 0u, p.wait_ns, p.status, kStatusTimeoutMma);
+    } else if (warp >= 4 && warp < 8) {
+        // ------------------------------------------------------------ scales into TMEM, a lane quarter per warp
+        const uint32_t quarter = (uint32_t)(warp & 3);
+        int stage = 0;
+        uint32_t phase = 0;
+        for (long long i = begin; i < end; ++i) {
+            const bool ok = mbar_wait(&sf_full[stage], phase, p.wait_ns, p.status, kStatusTimeoutMma);
+            if (!__all_sync(0xffffffffu, ok && s_abort == 0)) {
+                s_abort = 1;
+                break;
+            }
+            const uint32_t sfa_s = smem_u32(smem) + (uint32_t)stage * P::kStage + kWBytes + P::kDBytes + 16u * (uint32_t)lane;
+            const uint32_t sfb_s = sfa_s + kSfwBytes;
+            const uint32_t t = tmem + ((32u * quarter) << 16) + P::kSfTmem + (uint32_t)stage * P::kSfCols;
+            uint32_t va[16], vb[P::kHalves][16];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const uint4 a = ld_shared_v4(sfa_s + 512u * j);
+                va[4 * j] = a.x, va[4 * j + 1] = a.y, va[4 * j + 2] = a.z, va[4 * j + 3] = a.w;
+#pragma unroll
+                for (int h = 0; h < P::kHalves; ++h) {
+                    const uint4 b = ld_shared_v4(sfb_s + kSfBox * h + 512u * j);
+                    // columns: group j, then half h
+                    const int at = 4 * (P::kHalves * j + h);
+                    vb[at / 16][at % 16] = b.x, vb[at / 16][at % 16 + 1] = b.y;
+                    vb[at / 16][at % 16 + 2] = b.z, vb[at / 16][at % 16 + 3] = b.w;
+                }
+            }
+            tc_st_32x32b_x16(t, va);
+#pragma unroll
+            for (int h = 0; h < P::kHalves; ++h) tc_st_32x32b_x16(t + 16 + 16 * h, vb[h]);
+            tc_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&full[stage]);
+            if (++stage == kStages) {
+                stage = 0;
+                phase ^= 1u;
+            }
+        }
+    } else if (warp >= 8) {
+        // ------------------------------------------------------------ a unit's sums: digits together, to the workspace
+        const int quarter = warp & 3, n = 32 * quarter + lane;
+        int acc = 0;
+        uint32_t acc_phase = 0;
+        griddep_wait();   // an earlier call's joining kernel may read the pieces
+        for (long long i = begin; i < end;) {
+            const long long u = i / p.ks;
+            const bool ok = mbar_wait(&acc_full[acc], acc_phase, p.wait_ns, p.status, kStatusTimeoutEpilogue);
+            if (!__all_sync(0xffffffffu, ok && s_abort == 0)) {
+                s_abort = 1;
+                break;
+            }
+            tc_fence_after();
+            const int pass = (int)(u % p.passes);
+            const int rows = min(p.pass_rows, p.M - pass * p.pass_rows);
+            float* part = p.parts + (u + blockIdx.x) * (long long)p.pass_rows * BM + n;
+            const uint32_t d = tmem + ((32u * (uint32_t)quarter) << 16) + (uint32_t)(acc * NB);
+            for (int m = 0; m < rows; m += 2) {
+                uint32_t v[16];
+                tc_ld_32x32b_x16(d + 8 * m, v);   // (an odd number of rows: the second is not used)
+                tc_wait_ld_x16(v);
+                float y[2];
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    y[h] = __uint_as_float(v[8 * h + 7]);
+#pragma unroll
+                    for (int t = kDigits - 2; t >= 0; --t) y[h] = fmaf(y[h], 0.125f, __uint_as_float(v[8 * h + t]));
+                }
+                part[m * BM] = y[0];
+                if (m + 1 < rows) part[(m + 1) * BM] = y[1];
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&acc_empty[acc]);
+            if (++acc == P::kAccs) {
+                acc = 0;
+                acc_phase ^= 1u;
+            }
+            i = min(end, (u + 1) * p.ks);
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem, kTmemCols);
+    }
+}
+
+// ------------------------------------------------------------------ outputs
+
+struct JoinParams {
+    const float* parts;
+    const float* factors;
+    const float* w_gscale;
+    const float* gate;
+    long long gate_stride;
+    const __nv_bfloat16* bias;
+    const __nv_bfloat16* resid;
+    __nv_bfloat16* out;
+    long long N, chunk;
+    int passes, ks, pass_rows, swiglu;
+};
+
+// silu(g) = g * sigmoid(g) in a form that overflows nowhere (as the GEMM's epilogue has it).
 __device__ __forceinline__ float silu_f32(float g)
 {
     const float t = ex2_approx(-fabsf(g) * 1.4426950408889634f);
@@ -44,71 +460,121 @@ __device__ __forceinline__ float silu_f32(float g)
     return g * (g >= 0.0f ? r : t * r);
 }
 
-__global__ void __launch_bounds__(kThreads) linear_rows_kernel(const __grid_constant__ RowsParams p)
+// Block (tile, row): 128 outputs of a row.
+__global__ void __launch_bounds__(BM) rows_join_kernel(const __grid_constant__ JoinParams p)
 {
-    const LinearRowsJob& j = p.j;
-    const int lane = threadIdx.x & 31;
-    const long long warp = (long long)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
-    const long long outs = j.swiglu ? j.N / 2 : j.N;
-    if (warp >= outs) return;
+    const int m = blockIdx.y, i = threadIdx.x;
+    const int pass = m / p.pass_rows, mm = m - pass * p.pass_rows;
     griddep_wait();
-    const float alpha = *j.w_gscale;
-    for (int m0 = 0; m0 < j.M; m0 += kRowsAtOnce) {
-        float res[2][kRowsAtOnce];
-        for (int part = 0; part < (j.swiglu ? 2 : 1); ++part) {
-            const long long n = j.swiglu ? warp / 128 * 256 + warp % 128 + 128 * part : warp;
-            float acc[kRowsAtOnce] = {};
-            for (int b = lane; b < j.K / 16; b += 32) {
-                const uint2 w = *reinterpret_cast<const uint2*>(j.w_codes + n * (j.K / 2) + 8 * b);
-                const long long off = ((n >> 7) * (j.K / 64) + (b >> 2)) * 512 + (n & 31) * 16 + ((n & 127) >> 5) * 4 + (b & 3);
-                const float S = e4m3_value(j.w_sf[off]);
-                float f[16];
-                for (int k = 0; k < 8; ++k) {
-                    const float2 q = e2m1_pair(((k < 4 ? w.x : w.y) >> (8 * (k & 3))) & 0xFFu);
-                    f[2 * k] = q.x * S;
-                    f[2 * k + 1] = q.y * S;
-                }
-                for (int i = 0; i < kRowsAtOnce; ++i) {
-                    if (m0 + i >= j.M) break;
-                    const __nv_bfloat16* x = j.x + (m0 + i) * j.K + 16 * b;
-                    for (int k = 0; k < 16; ++k) acc[i] = fmaf(__bfloat162float(x[k]), f[k], acc[i]);
-                }
-            }
-            for (int i = 0; i < kRowsAtOnce; ++i) {
-                for (int o = 16; o > 0; o >>= 1) acc[i] += __shfl_xor_sync(0xffffffffu, acc[i], o);
-                res[part][i] = fmaf(alpha, acc[i], j.bias ? __bfloat162float(j.bias[n]) : 0.0f);
-            }
-        }
-        for (int i = 0; i < kRowsAtOnce && m0 + i < j.M; ++i) {
-            if (lane != 0) continue;
-            const long long m = m0 + i;
-            float v = res[0][i];
-            if (j.swiglu)
-                v = silu_f32(__bfloat162float(__float2bfloat16_rn(v))) * __bfloat162float(__float2bfloat16_rn(res[1][i]));
-            if (j.gate) v = fmaf(j.gate[m * j.gate_stride + warp], v, __bfloat162float(j.resid[m * j.N + warp]));
-            j.out[m * outs + warp] = __float2bfloat16_rn(v);
-        }
+    const float f = p.factors[m], s = *p.w_gscale;
+    auto sum = [&](long long tile) {
+        const long long u = tile * p.passes + pass;
+        const long long c0 = u * p.ks / p.chunk, c1 = ((u + 1) * p.ks - 1) / p.chunk;
+        const float* at = p.parts + ((u + c0) * p.pass_rows + mm) * BM + i;
+        float y = 0.0f;
+#pragma unroll 4
+        for (long long c = c0; c <= c1; ++c, at += (long long)p.pass_rows * BM) y += *at;
+        const long long n = tile * BM + i;
+        return fmaf(y * s, f, p.bias && n < p.N ? __bfloat162float(p.bias[n]) : 0.0f);
+    };
+    if (p.swiglu) {
+        const float g = __bfloat162float(__float2bfloat16_rn(sum(2ll * blockIdx.x)));
+        const float u = __bfloat162float(__float2bfloat16_rn(sum(2ll * blockIdx.x + 1)));
+        p.out[m * (p.N / 2) + (long long)blockIdx.x * BM + i] = __float2bfloat16_rn(silu_f32(g) * u);
+        return;
     }
+    const long long n = (long long)blockIdx.x * BM + i;
+    if (n >= p.N) return;
+    float v = sum(blockIdx.x);
+    if (p.gate) v = fmaf(p.gate[m * p.gate_stride + n], v, __bfloat162float(p.resid[m * p.N + n]));
+    p.out[m * p.N + n] = __float2bfloat16_rn(v);
+}
+
+template <int NB>
+cudaError_t launch_gemm_rows(const LinearRowsJob& job, const Layout& l, const GemmParams& p, unsigned ctas,
+                             cudaLaunchConfig_t cfg)
+{
+    CUtensorMap tmW, tmSfw, tmD, tmSfd;
+    const uint64_t kbytes = (uint64_t)job.K / 2;
+    const uint64_t d_tiles = (uint64_t)((l.digit_rows + 127) / 128);
+    if (!make_map_2d(&tmW, CU_TENSOR_MAP_DATA_TYPE_UINT8, job.w_codes, kbytes, (uint64_t)job.N, kbytes, BK / 2, BM,
+                     CU_TENSOR_MAP_SWIZZLE_128B) ||
+        !make_map_2d(&tmSfw, CU_TENSOR_MAP_DATA_TYPE_UINT8, job.w_sf, 256, (uint64_t)(l.tiles * l.kb4 * 2), 256, 256,
+                     kSfBox / 256, CU_TENSOR_MAP_SWIZZLE_NONE) ||
+        !make_map_2d(&tmD, CU_TENSOR_MAP_DATA_TYPE_UINT8, job.ws + l.codes, kbytes, (uint64_t)l.digit_rows, kbytes, BK / 2,
+                     (uint32_t)p.nb, CU_TENSOR_MAP_SWIZZLE_128B) ||
+        !make_map_2d(&tmSfd, CU_TENSOR_MAP_DATA_TYPE_UINT8, job.ws + l.scales, 256, d_tiles * (uint64_t)l.kb4 * 2, 256,
+                     256, kSfBox / 256, CU_TENSOR_MAP_SWIZZLE_NONE))
+        return cudaErrorInvalidValue;
+    const cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void*>(rows_gemm_kernel<NB>), (int)Plan<NB>::kSmem);
+    if (e != cudaSuccess) return e;
+    cfg.gridDim = dim3(ctas);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = Plan<NB>::kSmem;
+    return cudaLaunchKernelEx(&cfg, rows_gemm_kernel<NB>, tmW, tmSfw, tmD, tmSfd, p);
 }
 
 }  // namespace
 
-size_t linear_rows_workspace_bytes(int64_t, int64_t, int64_t) { return 256; }
+size_t linear_rows_workspace_bytes(int64_t M, int64_t N, int64_t K) { return layout(M, N, K).bytes; }
 
 cudaError_t launch_linear_rows(const LinearRowsJob& job, cudaStream_t s)
 {
-    RowsParams p{job};
-    const long long outs = job.swiglu ? job.N / 2 : job.N;
+    const Layout l = layout(job.M, job.N, job.K);
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.gridDim = dim3((unsigned)((outs + 3) / 4));
-    cfg.blockDim = dim3(kThreads);
     cfg.stream = s;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, linear_rows_kernel, p);
+
+    cfg.gridDim = dim3((unsigned)((job.K + kDigitColumns - 1) / kDigitColumns), (unsigned)job.M);
+    cfg.blockDim = dim3(kDigitThreads);
+    float* factors = reinterpret_cast<float*>(job.ws + kFactors);
+    cudaError_t e = cudaLaunchKernelEx(&cfg, digits_kernel, job.x, (int)job.K, l.pass_rows, (int)l.kb4,
+                                       job.ws + l.codes, job.ws + l.scales, factors);
+    if (e != cudaSuccess) return e;
+
+    GemmParams p{};
+    p.units = l.tiles * l.passes;
+    p.passes = l.passes;
+    p.ks = (int)((job.K + BK - 1) / BK);
+    p.kb4 = (int)l.kb4;
+    p.nb = kDigits * l.pass_rows;
+    p.pass_rows = l.pass_rows;
+    p.M = (int)job.M;
+    p.parts = reinterpret_cast<float*>(job.ws + l.parts);
+    p.status = reinterpret_cast<unsigned int*>(job.ws);
+    p.wait_ns = job.wait_limit_ns;
+    p.stall = job.stall;
+    const int sms = sm_count_current_device();
+    const long long most = sms < kMaxCtas ? sms : kMaxCtas, stages = p.units * p.ks;
+    p.chunk = (stages + most - 1) / most;
+    const unsigned ctas = (unsigned)((stages + p.chunk - 1) / p.chunk);
+    e = p.nb <= 64 ? launch_gemm_rows<64>(job, l, p, ctas, cfg)
+        : p.nb <= 128 ? launch_gemm_rows<128>(job, l, p, ctas, cfg)
+                      : launch_gemm_rows<256>(job, l, p, ctas, cfg);
+    if (e != cudaSuccess) return e;
+
+    JoinParams jp{};
+    jp.parts = p.parts;
+    jp.factors = factors;
+    jp.w_gscale = job.w_gscale;
+    jp.gate = job.gate;
+    jp.gate_stride = job.gate_stride;
+    jp.bias = job.bias;
+    jp.resid = job.resid;
+    jp.out = job.out;
+    jp.N = job.N;
+    jp.chunk = p.chunk;
+    jp.passes = l.passes;
+    jp.ks = p.ks;
+    jp.pass_rows = l.pass_rows;
+    jp.swiglu = job.swiglu;
+    cfg.gridDim = dim3((unsigned)(job.swiglu ? l.tiles / 2 : l.tiles), (unsigned)job.M);
+    cfg.blockDim = dim3(BM);
+    return cudaLaunchKernelEx(&cfg, rows_join_kernel, jp);
 }
 
 }  // namespace h3fp4

@@ -69,7 +69,7 @@ h3fp4_status cache_rows(const h3fp4_heads* k, const h3fp4_heads* v, int64_t M, c
 h3fp4_status rows_shape(int64_t M, int64_t N, int64_t K)
 {
     if (M < 1 || M > kRowsMax || N < 8 || N % 8 != 0 || N > (1 << 24)) return H3FP4_ERR_SHAPE;
-    if (K < 64 || K % 64 != 0 || K > (1 << 20)) return H3FP4_ERR_SHAPE;
+    if (K < 64 || K % 64 != 0 || K > (1 << 16)) return H3FP4_ERR_SHAPE;
     return H3FP4_OK;
 }
 

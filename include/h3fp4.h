@@ -475,7 +475,7 @@ H3FP4_API h3fp4_status h3fp4_block_norm(const void* x_bf16, const void* y_bf16, 
  *     out = bf16(R + g * (s_w * (x . W_q^T) + b))  or  bf16(s_w * (x . W_q^T) + b)
  * ("H3 Blackwell Runtime" README, "Checkpoints": pre-quantised weights).  Sums are fp32; x
  * enters with an error of at most 2^-22 of the largest magnitude of its block of 16.
- *   x: bf16 [M][K], finite, 1 <= M <= H3FP4_ROWS_MAX; K % 64 == 0, K <= 2^20; N % 8 == 0,
+ *   x: bf16 [M][K], finite, 1 <= M <= H3FP4_ROWS_MAX; K % 64 == 0, K <= 2^16; N % 8 == 0,
  *      N <= 2^24.
  *   w_codes, w_sf, w_gscale: output of h3fp4_quantize_weight.
  *   flags: H3FP4_EPI_BIAS (bias bf16 [N]); H3FP4_EPI_GATE_RESID (gate fp32, row m's at

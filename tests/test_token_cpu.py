@@ -131,7 +131,7 @@ def rows(lib, x=MB, M=4, N=256, K=128, wc=2 * MB, wsf=3 * MB, wg=4 * MB, gate=No
 def test_linear_rows_refusals(lib):
     G = dict(flags=4, gate=7 * MB, resid=8 * MB)
     for kw in (dict(M=0), dict(M=65), dict(M=-1), dict(N=0), dict(N=12), dict(N=(1 << 24) + 8), dict(K=0), dict(K=96),
-               dict(K=(1 << 20) + 64), dict(flags=64, N=128)):
+               dict(K=(1 << 16) + 64), dict(flags=64, N=128)):
         assert rows(lib, **kw) == SHAPE, kw
     for kw in (dict(x=None), dict(wc=None), dict(wsf=None), dict(wg=None), dict(out=None), dict(ws=None), dict(ws_bytes=0),
                dict(flags=1), dict(flags=2), dict(bias=7 * MB), dict(gate=7 * MB), dict(flags=4), dict(flags=4, gate=7 * MB),
