@@ -39,7 +39,7 @@ namespace {
 constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kTile = kCacheGroup * kWarps;   // tokens of a tile
-constexpr int kCols = 16;                     // query columns of a unit
+constexpr int kPartCols = 16;                 // query columns of a unit at most
 constexpr int kMaxCtas = 608;                 // of a launch: the workspace is made for as many
 constexpr float kRaise = 14.0f, kStart = 6.0f;  // in powers of two: see above
 // No key yet; and the lowest score that counts: where a column's largest is there, it left fp32's range.
@@ -53,17 +53,17 @@ struct Cut {
 // Partial sums: per CTA one of a unit that began before it, one of a unit that goes on after it.
 template <int W>
 struct Part {
-    static constexpr long long kFloats = kCols * (W + 2);
+    static constexpr long long kFloats = kPartCols * (W + 2);
 };
 
 constexpr size_t kCutOff = 256;
 constexpr size_t kPartOff = kCutOff + kMaxCtas * sizeof(Cut);
 
-template <int W>
+template <int W, int kCols>
 struct Config {
-    static constexpr int kSlots = W == 256 ? 3 : W == 128 ? 4 : 6;     // groups in flight per warp
-    static constexpr int kCtasPerSm = W == 256 ? 2 : 3;
-    static constexpr int kMergeRegs = W / 2 + 4;                       // a lane's state: O, two maxima, two sums
+    static constexpr int kSlots = W == 256 ? (kCols == 16 ? 3 : 2) : W == 128 ? 4 : 6;   // groups in flight per warp
+    static constexpr int kCtasPerSm = W == 256 ? (kCols == 16 ? 2 : 3) : kCols == 16 ? 3 : 4;
+    static constexpr int kMergeRegs = W * kCols / 32 + 4;              // a lane's state: O, two maxima, two sums
     static constexpr uint32_t kRing = kWarps * kSlots * CacheLayout<W>::kGroupBytes;
     static constexpr uint32_t kMerge = 2 * kMergeRegs * 32 * 4;
     static constexpr uint32_t kPrefix = (kCacheMaxSeqs + 1) * 8;
@@ -92,6 +92,7 @@ struct Seq {
     int coltiles, tiles;
 };
 
+template <int kCols>
 __device__ __forceinline__ Seq sequence(const AttnParams& p, int s)
 {
     Seq q;
@@ -205,52 +206,70 @@ __device__ __forceinline__ void ld_words(const uint8_t* p, uint32_t (&w)[N])
     }
 }
 
-// The state of a warp over the tokens it has seen, of columns g and g + 8: the exponents'
-// reference, the lane's part of the sums, and O (n tile j holds elements n W/8 + j).
-template <int W>
+// The state of a warp over the tokens it has seen, of the lane's two columns: the exponents'
+// reference, the lane's part of the sums, and O.
+//   16 columns: columns g and g + 8, O[j]: elements n W/8 + j of n = 2 c, 2 c + 1
+//    8 columns: columns 2 c and 2 c + 1, O[j]: elements g W/8 + 2 j and the next one
+template <int W, int kCols>
 struct State {
+    static constexpr int kO = kCols == 16 ? W / 8 : W / 16;
     float m[2], l[2];
-    float o[W / 8][4];
+    float o[kO][4];
 };
 
-template <int W>
-__device__ __forceinline__ void rescale(State<W>& st, int row, float to)
+// Which of the lane's two columns value i of a fragment belongs to.
+template <int kCols>
+__device__ __forceinline__ constexpr int column_of(int i) { return kCols == 16 ? i >> 1 : i & 1; }
+
+template <int W, int kCols>
+__device__ __forceinline__ void rescale(State<W, kCols>& st, int col, float to)
 {
-    const float f = exp2f(st.m[row] - to);
-    st.m[row] = to;
-    st.l[row] *= f;
+    const float f = exp2f(st.m[col] - to);
+    st.m[col] = to;
+    st.l[col] *= f;
 #pragma unroll
-    for (int j = 0; j < W / 8; ++j) {
-        st.o[j][2 * row] *= f;
-        st.o[j][2 * row + 1] *= f;
-    }
+    for (int j = 0; j < State<W, kCols>::kO; ++j)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (column_of<kCols>(i) == col) st.o[j][i] *= f;
 }
 
-// One group of 16 tokens.  `left`: how many of its tokens hold anything; lim: tokens that
-// columns g and g + 8 attend to, counted from the group's first.
-template <int W>
-__device__ __forceinline__ void group_step(State<W>& st, const uint8_t* gp, int lane, const uint32_t (&qa)[W / 16][4],
-                                           const float (&factor)[2], bool masked, int left, const int (&lim)[2])
+// A sum or a maximum over the lanes that share columns.
+template <int kCols, class F>
+__device__ __forceinline__ float over_lanes(float v, F f)
+{
+#pragma unroll
+    for (int o = kCols == 16 ? 1 : 4; o < (kCols == 16 ? 4 : 32); o <<= 1) v = f(v, __shfl_xor_sync(0xffffffffu, v, o));
+    return v;
+}
+
+// One group of 16 tokens.  kMasked: `left` tokens of it hold anything, `lim` are attended to by
+// the lane's two columns.
+template <int W, int kCols, bool kMasked>
+__device__ __forceinline__ void group_step(State<W, kCols>& st, const uint8_t* gp, int lane,
+                                           const uint32_t (&qf)[W / 16][kCols / 4], const float (&factor)[2], int left,
+                                           const int (&lim)[2])
 {
     using L = CacheLayout<W>;
-    const int c = lane & 3;
+    const int g = lane >> 2, c = lane & 3;
+    // ------------------------------------------------------------ scores of 8 values: two of the lane's
+    // columns by four tokens (16 columns: tokens 8 half + 2 c + (0, 1); 8 columns: tokens g, g + 8)
     float s[2][4];
-    // ------------------------------------------------------------ S = Q K^T, tokens 8 half + g
     {
-        uint32_t sc[W == 256 ? 2 : 1];   // the lane's scales of both halves
+        uint32_t sc[W == 256 ? 2 : 1];   // the lane's scales of tokens g (low half) and g + 8
         if constexpr (W == 256) ld_words<2>(gp + L::kKScale + lane * 8, sc);
         else if constexpr (W == 128) sc[0] = *reinterpret_cast<const uint32_t*>(gp + L::kKScale + lane * 4);
         else sc[0] = *reinterpret_cast<const uint16_t*>(gp + L::kKScale + lane * 2);
+        constexpr int kRuns = W == 256 ? 2 : 1, kWords = W == 64 ? 2 : 4;
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-            s[half][0] = s[half][1] = s[half][2] = s[half][3] = 0.0f;
-            constexpr int kRuns = W == 256 ? 2 : 1;
+        for (int h = 0; h < 2; ++h) s[h][0] = s[h][1] = s[h][2] = s[h][3] = 0.0f;
 #pragma unroll
-            for (int run = 0; run < kRuns; ++run) {
-                constexpr int kWords = W == 64 ? 2 : 4;
-                uint32_t w[kWords];
-                ld_words<kWords>(W == 64 ? gp + half * 256 + lane * 8 : gp + run * 1024 + half * 512 + lane * 16, w);
-                uint32_t pair;   // this run's scales of this half, f16x2 (W = 64: one, twice)
+        for (int run = 0; run < kRuns; ++run) {
+            uint32_t w[2][kWords], x[2][2];   // both tokens: codes, their two scales as f16x2
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+                ld_words<kWords>(W == 64 ? gp + half * 256 + lane * 8 : gp + run * 1024 + half * 512 + lane * 16, w[half]);
+                uint32_t pair;
                 if constexpr (W == 64) {
                     const uint32_t b = half ? sc[0] >> 8 : sc[0] & 0xFFu;
                     pair = e4m3x2_f16(b | (b << 8));
@@ -259,51 +278,83 @@ __device__ __forceinline__ void group_step(State<W>& st, const uint8_t* gp, int 
                 } else {
                     pair = e4m3x2_f16(run ? sc[half] >> 16 : sc[half]);
                 }
-                const uint32_t s0 = __byte_perm(pair, pair, 0x1010), s1 = __byte_perm(pair, pair, 0x3232);
+                x[half][0] = __byte_perm(pair, pair, 0x1010);
+                x[half][1] = __byte_perm(pair, pair, 0x3232);
+            }
 #pragma unroll
-                for (int i = 0; i < kWords; ++i) {
-                    uint32_t f[4];
-                    e2m1x8_f16(w[i], f);
-                    const uint32_t x = 2 * i < kWords ? s0 : s1;
-                    const int step = run * 8 + 2 * i;
-                    mma_f16(s[half], qa[step], mul_f16x2(f[0], x), mul_f16x2(f[1], x));
-                    mma_f16(s[half], qa[step + 1], mul_f16x2(f[2], x), mul_f16x2(f[3], x));
+            for (int i = 0; i < kWords; ++i) {
+                uint32_t f[2][4];
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                    e2m1x8_f16(w[half][i], f[half]);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) f[half][j] = mul_f16x2(f[half][j], x[half][2 * i < kWords ? 0 : 1]);
+                }
+                const int step = run * 8 + 2 * i;
+                if constexpr (kCols == 16) {
+                    // Q's 16 columns are A's rows, the tokens B's columns
+#pragma unroll
+                    for (int half = 0; half < 2; ++half) {
+                        mma_f16(s[half], qf[step], f[half][0], f[half][1]);
+                        mma_f16(s[half], qf[step + 1], f[half][2], f[half][3]);
+                    }
+                } else {
+                    // the tokens are A's rows, Q's 8 columns B's; two chains of sums
+                    const uint32_t a0[4] = {f[0][0], f[1][0], f[0][1], f[1][1]};
+                    const uint32_t a1[4] = {f[0][2], f[1][2], f[0][3], f[1][3]};
+                    mma_f16(s[0], a0, qf[step][0], qf[step][1]);
+                    mma_f16(s[1], a1, qf[step + 1][0], qf[step + 1][1]);
                 }
             }
         }
-    }
-    // ------------------------------------------------------------ exponents, column g (row 0) and g + 8
+        if constexpr (kCols == 8) {
 #pragma unroll
-    for (int half = 0; half < 2; ++half)
+            for (int i = 0; i < 4; ++i) s[0][i] += s[1][i];
+        }
+    }
+    // ------------------------------------------------------------ exponents
+    constexpr int kF = kCols / 8;
+#pragma unroll
+    for (int h = 0; h < kF; ++h)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            s[half][i] = max_nan(s[half][i] * factor[i >> 1], kLowest);
-            if (masked && 8 * half + 2 * c + (i & 1) >= lim[i >> 1]) s[half][i] = -INFINITY;
+            const int col = column_of<kCols>(i);
+            s[h][i] = max_nan(s[h][i] * factor[col], kLowest);
+            if (kMasked) {
+                const int token = kCols == 16 ? 8 * h + 2 * c + (i & 1) : g + 8 * (i >> 1);
+                if (token >= lim[col]) s[h][i] = -INFINITY;
+            }
         }
-    uint32_t pa[4];
     float top[2];
 #pragma unroll
-    for (int row = 0; row < 2; ++row)
-        top[row] = fmaxf(fmaxf(s[0][2 * row], s[0][2 * row + 1]), fmaxf(s[1][2 * row], s[1][2 * row + 1]));
+    for (int col = 0; col < 2; ++col) {
+        if constexpr (kCols == 16) top[col] = fmaxf(fmaxf(s[0][2 * col], s[0][2 * col + 1]), fmaxf(s[1][2 * col], s[1][2 * col + 1]));
+        else top[col] = fmaxf(s[0][col], s[0][2 + col]);
+    }
     if (__any_sync(0xffffffffu, top[0] > st.m[0] + kRaise || top[1] > st.m[1] + kRaise)) {
 #pragma unroll
-        for (int row = 0; row < 2; ++row) {
-            float t = top[row];
-            t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 1));
-            t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 2));
-            if (t > st.m[row] + kRaise) rescale<W>(st, row, t - kStart);
+        for (int col = 0; col < 2; ++col) {
+            const float t = over_lanes<kCols>(top[col], [](float a, float b) { return fmaxf(a, b); });
+            if (t > st.m[col] + kRaise) rescale<W, kCols>(st, col, t - kStart);
         }
     }
+    uint32_t pf[kCols == 16 ? 4 : 2];   // P as the second product's A (16 columns) or, transposed, its B
 #pragma unroll
-    for (int half = 0; half < 2; ++half) {
+    for (int h = 0; h < kF; ++h) {
         float e[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            e[i] = ex2_approx_ftz(s[half][i] - st.m[i >> 1]);
-            st.l[i >> 1] += e[i];
+            const int col = column_of<kCols>(i);
+            e[i] = ex2_approx_ftz(s[h][i] - st.m[col]);
+            st.l[col] += e[i];
         }
-        pa[2 * half] = pack_f16x2(e[0], e[1]);
-        pa[2 * half + 1] = pack_f16x2(e[2], e[3]);
+        pf[2 * h] = pack_f16x2(e[0], e[1]);
+        pf[2 * h + 1] = pack_f16x2(e[2], e[3]);
+    }
+    if constexpr (kCols == 8) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+            asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %0;" : "+r"(pf[h]));
     }
     // ------------------------------------------------------------ O += P V, token pairs 8 half + 2 c + (0, 1)
     constexpr int kVBlocks = W == 256 ? 2 : 1;      // scale blocks of a lane
@@ -311,13 +362,12 @@ __device__ __forceinline__ void group_step(State<W>& st, const uint8_t* gp, int 
     uint32_t vs[2][kVBlocks];
 #pragma unroll
     for (int b = 0; b < kVBlocks; ++b) {
-        const int g = lane >> 2;
         const int block = W == 64 ? g >> 1 : W == 128 ? g : 2 * g + b;
         const uint32_t four = *reinterpret_cast<const uint32_t*>(gp + L::kVScale + (block * 4 + c) * 4);
         vs[0][b] = e4m3x2_f16(four);
         vs[1][b] = e4m3x2_f16(four >> 16);
     }
-    if (masked) {
+    if (kMasked) {
         // tokens without data: their scales may be anything, NaN too
 #pragma unroll
         for (int half = 0; half < 2; ++half)
@@ -345,18 +395,28 @@ __device__ __forceinline__ void group_step(State<W>& st, const uint8_t* gp, int 
     }
 #pragma unroll
     for (int i = 0; i < kVWords; ++i) {
-        uint32_t even[2][4], odd[2][4];
+        uint32_t even[2][4], odd[2][4];   // elements 8 i + 2 j and the next one
+        const int blk = W == 256 ? i >> 1 : 0;
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
             const uint32_t a = w0[half][i], b = w1[half][i];
             e2m1x8_f16((a & 0x0F0F0F0Fu) | ((b << 4) & 0xF0F0F0F0u), even[half]);
             e2m1x8_f16(((a >> 4) & 0x0F0F0F0Fu) | (b & 0xF0F0F0F0u), odd[half]);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                even[half][j] = mul_f16x2(even[half][j], vs[half][blk]);
+                odd[half][j] = mul_f16x2(odd[half][j], vs[half][blk]);
+            }
         }
-        const int blk = W == 256 ? i >> 1 : 0;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            mma_f16(st.o[8 * i + 2 * j], pa, mul_f16x2(even[0][j], vs[0][blk]), mul_f16x2(even[1][j], vs[1][blk]));
-            mma_f16(st.o[8 * i + 2 * j + 1], pa, mul_f16x2(odd[0][j], vs[0][blk]), mul_f16x2(odd[1][j], vs[1][blk]));
+            if constexpr (kCols == 16) {
+                mma_f16(st.o[8 * i + 2 * j], pf, even[0][j], even[1][j]);
+                mma_f16(st.o[8 * i + 2 * j + 1], pf, odd[0][j], odd[1][j]);
+            } else {
+                const uint32_t a[4] = {even[0][j], odd[0][j], even[1][j], odd[1][j]};
+                mma_f16(st.o[4 * i + j], a, pf[0], pf[1]);
+            }
         }
     }
 }
@@ -369,12 +429,13 @@ __device__ __forceinline__ void join_scale(float a, float b, float& m, float& fa
     fb = exp2f(b - m);
 }
 
-template <int W>
-__global__ void __launch_bounds__(kThreads, Config<W>::kCtasPerSm)
+template <int W, int kCols>
+__global__ void __launch_bounds__(kThreads, Config<W, kCols>::kCtasPerSm)
     cache_attn_kernel(const __grid_constant__ AttnParams p)
 {
     using L = CacheLayout<W>;
-    using C = Config<W>;
+    using C = Config<W, kCols>;
+    using S = State<W, kCols>;
     extern __shared__ __align__(128) uint8_t smem[];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
     uint8_t* ring = smem + warp * (C::kSlots * L::kGroupBytes);
@@ -388,6 +449,7 @@ __global__ void __launch_bounds__(kThreads, Config<W>::kCtasPerSm)
         fence_mbarrier_init();
     }
     griddep_wait();
+    griddep_launch_dependents();
     const int nseq = p.c.nseq;
 
     // ------------------------------------------------------------ tiles before each sequence
@@ -395,7 +457,7 @@ __global__ void __launch_bounds__(kThreads, Config<W>::kCtasPerSm)
         const int per = (nseq + kThreads - 1) / kThreads, s0 = threadIdx.x * per;
         long long mine = 0;
         for (int s = s0; s < s0 + per && s < nseq; ++s) {
-            const Seq q = sequence(p, s);
+            const Seq q = sequence<kCols>(p, s);
             mine += (long long)p.c.Hkv * q.coltiles * q.tiles;
         }
         long long upto = mine;
@@ -410,7 +472,7 @@ __global__ void __launch_bounds__(kThreads, Config<W>::kCtasPerSm)
         long long before = upto - mine;
         for (int s = s0; s < s0 + per && s < nseq; ++s) {
             prefix[s] = before;
-            const Seq q = sequence(p, s);
+            const Seq q = sequence<kCols>(p, s);
             before += (long long)p.c.Hkv * q.coltiles * q.tiles;
         }
         if (threadIdx.x == kThreads - 1) prefix[nseq] = upto;
@@ -422,7 +484,7 @@ __global__ void __launch_bounds__(kThreads, Config<W>::kCtasPerSm)
 
     // rows of sequences that hold nothing
     for (int s = blockIdx.x; s < nseq; s += gridDim.x) {
-        const Seq q = sequence(p, s);
+        const Seq q = sequence<kCols>(p, s);
         if (q.tiles > 0) continue;
         const int vecs = p.c.D / 8;
         for (long long i = threadIdx.x; i < q.rows * p.Hq * vecs; i += kThreads) {
@@ -438,6 +500,7 @@ __global__ void __launch_bounds__(kThreads, Config<W>::kCtasPerSm)
     // ------------------------------------------------------------ units
     uint32_t phases = 0;    // of the ring's barriers, one bit each
     bool lost = false;      // a wait ran out: nothing more is loaded or computed
+    const int per_page = p.c.page / kCacheGroup;
     int s = 0;
     for (long long at = begin; at < end;) {
         // the sequence whose tiles hold `at`
@@ -450,69 +513,68 @@ __global__ void __launch_bounds__(kThreads, Config<W>::kCtasPerSm)
             }
             s = lo;
         }
-        const Seq q = sequence(p, s);
+        const Seq q = sequence<kCols>(p, s);
         const long long unit = (at - prefix[s]) / q.tiles;
         const int h = (int)(unit / q.coltiles), ct = (int)(unit % q.coltiles);
         const long long ubegin = prefix[s] + unit * q.tiles, uend = ubegin + q.tiles;
         const int t0 = (int)(at - ubegin), t1 = (int)(min(end, uend) - ubegin);
         // what each column attends to
         const int cols = (int)min((long long)kCols, q.rows * p.group - (long long)ct * kCols);
-        auto limit = [&](int col) -> long long {
+        auto limit = [&](int col) -> int {
             const long long row = ((long long)ct * kCols + col) / p.group;
-            return p.causal ? max(0ll, min(q.len, q.start + row + 1)) : q.len;
+            return (int)(p.causal ? max(0ll, min(q.len, q.start + row + 1)) : q.len);
         };
-        const long long least = limit(0), most = limit(cols - 1);
-        const long long mylim[2] = {g < cols ? limit(g) : most, g + 8 < cols ? limit(g + 8) : most};
+        // the lane's two columns
+        int mycol[2], mylim[2];
+        const int least = limit(0), most = limit(cols - 1);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            mycol[i] = kCols == 16 ? g + 8 * i : 2 * c + i;
+            mylim[i] = mycol[i] < cols ? limit(mycol[i]) : most;
+        }
 
         // this warp's groups: tile t's group of 16 tokens is 4 t + warp, up to the last token that any column sees
-        const int groups = (int)((most + kCacheGroup - 1) / kCacheGroup);
-        int n = 0;   // of this warp in [t0, t1)
-        if (groups > kWarps * t0 + warp) n = min(t1 - t0, (groups - (kWarps * t0 + warp) + kWarps - 1) / kWarps);
-        const int per_page = p.c.page / kCacheGroup;
+        const int groups = (most - 1) / kCacheGroup + (most > 0 ? 1 : 0);
+        const int g0 = kWarps * t0 + warp;   // the first, then every fourth
+        int n = 0;
+        if (groups > g0) n = min(t1 - t0, (groups - g0 + kWarps - 1) / kWarps);
         const int32_t* table = p.c.table + (long long)s * p.c.max_pages;
-        const long long head_bytes = (long long)per_page * L::kGroupBytes;
-        // page numbers of the next 32 groups, one per lane, and which of them the pool has
-        int page_at = 0, page = 0;
-        auto fetch_pages = [&](int i) {
-            page_at = i;
-            const int gi = kWarps * (t0 + i + lane) + warp;
-            page = -1;
+        // where the next 32 groups lie, one per lane (null: no page of the pool)
+        const uint8_t* where = nullptr;
+        auto look = [&](int i) {
+            const int gi = g0 + kWarps * (i + lane);
+            where = nullptr;
             if (i + lane < n) {
-                page = table[gi / per_page];
-                if (page < 0 || page >= p.c.n_pages) page = -1;
+                const int pg = table[gi / per_page];
+                if (pg >= 0 && pg < p.c.n_pages)
+                    where = p.c.pool + (((long long)pg * p.c.Hkv + h) * per_page + gi % per_page) * L::kGroupBytes;
             }
         };
         uint32_t there = 0;   // slots whose group exists
         auto load = [&](int i, int slot) {
-            if (i - page_at >= 32) fetch_pages(i);
-            const int pg = __shfl_sync(0xffffffffu, page, i - page_at);
-            const int gi = kWarps * (t0 + i) + warp;
-            there = (there & ~(1u << slot)) | (pg >= 0 ? 1u << slot : 0u);
+            if ((i & 31) == 0) look(i);
+            const uint64_t src = __shfl_sync(0xffffffffu, reinterpret_cast<uint64_t>(where), i & 31);
+            there = src ? there | (1u << slot) : there & ~(1u << slot);
             if (lane == 0 && !p.stall) {
-                if (pg < 0) {
-                    mbar_arrive(&bars[slot]);
-                } else {
+                if (src) {
                     mbar_arrive_expect_tx(&bars[slot], L::kGroupBytes);
-                    bulk_load(ring + slot * L::kGroupBytes,
-                              p.c.pool + ((long long)pg * p.c.Hkv + h) * head_bytes +
-                                  (long long)(gi % per_page) * L::kGroupBytes,
-                              L::kGroupBytes, &bars[slot]);
+                    bulk_load(ring + slot * L::kGroupBytes, reinterpret_cast<const void*>(src), L::kGroupBytes, &bars[slot]);
+                } else {
+                    mbar_arrive(&bars[slot]);
                 }
             }
         };
         int loaded = 0;
-        if (n > 0 && !lost) {
-            fetch_pages(0);
+        if (!lost)
             for (; loaded < min(n, C::kSlots); ++loaded) load(loaded, loaded);
-        }
 
-        // Q's fragments: the lane's elements of columns g and g + 8, scaled to f16's range
-        uint32_t qa[W / 16][4];
-        float factor[2];
+        // Q's fragments: the lane's elements of columns g (and g + 8), scaled to f16's range
+        uint32_t qf[W / 16][kCols / 4];
+        float factor[2], mine[kCols / 8];
         const float kg = p.c.k_gscale ? p.c.k_gscale[h] : 1.0f;
 #pragma unroll
-        for (int row = 0; row < 2; ++row) {
-            const int col = g + 8 * row;
+        for (int half = 0; half < kCols / 8; ++half) {
+            const int col = g + 8 * half;
             const long long id = (long long)ct * kCols + col;
             const __nv_bfloat16* src = nullptr;
             if (col < cols)
@@ -529,25 +591,29 @@ __global__ void __launch_bounds__(kThreads, Config<W>::kCtasPerSm)
             }
             top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
             top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-            // the largest to [2^14, 2^15): by at most 2^127 either way, in two steps where that is subnormal
+            // the largest to [2^14, 2^15), by a power of two in the normal range
             const int e = min(126, max(-126, 14 - ((int)(top >> 7) - 127)));
             const float up = pow2i(e);
-            factor[row] = p.scale_log2 * kg * pow2i(-e);
+            mine[half] = p.scale_log2 * kg * pow2i(-e);
 #pragma unroll
             for (int t = 0; t < W / 16; ++t) {
                 auto f16 = [&](uint32_t w) {
                     return pack_f16x2(__uint_as_float(w << 16) * up, __uint_as_float(w & 0xFFFF0000u) * up);
                 };
-                qa[t][row] = f16(raw[t].x);
-                qa[t][2 + row] = f16(raw[t].y);
+                qf[t][kCols == 16 ? half : 0] = f16(raw[t].x);
+                qf[t][kCols == 16 ? 2 + half : 1] = f16(raw[t].y);
             }
         }
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+            factor[i] = kCols == 16 ? mine[i % (kCols / 8)] : __shfl_sync(0xffffffffu, mine[0], 4 * (2 * c + i));
 
-        State<W> st;
+        S st;
         st.m[0] = st.m[1] = kNone;
         st.l[0] = st.l[1] = 0.0f;
 #pragma unroll
-        for (int j = 0; j < W / 8; ++j) st.o[j][0] = st.o[j][1] = st.o[j][2] = st.o[j][3] = 0.0f;
+        for (int j = 0; j < S::kO; ++j) st.o[j][0] = st.o[j][1] = st.o[j][2] = st.o[j][3] = 0.0f;
+        const int plain = max(0, min(n, (least / kCacheGroup - g0 + kWarps - 1) / kWarps));   // groups that all columns see whole
         int slot = 0;
         for (int i = 0; i < n && !lost; ++i) {
             const bool ok = mbar_wait(&bars[slot], (phases >> slot) & 1u, p.wait_ns, status, kStatusTimeoutMma);
@@ -563,14 +629,16 @@ __global__ void __launch_bounds__(kThreads, Config<W>::kCtasPerSm)
             }
             phases ^= 1u << slot;
             if ((there >> slot) & 1u) {
-                const long long first = (long long)(kWarps * (t0 + i) + warp) * kCacheGroup;
-                const bool masked = first + kCacheGroup > least;
-                const int lim[2] = {(int)min((long long)kCacheGroup, mylim[0] - first),
-                                    (int)min((long long)kCacheGroup, mylim[1] - first)};
-                group_step<W>(st, ring + slot * L::kGroupBytes, lane, qa, factor, masked,
-                              (int)min((long long)kCacheGroup, most - first), lim);
+                const uint8_t* gp = ring + slot * L::kGroupBytes;
+                if (i < plain) {
+                    group_step<W, kCols, false>(st, gp, lane, qf, factor, kCacheGroup, mylim);
+                } else {
+                    const int first = (g0 + kWarps * i) * kCacheGroup;
+                    const int lim[2] = {mylim[0] - first, mylim[1] - first};
+                    group_step<W, kCols, true>(st, gp, lane, qf, factor, most - first, lim);
+                }
             }
-            fence_proxy_async_smem();  // these reads, before the slot's next fill
+            // (the products that used the slot's last bytes have been issued, so these were read)
             __syncwarp();
             if (loaded < n) {
                 load(loaded, slot);
@@ -582,94 +650,88 @@ __global__ void __launch_bounds__(kThreads, Config<W>::kCtasPerSm)
 
         // ------------------------------------------------------------ the four warps' sums into warp 0
 #pragma unroll
-        for (int row = 0; row < 2; ++row) {
-            st.l[row] += __shfl_xor_sync(0xffffffffu, st.l[row], 1);
-            st.l[row] += __shfl_xor_sync(0xffffffffu, st.l[row], 2);
-        }
+        for (int i = 0; i < 2; ++i) st.l[i] = over_lanes<kCols>(st.l[i], [](float a, float b) { return a + b; });
 #pragma unroll
         for (int with = 2; with >= 1; with >>= 1) {
-            float* slot_m = merge + (warp & (with - 1)) * (C::kMergeRegs * 32) + lane;
+            float* other = merge + (warp & (with - 1)) * (C::kMergeRegs * 32) + lane;
             __syncthreads();
             if (warp >= with && warp < 2 * with) {
-                slot_m[0] = st.m[0], slot_m[32] = st.m[1], slot_m[64] = st.l[0], slot_m[96] = st.l[1];
+                other[0] = st.m[0], other[32] = st.m[1], other[64] = st.l[0], other[96] = st.l[1];
 #pragma unroll
-                for (int j = 0; j < W / 2; ++j) slot_m[32 * (4 + j)] = st.o[j >> 2][j & 3];
+                for (int j = 0; j < 4 * S::kO; ++j) other[32 * (4 + j)] = st.o[j >> 2][j & 3];
             }
             __syncthreads();
             if (warp < with) {
                 float fa[2], fb[2];
 #pragma unroll
-                for (int row = 0; row < 2; ++row) {
+                for (int i = 0; i < 2; ++i) {
                     float m;
-                    join_scale(st.m[row], slot_m[32 * row], m, fa[row], fb[row]);
-                    st.m[row] = m;
-                    st.l[row] = st.l[row] * fa[row] + slot_m[32 * (2 + row)] * fb[row];
+                    join_scale(st.m[i], other[32 * i], m, fa[i], fb[i]);
+                    st.m[i] = m;
+                    st.l[i] = st.l[i] * fa[i] + other[32 * (2 + i)] * fb[i];
                 }
 #pragma unroll
-                for (int j = 0; j < W / 2; ++j) {
-                    const int row = (j & 3) >> 1;
-                    st.o[j >> 2][j & 3] = st.o[j >> 2][j & 3] * fa[row] + slot_m[32 * (4 + j)] * fb[row];
+                for (int j = 0; j < 4 * S::kO; ++j) {
+                    const int col = column_of<kCols>(j & 3);
+                    st.o[j >> 2][j & 3] = st.o[j >> 2][j & 3] * fa[col] + other[32 * (4 + j)] * fb[col];
                 }
             }
         }
         if (warp == 0) {
             const bool whole = at == ubegin && uend <= end;
-            if (whole) {
-                const float vg = p.c.v_gscale ? p.c.v_gscale[h] : 1.0f;
+            const float vg = p.c.v_gscale ? p.c.v_gscale[h] : 1.0f;
+            float* part = reinterpret_cast<float*>(p.ws + kPartOff) + (2ll * blockIdx.x + (at == ubegin ? 1 : 0)) * Part<W>::kFloats;
 #pragma unroll
-                for (int row = 0; row < 2; ++row) {
-                    const int col = g + 8 * row;
-                    if (col >= cols) continue;
-                    const long long id = (long long)ct * kCols + col;
-                    const long long r = q.first + id / p.group;
-                    const int hq = h * p.group + (int)(id % p.group);
-                    const float f = norm(st.m[row], st.l[row], vg);
-                    __nv_bfloat16* o = p.out + r * p.out_row + (long long)hq * p.out_head;
-                    // elements n W/8 + j of n = 2 c, 2 c + 1
+            for (int i = 0; i < 2; ++i) {
+                const int col = mycol[i];
+                const long long id = (long long)ct * kCols + col;
+                const long long r = q.first + id / p.group;
+                const int hq = h * p.group + (int)(id % p.group);
+                // the lane's elements of the column in runs of W/8
+                constexpr int kRuns = kCols == 16 ? 2 : 1;
 #pragma unroll
-                    for (int k = 0; k < W / 4; k += 8) {
-                        const int e = k / (W / 8), j = k % (W / 8);
-                        uint32_t w[4];
+                for (int e = 0; e < kRuns; ++e) {
+                    auto value = [&](int j) { return kCols == 16 ? st.o[j][2 * i + e] : st.o[j >> 1][2 * (j & 1) + i]; };
+                    const int d = (kCols == 16 ? 2 * c + e : g) * (W / 8);
+                    if (whole) {
+                        if (col >= cols) continue;
+                        const float f = norm(st.m[i], st.l[i], vg);
+                        __nv_bfloat16* o = p.out + r * p.out_row + (long long)hq * p.out_head + d;
 #pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            w[i] = cvt_bf16x2(f2(st.o[j + 2 * i][2 * row + e] * f, st.o[j + 2 * i + 1][2 * row + e] * f));
-                        const int d = (2 * c + e) * (W / 8) + j;
-                        if (d < p.c.D) *reinterpret_cast<uint4*>(o + d) = make_uint4(w[0], w[1], w[2], w[3]);
-                    }
-                    if (p.lse && c == 0)
-                        p.lse[r * p.Hq + hq] = log_sum(st.m[row], st.l[row]);
-                }
-            } else {
-                float* part = reinterpret_cast<float*>(p.ws + kPartOff) +
-                              (2ll * blockIdx.x + (at == ubegin ? 1 : 0)) * Part<W>::kFloats;
+                        for (int j = 0; j < W / 8; j += 8) {
+                            uint32_t w[4];
 #pragma unroll
-                for (int row = 0; row < 2; ++row) {
-                    const int col = g + 8 * row;
-                    if (c == 0) {
-                        part[col] = st.m[row];
-                        part[kCols + col] = st.l[row];
-                    }
-                    float* o = part + 2 * kCols + col * W;
+                            for (int k = 0; k < 4; ++k)
+                                w[k] = cvt_bf16x2(f2(value(j + 2 * k) * f, value(j + 2 * k + 1) * f));
+                            if (d + j < p.c.D) *reinterpret_cast<uint4*>(o + j) = make_uint4(w[0], w[1], w[2], w[3]);
+                        }
+                    } else {
+                        float* o = part + 2 * kPartCols + col * W + d;
 #pragma unroll
-                    for (int k = 0; k < W / 4; k += 4) {
-                        const int e = k / (W / 8), j = k % (W / 8);
-                        *reinterpret_cast<float4*>(o + (2 * c + e) * (W / 8) + j) =
-                            make_float4(st.o[j][2 * row + e], st.o[j + 1][2 * row + e], st.o[j + 2][2 * row + e],
-                                        st.o[j + 3][2 * row + e]);
+                        for (int j = 0; j < W / 8; j += 4)
+                            *reinterpret_cast<float4*>(o + j) = make_float4(value(j), value(j + 1), value(j + 2), value(j + 3));
                     }
                 }
-                // the first cut of a unit stands with the CTA behind it
-                const long long before = ubegin / chunk;
-                if (lane == 0 && at != ubegin && before + 1 == blockIdx.x)
-                    *cut = Cut{s, h, ct, (int)((uend - 1) / chunk - before + 1)};
+                if (kCols == 16 ? c == 0 : g == 0) {
+                    if (!whole) {
+                        part[col] = st.m[i];
+                        part[kPartCols + col] = st.l[i];
+                    } else if (p.lse && col < cols) {
+                        p.lse[r * p.Hq + hq] = log_sum(st.m[i], st.l[i]);
+                    }
+                }
             }
+            // the first cut of a unit stands with the CTA behind it
+            const long long before = ubegin / chunk;
+            if (!whole && lane == 0 && at != ubegin && before + 1 == blockIdx.x)
+                *cut = Cut{s, h, ct, (int)((uend - 1) / chunk - before + 1)};
         }
         at = ubegin + t1;
     }
 }
 
 // One column of a unit that was cut: block (cut, column).
-template <int W>
+template <int W, int kCols>
 __global__ void __launch_bounds__(128) cache_join_kernel(const __grid_constant__ AttnParams p)
 {
     constexpr int kLanes = W / 4;                 // threads of a partial, four elements each
@@ -678,7 +740,7 @@ __global__ void __launch_bounds__(128) cache_join_kernel(const __grid_constant__
     griddep_wait();
     const Cut cut = reinterpret_cast<const Cut*>(p.ws + kCutOff)[blockIdx.x];
     if (cut.count == 0) return;
-    const Seq q = sequence(p, cut.seq);
+    const Seq q = sequence<kCols>(p, cut.seq);
     const long long id = (long long)cut.tile * kCols + blockIdx.y;
     if (id >= q.rows * p.group) return;
     const int col = blockIdx.y;
@@ -693,7 +755,7 @@ __global__ void __launch_bounds__(128) cache_join_kernel(const __grid_constant__
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
     float l = 0.0f;
-    for (int i = threadIdx.x & 31; i < cut.count; i += 32) l += part(i)[kCols + col] * exp2f(part(i)[col] - m);
+    for (int i = threadIdx.x & 31; i < cut.count; i += 32) l += part(i)[kPartCols + col] * exp2f(part(i)[col] - m);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
     const int lane = threadIdx.x % kLanes;
@@ -702,7 +764,7 @@ __global__ void __launch_bounds__(128) cache_join_kernel(const __grid_constant__
     for (int i = threadIdx.x / kLanes; i < cut.count; i += kSplit) {
         const float* a = part(i);
         const float f = exp2f(a[col] - m);
-        const float4 v = *reinterpret_cast<const float4*>(a + 2 * kCols + col * W + 4 * lane);
+        const float4 v = *reinterpret_cast<const float4*>(a + 2 * kPartCols + col * W + 4 * lane);
         acc.x = fmaf(v.x, f, acc.x), acc.y = fmaf(v.y, f, acc.y);
         acc.z = fmaf(v.z, f, acc.z), acc.w = fmaf(v.w, f, acc.w);
     }
@@ -722,11 +784,11 @@ __global__ void __launch_bounds__(128) cache_join_kernel(const __grid_constant__
     if (p.lse && lane == 0) p.lse[r * p.Hq + hq] = log_sum(m, l);
 }
 
-template <int W>
+template <int W, int kCols>
 cudaError_t launch(const AttnParams& p, cudaStream_t s)
 {
-    using C = Config<W>;
-    const cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void*>(cache_attn_kernel<W>), (int)C::kSmem);
+    using C = Config<W, kCols>;
+    const cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void*>(cache_attn_kernel<W, kCols>), (int)C::kSmem);
     if (e != cudaSuccess) return e;
     int ctas = sm_count_current_device() * C::kCtasPerSm;
     if (ctas > kMaxCtas) ctas = kMaxCtas;
@@ -740,12 +802,12 @@ cudaError_t launch(const AttnParams& p, cudaStream_t s)
     cfg.stream = s;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    const cudaError_t first = cudaLaunchKernelEx(&cfg, cache_attn_kernel<W>, p);
+    const cudaError_t first = cudaLaunchKernelEx(&cfg, cache_attn_kernel<W, kCols>, p);
     if (first != cudaSuccess) return first;
     cfg.gridDim = dim3((unsigned)ctas, kCols);
     cfg.blockDim = dim3(128);
     cfg.dynamicSmemBytes = 0;
-    return cudaLaunchKernelEx(&cfg, cache_join_kernel<W>, p);
+    return cudaLaunchKernelEx(&cfg, cache_join_kernel<W, kCols>, p);
 }
 
 }  // namespace
@@ -775,7 +837,12 @@ cudaError_t launch_cache_attn(const CacheAttnJob& job, cudaStream_t s)
     p.ws = job.ws;
     p.wait_ns = job.wait_limit_ns;
     const int w = cache_width(job.c.D);
-    return w == 64 ? launch<64>(p, s) : w == 128 ? launch<128>(p, s) : launch<256>(p, s);
+    // Eight columns a unit where a sequence has no more on average (its rows times the heads of a kv head):
+    // half the products, scores and registers.  Either is right for any rows.
+    const bool narrow = (p.M + p.c.nseq - 1) / p.c.nseq * p.group <= 8;
+    if (w == 64) return narrow ? launch<64, 8>(p, s) : launch<64, 16>(p, s);
+    if (w == 128) return narrow ? launch<128, 8>(p, s) : launch<128, 16>(p, s);
+    return narrow ? launch<256, 8>(p, s) : launch<256, 16>(p, s);
 }
 
 }  // namespace h3fp4
