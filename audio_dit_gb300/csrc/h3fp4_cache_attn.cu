@@ -38,7 +38,8 @@ namespace {
 
 constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
-constexpr int kTile = kCacheGroup * kWarps;   // tokens of a tile
+constexpr int kStep = 2 * kCacheGroup;        // tokens that a warp takes at a time
+constexpr int kTile = kStep * kWarps;         // tokens of a tile
 constexpr int kPartCols = 16;                 // query columns of a unit at most
 constexpr int kMaxCtas = 608;                 // of a launch: the workspace is made for as many
 constexpr float kRaise = 14.0f, kStart = 6.0f;  // in powers of two: see above
@@ -47,7 +48,8 @@ constexpr float kNone = -3.4e38f, kLowest = -3.0e38f;
 
 // What a CTA leaves for the joining kernel about the cut at its first tile.
 struct Cut {
-    int seq, head, tile, count;   // the unit, and of how many CTAs it takes partials (0: no first cut)
+    long long first;              // packed row of the unit's sequence's first
+    int head, col, cols, count;   // kv head, the unit's first column and how many; of how many CTAs it takes partials (0: no first cut)
 };
 
 // Partial sums: per CTA one of a unit that began before it, one of a unit that goes on after it.
@@ -58,18 +60,6 @@ struct Part {
 
 constexpr size_t kCutOff = 256;
 constexpr size_t kPartOff = kCutOff + kMaxCtas * sizeof(Cut);
-
-template <int W, int kCols>
-struct Config {
-    static constexpr int kSlots = W == 256 ? (kCols == 16 ? 3 : 2) : W == 128 ? 4 : 6;   // groups in flight per warp
-    static constexpr int kCtasPerSm = W == 256 ? (kCols == 16 ? 2 : 3) : kCols == 16 ? 3 : 4;
-    static constexpr int kMergeRegs = W * kCols / 32 + 4;              // a lane's state: O, two maxima, two sums
-    static constexpr uint32_t kRing = kWarps * kSlots * CacheLayout<W>::kGroupBytes;
-    static constexpr uint32_t kMerge = 2 * kMergeRegs * 32 * 4;
-    static constexpr uint32_t kPrefix = (kCacheMaxSeqs + 1) * 8;
-    static constexpr uint32_t kBars = kWarps * kSlots * 8;
-    static constexpr uint32_t kSmem = kRing + kMerge + kPrefix + kBars;
-};
 
 struct AttnParams {
     CacheView c;
@@ -84,36 +74,58 @@ struct AttnParams {
     unsigned long long wait_ns;
 };
 
-// The rows of sequence s and its units.  Row offsets may hold anything: they are kept inside
+// The rows of a sequence and its units.  Row offsets may hold anything: they are kept inside
 // the M rows that there are.
 struct Seq {
-    long long first, rows, len;   // packed rows [first, first + rows), tokens that the table has room for
-    long long start;              // position of the first row
-    int coltiles, tiles;
+    int first, rows, len;   // packed rows [first, first + rows), tokens that the table has room for
+    int start;              // position of the first row
 };
 
-template <int kCols>
 __device__ __forceinline__ Seq sequence(const AttnParams& p, int s)
 {
-    Seq q;
     long long a = s, b = s + 1;
     if (p.c.row_off) {
         a = p.c.row_off[s];
         b = p.c.row_off[s + 1];
     }
-    q.start = (long long)p.c.length[s] - (b - a);
+    const long long n = p.c.length[s], room = p.c.max_pages * p.c.page;
+    long long start = n - (b - a);
     if (a < 0) {
-        q.start -= a;
+        start -= a;
         a = 0;
     }
-    b = b < p.M ? b : p.M;
-    q.first = a;
-    q.rows = b > a ? b - a : 0;
-    q.len = cache_length(p.c, s);
-    q.coltiles = (int)((q.rows * p.group + kCols - 1) / kCols);
-    q.tiles = (int)((q.len + kTile - 1) / kTile);
+    b = min(b, p.M);
+    Seq q;
+    q.first = (int)a;
+    q.rows = b > a ? (int)(b - a) : 0;
+    q.len = (int)max(0ll, min(n, room));
+    q.start = (int)max(start, -(1ll << 30));
     return q;
 }
+
+// Units of a kv head, tiles of a unit.
+template <int kCols>
+__device__ __forceinline__ int col_tiles(const AttnParams& p, const Seq& q)
+{
+    return (int)(((long long)q.rows * p.group + kCols - 1) / kCols);
+}
+
+__device__ __forceinline__ int key_tiles(const Seq& q) { return (int)(((long long)q.len + kTile - 1) / kTile); }
+
+template <int W, int kCols>
+struct Config {
+    static constexpr int kSlots = W == 64 ? 3 : 2;                     // steps in flight per warp
+    static constexpr int kCtasPerSm = W == 256 ? 2 : kCols == 16 ? 3 : 4;
+    static constexpr int kMergeRegs = W * kCols / 32 + 4;              // a lane's state: O, two maxima, two sums
+    static constexpr uint32_t kSlot = 2 * CacheLayout<W>::kGroupBytes;
+    static constexpr uint32_t kRing = kWarps * kSlots * kSlot;
+    static constexpr uint32_t kMerge = 2 * kMergeRegs * 32 * 4;
+    static constexpr uint32_t kBars = kWarps * kSlots * 8;
+    static constexpr uint32_t kFixed = kRing + kMerge + kBars;
+    static_assert(kFixed % 16 == 0, "the sequences' table behind it");
+    // with the tiles before each sequence and the sequences
+    static uint32_t smem(int nseq) { return kFixed + (uint32_t)nseq * (sizeof(Seq) + 8) + 8; }
+};
 
 __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar)
 {
@@ -186,6 +198,13 @@ __device__ __forceinline__ float log_sum(float m, float l)
     return l == 0.0f ? -INFINITY : m < 0.99f * kLowest ? __int_as_float(0x7FFFFFFF) : (m + log2f(l)) * 0.6931471805599453f;
 }
 
+// a / b of non-negative values, in 32 bits where they fit (which costs a fifth).
+__device__ __forceinline__ long long div(long long a, long long b)
+{
+    if (((a | b) >> 32) == 0) return (uint32_t)a / (uint32_t)b;
+    return a / b;
+}
+
 // 2^x for an integer x in the normal range.
 __device__ __forceinline__ float pow2i(int x) { return __uint_as_float((uint32_t)(x + 127) << 23); }
 
@@ -243,120 +262,77 @@ __device__ __forceinline__ float over_lanes(float v, F f)
     return v;
 }
 
-// One group of 16 tokens.  kMasked: `left` tokens of it hold anything, `lim` are attended to by
-// the lane's two columns.
-template <int W, int kCols, bool kMasked>
-__device__ __forceinline__ void group_step(State<W, kCols>& st, const uint8_t* gp, int lane,
-                                           const uint32_t (&qf)[W / 16][kCols / 4], const float (&factor)[2], int left,
-                                           const int (&lim)[2])
+__device__ __forceinline__ uint32_t mul_half2(uint32_t a, __half2 b)
+{
+    const __half2 o = __hmul2(*reinterpret_cast<const __half2*>(&a), b);
+    return *reinterpret_cast<const uint32_t*>(&o);
+}
+
+// Scores of one group: two of the lane's columns by four tokens (16 columns: tokens 8 half + 2 c + (0, 1),
+// 8 columns: tokens g, g + 8, two chains of sums).
+template <int W, int kCols>
+__device__ __forceinline__ void scores(float (&s)[2][4], const uint8_t* gp, int lane, const uint32_t (&qf)[W / 16][kCols / 4])
 {
     using L = CacheLayout<W>;
-    const int g = lane >> 2, c = lane & 3;
-    // ------------------------------------------------------------ scores of 8 values: two of the lane's
-    // columns by four tokens (16 columns: tokens 8 half + 2 c + (0, 1); 8 columns: tokens g, g + 8)
-    float s[2][4];
-    {
-        uint32_t sc[W == 256 ? 2 : 1];   // the lane's scales of tokens g (low half) and g + 8
-        if constexpr (W == 256) ld_words<2>(gp + L::kKScale + lane * 8, sc);
-        else if constexpr (W == 128) sc[0] = *reinterpret_cast<const uint32_t*>(gp + L::kKScale + lane * 4);
-        else sc[0] = *reinterpret_cast<const uint16_t*>(gp + L::kKScale + lane * 2);
-        constexpr int kRuns = W == 256 ? 2 : 1, kWords = W == 64 ? 2 : 4;
+    uint32_t sc[W == 256 ? 2 : 1];   // the lane's scales of tokens g (low half) and g + 8
+    if constexpr (W == 256) ld_words<2>(gp + L::kKScale + lane * 8, sc);
+    else if constexpr (W == 128) sc[0] = *reinterpret_cast<const uint32_t*>(gp + L::kKScale + lane * 4);
+    else sc[0] = *reinterpret_cast<const uint16_t*>(gp + L::kKScale + lane * 2);
+    constexpr int kRuns = W == 256 ? 2 : 1, kWords = W == 64 ? 2 : 4;
 #pragma unroll
-        for (int h = 0; h < 2; ++h) s[h][0] = s[h][1] = s[h][2] = s[h][3] = 0.0f;
+    for (int h = 0; h < 2; ++h) s[h][0] = s[h][1] = s[h][2] = s[h][3] = 0.0f;
 #pragma unroll
-        for (int run = 0; run < kRuns; ++run) {
-            uint32_t w[2][kWords], x[2][2];   // both tokens: codes, their two scales as f16x2
+    for (int run = 0; run < kRuns; ++run) {
+        uint32_t w[2][kWords];   // both tokens: codes, their two scales
+        __half2 x[2];
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+            ld_words<kWords>(W == 64 ? gp + half * 256 + lane * 8 : gp + run * 1024 + half * 512 + lane * 16, w[half]);
+            uint32_t pair;
+            if constexpr (W == 64) pair = e4m3x2_f16(half ? sc[0] >> 8 : sc[0]);   // (its first half counts)
+            else if constexpr (W == 128) pair = e4m3x2_f16(half ? sc[0] >> 16 : sc[0]);
+            else pair = e4m3x2_f16(run ? sc[half] >> 16 : sc[half]);
+            x[half] = *reinterpret_cast<const __half2*>(&pair);
+        }
+#pragma unroll
+        for (int i = 0; i < kWords; ++i) {
+            uint32_t f[2][4];
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
-                ld_words<kWords>(W == 64 ? gp + half * 256 + lane * 8 : gp + run * 1024 + half * 512 + lane * 16, w[half]);
-                uint32_t pair;
-                if constexpr (W == 64) {
-                    const uint32_t b = half ? sc[0] >> 8 : sc[0] & 0xFFu;
-                    pair = e4m3x2_f16(b | (b << 8));
-                } else if constexpr (W == 128) {
-                    pair = e4m3x2_f16(half ? sc[0] >> 16 : sc[0]);
-                } else {
-                    pair = e4m3x2_f16(run ? sc[half] >> 16 : sc[half]);
-                }
-                x[half][0] = __byte_perm(pair, pair, 0x1010);
-                x[half][1] = __byte_perm(pair, pair, 0x3232);
-            }
+                const __half2 by = W == 64 || 2 * i < kWords ? __low2half2(x[half]) : __high2half2(x[half]);
+                e2m1x8_f16(w[half][i], f[half]);
 #pragma unroll
-            for (int i = 0; i < kWords; ++i) {
-                uint32_t f[2][4];
+                for (int j = 0; j < 4; ++j) f[half][j] = mul_half2(f[half][j], by);
+            }
+            const int step = run * 8 + 2 * i;
+            if constexpr (kCols == 16) {
+                // Q's 16 columns are A's rows, the tokens B's columns
 #pragma unroll
                 for (int half = 0; half < 2; ++half) {
-                    e2m1x8_f16(w[half][i], f[half]);
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) f[half][j] = mul_f16x2(f[half][j], x[half][2 * i < kWords ? 0 : 1]);
+                    mma_f16(s[half], qf[step], f[half][0], f[half][1]);
+                    mma_f16(s[half], qf[step + 1], f[half][2], f[half][3]);
                 }
-                const int step = run * 8 + 2 * i;
-                if constexpr (kCols == 16) {
-                    // Q's 16 columns are A's rows, the tokens B's columns
-#pragma unroll
-                    for (int half = 0; half < 2; ++half) {
-                        mma_f16(s[half], qf[step], f[half][0], f[half][1]);
-                        mma_f16(s[half], qf[step + 1], f[half][2], f[half][3]);
-                    }
-                } else {
-                    // the tokens are A's rows, Q's 8 columns B's; two chains of sums
-                    const uint32_t a0[4] = {f[0][0], f[1][0], f[0][1], f[1][1]};
-                    const uint32_t a1[4] = {f[0][2], f[1][2], f[0][3], f[1][3]};
-                    mma_f16(s[0], a0, qf[step][0], qf[step][1]);
-                    mma_f16(s[1], a1, qf[step + 1][0], qf[step + 1][1]);
-                }
+            } else {
+                // the tokens are A's rows, Q's 8 columns B's
+                const uint32_t a0[4] = {f[0][0], f[1][0], f[0][1], f[1][1]};
+                const uint32_t a1[4] = {f[0][2], f[1][2], f[0][3], f[1][3]};
+                mma_f16(s[0], a0, qf[step][0], qf[step][1]);
+                mma_f16(s[1], a1, qf[step + 1][0], qf[step + 1][1]);
             }
         }
-        if constexpr (kCols == 8) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) s[0][i] += s[1][i];
-        }
-    }
-    // ------------------------------------------------------------ exponents
-    constexpr int kF = kCols / 8;
-#pragma unroll
-    for (int h = 0; h < kF; ++h)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int col = column_of<kCols>(i);
-            s[h][i] = max_nan(s[h][i] * factor[col], kLowest);
-            if (kMasked) {
-                const int token = kCols == 16 ? 8 * h + 2 * c + (i & 1) : g + 8 * (i >> 1);
-                if (token >= lim[col]) s[h][i] = -INFINITY;
-            }
-        }
-    float top[2];
-#pragma unroll
-    for (int col = 0; col < 2; ++col) {
-        if constexpr (kCols == 16) top[col] = fmaxf(fmaxf(s[0][2 * col], s[0][2 * col + 1]), fmaxf(s[1][2 * col], s[1][2 * col + 1]));
-        else top[col] = fmaxf(s[0][col], s[0][2 + col]);
-    }
-    if (__any_sync(0xffffffffu, top[0] > st.m[0] + kRaise || top[1] > st.m[1] + kRaise)) {
-#pragma unroll
-        for (int col = 0; col < 2; ++col) {
-            const float t = over_lanes<kCols>(top[col], [](float a, float b) { return fmaxf(a, b); });
-            if (t > st.m[col] + kRaise) rescale<W, kCols>(st, col, t - kStart);
-        }
-    }
-    uint32_t pf[kCols == 16 ? 4 : 2];   // P as the second product's A (16 columns) or, transposed, its B
-#pragma unroll
-    for (int h = 0; h < kF; ++h) {
-        float e[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int col = column_of<kCols>(i);
-            e[i] = ex2_approx_ftz(s[h][i] - st.m[col]);
-            st.l[col] += e[i];
-        }
-        pf[2 * h] = pack_f16x2(e[0], e[1]);
-        pf[2 * h + 1] = pack_f16x2(e[2], e[3]);
     }
     if constexpr (kCols == 8) {
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
-            asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %0;" : "+r"(pf[h]));
+        for (int i = 0; i < 4; ++i) s[0][i] += s[1][i];
     }
-    // ------------------------------------------------------------ O += P V, token pairs 8 half + 2 c + (0, 1)
+}
+
+// O += P V of one group, token pairs 8 half + 2 c + (0, 1).  kMasked: `left` tokens of it hold anything.
+template <int W, int kCols, bool kMasked>
+__device__ __forceinline__ void values(State<W, kCols>& st, const uint8_t* gp, int lane, const uint32_t (&pf)[kCols / 4], int left)
+{
+    using L = CacheLayout<W>;
+    const int g = lane >> 2, c = lane & 3;
     constexpr int kVBlocks = W == 256 ? 2 : 1;      // scale blocks of a lane
     constexpr int kVWords = W == 64 ? 1 : W == 128 ? 2 : 4;  // words of a token
     uint32_t vs[2][kVBlocks];
@@ -421,6 +397,64 @@ __device__ __forceinline__ void group_step(State<W, kCols>& st, const uint8_t* g
     }
 }
 
+// Two groups of 16 tokens.  kMasked: of group e `left[e]` tokens hold anything and `lim[e]` are
+// attended to by the lane's two columns; scores that leave fp32's range downwards stay finite.
+template <int W, int kCols, bool kMasked>
+__device__ __forceinline__ void step(State<W, kCols>& st, const uint8_t* gp, int lane, const uint32_t (&qf)[W / 16][kCols / 4],
+                                     const float (&factor)[2], const int (&left)[2], const int (&lim)[2][2])
+{
+    constexpr int kF = kCols / 8;   // fragments of four scores a group
+    const int g = lane >> 2, c = lane & 3;
+    float s[2][2][4];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) scores<W, kCols>(s[e], gp + e * CacheLayout<W>::kGroupBytes, lane, qf);
+    float top[2] = {kNone, kNone};
+#pragma unroll
+    for (int e = 0; e < 2; ++e)
+#pragma unroll
+        for (int h = 0; h < kF; ++h)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int col = column_of<kCols>(i);
+                float& v = s[e][h][i];
+                v *= factor[col];
+                if (kMasked) {
+                    const int token = kCols == 16 ? 8 * h + 2 * c + (i & 1) : g + 8 * (i >> 1);
+                    v = token < lim[e][col] ? max_nan(v, kLowest) : -INFINITY;
+                }
+                top[col] = fmaxf(top[col], v);
+            }
+    if (__any_sync(0xffffffffu, top[0] > st.m[0] + kRaise || top[1] > st.m[1] + kRaise)) {
+#pragma unroll
+        for (int col = 0; col < 2; ++col) {
+            const float t = over_lanes<kCols>(top[col], [](float a, float b) { return fmaxf(a, b); });
+            if (t > st.m[col] + kRaise) rescale<W, kCols>(st, col, t - kStart);
+        }
+    }
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+        uint32_t pf[kCols / 4];   // P as the second product's A (16 columns) or, transposed, its B
+#pragma unroll
+        for (int h = 0; h < kF; ++h) {
+            float x[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int col = column_of<kCols>(i);
+                x[i] = ex2_approx_ftz(s[e][h][i] - st.m[col]);
+                st.l[col] += x[i];
+            }
+            pf[2 * h] = pack_f16x2(x[0], x[1]);
+            pf[2 * h + 1] = pack_f16x2(x[2], x[3]);
+        }
+        if constexpr (kCols == 8) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+                asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %0;" : "+r"(pf[h]));
+        }
+        values<W, kCols, kMasked>(st, gp + e * CacheLayout<W>::kGroupBytes, lane, pf, left[e]);
+    }
+}
+
 // The larger reference of two states, and what their sums are scaled with.
 __device__ __forceinline__ void join_scale(float a, float b, float& m, float& fa, float& fb)
 {
@@ -438,10 +472,12 @@ __global__ void __launch_bounds__(kThreads, Config<W, kCols>::kCtasPerSm)
     using S = State<W, kCols>;
     extern __shared__ __align__(128) uint8_t smem[];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
-    uint8_t* ring = smem + warp * (C::kSlots * L::kGroupBytes);
+    uint8_t* ring = smem + warp * (C::kSlots * C::kSlot);
     float* merge = reinterpret_cast<float*>(smem + C::kRing);
-    long long* prefix = reinterpret_cast<long long*>(smem + C::kRing + C::kMerge);
-    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::kRing + C::kMerge + C::kPrefix) + warp * C::kSlots;
+    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::kRing + C::kMerge) + warp * C::kSlots;
+    const int nseq = p.c.nseq;
+    Seq* seqs = reinterpret_cast<Seq*>(smem + C::kFixed);
+    long long* prefix = reinterpret_cast<long long*>(seqs + nseq);
     __shared__ long long warp_sum[kWarps];
     unsigned int* status = reinterpret_cast<unsigned int*>(p.ws);
     if (lane == 0) {
@@ -450,15 +486,17 @@ __global__ void __launch_bounds__(kThreads, Config<W, kCols>::kCtasPerSm)
     }
     griddep_wait();
     griddep_launch_dependents();
-    const int nseq = p.c.nseq;
 
     // ------------------------------------------------------------ tiles before each sequence
     {
-        const int per = (nseq + kThreads - 1) / kThreads, s0 = threadIdx.x * per;
+        // each thread's run of sequences
+        const int per = (nseq + kThreads - 1) / kThreads, s0 = min(nseq, (int)threadIdx.x * per), s1 = min(nseq, s0 + per);
+        auto tiles = [&](const Seq& q) { return (long long)p.c.Hkv * col_tiles<kCols>(p, q) * key_tiles(q); };
         long long mine = 0;
-        for (int s = s0; s < s0 + per && s < nseq; ++s) {
-            const Seq q = sequence<kCols>(p, s);
-            mine += (long long)p.c.Hkv * q.coltiles * q.tiles;
+        for (int s = s0; s < s1; ++s) {
+            const Seq q = sequence(p, s);
+            seqs[s] = q;
+            mine += tiles(q);
         }
         long long upto = mine;
 #pragma unroll
@@ -470,24 +508,23 @@ __global__ void __launch_bounds__(kThreads, Config<W, kCols>::kCtasPerSm)
         __syncthreads();
         for (int w = 0; w < warp; ++w) upto += warp_sum[w];
         long long before = upto - mine;
-        for (int s = s0; s < s0 + per && s < nseq; ++s) {
+        for (int s = s0; s < s1; ++s) {
             prefix[s] = before;
-            const Seq q = sequence<kCols>(p, s);
-            before += (long long)p.c.Hkv * q.coltiles * q.tiles;
+            before += tiles(seqs[s]);
         }
         if (threadIdx.x == kThreads - 1) prefix[nseq] = upto;
         __syncthreads();
     }
     const long long total = prefix[nseq];
-    const long long chunk = (total + gridDim.x - 1) / gridDim.x;
+    const long long chunk = max(1ll, div(total + gridDim.x - 1, gridDim.x));
     const long long begin = min(total, chunk * blockIdx.x), end = min(total, begin + chunk);
 
     // rows of sequences that hold nothing
     for (int s = blockIdx.x; s < nseq; s += gridDim.x) {
-        const Seq q = sequence<kCols>(p, s);
-        if (q.tiles > 0) continue;
+        const Seq q = seqs[s];
+        if (q.len > 0) continue;
         const int vecs = p.c.D / 8;
-        for (long long i = threadIdx.x; i < q.rows * p.Hq * vecs; i += kThreads) {
+        for (long long i = threadIdx.x; i < (long long)q.rows * p.Hq * vecs; i += kThreads) {
             const long long r = q.first + i / (p.Hq * vecs);
             const int h = (int)(i / vecs % p.Hq), v = (int)(i % vecs);
             *reinterpret_cast<uint4*>(p.out + r * p.out_row + (long long)h * p.out_head + 8 * v) = make_uint4(0, 0, 0, 0);
@@ -495,7 +532,7 @@ __global__ void __launch_bounds__(kThreads, Config<W, kCols>::kCtasPerSm)
         }
     }
     Cut* cut = reinterpret_cast<Cut*>(p.ws + kCutOff) + blockIdx.x;
-    if (threadIdx.x == 0) *cut = Cut{0, 0, 0, 0};
+    if (threadIdx.x == 0) *cut = Cut{0, 0, 0, 0, 0};
 
     // ------------------------------------------------------------ units
     uint32_t phases = 0;    // of the ring's barriers, one bit each
@@ -513,17 +550,16 @@ __global__ void __launch_bounds__(kThreads, Config<W, kCols>::kCtasPerSm)
             }
             s = lo;
         }
-        const Seq q = sequence<kCols>(p, s);
-        const long long unit = (at - prefix[s]) / q.tiles;
-        const int h = (int)(unit / q.coltiles), ct = (int)(unit % q.coltiles);
-        const long long ubegin = prefix[s] + unit * q.tiles, uend = ubegin + q.tiles;
+        const Seq q = seqs[s];
+        const int coltiles = col_tiles<kCols>(p, q), tiles = key_tiles(q);
+        const long long unit = div(at - prefix[s], tiles);
+        const int h = (int)div(unit, coltiles), ct = (int)(unit - (long long)h * coltiles);
+        const long long ubegin = prefix[s] + unit * tiles, uend = ubegin + tiles;
         const int t0 = (int)(at - ubegin), t1 = (int)(min(end, uend) - ubegin);
         // what each column attends to
-        const int cols = (int)min((long long)kCols, q.rows * p.group - (long long)ct * kCols);
-        auto limit = [&](int col) -> int {
-            const long long row = ((long long)ct * kCols + col) / p.group;
-            return (int)(p.causal ? max(0ll, min(q.len, q.start + row + 1)) : q.len);
-        };
+        // (rows times heads of a call are below 2^31)
+        const int cols = min(kCols, q.rows * p.group - ct * kCols);
+        auto limit = [&](int col) { return p.causal ? max(0, min(q.len, q.start + (ct * kCols + col) / p.group + 1)) : q.len; };
         // the lane's two columns
         int mycol[2], mylim[2];
         const int least = limit(0), most = limit(cols - 1);
@@ -533,62 +569,71 @@ __global__ void __launch_bounds__(kThreads, Config<W, kCols>::kCtasPerSm)
             mylim[i] = mycol[i] < cols ? limit(mycol[i]) : most;
         }
 
-        // this warp's groups: tile t's group of 16 tokens is 4 t + warp, up to the last token that any column sees
-        const int groups = (most - 1) / kCacheGroup + (most > 0 ? 1 : 0);
-        const int g0 = kWarps * t0 + warp;   // the first, then every fourth
-        int n = 0;
-        if (groups > g0) n = min(t1 - t0, (groups - g0 + kWarps - 1) / kWarps);
-        const int32_t* table = p.c.table + (long long)s * p.c.max_pages;
-        // where the next 32 groups lie, one per lane (null: no page of the pool)
-        const uint8_t* where = nullptr;
-        auto look = [&](int i) {
-            const int gi = g0 + kWarps * (i + lane);
-            where = nullptr;
-            if (i + lane < n) {
-                const int pg = table[gi / per_page];
-                if (pg >= 0 && pg < p.c.n_pages)
-                    where = p.c.pool + (((long long)pg * p.c.Hkv + h) * per_page + gi % per_page) * L::kGroupBytes;
-            }
-        };
-        uint32_t there = 0;   // slots whose group exists
-        auto load = [&](int i, int slot) {
-            if ((i & 31) == 0) look(i);
-            const uint64_t src = __shfl_sync(0xffffffffu, reinterpret_cast<uint64_t>(where), i & 31);
-            there = src ? there | (1u << slot) : there & ~(1u << slot);
-            if (lane == 0 && !p.stall) {
-                if (src) {
-                    mbar_arrive_expect_tx(&bars[slot], L::kGroupBytes);
-                    bulk_load(ring + slot * L::kGroupBytes, reinterpret_cast<const void*>(src), L::kGroupBytes, &bars[slot]);
-                } else {
-                    mbar_arrive(&bars[slot]);
-                }
-            }
-        };
-        int loaded = 0;
-        if (!lost)
-            for (; loaded < min(n, C::kSlots); ++loaded) load(loaded, loaded);
-
-        // Q's fragments: the lane's elements of columns g (and g + 8), scaled to f16's range
-        uint32_t qf[W / 16][kCols / 4];
-        float factor[2], mine[kCols / 8];
-        const float kg = p.c.k_gscale ? p.c.k_gscale[h] : 1.0f;
+        // Q: the lane's elements of columns g (and g + 8)
+        uint2 raw[kCols / 8][W / 16];
 #pragma unroll
         for (int half = 0; half < kCols / 8; ++half) {
-            const int col = g + 8 * half;
-            const long long id = (long long)ct * kCols + col;
+            const int col = g + 8 * half, id = ct * kCols + col;
             const __nv_bfloat16* src = nullptr;
             if (col < cols)
-                src = p.q.p + (q.first + id / p.group) * p.q.row + (long long)(h * p.group + (int)(id % p.group)) * p.q.head;
-            uint2 raw[W / 16];
-            uint32_t top = 0;
+                src = p.q.p + (long long)(q.first + id / p.group) * p.q.row + (long long)(h * p.group + id % p.group) * p.q.head;
 #pragma unroll
             for (int t = 0; t < W / 16; ++t) {
                 const int d = W == 64 ? 16 * c + 4 * t : (t >> 3) * 128 + 32 * c + 4 * (t & 7);
-                raw[t] = make_uint2(0, 0);
-                if (src && d < p.c.D) raw[t] = *reinterpret_cast<const uint2*>(src + d);
-                top = max(top, max(max(raw[t].x & 0x7FFFu, (raw[t].x >> 16) & 0x7FFFu),
-                                   max(raw[t].y & 0x7FFFu, (raw[t].y >> 16) & 0x7FFFu)));
+                raw[half][t] = make_uint2(0, 0);
+                if (src && d < p.c.D) raw[half][t] = *reinterpret_cast<const uint2*>(src + d);
             }
+        }
+        const float kg = p.c.k_gscale ? p.c.k_gscale[h] : 1.0f, vg = p.c.v_gscale ? p.c.v_gscale[h] : 1.0f;
+
+        // this warp's steps of 32 tokens: tile t's is 4 t + warp, up to the last token that any column sees
+        const int steps = most > 0 ? (most - 1) / kStep + 1 : 0;
+        const int g0 = kWarps * t0 + warp;   // the first, then every fourth
+        int n = 0;
+        if (steps > g0) n = min(t1 - t0, (steps - g0 + kWarps - 1) / kWarps);
+        const int32_t* table = p.c.table + (long long)s * p.c.max_pages;
+        // where the groups of the next 16 steps lie, one per lane, and which of them the pool has
+        const uint8_t* where = nullptr;
+        uint32_t has = 0;
+        auto look = [&](int i) {
+            const int gi = 2 * (g0 + kWarps * (i + (lane >> 1))) + (lane & 1);
+            int pg = -1;
+            if ((uint32_t)gi * kCacheGroup < (uint32_t)most) pg = table[gi / per_page];
+            const bool ok = pg >= 0 && pg < p.c.n_pages;
+            if (ok) where = p.c.pool + (((long long)pg * p.c.Hkv + h) * per_page + gi % per_page) * L::kGroupBytes;
+            has = __ballot_sync(0xffffffffu, ok);
+        };
+        uint32_t there = 0;   // which groups of the slots exist, two bits each
+        auto load = [&](int i, int slot) {
+            if ((i & 15) == 0) look(i);
+            const int first = 2 * (i & 15);
+            const uint32_t two = (has >> first) & 3u;
+            there = (there & ~(3u << (2 * slot))) | (two << (2 * slot));
+            if (lane - first == 0 || lane - first == 1) {
+                // (a copy may end before its bytes are expected: the arrival holds the phase open)
+                if (p.stall) return;
+                if (lane == first) {
+                    if (two) mbar_arrive_expect_tx(&bars[slot], __popc(two) * L::kGroupBytes);
+                    else mbar_arrive(&bars[slot]);
+                }
+                if ((two >> (lane - first)) & 1u)
+                    bulk_load(ring + slot * C::kSlot + (lane - first) * L::kGroupBytes, where, L::kGroupBytes, &bars[slot]);
+            }
+        };
+        int loaded = 0;
+        if (lost) n = 0;
+        for (; loaded < min(n, C::kSlots); ++loaded) load(loaded, loaded);
+
+        // ... scaled to f16's range
+        uint32_t qf[W / 16][kCols / 4];
+        float factor[2], mine[kCols / 8];
+#pragma unroll
+        for (int half = 0; half < kCols / 8; ++half) {
+            uint32_t top = 0;
+#pragma unroll
+            for (int t = 0; t < W / 16; ++t)
+                top = max(top, max(max(raw[half][t].x & 0x7FFFu, (raw[half][t].x >> 16) & 0x7FFFu),
+                                   max(raw[half][t].y & 0x7FFFu, (raw[half][t].y >> 16) & 0x7FFFu)));
             top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
             top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
             // the largest to [2^14, 2^15), by a power of two in the normal range
@@ -600,8 +645,8 @@ __global__ void __launch_bounds__(kThreads, Config<W, kCols>::kCtasPerSm)
                 auto f16 = [&](uint32_t w) {
                     return pack_f16x2(__uint_as_float(w << 16) * up, __uint_as_float(w & 0xFFFF0000u) * up);
                 };
-                qf[t][kCols == 16 ? half : 0] = f16(raw[t].x);
-                qf[t][kCols == 16 ? 2 + half : 1] = f16(raw[t].y);
+                qf[t][kCols == 16 ? half : 0] = f16(raw[half][t].x);
+                qf[t][kCols == 16 ? 2 + half : 1] = f16(raw[half][t].y);
             }
         }
 #pragma unroll
@@ -613,38 +658,50 @@ __global__ void __launch_bounds__(kThreads, Config<W, kCols>::kCtasPerSm)
         st.l[0] = st.l[1] = 0.0f;
 #pragma unroll
         for (int j = 0; j < S::kO; ++j) st.o[j][0] = st.o[j][1] = st.o[j][2] = st.o[j][3] = 0.0f;
-        const int plain = max(0, min(n, (least / kCacheGroup - g0 + kWarps - 1) / kWarps));   // groups that all columns see whole
+        // steps that all columns see whole, with scores that cannot leave fp32's range (a raw one is below 2^36)
+        const bool tame = __all_sync(0xffffffffu, fabsf(factor[0]) < 1e26f && fabsf(factor[1]) < 1e26f);
+        const int plain = tame ? max(0, min(n, (least / kStep - g0 + kWarps - 1) / kWarps)) : 0;
         int slot = 0;
-        for (int i = 0; i < n && !lost; ++i) {
-            const bool ok = mbar_wait(&bars[slot], (phases >> slot) & 1u, p.wait_ns, status, kStatusTimeoutMma);
-            if (!__all_sync(0xffffffffu, ok)) {
-                lost = true;
-                // copies in flight land before the CTA may end
-                if (!p.stall)
-                    for (int k = i; k < loaded; ++k) {
-                        (void)mbar_wait(&bars[slot], (phases >> slot) & 1u, p.wait_ns, status, kStatusTimeoutMma);
-                        slot = slot + 1 == C::kSlots ? 0 : slot + 1;
-                    }
-                break;
-            }
-            phases ^= 1u << slot;
-            if ((there >> slot) & 1u) {
-                const uint8_t* gp = ring + slot * L::kGroupBytes;
-                if (i < plain) {
-                    group_step<W, kCols, false>(st, gp, lane, qf, factor, kCacheGroup, mylim);
-                } else {
-                    const int first = (g0 + kWarps * i) * kCacheGroup;
-                    const int lim[2] = {mylim[0] - first, mylim[1] - first};
-                    group_step<W, kCols, true>(st, gp, lane, qf, factor, most - first, lim);
+#pragma unroll 1
+        for (int i = 0; i < n; ++i) {
+            {
+                const bool ok = mbar_wait(&bars[slot], (phases >> slot) & 1u, p.wait_ns, status, kStatusTimeoutMma);
+                if (!__all_sync(0xffffffffu, ok)) {
+                    lost = true;
+                    // copies in flight land before the CTA may end
+                    if (!p.stall)
+                        for (int k = i; k < loaded; ++k) {
+                            (void)mbar_wait(&bars[slot], (phases >> slot) & 1u, p.wait_ns, status, kStatusTimeoutMma);
+                            slot = slot + 1 == C::kSlots ? 0 : slot + 1;
+                        }
+                    break;
                 }
+                phases ^= 1u << slot;
+                const uint32_t two = (there >> (2 * slot)) & 3u;
+                const uint8_t* gp = ring + slot * C::kSlot;
+                if (i < plain && two == 3u) {
+                    const int left[2] = {kCacheGroup, kCacheGroup}, lim[2][2] = {};
+                    step<W, kCols, false>(st, gp, lane, qf, factor, left, lim);
+                } else if (two) {
+                    const int first = (g0 + kWarps * i) * kStep;
+                    int left[2], lim[2][2];
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const bool here = (two >> e) & 1u;
+                        left[e] = here ? most - first - e * kCacheGroup : 0;
+                        lim[e][0] = here ? mylim[0] - first - e * kCacheGroup : 0;
+                        lim[e][1] = here ? mylim[1] - first - e * kCacheGroup : 0;
+                    }
+                    step<W, kCols, true>(st, gp, lane, qf, factor, left, lim);
+                }
+                // (the products that used the slot's last bytes have been issued, so these were read)
+                __syncwarp();
+                if (loaded < n) {
+                    load(loaded, slot);
+                    ++loaded;
+                }
+                slot = slot + 1 == C::kSlots ? 0 : slot + 1;
             }
-            // (the products that used the slot's last bytes have been issued, so these were read)
-            __syncwarp();
-            if (loaded < n) {
-                load(loaded, slot);
-                ++loaded;
-            }
-            slot = slot + 1 == C::kSlots ? 0 : slot + 1;
         }
         __syncwarp();
 
@@ -679,14 +736,13 @@ __global__ void __launch_bounds__(kThreads, Config<W, kCols>::kCtasPerSm)
         }
         if (warp == 0) {
             const bool whole = at == ubegin && uend <= end;
-            const float vg = p.c.v_gscale ? p.c.v_gscale[h] : 1.0f;
             float* part = reinterpret_cast<float*>(p.ws + kPartOff) + (2ll * blockIdx.x + (at == ubegin ? 1 : 0)) * Part<W>::kFloats;
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 const int col = mycol[i];
-                const long long id = (long long)ct * kCols + col;
+                const int id = ct * kCols + col;
                 const long long r = q.first + id / p.group;
-                const int hq = h * p.group + (int)(id % p.group);
+                const int hq = h * p.group + id % p.group;
                 // the lane's elements of the column in runs of W/8
                 constexpr int kRuns = kCols == 16 ? 2 : 1;
 #pragma unroll
@@ -722,73 +778,92 @@ __global__ void __launch_bounds__(kThreads, Config<W, kCols>::kCtasPerSm)
                 }
             }
             // the first cut of a unit stands with the CTA behind it
-            const long long before = ubegin / chunk;
+            const long long before = div(ubegin, chunk);
             if (!whole && lane == 0 && at != ubegin && before + 1 == blockIdx.x)
-                *cut = Cut{s, h, ct, (int)((uend - 1) / chunk - before + 1)};
+                *cut = Cut{q.first, h, ct * kCols, cols, (int)(div(uend - 1, chunk) - before + 1)};
         }
         at = ubegin + t1;
     }
 }
 
-// One column of a unit that was cut: block (cut, column).
-template <int W, int kCols>
-__global__ void __launch_bounds__(128) cache_join_kernel(const __grid_constant__ AttnParams p)
+// Columns of a unit that was cut: block (cut, columns).  A warp works for one column by itself until the
+// last step, so that only latency counts: the cut, then references, sums and O of the partials together.
+constexpr int kJoinThreads = 512;
+
+template <int W>
+__global__ void __launch_bounds__(kJoinThreads) cache_join_kernel(const __grid_constant__ AttnParams p)
 {
-    constexpr int kLanes = W / 4;                 // threads of a partial, four elements each
-    constexpr int kSplit = 128 / kLanes;          // partials at a time
-    __shared__ float4 sum[128];
+    constexpr int kLanes = W / 4;                  // threads of a partial, four elements each
+    constexpr int kSplit = 4;                      // partials at a time
+    constexpr int kJoinCols = kJoinThreads / (kLanes * kSplit);
+    constexpr int kBatch = 4;                      // and of a thread in flight
+    __shared__ float weight[kJoinCols][kMaxCtas];
+    __shared__ float4 sum[kJoinThreads];
     griddep_wait();
     const Cut cut = reinterpret_cast<const Cut*>(p.ws + kCutOff)[blockIdx.x];
-    if (cut.count == 0) return;
-    const Seq q = sequence<kCols>(p, cut.seq);
-    const long long id = (long long)cut.tile * kCols + blockIdx.y;
-    if (id >= q.rows * p.group) return;
-    const int col = blockIdx.y;
+    if ((int)blockIdx.y * kJoinCols >= cut.cols || cut.count == 0) return;
+    const int t = threadIdx.x, lane = t & 31, mine = t / (kLanes * kSplit), split = t / kLanes % kSplit;
+    const int col = min((int)blockIdx.y * kJoinCols + mine, kPartCols - 1);   // (columns past the last are not written)
     // partial 0 is the CTA's before this one (its second), the others are the first ones
-    auto part = [&](int i) {
-        return reinterpret_cast<const float*>(p.ws + kPartOff) +
-               (2ll * ((long long)blockIdx.x - 1 + i) + (i == 0 ? 1 : 0)) * Part<W>::kFloats;
+    const float* parts = reinterpret_cast<const float*>(p.ws + kPartOff) + (2ll * blockIdx.x - 1) * Part<W>::kFloats;
+    auto part = [&](int i) { return parts + (i == 0 ? 0 : 2 * i - 1) * Part<W>::kFloats; };
+    const int at = 2 * kPartCols + col * W + 4 * (t % kLanes);
+    float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f), v[kBatch];
+    auto load = [&](int i0) {
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) {
+            const int i = i0 + k * kSplit;
+            v[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            if (i < cut.count) v[k] = *reinterpret_cast<const float4*>(part(i) + at);
+        }
     };
-    // the largest reference, then the sums under it
-    float m = kNone;
-    for (int i = threadIdx.x & 31; i < cut.count; i += 32) m = fmaxf(m, part(i)[col]);
+    load(split);
+    // the largest reference, then the sums under it (every warp of a column for itself: the same values)
+    float m = kNone, l = 0.0f;
+    for (int i = lane; i < cut.count; i += 32) m = fmaxf(m, part(i)[col]);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    float l = 0.0f;
-    for (int i = threadIdx.x & 31; i < cut.count; i += 32) l += part(i)[kPartCols + col] * exp2f(part(i)[col] - m);
+    for (int i = lane; i < cut.count; i += 32) {
+        const float w = exp2f(part(i)[col] - m);
+        weight[mine][i] = w;
+        l += part(i)[kPartCols + col] * w;
+    }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
-    const int lane = threadIdx.x % kLanes;
-    float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 4
-    for (int i = threadIdx.x / kLanes; i < cut.count; i += kSplit) {
-        const float* a = part(i);
-        const float f = exp2f(a[col] - m);
-        const float4 v = *reinterpret_cast<const float4*>(a + 2 * kPartCols + col * W + 4 * lane);
-        acc.x = fmaf(v.x, f, acc.x), acc.y = fmaf(v.y, f, acc.y);
-        acc.z = fmaf(v.z, f, acc.z), acc.w = fmaf(v.w, f, acc.w);
+    __syncwarp();
+    for (int i0 = split; i0 < cut.count; i0 += kBatch * kSplit) {
+        if (i0 >= kBatch * kSplit) load(i0);
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) {
+            const int i = i0 + k * kSplit;
+            const float f = i < cut.count ? weight[mine][i] : 0.0f;
+            acc.x = fmaf(v[k].x, f, acc.x), acc.y = fmaf(v[k].y, f, acc.y);
+            acc.z = fmaf(v[k].z, f, acc.z), acc.w = fmaf(v[k].w, f, acc.w);
+        }
     }
-    sum[threadIdx.x] = acc;
+    sum[t] = acc;
     __syncthreads();
-    if (threadIdx.x >= kLanes) return;
+    if (split > 0 || (int)blockIdx.y * kJoinCols + mine >= cut.cols) return;
+#pragma unroll
     for (int i = 1; i < kSplit; ++i) {
-        const float4 v = sum[threadIdx.x + i * kLanes];
-        acc.x += v.x, acc.y += v.y, acc.z += v.z, acc.w += v.w;
+        const float4 x = sum[t + i * kLanes];
+        acc.x += x.x, acc.y += x.y, acc.z += x.z, acc.w += x.w;
     }
-    const long long r = q.first + id / p.group;
-    const int hq = cut.head * p.group + (int)(id % p.group);
+    const int id = cut.col + col, d = 4 * (t % kLanes);
+    const long long r = cut.first + id / p.group;
+    const int hq = cut.head * p.group + id % p.group;
     const float f = norm(m, l, p.c.v_gscale ? p.c.v_gscale[cut.head] : 1.0f);
-    if (4 * lane < p.c.D)
-        *reinterpret_cast<uint2*>(p.out + r * p.out_row + (long long)hq * p.out_head + 4 * lane) =
+    if (d < p.c.D)
+        *reinterpret_cast<uint2*>(p.out + r * p.out_row + (long long)hq * p.out_head + d) =
             make_uint2(cvt_bf16x2(f2(acc.x * f, acc.y * f)), cvt_bf16x2(f2(acc.z * f, acc.w * f)));
-    if (p.lse && lane == 0) p.lse[r * p.Hq + hq] = log_sum(m, l);
+    if (p.lse && d == 0) p.lse[r * p.Hq + hq] = log_sum(m, l);
 }
 
 template <int W, int kCols>
 cudaError_t launch(const AttnParams& p, cudaStream_t s)
 {
     using C = Config<W, kCols>;
-    const cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void*>(cache_attn_kernel<W, kCols>), (int)C::kSmem);
+    const cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void*>(cache_attn_kernel<W, kCols>), (int)C::smem(kCacheMaxSeqs));
     if (e != cudaSuccess) return e;
     int ctas = sm_count_current_device() * C::kCtasPerSm;
     if (ctas > kMaxCtas) ctas = kMaxCtas;
@@ -798,16 +873,17 @@ cudaError_t launch(const AttnParams& p, cudaStream_t s)
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.gridDim = dim3((unsigned)ctas);
     cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = C::kSmem;
+    cfg.dynamicSmemBytes = C::smem(p.c.nseq);
     cfg.stream = s;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     const cudaError_t first = cudaLaunchKernelEx(&cfg, cache_attn_kernel<W, kCols>, p);
     if (first != cudaSuccess) return first;
-    cfg.gridDim = dim3((unsigned)ctas, kCols);
-    cfg.blockDim = dim3(128);
+    constexpr int kJoinCols = kJoinThreads / W;   // of a block
+    cfg.gridDim = dim3((unsigned)ctas, (kCols + kJoinCols - 1) / kJoinCols);
+    cfg.blockDim = dim3(kJoinThreads);
     cfg.dynamicSmemBytes = 0;
-    return cudaLaunchKernelEx(&cfg, cache_join_kernel<W, kCols>, p);
+    return cudaLaunchKernelEx(&cfg, cache_join_kernel<W>, p);
 }
 
 }  // namespace
