@@ -72,24 +72,37 @@ h3fp4_status check_shape(int64_t rows, int64_t K)
     return H3FP4_OK;
 }
 
-cudaError_t ensure_dynamic_smem(const void* func, int bytes)
+// Sets an attribute of `func` on the current device the first time it is asked for there.
+static cudaError_t ensure_attribute(const void* func, cudaFuncAttribute what, int value)
 {
     struct Entry {
         const void* func;
+        cudaFuncAttribute what;
         int dev;
     };
+    constexpr int kMost = 48 * kMaxDevices;
     static std::mutex mu;
-    static Entry done[16 * kMaxDevices];
+    static Entry done[kMost];
     static int ndone = 0;
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     std::lock_guard<std::mutex> lock(mu);
     for (int i = 0; i < ndone; ++i)
-        if (done[i].func == func && done[i].dev == dev) return cudaSuccess;
-    e = cudaFuncSetAttribute(func, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-    if (e == cudaSuccess && ndone < 16 * kMaxDevices) done[ndone++] = Entry{func, dev};
+        if (done[i].func == func && done[i].what == what && done[i].dev == dev) return cudaSuccess;
+    e = cudaFuncSetAttribute(func, what, value);
+    if (e == cudaSuccess && ndone < kMost) done[ndone++] = Entry{func, what, dev};
     return e;
+}
+
+cudaError_t ensure_dynamic_smem(const void* func, int bytes)
+{
+    return ensure_attribute(func, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+}
+
+cudaError_t ensure_shared_carveout(const void* func)
+{
+    return ensure_attribute(func, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
 }
 
 int sm_count_current_device()

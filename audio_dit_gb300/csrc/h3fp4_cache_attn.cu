@@ -19,7 +19,7 @@
 //
 // S = Q K^T: m16n8k16 with the columns as rows of A and the tokens as columns of B; what a lane
 // unpacks of a token is its B fragment.  O = P V: P stays where S was (the accumulator layout
-// is A's), V's fragment pairs two tokens, interleaved as nibbles before they are converted.
+// is A's, or a transposition away from B's), V's bytes hold two tokens as its fragment does.
 // Q is scaled per column by a power of two to f16's range (exact for elements within 2^31 of
 // the column's largest).  The reference of the exponent follows the true maximum only when
 // that passed it by 2^14: p lies in f16's upper range, and those below 2^-30 of the largest
@@ -46,10 +46,11 @@ constexpr float kRaise = 14.0f, kStart = 6.0f;  // in powers of two: see above
 // No key yet; and the lowest score that counts: where a column's largest is there, it left fp32's range.
 constexpr float kNone = -3.4e38f, kLowest = -3.0e38f;
 
-// What a CTA leaves for the joining kernel about the cut at its first tile.
+// What the joining kernel has to know about a unit that was cut, written by the CTA that began it.
 struct Cut {
-    long long first;              // packed row of the unit's sequence's first
-    int head, col, cols, count;   // kv head, the unit's first column and how many; of how many CTAs it takes partials (0: no first cut)
+    int first;                // packed row of the unit's sequence's first
+    int head, col, cols;      // kv head, the unit's first column and how many
+    int cta, count;           // the CTA that began the unit, and of how many CTAs it takes partials (0: not cut)
 };
 
 // Partial sums: per CTA one of a unit that began before it, one of a unit that goes on after it.
@@ -58,8 +59,9 @@ struct Part {
     static constexpr long long kFloats = kPartCols * (W + 2);
 };
 
+constexpr size_t kUnitsOff = 128;   // int: units of the last call
 constexpr size_t kCutOff = 256;
-constexpr size_t kPartOff = kCutOff + kMaxCtas * sizeof(Cut);
+constexpr size_t kPartOff = kCutOff + (kMaxCtas * sizeof(Cut) + 255) / 256 * 256;
 
 struct AttnParams {
     CacheView c;
@@ -69,6 +71,7 @@ struct AttnParams {
     float* lse;
     long long M;
     int Hq, group, causal, stall;
+    int by_unit;          // there are few units: a cut stands at its unit's number, else at its CTA's
     float scale_log2;
     uint8_t* ws;
     unsigned long long wait_ns;
@@ -119,7 +122,7 @@ struct Config {
     static constexpr int kMergeRegs = W * kCols / 32 + 4;              // a lane's state: O, two maxima, two sums
     static constexpr uint32_t kSlot = 2 * CacheLayout<W>::kGroupBytes;
     static constexpr uint32_t kRing = kWarps * kSlots * kSlot;
-    static constexpr uint32_t kMerge = 2 * kMergeRegs * 32 * 4;
+    static constexpr uint32_t kMerge = kWarps / 2 * kMergeRegs * 32 * 4;
     static constexpr uint32_t kBars = kWarps * kSlots * 8;
     static constexpr uint32_t kFixed = kRing + kMerge + kBars;
     static_assert(kFixed % 16 == 0, "the sequences' table behind it");
@@ -334,7 +337,6 @@ __device__ __forceinline__ void values(State<W, kCols>& st, const uint8_t* gp, i
     using L = CacheLayout<W>;
     const int g = lane >> 2, c = lane & 3;
     constexpr int kVBlocks = W == 256 ? 2 : 1;      // scale blocks of a lane
-    constexpr int kVWords = W == 64 ? 1 : W == 128 ? 2 : 4;  // words of a token
     uint32_t vs[2][kVBlocks];
 #pragma unroll
     for (int b = 0; b < kVBlocks; ++b) {
@@ -353,45 +355,37 @@ __device__ __forceinline__ void values(State<W, kCols>& st, const uint8_t* gp, i
                 vs[half][b] &= (t < left ? 0xFFFFu : 0u) | (t + 1 < left ? 0xFFFF0000u : 0u);
             }
     }
-    uint32_t w0[2][kVWords], w1[2][kVWords];
+    uint32_t w[2][4 * kVBlocks];
 #pragma unroll
     for (int half = 0; half < 2; ++half) {
-        if constexpr (W == 256) {
-            ld_words<4>(gp + L::kV + half * 1024 + lane * 16, w0[half]);
-            ld_words<4>(gp + L::kV + half * 1024 + 512 + lane * 16, w1[half]);
+        if constexpr (W == 64) {
+            uint32_t two[2];
+            ld_words<2>(gp + L::kV + half * 256 + lane * 8, two);
+            w[half][0] = two[0], w[half][1] = two[1];
         } else {
-            uint32_t w[2 * kVWords];
-            ld_words<2 * kVWords>(gp + L::kV + half * (32 * 8 * kVWords) + lane * (8 * kVWords), w);
 #pragma unroll
-            for (int i = 0; i < kVWords; ++i) {
-                w0[half][i] = w[i];
-                w1[half][i] = w[kVWords + i];
-            }
+            for (int b = 0; b < kVBlocks; ++b)
+                ld_words<4>(gp + L::kV + half * (8 * W / 2) + b * 512 + lane * 16, reinterpret_cast<uint32_t(&)[4]>(w[half][4 * b]));
         }
     }
 #pragma unroll
-    for (int i = 0; i < kVWords; ++i) {
-        uint32_t even[2][4], odd[2][4];   // elements 8 i + 2 j and the next one
-        const int blk = W == 256 ? i >> 1 : 0;
+    for (int i = 0; i < W / 32; ++i) {
+        uint32_t f[2][4];   // elements 4 i .. 4 i + 3
+        const int blk = i >> 2;
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
-            const uint32_t a = w0[half][i], b = w1[half][i];
-            e2m1x8_f16((a & 0x0F0F0F0Fu) | ((b << 4) & 0xF0F0F0F0u), even[half]);
-            e2m1x8_f16(((a >> 4) & 0x0F0F0F0Fu) | (b & 0xF0F0F0F0u), odd[half]);
+            e2m1x8_f16(w[half][i], f[half]);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                even[half][j] = mul_f16x2(even[half][j], vs[half][blk]);
-                odd[half][j] = mul_f16x2(odd[half][j], vs[half][blk]);
-            }
+            for (int j = 0; j < 4; ++j) f[half][j] = mul_f16x2(f[half][j], vs[half][blk]);
         }
+        if constexpr (kCols == 16) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            if constexpr (kCols == 16) {
-                mma_f16(st.o[8 * i + 2 * j], pf, even[0][j], even[1][j]);
-                mma_f16(st.o[8 * i + 2 * j + 1], pf, odd[0][j], odd[1][j]);
-            } else {
-                const uint32_t a[4] = {even[0][j], odd[0][j], even[1][j], odd[1][j]};
-                mma_f16(st.o[4 * i + j], a, pf[0], pf[1]);
+            for (int j = 0; j < 4; ++j) mma_f16(st.o[4 * i + j], pf, f[0][j], f[1][j]);
+        } else {
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const uint32_t a[4] = {f[0][2 * j], f[0][2 * j + 1], f[1][2 * j], f[1][2 * j + 1]};
+                mma_f16(st.o[2 * i + j], a, pf[0], pf[1]);
             }
         }
     }
@@ -422,8 +416,14 @@ __device__ __forceinline__ void step(State<W, kCols>& st, const uint8_t* gp, int
                     const int token = kCols == 16 ? 8 * h + 2 * c + (i & 1) : g + 8 * (i >> 1);
                     v = token < lim[e][col] ? max_nan(v, kLowest) : -INFINITY;
                 }
-                top[col] = fmaxf(top[col], v);
             }
+#pragma unroll
+    for (int e = 0; e < 2; ++e)
+#pragma unroll
+        for (int h = 0; h < kF; ++h)
+#pragma unroll
+            for (int col = 0; col < 2; ++col)
+                top[col] = max3(top[col], s[e][h][kCols == 16 ? 2 * col : col], s[e][h][kCols == 16 ? 2 * col + 1 : 2 + col]);
     if (__any_sync(0xffffffffu, top[0] > st.m[0] + kRaise || top[1] > st.m[1] + kRaise)) {
 #pragma unroll
         for (int col = 0; col < 2; ++col) {
@@ -531,8 +531,17 @@ __global__ void __launch_bounds__(kThreads, Config<W, kCols>::kCtasPerSm)
             if (p.lse && v == 0) p.lse[r * p.Hq + h] = -INFINITY;
         }
     }
-    Cut* cut = reinterpret_cast<Cut*>(p.ws + kCutOff) + blockIdx.x;
-    if (threadIdx.x == 0) *cut = Cut{0, 0, 0, 0, 0};
+    // Cuts.  By unit: units in the order of their sequences, empty ones have no number.
+    Cut* cuts = reinterpret_cast<Cut*>(p.ws + kCutOff);
+    auto units_before = [&](int s) {
+        long long n = 0;
+        for (int i = 0; i < s; ++i) n += seqs[i].len > 0 ? (long long)p.c.Hkv * col_tiles<kCols>(p, seqs[i]) : 0;
+        return n;
+    };
+    if (threadIdx.x == 0) {
+        if (!p.by_unit) cuts[blockIdx.x].count = 0;
+        else if (blockIdx.x == 0) *reinterpret_cast<int*>(p.ws + kUnitsOff) = (int)min((long long)kMaxCtas, units_before(nseq));
+    }
 
     // ------------------------------------------------------------ units
     uint32_t phases = 0;    // of the ring's barriers, one bit each
@@ -705,11 +714,11 @@ __global__ void __launch_bounds__(kThreads, Config<W, kCols>::kCtasPerSm)
         }
         __syncwarp();
 
-        // ------------------------------------------------------------ the four warps' sums into warp 0
+        // ------------------------------------------------------------ the warps' sums into warp 0
 #pragma unroll
         for (int i = 0; i < 2; ++i) st.l[i] = over_lanes<kCols>(st.l[i], [](float a, float b) { return a + b; });
 #pragma unroll
-        for (int with = 2; with >= 1; with >>= 1) {
+        for (int with = kWarps / 2; with >= 1; with >>= 1) {
             float* other = merge + (warp & (with - 1)) * (C::kMergeRegs * 32) + lane;
             __syncthreads();
             if (warp >= with && warp < 2 * with) {
@@ -770,42 +779,46 @@ __global__ void __launch_bounds__(kThreads, Config<W, kCols>::kCtasPerSm)
                 }
                 if (kCols == 16 ? c == 0 : g == 0) {
                     if (!whole) {
-                        part[col] = st.m[i];
-                        part[kPartCols + col] = st.l[i];
+                        part[2 * col] = st.m[i];
+                        part[2 * col + 1] = st.l[i];
                     } else if (p.lse && col < cols) {
                         p.lse[r * p.Hq + hq] = log_sum(st.m[i], st.l[i]);
                     }
                 }
             }
-            // the first cut of a unit stands with the CTA behind it
-            const long long before = div(ubegin, chunk);
-            if (!whole && lane == 0 && at != ubegin && before + 1 == blockIdx.x)
-                *cut = Cut{q.first, h, ct * kCols, cols, (int)(div(uend - 1, chunk) - before + 1)};
+            if (lane == 0 && at == ubegin && (p.by_unit || !whole)) {
+                const int count = whole ? 0 : (int)(div(uend - 1, chunk) - blockIdx.x + 1);
+                const long long i = p.by_unit ? units_before(s) + unit : blockIdx.x;
+                // (row offsets that overlap make more units than there can be)
+                if (i < kMaxCtas) cuts[i] = Cut{q.first, h, ct * kCols, cols, (int)blockIdx.x, count};
+            }
         }
         at = ubegin + t1;
     }
 }
 
-// Columns of a unit that was cut: block (cut, columns).  A warp works for one column by itself until the
-// last step, so that only latency counts: the cut, then references, sums and O of the partials together.
+// Columns of a unit that was cut: block (cut, columns).  Latency counts: the
+// cut, then references, sums and O of the partials together.
 constexpr int kJoinThreads = 512;
 
-template <int W>
+template <int W, int kSplit>
 __global__ void __launch_bounds__(kJoinThreads) cache_join_kernel(const __grid_constant__ AttnParams p)
 {
-    constexpr int kLanes = W / 4;                  // threads of a partial, four elements each
-    constexpr int kSplit = 4;                      // partials at a time
+    constexpr int kLanes = W / 4;                  // threads of a partial, four elements each; kSplit partials at a time
     constexpr int kJoinCols = kJoinThreads / (kLanes * kSplit);
     constexpr int kBatch = 4;                      // and of a thread in flight
     __shared__ float weight[kJoinCols][kMaxCtas];
     __shared__ float4 sum[kJoinThreads];
+    __shared__ float red[2][kJoinThreads / 32];
     griddep_wait();
+    griddep_launch_dependents();
+    if (p.by_unit && (int)blockIdx.x >= *reinterpret_cast<const int*>(p.ws + kUnitsOff)) return;
     const Cut cut = reinterpret_cast<const Cut*>(p.ws + kCutOff)[blockIdx.x];
-    if ((int)blockIdx.y * kJoinCols >= cut.cols || cut.count == 0) return;
+    if (cut.count == 0 || (int)blockIdx.y * kJoinCols >= cut.cols) return;
     const int t = threadIdx.x, lane = t & 31, mine = t / (kLanes * kSplit), split = t / kLanes % kSplit;
     const int col = min((int)blockIdx.y * kJoinCols + mine, kPartCols - 1);   // (columns past the last are not written)
-    // partial 0 is the CTA's before this one (its second), the others are the first ones
-    const float* parts = reinterpret_cast<const float*>(p.ws + kPartOff) + (2ll * blockIdx.x - 1) * Part<W>::kFloats;
+    // partial 0 is its CTA's second, the others are the first ones
+    const float* parts = reinterpret_cast<const float*>(p.ws + kPartOff) + (2ll * cut.cta + 1) * Part<W>::kFloats;
     auto part = [&](int i) { return parts + (i == 0 ? 0 : 2 * i - 1) * Part<W>::kFloats; };
     const int at = 2 * kPartCols + col * W + 4 * (t % kLanes);
     float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f), v[kBatch];
@@ -818,19 +831,40 @@ __global__ void __launch_bounds__(kJoinThreads) cache_join_kernel(const __grid_c
         }
     };
     load(split);
-    // the largest reference, then the sums under it (every warp of a column for itself: the same values)
+    // references and sums: a partial per thread of the column, all in flight at once
+    constexpr int kThreadsOfCol = kLanes * kSplit, kWarpsOfCol = kThreadsOfCol / 32;
+    constexpr int kMine = (kMaxCtas + kThreadsOfCol - 1) / kThreadsOfCol;
+    float2 ml[kMine];
     float m = kNone, l = 0.0f;
-    for (int i = lane; i < cut.count; i += 32) m = fmaxf(m, part(i)[col]);
+#pragma unroll
+    for (int k = 0; k < kMine; ++k) {
+        const int i = t % kThreadsOfCol + k * kThreadsOfCol;
+        ml[k] = make_float2(kNone, 0.0f);
+        if (i < cut.count) ml[k] = *reinterpret_cast<const float2*>(part(i) + 2 * col);
+    }
+#pragma unroll
+    for (int k = 0; k < kMine; ++k) m = fmaxf(m, ml[k].x);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    for (int i = lane; i < cut.count; i += 32) {
-        const float w = exp2f(part(i)[col] - m);
-        weight[mine][i] = w;
-        l += part(i)[kPartCols + col] * w;
+    const int warp0 = mine * kWarpsOfCol;
+    if (lane == 0) red[0][t >> 5] = m;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kWarpsOfCol; ++w) m = fmaxf(m, red[0][warp0 + w]);
+#pragma unroll
+    for (int k = 0; k < kMine; ++k) {
+        const int i = t % kThreadsOfCol + k * kThreadsOfCol;
+        const float w = exp2f(ml[k].x - m);
+        if (i < cut.count) weight[mine][i] = w;
+        l += ml[k].y * w;
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
-    __syncwarp();
+    if (lane == 0) red[1][t >> 5] = l;
+    __syncthreads();
+    l = 0.0f;
+#pragma unroll
+    for (int w = 0; w < kWarpsOfCol; ++w) l += red[1][warp0 + w];
     for (int i0 = split; i0 < cut.count; i0 += kBatch * kSplit) {
         if (i0 >= kBatch * kSplit) load(i0);
 #pragma unroll
@@ -850,7 +884,7 @@ __global__ void __launch_bounds__(kJoinThreads) cache_join_kernel(const __grid_c
         acc.x += x.x, acc.y += x.y, acc.z += x.z, acc.w += x.w;
     }
     const int id = cut.col + col, d = 4 * (t % kLanes);
-    const long long r = cut.first + id / p.group;
+    const long long r = (long long)cut.first + id / p.group;
     const int hq = cut.head * p.group + id % p.group;
     const float f = norm(m, l, p.c.v_gscale ? p.c.v_gscale[cut.head] : 1.0f);
     if (d < p.c.D)
@@ -860,8 +894,11 @@ __global__ void __launch_bounds__(kJoinThreads) cache_join_kernel(const __grid_c
 }
 
 template <int W, int kCols>
-cudaError_t launch(const AttnParams& p, cudaStream_t s)
+cudaError_t launch(AttnParams p, cudaStream_t s)
 {
+    // at most: a sequence's columns fill all but one of its units
+    const long long units = p.c.Hkv * (p.c.nseq + p.M * p.group / kCols);
+    p.by_unit = units <= kMaxCtas;
     using C = Config<W, kCols>;
     const cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void*>(cache_attn_kernel<W, kCols>), (int)C::smem(kCacheMaxSeqs));
     if (e != cudaSuccess) return e;
@@ -879,11 +916,23 @@ cudaError_t launch(const AttnParams& p, cudaStream_t s)
     cfg.numAttrs = 1;
     const cudaError_t first = cudaLaunchKernelEx(&cfg, cache_attn_kernel<W, kCols>, p);
     if (first != cudaSuccess) return first;
-    constexpr int kJoinCols = kJoinThreads / W;   // of a block
-    cfg.gridDim = dim3((unsigned)ctas, (kCols + kJoinCols - 1) / kJoinCols);
+    // Few units, so that each was cut into many: their partials by many threads, a block per unit and column
+    // (8 units of 76 partials: 3.5 us of the call against 7 with four partials at a time).
+    constexpr int kMany = W == 64 ? 32 : W == 128 ? 16 : 8;
+    constexpr int few_cols = kJoinThreads / (W / 4 * kMany), cols = kJoinThreads / W;
+    static_assert(few_cols >= 1, "a column at least");
     cfg.blockDim = dim3(kJoinThreads);
     cfg.dynamicSmemBytes = 0;
-    return cudaLaunchKernelEx(&cfg, cache_join_kernel<W>, p);
+    auto join = [&](const cudaLaunchConfig_t& cfg, void (*kernel)(AttnParams)) {
+        const cudaError_t e = ensure_shared_carveout(reinterpret_cast<const void*>(kernel));
+        return e == cudaSuccess ? cudaLaunchKernelEx(&cfg, kernel, p) : e;
+    };
+    if (p.by_unit && 16 * units <= ctas) {
+        cfg.gridDim = dim3((unsigned)units, (kCols + few_cols - 1) / few_cols);
+        return join(cfg, cache_join_kernel<W, kMany>);
+    }
+    cfg.gridDim = dim3((unsigned)(p.by_unit ? units : ctas), (kCols + cols - 1) / cols);
+    return join(cfg, cache_join_kernel<W, 4>);
 }
 
 }  // namespace

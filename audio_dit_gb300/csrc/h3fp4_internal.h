@@ -121,6 +121,10 @@ h3fp4_status check_shape(int64_t rows, int64_t K);
 // attribute belongs to each device's context.
 cudaError_t ensure_dynamic_smem(const void* func, int bytes);
 
+// The same for a small kernel that runs next to one with much shared memory: it asks for the same
+// division of L1, so that an SM need not drain and change it between the two.
+cudaError_t ensure_shared_carveout(const void* func);
+
 // Synchronous: FP4 MMA loop on every SM, returns TFLOP/s (status word for its bounded wait).
 cudaError_t measure_fp4_peak(int iters, unsigned int* status, float* tflops);
 

@@ -532,7 +532,10 @@ cudaError_t launch_linear_rows(const LinearRowsJob& job, cudaStream_t s)
     cfg.gridDim = dim3((unsigned)((job.K + kDigitColumns - 1) / kDigitColumns), (unsigned)job.M);
     cfg.blockDim = dim3(kDigitThreads);
     float* factors = reinterpret_cast<float*>(job.ws + kFactors);
-    cudaError_t e = cudaLaunchKernelEx(&cfg, digits_kernel, job.x, (int)job.K, l.pass_rows, (int)l.kb4,
+    cudaError_t e = ensure_shared_carveout(reinterpret_cast<const void*>(digits_kernel));
+    if (e == cudaSuccess) e = ensure_shared_carveout(reinterpret_cast<const void*>(rows_join_kernel));
+    if (e != cudaSuccess) return e;
+    e = cudaLaunchKernelEx(&cfg, digits_kernel, job.x, (int)job.K, l.pass_rows, (int)l.kb4,
                                        job.ws + l.codes, job.ws + l.scales, factors);
     if (e != cudaSuccess) return e;
 

@@ -11,10 +11,9 @@
 //   K: token t = 8 half + g, elements in chunks of 16 bytes (8 where W is 64), chunk c
 //      of 128 (64) elements: the lane's elements of one token are its k indices.
 //      Scales: the lane's of both halves side by side.
-//   V: tokens 8 half + 2 c + e (e = 0, 1) are a k pair of the lane, elements
-//      g W/8 .. are its n indices: W/16 bytes per token, both tokens side by side
-//      (W = 256: one after the other in two lines).
-//      Scales: [block][c][half][e].
+//   V: tokens 8 half + 2 c + e (e = 0, 1) are a k pair of the lane, elements g W/8 .. are its
+//      n indices: a byte per element, token e = 0 in its low four bits, in lines of 16 bytes
+//      (8 where W is 64) a lane.  Scales: [block][c][half][e].
 #pragma once
 #include <cstdint>
 
@@ -40,13 +39,14 @@ struct CacheLayout {
         if (W == 128) return kKScale + ((g * 4 + (b >> 1)) * 2 + half) * 2 + (b & 1);
         return kKScale + ((g * 4 + ((b & 7) >> 1)) * 2 + half) * 4 + (b >> 3) * 2 + (b & 1);
     }
-    // V: eight bytes at one place, or (W = 64) four at each of two, the second at + 32.
+    // V: 16 bytes of elements [16 b, 16 b + 16), shared by two tokens (W = 64: eight at each of two
+    // places, the second at + 32); token t's are their low or, for odd t, high four bits.
     static __device__ __forceinline__ int v_codes(int t, int b)
     {
-        const int half = t >> 3, c = (t & 7) >> 1, e = t & 1;
-        if (W == 64) return kV + half * 256 + (8 * b + c) * 8 + e * 4;
-        if (W == 128) return kV + half * 512 + (4 * b + c) * 16 + e * 8;
-        return kV + half * 1024 + e * 512 + (4 * (b >> 1) + c) * 16 + (b & 1) * 8;
+        const int half = t >> 3, c = (t & 7) >> 1;
+        if (W == 64) return kV + half * 256 + (8 * b + c) * 8;
+        if (W == 128) return kV + half * 512 + (4 * b + c) * 16;
+        return kV + half * 1024 + (b & 1) * 512 + (4 * (b >> 1) + c) * 16;
     }
     static __device__ __forceinline__ int v_scale(int t, int b)
     {

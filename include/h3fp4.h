@@ -535,7 +535,8 @@ H3FP4_API size_t h3fp4_cache_page_bytes(int heads, int dim, int page);
  * places in the cache, quantised as h3fp4_quantize_act does with H3FP4_GSCALE_GIVEN
  * and the head's global scale ("H3 Runtime Current State", "Owned Performance
  * Kernels": tensor scale/QDATA; the pages have no cache).  Inputs must be finite.
- * The places of a call's rows must differ.  0 <= M <= 2^31 - 256. */
+ * The places of a call's rows must differ, and sequences of one call must not write to
+ * the same page.  0 <= M <= 2^31 - 256. */
 H3FP4_API h3fp4_status h3fp4_cache_append(const h3fp4_heads* k, const h3fp4_heads* v, int64_t M,
                                           const h3fp4_cache* cache, cudaStream_t stream);
 
