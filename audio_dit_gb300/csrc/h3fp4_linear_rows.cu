@@ -237,53 +237,64 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
     griddep_launch_dependents();
+    // this CTA's stages: `todo` from stage kb0 of unit u0 on (counted on by every role, as divisions take
+    // a lone warp longer than a stage does)
     const long long begin = p.chunk * blockIdx.x;
-    const long long end = min(p.units * p.ks, begin + p.chunk);
+    const int todo = (int)(min(p.units * p.ks, begin + p.chunk) - begin);
+    const int u0 = (int)(begin / p.ks), kb0 = (int)(begin - (long long)u0 * p.ks);
 
     if (warp == 0) {
         // ------------------------------------------------------------ producer
         const uint32_t d_bytes = (uint32_t)p.nb * (BK / 2);
         const uint32_t d_halves = (uint32_t)(p.nb + 127) / 128;
-        auto load_w = [&](long long i, int stage) {
-            const long long u = i / p.ks;
-            const int kb = (int)(i % p.ks), tile = (int)(u / p.passes);
+        struct At {   // a stage's place
+            int kb, pass, tile;
+        };
+        auto next = [&](At& a) {
+            if (++a.kb < p.ks) return;
+            a.kb = 0;
+            if (++a.pass < p.passes) return;
+            a.pass = 0;
+            ++a.tile;
+        };
+        auto load_w = [&](const At& a, int stage) {
             uint8_t* st = smem + stage * P::kStage;
             mbar_arrive_expect_tx(&sf_full[stage], kSfwBytes + d_halves * kSfBox);
-            tma_load_2d(st + kWBytes + P::kDBytes, &tmSfw, &sf_full[stage], 0, (tile * p.kb4 + kb * 4) * 2);
+            tma_load_2d(st + kWBytes + P::kDBytes, &tmSfw, &sf_full[stage], 0, (a.tile * p.kb4 + a.kb * 4) * 2);
             mbar_arrive_expect_tx(&full[stage], kWBytes + d_bytes);
-            tma_load_2d(st, &tmW, &full[stage], kb * (BK / 2), tile * BM);
+            tma_load_2d(st, &tmW, &full[stage], a.kb * (BK / 2), a.tile * BM);
         };
-        auto load_d = [&](long long i, int stage) {
-            const int kb = (int)(i % p.ks), pass = (int)(i / p.ks % p.passes);
+        auto load_d = [&](const At& a, int stage) {
             uint8_t* st = smem + stage * P::kStage;
             for (uint32_t h = 0; h < d_halves; ++h)
                 tma_load_2d(st + kWBytes + P::kDBytes + kSfwBytes + h * kSfBox, &tmSfd, &sf_full[stage], 0,
-                            ((2 * pass + (int)h) * p.kb4 + kb * 4) * 2);
-            tma_load_2d(st + kWBytes, &tmD, &full[stage], kb * (BK / 2), 256 * pass);
+                            ((2 * a.pass + (int)h) * p.kb4 + a.kb * 4) * 2);
+            tma_load_2d(st + kWBytes, &tmD, &full[stage], a.kb * (BK / 2), 256 * a.pass);
         };
-        const int ahead = (int)min((long long)kStages, end - begin);
+        const int ahead = min(kStages, todo);
         uint32_t fills[kStages] = {};
         if (!p.stall) {
-            if (elect_one())
-                for (int i = 0; i < ahead; ++i) load_w(begin + i, i);
+            At w{kb0, u0 % p.passes, u0 / p.passes}, d = w;
+            for (int i = 0; i < ahead; ++i, next(w))
+                if (elect_one()) load_w(w, i);
             __syncwarp();
             griddep_wait();
-            if (elect_one())
-                for (int i = 0; i < ahead; ++i) load_d(begin + i, i);
+            for (int i = 0; i < ahead; ++i, next(d))
+                if (elect_one()) load_d(d, i);
             __syncwarp();
 #pragma unroll
             for (int i = 0; i < kStages; ++i) fills[i] = i < ahead ? 1 : 0;
             int stage = 0;
             uint32_t phase = 0;
-            for (long long i = begin + ahead; i < end; ++i) {
+            for (int i = ahead; i < todo; ++i, next(w)) {
                 const bool ok = mbar_wait(&empty[stage], phase, p.wait_ns, p.status, kStatusTimeoutProducer);
                 if (!__all_sync(0xffffffffu, ok && s_abort == 0)) {
                     s_abort = 1;
                     break;
                 }
                 if (elect_one()) {
-                    load_w(i, stage);
-                    load_d(i, stage);
+                    load_w(w, stage);
+                    load_d(w, stage);
                 }
                 __syncwarp();
                 ++fills[stage];
@@ -306,18 +317,19 @@ __global__ void __launch_bounds__(kThreads, 1)
         int stage = 0, acc = 0;
         uint32_t phase = 0, acc_phase = 0;
         bool ok = true;
-        for (long long i = begin; i < end && ok;) {
-            const long long last = min(end, (i / p.ks + 1) * p.ks);
+        for (int left = todo, kb = kb0; left > 0 && ok; kb = 0) {
+            const int n = min(left, p.ks - kb);   // stages of this unit
+            left -= n;
             ok = mbar_wait(&acc_empty[acc], acc_phase ^ 1u, p.wait_ns, p.status, kStatusTimeoutMma);
             ok = __all_sync(0xffffffffu, ok && s_abort == 0);
             tc_fence_after();
             const uint32_t d = tmem + (uint32_t)(acc * NB);
-            for (bool first = true; i < last && ok; ++i, first = false) {
+            for (int i = 0; i < n; ++i) {
                 ok = mbar_wait(&full[stage], phase, p.wait_ns, p.status, kStatusTimeoutMma);
                 ok = __all_sync(0xffffffffu, ok && s_abort == 0);
                 if (!ok) break;
                 tc_fence_after();
-                const int nk = min(4, p.kb4 - (int)(i % p.ks) * 4);
+                const int nk = min(4, p.kb4 - (kb + i) * 4);
                 const uint32_t st = smem_u32(smem) + (uint32_t)stage * P::kStage;
                 const uint64_t a = smem_desc(st, 16, 1024, 2), b = smem_desc(st + kWBytes, 16, 1024, 2);
                 const uint32_t sfa = tmem + P::kSfTmem + (uint32_t)stage * P::kSfCols, sfb = sfa + 16;
@@ -326,7 +338,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int j = 0; j < 4; ++j)
                         if (j < nk)
                             mma_mxf4nvf4(d, a + 2u * j, b + 2u * j, idesc, sfa + 4u * j, sfb + 4u * P::kHalves * j,
-                                         !first || j > 0 ? 1u : 0u);
+                                         i > 0 || j > 0 ? 1u : 0u);
                     tc_commit(&empty[stage]);
                 }
                 __syncwarp();
@@ -352,7 +364,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t quarter = (uint32_t)(warp & 3);
         int stage = 0;
         uint32_t phase = 0;
-        for (long long i = begin; i < end; ++i) {
+        for (int i = 0; i < todo; ++i) {
             const bool ok = mbar_wait(&sf_full[stage], phase, p.wait_ns, p.status, kStatusTimeoutMma);
             if (!__all_sync(0xffffffffu, ok && s_abort == 0)) {
                 s_abort = 1;
@@ -393,17 +405,18 @@ __global__ void __launch_bounds__(kThreads, 1)
         int acc = 0;
         uint32_t acc_phase = 0;
         griddep_wait();   // an earlier call's joining kernel may read the pieces
-        for (long long i = begin; i < end;) {
-            const long long u = i / p.ks;
+        int pass = u0 % p.passes;
+        long long piece = (long long)u0 + blockIdx.x;
+        for (int left = todo, kb = kb0; left > 0; kb = 0) {
+            left -= min(left, p.ks - kb);
             const bool ok = mbar_wait(&acc_full[acc], acc_phase, p.wait_ns, p.status, kStatusTimeoutEpilogue);
             if (!__all_sync(0xffffffffu, ok && s_abort == 0)) {
                 s_abort = 1;
                 break;
             }
             tc_fence_after();
-            const int pass = (int)(u % p.passes);
             const int rows = min(p.pass_rows, p.M - pass * p.pass_rows);
-            float* part = p.parts + (u + blockIdx.x) * (long long)p.pass_rows * BM + n;
+            float* part = p.parts + piece * p.pass_rows * BM + n;
             const uint32_t d = tmem + ((32u * (uint32_t)quarter) << 16) + (uint32_t)(acc * NB);
             for (int m = 0; m < rows; m += 2) {
                 uint32_t v[16];
@@ -426,7 +439,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 acc = 0;
                 acc_phase ^= 1u;
             }
-            i = min(end, (u + 1) * p.ks);
+            ++piece;
+            if (++pass == p.passes) pass = 0;
         }
     }
     tc_fence_before();
