@@ -71,7 +71,7 @@ template <int kRow>
 __device__ __forceinline__ float row_sum(float v, float (&part)[2][32], uint32_t& turn)
 {
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    for (int o = (kRow < 32 ? kRow : 32) / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
     if constexpr (kRow > 32) {
         constexpr int kWarps = kRow / 32;
         const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -85,10 +85,11 @@ __device__ __forceinline__ float row_sum(float v, float (&part)[2][32], uint32_t
     return v;
 }
 
-// kRow threads per row (32: four rows to a block of 128 threads, which never wait
-// for one another; else one row to a block), kVec vectors of eight elements each.
+// kRow threads per row (up to 32: several rows to a block of 128 threads, warps that never wait for one
+// another; else one row to a block), kVec vectors of eight elements each.
 template <int kRow, int kVec>
-__global__ void __launch_bounds__(kRow < 128 ? 128 : kRow) block_norm_kernel(const __grid_constant__ BlockNormParams p)
+__global__ void __launch_bounds__(kRow < 128 ? 128 : kRow, kRow == 32 && kVec == 4 ? 5 : kRow <= 128 ? 8 : kRow == 256 ? 4 : 1)
+    block_norm_kernel(const __grid_constant__ BlockNormParams p)
 {
     constexpr int kRows = kRow < 128 ? 128 / kRow : 1;  // rows of a block
     __shared__ float part[2][32];
@@ -96,8 +97,10 @@ __global__ void __launch_bounds__(kRow < 128 ? 128 : kRow) block_norm_kernel(con
     const int nv = p.K >> 3;
     uint32_t turn = 0, top = 0;
     griddep_wait();
-    for (long long r = (long long)blockIdx.x * kRows + threadIdx.x / kRow; r < p.M; r += (long long)gridDim.x * kRows) {
-        const long long row = r * p.K;
+    for (long long r0 = (long long)blockIdx.x * kRows; r0 < p.M; r0 += (long long)gridDim.x * kRows) {
+        // (threads past the last row go over it again and write nothing)
+        const bool mine = r0 + threadIdx.x / kRow < p.M;
+        const long long r = mine ? r0 + threadIdx.x / kRow : p.M - 1, row = r * p.K;
         uint4 vx[kVec], vy[kVec];
 #pragma unroll
         for (int i = 0; i < kVec; ++i) {
@@ -145,7 +148,7 @@ __global__ void __launch_bounds__(kRow < 128 ? 128 : kRow) block_norm_kernel(con
                 }
 #pragma unroll
                 for (int j = 0; j < 8; ++j) f[i][j] = fmaf(p.x_scale, f[i][j], y[j]);
-                if (p.x_out) *reinterpret_cast<uint4*>(p.x_out + row + 8 * v) = pack_bf8(f[i]);
+                if (p.x_out && mine) *reinterpret_cast<uint4*>(p.x_out + row + 8 * v) = pack_bf8(f[i]);
             }
         }
         if (!p.out) continue;
@@ -192,7 +195,7 @@ __global__ void __launch_bounds__(kRow < 128 ? 128 : kRow) block_norm_kernel(con
                 for (int j = 0; j < 8; ++j) f[i][j] += w[j];
             }
             const uint4 o = pack_bf8(f[i]);
-            *reinterpret_cast<uint4*>(p.out + row + 8 * v) = o;
+            if (mine) *reinterpret_cast<uint4*>(p.out + row + 8 * v) = o;
             if (p.amax) {
                 // magnitudes of bf16 values in the order of their bits (a NaN is above all)
                 const uint32_t words[4] = {o.x, o.y, o.z, o.w};
@@ -207,6 +210,194 @@ __global__ void __launch_bounds__(kRow < 128 ? 128 : kRow) block_norm_kernel(con
         // the largest of all, in whatever order they come
         if ((threadIdx.x & 31) == 0 && top != 0) atomicMax(p.amax, top);
     }
+}
+
+// The same for many rows: a block keeps its columns' vectors in registers, folded into three
+// (y_weight gate, weight (1 + scale), shift), and takes rows one after the other.  Its threads copy their
+// columns of the next rows to shared memory ahead of time (each for itself, nothing waits for others), so
+// that enough bytes are on their way whatever the sums wait for.
+constexpr int kRing = 4;   // rows ahead
+
+
+__device__ __forceinline__ void copy16(void* dst, const void* src)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
+
+template <int kVec, int kThreads, int kBlocks>
+__global__ void __launch_bounds__(kThreads, kBlocks)
+    block_norm_ring_kernel(const __grid_constant__ BlockNormParams p)
+{
+    extern __shared__ __align__(128) uint8_t smem[];
+    __shared__ float part[2][32];
+    const int t = threadIdx.x, threads = blockDim.x, warp = t >> 5, lane = t & 31, warps = threads >> 5;
+    const int nv = p.K >> 3;
+    uint4* ring = reinterpret_cast<uint4*>(smem) + t;   // [row][x, y][vector of the thread][thread]
+    constexpr int kY = kVec, kSlot = 2 * kVec;
+    griddep_wait();
+    auto load = [&](long long r, int slot) {
+#pragma unroll
+        for (int i = 0; i < kVec; ++i) {
+            const int v = t + i * threads;
+            if (r < p.M && v < nv) {
+                copy16(ring + (slot * kSlot + i) * threads, p.x + r * p.K + 8 * v);
+                if (p.y) copy16(ring + (slot * kSlot + kY + i) * threads, p.y + r * p.K + 8 * v);
+            }
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");   // (also where there is nothing: groups are counted)
+    };
+#pragma unroll
+    for (int i = 0; i < kRing; ++i) load(blockIdx.x + (long long)i * gridDim.x, i);
+    uint32_t turn = 0, top = 0;
+    // a sum over the block: consecutive ones use different halves of `part`, so one barrier each is enough
+    auto block_sum = [&](float v) {
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+        if (lane == 0) part[turn][warp] = v;
+        __syncthreads();
+        v = lane < warps ? part[turn][lane] : 0.0f;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+        turn ^= 1u;
+        return v;
+    };
+    // the vectors of the thread's i-th columns: what y, the normed r are multiplied with, what is added
+    auto y_vector = [&](long long at, int v, float (&a)[8]) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) a[j] = 1.0f;
+        if (p.gate) load_f8(p.gate + at + 8 * v, a);
+        if (p.y_weight) {
+            float w[8];
+            load_f8(p.y_weight + at + 8 * v, w);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) a[j] *= w[j];
+        }
+    };
+    auto out_vectors = [&](long long at, int v, float (&b)[8], float (&c)[8]) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) b[j] = 1.0f, c[j] = 0.0f;
+        if (p.weight) load_f8(p.weight + at + 8 * v, b);
+        if (p.scale) {
+            float w[8];
+            load_f8(p.scale + at + 8 * v, w);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) b[j] *= 1.0f + w[j];
+        }
+        if (p.shift) load_f8(p.shift + at + 8 * v, c);
+    };
+    float va[kVec][8], vb[kVec][8], vc[kVec][8];
+    long long seg_end = 0;
+    int slot = 0;
+    for (long long r = blockIdx.x; r < p.M; r += gridDim.x) {
+        if (r >= seg_end) {
+            const int sg = segment_of(p.seg, r);
+            seg_end = p.seg.off[sg + 1];
+            const long long at = (long long)sg * p.K;
+#pragma unroll
+            for (int i = 0; i < kVec; ++i) {
+                const int v = min(t + i * threads, nv - 1);
+                y_vector(at, v, va[i]);
+                out_vectors(at, v, vb[i], vc[i]);
+            }
+        }
+        asm volatile("cp.async.wait_group %0;" ::"n"(kRing - 1) : "memory");
+        float f[kVec][8], y[kVec][8];
+#pragma unroll
+        for (int i = 0; i < kVec; ++i) {
+            const uint4 zero = make_uint4(0, 0, 0, 0);
+            const bool real = t + i * threads < nv;
+            unpack_bf8(real ? ring[(slot * kSlot + i) * threads] : zero, f[i]);
+            if (p.y) unpack_bf8(real ? ring[(slot * kSlot + kY + i) * threads] : zero, y[i]);
+        }
+        const long long row = r * p.K;
+        if (p.y) {
+            float rs = 1.0f;
+            if (p.post) {
+                float sum = 0.0f;
+#pragma unroll
+                for (int i = 0; i < kVec; ++i)
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) sum = fmaf(y[i][j], y[i][j], sum);
+                rs = rsqrtf(fmaf(block_sum(sum), p.inv_k, p.eps));
+            }
+#pragma unroll
+            for (int i = 0; i < kVec; ++i) {
+                const int v = t + i * threads;
+#pragma unroll
+                for (int j = 0; j < 8; ++j) f[i][j] = fmaf(p.x_scale, f[i][j], y[i][j] * rs * va[i][j]);
+                if (p.x_out && v < nv) *reinterpret_cast<uint4*>(p.x_out + row + 8 * v) = pack_bf8(f[i]);
+            }
+        }
+        float mean = 0.0f;
+        if (p.layer) {
+            float sum = 0.0f;
+#pragma unroll
+            for (int i = 0; i < kVec; ++i)
+#pragma unroll
+                for (int j = 0; j < 8; ++j) sum += f[i][j];   // (places past the row hold zeros)
+            mean = block_sum(sum) * p.inv_k;
+        }
+        float sum = 0.0f;
+#pragma unroll
+        for (int i = 0; i < kVec; ++i) {
+            if (t + i * threads >= nv) continue;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                f[i][j] -= mean;
+                sum = fmaf(f[i][j], f[i][j], sum);
+            }
+        }
+        sum = block_sum(sum);
+        // (the sum has used what the thread read of the slot)
+        load(r + (long long)kRing * gridDim.x, slot);
+        if (p.out) {
+            const float rs = rsqrtf(fmaf(sum, p.inv_k, p.eps));
+#pragma unroll
+            for (int i = 0; i < kVec; ++i) {
+                const int v = t + i * threads;
+                if (v >= nv) continue;
+#pragma unroll
+                for (int j = 0; j < 8; ++j) f[i][j] = fmaf(f[i][j] * rs, vb[i][j], vc[i][j]);
+                const uint4 o = pack_bf8(f[i]);
+                *reinterpret_cast<uint4*>(p.out + row + 8 * v) = o;
+                if (p.amax) {
+                    const uint32_t words[4] = {o.x, o.y, o.z, o.w};
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        top = max(top, max((words[j] << 16) & 0x7FFF0000u, words[j] & 0x7FFF0000u));
+                }
+            }
+        }
+        slot = slot + 1 == kRing ? 0 : slot + 1;
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    if (p.amax) {
+        top = __reduce_max_sync(0xffffffffu, top);
+        if (lane == 0 && top != 0) atomicMax(p.amax, top);
+    }
+}
+
+template <int kVec, int kThreads, int kBlocks>
+cudaError_t launch_ring(const BlockNormParams& p, cudaStream_t s)
+{
+    const int nv = p.K / 8, threads = ((nv + kVec - 1) / kVec + 31) / 32 * 32;
+    const int bytes = kRing * 2 * kVec * 16 * threads;
+    const cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void*>(block_norm_ring_kernel<kVec, kThreads, kBlocks>),
+                                              kRing * 2 * kVec * 16 * kThreads);
+    if (e != cudaSuccess) return e;
+    // as many as are resident at the registers that kThreads leave
+    const long long most = (long long)sm_count_current_device() * (kThreads * kBlocks / threads);
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.gridDim = dim3((unsigned)(p.M < most ? p.M : most));
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = bytes;
+    cfg.stream = s;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, block_norm_ring_kernel<kVec, kThreads, kBlocks>, p);
 }
 
 template <int kRow, int kVec>
@@ -257,14 +448,16 @@ cudaError_t launch_block_norm(const BlockNormJob& job, cudaStream_t s)
     p.K = job.K;
     p.seg = job.seg;
     const int nv = job.K / 8;
+    // Rows of up to 64 vectors by parts of a warp, wider ones by a block and from its ring: so also single
+    // rows, whose vectors it fetches while the sums are made (128 rows of 3072 2.7 us against 4.0 for blocks
+    // that read the vectors when they need them, 8192 rows 36 against 48).
+    if (nv <= 8) return launch<8, 1>(p, s);
+    if (nv <= 16) return launch<16, 1>(p, s);
     if (nv <= 32) return launch<32, 1>(p, s);
     if (nv <= 64) return launch<32, 2>(p, s);
-    if (nv <= 128) return launch<32, 4>(p, s);
-    if (nv <= 256) return launch<128, 2>(p, s);
-    if (nv <= 384) return launch<128, 3>(p, s);
-    if (nv <= 512) return launch<128, 4>(p, s);
-    if (nv <= 768) return launch<256, 3>(p, s);
-    if (nv <= 1024) return launch<256, 4>(p, s);
+    if (nv <= 384) return launch_ring<1, 384, 2>(p, s);
+    if (nv <= 512) return launch_ring<1, 512, 2>(p, s);
+    if (nv <= 1024) return launch_ring<2, 512, 1>(p, s);
     if (nv <= 2048) return launch<1024, 2>(p, s);
     return launch<1024, 4>(p, s);
 }

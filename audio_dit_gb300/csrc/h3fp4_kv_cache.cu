@@ -5,7 +5,7 @@
 //
 // with the quantiser's own arithmetic (nvfp4_encode.cuh), s the head's global scale.
 // Memory-bound: 4 bytes of bf16 per pair of K and V elements and 9/8 of the cache.
-// A warp takes one row; a lane one block of 16 elements at a time.
+// A warp takes a run of rows.
 #include <cstdint>
 
 #include <cuda_bf16.h>
@@ -51,160 +51,220 @@ __device__ __forceinline__ uint32_t gather(uint32_t x)
     return (x | (x >> 8)) & 0xFFFFu;
 }
 
-// Codes (eight of 16 elements in each word) and scale of a block.
-__device__ __forceinline__ void encode(const __nv_bfloat16* x, float s, uint32_t (&w)[2], uint32_t& S)
+// Sixteen bf16 values.
+__device__ __forceinline__ V16 load16(const __nv_bfloat16* x)
 {
     V16 v;
     *reinterpret_cast<uint4*>(v.w) = *reinterpret_cast<const uint4*>(x);
     *reinterpret_cast<uint4*>(v.w + 4) = *reinterpret_cast<const uint4*>(x + 8);
+    return v;
+}
+
+// Codes (eight of 16 elements in each word) and scale of a block.
+__device__ __forceinline__ uint32_t encode(const V16& v, float s, uint32_t (&w)[2])
+{
     float f[16];
     unpack16(v, f);
     float top = 0.0f;
 #pragma unroll
     for (int k = 0; k < 16; ++k) top = fmaxf(top, fabsf(f[k]));
-    S = block_scale_code(top, s);
+    const uint32_t S = block_scale_code(top, s);
     const float rcp = block_rcp(S, s);
 #pragma unroll
     for (int k = 0; k < 16; ++k) f[k] = __fmul_rn(f[k], rcp);
     w[0] = e2m1x8(reinterpret_cast<const float(&)[8]>(f[0]));
     w[1] = e2m1x8(reinterpret_cast<const float(&)[8]>(f[8]));
+    return S;
 }
 
-__device__ __forceinline__ void decode(const uint32_t (&w)[2], uint32_t code, float s, __nv_bfloat16* y)
+__device__ __forceinline__ uint4 decode(uint32_t w, uint32_t code, float s)
 {
     const float S = e4m3_value(code);
-    uint32_t o[8];
+    uint32_t o[4];
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-        const float2 q = e2m1_pair((w[k >> 2] >> (8 * (k & 3))) & 0xFFu);
+    for (int k = 0; k < 4; ++k) {
+        const float2 q = e2m1_pair((w >> (8 * k)) & 0xFFu);
         o[k] = cvt_bf16x2(f2(q.x * S * s, q.y * S * s));
     }
-    *reinterpret_cast<uint4*>(y) = make_uint4(o[0], o[1], o[2], o[3]);
-    *reinterpret_cast<uint4*>(y + 8) = make_uint4(o[4], o[5], o[6], o[7]);
+    return make_uint4(o[0], o[1], o[2], o[3]);
 }
 
 // The 16 bytes that two tokens' values share.
 template <int W>
 struct Shared16 {
+    static constexpr int kSecond = W == 64 ? 32 : 8;
     uint32_t w[4];
     __device__ __forceinline__ void load(const uint8_t* p)
     {
-        constexpr int kSecond = W == 64 ? 32 : 8;
         const uint2 a = *reinterpret_cast<const uint2*>(p), b = *reinterpret_cast<const uint2*>(p + kSecond);
         w[0] = a.x, w[1] = a.y, w[2] = b.x, w[3] = b.y;
     }
     __device__ __forceinline__ void store(uint8_t* p) const
     {
-        constexpr int kSecond = W == 64 ? 32 : 8;
         *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
         *reinterpret_cast<uint2*>(p + kSecond) = make_uint2(w[2], w[3]);
     }
 };
 
-template <int W, bool kRead>
-__global__ void __launch_bounds__(kThreads) cache_rows_kernel(const __grid_constant__ CacheRowsJob p)
+// The rows of a warp, one after the other: the sequence of each, and its place.
+struct Rows {
+    int s = -1;
+    long long first = 0, end = 0, len = 0, n = 0;   // the sequence's rows, tokens that there is room for, its length
+
+    // Position of row r, or -1 where it has none: one warp, all lanes.
+    __device__ __forceinline__ long long place(const CacheView& c, long long r, int lane)
+    {
+        if (s < 0 || r >= end) {
+            s = cache_sequence(c, r, lane);
+            if (s < 0) return -1;
+            first = c.row_off ? c.row_off[s] : r;
+            end = c.row_off ? c.row_off[s + 1] : r + 1;
+            n = c.length[s];
+            len = cache_length(c, s);
+        }
+        const long long pos = n - (end - r);
+        return pos < len ? pos : -1;
+    }
+};
+
+// A lane takes a block of 16 elements of a head at a time.
+template <int W>
+__global__ void __launch_bounds__(kThreads, 6) cache_append_kernel(const __grid_constant__ CacheRowsJob p, int rows_per_warp)
 {
     using L = CacheLayout<W>;
-    const int lane = threadIdx.x & 31;
+    constexpr int kHeads = 32 / L::kBlocks;   // heads of a warp at a time
+    const int lane = threadIdx.x & 31, b = lane % L::kBlocks, h0 = lane / L::kBlocks;
     const CacheView& c = p.c;
+    const bool real = 16 * b < c.D;
+    const long long head_bytes = (long long)(c.page / kCacheGroup) * L::kGroupBytes;
     griddep_wait();
-    const long long warps = (long long)gridDim.x * (kThreads / 32);
-    for (long long r = (long long)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5); r < p.M; r += warps) {
-        const int s = cache_sequence(c, r, lane);
-        if (s < 0) continue;
-        const long long first = c.row_off ? c.row_off[s] : r, end = c.row_off ? c.row_off[s + 1] : r + 1;
-        const long long pos = (long long)c.length[s] - (end - r), len = cache_length(c, s);
-        if (pos < 0 || pos >= len) continue;
-        uint8_t* base = cache_group<W>(c, s, pos, 0);
+    const long long warp = (long long)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
+    const long long r0 = warp * rows_per_warp, r1 = min((long long)p.M, r0 + rows_per_warp);
+    Rows rows;
+    for (long long r = r0; r < r1; ++r) {
+        const long long pos = rows.place(c, r, lane);
+        if (pos < 0) continue;
+        uint8_t* base = cache_group<W>(c, rows.s, pos, 0);
         if (!base) continue;
-        const int t = (int)(pos % c.page) % kCacheGroup;
-        const long long head_bytes = (long long)(c.page / kCacheGroup) * L::kGroupBytes;
-        // Two tokens share V's bytes: the row of the first writes both where the call has both, else a
-        // row keeps the other token's bits.
-        const bool with_next = !(t & 1) && r + 1 < min(end, (long long)p.M) && pos + 1 < len;
-        const bool with_last = (t & 1) && r > first && r > 0;
-        const int blocks = 2 * c.Hkv * L::kBlocks;  // K's, then V's
-        for (int i = lane; i < blocks; i += 32) {
-            const bool is_v = i >= blocks / 2;
-            const int j = is_v ? i - blocks / 2 : i;
-            const int h = j / L::kBlocks, b = j % L::kBlocks;
-            uint8_t* g = base + h * head_bytes;
-            const HeadsIn& x = is_v ? p.v : p.k;
-            const float* gs = is_v ? c.v_gscale : c.k_gscale;
-            const float sc = gs ? gs[h] : 1.0f;
-            const long long at = r * x.row + (long long)h * x.head + 16 * b;
-            const bool real = 16 * b < c.D;
-            if constexpr (kRead) {
-                if (!real) continue;
-                uint32_t w[2];
-                if (is_v) {
-                    Shared16<W> m;
-                    m.load(g + L::v_codes(t, b));
-                    const int shift = 4 * (t & 1);
-                    w[0] = gather(m.w[0] >> shift) | (gather(m.w[1] >> shift) << 16);
-                    w[1] = gather(m.w[2] >> shift) | (gather(m.w[3] >> shift) << 16);
-                } else {
-                    const uint2 m = *reinterpret_cast<const uint2*>(g + L::k_codes(t, b));
-                    w[0] = m.x, w[1] = m.y;
-                }
-                decode(w, g[is_v ? L::v_scale(t, b) : L::k_scale(t, b)], sc, (is_v ? p.v_out : p.k_out) + at);
-            } else {
-                if (is_v && with_last) continue;
-                uint32_t w[2] = {0, 0}, S = 0;
-                if (real) encode(x.p + at, sc, w, S);
-                if (!is_v) {
-                    *reinterpret_cast<uint2*>(g + L::k_codes(t, b)) = make_uint2(w[0], w[1]);
-                    g[L::k_scale(t, b)] = (uint8_t)S;
-                    continue;
-                }
-                Shared16<W> m;
-                if (!with_next) m.load(g + L::v_codes(t, b));
-                const int shift = 4 * (t & 1);
-                const uint32_t keep = 0xF0F0F0F0u >> shift;
+        const int t = (int)((uint32_t)pos % (uint32_t)c.page) % kCacheGroup, shift = 4 * (t & 1);
+        // Two tokens share V's bytes: the row of the first writes both where the call has both, else a row
+        // keeps the other token's bits.
+        const bool with_next = !(t & 1) && r + 1 < min(rows.end, (long long)p.M) && pos + 1 < rows.len;
+        const bool with_last = (t & 1) && r > rows.first && r > 0;
+        const __nv_bfloat16* kp = p.k.p + r * p.k.row + h0 * p.k.head + 16 * b;
+        const __nv_bfloat16* vp = p.v.p + r * p.v.row + h0 * p.v.head + 16 * b;
+        uint8_t* g = base + h0 * head_bytes;
+        for (int h = h0; h < c.Hkv; h += kHeads, kp += kHeads * p.k.head, vp += kHeads * p.v.head, g += kHeads * head_bytes) {
+            // (blocks past the head are zeros under a scale of zero)
+            V16 k = {}, v = {}, v2 = {};
+            if (real) {
+                k = load16(kp);
+                if (!with_last) v = load16(vp);
+                if (with_next) v2 = load16(vp + p.v.row);
+            }
+            uint32_t w[2];
+            const uint32_t S = encode(k, c.k_gscale ? c.k_gscale[h] : 1.0f, w);
+            *reinterpret_cast<uint2*>(g + L::k_codes(t, b)) = make_uint2(w[0], w[1]);
+            g[L::k_scale(t, b)] = (uint8_t)S;
+            if (with_last) continue;
+            const float gs = c.v_gscale ? c.v_gscale[h] : 1.0f;
+            Shared16<W> m = {};
+            if (!with_next) m.load(g + L::v_codes(t, b));
+            const uint32_t keep = 0xF0F0F0F0u >> shift;
+            g[L::v_scale(t, b)] = (uint8_t)encode(v, gs, w);
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const uint32_t mine = spread(w[k >> 1] >> (16 * (k & 1))) << shift;
-                    m.w[k] = with_next ? mine : (m.w[k] & keep) | mine;
-                }
-                g[L::v_scale(t, b)] = (uint8_t)S;
-                if (with_next) {
-                    w[0] = w[1] = S = 0;
-                    if (real) encode(x.p + at + x.row, sc, w, S);
+            for (int i = 0; i < 4; ++i) m.w[i] = (m.w[i] & keep) | (spread(w[i >> 1] >> (16 * (i & 1))) << shift);
+            if (with_next) {
+                g[L::v_scale(t + 1, b)] = (uint8_t)encode(v2, gs, w);
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) m.w[k] |= spread(w[k >> 1] >> (16 * (k & 1))) << 4;
-                    g[L::v_scale(t + 1, b)] = (uint8_t)S;
-                }
-                m.store(g + L::v_codes(t, b));
+                for (int i = 0; i < 4; ++i) m.w[i] |= spread(w[i >> 1] >> (16 * (i & 1))) << 4;
+            }
+            m.store(g + L::v_codes(t, b));
+        }
+    }
+}
+
+// A lane takes half a block, so that whole lines of bf16 are written.
+template <int W>
+__global__ void __launch_bounds__(kThreads) cache_read_kernel(const __grid_constant__ CacheRowsJob p, int rows_per_warp)
+{
+    using L = CacheLayout<W>;
+    constexpr int kLanes = 2 * L::kBlocks;    // of a head
+    constexpr int kHeads = 32 / kLanes;       // heads of a warp at a time
+    constexpr int kBatch = 4;                 // and how many of them it has in flight
+    const int lane = threadIdx.x & 31, b = lane % kLanes >> 1, half = lane & 1, h0 = lane / kLanes;
+    const CacheView& c = p.c;
+    const int d = 16 * b + 8 * half;
+    const long long head_bytes = (long long)(c.page / kCacheGroup) * L::kGroupBytes;
+    griddep_wait();
+    const long long warp = (long long)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
+    const long long r0 = warp * rows_per_warp, r1 = min((long long)p.M, r0 + rows_per_warp);
+    Rows rows;
+    for (long long r = r0; r < r1; ++r) {
+        const long long pos = rows.place(c, r, lane);
+        if (pos < 0) continue;
+        const uint8_t* base = cache_group<W>(c, rows.s, pos, 0);
+        if (!base || d >= c.D) continue;
+        const int t = (int)((uint32_t)pos % (uint32_t)c.page) % kCacheGroup, shift = 4 * (t & 1);
+        for (int h1 = h0; h1 < c.Hkv; h1 += kHeads * kBatch) {
+            uint32_t k[kBatch], sk[kBatch], sv[kBatch];
+            uint2 v[kBatch];
+            float gk[kBatch], gv[kBatch];
+#pragma unroll
+            for (int u = 0; u < kBatch; ++u) {
+                const int h = h1 + u * kHeads;
+                if (h >= c.Hkv) continue;
+                const uint8_t* g = base + h * head_bytes;
+                k[u] = *reinterpret_cast<const uint32_t*>(g + L::k_codes(t, b) + 4 * half);
+                v[u] = *reinterpret_cast<const uint2*>(g + L::v_codes(t, b) + half * Shared16<W>::kSecond);
+                sk[u] = g[L::k_scale(t, b)];
+                sv[u] = g[L::v_scale(t, b)];
+                gk[u] = c.k_gscale ? c.k_gscale[h] : 1.0f;
+                gv[u] = c.v_gscale ? c.v_gscale[h] : 1.0f;
+            }
+#pragma unroll
+            for (int u = 0; u < kBatch; ++u) {
+                const int h = h1 + u * kHeads;
+                if (h >= c.Hkv) continue;
+                const uint32_t codes = gather(v[u].x >> shift) | (gather(v[u].y >> shift) << 16);
+                *reinterpret_cast<uint4*>(p.k_out + r * p.k.row + h * p.k.head + d) = decode(k[u], sk[u], gk[u]);
+                *reinterpret_cast<uint4*>(p.v_out + r * p.v.row + h * p.v.head + d) = decode(codes, sv[u], gv[u]);
             }
         }
     }
 }
 
-template <bool kRead>
-cudaError_t launch(const CacheRowsJob& job, cudaStream_t s)
+template <int W>
+constexpr void (*kernel_of(bool read))(CacheRowsJob, int)
+{
+    return read ? cache_read_kernel<W> : cache_append_kernel<W>;
+}
+
+cudaError_t launch(const CacheRowsJob& job, bool read, cudaStream_t s)
 {
     if (job.M == 0) return cudaSuccess;
-    const long long blocks = (job.M + kThreads / 32 - 1) / (kThreads / 32);
-    const long long most = (long long)sm_count_current_device() * 16;
+    // as many warps as are resident, each with a run of rows
+    const long long most = (long long)sm_count_current_device() * (read ? 64 : 24);
+    const int per_warp = (int)((job.M + most - 1) / most);
+    const long long warps = (job.M + per_warp - 1) / per_warp;
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.gridDim = dim3((unsigned)(blocks < most ? blocks : most));
+    cfg.gridDim = dim3((unsigned)((warps + kThreads / 32 - 1) / (kThreads / 32)));
     cfg.blockDim = dim3(kThreads);
     cfg.stream = s;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     const int w = cache_width(job.c.D);
-    if (w == 64) return cudaLaunchKernelEx(&cfg, cache_rows_kernel<64, kRead>, job);
-    if (w == 128) return cudaLaunchKernelEx(&cfg, cache_rows_kernel<128, kRead>, job);
-    return cudaLaunchKernelEx(&cfg, cache_rows_kernel<256, kRead>, job);
+    return cudaLaunchKernelEx(&cfg, w == 64 ? kernel_of<64>(read) : w == 128 ? kernel_of<128>(read) : kernel_of<256>(read), job,
+                              per_warp);
 }
 
 }  // namespace
 
-cudaError_t launch_cache_append(const CacheRowsJob& job, cudaStream_t s) { return launch<false>(job, s); }
+cudaError_t launch_cache_append(const CacheRowsJob& job, cudaStream_t s) { return launch(job, false, s); }
 
-cudaError_t launch_cache_read(const CacheRowsJob& job, cudaStream_t s) { return launch<true>(job, s); }
+cudaError_t launch_cache_read(const CacheRowsJob& job, cudaStream_t s) { return launch(job, true, s); }
 
 }  // namespace h3fp4

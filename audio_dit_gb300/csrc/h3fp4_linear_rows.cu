@@ -96,10 +96,10 @@ __device__ __forceinline__ float pow2i(int x) { return __uint_as_float((uint32_t
 
 // ------------------------------------------------------------------ digits
 
-constexpr int kDigitThreads = 128;
+constexpr int kDigitThreads = 256;
 constexpr int kDigitColumns = kDigitThreads * 8;   // of x per CTA
 
-// Block (columns, row): the digits of 1024 columns of a row, two threads a block of 16.
+// Block (columns, row): the digits of 2048 columns of a row, two threads a block of 16.
 __global__ void __launch_bounds__(kDigitThreads)
     digits_kernel(const __nv_bfloat16* x, int K, int pass_rows, int kb4, uint8_t* codes, uint8_t* scales, float* factors)
 {
@@ -112,12 +112,13 @@ __global__ void __launch_bounds__(kDigitThreads)
     auto top2 = [](uint32_t w) { return max(w & 0x7FFFu, (w >> 16) & 0x7FFFu); };
     auto top8 = [&](const uint4& v) { return max(max(top2(v.x), top2(v.y)), max(top2(v.z), top2(v.w))); };
     uint32_t top = 0;
-#pragma unroll 4
+#pragma unroll 8
     for (int i = t; i < K / 8; i += kDigitThreads) top = max(top, top8(reinterpret_cast<const uint4*>(row)[i]));
     top = __reduce_max_sync(0xffffffffu, top);
     if (lane == 0) tops[t >> 5] = top;
     __syncthreads();
-    top = max(max(tops[0], tops[1]), max(tops[2], tops[3]));
+#pragma unroll
+    for (int i = 0; i < kDigitThreads / 32; ++i) top = max(top, tops[i]);
     const int e_row = max(1, (int)(top >> 7)) - 127 - 1;   // digits of the largest lie in [2, 4)
     if (blockIdx.x == 0 && t == 0) {
         // 2^(e_row - 8): the scales are that much larger (in two factors, either may be subnormal together)
@@ -418,19 +419,17 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int rows = min(p.pass_rows, p.M - pass * p.pass_rows);
             float* part = p.parts + piece * p.pass_rows * BM + n;
             const uint32_t d = tmem + ((32u * (uint32_t)quarter) << 16) + (uint32_t)(acc * NB);
-            for (int m = 0; m < rows; m += 2) {
-                uint32_t v[16];
-                tc_ld_32x32b_x16(d + 8 * m, v);   // (an odd number of rows: the second is not used)
-                tc_wait_ld_x16(v);
-                float y[2];
+            for (int m = 0; m < rows; m += 4) {
+                uint32_t v[32];
+                tc_ld_32x32b_x32(d + 8 * m, v);   // (rows past the last are not used)
+                tc_wait_ld_x32(v);
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    y[h] = __uint_as_float(v[8 * h + 7]);
+                for (int h = 0; h < 4; ++h) {
+                    float y = __uint_as_float(v[8 * h + 7]);
 #pragma unroll
-                    for (int t = kDigits - 2; t >= 0; --t) y[h] = fmaf(y[h], 0.125f, __uint_as_float(v[8 * h + t]));
+                    for (int t = kDigits - 2; t >= 0; --t) y = fmaf(y, 0.125f, __uint_as_float(v[8 * h + t]));
+                    if (m + h < rows) part[(m + h) * BM] = y;
                 }
-                part[m * BM] = y[0];
-                if (m + 1 < rows) part[(m + 1) * BM] = y[1];
             }
             tc_fence_before();
             __syncwarp();
@@ -463,7 +462,7 @@ struct JoinParams {
     const __nv_bfloat16* resid;
     __nv_bfloat16* out;
     long long N, chunk;
-    int passes, ks, pass_rows, swiglu;
+    int passes, ks, pass_rows, swiglu, M;
 };
 
 // silu(g) = g * sigmoid(g) in a form that overflows nowhere (as the GEMM's epilogue has it).
@@ -474,34 +473,61 @@ __device__ __forceinline__ float silu_f32(float g)
     return g * (g >= 0.0f ? r : t * r);
 }
 
-// Block (tile, row): 128 outputs of a row.
+// Block (tile, rows): 128 outputs of kRows rows of a pass, the loads of all rows in flight.
+template <int kRows>
 __global__ void __launch_bounds__(BM) rows_join_kernel(const __grid_constant__ JoinParams p)
 {
-    const int m = blockIdx.y, i = threadIdx.x;
-    const int pass = m / p.pass_rows, mm = m - pass * p.pass_rows;
+    const int i = threadIdx.x, groups = (p.pass_rows + kRows - 1) / kRows;   // of a pass
+    const int pass = blockIdx.y / groups, mm = (blockIdx.y - pass * groups) * kRows, m0 = pass * p.pass_rows + mm;
+    const int rows = min(kRows, min(p.pass_rows - mm, p.M - m0));
+    if (rows <= 0) return;
     griddep_wait();
-    const float f = p.factors[m], s = *p.w_gscale;
-    auto sum = [&](long long tile) {
-        const long long u = tile * p.passes + pass;
-        const long long c0 = u * p.ks / p.chunk, c1 = ((u + 1) * p.ks - 1) / p.chunk;
+    griddep_launch_dependents();
+    const float s = *p.w_gscale;
+    // the sums of a tile's output i, of all rows
+    auto sums = [&](long long tile, float (&y)[kRows]) {
+        float bias = 0.0f;
+        if (p.bias && tile * BM + i < p.N) bias = __bfloat162float(p.bias[tile * BM + i]);
+        const long long u = tile * p.passes + pass, first = u * p.ks;
+        // (below 2^32 stages for all sizes that are taken)
+        const int c0 = (uint32_t)first / (uint32_t)p.chunk, c1 = (uint32_t)(first + p.ks - 1) / (uint32_t)p.chunk;
         const float* at = p.parts + ((u + c0) * p.pass_rows + mm) * BM + i;
-        float y = 0.0f;
-#pragma unroll 4
-        for (long long c = c0; c <= c1; ++c, at += (long long)p.pass_rows * BM) y += *at;
-        const long long n = tile * BM + i;
-        return fmaf(y * s, f, p.bias && n < p.N ? __bfloat162float(p.bias[n]) : 0.0f);
+#pragma unroll
+        for (int k = 0; k < kRows; ++k) y[k] = 0.0f;
+#pragma unroll(kRows > 1 ? 2 : 8)
+        for (int c = c0; c <= c1; ++c, at += (long long)p.pass_rows * BM)
+#pragma unroll
+            for (int k = 0; k < kRows; ++k)
+                if (k < rows) y[k] += at[k * BM];
+#pragma unroll
+        for (int k = 0; k < kRows; ++k)
+            if (k < rows) y[k] = fmaf(y[k] * s, p.factors[m0 + k], bias);
     };
+    float y[kRows];
     if (p.swiglu) {
-        const float g = __bfloat162float(__float2bfloat16_rn(sum(2ll * blockIdx.x)));
-        const float u = __bfloat162float(__float2bfloat16_rn(sum(2ll * blockIdx.x + 1)));
-        p.out[m * (p.N / 2) + (long long)blockIdx.x * BM + i] = __float2bfloat16_rn(silu_f32(g) * u);
+        float u[kRows];
+        sums(2ll * blockIdx.x, y);
+        sums(2ll * blockIdx.x + 1, u);
+#pragma unroll
+        for (int k = 0; k < kRows; ++k)
+            if (k < rows)
+                p.out[(m0 + k) * (p.N / 2) + (long long)blockIdx.x * BM + i] = __float2bfloat16_rn(
+                    silu_f32(__bfloat162float(__float2bfloat16_rn(y[k]))) * __bfloat162float(__float2bfloat16_rn(u[k])));
         return;
     }
     const long long n = (long long)blockIdx.x * BM + i;
     if (n >= p.N) return;
-    float v = sum(blockIdx.x);
-    if (p.gate) v = fmaf(p.gate[m * p.gate_stride + n], v, __bfloat162float(p.resid[m * p.N + n]));
-    p.out[m * p.N + n] = __float2bfloat16_rn(v);
+    float g[kRows], r[kRows];
+#pragma unroll
+    for (int k = 0; k < kRows; ++k)
+        if (p.gate && k < rows) {
+            g[k] = p.gate[(m0 + k) * p.gate_stride + n];
+            r[k] = __bfloat162float(p.resid[(m0 + k) * p.N + n]);
+        }
+    sums(blockIdx.x, y);
+#pragma unroll
+    for (int k = 0; k < kRows; ++k)
+        if (k < rows) p.out[(m0 + k) * p.N + n] = __float2bfloat16_rn(p.gate ? fmaf(g[k], y[k], r[k]) : y[k]);
 }
 
 template <int NB>
@@ -547,7 +573,6 @@ cudaError_t launch_linear_rows(const LinearRowsJob& job, cudaStream_t s)
     cfg.blockDim = dim3(kDigitThreads);
     float* factors = reinterpret_cast<float*>(job.ws + kFactors);
     cudaError_t e = ensure_shared_carveout(reinterpret_cast<const void*>(digits_kernel));
-    if (e == cudaSuccess) e = ensure_shared_carveout(reinterpret_cast<const void*>(rows_join_kernel));
     if (e != cudaSuccess) return e;
     e = cudaLaunchKernelEx(&cfg, digits_kernel, job.x, (int)job.K, l.pass_rows, (int)l.kb4,
                                        job.ws + l.codes, job.ws + l.scales, factors);
@@ -589,9 +614,20 @@ cudaError_t launch_linear_rows(const LinearRowsJob& job, cudaStream_t s)
     jp.ks = p.ks;
     jp.pass_rows = l.pass_rows;
     jp.swiglu = job.swiglu;
-    cfg.gridDim = dim3((unsigned)(job.swiglu ? l.tiles / 2 : l.tiles), (unsigned)job.M);
+    jp.M = (int)job.M;
+    auto join = [&](void (*kernel)(JoinParams)) {
+        const cudaError_t e = ensure_shared_carveout(reinterpret_cast<const void*>(kernel));
+        return e == cudaSuccess ? cudaLaunchKernelEx(&cfg, kernel, jp) : e;
+    };
+    // four rows a thread where there are many blocks (61 rows of 49 tiles 8 -> 5 us cold)
+    const unsigned tiles = (unsigned)(job.swiglu ? l.tiles / 2 : l.tiles);
     cfg.blockDim = dim3(BM);
-    return cudaLaunchKernelEx(&cfg, rows_join_kernel, jp);
+    if (tiles * job.M > 1216) {
+        cfg.gridDim = dim3(tiles, (unsigned)(l.passes * ((l.pass_rows + 3) / 4)));
+        return join(rows_join_kernel<4>);
+    }
+    cfg.gridDim = dim3(tiles, (unsigned)(l.passes * l.pass_rows));
+    return join(rows_join_kernel<1>);
 }
 
 }  // namespace h3fp4

@@ -60,6 +60,18 @@ CASES = [  # M, K, offsets, y, post, layer, vectors
     (2, 16392, [0, 0, 1, 2], True, True, True, ALL),
     (2, 32768, None, True, True, True, ALL),
     (2000, 64, [0, 1, 2, 3, 4, 5, 6, 7, 2000], True, True, False, ALL),
+    (1501, 72, [0, 1500, 1501], True, False, True, ALL),
+    (1027, 128, None, False, False, False, ("scale",)),
+    # many rows: the vectors kept, or read for each row
+    (1024, 520, [0, 1, 700, 701, 1024], True, True, True, ALL),
+    (1100, 1024, None, False, False, True, ("shift", "scale")),
+    (1500, 3072, [0, 3, 900, 1500], True, True, False, ALL),
+    (1025, 4096, [0, 1024, 1025], True, False, True, ("gate", "shift", "scale")),
+    (1300, 5192, [0, 600, 600, 1300], True, True, True, ALL),
+    (1024, 8192, None, True, True, False, ("y_weight", "weight")),
+    (1030, 8200, [0, 1029, 1030], True, True, True, ALL),
+    (1024, 16384, [0, 1023, 1024], True, True, True, ALL),
+    (1024, 16392, None, True, False, False, ("gate", "weight")),
 ]
 
 
