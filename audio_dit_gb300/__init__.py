@@ -30,6 +30,7 @@ __all__ = [
     "h3fp4_cache_attn", "h3fp4_cache_page_bytes", "h3fp4_cache_attn_workspace_bytes", "alloc_kv_cache",
     "alloc_cache_attn_workspace", "h3fp4_linear_rows",
     "h3fp4_linear_rows_workspace_bytes", "alloc_rows_workspace", "ROWS_MAX", "h3fp4_selftest_cache_attn_timeout",
+    "h3fp4_selftest_linear_rows_timeout",
 ]
 
 PROLOGUE_MOD = 1
@@ -108,6 +109,7 @@ def load_library():
                                    vp]),
         "h3fp4_linear_rows": (i32, [vp, i64, i64, i64, vp, vp, vp, vp, i64, vp, vp, vp, i32, vp, sz, vp]),
         "h3fp4_linear_rows_workspace_bytes": (sz, [i64, i64, i64]),
+        "h3fp4_selftest_linear_rows_timeout": (i32, [vp, C.c_uint64, vp]),
         "h3fp4_cache_page_bytes": (sz, [i32, i32, i32]),
         "h3fp4_cache_append": (i32, [hp, hp, i64, vp, vp]),
         "h3fp4_cache_read": (i32, [hp, hp, i64, vp, vp]),
@@ -586,6 +588,13 @@ def h3fp4_linear_rows(x: torch.Tensor, w_codes: torch.Tensor, w_sf: torch.Tensor
         _f32(w_gscale, "w_gscale", (1,)), None if gate is None else _f32(gate, "gate", gate_shape), stride,
         _bf16(bias, "bias", (N,)), _bf16(resid, "resid", (M, N)), _bf16(out, "out", (M, N // 2 if swiglu else N)), flags,
         _workspace(ws), ws.numel(), _stream(stream)), "h3fp4_linear_rows")
+
+
+def h3fp4_selftest_linear_rows_timeout(ws: torch.Tensor, limit_ns: int, stream=None) -> None:
+    if ws.numel() < h3fp4_linear_rows_workspace_bytes(64, 128, 1024):
+        raise ValueError("ws must be a workspace for 64 rows of 1024 columns and 128 outputs")
+    _check(load_library().h3fp4_selftest_linear_rows_timeout(_ptr(ws, "ws", torch.uint8), int(limit_ns),
+                                                             _stream(stream)), "h3fp4_selftest_linear_rows_timeout")
 
 
 def h3fp4_linear_rows_workspace_bytes(M: int, N: int, K: int) -> int:

@@ -494,6 +494,10 @@ H3FP4_API h3fp4_status h3fp4_linear_rows(const void* x_bf16, int64_t M, int64_t 
 /* Workspace bytes of h3fp4_linear_rows; 0 for sizes it refuses. */
 H3FP4_API size_t h3fp4_linear_rows_workspace_bytes(int64_t M, int64_t N, int64_t K);
 
+/* Failure-detection self-test of h3fp4_linear_rows, as h3fp4_selftest_attn_timeout: its
+ * copies are left out.  ws: h3fp4_linear_rows_workspace_bytes(64, 128, 1024) bytes. */
+H3FP4_API h3fp4_status h3fp4_selftest_linear_rows_timeout(void* ws, uint64_t limit_ns, cudaStream_t stream);
+
 /* A paged cache of keys and values held in four bits, and the sequences of a call.
  *   pool: device, 16-byte aligned, n_pages * h3fp4_cache_page_bytes(heads, dim, page)
  *      bytes.  A page holds `page` tokens (16 to 1024, a multiple of 16) of all heads:

@@ -155,3 +155,13 @@ def test_near_the_linear():
     A.h3fp4_linear_rows(x, *wq, one, A.alloc_rows_workspace(M, N, K), bias=b, swiglu=True)
     A.h3fp4_linear(x, *wq, two, A.alloc_workspace(M, N, K), bias=b, swiglu=True)
     assert float((one.float() - two.float()).norm() / one.float().norm()) < 0.25
+
+
+def test_waits_that_run_out():
+    import audio_dit_gb300 as A
+    ws = A.alloc_rows_workspace(64, 128, 1024)
+    A.h3fp4_selftest_linear_rows_timeout(ws, 1000000)
+    with pytest.raises(A.H3FP4Error) as e:
+        A.h3fp4_check(ws)
+    assert e.value.status == 5
+    A.h3fp4_check(ws)                                                 # read and cleared
