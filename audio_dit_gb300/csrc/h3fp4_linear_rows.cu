@@ -23,6 +23,7 @@
 // gives the same bits.  Each starts while the one before it drains; the first W tiles are on
 // their way before the digits are there.
 #include <cstdint>
+#include <mutex>
 
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -99,41 +100,32 @@ __device__ __forceinline__ float pow2i(int x) { return __uint_as_float((uint32_t
 constexpr int kDigitThreads = 256;
 constexpr int kDigitColumns = kDigitThreads * 8;   // of x per CTA
 
-// Block (columns, row): the digits of 2048 columns of a row, two threads a block of 16.
-__global__ void __launch_bounds__(kDigitThreads)
-    digits_kernel(const __nv_bfloat16* x, int K, int pass_rows, int kb4, uint8_t* codes, uint8_t* scales, float* factors)
+// The largest magnitude of bf16 pairs, as its bits (they order like the values).
+__device__ __forceinline__ uint32_t top_bits(const uint4& v)
 {
-    __shared__ uint32_t tops[kDigitThreads / 32];
-    const int m = blockIdx.y, t = threadIdx.x, lane = t & 31;
-    const __nv_bfloat16* row = x + (long long)m * K;
-    griddep_wait();
-    griddep_launch_dependents();   // the weights may be fetched: nothing before this call writes them any more
-    // the row's largest magnitude (non-negative bf16 values order like their bits)
-    auto top2 = [](uint32_t w) { return max(w & 0x7FFFu, (w >> 16) & 0x7FFFu); };
-    auto top8 = [&](const uint4& v) { return max(max(top2(v.x), top2(v.y)), max(top2(v.z), top2(v.w))); };
-    uint32_t top = 0;
-#pragma unroll 8
-    for (int i = t; i < K / 8; i += kDigitThreads) top = max(top, top8(reinterpret_cast<const uint4*>(row)[i]));
-    top = __reduce_max_sync(0xffffffffu, top);
-    if (lane == 0) tops[t >> 5] = top;
-    __syncthreads();
-#pragma unroll
-    for (int i = 0; i < kDigitThreads / 32; ++i) top = max(top, tops[i]);
-    const int e_row = max(1, (int)(top >> 7)) - 127 - 1;   // digits of the largest lie in [2, 4)
-    if (blockIdx.x == 0 && t == 0) {
-        // 2^(e_row - 8): the scales are that much larger (in two factors, either may be subnormal together)
-        factors[m] = pow2i(e_row / 2) * pow2i(e_row - e_row / 2 - 8);
-    }
-    const int col = blockIdx.x * kDigitColumns + 8 * t;
-    const bool real = col < K;
-    uint4 v = make_uint4(0, 0, 0, 0);
-    if (real) v = *reinterpret_cast<const uint4*>(row + col);
-    uint32_t btop = top8(v);
-    btop = max(btop, __shfl_xor_sync(0xffffffffu, btop, 1));
-    // binades below the row's largest, as far as E4M3 goes: 2^8 down to 2^-9
-    const int below = min(17, e_row - (max(1, (int)(btop >> 7)) - 127 - 1));
-    const int k = 8 - below;
-    const uint32_t S = k >= -6 ? (uint32_t)(k + 7) << 3 : 1u << (k + 9);
+    auto two = [](uint32_t w) { return max(w & 0x7FFFu, (w >> 16) & 0x7FFFu); };
+    return max(max(two(v.x), two(v.y)), max(two(v.z), two(v.w)));
+}
+
+// The exponent of the digits' unit where the largest magnitude is `top`: it lies in [2, 4) of them.
+__device__ __forceinline__ int unit_of(uint32_t top) { return max(1, (int)(top >> 7)) - 127 - 1; }
+
+// 2^(e_row - 8), what the sums of a row's digits are in (either factor may be subnormal together).
+__device__ __forceinline__ float row_factor(int e_row) { return pow2i(e_row / 2) * pow2i(e_row - e_row / 2 - 8); }
+
+// The digits of a lane's eight elements of x, eight codes a word; the scale of its block of 16, which it
+// shares with the lane beside it: binades below the row's, as far as E4M3 goes (2^8 down to 2^-9).
+struct Digits {
+    uint32_t code[kDigits], scale;
+};
+
+__device__ __forceinline__ Digits digits_of(const uint4& v, int e_row)
+{
+    Digits o;
+    uint32_t top = top_bits(v);
+    top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+    const int below = min(17, e_row - unit_of(top)), k = 8 - below;
+    o.scale = k >= -6 ? (uint32_t)(k + 7) << 3 : 1u << (k + 9);
     const int e = below - e_row;   // what x is scaled with: two factors, as the sum may pass 127
     const float up0 = pow2i(e / 2), up1 = pow2i(e - e / 2);
     float r[8];
@@ -143,11 +135,9 @@ __global__ void __launch_bounds__(kDigitThreads)
         r[2 * i] = bf16_lo(w[i]) * up0 * up1;
         r[2 * i + 1] = bf16_hi(w[i]) * up0 * up1;
     }
-    const int pass = m / pass_rows, r0 = 256 * pass + kDigits * (m - pass * pass_rows);
 #pragma unroll
     for (int d = 0; d < kDigits; ++d) {
-        const uint32_t c = e2m1x8(r);
-        if (real) *reinterpret_cast<uint32_t*>(codes + (long long)(r0 + d) * (K / 2) + col / 2) = c;
+        o.code[d] = e2m1x8(r);
         uint32_t q[4];
         asm("{\n\t.reg .b8 a, b, c, d;\n\t"
             "mov.b32 {a, b, c, d}, %4;\n\t"
@@ -156,7 +146,7 @@ __global__ void __launch_bounds__(kDigitThreads)
             "cvt.rn.f16x2.e2m1x2 %2, c;\n\t"
             "cvt.rn.f16x2.e2m1x2 %3, d;\n\t}"
             : "=r"(q[0]), "=r"(q[1]), "=r"(q[2]), "=r"(q[3])
-            : "r"(c));
+            : "r"(o.code[d]));
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             float lo, hi;
@@ -167,15 +157,51 @@ __global__ void __launch_bounds__(kDigitThreads)
             r[2 * i + 1] = (r[2 * i + 1] - hi) * 8.0f;
         }
     }
-    // Eight lanes have the four scales of a 64-column group; each writes the word of one digit row.
+    return o;
+}
+
+// Eight lanes have the four scales of a 64-column group: their word, for each of them.
+__device__ __forceinline__ uint32_t scale_word(uint32_t scale, int lane)
+{
     uint32_t word = 0;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) word |= __shfl_sync(0xffffffffu, S, (lane & ~7) + 2 * i) << (8 * i);
-    if (real) {
-        const int rr = r0 + (lane & 7);
-        *reinterpret_cast<uint32_t*>(scales + ((long long)(rr >> 7) * kb4 + (col >> 6)) * 512 + (rr & 31) * 16 +
-                                     ((rr & 127) >> 5) * 4) = word;
-    }
+    for (int i = 0; i < 4; ++i) word |= __shfl_sync(0xffffffffu, scale, (lane & ~7) + 2 * i) << (8 * i);
+    return word;
+}
+
+// Block (columns, row): the digits of 2048 columns of a row, two threads a block of 16.
+__global__ void __launch_bounds__(kDigitThreads)
+    digits_kernel(const __nv_bfloat16* x, int K, int pass_rows, int kb4, uint8_t* codes, uint8_t* scales, float* factors)
+{
+    __shared__ uint32_t tops[kDigitThreads / 32];
+    const int m = blockIdx.y, t = threadIdx.x, lane = t & 31;
+    const __nv_bfloat16* row = x + (long long)m * K;
+    griddep_wait();
+    griddep_launch_dependents();   // the weights may be fetched: nothing before this call writes them any more
+    uint32_t top = 0;
+#pragma unroll 8
+    for (int i = t; i < K / 8; i += kDigitThreads) top = max(top, top_bits(reinterpret_cast<const uint4*>(row)[i]));
+    top = __reduce_max_sync(0xffffffffu, top);
+    if (lane == 0) tops[t >> 5] = top;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kDigitThreads / 32; ++i) top = max(top, tops[i]);
+    const int e_row = unit_of(top);
+    if (blockIdx.x == 0 && t == 0) factors[m] = row_factor(e_row);
+    const int col = blockIdx.x * kDigitColumns + 8 * t;
+    const bool real = col < K;
+    uint4 v = make_uint4(0, 0, 0, 0);
+    if (real) v = *reinterpret_cast<const uint4*>(row + col);
+    const Digits o = digits_of(v, e_row);
+    const uint32_t word = scale_word(o.scale, lane);
+    if (!real) return;
+    const int pass = m / pass_rows, r0 = 256 * pass + kDigits * (m - pass * pass_rows);
+#pragma unroll
+    for (int d = 0; d < kDigits; ++d)
+        *reinterpret_cast<uint32_t*>(codes + (long long)(r0 + d) * (K / 2) + col / 2) = o.code[d];
+    const int rr = r0 + (lane & 7);   // each lane writes the word of one digit row
+    *reinterpret_cast<uint32_t*>(scales + ((long long)(rr >> 7) * kb4 + (col >> 6)) * 512 + (rr & 31) * 16 +
+                                 ((rr & 127) >> 5) * 4) = word;
 }
 
 // ------------------------------------------------------------------ products
@@ -189,6 +215,70 @@ struct GemmParams {
     unsigned long long wait_ns;
     int stall;
 };
+
+// A stage's scale tiles from shared memory into one lane quarter of TMEM (each quarter holds a copy).
+template <int NB>
+__device__ __forceinline__ void store_scales(uint32_t stage_smem, uint32_t tmem, uint32_t quarter, int lane)
+{
+    using P = Plan<NB>;
+    const uint32_t sfa_s = stage_smem + kWBytes + P::kDBytes + 16u * (uint32_t)lane, sfb_s = sfa_s + kSfwBytes;
+    const uint32_t t = tmem + ((32u * quarter) << 16) + P::kSfTmem;
+    uint32_t va[16], vb[P::kHalves][16];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const uint4 a = ld_shared_v4(sfa_s + 512u * j);
+        va[4 * j] = a.x, va[4 * j + 1] = a.y, va[4 * j + 2] = a.z, va[4 * j + 3] = a.w;
+#pragma unroll
+        for (int h = 0; h < P::kHalves; ++h) {
+            const uint4 b = ld_shared_v4(sfb_s + kSfBox * h + 512u * j);
+            // columns: group j, then half h
+            const int at = 4 * (P::kHalves * j + h);
+            vb[at / 16][at % 16] = b.x, vb[at / 16][at % 16 + 1] = b.y;
+            vb[at / 16][at % 16 + 2] = b.z, vb[at / 16][at % 16 + 3] = b.w;
+        }
+    }
+    tc_st_32x32b_x16(t, va);
+#pragma unroll
+    for (int h = 0; h < P::kHalves; ++h) tc_st_32x32b_x16(t + 16 + 16 * h, vb[h]);
+    tc_wait_st();
+    tc_fence_before();
+    __syncwarp();
+}
+
+// The MMAs of a stage and the release of its slot, by one lane.
+template <int NB>
+__device__ __forceinline__ void multiply(uint32_t stage_smem, uint32_t tmem, uint32_t d, uint32_t idesc, int nk, bool first,
+                                         uint64_t* empty)
+{
+    using P = Plan<NB>;
+    const uint64_t a = smem_desc(stage_smem, 16, 1024, 2), b = smem_desc(stage_smem + kWBytes, 16, 1024, 2);
+    const uint32_t sfa = tmem + P::kSfTmem, sfb = sfa + 16;
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+        if (j < nk)
+            mma_mxf4nvf4(d, a + 2u * j, b + 2u * j, idesc, sfa + 4u * j, sfb + 4u * P::kHalves * j, !first || j > 0 ? 1u : 0u);
+    tc_commit(empty);
+}
+
+// E2M1 operands, K-major, N = nb, M = 128, UE4M3 scales.
+__device__ __forceinline__ uint32_t mma_desc(int nb)
+{
+    return (1u << 7) | (1u << 10) | ((uint32_t)(nb >> 3) << 17) | ((uint32_t)(BM >> 4) << 24);
+}
+
+// Four rows' sums from their 32 columns of the accumulator: digit d weighs 8^-d.
+__device__ __forceinline__ void four_rows(uint32_t tmem, float (&y)[4])
+{
+    uint32_t v[32];
+    tc_ld_32x32b_x32(tmem, v);
+    tc_wait_ld_x32(v);
+#pragma unroll
+    for (int h = 0; h < 4; ++h) {
+        y[h] = __uint_as_float(v[8 * h + 7]);
+#pragma unroll
+        for (int t = kDigits - 2; t >= 0; --t) y[h] = fmaf(y[h], 0.125f, __uint_as_float(v[8 * h + t]));
+    }
+}
 
 template <int NB>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -313,8 +403,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
     } else if (warp == 1) {
         // ------------------------------------------------------------ MMA
-        // E2M1 operands, K-major, N = nb, M = 128, UE4M3 scales
-        const uint32_t idesc = (1u << 7) | (1u << 10) | ((uint32_t)(p.nb >> 3) << 17) | ((uint32_t)(BM >> 4) << 24);
+        const uint32_t idesc = mma_desc(p.nb);
         int stage = 0, acc = 0;
         uint32_t phase = 0, acc_phase = 0;
         bool ok = true;
@@ -330,18 +419,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 ok = __all_sync(0xffffffffu, ok && s_abort == 0);
                 if (!ok) break;
                 tc_fence_after();
-                const int nk = min(4, p.kb4 - (kb + i) * 4);
-                const uint32_t st = smem_u32(smem) + (uint32_t)stage * P::kStage;
-                const uint64_t a = smem_desc(st, 16, 1024, 2), b = smem_desc(st + kWBytes, 16, 1024, 2);
-                const uint32_t sfa = tmem + P::kSfTmem + (uint32_t)stage * P::kSfCols, sfb = sfa + 16;
-                if (elect_one()) {
-#pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        if (j < nk)
-                            mma_mxf4nvf4(d, a + 2u * j, b + 2u * j, idesc, sfa + 4u * j, sfb + 4u * P::kHalves * j,
-                                         i > 0 || j > 0 ? 1u : 0u);
-                    tc_commit(&empty[stage]);
-                }
+                if (elect_one())
+                    multiply<NB>(smem_u32(smem) + (uint32_t)stage * P::kStage, tmem + (uint32_t)stage * P::kSfCols, d, idesc,
+                                 min(4, p.kb4 - (kb + i) * 4), i == 0, &empty[stage]);
                 __syncwarp();
                 if (++stage == kStages) {
                     stage = 0;
@@ -371,29 +451,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 s_abort = 1;
                 break;
             }
-            const uint32_t sfa_s = smem_u32(smem) + (uint32_t)stage * P::kStage + kWBytes + P::kDBytes + 16u * (uint32_t)lane;
-            const uint32_t sfb_s = sfa_s + kSfwBytes;
-            const uint32_t t = tmem + ((32u * quarter) << 16) + P::kSfTmem + (uint32_t)stage * P::kSfCols;
-            uint32_t va[16], vb[P::kHalves][16];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const uint4 a = ld_shared_v4(sfa_s + 512u * j);
-                va[4 * j] = a.x, va[4 * j + 1] = a.y, va[4 * j + 2] = a.z, va[4 * j + 3] = a.w;
-#pragma unroll
-                for (int h = 0; h < P::kHalves; ++h) {
-                    const uint4 b = ld_shared_v4(sfb_s + kSfBox * h + 512u * j);
-                    // columns: group j, then half h
-                    const int at = 4 * (P::kHalves * j + h);
-                    vb[at / 16][at % 16] = b.x, vb[at / 16][at % 16 + 1] = b.y;
-                    vb[at / 16][at % 16 + 2] = b.z, vb[at / 16][at % 16 + 3] = b.w;
-                }
-            }
-            tc_st_32x32b_x16(t, va);
-#pragma unroll
-            for (int h = 0; h < P::kHalves; ++h) tc_st_32x32b_x16(t + 16 + 16 * h, vb[h]);
-            tc_wait_st();
-            tc_fence_before();
-            __syncwarp();
+            store_scales<NB>(smem_u32(smem) + (uint32_t)stage * P::kStage, tmem + (uint32_t)stage * P::kSfCols, quarter, lane);
             if (lane == 0) mbar_arrive(&full[stage]);
             if (++stage == kStages) {
                 stage = 0;
@@ -420,16 +478,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             float* part = p.parts + piece * p.pass_rows * BM + n;
             const uint32_t d = tmem + ((32u * (uint32_t)quarter) << 16) + (uint32_t)(acc * NB);
             for (int m = 0; m < rows; m += 4) {
-                uint32_t v[32];
-                tc_ld_32x32b_x32(d + 8 * m, v);   // (rows past the last are not used)
-                tc_wait_ld_x32(v);
+                float y[4];
+                four_rows(d + 8 * m, y);   // (rows past the last are not used)
 #pragma unroll
-                for (int h = 0; h < 4; ++h) {
-                    float y = __uint_as_float(v[8 * h + 7]);
-#pragma unroll
-                    for (int t = kDigits - 2; t >= 0; --t) y = fmaf(y, 0.125f, __uint_as_float(v[8 * h + t]));
-                    if (m + h < rows) part[(m + h) * BM] = y;
-                }
+                for (int h = 0; h < 4; ++h)
+                    if (m + h < rows) part[(m + h) * BM] = y[h];
             }
             tc_fence_before();
             __syncwarp();
@@ -530,6 +583,351 @@ __global__ void __launch_bounds__(BM) rows_join_kernel(const __grid_constant__ J
         if (k < rows) p.out[(m0 + k) * p.N + n] = __float2bfloat16_rn(p.gate ? fmaf(g[k], y[k], r[k]) : y[k]);
 }
 
+// ------------------------------------------------------------------ up to eight rows, in one kernel
+//
+// A launch, its start and the wait for the one before cost what a small weight's reading does.  So where a
+// wave of CTAs has all tiles, a cluster of `split` CTAs (with SwiGLU twice as many: the gate and the up tile)
+// takes one: each makes the digits of its own columns of x (under an exponent of its own) beside the other
+// roles, multiplies, and adds its sums to those of the others in the first one's shared memory, which
+// finishes the outputs.
+constexpr int kFewRows = 8;
+constexpr int kFewThreads = 512;     // as above, and four warps of digits
+constexpr int kMaxCluster = 8;
+constexpr int kFewStages = 6;
+
+struct FewParams {
+    const __nv_bfloat16* x;
+    JoinParams j;
+    long long K;
+    int split, ks, kb4;
+    unsigned int* status;
+    unsigned long long wait_ns;
+    int stall;
+};
+
+__global__ void __launch_bounds__(kFewThreads, 1)
+    rows_few_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmSfw, const FewParams p)
+{
+    extern __shared__ __align__(1024) uint8_t smem[];
+    using P = Plan<64>;
+    constexpr int kStages = kFewStages;
+    constexpr uint32_t kRedOff = kStages * P::kStage, kBarOff = kRedOff + kMaxCluster * kFewRows * BM * 4;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if ((smem_u32(smem) & 1023u) != 0) {   // (the same in every CTA)
+        if (threadIdx.x == 0) atomicOr(p.status, kStatusBadSmemAlign);
+        return;
+    }
+    float* red = reinterpret_cast<float*>(smem + kRedOff);            // the first CTA's: [rank][row][output]
+    uint64_t* full = reinterpret_cast<uint64_t*>(smem + kBarOff);     // codes landed, digits and scales stored
+    uint64_t* empty = full + kStages;
+    uint64_t* sf_full = empty + kStages;                              // scale tiles landed and written
+    uint64_t* acc_full = sf_full + kStages;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(acc_full + 1);
+    volatile int& s_abort = *reinterpret_cast<volatile int*>(tmem_slot + 1);
+    float* factor = reinterpret_cast<float*>(tmem_slot + 2);          // per row
+    uint32_t* tops = reinterpret_cast<uint32_t*>(factor + kFewRows);  // per row and digit warp
+    if (threadIdx.x == 0) {
+        s_abort = 0;
+        for (int i = 0; i < kStages; ++i) {
+            mbar_init(&full[i], 1 + 4 + 4);
+            mbar_init(&empty[i], 1);
+            mbar_init(&sf_full[i], 1 + 4);
+        }
+        mbar_init(acc_full, 1);
+        fence_mbarrier_init();
+        prefetch_tensormap(&tmW);
+        prefetch_tensormap(&tmSfw);
+    }
+    if (warp == 1) {
+        tmem_alloc(tmem_slot, kTmemCols);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    cluster_arrive();   // (waited for before anything is written to the first CTA)
+    const uint32_t tmem = *tmem_slot;
+    const int M = p.j.M;
+    const int rank = (int)cluster_ctarank(), size = p.j.swiglu ? 2 * p.split : p.split;
+    const int group = blockIdx.x / size, part = rank % p.split;
+    const int tile = p.j.swiglu ? 2 * group + rank / p.split : group;
+    const int kb0 = p.ks * part / p.split, n = p.ks * (part + 1) / p.split - kb0;
+    griddep_wait();
+    griddep_launch_dependents();
+
+    if (warp == 0) {
+        // ------------------------------------------------------------ W and its scales
+        uint32_t fills[kStages] = {};
+        int stage = 0;
+        uint32_t phase = 1;   // (the first fills wait for nothing)
+        for (int i = 0; i < n && !p.stall; ++i) {
+            const bool ok = mbar_wait(&empty[stage], phase, p.wait_ns, p.status, kStatusTimeoutProducer);
+            if (!__all_sync(0xffffffffu, ok && s_abort == 0)) {
+                s_abort = 1;
+                break;
+            }
+            if (elect_one()) {
+                uint8_t* st = smem + stage * P::kStage;
+                mbar_arrive_expect_tx(&sf_full[stage], kSfwBytes);
+                tma_load_2d(st + kWBytes + P::kDBytes, &tmSfw, &sf_full[stage], 0, (tile * p.kb4 + (kb0 + i) * 4) * 2);
+                mbar_arrive_expect_tx(&full[stage], kWBytes);
+                tma_load_2d(st, &tmW, &full[stage], (kb0 + i) * (BK / 2), tile * BM);
+            }
+            __syncwarp();
+            ++fills[stage];
+            if (++stage == kStages) {
+                stage = 0;
+                phase ^= 1u;
+            }
+        }
+        // every copy lands before the CTA may end
+        for (int i = 0; i < kStages; ++i)
+            if (fills[i] > 0) {
+                (void)mbar_wait(&sf_full[i], (fills[i] - 1u) & 1u, p.wait_ns, p.status, kStatusTimeoutProducer);
+                (void)mbar_wait(&full[i], (fills[i] - 1u) & 1u, p.wait_ns, p.status, kStatusTimeoutProducer);
+            }
+    } else if (warp == 1) {
+        // ------------------------------------------------------------ MMA
+        const uint32_t idesc = mma_desc(kDigits * M);
+        int stage = 0;
+        uint32_t phase = 0;
+        for (int i = 0; i < n; ++i) {
+            const bool ok = mbar_wait(&full[stage], phase, p.wait_ns, p.status, kStatusTimeoutMma);
+            if (!__all_sync(0xffffffffu, ok && s_abort == 0)) {
+                s_abort = 1;
+                break;
+            }
+            tc_fence_after();
+            if (elect_one())
+                multiply<64>(smem_u32(smem) + (uint32_t)stage * P::kStage, tmem + (uint32_t)stage * P::kSfCols, tmem, idesc,
+                             min(4, p.kb4 - (kb0 + i) * 4), i == 0, &empty[stage]);
+            __syncwarp();
+            if (++stage == kStages) {
+                stage = 0;
+                phase ^= 1u;
+            }
+        }
+        // every MMA ends before TMEM is released
+        if (elect_one()) tc_commit(acc_full);
+        __syncwarp();
+        (void)mbar_wait(acc_full, 0u, p.wait_ns, p.status, kStatusTimeoutMma);
+    } else if (warp >= 4 && warp < 8) {
+        // ------------------------------------------------------------ scales into TMEM, a lane quarter per warp
+        int stage = 0;
+        uint32_t phase = 0;
+        for (int i = 0; i < n; ++i) {
+            const bool ok = mbar_wait(&sf_full[stage], phase, p.wait_ns, p.status, kStatusTimeoutMma);
+            if (!__all_sync(0xffffffffu, ok && s_abort == 0)) {
+                s_abort = 1;
+                break;
+            }
+            store_scales<64>(smem_u32(smem) + (uint32_t)stage * P::kStage, tmem + (uint32_t)stage * P::kSfCols,
+                             (uint32_t)(warp & 3), lane);
+            if (lane == 0) mbar_arrive(&full[stage]);
+            if (++stage == kStages) {
+                stage = 0;
+                phase ^= 1u;
+            }
+        }
+    } else if (warp >= 12) {
+        // ------------------------------------------------------------ digits: warp w takes rows w and w + 4
+        const int w = warp - 12, t = threadIdx.x - 12 * 32;
+        const int c0 = kb0 * BK, vecs = ((int)min((long long)(kb0 + n) * BK, p.K) - c0) / 8;
+        for (int m = 0; m < M; ++m) {
+            const uint4* x = reinterpret_cast<const uint4*>(p.x + m * p.K + c0);
+            uint32_t top = 0;
+#pragma unroll 4
+            for (int i = t; i < vecs; i += 128) top = max(top, top_bits(x[i]));
+            top = __reduce_max_sync(0xffffffffu, top);
+            if (lane == 0) tops[4 * m + w] = top;
+        }
+        named_bar_sync(2, 128);
+        int e_row[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int m = w + 4 * h;
+            if (m >= M) continue;
+            e_row[h] = unit_of(max(max(tops[4 * m], tops[4 * m + 1]), max(tops[4 * m + 2], tops[4 * m + 3])));
+            if (lane == 0) factor[m] = row_factor(e_row[h]);
+        }
+        asm volatile("bar.arrive 3, 256;" ::: "memory");   // the factors are there
+        int stage = 0;
+        uint32_t phase = 1;
+        for (int i = 0; i < n; ++i) {
+            const bool ok = mbar_wait(&empty[stage], phase, p.wait_ns, p.status, kStatusTimeoutProducer);
+            if (!__all_sync(0xffffffffu, ok && s_abort == 0)) {
+                s_abort = 1;
+                break;
+            }
+            uint8_t* codes = smem + stage * P::kStage + kWBytes;
+            uint8_t* scales = codes + P::kDBytes + kSfwBytes;
+            const int col = (kb0 + i) * BK + 8 * lane;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int m = w + 4 * h;
+                if (m >= M) continue;
+                uint4 v = make_uint4(0, 0, 0, 0);
+                if (col < p.K) v = *reinterpret_cast<const uint4*>(p.x + m * p.K + col);
+                const Digits o = digits_of(v, e_row[h]);
+                // row 8 m + d of 128 bytes, its 16-byte chunks swizzled by the row in its eight
+#pragma unroll
+                for (int d = 0; d < kDigits; ++d)
+                    *reinterpret_cast<uint32_t*>(codes + (kDigits * m + d) * 128 + (((lane >> 2) ^ d) << 4) + 4 * (lane & 3)) =
+                        o.code[d];
+                const int r = kDigits * m + (lane & 7);
+                *reinterpret_cast<uint32_t*>(scales + (lane >> 3) * 512 + (r & 31) * 16 + (r >> 5) * 4) =
+                    scale_word(o.scale, lane);
+            }
+            fence_proxy_async_smem();   // the codes, for the MMAs
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(&sf_full[stage]);
+                mbar_arrive(&full[stage]);
+            }
+            if (++stage == kStages) {
+                stage = 0;
+                phase ^= 1u;
+            }
+        }
+    } else if (warp >= 8) {
+        // ------------------------------------------------------------ sums to the cluster's first CTA
+        const int quarter = warp & 3, o = 32 * quarter + lane;
+        asm volatile("bar.sync 3, 256;" ::: "memory");
+        const bool ok = mbar_wait(acc_full, 0u, p.wait_ns, p.status, kStatusTimeoutEpilogue);
+        if (!__all_sync(0xffffffffu, ok)) s_abort = 1;
+        tc_fence_after();
+        cluster_wait();   // the first CTA has begun
+        const uint32_t to = mapa_shared(smem_u32(red), 0) + 4u * (uint32_t)(rank * kFewRows * BM + o);
+#pragma unroll
+        for (int m = 0; m < kFewRows; m += 4) {
+            if (m >= M) continue;
+            float y[4];
+            four_rows(tmem + ((32u * (uint32_t)quarter) << 16) + 8 * m, y);
+#pragma unroll
+            for (int h = 0; h < 4; ++h)
+                if (m + h < M)
+                    st_shared_cluster_u32(to + 4u * (uint32_t)((m + h) * BM), __float_as_uint(y[h] * factor[m + h]));
+        }
+    }
+    __syncwarp();
+    if (warp < 8 || warp >= 12) cluster_wait();
+    tc_fence_before();
+    cluster_sync();   // all sums are there (and all warps of this CTA through)
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem, kTmemCols);
+    }
+    if (rank != 0 || warp < 8 || warp >= 12) return;
+    const int o = threadIdx.x - 8 * 32;
+    const float s = *p.j.w_gscale;
+    auto value = [&](int first, long long at, int m) {
+        float y = 0.0f;
+        for (int r = first; r < first + p.split; ++r) y += red[(r * kFewRows + m) * BM + o];
+        const long long nn = at * BM + o;
+        return fmaf(y, s, p.j.bias && nn < p.j.N ? __bfloat162float(p.j.bias[nn]) : 0.0f);
+    };
+    if (p.j.swiglu) {
+        for (int m = 0; m < M; ++m) {
+            const float g = __bfloat162float(__float2bfloat16_rn(value(0, 2ll * group, m)));
+            const float u = __bfloat162float(__float2bfloat16_rn(value(p.split, 2ll * group + 1, m)));
+            p.j.out[m * (p.j.N / 2) + (long long)group * BM + o] = __float2bfloat16_rn(silu_f32(g) * u);
+        }
+        return;
+    }
+    const long long nn = (long long)tile * BM + o;
+    if (nn >= p.j.N) return;
+    for (int m = 0; m < M; ++m) {
+        float v = value(0, tile, m);
+        if (p.j.gate) v = fmaf(p.j.gate[m * p.j.gate_stride + nn], v, __bfloat162float(p.j.resid[m * p.j.N + nn]));
+        p.j.out[m * p.j.N + nn] = __float2bfloat16_rn(v);
+    }
+}
+
+constexpr uint32_t kFewSmem = kFewStages * Plan<64>::kStage + kMaxCluster * kFewRows * BM * 4 + 8 * (3 * kFewStages + 1) + 8 + 4 * kFewRows + 16 * kFewRows;
+static_assert(kFewSmem <= 232448, "shared memory budget");
+
+cudaLaunchConfig_t few_config(unsigned ctas, int cluster, cudaLaunchAttribute (&attr)[2], cudaStream_t s)
+{
+    cudaLaunchConfig_t cfg = {};
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = (unsigned)cluster;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.gridDim = dim3(ctas);
+    cfg.blockDim = dim3(kFewThreads);
+    cfg.dynamicSmemBytes = kFewSmem;
+    cfg.stream = s;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cfg;
+}
+
+// Clusters of `size` CTAs that the current device holds at once (looked up once per device).
+int few_clusters(int size)
+{
+    static std::mutex mu;
+    static int known[64][kMaxCluster + 1] = {};
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
+    std::lock_guard<std::mutex> lock(mu);
+    int& n = known[dev][size];
+    if (n == 0) {
+        cudaLaunchAttribute attr[2];
+        const cudaLaunchConfig_t cfg = few_config((unsigned)size, size, attr, nullptr);
+        if (ensure_dynamic_smem(reinterpret_cast<const void*>(rows_few_kernel), (int)kFewSmem) != cudaSuccess ||
+            cudaOccupancyMaxActiveClusters(&n, rows_few_kernel, &cfg) != cudaSuccess || n <= 0)
+            n = -1;
+    }
+    return n > 0 ? n : 0;
+}
+
+// CTAs per tile of the one-kernel form; 0 where the others take less time.
+int few_split(const LinearRowsJob& job, const Layout& l)
+{
+    if (job.M > kFewRows) return 0;
+    const int ks = (int)((job.K + BK - 1) / BK), tiles_of = job.swiglu ? 2 : 1;
+    const long long groups = l.tiles / tiles_of;
+    int best = 0;
+    for (int split = 1; split * tiles_of <= kMaxCluster && split <= ks; ++split)
+        if (groups <= few_clusters(split * tiles_of)) best = split;
+    if (best == 0) return 0;
+    // A stage takes an SM 0.4 us; the three kernels share the stages evenly but take 3 us more.
+    const double stages = (double)l.tiles * ks / sm_count_current_device();
+    return ((ks + best - 1) / best - stages) * 0.4 < 3.0 ? best : 0;
+}
+
+// The maps of the weights' codes and scales.
+bool weight_maps(const LinearRowsJob& job, const Layout& l, CUtensorMap* codes, CUtensorMap* scales)
+{
+    const uint64_t kbytes = (uint64_t)job.K / 2;
+    return make_map_2d(codes, CU_TENSOR_MAP_DATA_TYPE_UINT8, job.w_codes, kbytes, (uint64_t)job.N, kbytes, BK / 2, BM,
+                       CU_TENSOR_MAP_SWIZZLE_128B) &&
+           make_map_2d(scales, CU_TENSOR_MAP_DATA_TYPE_UINT8, job.w_sf, 256, (uint64_t)(l.tiles * l.kb4 * 2), 256, 256,
+                       kSfBox / 256, CU_TENSOR_MAP_SWIZZLE_NONE);
+}
+
+cudaError_t launch_few(const LinearRowsJob& job, const Layout& l, const JoinParams& jp, int split, cudaStream_t s)
+{
+    CUtensorMap tmW, tmSfw;
+    if (!weight_maps(job, l, &tmW, &tmSfw)) return cudaErrorInvalidValue;
+    const cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void*>(rows_few_kernel), (int)kFewSmem);
+    if (e != cudaSuccess) return e;
+    FewParams p{};
+    p.x = job.x;
+    p.j = jp;
+    p.K = job.K;
+    p.split = split;
+    p.ks = (int)((job.K + BK - 1) / BK);
+    p.kb4 = (int)l.kb4;
+    p.status = reinterpret_cast<unsigned int*>(job.ws);
+    p.wait_ns = job.wait_limit_ns;
+    p.stall = job.stall;
+    cudaLaunchAttribute attr[2];
+    const cudaLaunchConfig_t cfg = few_config((unsigned)(l.tiles * split), job.swiglu ? 2 * split : split, attr, s);
+    return cudaLaunchKernelEx(&cfg, rows_few_kernel, tmW, tmSfw, p);
+}
+
 template <int NB>
 cudaError_t launch_gemm_rows(const LinearRowsJob& job, const Layout& l, const GemmParams& p, unsigned ctas,
                              cudaLaunchConfig_t cfg)
@@ -537,10 +935,7 @@ cudaError_t launch_gemm_rows(const LinearRowsJob& job, const Layout& l, const Ge
     CUtensorMap tmW, tmSfw, tmD, tmSfd;
     const uint64_t kbytes = (uint64_t)job.K / 2;
     const uint64_t d_tiles = (uint64_t)((l.digit_rows + 127) / 128);
-    if (!make_map_2d(&tmW, CU_TENSOR_MAP_DATA_TYPE_UINT8, job.w_codes, kbytes, (uint64_t)job.N, kbytes, BK / 2, BM,
-                     CU_TENSOR_MAP_SWIZZLE_128B) ||
-        !make_map_2d(&tmSfw, CU_TENSOR_MAP_DATA_TYPE_UINT8, job.w_sf, 256, (uint64_t)(l.tiles * l.kb4 * 2), 256, 256,
-                     kSfBox / 256, CU_TENSOR_MAP_SWIZZLE_NONE) ||
+    if (!weight_maps(job, l, &tmW, &tmSfw) ||
         !make_map_2d(&tmD, CU_TENSOR_MAP_DATA_TYPE_UINT8, job.ws + l.codes, kbytes, (uint64_t)l.digit_rows, kbytes, BK / 2,
                      (uint32_t)p.nb, CU_TENSOR_MAP_SWIZZLE_128B) ||
         !make_map_2d(&tmSfd, CU_TENSOR_MAP_DATA_TYPE_UINT8, job.ws + l.scales, 256, d_tiles * (uint64_t)l.kb4 * 2, 256,
@@ -561,6 +956,17 @@ size_t linear_rows_workspace_bytes(int64_t M, int64_t N, int64_t K) { return lay
 cudaError_t launch_linear_rows(const LinearRowsJob& job, cudaStream_t s)
 {
     const Layout l = layout(job.M, job.N, job.K);
+    JoinParams jp{};
+    jp.w_gscale = job.w_gscale;
+    jp.gate = job.gate;
+    jp.gate_stride = job.gate_stride;
+    jp.bias = job.bias;
+    jp.resid = job.resid;
+    jp.out = job.out;
+    jp.N = job.N;
+    jp.swiglu = job.swiglu;
+    jp.M = (int)job.M;
+    if (const int split = few_split(job, l)) return launch_few(job, l, jp, split, s);
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -599,22 +1005,12 @@ cudaError_t launch_linear_rows(const LinearRowsJob& job, cudaStream_t s)
                       : launch_gemm_rows<256>(job, l, p, ctas, cfg);
     if (e != cudaSuccess) return e;
 
-    JoinParams jp{};
     jp.parts = p.parts;
     jp.factors = factors;
-    jp.w_gscale = job.w_gscale;
-    jp.gate = job.gate;
-    jp.gate_stride = job.gate_stride;
-    jp.bias = job.bias;
-    jp.resid = job.resid;
-    jp.out = job.out;
-    jp.N = job.N;
     jp.chunk = p.chunk;
     jp.passes = l.passes;
     jp.ks = p.ks;
     jp.pass_rows = l.pass_rows;
-    jp.swiglu = job.swiglu;
-    jp.M = (int)job.M;
     auto join = [&](void (*kernel)(JoinParams)) {
         const cudaError_t e = ensure_shared_carveout(reinterpret_cast<const void*>(kernel));
         return e == cudaSuccess ? cudaLaunchKernelEx(&cfg, kernel, jp) : e;

@@ -182,21 +182,25 @@ h3fp4_status h3fp4_selftest_linear_rows_timeout(void* ws, uint64_t limit_ns, cud
     if (!aligned16(ws)) return H3FP4_ERR_ALIGN;
     const h3fp4_status st = check_device();
     if (st != H3FP4_OK) return st;
-    // One row of 256 columns and 128 outputs, all data (whatever it is) in the workspace of another size.
-    uint8_t* data = static_cast<uint8_t*>(ws) + linear_rows_workspace_bytes(1, 128, 256);
+    // One and nine rows (the one-kernel and the other form) of 256 columns and 128 outputs, all data (whatever
+    // it is) in the workspace of another size.
+    uint8_t* data = static_cast<uint8_t*>(ws) + linear_rows_workspace_bytes(9, 128, 256);
     LinearRowsJob job{};
     job.x = reinterpret_cast<const __nv_bfloat16*>(data);
     job.w_codes = data;
     job.w_sf = data;
     job.w_gscale = reinterpret_cast<const float*>(data);
     job.out = reinterpret_cast<__nv_bfloat16*>(data + 128 * 128);
-    job.M = 1;
     job.N = 128;
     job.K = 256;
     job.ws = static_cast<uint8_t*>(ws);
     job.wait_limit_ns = limit_ns ? limit_ns : 1;
     job.stall = 1;
-    return launch_linear_rows(job, stream) == cudaSuccess ? H3FP4_OK : H3FP4_ERR_CUDA;
+    for (int rows : {1, 9}) {
+        job.M = rows;
+        if (launch_linear_rows(job, stream) != cudaSuccess) return H3FP4_ERR_CUDA;
+    }
+    return H3FP4_OK;
 }
 
 size_t h3fp4_cache_page_bytes(int heads, int dim, int page)

@@ -75,6 +75,13 @@ CASES = [  # M, N, K, bias, gate ("rows", "one" or None), swiglu
     (64, 1024, 1024, True, "rows", False),
     (64, 3072, 12288, True, "one", False),
     (5, 40000, 64, True, None, False),
+    (4, 1024, 8192, True, "rows", False),                             # eight CTAs a tile, four stages each
+    (8, 9216, 4096, False, None, False),                              # more stages than the ring has
+    (6, 512, 14336, True, None, True),                                # gate and up tiles of four CTAs each
+    (8, 128, 65536, False, "one", False),
+    (2, 24, 1856, True, None, False),
+    (3, 20480, 3072, True, "rows", False),                            # more tiles than a wave: the other form
+    (1, 57344, 512, True, None, True),
 ]
 
 

@@ -150,7 +150,7 @@ def test_linear_rows_python_checks(lib):
     assert lib.h3fp4_selftest_linear_rows_timeout(None, 1, None) == INVALID
     assert lib.h3fp4_selftest_linear_rows_timeout(C.c_void_p(4104), 1, None) == ALIGN
     assert (A.h3fp4_linear_rows_workspace_bytes(64, 128, 1024)
-            >= A.h3fp4_linear_rows_workspace_bytes(1, 128, 256) + 128 * 128 + 1024)   # what the self-test lays out
+            >= A.h3fp4_linear_rows_workspace_bytes(9, 128, 256) + 128 * 128 + 9 * 256)   # what the self-test lays out
     assert A.ROWS_MAX == 64 and A.h3fp4_linear_rows_workspace_bytes(1, 8, 64) >= 256
     for bad in ((65, 8, 64), (0, 8, 64), (1, 4, 64), (1, 8, 32)):
         assert A.h3fp4_linear_rows_workspace_bytes(*bad) == 0
