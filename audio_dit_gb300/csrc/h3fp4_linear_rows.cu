@@ -128,33 +128,34 @@ __device__ __forceinline__ Digits digits_of(const uint4& v, int e_row)
     o.scale = k >= -6 ? (uint32_t)(k + 7) << 3 : 1u << (k + 9);
     const int e = below - e_row;   // what x is scaled with: two factors, as the sum may pass 127
     const float up0 = pow2i(e / 2), up1 = pow2i(e - e / 2);
-    float r[8];
+    // What is left, in f16 pairs: below 4 with eight significant bits it is exact (elements below 2^-16 of the
+    // block's largest to 2^-25 of the unit), and so is every difference.
+    uint32_t r[4];
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        r[2 * i] = bf16_lo(w[i]) * up0 * up1;
-        r[2 * i + 1] = bf16_hi(w[i]) * up0 * up1;
-    }
+    for (int i = 0; i < 4; ++i)
+        asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r[i]) : "f"(bf16_hi(w[i]) * up0 * up1), "f"(bf16_lo(w[i]) * up0 * up1));
 #pragma unroll
     for (int d = 0; d < kDigits; ++d) {
-        o.code[d] = e2m1x8(r);
         uint32_t q[4];
         asm("{\n\t.reg .b8 a, b, c, d;\n\t"
-            "mov.b32 {a, b, c, d}, %4;\n\t"
-            "cvt.rn.f16x2.e2m1x2 %0, a;\n\t"
-            "cvt.rn.f16x2.e2m1x2 %1, b;\n\t"
-            "cvt.rn.f16x2.e2m1x2 %2, c;\n\t"
-            "cvt.rn.f16x2.e2m1x2 %3, d;\n\t}"
-            : "=r"(q[0]), "=r"(q[1]), "=r"(q[2]), "=r"(q[3])
-            : "r"(o.code[d]));
+            "cvt.rn.satfinite.e2m1x2.f16x2 a, %5;\n\t"
+            "cvt.rn.satfinite.e2m1x2.f16x2 b, %6;\n\t"
+            "cvt.rn.satfinite.e2m1x2.f16x2 c, %7;\n\t"
+            "cvt.rn.satfinite.e2m1x2.f16x2 d, %8;\n\t"
+            "mov.b32 %0, {a, b, c, d};\n\t"
+            "cvt.rn.f16x2.e2m1x2 %1, a;\n\t"
+            "cvt.rn.f16x2.e2m1x2 %2, b;\n\t"
+            "cvt.rn.f16x2.e2m1x2 %3, c;\n\t"
+            "cvt.rn.f16x2.e2m1x2 %4, d;\n\t}"
+            : "=r"(o.code[d]), "=r"(q[0]), "=r"(q[1]), "=r"(q[2]), "=r"(q[3])
+            : "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]));
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            float lo, hi;
-            asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\tcvt.f32.f16 %0, l;\n\tcvt.f32.f16 %1, h;\n\t}"
-                : "=f"(lo), "=f"(hi)
-                : "r"(q[i]));
-            r[2 * i] = (r[2 * i] - lo) * 8.0f;   // (exact)
-            r[2 * i + 1] = (r[2 * i + 1] - hi) * 8.0f;
+            constexpr uint32_t k8 = 0x48004800u, kMinus8 = 0xC800C800u;   // 8 and -8, twice
+            uint32_t r8;
+            asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r8) : "r"(r[i]), "r"(k8));
+            asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r[i]) : "r"(q[i]), "r"(kMinus8), "r"(r8));
         }
     }
     return o;
@@ -240,9 +241,41 @@ __device__ __forceinline__ void store_scales(uint32_t stage_smem, uint32_t tmem,
     tc_st_32x32b_x16(t, va);
 #pragma unroll
     for (int h = 0; h < P::kHalves; ++h) tc_st_32x32b_x16(t + 16 + 16 * h, vb[h]);
-    tc_wait_st();
-    tc_fence_before();
-    __syncwarp();
+}
+
+// The scale warps' role over n stages.  Stages that are there already go together: their stores are waited
+// for once (one takes 0.3 us by itself).
+template <int NB, int kStages>
+__device__ __forceinline__ void scales_role(uint32_t smem, uint32_t tmem, uint64_t* sf_full, uint64_t* full, int n,
+                                            uint32_t quarter, int lane, unsigned long long wait_ns, unsigned int* status,
+                                            volatile int& s_abort)
+{
+    using P = Plan<NB>;
+    constexpr int kTogether = 3;
+    int stage = 0;
+    uint32_t phase = 0;
+    for (int i = 0; i < n;) {
+        const bool ok = mbar_wait(&sf_full[stage], phase, wait_ns, status, kStatusTimeoutMma);
+        if (!__all_sync(0xffffffffu, ok && s_abort == 0)) {
+            s_abort = 1;
+            return;
+        }
+        const int first = stage;
+        int together = 0;
+        do {
+            store_scales<NB>(smem + (uint32_t)stage * P::kStage, tmem + (uint32_t)stage * P::kSfCols, quarter, lane);
+            ++together;
+            if (++stage == kStages) {
+                stage = 0;
+                phase ^= 1u;
+            }
+        } while (together < kTogether && i + together < n && __all_sync(0xffffffffu, mbar_test(&sf_full[stage], phase)));
+        i += together;
+        tc_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane < together) mbar_arrive(&full[first + lane < kStages ? first + lane : first + lane - kStages]);
+    }
 }
 
 // The MMAs of a stage and the release of its slot, by one lane.
@@ -442,22 +475,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         (void)mbar_wait(done_bar, 0u, p.wait_ns, p.status, kStatusTimeoutMma);
     } else if (warp >= 4 && warp < 8) {
         // ------------------------------------------------------------ scales into TMEM, a lane quarter per warp
-        const uint32_t quarter = (uint32_t)(warp & 3);
-        int stage = 0;
-        uint32_t phase = 0;
-        for (int i = 0; i < todo; ++i) {
-            const bool ok = mbar_wait(&sf_full[stage], phase, p.wait_ns, p.status, kStatusTimeoutMma);
-            if (!__all_sync(0xffffffffu, ok && s_abort == 0)) {
-                s_abort = 1;
-                break;
-            }
-            store_scales<NB>(smem_u32(smem) + (uint32_t)stage * P::kStage, tmem + (uint32_t)stage * P::kSfCols, quarter, lane);
-            if (lane == 0) mbar_arrive(&full[stage]);
-            if (++stage == kStages) {
-                stage = 0;
-                phase ^= 1u;
-            }
-        }
+        scales_role<NB, kStages>(smem_u32(smem), tmem, sf_full, full, todo, (uint32_t)(warp & 3), lane, p.wait_ns, p.status,
+                                 s_abort);
     } else if (warp >= 8) {
         // ------------------------------------------------------------ a unit's sums: digits together, to the workspace
         const int quarter = warp & 3, n = 32 * quarter + lane;
@@ -590,10 +609,15 @@ __global__ void __launch_bounds__(BM) rows_join_kernel(const __grid_constant__ J
 // takes one: each makes the digits of its own columns of x (under an exponent of its own) beside the other
 // roles, multiplies, and adds its sums to those of the others in the first one's shared memory, which
 // finishes the outputs.
-constexpr int kFewRows = 8;
-constexpr int kFewThreads = 512;     // as above, and four warps of digits
+constexpr int kFewThreads = 512;     // producer, MMA, 2 idle; 4 scale warps; 8 warps of digits, 4 of them of outputs
 constexpr int kMaxCluster = 8;
+
+constexpr int kFewRows = 8;
 constexpr int kFewStages = 6;
+constexpr uint32_t kFewRedOff = kFewStages * Plan<64>::kStage;
+constexpr uint32_t kFewBarOff = kFewRedOff + kMaxCluster * kFewRows * BM * 4;
+constexpr uint32_t kFewSmem = kFewBarOff + 8 * (3 * kFewStages + 1) + 8 + 4 * 8;
+static_assert(kFewSmem <= 232448, "shared memory budget");
 
 struct FewParams {
     const __nv_bfloat16* x;
@@ -611,27 +635,26 @@ __global__ void __launch_bounds__(kFewThreads, 1)
     extern __shared__ __align__(1024) uint8_t smem[];
     using P = Plan<64>;
     constexpr int kStages = kFewStages;
-    constexpr uint32_t kRedOff = kStages * P::kStage, kBarOff = kRedOff + kMaxCluster * kFewRows * BM * 4;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if ((smem_u32(smem) & 1023u) != 0) {   // (the same in every CTA)
         if (threadIdx.x == 0) atomicOr(p.status, kStatusBadSmemAlign);
         return;
     }
-    float* red = reinterpret_cast<float*>(smem + kRedOff);            // the first CTA's: [rank][row][output]
-    uint64_t* full = reinterpret_cast<uint64_t*>(smem + kBarOff);     // codes landed, digits and scales stored
+    float* red = reinterpret_cast<float*>(smem + kFewRedOff);            // the first CTA's: [rank][row][output]
+    uint64_t* full = reinterpret_cast<uint64_t*>(smem + kFewBarOff);     // codes landed, digits and scales stored
     uint64_t* empty = full + kStages;
     uint64_t* sf_full = empty + kStages;                              // scale tiles landed and written
     uint64_t* acc_full = sf_full + kStages;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(acc_full + 1);
     volatile int& s_abort = *reinterpret_cast<volatile int*>(tmem_slot + 1);
-    float* factor = reinterpret_cast<float*>(tmem_slot + 2);          // per row
-    uint32_t* tops = reinterpret_cast<uint32_t*>(factor + kFewRows);  // per row and digit warp
+    uint32_t* tops = tmem_slot + 2;   // per warp of digits: the largest that it read
+    const int M = p.j.M, row_warps = M > 4 ? 8 : M > 2 ? 4 : M;   // warps of digits per stage
     if (threadIdx.x == 0) {
         s_abort = 0;
         for (int i = 0; i < kStages; ++i) {
-            mbar_init(&full[i], 1 + 4 + 4);
+            mbar_init(&full[i], 1 + 4 + row_warps);   // W, the scale warps, those of digits
             mbar_init(&empty[i], 1);
-            mbar_init(&sf_full[i], 1 + 4);
+            mbar_init(&sf_full[i], 1 + row_warps);
         }
         mbar_init(acc_full, 1);
         fence_mbarrier_init();
@@ -647,7 +670,6 @@ __global__ void __launch_bounds__(kFewThreads, 1)
     tc_fence_after();
     cluster_arrive();   // (waited for before anything is written to the first CTA)
     const uint32_t tmem = *tmem_slot;
-    const int M = p.j.M;
     const int rank = (int)cluster_ctarank(), size = p.j.swiglu ? 2 * p.split : p.split;
     const int group = blockIdx.x / size, part = rank % p.split;
     const int tile = p.j.swiglu ? 2 * group + rank / p.split : group;
@@ -713,90 +735,113 @@ __global__ void __launch_bounds__(kFewThreads, 1)
         (void)mbar_wait(acc_full, 0u, p.wait_ns, p.status, kStatusTimeoutMma);
     } else if (warp >= 4 && warp < 8) {
         // ------------------------------------------------------------ scales into TMEM, a lane quarter per warp
-        int stage = 0;
-        uint32_t phase = 0;
-        for (int i = 0; i < n; ++i) {
-            const bool ok = mbar_wait(&sf_full[stage], phase, p.wait_ns, p.status, kStatusTimeoutMma);
-            if (!__all_sync(0xffffffffu, ok && s_abort == 0)) {
-                s_abort = 1;
-                break;
-            }
-            store_scales<64>(smem_u32(smem) + (uint32_t)stage * P::kStage, tmem + (uint32_t)stage * P::kSfCols,
-                             (uint32_t)(warp & 3), lane);
-            if (lane == 0) mbar_arrive(&full[stage]);
-            if (++stage == kStages) {
-                stage = 0;
-                phase ^= 1u;
-            }
-        }
-    } else if (warp >= 12) {
-        // ------------------------------------------------------------ digits: warp w takes rows w and w + 4
-        const int w = warp - 12, t = threadIdx.x - 12 * 32;
-        const int c0 = kb0 * BK, vecs = ((int)min((long long)(kb0 + n) * BK, p.K) - c0) / 8;
-        for (int m = 0; m < M; ++m) {
-            const uint4* x = reinterpret_cast<const uint4*>(p.x + m * p.K + c0);
-            uint32_t top = 0;
+        scales_role<64, kStages>(smem_u32(smem), tmem, sf_full, full, n, (uint32_t)(warp & 3), lane, p.wait_ns, p.status,
+                                 s_abort);
+    } else if (warp >= 8) {
+        // ------------------------------------------------------------ digits: warp w takes row w % row_warps in some of
+        // the ring's slots.  A slot is always the same warp's: a parity tells a phase only from its neighbours, so
+        // whoever waits for a slot has to have waited for its fill before (dealt out by stages, warps took a slot
+        // whose last but one fill was still in use for free).  What it reads for the row's largest it keeps.
+        constexpr int kKept = 8;
+        const int w = warp - 8, m = w % row_warps, every = 8 / row_warps;
+        const int slot0 = w / row_warps;   // its slots: slot0, slot0 + every, ...
+        auto after = [&](int i) {          // the stage of its that follows stage i of its (n or more: none)
+            const int slot = i % kStages;
+            return slot + every < kStages ? i + every : i - slot + kStages + slot0;
+        };
+        const long long c0 = (long long)kb0 * BK + 8 * lane;
+        auto read = [&](int i) {
+            uint4 v = make_uint4(0, 0, 0, 0);
+            if (m < M && i < n && c0 + (long long)i * BK < p.K)
+                v = *reinterpret_cast<const uint4*>(p.x + m * p.K + c0 + i * BK);
+            return v;
+        };
+        int at[kKept + 1];   // its first stages
+        at[0] = slot0 < kStages ? slot0 : n;
+#pragma unroll
+        for (int k = 0; k < kKept; ++k) at[k + 1] = at[k] < n ? after(at[k]) : n;
+        uint4 kept[kKept];
+        uint32_t top = 0;
+#pragma unroll
+        for (int k = 0; k < kKept; ++k) kept[k] = read(at[k]);
+#pragma unroll
+        for (int k = 0; k < kKept; ++k) top = max(top, top_bits(kept[k]));
 #pragma unroll 4
-            for (int i = t; i < vecs; i += 128) top = max(top, top_bits(x[i]));
-            top = __reduce_max_sync(0xffffffffu, top);
-            if (lane == 0) tops[4 * m + w] = top;
-        }
-        named_bar_sync(2, 128);
-        int e_row[2];
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const int m = w + 4 * h;
-            if (m >= M) continue;
-            e_row[h] = unit_of(max(max(tops[4 * m], tops[4 * m + 1]), max(tops[4 * m + 2], tops[4 * m + 3])));
-            if (lane == 0) factor[m] = row_factor(e_row[h]);
-        }
-        asm volatile("bar.arrive 3, 256;" ::: "memory");   // the factors are there
-        int stage = 0;
-        uint32_t phase = 1;
-        for (int i = 0; i < n; ++i) {
-            const bool ok = mbar_wait(&empty[stage], phase, p.wait_ns, p.status, kStatusTimeoutProducer);
+        for (int i = at[kKept]; i < n; i = after(i)) top = max(top, top_bits(read(i)));
+        top = __reduce_max_sync(0xffffffffu, top);
+        if (lane == 0) tops[w] = top;
+        named_bar_sync(2, 256);
+        for (int k = m; k < 8; k += row_warps) top = max(top, tops[k]);
+        const int e_row = unit_of(top);
+        auto put = [&](int i, const uint4& v) {
+            const int stage = i % kStages;
+            const bool ok = mbar_wait(&empty[stage], (uint32_t)(i / kStages & 1) ^ 1u, p.wait_ns, p.status,
+                                      kStatusTimeoutProducer);
             if (!__all_sync(0xffffffffu, ok && s_abort == 0)) {
                 s_abort = 1;
-                break;
+                return false;
             }
-            uint8_t* codes = smem + stage * P::kStage + kWBytes;
-            uint8_t* scales = codes + P::kDBytes + kSfwBytes;
-            const int col = (kb0 + i) * BK + 8 * lane;
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const int m = w + 4 * h;
-                if (m >= M) continue;
-                uint4 v = make_uint4(0, 0, 0, 0);
-                if (col < p.K) v = *reinterpret_cast<const uint4*>(p.x + m * p.K + col);
-                const Digits o = digits_of(v, e_row[h]);
+            if (m < M) {
+                uint8_t* codes = smem + stage * P::kStage + kWBytes;
+                uint8_t* scales = codes + P::kDBytes + kSfwBytes;
+                const Digits o = digits_of(v, e_row);
                 // row 8 m + d of 128 bytes, its 16-byte chunks swizzled by the row in its eight
 #pragma unroll
                 for (int d = 0; d < kDigits; ++d)
                     *reinterpret_cast<uint32_t*>(codes + (kDigits * m + d) * 128 + (((lane >> 2) ^ d) << 4) + 4 * (lane & 3)) =
                         o.code[d];
-                const int r = kDigits * m + (lane & 7);
-                *reinterpret_cast<uint32_t*>(scales + (lane >> 3) * 512 + (r & 31) * 16 + (r >> 5) * 4) =
+                const int row = kDigits * m + (lane & 7);
+                *reinterpret_cast<uint32_t*>(scales + (lane >> 3) * 512 + (row & 31) * 16 + (row >> 5) * 4) =
                     scale_word(o.scale, lane);
+                fence_proxy_async_smem();   // the codes, for the MMAs
             }
-            fence_proxy_async_smem();   // the codes, for the MMAs
             __syncwarp();
             if (lane == 0) {
                 mbar_arrive(&sf_full[stage]);
                 mbar_arrive(&full[stage]);
             }
-            if (++stage == kStages) {
-                stage = 0;
-                phase ^= 1u;
-            }
+            return true;
+        };
+        bool on = true;
+#pragma unroll
+        for (int k = 0; k < kKept; ++k)
+            if (on && at[k] < n) on = put(at[k], kept[k]);
+        uint4 next = read(at[kKept]);
+        for (int i = at[kKept]; on && i < n;) {
+            const int then = after(i);
+            const uint4 v = next;
+            next = read(then);
+            on = put(i, v);
+            i = then;
         }
-    } else if (warp >= 8) {
+    }
+    // what the first CTA's last four warps need for the outputs
+    const int o = (int)threadIdx.x - 12 * 32;
+    const long long out0 = (p.j.swiglu ? 2ll * group : (long long)tile) * BM + o;   // the first tile's row of W
+    float s = 0.0f, bias[2] = {0.0f, 0.0f}, gate[kFewRows], resid[kFewRows];
+    if (warp >= 12) {
         // ------------------------------------------------------------ sums to the cluster's first CTA
-        const int quarter = warp & 3, o = 32 * quarter + lane;
-        asm volatile("bar.sync 3, 256;" ::: "memory");
+        const int quarter = warp & 3;
+        if (rank == 0) {
+            s = *p.j.w_gscale;
+            if (p.j.bias && out0 < p.j.N) bias[0] = __bfloat162float(p.j.bias[out0]);
+            if (p.j.bias && p.j.swiglu) bias[1] = __bfloat162float(p.j.bias[out0 + BM]);
+#pragma unroll
+            for (int m = 0; m < kFewRows; ++m)
+                if (p.j.gate && m < M && out0 < p.j.N) {
+                    gate[m] = p.j.gate[m * p.j.gate_stride + out0];
+                    resid[m] = __bfloat162float(p.j.resid[m * p.j.N + out0]);
+                }
+        }
         const bool ok = mbar_wait(acc_full, 0u, p.wait_ns, p.status, kStatusTimeoutEpilogue);
         if (!__all_sync(0xffffffffu, ok)) s_abort = 1;
         tc_fence_after();
         cluster_wait();   // the first CTA has begun
+        auto factor = [&](int row) {   // (the barrier of the digits was behind what the warps read)
+            uint32_t top = 0;
+            for (int k = row; k < 8; k += row_warps) top = max(top, tops[k]);
+            return row_factor(unit_of(top));
+        };
         const uint32_t to = mapa_shared(smem_u32(red), 0) + 4u * (uint32_t)(rank * kFewRows * BM + o);
 #pragma unroll
         for (int m = 0; m < kFewRows; m += 4) {
@@ -806,45 +851,37 @@ __global__ void __launch_bounds__(kFewThreads, 1)
 #pragma unroll
             for (int h = 0; h < 4; ++h)
                 if (m + h < M)
-                    st_shared_cluster_u32(to + 4u * (uint32_t)((m + h) * BM), __float_as_uint(y[h] * factor[m + h]));
+                    st_shared_cluster_u32(to + 4u * (uint32_t)((m + h) * BM), __float_as_uint(y[h] * factor(m + h)));
         }
     }
     __syncwarp();
-    if (warp < 8 || warp >= 12) cluster_wait();
+    if (warp < 12) cluster_wait();
     tc_fence_before();
     cluster_sync();   // all sums are there (and all warps of this CTA through)
     if (warp == 1) {
         tc_fence_after();
         tmem_dealloc(tmem, kTmemCols);
     }
-    if (rank != 0 || warp < 8 || warp >= 12) return;
-    const int o = threadIdx.x - 8 * 32;
-    const float s = *p.j.w_gscale;
-    auto value = [&](int first, long long at, int m) {
+    if (rank != 0 || warp < 12 || out0 >= p.j.N) return;
+    auto value = [&](int first, int m, float b) {
         float y = 0.0f;
         for (int r = first; r < first + p.split; ++r) y += red[(r * kFewRows + m) * BM + o];
-        const long long nn = at * BM + o;
-        return fmaf(y, s, p.j.bias && nn < p.j.N ? __bfloat162float(p.j.bias[nn]) : 0.0f);
+        return fmaf(y, s, b);
     };
-    if (p.j.swiglu) {
-        for (int m = 0; m < M; ++m) {
-            const float g = __bfloat162float(__float2bfloat16_rn(value(0, 2ll * group, m)));
-            const float u = __bfloat162float(__float2bfloat16_rn(value(p.split, 2ll * group + 1, m)));
+#pragma unroll
+    for (int m = 0; m < kFewRows; ++m) {
+        if (m >= M) break;
+        float v = value(0, m, bias[0]);
+        if (p.j.swiglu) {
+            const float g = __bfloat162float(__float2bfloat16_rn(v));
+            const float u = __bfloat162float(__float2bfloat16_rn(value(p.split, m, bias[1])));
             p.j.out[m * (p.j.N / 2) + (long long)group * BM + o] = __float2bfloat16_rn(silu_f32(g) * u);
+        } else {
+            if (p.j.gate) v = fmaf(gate[m], v, resid[m]);
+            p.j.out[m * p.j.N + out0] = __float2bfloat16_rn(v);
         }
-        return;
-    }
-    const long long nn = (long long)tile * BM + o;
-    if (nn >= p.j.N) return;
-    for (int m = 0; m < M; ++m) {
-        float v = value(0, tile, m);
-        if (p.j.gate) v = fmaf(p.j.gate[m * p.j.gate_stride + nn], v, __bfloat162float(p.j.resid[m * p.j.N + nn]));
-        p.j.out[m * p.j.N + nn] = __float2bfloat16_rn(v);
     }
 }
-
-constexpr uint32_t kFewSmem = kFewStages * Plan<64>::kStage + kMaxCluster * kFewRows * BM * 4 + 8 * (3 * kFewStages + 1) + 8 + 4 * kFewRows + 16 * kFewRows;
-static_assert(kFewSmem <= 232448, "shared memory budget");
 
 cudaLaunchConfig_t few_config(unsigned ctas, int cluster, cudaLaunchAttribute (&attr)[2], cudaStream_t s)
 {
@@ -892,9 +929,10 @@ int few_split(const LinearRowsJob& job, const Layout& l)
     for (int split = 1; split * tiles_of <= kMaxCluster && split <= ks; ++split)
         if (groups <= few_clusters(split * tiles_of)) best = split;
     if (best == 0) return 0;
-    // A stage takes an SM 0.4 us; the three kernels share the stages evenly but take 3 us more.
-    const double stages = (double)l.tiles * ks / sm_count_current_device();
-    return ((ks + best - 1) / best - stages) * 0.4 < 3.0 ? best : 0;
+    // A stage takes an SM 0.4 us (0.75 with eight rows, whose digits every CTA makes for itself); the three kernels
+    // share the stages evenly but take 3 us more.
+    const double stages = (double)l.tiles * ks / sm_count_current_device(), stage = job.M <= 4 ? 0.4 : 0.75;
+    return (ks + best - 1) / best * stage < stages * 0.4 + 3.0 ? best : 0;
 }
 
 // The maps of the weights' codes and scales.

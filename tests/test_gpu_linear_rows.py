@@ -82,6 +82,15 @@ CASES = [  # M, N, K, bias, gate ("rows", "one" or None), swiglu
     (2, 24, 1856, True, None, False),
     (3, 20480, 3072, True, "rows", False),                            # more tiles than a wave: the other form
     (1, 57344, 512, True, None, True),
+    (16, 6144, 4096, True, "rows", False),
+    (13, 1024, 14336, False, None, True),
+    (9, 3000, 1984, True, "one", False),
+    (12, 256, 65536, False, None, False),
+    (1, 4096, 14336, True, None, False),                              # few rows, rings that are filled again and again
+    (2, 4096, 14336, False, "rows", False),
+    (3, 128, 65536, True, None, False),
+    (1, 128, 65536, False, None, False),
+    (2, 256, 65536, True, None, True),
 ]
 
 
