@@ -180,8 +180,16 @@ __global__ void __launch_bounds__(kDigitThreads)
     griddep_wait();
     griddep_launch_dependents();   // the weights may be fetched: nothing before this call writes them any more
     uint32_t top = 0;
-#pragma unroll 8
-    for (int i = t; i < K / 8; i += kDigitThreads) top = max(top, top_bits(reinterpret_cast<const uint4*>(row)[i]));
+    for (int i = t; i < K / 8; i += 4 * kDigitThreads) {
+        uint4 v[4];   // in flight together (one after another they took 4 us of 14336 columns)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const int at = i + k * kDigitThreads;
+            v[k] = at < K / 8 ? reinterpret_cast<const uint4*>(row)[at] : make_uint4(0, 0, 0, 0);
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) top = max(top, top_bits(v[k]));
+    }
     top = __reduce_max_sync(0xffffffffu, top);
     if (lane == 0) tops[t >> 5] = top;
     __syncthreads();
@@ -556,40 +564,55 @@ __global__ void __launch_bounds__(BM) rows_join_kernel(const __grid_constant__ J
     griddep_wait();
     griddep_launch_dependents();
     const float s = *p.w_gscale;
-    // the sums of a tile's output i, of all rows
-    auto sums = [&](long long tile, float (&y)[kRows]) {
-        float bias = 0.0f;
-        if (p.bias && tile * BM + i < p.N) bias = __bfloat162float(p.bias[tile * BM + i]);
-        const long long u = tile * p.passes + pass, first = u * p.ks;
-        // (below 2^32 stages for all sizes that are taken)
-        const int c0 = (uint32_t)first / (uint32_t)p.chunk, c1 = (uint32_t)(first + p.ks - 1) / (uint32_t)p.chunk;
-        const float* at = p.parts + ((u + c0) * p.pass_rows + mm) * BM + i;
+    // the sums of output i of kTiles tiles, of all rows
+    auto sums = [&](long long tile, auto& y) {
+        constexpr int kTiles = sizeof(y) / sizeof(y[0]);
+        float bias[kTiles];
+        const float* at[kTiles];
+        int left[kTiles], most = 0;
 #pragma unroll
-        for (int k = 0; k < kRows; ++k) y[k] = 0.0f;
-#pragma unroll(kRows > 1 ? 2 : 8)
-        for (int c = c0; c <= c1; ++c, at += (long long)p.pass_rows * BM)
+        for (int t = 0; t < kTiles; ++t) {
+            const long long u = (tile + t) * p.passes + pass, first = u * p.ks;
+            // (below 2^32 stages for all sizes that are taken)
+            const int c0 = (uint32_t)first / (uint32_t)p.chunk, c1 = (uint32_t)(first + p.ks - 1) / (uint32_t)p.chunk;
+            left[t] = c1 - c0 + 1;
+            most = max(most, left[t]);
+            at[t] = p.parts + ((u + c0) * p.pass_rows + mm) * BM + i;
+            const long long n = (tile + t) * BM + i;
+            bias[t] = p.bias && n < p.N ? __bfloat162float(p.bias[n]) : 0.0f;
 #pragma unroll
-            for (int k = 0; k < kRows; ++k)
-                if (k < rows) y[k] += at[k * BM];
+            for (int k = 0; k < kRows; ++k) y[t][k] = 0.0f;
+        }
+        const long long step = (long long)p.pass_rows * BM;
+#pragma unroll(kRows > 1 ? 2 : 4)
+        for (int c = 0; c < most; ++c)
 #pragma unroll
-        for (int k = 0; k < kRows; ++k)
-            if (k < rows) y[k] = fmaf(y[k] * s, p.factors[m0 + k], bias);
+            for (int t = 0; t < kTiles; ++t)
+#pragma unroll
+                for (int k = 0; k < kRows; ++k)
+                    if (k < rows && c < left[t]) y[t][k] += at[t][c * step + k * BM];
+#pragma unroll
+        for (int k = 0; k < kRows; ++k) {
+            if (k >= rows) continue;
+            const float f = p.factors[m0 + k];
+#pragma unroll
+            for (int t = 0; t < kTiles; ++t) y[t][k] = fmaf(y[t][k] * s, f, bias[t]);
+        }
     };
-    float y[kRows];
     if (p.swiglu) {
-        float u[kRows];
+        float y[2][kRows];
         sums(2ll * blockIdx.x, y);
-        sums(2ll * blockIdx.x + 1, u);
 #pragma unroll
         for (int k = 0; k < kRows; ++k)
             if (k < rows)
-                p.out[(m0 + k) * (p.N / 2) + (long long)blockIdx.x * BM + i] = __float2bfloat16_rn(
-                    silu_f32(__bfloat162float(__float2bfloat16_rn(y[k]))) * __bfloat162float(__float2bfloat16_rn(u[k])));
+                p.out[(m0 + k) * (p.N / 2) + (long long)blockIdx.x * BM + i] =
+                    __float2bfloat16_rn(silu_f32(__bfloat162float(__float2bfloat16_rn(y[0][k]))) *
+                                        __bfloat162float(__float2bfloat16_rn(y[1][k])));
         return;
     }
     const long long n = (long long)blockIdx.x * BM + i;
     if (n >= p.N) return;
-    float g[kRows], r[kRows];
+    float g[kRows], r[kRows], y[1][kRows];
 #pragma unroll
     for (int k = 0; k < kRows; ++k)
         if (p.gate && k < rows) {
@@ -599,10 +622,10 @@ __global__ void __launch_bounds__(BM) rows_join_kernel(const __grid_constant__ J
     sums(blockIdx.x, y);
 #pragma unroll
     for (int k = 0; k < kRows; ++k)
-        if (k < rows) p.out[(m0 + k) * p.N + n] = __float2bfloat16_rn(p.gate ? fmaf(g[k], y[k], r[k]) : y[k]);
+        if (k < rows) p.out[(m0 + k) * p.N + n] = __float2bfloat16_rn(p.gate ? fmaf(g[k], y[0][k], r[k]) : y[0][k]);
 }
 
-// ------------------------------------------------------------------ up to eight rows, in one kernel
+// ------------------------------------------------------------------ up to four rows, in one kernel
 //
 // A launch, its start and the wait for the one before cost what a small weight's reading does.  So where a
 // wave of CTAs has all tiles, a cluster of `split` CTAs (with SwiGLU twice as many: the gate and the up tile)
@@ -612,9 +635,10 @@ __global__ void __launch_bounds__(BM) rows_join_kernel(const __grid_constant__ J
 constexpr int kFewThreads = 512;     // producer, MMA, 2 idle; 4 scale warps; 8 warps of digits, 4 of them of outputs
 constexpr int kMaxCluster = 8;
 
-constexpr int kFewRows = 8;
-constexpr int kFewStages = 6;
-constexpr uint32_t kFewRedOff = kFewStages * Plan<64>::kStage;
+constexpr int kFewRows = 4;
+constexpr int kFewStages = 8;
+using FewPlan = Plan<kDigits * kFewRows>;
+constexpr uint32_t kFewRedOff = kFewStages * FewPlan::kStage;
 constexpr uint32_t kFewBarOff = kFewRedOff + kMaxCluster * kFewRows * BM * 4;
 constexpr uint32_t kFewSmem = kFewBarOff + 8 * (3 * kFewStages + 1) + 8 + 4 * 8;
 static_assert(kFewSmem <= 232448, "shared memory budget");
@@ -633,7 +657,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
     rows_few_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmSfw, const FewParams p)
 {
     extern __shared__ __align__(1024) uint8_t smem[];
-    using P = Plan<64>;
+    using P = FewPlan;
     constexpr int kStages = kFewStages;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if ((smem_u32(smem) & 1023u) != 0) {   // (the same in every CTA)
@@ -648,7 +672,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(acc_full + 1);
     volatile int& s_abort = *reinterpret_cast<volatile int*>(tmem_slot + 1);
     uint32_t* tops = tmem_slot + 2;   // per warp of digits: the largest that it read
-    const int M = p.j.M, row_warps = M > 4 ? 8 : M > 2 ? 4 : M;   // warps of digits per stage
+    const int M = p.j.M, row_warps = M > 2 ? 4 : M;   // warps of digits per stage
     if (threadIdx.x == 0) {
         s_abort = 0;
         for (int i = 0; i < kStages; ++i) {
@@ -721,8 +745,8 @@ __global__ void __launch_bounds__(kFewThreads, 1)
             }
             tc_fence_after();
             if (elect_one())
-                multiply<64>(smem_u32(smem) + (uint32_t)stage * P::kStage, tmem + (uint32_t)stage * P::kSfCols, tmem, idesc,
-                             min(4, p.kb4 - (kb0 + i) * 4), i == 0, &empty[stage]);
+                multiply<kDigits * kFewRows>(smem_u32(smem) + (uint32_t)stage * P::kStage, tmem + (uint32_t)stage * P::kSfCols,
+                                             tmem, idesc, min(4, p.kb4 - (kb0 + i) * 4), i == 0, &empty[stage]);
             __syncwarp();
             if (++stage == kStages) {
                 stage = 0;
@@ -735,20 +759,17 @@ __global__ void __launch_bounds__(kFewThreads, 1)
         (void)mbar_wait(acc_full, 0u, p.wait_ns, p.status, kStatusTimeoutMma);
     } else if (warp >= 4 && warp < 8) {
         // ------------------------------------------------------------ scales into TMEM, a lane quarter per warp
-        scales_role<64, kStages>(smem_u32(smem), tmem, sf_full, full, n, (uint32_t)(warp & 3), lane, p.wait_ns, p.status,
-                                 s_abort);
+        scales_role<kDigits * kFewRows, kStages>(smem_u32(smem), tmem, sf_full, full, n, (uint32_t)(warp & 3), lane, p.wait_ns,
+                                                 p.status, s_abort);
     } else if (warp >= 8) {
-        // ------------------------------------------------------------ digits: warp w takes row w % row_warps in some of
-        // the ring's slots.  A slot is always the same warp's: a parity tells a phase only from its neighbours, so
-        // whoever waits for a slot has to have waited for its fill before (dealt out by stages, warps took a slot
-        // whose last but one fill was still in use for free).  What it reads for the row's largest it keeps.
+        // ------------------------------------------------------------ digits: warp w takes row w % row_warps of every
+        // eighth, fourth or second stage.  A slot of the ring is always the same warp's: a parity tells a phase only
+        // from its neighbours, so whoever waits for a slot has to have waited for its fill before (with six stages
+        // warps took a slot whose last but one fill was still in use for free).  What it reads for the row's
+        // largest it keeps.
+        static_assert(kStages % 8 == 0, "a slot is one warp's");
         constexpr int kKept = 8;
-        const int w = warp - 8, m = w % row_warps, every = 8 / row_warps;
-        const int slot0 = w / row_warps;   // its slots: slot0, slot0 + every, ...
-        auto after = [&](int i) {          // the stage of its that follows stage i of its (n or more: none)
-            const int slot = i % kStages;
-            return slot + every < kStages ? i + every : i - slot + kStages + slot0;
-        };
+        const int w = warp - 8, m = w % row_warps, every = 8 / row_warps, i0 = w / row_warps;
         const long long c0 = (long long)kb0 * BK + 8 * lane;
         auto read = [&](int i) {
             uint4 v = make_uint4(0, 0, 0, 0);
@@ -756,18 +777,14 @@ __global__ void __launch_bounds__(kFewThreads, 1)
                 v = *reinterpret_cast<const uint4*>(p.x + m * p.K + c0 + i * BK);
             return v;
         };
-        int at[kKept + 1];   // its first stages
-        at[0] = slot0 < kStages ? slot0 : n;
-#pragma unroll
-        for (int k = 0; k < kKept; ++k) at[k + 1] = at[k] < n ? after(at[k]) : n;
         uint4 kept[kKept];
         uint32_t top = 0;
 #pragma unroll
-        for (int k = 0; k < kKept; ++k) kept[k] = read(at[k]);
+        for (int k = 0; k < kKept; ++k) kept[k] = read(i0 + k * every);
 #pragma unroll
         for (int k = 0; k < kKept; ++k) top = max(top, top_bits(kept[k]));
 #pragma unroll 4
-        for (int i = at[kKept]; i < n; i = after(i)) top = max(top, top_bits(read(i)));
+        for (int i = i0 + kKept * every; i < n; i += every) top = max(top, top_bits(read(i)));
         top = __reduce_max_sync(0xffffffffu, top);
         if (lane == 0) tops[w] = top;
         named_bar_sync(2, 256);
@@ -805,14 +822,12 @@ __global__ void __launch_bounds__(kFewThreads, 1)
         bool on = true;
 #pragma unroll
         for (int k = 0; k < kKept; ++k)
-            if (on && at[k] < n) on = put(at[k], kept[k]);
-        uint4 next = read(at[kKept]);
-        for (int i = at[kKept]; on && i < n;) {
-            const int then = after(i);
-            const uint4 v = next;
-            next = read(then);
+            if (on && i0 + k * every < n) on = put(i0 + k * every, kept[k]);
+        int i = i0 + kKept * every;
+        for (uint4 v = read(i); on && i < n; i += every) {
+            const uint4 next = read(i + every);
             on = put(i, v);
-            i = then;
+            v = next;
         }
     }
     // what the first CTA's last four warps need for the outputs
@@ -843,16 +858,12 @@ __global__ void __launch_bounds__(kFewThreads, 1)
             return row_factor(unit_of(top));
         };
         const uint32_t to = mapa_shared(smem_u32(red), 0) + 4u * (uint32_t)(rank * kFewRows * BM + o);
+        static_assert(kFewRows == 4, "all sums at once");
+        float y[4];
+        four_rows(tmem + ((32u * (uint32_t)quarter) << 16), y);
 #pragma unroll
-        for (int m = 0; m < kFewRows; m += 4) {
-            if (m >= M) continue;
-            float y[4];
-            four_rows(tmem + ((32u * (uint32_t)quarter) << 16) + 8 * m, y);
-#pragma unroll
-            for (int h = 0; h < 4; ++h)
-                if (m + h < M)
-                    st_shared_cluster_u32(to + 4u * (uint32_t)((m + h) * BM), __float_as_uint(y[h] * factor(m + h)));
-        }
+        for (int m = 0; m < 4; ++m)
+            if (m < M) st_shared_cluster_u32(to + 4u * (uint32_t)(m * BM), __float_as_uint(y[m] * factor(m)));
     }
     __syncwarp();
     if (warp < 12) cluster_wait();
@@ -929,10 +940,12 @@ int few_split(const LinearRowsJob& job, const Layout& l)
     for (int split = 1; split * tiles_of <= kMaxCluster && split <= ks; ++split)
         if (groups <= few_clusters(split * tiles_of)) best = split;
     if (best == 0) return 0;
-    // A stage takes an SM 0.4 us (0.75 with eight rows, whose digits every CTA makes for itself); the three kernels
-    // share the stages evenly but take 3 us more.
-    const double stages = (double)l.tiles * ks / sm_count_current_device(), stage = job.M <= 4 ? 0.4 : 0.75;
-    return (ks + best - 1) / best * stage < stages * 0.4 + 3.0 ? best : 0;
+    // A stage takes an SM 0.4 us; the three kernels share the stages evenly but take 3 us more.  (Measured, one row:
+    // 9216 x 3072 6.6 us against 8.4, 4096 x 14336 9.2 against 12.2, 2048 x 2048 4.8 against 6.0; 512 x 65536, whose
+    // tiles would keep 64 SMs, 13.1 us with three kernels.  Of eight rows' digits each CTA has too many to make:
+    // 9216 x 3072 9.0 us against 9.2, 4096 x 14336 15.2 against 12.5.)
+    const double stages = (double)l.tiles * ks / sm_count_current_device();
+    return (ks + best - 1) / best * 0.4 < stages * 0.4 + 3.0 ? best : 0;
 }
 
 // The maps of the weights' codes and scales.

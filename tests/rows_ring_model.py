@@ -13,10 +13,9 @@ __all__ = ["failures"]
 
 
 class Model:
-    def __init__(self, rng, rows, n, stages, together, by_slot=True):
+    def __init__(self, rng, rows, n, stages, together):
         self.rng, self.n, self.stages, self.together = rng, n, stages, together
-        self.row_warps = 8 if rows > 4 else 4 if rows > 2 else rows
-        self.by_slot = by_slot
+        self.row_warps = 4 if rows > 2 else rows
         self.full = [Bar(1 + 4 + self.row_warps, f"full {i}") for i in range(stages)]
         self.sf_full = [Bar(1 + self.row_warps, f"sf_full {i}") for i in range(stages)]
         self.empty = [Bar(1, f"empty {i}") for i in range(stages)]
@@ -28,15 +27,7 @@ class Model:
         self.time, self.events = 0.0, []
 
     def owned(self, warp):
-        every, mine = 8 // self.row_warps, warp // self.row_warps
-        if not self.by_slot:
-            return list(range(mine, self.n, every))
-        got, i = [], mine if mine < self.stages else self.n
-        while i < self.n:                                                # (as the kernel goes on)
-            got.append(i)
-            slot = i % self.stages
-            i = i + every if slot + every < self.stages else i - slot + self.stages + mine
-        return got
+        return range(warp // self.row_warps, self.n, 8 // self.row_warps)
 
     def slow(self):
         return self.rng.choice([0.1, 1.0, 1.0, 5.0, 40.0]) * self.rng.random()
@@ -146,13 +137,13 @@ class Model:
         need(self.done == self.n, "stages left over")
 
 
-def failures(runs, stages, together, by_slot=True, seed=1):
+def failures(runs, stages, together, seed=1):
     """What went wrong in so many runs of random rows and stages: {message: count}."""
     rng, found = random.Random(seed), {}
     for _ in range(runs):
-        rows = rng.choice((1, 2, 3, 5, 8))
+        rows = rng.choice((1, 2, 3, 4))
         try:
-            Model(rng, rows, rng.choice([1, 2, 5, 7, 13, 24, 40]), stages, together, by_slot).run()
+            Model(rng, rows, rng.choice([1, 2, 5, 7, 13, 24, 40]), stages, together).run()
         except Broken as e:
             found[str(e.args[0])] = found.get(str(e.args[0]), 0) + 1
     return found

@@ -91,6 +91,11 @@ CASES = [  # M, N, K, bias, gate ("rows", "one" or None), swiglu
     (3, 128, 65536, True, None, False),
     (1, 128, 65536, False, None, False),
     (2, 256, 65536, True, None, True),
+    (1, 24576, 2560, False, "rows", False),                           # few rows, several tiles a CTA
+    (2, 24576, 2112, True, None, True),
+    (3, 40960, 1088, True, "one", False),
+    (4, 49000, 64, True, None, False),
+    (4, 28672, 1984, True, None, True),
 ]
 
 

@@ -1,5 +1,5 @@
 """The barriers of the one-kernel linear of a few rows, as modelled in rows_ring_model.py (CPU): no role goes on too early
-and none waits for ever; with digits dealt out by stages instead of slots the model fails."""
+and none waits for ever; with a ring whose slots go from warp to warp the model fails."""
 import os
 import re
 
@@ -14,8 +14,8 @@ def kernel():
     text = open(os.path.join(ROOT, "audio_dit_gb300", "csrc", "h3fp4_linear_rows.cu")).read()
     stages = int(re.search(r"kFewStages = (\d);", text).group(1))
     together = int(re.search(r"kTogether = (\d);", text).group(1))
-    assert "slot + every < kStages ? i + every : i - slot + kStages + slot0" in text and "slot0 = w / row_warps" in text
-    assert "M > 4 ? 8 : M > 2 ? 4 : M" in text
+    assert "every = 8 / row_warps, i0 = w / row_warps" in text
+    assert "row_warps = M > 2 ? 4 : M;" in text
     assert "1 + 4 + row_warps" in text and "mbar_init(&sf_full[i], 1 + row_warps)" in text
     return stages, together
 
@@ -24,6 +24,6 @@ def test_the_kernels_waits():
     assert failures(RUNS, *kernel()) == {}
 
 
-def test_digits_by_stages_are_not_enough():
-    """A warp that skips fills of a slot takes one that is in use for free: seen as a launch failure."""
-    assert failures(RUNS, *kernel(), by_slot=False) != {}
+def test_slots_have_to_be_one_warps():
+    """A warp that skips fills of a slot takes one that is in use for free: seen as a launch failure with six stages."""
+    assert failures(RUNS, 6, kernel()[1]) != {}
