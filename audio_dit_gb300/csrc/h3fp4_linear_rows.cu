@@ -561,47 +561,57 @@ __global__ void __launch_bounds__(BM) rows_join_kernel(const __grid_constant__ J
     const int pass = blockIdx.y / groups, mm = (blockIdx.y - pass * groups) * kRows, m0 = pass * p.pass_rows + mm;
     const int rows = min(kRows, min(p.pass_rows - mm, p.M - m0));
     if (rows <= 0) return;
-    griddep_wait();
-    griddep_launch_dependents();
+    // What no kernel of this call writes is read ahead of the wait: what wrote it has ended (the digits kernel waited
+    // for that, and this one starts behind its start).
     const float s = *p.w_gscale;
-    // the sums of output i of kTiles tiles, of all rows
-    auto sums = [&](long long tile, auto& y) {
-        constexpr int kTiles = sizeof(y) / sizeof(y[0]);
-        float bias[kTiles];
-        const float* at[kTiles];
-        int left[kTiles], most = 0;
+    const long long tile = p.swiglu ? 2ll * blockIdx.x : blockIdx.x;
+    auto at = [&](long long t, int& pieces) {   // output i's sums of a tile
+        const long long u = t * p.passes + pass, first = u * p.ks;
+        // (below 2^32 stages for all sizes that are taken)
+        const int c0 = (uint32_t)first / (uint32_t)p.chunk, c1 = (uint32_t)(first + p.ks - 1) / (uint32_t)p.chunk;
+        pieces = c1 - c0 + 1;
+        return p.parts + ((u + c0) * p.pass_rows + mm) * BM + i;
+    };
+    const long long n = tile * BM + i, step = (long long)p.pass_rows * BM;
+    if (n >= p.N) return;
+    float bias[2], g[kRows], r[kRows], f[kRows];
+    bias[0] = p.bias ? __bfloat162float(p.bias[n]) : 0.0f;
+    bias[1] = p.bias && p.swiglu ? __bfloat162float(p.bias[n + BM]) : 0.0f;
 #pragma unroll
-        for (int t = 0; t < kTiles; ++t) {
-            const long long u = (tile + t) * p.passes + pass, first = u * p.ks;
-            // (below 2^32 stages for all sizes that are taken)
-            const int c0 = (uint32_t)first / (uint32_t)p.chunk, c1 = (uint32_t)(first + p.ks - 1) / (uint32_t)p.chunk;
-            left[t] = c1 - c0 + 1;
-            most = max(most, left[t]);
-            at[t] = p.parts + ((u + c0) * p.pass_rows + mm) * BM + i;
-            const long long n = (tile + t) * BM + i;
-            bias[t] = p.bias && n < p.N ? __bfloat162float(p.bias[n]) : 0.0f;
+    for (int k = 0; k < kRows; ++k)
+        if (p.gate && k < rows) {
+            g[k] = p.gate[(m0 + k) * p.gate_stride + n];
+            r[k] = __bfloat162float(p.resid[(m0 + k) * p.N + n]);
+        }
+    int left[2] = {0, 0};
+    const float* from[2] = {at(tile, left[0]), nullptr};
+    if (p.swiglu) from[1] = at(tile + 1, left[1]);
+    const int most = max(left[0], left[1]);
+    griddep_wait();
+    griddep_launch_dependents();   // (behind the wait: a next call's first kernels took SMs from this one's products)
+#pragma unroll
+    for (int k = 0; k < kRows; ++k) f[k] = k < rows ? p.factors[m0 + k] : 0.0f;
+    auto sums = [&](auto& y) {
+        constexpr int kTiles = sizeof(y) / sizeof(y[0]);
+#pragma unroll
+        for (int t = 0; t < kTiles; ++t)
 #pragma unroll
             for (int k = 0; k < kRows; ++k) y[t][k] = 0.0f;
-        }
-        const long long step = (long long)p.pass_rows * BM;
 #pragma unroll(kRows > 1 ? 2 : 4)
         for (int c = 0; c < most; ++c)
 #pragma unroll
             for (int t = 0; t < kTiles; ++t)
 #pragma unroll
                 for (int k = 0; k < kRows; ++k)
-                    if (k < rows && c < left[t]) y[t][k] += at[t][c * step + k * BM];
+                    if (k < rows && c < left[t]) y[t][k] += from[t][c * step + k * BM];
 #pragma unroll
-        for (int k = 0; k < kRows; ++k) {
-            if (k >= rows) continue;
-            const float f = p.factors[m0 + k];
+        for (int t = 0; t < kTiles; ++t)
 #pragma unroll
-            for (int t = 0; t < kTiles; ++t) y[t][k] = fmaf(y[t][k] * s, f, bias[t]);
-        }
+            for (int k = 0; k < kRows; ++k) y[t][k] = fmaf(y[t][k] * s, f[k], bias[t]);
     };
     if (p.swiglu) {
         float y[2][kRows];
-        sums(2ll * blockIdx.x, y);
+        sums(y);
 #pragma unroll
         for (int k = 0; k < kRows; ++k)
             if (k < rows)
@@ -610,16 +620,8 @@ __global__ void __launch_bounds__(BM) rows_join_kernel(const __grid_constant__ J
                                         __bfloat162float(__float2bfloat16_rn(y[1][k])));
         return;
     }
-    const long long n = (long long)blockIdx.x * BM + i;
-    if (n >= p.N) return;
-    float g[kRows], r[kRows], y[1][kRows];
-#pragma unroll
-    for (int k = 0; k < kRows; ++k)
-        if (p.gate && k < rows) {
-            g[k] = p.gate[(m0 + k) * p.gate_stride + n];
-            r[k] = __bfloat162float(p.resid[(m0 + k) * p.N + n]);
-        }
-    sums(blockIdx.x, y);
+    float y[1][kRows];
+    sums(y);
 #pragma unroll
     for (int k = 0; k < kRows; ++k)
         if (k < rows) p.out[(m0 + k) * p.N + n] = __float2bfloat16_rn(p.gate ? fmaf(g[k], y[0][k], r[k]) : y[0][k]);
