@@ -96,6 +96,10 @@ CASES = [  # M, N, K, bias, gate ("rows", "one" or None), swiglu
     (3, 40960, 1088, True, "one", False),
     (4, 49000, 64, True, None, False),
     (4, 28672, 1984, True, None, True),
+    (64, 128, 256, True, "rows", False),                              # the most rows, one tile
+    (40, 40000, 192, False, "one", False),                            # several tiles a CTA, two passes
+    (21, 24320, 320, True, None, True),
+    (32, 3080, 4160, True, "rows", False),
 ]
 
 
