@@ -208,6 +208,24 @@ __device__ __forceinline__ long long div(long long a, long long b)
     return a / b;
 }
 
+// How the tiles of a call are cut over its CTAs: shares that differ by one at most (shares of the rounded-up mean
+// left CTAs idle: one token over 131072 keys 37.3 -> 35.0 us), none empty but where there are fewer tiles.
+struct Shares {
+    long long total;
+    int ctas;
+
+    // CTA b's first tile
+    __device__ __forceinline__ long long start(int b) const
+    {
+        return total < ctas ? min(total, (long long)b) : div(total * b, ctas);
+    }
+    // the CTA that has tile x: the last one that starts at x or before
+    __device__ __forceinline__ int owner(long long x) const
+    {
+        return total < ctas ? (int)x : (int)div((x + 1) * ctas + total - 1, total) - 1;
+    }
+};
+
 // 2^x for an integer x in the normal range.
 __device__ __forceinline__ float pow2i(int x) { return __uint_as_float((uint32_t)(x + 127) << 23); }
 
@@ -516,8 +534,8 @@ __global__ void __launch_bounds__(kThreads, Config<W, kCols>::kCtasPerSm)
         __syncthreads();
     }
     const long long total = prefix[nseq];
-    const long long chunk = max(1ll, div(total + gridDim.x - 1, gridDim.x));
-    const long long begin = min(total, chunk * blockIdx.x), end = min(total, begin + chunk);
+    const Shares shares{total, (int)gridDim.x};
+    const long long begin = shares.start(blockIdx.x), end = shares.start(blockIdx.x + 1);
 
     // rows of sequences that hold nothing
     for (int s = blockIdx.x; s < nseq; s += gridDim.x) {
@@ -787,7 +805,7 @@ __global__ void __launch_bounds__(kThreads, Config<W, kCols>::kCtasPerSm)
                 }
             }
             if (lane == 0 && at == ubegin && (p.by_unit || !whole)) {
-                const int count = whole ? 0 : (int)(div(uend - 1, chunk) - blockIdx.x + 1);
+                const int count = whole ? 0 : shares.owner(uend - 1) - (int)blockIdx.x + 1;
                 const long long i = p.by_unit ? units_before(s) + unit : blockIdx.x;
                 // (row offsets that overlap make more units than there can be)
                 if (i < kMaxCtas) cuts[i] = Cut{q.first, h, ct * kCols, cols, (int)blockIdx.x, count};
