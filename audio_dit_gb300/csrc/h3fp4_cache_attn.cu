@@ -9,17 +9,27 @@
 // matrix products, about 1 instruction in all; the 47 G (token, head) pairs a second that HBM
 // delivers at heads of 128 leave 1.5.
 //
-// A unit of work is (sequence, kv head, 16 columns); its keys come in tiles of 64, four warps
-// taking a group of 16 each.  All units' tiles are one row of work that is cut evenly over the
-// CTAs, from the lengths on the device: the same launch serves any lengths, so it can be
-// captured.  Every warp has a ring of groups that bulk copies fill, its own running maximum,
+// A unit of work is (sequence, kv head, 8 or 16 columns); its keys come in tiles of 128, four
+// warps taking 32 each.  All units' tiles are one row of work that is cut evenly over the CTAs,
+// from the lengths on the device: the same launch serves any lengths, so it can be captured.
+// Every warp has a ring of steps of 32 tokens that bulk copies fill, its own running maximum,
 // sum and output; the four are joined at a unit's end.  A unit that was cut leaves partial sums
 // in the workspace, which a second kernel joins.  All orders are fixed: the same call gives
 // the same bits.
 //
-// S = Q K^T: m16n8k16 with the columns as rows of A and the tokens as columns of B; what a lane
-// unpacks of a token is its B fragment.  O = P V: P stays where S was (the accumulator layout
-// is A's, or a transposition away from B's), V's bytes hold two tokens as its fragment does.
+// Measured, calls back to back over three caches, of the measured 6793 GB/s: 64 tokens of 64
+// sequences over 524288 keys, 32 heads on 8 of 128, 113 us (5340 GB/s; the products, scores and
+// unpacking of two thirds of the issue slots beside the loads), one token over 131072 keys
+// 34.9 us (4330 GB/s: 3 us until the first keys are there, 4 us for the second kernel), 31 rows
+// of 6 sequences over 4433 keys, 28 heads on 4 of 64, 14.1 us (launches and latencies; the
+// bytes take 0.2).  Two CTAs of eight warps in place of four of four take 121 us for the first,
+// three CTAs an SM 117; shares by the order in which an SM's CTAs issue (the first ended at 86,
+// the last at 101 us) change nothing, as the bytes come no faster.
+//
+// S = Q K^T: m16n8k16; with 16 columns they are the rows of A and the tokens the columns of B,
+// with 8 the tokens are A's rows: what a lane unpacks of a token is its fragment either way.
+// O = P V: P stays where S was (the accumulator layout is A's, or a transposition away from
+// B's), V's bytes hold two tokens as its fragment does.
 // Q is scaled per column by a power of two to f16's range (exact for elements within 2^31 of
 // the column's largest).  The reference of the exponent follows the true maximum only when
 // that passed it by 2^14: p lies in f16's upper range, and those below 2^-30 of the largest

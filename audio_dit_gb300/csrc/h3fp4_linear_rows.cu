@@ -11,17 +11,36 @@
 // e_b the exponent of x's block of 16.  Up to 4, E2M1's steps are at most 1, so what is left
 // shrinks by 8 each time: eight digits are exact for elements within 2^-16 of their block's
 // largest and within 2^-23 of it otherwise.  All digits of a block share its scale
-// 2^(e_b - e_row + 8), a power of two that E4M3 holds for 17 binades; e_row is the row's.  The
-// matrix unit multiplies 8 M <= 256 digit rows by each W tile in the time that the tile takes
-// to arrive (M = 32: 128 of 199 cycles); more than 32 rows take two passes over the tile, the
-// second from L2.  The products and the sums of 16 are exact, the accumulators fp32.
+// 2^(e_b - e_row + 8), a power of two that E4M3 holds for 17 binades (blocks further below are
+// held to 2^-40 of the row's largest); e_row is the row's.  The matrix unit multiplies 8 M <=
+// 256 digit rows by each W tile in the time that the tile takes to arrive (M = 32: 128 of 199
+// cycles); more than 32 rows take two passes over the tile, the second from L2.  The products
+// and the sums of 16 are exact, the accumulators fp32.
 //
-// Three kernels: digits_kernel writes the digits, their scales and the rows' factors;
+// Two forms, by size (few_split).  One kernel, up to four rows where a wave of CTAs has all
+// tiles of W: rows_few_kernel, digits beside the products, a tile's CTAs joined in a cluster.
+// Else three: digits_kernel writes the digits, their scales and the rows' factors;
 // rows_gemm_kernel multiplies.  Its work is one row of (W tile, pass, 256-column K stage), cut
 // evenly over one CTA per SM, and the sums of each (tile, CTA) piece go to the workspace;
-// rows_join_kernel adds the pieces of a tile in order and finishes the outputs.  The same call
-// gives the same bits.  Each starts while the one before it drains; the first W tiles are on
-// their way before the digits are there.
+// rows_join_kernel adds the pieces of a tile in order and finishes the outputs.  Each starts
+// while the one before it drains; the first W tiles are on their way before the digits are
+// there.  The same call gives the same bits.
+//
+// Measured, calls back to back over three sets of weights, of the measured 6793 GB/s:
+//     rows  W               us     GB/s     bound by
+//        1  9216 x 3072     6.4    2500     a launch, its start, one load's latency and the join (4.7 us of 2048 x 2048)
+//        1  4096 x 14336    8.8    3760     the same, and the clusters' uneven stages
+//        1  57344 x 8192    47.2   5600     HBM, and 3 kernels' ends (about 6 us)
+//       16  4096 x 14336    12.5   2660     digits and joining, 7 us of them
+//       16  57344 x 8192    50.9   5190     HBM
+//       32  57344 x 8192    61.1   4330     a stage's way through the ring of four: 54 KB, of them 32 KB digits
+//       64  57344 x 8192    108    2440     the same, two passes
+// What was built and measured and is not here: whoever brings a tile's last piece joins it, in
+// place of the third kernel (16 rows of 4096 x 14336 20 us against 13: few threads have all the
+// pieces to read); the digits of one row beside the products of the three-kernel form (gains
+// nothing once a row's loads were in flight together); pairs of CTAs that share the digits of
+// more than 16 rows (64 rows of 57344 x 8192 101 us, but 61 rows of 6152 x 4160 13.8 against
+// 13.4 and 4096 x 4096 12.2 against 11.2).
 #include <cstdint>
 #include <mutex>
 

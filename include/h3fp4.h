@@ -48,8 +48,8 @@
  *   - All calls are asynchronous on `stream`; the return value reports host
  *     validation and launch errors only.  Device-side wait timeouts are
  *     recorded in the workspace status word; read them with h3fp4_check().
- *   - Shapes: K % 64 == 0, N % 8 == 0, rows >= 1 (the norm and attention calls
- *     state their own); 16-byte aligned pointers
+ *   - Shapes: K % 64 == 0, N % 8 == 0, rows >= 1 (the norm, attention, cache
+ *     and few-row calls state their own); 16-byte aligned pointers
  *     (codes, sf, bf16 tensors, workspace); violations return
  *     H3FP4_ERR_SHAPE / H3FP4_ERR_ALIGN and launch nothing.
  *   - Only sm_103 devices are accepted (H3FP4_ERR_UNSUPPORTED_DEVICE
@@ -67,8 +67,8 @@
  *     another number of SMs they are right, but cut for 152 (fewer SMs run the
  *     last CTAs alone, more stay idle).  Results do not depend on timing: the same
  *     call gives the same bits.
- *   - Calls issue only kernel launches and (with H3FP4_EPI_AMAX) one memset
- *     on `stream`, so a fixed sequence of calls can be captured into a CUDA
+ *   - Calls issue only kernel launches and (with H3FP4_EPI_AMAX or out_amax)
+ *     one memset on `stream`, so a fixed sequence of calls can be captured into a CUDA
  *     graph.  Make one eager call per device before the first capture: it
  *     performs the library's one-time per-device setup (kernel attributes,
  *     occupancy queries).
@@ -474,7 +474,8 @@ H3FP4_API h3fp4_status h3fp4_block_norm(const void* x_bf16, const void* y_bf16, 
  * h3fp4_linear, with the activations as they are instead of quantised
  *     out = bf16(R + g * (s_w * (x . W_q^T) + b))  or  bf16(s_w * (x . W_q^T) + b)
  * ("H3 Blackwell Runtime" README, "Checkpoints": pre-quantised weights).  Sums are fp32; x
- * enters with an error of at most 2^-22 of the largest magnitude of its block of 16.
+ * enters with an error of at most 2^-22 of the largest magnitude of its block of 16, or 2^-40
+ * of its row's.
  *   x: bf16 [M][K], finite, 1 <= M <= H3FP4_ROWS_MAX; K % 64 == 0, K <= 2^16; N % 8 == 0,
  *      N <= 2^24.
  *   w_codes, w_sf, w_gscale: output of h3fp4_quantize_weight.
@@ -539,8 +540,8 @@ H3FP4_API size_t h3fp4_cache_page_bytes(int heads, int dim, int page);
  * places in the cache, quantised as h3fp4_quantize_act does with H3FP4_GSCALE_GIVEN
  * and the head's global scale ("H3 Runtime Current State", "Owned Performance
  * Kernels": tensor scale/QDATA; the pages have no cache).  Inputs must be finite.
- * The places of a call's rows must differ, and sequences of one call must not write to
- * the same page.  0 <= M <= 2^31 - 256. */
+ * The places of a call's rows must differ, and neither sequences of one call nor calls
+ * that run at the same time may write to the same page.  0 <= M <= 2^31 - 256. */
 H3FP4_API h3fp4_status h3fp4_cache_append(const h3fp4_heads* k, const h3fp4_heads* v, int64_t M,
                                           const h3fp4_cache* cache, cudaStream_t stream);
 
