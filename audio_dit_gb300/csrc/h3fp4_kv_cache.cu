@@ -1,9 +1,13 @@
 // Rows into the 4-bit cache and back.
 //
-//     S = e4m3(max |x| / 6 / s),  q = e2m1(x / (S s))     per 16 elements of a head
+//     S = e4m3(max |x| (1/6) / s),  q = e2m1(x / (S s))   per 16 elements of a head
 //     x' = bf16(q S s)                                     on the way back
 //
-// with the quantiser's own arithmetic (nvfp4_encode.cuh), s the head's global scale.
+// s the head's global scale, each step one rounding to fp32.  As the activations' quantiser
+// (nvfp4_encode.cuh) but for the sixth, which is a product with RN(1/6) as in the elementary
+// form of this format, where that one divides: the two are one step of fp32 apart at most, and
+// their codes differ only where that step crosses a tie of E4M3 (a head whose global scale is
+// 1.25 x 1.75 2^k / 2688 has 1.5 % of such blocks, other mantissas none).
 // Memory-bound: 4 bytes of bf16 per pair of K and V elements and 9/8 of the cache.
 // A warp takes a run of rows.  Measured, 8 heads of 128: 16384 rows in 25 us (3450 GB/s: the
 // loads' latency beside 55 % of the issue slots; loading ahead needs registers that take the
@@ -70,7 +74,7 @@ __device__ __forceinline__ uint32_t encode(const V16& v, float s, uint32_t (&w)[
     float top = 0.0f;
 #pragma unroll
     for (int k = 0; k < 16; ++k) top = fmaxf(top, fabsf(f[k]));
-    const uint32_t S = block_scale_code(top, s);
+    const uint32_t S = cvt_e4m3(__fdiv_rn(__fmul_rn(top, 1.0f / 6.0f), s));
     const float rcp = block_rcp(S, s);
 #pragma unroll
     for (int k = 0; k < 16; ++k) f[k] = __fmul_rn(f[k], rcp);

@@ -538,7 +538,7 @@ H3FP4_API size_t h3fp4_cache_page_bytes(int heads, int dim, int page);
 
 /* Writes the rows k, v [M][heads][dim] (views as for the attention calls) to their
  * places in the cache, quantised as h3fp4_quantize_act does with H3FP4_GSCALE_GIVEN
- * and the head's global scale ("H3 Runtime Current State", "Owned Performance
+ * and the head's global scale, but with bmax * RN(1/6) for bmax / 6 ("H3 Runtime Current State", "Owned Performance
  * Kernels": tensor scale/QDATA; the pages have no cache).  Inputs must be finite.
  * The places of a call's rows must differ, and neither sequences of one call nor calls
  * that run at the same time may write to the same page.  0 <= M <= 2^31 - 256. */

@@ -46,10 +46,10 @@ _E2M1 = torch.tensor([0.0, 0.5, 1.0, 1.5, 2.0, 3.0, 4.0, 6.0], dtype=torch.float
 
 def held(x, gscale):
     """float64 [..., H, D] of what bf16 rows are held as: blocks of 16 under the heads' global scales (fp32 [H]), each
-    step of the format one fp32 operation, and the bf16 that comes back."""
+    step of the format one fp32 operation (a sixth is a product with the rounded 1/6), and the bf16 that comes back."""
     s = gscale[:, None]
     b = x.float().unflatten(-1, (-1, 16))
-    S = (b.abs().amax(-1) / 6.0 / s).clamp(max=448.0).to(torch.float8_e4m3fn).float()
+    S = (b.abs().amax(-1) * torch.tensor(1.0 / 6.0) / s).clamp(max=448.0).to(torch.float8_e4m3fn).float()
     eff = S * s
     r = torch.where(eff == 0, torch.zeros_like(eff), (1.0 / eff).clamp(max=torch.finfo(torch.float32).max))
     q = (b * r[..., None]).double()

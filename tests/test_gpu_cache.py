@@ -79,6 +79,29 @@ def test_rows_in_and_out(before, rows, heads, D, page):
     assert torch.equal(bits(back[:, heads:]), bits(ko.t[last])) and torch.equal(bits(back[:, :heads]), bits(vo.t[last]))
 
 
+def test_scales_at_ties():
+    """Block maxima of every bf16 mantissa under global scales that put some of them on ties of E4M3."""
+    import audio_dit_gb300 as A
+    tops = torch.tensor([m * 2.0 ** (e - 7) for e in range(-6, 1) for m in range(128, 256)])
+    rows = torch.stack([tops * f for f in (1.0, -0.75, 0.5, 0.25) * 4], -1).bfloat16()
+    k = rows[:, None].expand(-1, 2, -1).contiguous()
+    s = torch.tensor([1.75, 1.5]) * torch.tensor(1.0 / 2688.0) * 1.25
+    want = T.held(k, s)[1]
+    old = k.float().abs().amax(-1) / 6.0 / s
+    new = k.float().abs().amax(-1) * torch.tensor(1.0 / 6.0) / s
+    assert int((old.to(torch.float8_e4m3fn).float() != new.to(torch.float8_e4m3fn).float()).sum()) > 0
+    n = len(rows)
+    cache = A.alloc_kv_cache(n // 16, 2, 16, 16)
+    table = torch.arange(n // 16, dtype=torch.int32, device="cuda")[None]
+    length, off = torch.tensor([n], dtype=torch.int32, device="cuda"), torch.tensor([0, n], dtype=torch.int32, device="cuda")
+    g = dict(k_gscale=s.cuda(), v_gscale=s.flip(0).cuda())
+    A.h3fp4_cache_append(k.cuda(), k.cuda(), cache, table, length, off, **g)
+    ko, vo = (torch.empty(n, 2, 16, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    A.h3fp4_cache_read(ko, vo, cache, table, length, off, **g)
+    assert torch.equal(bits(ko.cpu()), bits(want))
+    assert torch.equal(bits(vo.cpu()), bits(T.held(k, s.flip(0))[1]))
+
+
 def test_rows_without_a_place():
     import audio_dit_gb300 as A
     rng = np.random.default_rng(1)
