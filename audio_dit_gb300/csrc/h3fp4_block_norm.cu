@@ -204,7 +204,8 @@ __global__ void __launch_bounds__(kRow < 128 ? 128 : kRow, kRow == 32 && kVec ==
                 for (int j = 0; j < 8; ++j) f[i][j] += w[j];
             }
             const uint4 o = pack_bf8(f[i]);
-            if (mine) *reinterpret_cast<uint4*>(p.out + row + 8 * v) = o;
+            if (!mine) continue;   // (in place: the row may have been written by now)
+            *reinterpret_cast<uint4*>(p.out + row + 8 * v) = o;
             if (p.amax) {
                 // magnitudes of bf16 values in the order of their bits (a NaN is above all)
                 const uint32_t words[4] = {o.x, o.y, o.z, o.w};

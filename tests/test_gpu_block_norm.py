@@ -143,6 +143,19 @@ def test_no_rows_large_means_and_nan():
         assert bool(out[[0, 1, 2, 4]].isfinite().all()) and bool(amax.isnan()) == (eps == 0)
 
 
+def test_largest_of_rows_in_place():
+    """Rows that do not fill a block, in place: r = y - x here, and y - r is x, whose norm has a far larger element."""
+    import audio_dit_gb300 as A
+    for M, K in ((1, 64), (3, 64), (17, 64), (5, 128), (9, 256), (2, 512)):
+        x0 = torch.zeros(M, K, dtype=torch.bfloat16, device="cuda")
+        x0[:, 3] = 1
+        y, out, amax = torch.ones_like(x0), torch.empty_like(x0), torch.empty(1, device="cuda")
+        for _ in range(50):
+            x = x0.clone()
+            A.h3fp4_block_norm(x, out, y=y, x_out=x, x_scale=-1.0, out_amax=amax)
+            assert float(amax) == float(out.float().abs().max()) < 2
+
+
 def test_feeds_the_linear():
     """Norm with max|out|, its scale, and the linear in one pass: the same bits as the two-pass quantisation."""
     import audio_dit_gb300 as A
