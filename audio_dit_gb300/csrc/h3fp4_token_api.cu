@@ -1,5 +1,6 @@
 // C ABI of a token's way through a block (h3fp4_block_norm, h3fp4_linear_rows,
-// h3fp4_cache_append, h3fp4_cache_read, h3fp4_cache_attn): argument validation and job set-up.  Nothing here allocates device memory or synchronises.
+// h3fp4_cache_append, h3fp4_cache_read, h3fp4_cache_attn): argument validation and job
+// set-up.  Nothing here allocates device memory or synchronises.
 #include <cmath>
 #include <cstdint>
 
@@ -8,10 +9,15 @@
 namespace h3fp4 {
 namespace {
 
-bool overlap(const void* a, const void* b, int64_t bytes)
+bool overlap(const void* a, uint64_t a_bytes, const void* b, uint64_t b_bytes)
 {
     const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
-    return a && b && x < y + (uint64_t)bytes && y < x + (uint64_t)bytes;
+    return a && b && x < y + b_bytes && y < x + a_bytes;
+}
+
+bool overlap(const void* a, const void* b, int64_t bytes)
+{
+    return overlap(a, (uint64_t)bytes, b, (uint64_t)bytes);
 }
 
 bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
@@ -152,10 +158,20 @@ h3fp4_status h3fp4_linear_rows(const void* x, int64_t M, int64_t N, int64_t K, c
     for (const void* p : {x, w_codes, w_sf, bias, resid, static_cast<const void*>(out), static_cast<const void*>(ws)})
         if (!aligned16(p)) return H3FP4_ERR_ALIGN;
     if (!aligned4(w_gscale) || !aligned4(gate)) return H3FP4_ERR_ALIGN;
-    if (ws_bytes < linear_rows_workspace_bytes(M, N, K)) return H3FP4_ERR_INVALID;
-    // resid may be out itself; nothing else may overlap it
-    const int64_t outs = M * (swiglu ? N / 2 : N) * 2;
-    if (out == x || (gated && out != resid && overlap(out, resid, outs))) return H3FP4_ERR_INVALID;
+    const size_t need = linear_rows_workspace_bytes(M, N, K);
+    if (ws_bytes < need) return H3FP4_ERR_INVALID;
+    // resid may be out itself; nothing else may overlap it, or the workspace
+    const uint64_t outs = (uint64_t)(M * (swiglu ? N / 2 : N)) * 2;
+    if (out != resid && overlap(out, outs, resid, outs)) return H3FP4_ERR_INVALID;
+    const struct {
+        const void* p;
+        int64_t bytes;
+    } read[] = {{x, M * K * 2}, {w_codes, N * K / 2}, {w_sf, (N + 127) / 128 * 128 * K / 16}, {bias, N * 2},
+                {gate, ((M - 1) * gate_stride + N) * 4}};
+    for (const auto& r : read)
+        if (overlap(out, outs, r.p, (uint64_t)r.bytes) || overlap(ws, need, r.p, (uint64_t)r.bytes))
+            return H3FP4_ERR_INVALID;
+    if (overlap(out, outs, ws, need) || overlap(resid, outs, ws, need)) return H3FP4_ERR_INVALID;
     if ((st = check_device()) != H3FP4_OK) return st;
     LinearRowsJob job{};
     job.x = static_cast<const __nv_bfloat16*>(x);

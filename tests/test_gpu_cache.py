@@ -189,6 +189,12 @@ ATTN = [  # lengths, rows, heads of q and kv, D, page, causal
     ([4097, 3], [4, 3], 64, 2, 64, 64, True),
     ([20] * 300, [1] * 300, 2, 1, 64, 16, True),
     ([9000, 1, 2000], [1, 1, 17], 16, 2, 128, 64, True),
+    ([128 * 76], [1], 32, 8, 128, 64, True),                          # as many tiles as CTAs, and some more and less
+    ([128 * 76 + 1], [1], 32, 8, 128, 64, True),
+    ([128 * 607], [1], 4, 1, 128, 64, False),
+    ([128 * 1217 - 5], [1], 4, 1, 64, 64, True),
+    ([18 + i % 40 for i in range(1024)], [1] * 1024, 4, 2, 256, 16, True),   # the most sequences
+    ([40] * 1024, [2] * 1024, 16, 4, 64, 16, True),
 ]
 
 

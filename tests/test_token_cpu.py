@@ -136,7 +136,10 @@ def test_linear_rows_refusals(lib):
     for kw in (dict(x=None), dict(wc=None), dict(wsf=None), dict(wg=None), dict(out=None), dict(ws=None), dict(ws_bytes=0),
                dict(flags=1), dict(flags=2), dict(bias=7 * MB), dict(gate=7 * MB), dict(flags=4), dict(flags=4, gate=7 * MB),
                dict(flags=4, resid=7 * MB), {**G, "flags": 68}, {**G, "stride": 255}, {**G, "stride": -1},
-               {**G, "resid": 5 * MB + 16}, dict(out=MB)):
+               {**G, "resid": 5 * MB + 16}, dict(out=MB), dict(out=MB + 1024 - 16), dict(out=MB - 2048 + 16),
+               dict(out=2 * MB + 16384 - 16), dict(out=3 * MB + 2048 - 16), dict(flags=2, bias=5 * MB + 2048 - 16),
+               {**G, "gate": 5 * MB + 2048 - 4}, {**G, "stride": 256, "gate": 5 * MB - 4096 + 4}, dict(out=6 * MB - 2048 + 16),
+               dict(ws=MB + 1024 - 16), dict(ws=2 * MB + 16384 - 256), {**G, "resid": 6 * MB + 256}):
         assert rows(lib, **kw) == INVALID, kw
     for kw in (dict(x=MB + 2), dict(wc=2 * MB + 8), dict(wsf=3 * MB + 8), dict(wg=4 * MB + 2), dict(out=5 * MB + 4),
                dict(ws=6 * MB + 8), dict(flags=2, bias=7 * MB + 2), {**G, "gate": 7 * MB + 2}, {**G, "resid": 8 * MB + 8}):
