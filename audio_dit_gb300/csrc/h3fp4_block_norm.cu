@@ -12,15 +12,17 @@
 // sum over the registers), and each output is rounded once.
 //
 // Rows of up to 512 by parts of a warp; up to 8192 by a block that copies rows ahead into a
-// ring of four (each thread its own columns, so that no barrier guards it) and keeps a
-// segment's vectors for its columns folded to three in registers; wider ones by a block that
-// reads x, y and the vectors when they are needed.  Measured, of the measured 6793 GB/s:
-// 31744 rows of 3072 with gate and modulation 135 us (5780 GB/s), 4099 of 5192 with both norms
-// 43 us (4010; two block sums a row, one after the other, and rows that end inside a sector:
-// 8192 rows of 5192 take 73 us where as many of 6144 take 68), 8192 of 3072 36 us, one row
-// 2.3 us (a launch).  Of wider ones 2048 rows of 16384 take 90 us (2990 GB/s).  The second
-// norm's sum behind one barrier with the next row's first: 42 us for 43, but 146 for 135
-// without a first norm, so each has its own.
+// ring of three (each thread its own columns, so that no barrier guards it), keeps a segment's
+// vectors for its columns folded to three in registers and computes in pairs; wider ones by a
+// block that reads x, y and the vectors when they are needed.  Measured, of the measured 6793
+// GB/s: 31744 rows of 3072 with gate and modulation 123 us (6320 GB/s), 4099 of 5192 with both
+// norms 38.5 us (4430; two block sums a row, one after the other, and rows that end inside a
+// sector: 8192 rows of 5192 take 65 us, where as many of 6144 take 63), 8192 of 3072 33 us,
+// one row 2.2 us (a launch).  8192 rows of 8192 take 90 us, as few as 82 with less ahead: whole
+// tensors of a power of two apart.  Of wider ones 2048 rows of 16384 take 90 us (2990 GB/s).
+// In single values, with the warps' sums joined by shuffles, the first took 135 us and the
+// second 43.  The second norm's sum behind one barrier with the next row's first: 42 for that
+// 43, but 146 for the 135 without a first norm.  Rings of two: 131 and 40 us.
 #include <cstdint>
 
 #include <cuda_bf16.h>
@@ -72,6 +74,26 @@ __device__ __forceinline__ uint4 pack_bf8(const float (&f)[8])
 {
     return make_uint4(cvt_bf16x2(f2(f[0], f[1])), cvt_bf16x2(f2(f[2], f[3])), cvt_bf16x2(f2(f[4], f[5])),
                       cvt_bf16x2(f2(f[6], f[7])));
+}
+
+// The same in pairs.
+__device__ __forceinline__ void unpack_pairs(const uint4& v, uint64_t (&f)[4])
+{
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) f[i] = f2(bf16_lo(w[i]), bf16_hi(w[i]));
+}
+
+__device__ __forceinline__ uint4 pack_pairs(const uint64_t (&f)[4])
+{
+    return make_uint4(cvt_bf16x2(f[0]), cvt_bf16x2(f[1]), cvt_bf16x2(f[2]), cvt_bf16x2(f[3]));
+}
+
+__device__ __forceinline__ float both(uint64_t v)
+{
+    float lo, hi;
+    unf2(v, lo, hi);
+    return lo + hi;
 }
 
 // Sum over the threads of a row.  Rows of several warps meet in shared memory;
@@ -226,7 +248,7 @@ __global__ void __launch_bounds__(kRow < 128 ? 128 : kRow, kRow == 32 && kVec ==
 // (y_weight gate, weight (1 + scale), shift), and takes rows one after the other.  Its threads copy their
 // columns of the next rows to shared memory ahead of time (each for itself, nothing waits for others), so
 // that enough bytes are on their way whatever the sums wait for.
-constexpr int kRing = 4;   // rows ahead
+constexpr int kRing = 3;   // rows ahead
 
 
 __device__ __forceinline__ void copy16(void* dst, const void* src)
@@ -239,11 +261,14 @@ __global__ void __launch_bounds__(kThreads, kBlocks)
     block_norm_ring_kernel(const __grid_constant__ BlockNormParams p)
 {
     extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ float part[2][32];
-    const int t = threadIdx.x, threads = blockDim.x, warp = t >> 5, lane = t & 31, warps = threads >> 5;
+    __shared__ __align__(16) float part[2][kThreads / 32];   // of warps that there are not: zeros
+    static_assert(kThreads % 128 == 0, "four sums a load");
+    const int t = threadIdx.x, threads = blockDim.x, warp = t >> 5, lane = t & 31;
     const int nv = p.K >> 3;
     uint4* ring = reinterpret_cast<uint4*>(smem) + t;   // [row][x, y][vector of the thread][thread]
     constexpr int kY = kVec, kSlot = 2 * kVec;
+    for (int i = t; i < 2 * kThreads / 32; i += threads) (&part[0][0])[i] = 0.0f;
+    __syncthreads();
     griddep_wait();
     auto load = [&](long long r, int slot) {
 #pragma unroll
@@ -265,10 +290,17 @@ __global__ void __launch_bounds__(kThreads, kBlocks)
         for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
         if (lane == 0) part[turn][warp] = v;
         __syncthreads();
-        v = lane < warps ? part[turn][lane] : 0.0f;
+        // (all warps' sums by each thread: fewer steps one after another than by shuffles)
+        float four[kThreads / 128];
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+        for (int i = 0; i < kThreads / 128; ++i) {
+            const float4 x = *reinterpret_cast<const float4*>(&part[turn][4 * i]);
+            four[i] = (x.x + x.y) + (x.z + x.w);
+        }
         turn ^= 1u;
+        v = four[0];
+#pragma unroll
+        for (int i = 1; i < kThreads / 128; ++i) v += four[i];
         return v;
     };
     // the vectors of the thread's i-th columns: what y, the normed r are multiplied with, what is added
@@ -295,7 +327,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks)
         }
         if (p.shift) load_f8(p.shift + at + 8 * v, c);
     };
-    float va[kVec][8], vb[kVec][8], vc[kVec][8];
+    uint64_t va[kVec][4], vb[kVec][4], vc[kVec][4];   // pairs, as all below
     long long seg_end = 0;
     int slot = 0;
     for (long long r = blockIdx.x; r < p.M; r += gridDim.x) {
@@ -306,58 +338,69 @@ __global__ void __launch_bounds__(kThreads, kBlocks)
 #pragma unroll
             for (int i = 0; i < kVec; ++i) {
                 const int v = min(t + i * threads, nv - 1);
-                y_vector(at, v, va[i]);
-                out_vectors(at, v, vb[i], vc[i]);
+                float a[8], b[8], c[8];
+                y_vector(at, v, a);
+                out_vectors(at, v, b, c);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    va[i][j] = f2(a[2 * j], a[2 * j + 1]);
+                    vb[i][j] = f2(b[2 * j], b[2 * j + 1]);
+                    vc[i][j] = f2(c[2 * j], c[2 * j + 1]);
+                }
             }
         }
         asm volatile("cp.async.wait_group %0;" ::"n"(kRing - 1) : "memory");
-        float f[kVec][8], y[kVec][8];
+        uint64_t f[kVec][4], y[kVec][4];
 #pragma unroll
         for (int i = 0; i < kVec; ++i) {
             const uint4 zero = make_uint4(0, 0, 0, 0);
             const bool real = t + i * threads < nv;
-            unpack_bf8(real ? ring[(slot * kSlot + i) * threads] : zero, f[i]);
-            if (p.y) unpack_bf8(real ? ring[(slot * kSlot + kY + i) * threads] : zero, y[i]);
+            unpack_pairs(real ? ring[(slot * kSlot + i) * threads] : zero, f[i]);
+            if (p.y) unpack_pairs(real ? ring[(slot * kSlot + kY + i) * threads] : zero, y[i]);
         }
         const long long row = r * p.K;
         if (p.y) {
-            float rs = 1.0f;
             if (p.post) {
-                float sum = 0.0f;
+                uint64_t sum = 0;
 #pragma unroll
                 for (int i = 0; i < kVec; ++i)
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) sum = fmaf(y[i][j], y[i][j], sum);
-                rs = rsqrtf(fmaf(block_sum(sum), p.inv_k, p.eps));
+                    for (int j = 0; j < 4; ++j) sum = fma2(y[i][j], y[i][j], sum);
+                const float rs = rsqrtf(fmaf(block_sum(both(sum)), p.inv_k, p.eps));
+#pragma unroll
+                for (int i = 0; i < kVec; ++i)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) y[i][j] = mul2(y[i][j], f2(rs, rs));
             }
 #pragma unroll
             for (int i = 0; i < kVec; ++i) {
                 const int v = t + i * threads;
 #pragma unroll
-                for (int j = 0; j < 8; ++j) f[i][j] = fmaf(p.x_scale, f[i][j], y[i][j] * rs * va[i][j]);
-                if (p.x_out && v < nv) *reinterpret_cast<uint4*>(p.x_out + row + 8 * v) = pack_bf8(f[i]);
+                for (int j = 0; j < 4; ++j)
+                    f[i][j] = fma2(f2(p.x_scale, p.x_scale), f[i][j], mul2(y[i][j], va[i][j]));
+                if (p.x_out && v < nv) *reinterpret_cast<uint4*>(p.x_out + row + 8 * v) = pack_pairs(f[i]);
             }
         }
-        float mean = 0.0f;
         if (p.layer) {
-            float sum = 0.0f;
+            uint64_t sum = 0;
 #pragma unroll
             for (int i = 0; i < kVec; ++i)
 #pragma unroll
-                for (int j = 0; j < 8; ++j) sum += f[i][j];   // (places past the row hold zeros)
-            mean = block_sum(sum) * p.inv_k;
+                for (int j = 0; j < 4; ++j) sum = add2(sum, f[i][j]);   // (places past the row hold zeros)
+            const float mean = block_sum(both(sum)) * p.inv_k;
+#pragma unroll
+            for (int i = 0; i < kVec; ++i)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) f[i][j] = add2(f[i][j], f2(-mean, -mean));
         }
-        float sum = 0.0f;
+        uint64_t pairs = 0;
 #pragma unroll
         for (int i = 0; i < kVec; ++i) {
             if (t + i * threads >= nv) continue;
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                f[i][j] -= mean;
-                sum = fmaf(f[i][j], f[i][j], sum);
-            }
+            for (int j = 0; j < 4; ++j) pairs = fma2(f[i][j], f[i][j], pairs);
         }
-        sum = block_sum(sum);
+        const float sum = block_sum(both(pairs));
         // (the sum has used what the thread read of the slot)
         load(r + (long long)kRing * gridDim.x, slot);
         if (p.out) {
@@ -367,8 +410,8 @@ __global__ void __launch_bounds__(kThreads, kBlocks)
                 const int v = t + i * threads;
                 if (v >= nv) continue;
 #pragma unroll
-                for (int j = 0; j < 8; ++j) f[i][j] = fmaf(f[i][j] * rs, vb[i][j], vc[i][j]);
-                const uint4 o = pack_bf8(f[i]);
+                for (int j = 0; j < 4; ++j) f[i][j] = fma2(mul2(f[i][j], f2(rs, rs)), vb[i][j], vc[i][j]);
+                const uint4 o = pack_pairs(f[i]);
                 *reinterpret_cast<uint4*>(p.out + row + 8 * v) = o;
                 if (p.amax) {
                     const uint32_t words[4] = {o.x, o.y, o.z, o.w};
@@ -459,8 +502,8 @@ cudaError_t launch_block_norm(const BlockNormJob& job, cudaStream_t s)
     p.seg = job.seg;
     const int nv = job.K / 8;
     // Rows of up to 64 vectors by parts of a warp, wider ones by a block and from its ring: so also single
-    // rows, whose vectors it fetches while the sums are made (128 rows of 3072 2.7 us against 4.0 for blocks
-    // that read the vectors when they need them, 8192 rows 36 against 48).
+    // rows, whose vectors it fetches while the sums are made (128 rows of 3072 2.5 us against 4.0 for blocks
+    // that read the vectors when they need them, 8192 rows 33 against 48).
     if (nv <= 8) return launch<8, 1>(p, s);
     if (nv <= 16) return launch<16, 1>(p, s);
     if (nv <= 32) return launch<32, 1>(p, s);
