@@ -9,9 +9,10 @@
 // their codes differ only where that step crosses a tie of E4M3 (a head whose global scale is
 // 1.25 x 1.75 2^k / 2688 has 1.5 % of such blocks, other mantissas none).
 // Memory-bound: 4 bytes of bf16 per pair of K and V elements and 9/8 of the cache.
-// A warp takes a run of rows.  Measured, 8 heads of 128: 16384 rows in 25 us (3450 GB/s: the
+// A warp takes a run of rows.  Measured, 8 heads of 128: 16384 rows in 22 us (3940 GB/s: the
 // loads' latency beside 55 % of the issue slots; loading ahead needs registers that take the
-// warps away, 26.7 us), 25385 rows out 26 us (5130 GB/s); 64 rows 3.7 and 3.2 us (a launch).
+// warps away, 26.7 us), 25385 rows out 25.5 us (5230 GB/s; with more warps an SM 27 to 35, with
+// fewer instructions for a code, but more registers, 27); 64 rows 4.2 and 3.2 us (a launch).
 #include <cstdint>
 
 #include <cuda_bf16.h>
@@ -73,11 +74,11 @@ __device__ __forceinline__ uint32_t encode(const V16& v, float s, uint32_t (&w)[
     unpack16(v, f);
     float top = 0.0f;
 #pragma unroll
-    for (int k = 0; k < 16; ++k) top = fmaxf(top, fabsf(f[k]));
+    for (int k = 0; k < 16; k += 2) top = max3(top, fabsf(f[k]), fabsf(f[k + 1]));
     const uint32_t S = cvt_e4m3(__fdiv_rn(__fmul_rn(top, 1.0f / 6.0f), s));
     const float rcp = block_rcp(S, s);
 #pragma unroll
-    for (int k = 0; k < 16; ++k) f[k] = __fmul_rn(f[k], rcp);
+    for (int k = 0; k < 16; k += 2) unf2(mul2(f2(f[k], f[k + 1]), f2(rcp, rcp)), f[k], f[k + 1]);
     w[0] = e2m1x8(reinterpret_cast<const float(&)[8]>(f[0]));
     w[1] = e2m1x8(reinterpret_cast<const float(&)[8]>(f[8]));
     return S;
@@ -135,7 +136,7 @@ struct Rows {
 
 // A lane takes a block of 16 elements of a head at a time.
 template <int W>
-__global__ void __launch_bounds__(kThreads, 6) cache_append_kernel(const __grid_constant__ CacheRowsJob p, int rows_per_warp)
+__global__ void __launch_bounds__(kThreads, 7) cache_append_kernel(const __grid_constant__ CacheRowsJob p, int rows_per_warp)
 {
     using L = CacheLayout<W>;
     constexpr int kHeads = 32 / L::kBlocks;   // heads of a warp at a time
@@ -249,8 +250,9 @@ constexpr void (*kernel_of(bool read))(CacheRowsJob, int)
 cudaError_t launch(const CacheRowsJob& job, bool read, cudaStream_t s)
 {
     if (job.M == 0) return cudaSuccess;
-    // as many warps as are resident, each with a run of rows
-    const long long most = (long long)sm_count_current_device() * (read ? 64 : 24);
+    // each warp with a run of rows: on the way in as many as are resident, on the way out half as many again (25.5
+    // us of 25385 rows; 26.0 with fewer, 27.4 with twice as many)
+    const long long most = (long long)sm_count_current_device() * (read ? 96 : 28);
     const int per_warp = (int)((job.M + most - 1) / most);
     const long long warps = (job.M + per_warp - 1) / per_warp;
     cudaLaunchConfig_t cfg = {};
