@@ -840,9 +840,11 @@ __global__ void __launch_bounds__(kJoinThreads) cache_join_kernel(const __grid_c
     __shared__ float red[2][kJoinThreads / 32];
     griddep_wait();
     griddep_launch_dependents();
-    if (p.by_unit && (int)blockIdx.x >= *reinterpret_cast<const int*>(p.ws + kUnitsOff)) return;
+    // (both loads in flight; a cut past the units' is not looked at)
+    const int units = p.by_unit ? *reinterpret_cast<const volatile int*>(p.ws + kUnitsOff) : kMaxCtas;
     const Cut cut = reinterpret_cast<const Cut*>(p.ws + kCutOff)[blockIdx.x];
-    if (cut.count == 0 || (int)blockIdx.y * kJoinCols >= cut.cols) return;
+    if ((int)blockIdx.x >= units || cut.count == 0 || (int)blockIdx.y * kJoinCols >= cut.cols) return;
+    const float vg = p.c.v_gscale ? __ldg(p.c.v_gscale + cut.head) : 1.0f;
     const int t = threadIdx.x, lane = t & 31, mine = t / (kLanes * kSplit), split = t / kLanes % kSplit;
     const int col = min((int)blockIdx.y * kJoinCols + mine, kPartCols - 1);   // (columns past the last are not written)
     // partial 0 is its CTA's second, the others are the first ones
@@ -914,7 +916,7 @@ __global__ void __launch_bounds__(kJoinThreads) cache_join_kernel(const __grid_c
     const int id = cut.col + col, d = 4 * (t % kLanes);
     const long long r = (long long)cut.first + id / p.group;
     const int hq = cut.head * p.group + id % p.group;
-    const float f = norm(m, l, p.c.v_gscale ? p.c.v_gscale[cut.head] : 1.0f);
+    const float f = norm(m, l, vg);
     if (d < p.c.D)
         *reinterpret_cast<uint2*>(p.out + r * p.out_row + (long long)hq * p.out_head + d) =
             make_uint2(cvt_bf16x2(f2(acc.x * f, acc.y * f)), cvt_bf16x2(f2(acc.z * f, acc.w * f)));
