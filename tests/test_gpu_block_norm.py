@@ -72,6 +72,11 @@ CASES = [  # M, K, offsets, y, post, layer, vectors
     (1030, 8200, [0, 1029, 1030], True, True, True, ALL),
     (1024, 16384, [0, 1023, 1024], True, True, True, ALL),
     (1024, 16392, None, True, False, False, ("gate", "weight")),
+    (300, 8200, [0, 299, 300], True, True, True, ALL),
+    (97, 72, [0, 5, 97], True, True, False, ALL),
+    (1001, 136, None, True, False, True, ("gate", "scale")),
+    (70001, 264, [0, 33, 70001], True, True, False, ALL),
+    (33, 8200, None, False, False, False, ("weight",)),
 ]
 
 
