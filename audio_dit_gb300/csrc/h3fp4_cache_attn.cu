@@ -18,10 +18,10 @@
 // the same bits.
 //
 // Measured, calls back to back over three caches, of the measured 6793 GB/s: 64 tokens of 64
-// sequences over 524288 keys, 32 heads on 8 of 128, 113 us (5340 GB/s; the products, scores and
+// sequences over 524288 keys, 32 heads on 8 of 128, 112 us (5390 GB/s; the products, scores and
 // unpacking of two thirds of the issue slots beside the loads), one token over 131072 keys
-// 34.9 us (4330 GB/s: 3 us until the first keys are there, 4 us for the second kernel), 31 rows
-// of 6 sequences over 4433 keys, 28 heads on 4 of 64, 14.1 us (launches and latencies; the
+// 34.7 us (4360 GB/s: 3 us until the first keys are there, 4 us for the second kernel), 31 rows
+// of 6 sequences over 4433 keys, 28 heads on 4 of 64, 12.2 us (launches and latencies; the
 // bytes take 0.2).  Two CTAs of eight warps in place of four of four take 121 us for the first,
 // three CTAs an SM 117; shares by the order in which an SM's CTAs issue (the first ended at 86,
 // the last at 101 us) change nothing, as the bytes come no faster.
@@ -52,6 +52,7 @@ constexpr int kStep = 2 * kCacheGroup;        // tokens that a warp takes at a t
 constexpr int kTile = kStep * kWarps;         // tokens of a tile
 constexpr int kPartCols = 16;                 // query columns of a unit at most
 constexpr int kMaxCtas = 608;                 // of a launch: the workspace is made for as many
+constexpr long long kNear = 2;                // tiles that a cut is moved by at most
 constexpr float kRaise = 14.0f, kStart = 6.0f;  // in powers of two: see above
 // No key yet; and the lowest score that counts: where a column's largest is there, it left fp32's range.
 constexpr float kNone = -3.4e38f, kLowest = -3.0e38f;
@@ -219,20 +220,40 @@ __device__ __forceinline__ long long div(long long a, long long b)
 }
 
 // How the tiles of a call are cut over its CTAs: shares that differ by one at most (shares of the rounded-up mean
-// left CTAs idle: one token over 131072 keys 37.3 -> 35.0 us), none empty but where there are fewer tiles.
+// left CTAs idle: one token over 131072 keys 37.3 -> 35.0 us), none empty but where there are fewer tiles.  A second
+// unit costs a CTA more than some tiles do (its keys' places, queries and first copies come one after another), so a
+// cut up to kNear tiles from a unit's edge is moved there: 31 rows of 6 sequences 14.1 -> 12.2 us, 10 of 5 over 50000
+// keys, heads of 64, 17.5 -> 14.8, the batch 113.3 -> 112.1 (and 114.7 with three tiles for two, where shares differ).
 struct Shares {
     long long total;
     int ctas;
 
-    // CTA b's first tile
-    __device__ __forceinline__ long long start(int b) const
+    // CTA b's first tile, before it is moved
+    __device__ __forceinline__ long long raw(int b) const
     {
         return total < ctas ? min(total, (long long)b) : div(total * b, ctas);
     }
-    // the CTA that has tile x: the last one that starts at x or before
-    __device__ __forceinline__ int owner(long long x) const
+    // where the cut before CTA b goes that lies inside a unit from `first` to `last`: of the two cuts around a unit's
+    // edge the nearer one is moved
+    __device__ __forceinline__ long long moved(int b, long long x, long long first, long long last) const
     {
-        return total < ctas ? (int)x : (int)div((x + 1) * ctas + total - 1, total) - 1;
+        const long long up = last - x, down = x - first;
+        if (total < ctas || down == 0) return x;
+        if (up <= kNear) {
+            const long long next = raw(b + 1);
+            if (next > last && up <= next - last) return last;
+        }
+        if (down > kNear) return x;
+        const long long before = raw(b - 1);
+        return before < first && down < first - before ? first : x;
+    }
+    // the CTA that has the last tile of a unit
+    __device__ __forceinline__ int owner_of_last(long long first, long long last) const
+    {
+        if (total < ctas) return (int)(last - 1);
+        const int c = (int)div(last * ctas + total - 1, total) - 1;
+        const long long x = raw(c);
+        return x > first && moved(c, x, first, last) == last ? c - 1 : c;
     }
 };
 
@@ -545,7 +566,30 @@ __global__ void __launch_bounds__(kThreads, Config<W, kCols>::kCtasPerSm)
     }
     const long long total = prefix[nseq];
     const Shares shares{total, (int)gridDim.x};
-    const long long begin = shares.start(blockIdx.x), end = shares.start(blockIdx.x + 1);
+    // the sequence whose tiles hold x < total (the last one that begins there or before), by a warp: in steps of 32
+    auto holder = [&](long long x) {
+        int lo = 0, each = 1;
+        while (each * 32 < nseq) each *= 32;
+        for (; each > 0; each /= 32) {
+            const int i = lo + lane * each;
+            lo += (__popc(__ballot_sync(0xffffffffu, i < nseq && prefix[i] <= x)) - 1) * each;
+        }
+        return lo;
+    };
+    // this CTA's tiles: two warps look for their ends
+    __shared__ long long ends[2];
+    if (warp < 2) {
+        const int b = blockIdx.x + warp;
+        long long x = shares.raw(b);
+        if (x < total) {
+            const int s = holder(x), tiles = key_tiles(seqs[s]);
+            const long long first = prefix[s] + div(x - prefix[s], tiles) * tiles;
+            x = shares.moved(b, x, first, first + tiles);
+        }
+        if (lane == 0) ends[warp] = x;
+    }
+    __syncthreads();
+    const long long begin = ends[0], end = ends[1];
 
     // rows of sequences that hold nothing
     for (int s = blockIdx.x; s < nseq; s += gridDim.x) {
@@ -575,18 +619,8 @@ __global__ void __launch_bounds__(kThreads, Config<W, kCols>::kCtasPerSm)
     uint32_t phases = 0;    // of the ring's barriers, one bit each
     bool lost = false;      // a wait ran out: nothing more is loaded or computed
     const int per_page = p.c.page / kCacheGroup;
-    int s = 0;
     for (long long at = begin; at < end;) {
-        // the sequence whose tiles hold `at`
-        {
-            int lo = s, hi = nseq;
-            while (hi - lo > 1) {
-                const int mid = (lo + hi) / 2;
-                if (prefix[mid] <= at) lo = mid;
-                else hi = mid;
-            }
-            s = lo;
-        }
+        const int s = holder(at);
         const Seq q = seqs[s];
         const int coltiles = col_tiles<kCols>(p, q), tiles = key_tiles(q);
         const long long unit = div(at - prefix[s], tiles);
@@ -815,7 +849,7 @@ __global__ void __launch_bounds__(kThreads, Config<W, kCols>::kCtasPerSm)
                 }
             }
             if (lane == 0 && at == ubegin && (p.by_unit || !whole)) {
-                const int count = whole ? 0 : shares.owner(uend - 1) - (int)blockIdx.x + 1;
+                const int count = whole ? 0 : shares.owner_of_last(ubegin, uend) - (int)blockIdx.x + 1;
                 const long long i = p.by_unit ? units_before(s) + unit : blockIdx.x;
                 // (row offsets that overlap make more units than there can be)
                 if (i < kMaxCtas) cuts[i] = Cut{q.first, h, ct * kCols, cols, (int)blockIdx.x, count};
