@@ -144,7 +144,7 @@ def _ptr(t: Optional[torch.Tensor], what: str, dtype=None):
     return t.data_ptr()
 
 
-_BF16, _F32 = torch.bfloat16, torch.float32
+_Tensor, _BF16, _F32, _I32, _U8 = torch.Tensor, torch.bfloat16, torch.float32, torch.int32, torch.uint8
 
 
 def _heads(t: torch.Tensor, what: str, rows: int, heads: int, d: int):
@@ -205,7 +205,7 @@ def _mask(t: Optional[torch.Tensor], what: str, n: int):
 def _f32(t: Optional[torch.Tensor], what: str, shape):
     if t is None:
         return None
-    if isinstance(t, torch.Tensor) and t.dtype is _F32 and t.shape == shape and t.is_cuda and t.is_contiguous():
+    if isinstance(t, _Tensor) and t.dtype is _F32 and t.shape == shape and t.is_cuda and t.is_contiguous():
         return t.data_ptr()
     _ptr(t, what, _F32)
     raise ValueError(f"{what} must be {list(shape)}, got {list(t.shape)}")
@@ -214,7 +214,7 @@ def _f32(t: Optional[torch.Tensor], what: str, shape):
 def _bf16(t: Optional[torch.Tensor], what: str, shape):
     if t is None:
         return None
-    if isinstance(t, torch.Tensor) and t.dtype is _BF16 and t.shape == shape and t.is_cuda and t.is_contiguous():
+    if isinstance(t, _Tensor) and t.dtype is _BF16 and t.shape == shape and t.is_cuda and t.is_contiguous():
         return t.data_ptr()
     _ptr(t, what, _BF16)
     raise ValueError(f"{what} must be {list(shape)}, got {list(t.shape)}")
@@ -253,10 +253,10 @@ def _check(status: int, what: str):
         raise H3FP4Error(status, what)
 
 
-def _workspace(ws: torch.Tensor) -> int:
-    if isinstance(ws, torch.Tensor) and ws.dtype is torch.uint8 and ws.is_cuda and ws.is_contiguous():
+def _workspace(ws: torch.Tensor, what: str = "ws") -> int:
+    if isinstance(ws, _Tensor) and ws.dtype is _U8 and ws.is_cuda and ws.is_contiguous():
         return ws.data_ptr()
-    return _ptr(ws, "ws", torch.uint8)
+    return _ptr(ws, what, _U8)
 
 
 # ------------------------------------------------------------------ C-ABI functions
@@ -604,9 +604,9 @@ def h3fp4_linear_rows_workspace_bytes(M: int, N: int, K: int) -> int:
 def _i32(t: Optional[torch.Tensor], what: str, shape):
     if t is None:
         return 0
-    if isinstance(t, torch.Tensor) and t.dtype is torch.int32 and t.shape == shape and t.is_cuda and t.is_contiguous():
+    if isinstance(t, _Tensor) and t.dtype is _I32 and t.shape == shape and t.is_cuda and t.is_contiguous():
         return t.data_ptr()
-    _ptr(t, what, torch.int32)
+    _ptr(t, what, _I32)
     raise ValueError(f"{what} must be {list(shape)}, got {list(t.shape)}")
 
 
@@ -617,19 +617,24 @@ def _cache_width(D: int) -> int:
 def _cache(cache: torch.Tensor, table: torch.Tensor, length: torch.Tensor, row_off: Optional[torch.Tensor], M: int,
            D: int, k_gscale: Optional[torch.Tensor], v_gscale: Optional[torch.Tensor]):
     """The fields of an h3fp4_cache, and its number of heads."""
-    at = _ptr(cache, "cache", torch.uint8)
-    if cache.dim() != 4 or cache.shape[3] != _cache_width(D) * 9 // 8:
-        raise ValueError(f"cache must be [pages, heads, page, {_cache_width(D) * 9 // 8}] for heads of {D}, got "
-                         f"{list(cache.shape)}")
-    n_pages, heads, page, _ = cache.shape
-    if not isinstance(table, torch.Tensor) or table.dim() != 2:
-        raise ValueError("table must be an int32 tensor [nseq, max_pages]")
-    nseq, max_pages = table.shape
+    at = _workspace(cache, "cache")
+    width = 72 if D <= 64 else 144 if D <= 128 else 288                # nine eighths of the room of a head
+    try:
+        n_pages, heads, page, held = cache.shape
+    except ValueError:
+        held = None
+    if held != width:
+        raise ValueError(f"cache must be [pages, heads, page, {width}] for heads of {D}, got {list(cache.shape)}")
+    try:
+        nseq, max_pages = shape = table.shape
+    except (AttributeError, ValueError):
+        raise ValueError("table must be an int32 tensor [nseq, max_pages]") from None
     if row_off is None and nseq != M:
         raise ValueError(f"without row_off there is one row per sequence: {M} rows, {nseq} sequences")
-    return (at, n_pages, page, heads, D, _i32(table, "table", (nseq, max_pages)), max_pages,
-            _i32(length, "length", (nseq,)), _i32(row_off, "row_off", (nseq + 1,)), nseq,
-            _f32(k_gscale, "k_gscale", (heads,)) or 0, _f32(v_gscale, "v_gscale", (heads,)) or 0), heads
+    of_heads = (heads,)
+    return (at, n_pages, page, heads, D, _i32(table, "table", shape), max_pages, _i32(length, "length", (nseq,)),
+            _i32(row_off, "row_off", (nseq + 1,)), nseq, _f32(k_gscale, "k_gscale", of_heads) or 0,
+            _f32(v_gscale, "v_gscale", of_heads) or 0), heads
 
 
 def _cache_rows(name: str, k, v, cache, table, length, row_off, k_gscale, v_gscale, stream):

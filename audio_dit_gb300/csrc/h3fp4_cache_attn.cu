@@ -605,14 +605,18 @@ __global__ void __launch_bounds__(kThreads, Config<W, kCols>::kCtasPerSm)
     }
     // Cuts.  By unit: units in the order of their sequences, empty ones have no number.
     Cut* cuts = reinterpret_cast<Cut*>(p.ws + kCutOff);
-    auto units_before = [&](int s) {
-        long long n = 0;
-        for (int i = 0; i < s; ++i) n += seqs[i].len > 0 ? (long long)p.c.Hkv * col_tiles<kCols>(p, seqs[i]) : 0;
-        return n;
+    auto units_before = [&](int s) {   // by a warp
+        int n = 0;
+        for (int i = lane; i < s; i += 32)
+            n += seqs[i].len > 0 ? (int)min((long long)kMaxCtas, (long long)p.c.Hkv * col_tiles<kCols>(p, seqs[i])) : 0;
+        return __reduce_add_sync(0xffffffffu, n);   // (more than there can be where row offsets overlap)
     };
-    if (threadIdx.x == 0) {
-        if (!p.by_unit) cuts[blockIdx.x].count = 0;
-        else if (blockIdx.x == 0) *reinterpret_cast<int*>(p.ws + kUnitsOff) = (int)min((long long)kMaxCtas, units_before(nseq));
+    if (warp == 0) {
+        const int units = p.by_unit && blockIdx.x == 0 ? units_before(nseq) : 0;
+        if (lane == 0) {
+            if (!p.by_unit) cuts[blockIdx.x].count = 0;
+            else if (blockIdx.x == 0) *reinterpret_cast<int*>(p.ws + kUnitsOff) = min(kMaxCtas, units);
+        }
     }
 
     // ------------------------------------------------------------ units
@@ -848,11 +852,11 @@ __global__ void __launch_bounds__(kThreads, Config<W, kCols>::kCtasPerSm)
                     }
                 }
             }
-            if (lane == 0 && at == ubegin && (p.by_unit || !whole)) {
-                const int count = whole ? 0 : shares.owner_of_last(ubegin, uend) - (int)blockIdx.x + 1;
+            if (at == ubegin && (p.by_unit || !whole)) {
                 const long long i = p.by_unit ? units_before(s) + unit : blockIdx.x;
+                const int count = whole ? 0 : shares.owner_of_last(ubegin, uend) - (int)blockIdx.x + 1;
                 // (row offsets that overlap make more units than there can be)
-                if (i < kMaxCtas) cuts[i] = Cut{q.first, h, ct * kCols, cols, (int)blockIdx.x, count};
+                if (lane == 0 && i < kMaxCtas) cuts[i] = Cut{q.first, h, ct * kCols, cols, (int)blockIdx.x, count};
             }
         }
         at = ubegin + t1;
