@@ -17,7 +17,7 @@
 // cycles); more than 32 rows take two passes over the tile, the second from L2.  The products
 // and the sums of 16 are exact, the accumulators fp32.
 //
-// Two forms, by size (few_split).  One kernel, up to four rows where a wave of CTAs has all
+// Two forms, by size (few_split).  One kernel, up to eight rows where a wave of CTAs has all
 // tiles of W: rows_few_kernel, digits beside the products, a tile's CTAs joined in a cluster.
 // Else three: digits_kernel writes the digits, their scales and the rows' factors;
 // rows_gemm_kernel multiplies.  Its work is one row of (W tile, pass, 256-column K stage), cut
@@ -28,7 +28,7 @@
 //
 // Measured, calls back to back over three sets of weights, of the measured 6793 GB/s:
 //     rows  W               us     GB/s     bound by
-//        1  9216 x 3072     6.4    2500     a launch, its start, one load's latency and the join (4.7 us of 2048 x 2048)
+//        1  9216 x 3072     6.3    2530     a launch, its start, one load's latency and the join (4.7 us of 2048 x 2048)
 //        1  4096 x 14336    8.8    3760     the same, and the clusters' uneven stages
 //        1  57344 x 8192    47.2   5600     HBM, and 3 kernels' ends (about 6 us)
 //       16  4096 x 14336    12.5   2660     digits and joining, 7 us of them
@@ -646,7 +646,7 @@ __global__ void __launch_bounds__(BM) rows_join_kernel(const __grid_constant__ J
         if (k < rows) p.out[(m0 + k) * p.N + n] = __float2bfloat16_rn(p.gate ? fmaf(g[k], y[0][k], r[k]) : y[0][k]);
 }
 
-// ------------------------------------------------------------------ up to four rows, in one kernel
+// ------------------------------------------------------------------ up to eight rows, in one kernel
 //
 // A launch, its start and the wait for the one before cost what a small weight's reading does.  So where a
 // wave of CTAs has all tiles, a cluster of `split` CTAs (with SwiGLU twice as many: the gate and the up tile)
@@ -656,13 +656,18 @@ __global__ void __launch_bounds__(BM) rows_join_kernel(const __grid_constant__ J
 constexpr int kFewThreads = 512;     // producer, MMA, 2 idle; 4 scale warps; 8 warps of digits, 4 of them of outputs
 constexpr int kMaxCluster = 8;
 
-constexpr int kFewRows = 4;
-constexpr int kFewStages = 8;
-using FewPlan = Plan<kDigits * kFewRows>;
-constexpr uint32_t kFewRedOff = kFewStages * FewPlan::kStage;
-constexpr uint32_t kFewBarOff = kFewRedOff + kMaxCluster * kFewRows * BM * 4;
-constexpr uint32_t kFewSmem = kFewBarOff + 8 * (3 * kFewStages + 1) + 8 + 4 * 8;
-static_assert(kFewSmem <= 232448, "shared memory budget");
+constexpr int kFewRows = 8;
+
+template <int kRows>   // four or eight
+struct FewPlan : Plan<kDigits * kRows> {
+    using P = Plan<kDigits * kRows>;
+    static constexpr int kStages = kRows == 4 ? 8 : 6;
+    static constexpr uint32_t kRedOff = kStages * P::kStage;
+    static constexpr uint32_t kBarOff = kRedOff + kMaxCluster * kRows * BM * 4;
+    static constexpr uint32_t kSmem = kBarOff + 8 * (3 * kStages + 1) + 8 + 4 * 8;
+    static_assert(kSmem <= 232448, "shared memory budget");
+    static_assert(P::kSfTmem + kStages * P::kSfCols <= kTmemCols, "TMEM budget");
+};
 
 struct FewParams {
     const __nv_bfloat16* x;
@@ -674,26 +679,27 @@ struct FewParams {
     int stall;
 };
 
+template <int kRows>
 __global__ void __launch_bounds__(kFewThreads, 1)
     rows_few_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmSfw, const FewParams p)
 {
     extern __shared__ __align__(1024) uint8_t smem[];
-    using P = FewPlan;
-    constexpr int kStages = kFewStages;
+    using P = FewPlan<kRows>;
+    constexpr int kStages = P::kStages, kNB = kDigits * kRows;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if ((smem_u32(smem) & 1023u) != 0) {   // (the same in every CTA)
         if (threadIdx.x == 0) atomicOr(p.status, kStatusBadSmemAlign);
         return;
     }
-    float* red = reinterpret_cast<float*>(smem + kFewRedOff);            // the first CTA's: [rank][row][output]
-    uint64_t* full = reinterpret_cast<uint64_t*>(smem + kFewBarOff);     // codes landed, digits and scales stored
+    float* red = reinterpret_cast<float*>(smem + P::kRedOff);            // the first CTA's: [rank][row][output]
+    uint64_t* full = reinterpret_cast<uint64_t*>(smem + P::kBarOff);     // codes landed, digits and scales stored
     uint64_t* empty = full + kStages;
     uint64_t* sf_full = empty + kStages;                              // scale tiles landed and written
     uint64_t* acc_full = sf_full + kStages;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(acc_full + 1);
     volatile int& s_abort = *reinterpret_cast<volatile int*>(tmem_slot + 1);
     uint32_t* tops = tmem_slot + 2;   // per warp of digits: the largest that it read
-    const int M = p.j.M, row_warps = M > 2 ? 4 : M;   // warps of digits per stage
+    const int M = p.j.M, row_warps = kRows == 8 ? 8 : M > 2 ? 4 : M;   // warps of digits per stage
     if (threadIdx.x == 0) {
         s_abort = 0;
         for (int i = 0; i < kStages; ++i) {
@@ -766,7 +772,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
             }
             tc_fence_after();
             if (elect_one())
-                multiply<kDigits * kFewRows>(smem_u32(smem) + (uint32_t)stage * P::kStage, tmem + (uint32_t)stage * P::kSfCols,
+                multiply<kNB>(smem_u32(smem) + (uint32_t)stage * P::kStage, tmem + (uint32_t)stage * P::kSfCols,
                                              tmem, idesc, min(4, p.kb4 - (kb0 + i) * 4), i == 0, &empty[stage]);
             __syncwarp();
             if (++stage == kStages) {
@@ -780,7 +786,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
         (void)mbar_wait(acc_full, 0u, p.wait_ns, p.status, kStatusTimeoutMma);
     } else if (warp >= 4 && warp < 8) {
         // ------------------------------------------------------------ scales into TMEM, a lane quarter per warp
-        scales_role<kDigits * kFewRows, kStages>(smem_u32(smem), tmem, sf_full, full, n, (uint32_t)(warp & 3), lane, p.wait_ns,
+        scales_role<kNB, kStages>(smem_u32(smem), tmem, sf_full, full, n, (uint32_t)(warp & 3), lane, p.wait_ns,
                                                  p.status, s_abort);
     } else if (warp >= 8) {
         // ------------------------------------------------------------ digits: warp w takes row w % row_warps of every
@@ -788,7 +794,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
         // from its neighbours, so whoever waits for a slot has to have waited for its fill before (with six stages
         // warps took a slot whose last but one fill was still in use for free).  What it reads for the row's
         // largest it keeps.
-        static_assert(kStages % 8 == 0, "a slot is one warp's");
+        static_assert(kStages % 8 == 0 || kRows == 8, "a slot is one warp's");   // (eight rows: every slot is each one's)
         constexpr int kKept = 8;
         const int w = warp - 8, m = w % row_warps, every = 8 / row_warps, i0 = w / row_warps;
         const long long c0 = (long long)kb0 * BK + 8 * lane;
@@ -854,7 +860,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
     // what the first CTA's last four warps need for the outputs
     const int o = (int)threadIdx.x - 12 * 32;
     const long long out0 = (p.j.swiglu ? 2ll * group : (long long)tile) * BM + o;   // the first tile's row of W
-    float s = 0.0f, bias[2] = {0.0f, 0.0f}, gate[kFewRows], resid[kFewRows];
+    float s = 0.0f, bias[2] = {0.0f, 0.0f}, gate[kRows], resid[kRows];
     if (warp >= 12) {
         // ------------------------------------------------------------ sums to the cluster's first CTA
         const int quarter = warp & 3;
@@ -863,7 +869,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
             if (p.j.bias && out0 < p.j.N) bias[0] = __bfloat162float(p.j.bias[out0]);
             if (p.j.bias && p.j.swiglu) bias[1] = __bfloat162float(p.j.bias[out0 + BM]);
 #pragma unroll
-            for (int m = 0; m < kFewRows; ++m)
+            for (int m = 0; m < kRows; ++m)
                 if (p.j.gate && m < M && out0 < p.j.N) {
                     gate[m] = p.j.gate[m * p.j.gate_stride + out0];
                     resid[m] = __bfloat162float(p.j.resid[m * p.j.N + out0]);
@@ -878,13 +884,16 @@ __global__ void __launch_bounds__(kFewThreads, 1)
             for (int k = row; k < 8; k += row_warps) top = max(top, tops[k]);
             return row_factor(unit_of(top));
         };
-        const uint32_t to = mapa_shared(smem_u32(red), 0) + 4u * (uint32_t)(rank * kFewRows * BM + o);
-        static_assert(kFewRows == 4, "all sums at once");
-        float y[4];
-        four_rows(tmem + ((32u * (uint32_t)quarter) << 16), y);
+        const uint32_t to = mapa_shared(smem_u32(red), 0) + 4u * (uint32_t)(rank * kRows * BM + o);
 #pragma unroll
-        for (int m = 0; m < 4; ++m)
-            if (m < M) st_shared_cluster_u32(to + 4u * (uint32_t)(m * BM), __float_as_uint(y[m] * factor(m)));
+        for (int m0 = 0; m0 < kRows; m0 += 4) {
+            if (m0 >= M) continue;
+            float y[4];
+            four_rows(tmem + ((32u * (uint32_t)quarter) << 16) + 8 * m0, y);
+#pragma unroll
+            for (int h = 0; h < 4; ++h)
+                if (m0 + h < M) st_shared_cluster_u32(to + 4u * (uint32_t)((m0 + h) * BM), __float_as_uint(y[h] * factor(m0 + h)));
+        }
     }
     __syncwarp();
     if (warp < 12) cluster_wait();
@@ -897,11 +906,11 @@ __global__ void __launch_bounds__(kFewThreads, 1)
     if (rank != 0 || warp < 12 || out0 >= p.j.N) return;
     auto value = [&](int first, int m, float b) {
         float y = 0.0f;
-        for (int r = first; r < first + p.split; ++r) y += red[(r * kFewRows + m) * BM + o];
+        for (int r = first; r < first + p.split; ++r) y += red[(r * kRows + m) * BM + o];
         return fmaf(y, s, b);
     };
 #pragma unroll
-    for (int m = 0; m < kFewRows; ++m) {
+    for (int m = 0; m < kRows; ++m) {
         if (m >= M) break;
         float v = value(0, m, bias[0]);
         if (p.j.swiglu) {
@@ -915,6 +924,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
     }
 }
 
+template <int kRows>
 cudaLaunchConfig_t few_config(unsigned ctas, int cluster, cudaLaunchAttribute (&attr)[2], cudaStream_t s)
 {
     cudaLaunchConfig_t cfg = {};
@@ -925,7 +935,7 @@ cudaLaunchConfig_t few_config(unsigned ctas, int cluster, cudaLaunchAttribute (&
     attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.gridDim = dim3(ctas);
     cfg.blockDim = dim3(kFewThreads);
-    cfg.dynamicSmemBytes = kFewSmem;
+    cfg.dynamicSmemBytes = FewPlan<kRows>::kSmem;
     cfg.stream = s;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
@@ -933,6 +943,7 @@ cudaLaunchConfig_t few_config(unsigned ctas, int cluster, cudaLaunchAttribute (&
 }
 
 // Clusters of `size` CTAs that the current device holds at once (looked up once per device).
+template <int kRows>
 int few_clusters(int size)
 {
     static std::mutex mu;
@@ -943,30 +954,31 @@ int few_clusters(int size)
     int& n = known[dev][size];
     if (n == 0) {
         cudaLaunchAttribute attr[2];
-        const cudaLaunchConfig_t cfg = few_config((unsigned)size, size, attr, nullptr);
-        if (ensure_dynamic_smem(reinterpret_cast<const void*>(rows_few_kernel), (int)kFewSmem) != cudaSuccess ||
-            cudaOccupancyMaxActiveClusters(&n, rows_few_kernel, &cfg) != cudaSuccess || n <= 0)
+        const cudaLaunchConfig_t cfg = few_config<kRows>((unsigned)size, size, attr, nullptr);
+        if (ensure_dynamic_smem(reinterpret_cast<const void*>(rows_few_kernel<kRows>), (int)FewPlan<kRows>::kSmem) != cudaSuccess ||
+            cudaOccupancyMaxActiveClusters(&n, rows_few_kernel<kRows>, &cfg) != cudaSuccess || n <= 0)
             n = -1;
     }
     return n > 0 ? n : 0;
 }
 
 // CTAs per tile of the one-kernel form; 0 where the others take less time.
+template <int kRows>
 int few_split(const LinearRowsJob& job, const Layout& l)
 {
-    if (job.M > kFewRows) return 0;
     const int ks = (int)((job.K + BK - 1) / BK), tiles_of = job.swiglu ? 2 : 1;
     const long long groups = l.tiles / tiles_of;
     int best = 0;
     for (int split = 1; split * tiles_of <= kMaxCluster && split <= ks; ++split)
-        if (groups <= few_clusters(split * tiles_of)) best = split;
+        if (groups <= few_clusters<kRows>(split * tiles_of)) best = split;
     if (best == 0) return 0;
-    // A stage takes an SM 0.4 us; the three kernels share the stages evenly but take 3 us more.  (Measured, one row:
-    // 9216 x 3072 6.6 us against 8.4, 4096 x 14336 9.2 against 12.2, 2048 x 2048 4.8 against 6.0; 512 x 65536, whose
-    // tiles would keep 64 SMs, 13.1 us with three kernels.  Of eight rows' digits each CTA has too many to make:
-    // 9216 x 3072 9.0 us against 9.2, 4096 x 14336 15.2 against 12.5.)
-    const double stages = (double)l.tiles * ks / sm_count_current_device();
-    return (ks + best - 1) / best * 0.4 < stages * 0.4 + 3.0 ? best : 0;
+    // A stage takes an SM 0.4 us (0.75 with five to eight rows, whose digits every CTA makes for itself); the three
+    // kernels share the stages evenly but take 3 us more.  (Measured, one row: 9216 x 3072 6.4 us against 8.4,
+    // 4096 x 14336 8.8 against 12.2, 2048 x 2048 4.7 against 6.0; 512 x 65536, whose tiles would keep 64 SMs, 13.1 us
+    // with three kernels.  Eight rows: 2048 x 2048 5.8 us against 5.7 and from Python 8.5
+    // against 12.6, 9216 x 3072 8.3 against 7.9 and 9.0 against 12.9, 4096 x 14336 15.2 against 12.0.)
+    const double stages = (double)l.tiles * ks / sm_count_current_device(), stage = kRows == 4 ? 0.4 : 0.75;
+    return (ks + best - 1) / best * stage < stages * 0.4 + 3.0 ? best : 0;
 }
 
 // The maps of the weights' codes and scales.
@@ -979,11 +991,12 @@ bool weight_maps(const LinearRowsJob& job, const Layout& l, CUtensorMap* codes, 
                        kSfBox / 256, CU_TENSOR_MAP_SWIZZLE_NONE);
 }
 
+template <int kRows>
 cudaError_t launch_few(const LinearRowsJob& job, const Layout& l, const JoinParams& jp, int split, cudaStream_t s)
 {
     CUtensorMap tmW, tmSfw;
     if (!weight_maps(job, l, &tmW, &tmSfw)) return cudaErrorInvalidValue;
-    const cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void*>(rows_few_kernel), (int)kFewSmem);
+    const cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void*>(rows_few_kernel<kRows>), (int)FewPlan<kRows>::kSmem);
     if (e != cudaSuccess) return e;
     FewParams p{};
     p.x = job.x;
@@ -996,8 +1009,8 @@ cudaError_t launch_few(const LinearRowsJob& job, const Layout& l, const JoinPara
     p.wait_ns = job.wait_limit_ns;
     p.stall = job.stall;
     cudaLaunchAttribute attr[2];
-    const cudaLaunchConfig_t cfg = few_config((unsigned)(l.tiles * split), job.swiglu ? 2 * split : split, attr, s);
-    return cudaLaunchKernelEx(&cfg, rows_few_kernel, tmW, tmSfw, p);
+    const cudaLaunchConfig_t cfg = few_config<kRows>((unsigned)(l.tiles * split), job.swiglu ? 2 * split : split, attr, s);
+    return cudaLaunchKernelEx(&cfg, rows_few_kernel<kRows>, tmW, tmSfw, p);
 }
 
 template <int NB>
@@ -1038,7 +1051,11 @@ cudaError_t launch_linear_rows(const LinearRowsJob& job, cudaStream_t s)
     jp.N = job.N;
     jp.swiglu = job.swiglu;
     jp.M = (int)job.M;
-    if (const int split = few_split(job, l)) return launch_few(job, l, jp, split, s);
+    if (job.M <= 4) {
+        if (const int split = few_split<4>(job, l)) return launch_few<4>(job, l, jp, split, s);
+    } else if (job.M <= kFewRows) {
+        if (const int split = few_split<8>(job, l)) return launch_few<8>(job, l, jp, split, s);
+    }
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

@@ -15,7 +15,7 @@ __all__ = ["failures"]
 class Model:
     def __init__(self, rng, rows, n, stages, together):
         self.rng, self.n, self.stages, self.together = rng, n, stages, together
-        self.row_warps = 4 if rows > 2 else rows
+        self.row_warps = 8 if rows > 4 else 4 if rows > 2 else rows
         self.full = [Bar(1 + 4 + self.row_warps, f"full {i}") for i in range(stages)]
         self.sf_full = [Bar(1 + self.row_warps, f"sf_full {i}") for i in range(stages)]
         self.empty = [Bar(1, f"empty {i}") for i in range(stages)]
@@ -137,11 +137,11 @@ class Model:
         need(self.done == self.n, "stages left over")
 
 
-def failures(runs, stages, together, seed=1):
-    """What went wrong in so many runs of random rows and stages: {message: count}."""
+def failures(runs, rows_of, stages, together, seed=1):
+    """What went wrong in so many runs of some of these rows and random stages: {message: count}."""
     rng, found = random.Random(seed), {}
     for _ in range(runs):
-        rows = rng.choice((1, 2, 3, 4))
+        rows = rng.choice(rows_of)
         try:
             Model(rng, rows, rng.choice([1, 2, 5, 7, 13, 24, 40]), stages, together).run()
         except Broken as e:

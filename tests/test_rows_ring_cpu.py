@@ -9,21 +9,26 @@ ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 RUNS = 300
 
 
+FEW, MORE = (1, 2, 3, 4), (5, 6, 8)
+
+
 def kernel():
-    """Stages, and how many stages' scales go together, as the kernel's source has them."""
+    """Stages of the two forms, and how many stages' scales go together, as the kernel's source has them."""
     text = open(os.path.join(ROOT, "audio_dit_gb300", "csrc", "h3fp4_linear_rows.cu")).read()
-    stages = int(re.search(r"kFewStages = (\d);", text).group(1))
+    few, more = (int(n) for n in re.search(r"kStages = kRows == 4 \? (\d) : (\d);", text).groups())
     together = int(re.search(r"kTogether = (\d);", text).group(1))
     assert "every = 8 / row_warps, i0 = w / row_warps" in text
-    assert "row_warps = M > 2 ? 4 : M;" in text
+    assert "row_warps = kRows == 8 ? 8 : M > 2 ? 4 : M;" in text
     assert "1 + 4 + row_warps" in text and "mbar_init(&sf_full[i], 1 + row_warps)" in text
-    return stages, together
+    return few, more, together
 
 
 def test_the_kernels_waits():
-    assert failures(RUNS, *kernel()) == {}
+    few, more, together = kernel()
+    assert failures(RUNS, FEW, few, together) == {}
+    assert failures(RUNS, MORE, more, together) == {}
 
 
 def test_slots_have_to_be_one_warps():
     """A warp that skips fills of a slot takes one that is in use for free: seen as a launch failure with six stages."""
-    assert failures(RUNS, 6, kernel()[1]) != {}
+    assert failures(RUNS, FEW, 6, kernel()[2]) != {}
