@@ -129,8 +129,14 @@ __device__ __forceinline__ uint32_t top_bits(const uint4& v)
 // The exponent of the digits' unit where the largest magnitude is `top`: it lies in [2, 4) of them.
 __device__ __forceinline__ int unit_of(uint32_t top) { return max(1, (int)(top >> 7)) - 127 - 1; }
 
-// 2^(e_row - 8), what the sums of a row's digits are in (either factor may be subnormal together).
-__device__ __forceinline__ float row_factor(int e_row) { return pow2i(e_row / 2) * pow2i(e_row - e_row / 2 - 8); }
+// 2^(e_row - 8), what the sums of a row's digits are in (either factor may be subnormal together); NaN where the
+// row holds an infinity or a NaN, which digits cannot say.
+__device__ __forceinline__ float row_factor(uint32_t top)
+{
+    if (top >= 0x7F80u) return __int_as_float(0x7FFFFFFF);
+    const int e_row = unit_of(top);
+    return pow2i(e_row / 2) * pow2i(e_row - e_row / 2 - 8);
+}
 
 // The digits of a lane's eight elements of x, eight codes a word; the scale of its block of 16, which it
 // shares with the lane beside it: binades below the row's, as far as E4M3 goes (2^8 down to 2^-9).
@@ -215,7 +221,7 @@ __global__ void __launch_bounds__(kDigitThreads)
 #pragma unroll
     for (int i = 0; i < kDigitThreads / 32; ++i) top = max(top, tops[i]);
     const int e_row = unit_of(top);
-    if (blockIdx.x == 0 && t == 0) factors[m] = row_factor(e_row);
+    if (blockIdx.x == 0 && t == 0) factors[m] = row_factor(top);
     const int col = blockIdx.x * kDigitColumns + 8 * t;
     const bool real = col < K;
     uint4 v = make_uint4(0, 0, 0, 0);
@@ -882,7 +888,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
         auto factor = [&](int row) {   // (the barrier of the digits was behind what the warps read)
             uint32_t top = 0;
             for (int k = row; k < 8; k += row_warps) top = max(top, tops[k]);
-            return row_factor(unit_of(top));
+            return row_factor(top);
         };
         const uint32_t to = mapa_shared(smem_u32(red), 0) + 4u * (uint32_t)(rank * kRows * BM + o);
 #pragma unroll

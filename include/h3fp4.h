@@ -476,7 +476,7 @@ H3FP4_API h3fp4_status h3fp4_block_norm(const void* x_bf16, const void* y_bf16, 
  * ("H3 Blackwell Runtime" README, "Checkpoints": pre-quantised weights).  Sums are fp32; x
  * enters with an error of at most 2^-22 of the largest magnitude of its block of 16, or 2^-40
  * of its row's.
- *   x: bf16 [M][K], finite, 1 <= M <= H3FP4_ROWS_MAX; K % 64 == 0, K <= 2^16; N % 8 == 0,
+ *   x: bf16 [M][K] (a row with an infinity or a NaN gives NaN), 1 <= M <= H3FP4_ROWS_MAX; K % 64 == 0, K <= 2^16; N % 8 == 0,
  *      N <= 2^24.
  *   w_codes, w_sf, w_gscale: output of h3fp4_quantize_weight.
  *   flags: H3FP4_EPI_BIAS (bias bf16 [N]); H3FP4_EPI_GATE_RESID (gate fp32, row m's at

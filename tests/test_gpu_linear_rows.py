@@ -150,6 +150,25 @@ def test_ranges_and_zero_rows():
     assert not bool(out[4].any())
 
 
+@pytest.mark.parametrize("M,N,K,swiglu", [(3, 256, 1024, False), (7, 512, 512, True), (20, 384, 2112, False), (40, 256, 320, True)])
+def test_rows_that_are_not_finite(M, N, K, swiglu):
+    """They are NaN, and the others have the bits that they have without them."""
+    import audio_dit_gb300 as A
+    torch.manual_seed(M)
+    x, w = torch.randn(M, K, device="cuda").bfloat16(), (torch.randn(N, K, device="cuda") * 0.05).bfloat16()
+    wq = A.alloc_nvfp4(N, K)
+    A.h3fp4_quantize_weight(w, *wq, A.alloc_workspace(256, N, K))
+    ws = A.alloc_rows_workspace(M, N, K)
+    good, bad = (torch.empty(M, N // 2 if swiglu else N, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    A.h3fp4_linear_rows(x, *wq, good, ws, swiglu=swiglu)
+    x[0, K - 1], x[M - 1, 5], x[M // 2, 0] = float("nan"), float("inf"), float("-inf")
+    A.h3fp4_linear_rows(x, *wq, bad, ws, swiglu=swiglu)
+    A.h3fp4_check(ws)
+    rest = [m for m in range(M) if m not in (0, M // 2, M - 1)]
+    assert bool(bad[[0, M // 2, M - 1]].isnan().all()) and bool(good.isfinite().all())
+    assert torch.equal(bad[rest].view(torch.int16), good[rest].view(torch.int16))
+
+
 def test_captured():
     import audio_dit_gb300 as A
     rng = np.random.default_rng(4)
