@@ -18,9 +18,9 @@
 // the same bits.
 //
 // Measured, calls back to back over three caches, of the measured 6793 GB/s: 64 tokens of 64
-// sequences over 524288 keys, 32 heads on 8 of 128, 112 us (5390 GB/s; the products, scores and
+// sequences over 524288 keys, 32 heads on 8 of 128, 113 us (5340 GB/s; the products, scores and
 // unpacking of two thirds of the issue slots beside the loads), one token over 131072 keys
-// 34.7 us (4360 GB/s: 3 us until the first keys are there, 4 us for the second kernel), 31 rows
+// 35.1 us (4310 GB/s: 3 us until the first keys are there, 4 us for the second kernel), 31 rows
 // of 6 sequences over 4433 keys, 28 heads on 4 of 64, 12.2 us (launches and latencies; the
 // bytes take 0.2).  Two CTAs of eight warps in place of four of four take 121 us for the first,
 // three CTAs an SM 117; shares by the order in which an SM's CTAs issue (the first ended at 86,
@@ -34,6 +34,7 @@
 // the column's largest).  The reference of the exponent follows the true maximum only when
 // that passed it by 2^14: p lies in f16's upper range, and those below 2^-30 of the largest
 // vanish.  Scores, sums and O are fp32.
+#include <algorithm>
 #include <cstdint>
 
 #include <cuda_bf16.h>
@@ -51,6 +52,7 @@ constexpr int kThreads = 32 * kWarps;
 constexpr int kStep = 2 * kCacheGroup;        // tokens that a warp takes at a time
 constexpr int kTile = kStep * kWarps;         // tokens of a tile
 constexpr int kPartCols = 16;                 // query columns of a unit at most
+constexpr uint32_t kSmemOfSm = 228 * 1024;
 constexpr int kMaxCtas = 608;                 // of a launch: the workspace is made for as many
 constexpr long long kNear = 2;                // tiles that a cut is moved by at most
 constexpr float kRaise = 14.0f, kStart = 6.0f;  // in powers of two: see above
@@ -623,14 +625,37 @@ __global__ void __launch_bounds__(kThreads, Config<W, kCols>::kCtasPerSm)
     uint32_t phases = 0;    // of the ring's barriers, one bit each
     bool lost = false;      // a wait ran out: nothing more is loaded or computed
     const int per_page = p.c.page / kCacheGroup;
+    // Of short units, of which this CTA has four and more whole ones, each warp takes some by itself (`solo`): their
+    // latencies, one after another, are what they cost (1024 sequences of 64 keys 159 -> 57 us).  Units of eight columns
+    // only: with 16 the registers that this takes cost more (10 % of 256 rows over 262144 keys).
+    constexpr bool kSolo = kCols == 8;
+    long long run_end = begin, next = begin;   // of a run of such units, and the warp's next one
     for (long long at = begin; at < end;) {
-        const int s = holder(at);
+        const bool solo = kSolo && at < run_end;
+        if (solo && next >= run_end) {
+            at = run_end;
+            continue;
+        }
+        const long long here = solo ? next : at;
+        const int s = holder(here);
         const Seq q = seqs[s];
         const int coltiles = col_tiles<kCols>(p, q), tiles = key_tiles(q);
-        const long long unit = div(at - prefix[s], tiles);
+        const long long unit = div(here - prefix[s], tiles);
+        if (kSolo && !solo && here == prefix[s] + unit * tiles && (long long)kWarps * tiles <= end - here) {
+            int to = s;   // sequences of as many tiles
+            while (to + 1 < nseq && prefix[to + 1] < end && key_tiles(seqs[to + 1]) == tiles) ++to;
+            const long long units = div(min(end, prefix[to + 1]) - here, tiles);
+            if (units >= kWarps) {
+                run_end = here + units * tiles;
+                next = here + (long long)warp * tiles;
+                continue;
+            }
+        }
+        if (solo) next += (long long)kWarps * tiles;
         const int h = (int)div(unit, coltiles), ct = (int)(unit - (long long)h * coltiles);
         const long long ubegin = prefix[s] + unit * tiles, uend = ubegin + tiles;
-        const int t0 = (int)(at - ubegin), t1 = (int)(min(end, uend) - ubegin);
+        const int t0 = (int)(here - ubegin), t1 = (int)(min(end, uend) - ubegin);
+        const bool begins = here == ubegin, whole = begins && uend <= end;
         // what each column attends to
         // (rows times heads of a call are below 2^31)
         const int cols = min(kCols, q.rows * p.group - ct * kCols);
@@ -663,15 +688,16 @@ __global__ void __launch_bounds__(kThreads, Config<W, kCols>::kCtasPerSm)
 
         // this warp's steps of 32 tokens: tile t's is 4 t + warp, up to the last token that any column sees
         const int steps = most > 0 ? (most - 1) / kStep + 1 : 0;
-        const int g0 = kWarps * t0 + warp;   // the first, then every fourth
+        const int every = solo ? 1 : kWarps, g0 = solo ? 0 : kWarps * t0 + warp;   // the first, and the stride
         int n = 0;
-        if (steps > g0) n = min(t1 - t0, (steps - g0 + kWarps - 1) / kWarps);
+        if (solo) n = steps;
+        else if (steps > g0) n = min(t1 - t0, (steps - g0 + kWarps - 1) / kWarps);
         const int32_t* table = p.c.table + (long long)s * p.c.max_pages;
         // where the groups of the next 16 steps lie, one per lane, and which of them the pool has
         const uint8_t* where = nullptr;
         uint32_t has = 0;
         auto look = [&](int i) {
-            const int gi = 2 * (g0 + kWarps * (i + (lane >> 1))) + (lane & 1);
+            const int gi = 2 * (g0 + every * (i + (lane >> 1))) + (lane & 1);
             int pg = -1;
             if ((uint32_t)gi * kCacheGroup < (uint32_t)most) pg = table[gi / per_page];
             const bool ok = pg >= 0 && pg < p.c.n_pages;
@@ -735,7 +761,8 @@ __global__ void __launch_bounds__(kThreads, Config<W, kCols>::kCtasPerSm)
         for (int j = 0; j < S::kO; ++j) st.o[j][0] = st.o[j][1] = st.o[j][2] = st.o[j][3] = 0.0f;
         // steps that all columns see whole, with scores that cannot leave fp32's range (a raw one is below 2^36)
         const bool tame = __all_sync(0xffffffffu, fabsf(factor[0]) < 1e26f && fabsf(factor[1]) < 1e26f);
-        const int plain = tame ? max(0, min(n, (least / kStep - g0 + kWarps - 1) / kWarps)) : 0;
+        const int whole_steps = max(0, least / kStep - g0);
+        const int plain = tame ? min(n, solo ? whole_steps : (whole_steps + kWarps - 1) / kWarps) : 0;
         int slot = 0;
 #pragma unroll 1
         for (int i = 0; i < n; ++i) {
@@ -758,7 +785,7 @@ __global__ void __launch_bounds__(kThreads, Config<W, kCols>::kCtasPerSm)
                     const int left[2] = {kCacheGroup, kCacheGroup}, lim[2][2] = {};
                     step<W, kCols, false>(st, gp, lane, qf, factor, left, lim);
                 } else if (two) {
-                    const int first = (g0 + kWarps * i) * kStep;
+                    const int first = (g0 + every * i) * kStep;
                     int left[2], lim[2][2];
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
@@ -784,7 +811,7 @@ __global__ void __launch_bounds__(kThreads, Config<W, kCols>::kCtasPerSm)
 #pragma unroll
         for (int i = 0; i < 2; ++i) st.l[i] = over_lanes<kCols>(st.l[i], [](float a, float b) { return a + b; });
 #pragma unroll
-        for (int with = kWarps / 2; with >= 1; with >>= 1) {
+        for (int with = solo ? 0 : kWarps / 2; with >= 1; with >>= 1) {
             float* other = merge + (warp & (with - 1)) * (C::kMergeRegs * 32) + lane;
             __syncthreads();
             if (warp >= with && warp < 2 * with) {
@@ -809,9 +836,8 @@ __global__ void __launch_bounds__(kThreads, Config<W, kCols>::kCtasPerSm)
                 }
             }
         }
-        if (warp == 0) {
-            const bool whole = at == ubegin && uend <= end;
-            float* part = reinterpret_cast<float*>(p.ws + kPartOff) + (2ll * blockIdx.x + (at == ubegin ? 1 : 0)) * Part<W>::kFloats;
+        if (warp == 0 || solo) {
+            float* part = reinterpret_cast<float*>(p.ws + kPartOff) + (2ll * blockIdx.x + (begins ? 1 : 0)) * Part<W>::kFloats;
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 const int col = mycol[i];
@@ -852,14 +878,14 @@ __global__ void __launch_bounds__(kThreads, Config<W, kCols>::kCtasPerSm)
                     }
                 }
             }
-            if (at == ubegin && (p.by_unit || !whole)) {
+            if (begins && (p.by_unit || !whole)) {
                 const long long i = p.by_unit ? units_before(s) + unit : blockIdx.x;
                 const int count = whole ? 0 : shares.owner_of_last(ubegin, uend) - (int)blockIdx.x + 1;
                 // (row offsets that overlap make more units than there can be)
                 if (lane == 0 && i < kMaxCtas) cuts[i] = Cut{q.first, h, ct * kCols, cols, (int)blockIdx.x, count};
             }
         }
-        at = ubegin + t1;
+        if (!solo) at = ubegin + t1;
     }
 }
 
@@ -970,7 +996,9 @@ cudaError_t launch(AttnParams p, cudaStream_t s)
     using C = Config<W, kCols>;
     const cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void*>(cache_attn_kernel<W, kCols>), (int)C::smem(kCacheMaxSeqs));
     if (e != cudaSuccess) return e;
-    int ctas = sm_count_current_device() * C::kCtasPerSm;
+    // as many as an SM holds beside a table of so many sequences (a second wave of CTAs would take as long again)
+    const int held = std::max(1, std::min(C::kCtasPerSm, (int)(kSmemOfSm / (C::smem(p.c.nseq) + 1024))));
+    int ctas = sm_count_current_device() * held;
     if (ctas > kMaxCtas) ctas = kMaxCtas;
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[1];

@@ -195,6 +195,10 @@ ATTN = [  # lengths, rows, heads of q and kv, D, page, causal
     ([128 * 1217 - 5], [1], 4, 1, 64, 64, True),
     ([18 + i % 40 for i in range(1024)], [1] * 1024, 4, 2, 256, 16, True),   # the most sequences
     ([40] * 1024, [2] * 1024, 16, 4, 64, 16, True),
+    ([1 + i * 37 % 128 for i in range(700)], [1] * 700, 16, 4, 128, 32, True),  # many short units, which warps take alone
+    ([1 + i * 53 % 600 for i in range(300)], [1] * 300, 8, 8, 64, 16, False),
+    ([130] * 500 + [5] * 300 + [0] * 20 + [257] * 200, [1] * 1020, 4, 1, 128, 64, True),
+    ([64] * 400, [2] * 400, 8, 2, 256, 16, True),
 ]
 
 
