@@ -544,6 +544,7 @@ __global__ void __launch_bounds__(kThreads, Config<W, kCols>::kCtasPerSm)
         const int per = (nseq + kThreads - 1) / kThreads, s0 = min(nseq, (int)threadIdx.x * per), s1 = min(nseq, s0 + per);
         auto tiles = [&](const Seq& q) { return (long long)p.c.Hkv * col_tiles<kCols>(p, q) * key_tiles(q); };
         long long mine = 0;
+#pragma unroll 4
         for (int s = s0; s < s1; ++s) {
             const Seq q = sequence(p, s);
             seqs[s] = q;
