@@ -138,6 +138,10 @@ __device__ __forceinline__ float row_factor(uint32_t top)
     return pow2i(e_row / 2) * pow2i(e_row - e_row / 2 - 8);
 }
 
+// y s f of a row's sum of digits y, the weight's global scale s and the row's factor f.  The two scales may lie at
+// opposite ends of the range: y (below 2^40) meets first whichever keeps it inside, so that what fits fp32 comes out.
+__device__ __forceinline__ float scaled(float y, float s, float f) { return f >= 1.0f ? y * s * f : y * f * s; }
+
 // The digits of a lane's eight elements of x, eight codes a word; the scale of its block of 16, which it
 // shares with the lane beside it: binades below the row's, as far as E4M3 goes (2^8 down to 2^-9).
 struct Digits {
@@ -632,7 +636,7 @@ __global__ void __launch_bounds__(BM) rows_join_kernel(const __grid_constant__ J
 #pragma unroll
         for (int t = 0; t < kTiles; ++t)
 #pragma unroll
-            for (int k = 0; k < kRows; ++k) y[t][k] = fmaf(y[t][k] * s, f[k], bias[t]);
+            for (int k = 0; k < kRows; ++k) y[t][k] = scaled(y[t][k], s, f[k]) + bias[t];
     };
     if (p.swiglu) {
         float y[2][kRows];
@@ -863,15 +867,15 @@ __global__ void __launch_bounds__(kFewThreads, 1)
             v = next;
         }
     }
-    // what the first CTA's last four warps need for the outputs
+    // what the last four warps need, most of it the first CTA's for the outputs
     const int o = (int)threadIdx.x - 12 * 32;
     const long long out0 = (p.j.swiglu ? 2ll * group : (long long)tile) * BM + o;   // the first tile's row of W
     float s = 0.0f, bias[2] = {0.0f, 0.0f}, gate[kRows], resid[kRows];
     if (warp >= 12) {
         // ------------------------------------------------------------ sums to the cluster's first CTA
         const int quarter = warp & 3;
+        s = *p.j.w_gscale;
         if (rank == 0) {
-            s = *p.j.w_gscale;
             if (p.j.bias && out0 < p.j.N) bias[0] = __bfloat162float(p.j.bias[out0]);
             if (p.j.bias && p.j.swiglu) bias[1] = __bfloat162float(p.j.bias[out0 + BM]);
 #pragma unroll
@@ -898,7 +902,8 @@ __global__ void __launch_bounds__(kFewThreads, 1)
             four_rows(tmem + ((32u * (uint32_t)quarter) << 16) + 8 * m0, y);
 #pragma unroll
             for (int h = 0; h < 4; ++h)
-                if (m0 + h < M) st_shared_cluster_u32(to + 4u * (uint32_t)((m0 + h) * BM), __float_as_uint(y[h] * factor(m0 + h)));
+                if (m0 + h < M)
+                    st_shared_cluster_u32(to + 4u * (uint32_t)((m0 + h) * BM), __float_as_uint(scaled(y[h], s, factor(m0 + h))));
         }
     }
     __syncwarp();
@@ -913,7 +918,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
     auto value = [&](int first, int m, float b) {
         float y = 0.0f;
         for (int r = first; r < first + p.split; ++r) y += red[(r * kRows + m) * BM + o];
-        return fmaf(y, s, b);
+        return y + b;
     };
 #pragma unroll
     for (int m = 0; m < kRows; ++m) {
