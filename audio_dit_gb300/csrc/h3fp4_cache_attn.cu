@@ -599,8 +599,9 @@ __global__ void __launch_bounds__(kThreads, Config<W, kCols>::kCtasPerSm)
         const Seq q = seqs[s];
         if (q.len > 0) continue;
         const int vecs = p.c.D / 8;
-        for (long long i = threadIdx.x; i < (long long)q.rows * p.Hq * vecs; i += kThreads) {
-            const long long r = q.first + i / (p.Hq * vecs);
+        const long long of_row = (long long)p.Hq * vecs;   // (past 32 bits from 2^26 heads of 256 on)
+        for (long long i = threadIdx.x; i < q.rows * of_row; i += kThreads) {
+            const long long r = q.first + i / of_row;
             const int h = (int)(i / vecs % p.Hq), v = (int)(i % vecs);
             *reinterpret_cast<uint4*>(p.out + r * p.out_row + (long long)h * p.out_head + 8 * v) = make_uint4(0, 0, 0, 0);
             if (p.lse && v == 0) p.lse[r * p.Hq + h] = -INFINITY;
