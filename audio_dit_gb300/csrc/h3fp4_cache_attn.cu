@@ -381,9 +381,38 @@ __device__ __forceinline__ void scores(float (&s)[2][4], const uint8_t* gp, int 
     }
 }
 
-// O += P V of one group, token pairs 8 half + 2 c + (0, 1).  kMasked: `left` tokens of it hold anything.
+// NaN into the outputs of the columns that see a token whose block of V is NaN, of a group in the pool: of the lane's
+// two columns, `lim` tokens of it each.
+template <int W, int kCols>
+__device__ __forceinline__ void nan_values(State<W, kCols>& st, const uint8_t* gp, int lane, const int (&lim)[2])
+{
+    constexpr int kRuns = kCols == 16 ? 2 : 1, kVBlocks = W == 256 ? 2 : 1;   // of the lane's elements, of a run
+    const int g = lane >> 2, c = lane & 3;
+#pragma unroll
+    for (int run = 0; run < kRuns; ++run)
+#pragma unroll
+        for (int b = 0; b < kVBlocks; ++b) {
+            const int block = ((kCols == 16 ? 2 * c + run : g) * (W / 8) >> 4) + b;
+            const uint8_t* scale = gp + CacheLayout<W>::kVScale + block * 16;   // 16 tokens'
+            int first = kCacheGroup;                                           // the first that is NaN
+#pragma unroll 1
+            for (int t = kCacheGroup - 1; t >= 0; --t)
+                if ((scale[((t & 7) >> 1) * 4 + (t >> 3) * 2 + (t & 1)] & 0x7Fu) == 0x7Fu) first = t;
+#pragma unroll
+            for (int j = 0; j < State<W, kCols>::kO; ++j)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if ((kCols == 8 || (i & 1) == run) && (kCols == 16 ? j >> 4 : j >> 3) == b &&
+                        first < min(kCacheGroup, lim[column_of<kCols>(i)]))
+                        st.o[j][i] = __int_as_float(0x7FFFFFFF);
+        }
+}
+
+// O += P V of one group, token pairs 8 half + 2 c + (0, 1).  kMasked: `left` tokens of it hold anything; blocks that
+// are NaN count as zeros and are reported.
 template <int W, int kCols, bool kMasked>
-__device__ __forceinline__ void values(State<W, kCols>& st, const uint8_t* gp, int lane, const uint32_t (&pf)[kCols / 4], int left)
+__device__ __forceinline__ void values(State<W, kCols>& st, const uint8_t* gp, int lane, const uint32_t (&pf)[kCols / 4], int left,
+                                       bool& nan)
 {
     using L = CacheLayout<W>;
     const int g = lane >> 2, c = lane & 3;
@@ -404,6 +433,16 @@ __device__ __forceinline__ void values(State<W, kCols>& st, const uint8_t* gp, i
             for (int b = 0; b < kVBlocks; ++b) {
                 const int t = 8 * half + 2 * c;
                 vs[half][b] &= (t < left ? 0xFFFFu : 0u) | (t + 1 < left ? 0xFFFF0000u : 0u);
+            }
+        // (a product of NaN with a p of zero would be NaN for columns that do not see the token)
+#pragma unroll
+        for (int half = 0; half < 2; ++half)
+#pragma unroll
+            for (int b = 0; b < kVBlocks; ++b) {
+                const uint32_t v = vs[half][b] & 0x7FFF7FFFu;
+                const uint32_t bad = (v & 0xFFFFu) > 0x7C00u ? 0xFFFFu : 0u, bad2 = v > 0x7C00FFFFu ? 0xFFFF0000u : 0u;
+                nan |= (bad | bad2) != 0;
+                vs[half][b] &= ~(bad | bad2);
             }
     }
     uint32_t w[2][4 * kVBlocks];
@@ -446,7 +485,7 @@ __device__ __forceinline__ void values(State<W, kCols>& st, const uint8_t* gp, i
 // attended to by the lane's two columns; scores that leave fp32's range downwards stay finite.
 template <int W, int kCols, bool kMasked>
 __device__ __forceinline__ void step(State<W, kCols>& st, const uint8_t* gp, int lane, const uint32_t (&qf)[W / 16][kCols / 4],
-                                     const float (&factor)[2], const int (&left)[2], const int (&lim)[2][2])
+                                     const float (&factor)[2], const int (&left)[2], const int (&lim)[2][2], bool& nan)
 {
     constexpr int kF = kCols / 8;   // fragments of four scores a group
     const int g = lane >> 2, c = lane & 3;
@@ -502,7 +541,7 @@ __device__ __forceinline__ void step(State<W, kCols>& st, const uint8_t* gp, int
             for (int h = 0; h < 2; ++h)
                 asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %0;" : "+r"(pf[h]));
         }
-        values<W, kCols, kMasked>(st, gp + e * CacheLayout<W>::kGroupBytes, lane, pf, left[e]);
+        values<W, kCols, kMasked>(st, gp + e * CacheLayout<W>::kGroupBytes, lane, pf, left[e], nan);
     }
 }
 
@@ -766,6 +805,7 @@ __global__ void __launch_bounds__(kThreads, Config<W, kCols>::kCtasPerSm)
         const int whole_steps = max(0, least / kStep - g0);
         const int plain = tame ? min(n, solo ? whole_steps : (whole_steps + kWarps - 1) / kWarps) : 0;
         int slot = 0;
+        bool nan = false;   // a masked step left out blocks of V that are NaN
 #pragma unroll 1
         for (int i = 0; i < n; ++i) {
             {
@@ -785,7 +825,7 @@ __global__ void __launch_bounds__(kThreads, Config<W, kCols>::kCtasPerSm)
                 const uint8_t* gp = ring + slot * C::kSlot;
                 if (i < plain && two == 3u) {
                     const int left[2] = {kCacheGroup, kCacheGroup}, lim[2][2] = {};
-                    step<W, kCols, false>(st, gp, lane, qf, factor, left, lim);
+                    step<W, kCols, false>(st, gp, lane, qf, factor, left, lim, nan);
                 } else if (two) {
                     const int first = (g0 + every * i) * kStep;
                     int left[2], lim[2][2];
@@ -796,7 +836,7 @@ __global__ void __launch_bounds__(kThreads, Config<W, kCols>::kCtasPerSm)
                         lim[e][0] = here ? mylim[0] - first - e * kCacheGroup : 0;
                         lim[e][1] = here ? mylim[1] - first - e * kCacheGroup : 0;
                     }
-                    step<W, kCols, true>(st, gp, lane, qf, factor, left, lim);
+                    step<W, kCols, true>(st, gp, lane, qf, factor, left, lim, nan);
                 }
                 // (the products that used the slot's last bytes have been issued, so these were read)
                 __syncwarp();
@@ -808,6 +848,17 @@ __global__ void __launch_bounds__(kThreads, Config<W, kCols>::kCtasPerSm)
             }
         }
         __syncwarp();
+        // blocks of V that are NaN, for the columns that see their tokens (looked for again in the pool: hardly ever)
+        if (__any_sync(0xffffffffu, nan))
+#pragma unroll 1
+            for (int k = 0; k < 2 * n; ++k) {
+                const int gi = 2 * (g0 + every * (k >> 1)) + (k & 1);
+                const int pg = (uint32_t)gi * kCacheGroup < (uint32_t)most ? table[gi / per_page] : -1;
+                if (pg < 0 || pg >= p.c.n_pages) continue;
+                const int lim[2] = {mylim[0] - gi * kCacheGroup, mylim[1] - gi * kCacheGroup};
+                nan_values<W, kCols>(st, p.c.pool + (((long long)pg * p.c.Hkv + h) * per_page + gi % per_page) * L::kGroupBytes,
+                                     lane, lim);
+            }
 
         // ------------------------------------------------------------ the warps' sums into warp 0
 #pragma unroll

@@ -74,7 +74,7 @@ __device__ __forceinline__ uint32_t encode(const V16& v, float s, uint32_t (&w)[
     unpack16(v, f);
     float top = 0.0f;
 #pragma unroll
-    for (int k = 0; k < 16; k += 2) top = max3(top, fabsf(f[k]), fabsf(f[k + 1]));
+    for (int k = 0; k < 16; k += 2) top = max3_nan(top, fabsf(f[k]), fabsf(f[k + 1]));   // (a NaN stays: E4M3's scale is NaN)
     const uint32_t S = cvt_e4m3(__fdiv_rn(__fmul_rn(top, 1.0f / 6.0f), s));
     const float rcp = block_rcp(S, s);
 #pragma unroll

@@ -616,6 +616,14 @@ __device__ __forceinline__ float max3(float a, float b, float c)
     return d;
 }
 
+// The same, NaN where any of them is.
+__device__ __forceinline__ float max3_nan(float a, float b, float c)
+{
+    float d;
+    asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+
 // The hardware's approximate 2^x and 1/x (PTX ex2.approx.f32, rcp.approx.f32;
 // no .ftz, so subnormal arguments and results keep their values).
 __device__ __forceinline__ float ex2_approx(float x)

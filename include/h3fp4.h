@@ -539,7 +539,8 @@ H3FP4_API size_t h3fp4_cache_page_bytes(int heads, int dim, int page);
 /* Writes the rows k, v [M][heads][dim] (views as for the attention calls) to their
  * places in the cache, quantised as h3fp4_quantize_act does with H3FP4_GSCALE_GIVEN
  * and the head's global scale, but with bmax * RN(1/6) for bmax / 6 ("H3 Runtime Current State", "Owned Performance
- * Kernels": tensor scale/QDATA; the pages have no cache).  Inputs must be finite.
+ * Kernels": tensor scale/QDATA; the pages have no cache).  A block of 16 with a NaN
+ * is held as NaN, an infinity as the largest that its head's scale allows.
  * The places of a call's rows must differ, and neither sequences of one call nor calls
  * that run at the same time may write to the same page.  0 <= M <= 2^31 - 256. */
 H3FP4_API h3fp4_status h3fp4_cache_append(const h3fp4_heads* k, const h3fp4_heads* v, int64_t M,
@@ -561,6 +562,7 @@ H3FP4_API h3fp4_status h3fp4_cache_read(const h3fp4_heads* k, const h3fp4_heads*
  *   Scores, statistics and sums are fp32; keys and values enter as they are held, q
  *   unrounded (elements below 2^-31 of the largest of their row and head are rounded),
  *   the p_j rounded to fp16 for their product with V.
+ *   Keys and values that are NaN count for the rows that attend to them alone.
  *   A row without a key gives out = 0 and lse = -inf; one whose largest score
  *   scale * log2(e) * (q . k) is beyond 3e38 either way is NaN.
  *   scale > 0, scale * log2(e) finite.  lse: fp32 [M][Hq], 4-byte aligned, or NULL.
