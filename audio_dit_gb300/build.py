@@ -20,7 +20,7 @@ SOURCES = ["h3fp4_api.cu", "h3fp4_quant.cu", "h3fp4_gemm.cu", "h3fp4_peak.cu", "
            "h3fp4_heads_api.cu", "h3fp4_norm_rope.cu", "h3fp4_attn.cu", "h3fp4_token_api.cu", "h3fp4_block_norm.cu",
            "h3fp4_kv_cache.cu", "h3fp4_cache_attn.cu", "h3fp4_linear_rows.cu"]
 HEADERS = ["h3fp4_internal.h", "ptx_sm103.cuh", "nvfp4_encode.cuh", "act_prologue.cuh", "h3fp4_heads.h", "tensor_map.h",
-           "attn_plan.h", "h3fp4_token.h", "kv_cache.cuh"]
+           "attn_plan.h", "h3fp4_token.h", "kv_cache.cuh", "spans.h"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -5,6 +5,7 @@
 #include <cstdint>
 
 #include "h3fp4_token.h"
+#include "spans.h"
 
 namespace h3fp4 {
 namespace {
@@ -18,6 +19,13 @@ bool overlap(const void* a, uint64_t a_bytes, const void* b, uint64_t b_bytes)
 bool overlap(const void* a, const void* b, int64_t bytes)
 {
     return overlap(a, (uint64_t)bytes, b, (uint64_t)bytes);
+}
+
+Span run(const void* p, uint64_t bytes) { return Span{p, 1, 0, 1, 0, p ? bytes : 0}; }
+
+Span view(const h3fp4_heads& t, int64_t rows, int64_t heads, int D)
+{
+    return Span{t.ptr, rows, 2 * t.row_stride, heads, 2 * t.head_stride, 2 * (uint64_t)D};
 }
 
 bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
@@ -52,6 +60,17 @@ h3fp4_status cache_view(const h3fp4_cache* c, int64_t M, CacheView* out)
     return H3FP4_OK;
 }
 
+// Whether `s`, which a call writes, shares memory with the cache's pool or what describes its sequences.
+bool overlaps_cache(const Span& s, const CacheView& c)
+{
+    const uint64_t page = h3fp4_cache_page_bytes(c.Hkv, c.D, c.page), heads = 4 * (uint64_t)c.Hkv;
+    for (const Span& o : {run(c.pool, (uint64_t)c.n_pages * page), run(c.table, 4 * (uint64_t)c.nseq * (uint64_t)c.max_pages),
+                          run(c.length, 4 * (uint64_t)c.nseq), run(c.row_off, 4 * ((uint64_t)c.nseq + 1)),
+                          run(c.k_gscale, heads), run(c.v_gscale, heads)})
+        if (overlap(s, o)) return true;
+    return false;
+}
+
 h3fp4_status cache_rows(const h3fp4_heads* k, const h3fp4_heads* v, int64_t M, const h3fp4_cache* cache, bool read,
                         cudaStream_t stream)
 {
@@ -60,7 +79,13 @@ h3fp4_status cache_rows(const h3fp4_heads* k, const h3fp4_heads* v, int64_t M, c
     if (st != H3FP4_OK) return st;
     for (const h3fp4_heads* t : {k, v})
         if ((st = read ? check_out(t, M, job.c.Hkv, job.c.D) : check_in(t, M)) != H3FP4_OK) return st;
-    if (read && M > 0 && k->ptr == v->ptr) return H3FP4_ERR_INVALID;
+    if (M > 0) {
+        const Span rows[] = {view(*k, M, job.c.Hkv, job.c.D), view(*v, M, job.c.Hkv, job.c.D)};
+        const Span pool = run(job.c.pool, (uint64_t)job.c.n_pages * h3fp4_cache_page_bytes(job.c.Hkv, job.c.D, job.c.page));
+        if (read && overlap(rows[0], rows[1])) return H3FP4_ERR_INVALID;
+        for (const Span& s : rows)
+            if (read ? overlaps_cache(s, job.c) : overlap(s, pool)) return H3FP4_ERR_INVALID;
+    }
     if ((st = check_device()) != H3FP4_OK) return st;
     if (M == 0) return H3FP4_OK;
     job.k = in(k);
@@ -257,7 +282,15 @@ h3fp4_status h3fp4_cache_attn(const h3fp4_heads* q, int64_t M, int Hq, const h3f
     if ((st = check_in(q, M)) != H3FP4_OK || (st = check_out(out, M, Hq, job.c.D)) != H3FP4_OK) return st;
     if (!ws || ws_bytes < cache_attn_workspace_bytes(job.c.D)) return H3FP4_ERR_INVALID;
     if (!aligned16(ws) || !aligned4(lse)) return H3FP4_ERR_ALIGN;
-    if (M > 0 && out->ptr == q->ptr) return H3FP4_ERR_INVALID;
+    if (M > 0) {
+        const Span qs = view(*q, M, Hq, job.c.D), outs = view(*out, M, Hq, job.c.D);
+        const Span sums = run(lse, 4 * (uint64_t)M * (uint64_t)Hq), work = run(ws, cache_attn_workspace_bytes(job.c.D));
+        if (overlap(outs, qs) || overlap(sums, qs) || overlap(work, qs) || overlap(outs, sums) || overlap(outs, work) ||
+            overlap(sums, work))
+            return H3FP4_ERR_INVALID;
+        for (const Span& s : {outs, sums, work})
+            if (overlaps_cache(s, job.c)) return H3FP4_ERR_INVALID;
+    }
     if ((st = check_device()) != H3FP4_OK) return st;
     if (M == 0) return H3FP4_OK;
     job.q = in(q);

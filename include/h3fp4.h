@@ -542,13 +542,15 @@ H3FP4_API size_t h3fp4_cache_page_bytes(int heads, int dim, int page);
  * Kernels": tensor scale/QDATA; the pages have no cache).  A block of 16 with a NaN
  * is held as NaN, an infinity as the largest that its head's scale allows.
  * The places of a call's rows must differ, and neither sequences of one call nor calls
- * that run at the same time may write to the same page.  0 <= M <= 2^31 - 256. */
+ * that run at the same time may write to the same page.  k and v lie outside the pool.
+ * 0 <= M <= 2^31 - 256. */
 H3FP4_API h3fp4_status h3fp4_cache_append(const h3fp4_heads* k, const h3fp4_heads* v, int64_t M,
                                           const h3fp4_cache* cache, cudaStream_t stream);
 
 /* The way back: k, v [M][heads][dim] (outputs) receive bf16(e2m1 * e4m3 * s) of the
  * rows' places, for instance a sequence's cached context for h3fp4_cross_attn or
- * h3fp4_shared_attn.  Rows without a place are left as they are. */
+ * h3fp4_shared_attn.  Rows without a place are left as they are.  k and v may lie between
+ * one another, as views of one buffer with the same strides do, and overlap nothing. */
 H3FP4_API h3fp4_status h3fp4_cache_read(const h3fp4_heads* k, const h3fp4_heads* v, int64_t M,
                                         const h3fp4_cache* cache, cudaStream_t stream);
 
@@ -566,7 +568,8 @@ H3FP4_API h3fp4_status h3fp4_cache_read(const h3fp4_heads* k, const h3fp4_heads*
  *   A row without a key gives out = 0 and lse = -inf; one whose largest score
  *   scale * log2(e) * (q . k) is beyond 3e38 either way is NaN.
  *   scale > 0, scale * log2(e) finite.  lse: fp32 [M][Hq], 4-byte aligned, or NULL.
- *   flags: H3FP4_CAUSAL.  out may not overlap q.
+ *   flags: H3FP4_CAUSAL.  out, lse and ws overlap nothing (q and out may be views of one
+ *      buffer with the same strides that lie between one another).
  *   ws: device workspace of h3fp4_cache_attn_workspace_bytes(dim) bytes (ws_bytes is
  *      checked), first 256 bytes zeroed once before first use; h3fp4_check(ws) reports
  *      device waits that timed out.  Concurrent calls must not share one workspace. */
