@@ -140,6 +140,13 @@ h3fp4_status h3fp4_block_norm(const void* x, const void* y, int64_t M, int64_t K
     BlockNormJob job{};
     h3fp4_status st = make_segments(seg_off, seg_off == nullptr && nseg <= 0 ? 1 : nseg, M, &job.seg);
     if (st != H3FP4_OK) return st;
+    for (const float* v : {y_weight, gate, weight, shift, scale}) {
+        const uint64_t vec = 4 * (uint64_t)job.seg.nseg * (uint64_t)K;
+        if (overlap(x_out, (uint64_t)bytes, v, vec) || overlap(out, (uint64_t)bytes, v, vec) || overlap(out_amax, 4, v, vec))
+            return H3FP4_ERR_INVALID;
+    }
+    for (const void* o : {x, y, static_cast<const void*>(x_out), static_cast<const void*>(out)})
+        if (overlap(out_amax, 4, o, (uint64_t)bytes)) return H3FP4_ERR_INVALID;
     if ((st = check_device()) != H3FP4_OK) return st;
     job.x = static_cast<const __nv_bfloat16*>(x);
     job.y = static_cast<const __nv_bfloat16*>(y);
@@ -191,7 +198,7 @@ h3fp4_status h3fp4_linear_rows(const void* x, int64_t M, int64_t N, int64_t K, c
     const struct {
         const void* p;
         int64_t bytes;
-    } read[] = {{x, M * K * 2}, {w_codes, N * K / 2}, {w_sf, (N + 127) / 128 * 128 * K / 16}, {bias, N * 2},
+    } read[] = {{w_gscale, 4}, {x, M * K * 2}, {w_codes, N * K / 2}, {w_sf, (N + 127) / 128 * 128 * K / 16}, {bias, N * 2},
                 {gate, ((M - 1) * gate_stride + N) * 4}};
     for (const auto& r : read)
         if (overlap(out, outs, r.p, (uint64_t)r.bytes) || overlap(ws, need, r.p, (uint64_t)r.bytes))
