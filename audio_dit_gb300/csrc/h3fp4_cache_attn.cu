@@ -408,11 +408,13 @@ __device__ __forceinline__ void nan_values(State<W, kCols>& st, const uint8_t* g
         }
 }
 
+constexpr uint32_t kSawNan = 1u << 31;   // a masked step left out blocks of V that are NaN
+
 // O += P V of one group, token pairs 8 half + 2 c + (0, 1).  kMasked: `left` tokens of it hold anything; blocks that
 // are NaN count as zeros and are reported.
 template <int W, int kCols, bool kMasked>
 __device__ __forceinline__ void values(State<W, kCols>& st, const uint8_t* gp, int lane, const uint32_t (&pf)[kCols / 4], int left,
-                                       bool& nan)
+                                       uint32_t& flags)
 {
     using L = CacheLayout<W>;
     const int g = lane >> 2, c = lane & 3;
@@ -441,7 +443,7 @@ __device__ __forceinline__ void values(State<W, kCols>& st, const uint8_t* gp, i
             for (int b = 0; b < kVBlocks; ++b) {
                 const uint32_t v = vs[half][b] & 0x7FFF7FFFu;
                 const uint32_t bad = (v & 0xFFFFu) > 0x7C00u ? 0xFFFFu : 0u, bad2 = v > 0x7C00FFFFu ? 0xFFFF0000u : 0u;
-                nan |= (bad | bad2) != 0;
+                if (bad | bad2) flags |= kSawNan;
                 vs[half][b] &= ~(bad | bad2);
             }
     }
@@ -485,7 +487,8 @@ __device__ __forceinline__ void values(State<W, kCols>& st, const uint8_t* gp, i
 // attended to by the lane's two columns; scores that leave fp32's range downwards stay finite.
 template <int W, int kCols, bool kMasked>
 __device__ __forceinline__ void step(State<W, kCols>& st, const uint8_t* gp, int lane, const uint32_t (&qf)[W / 16][kCols / 4],
-                                     const float (&factor)[2], const int (&left)[2], const int (&lim)[2][2], bool& nan)
+                                     const float (&factor)[2], const int (&left)[2], const int (&lim)[2][2],
+                                     uint32_t& flags)
 {
     constexpr int kF = kCols / 8;   // fragments of four scores a group
     const int g = lane >> 2, c = lane & 3;
@@ -541,7 +544,7 @@ __device__ __forceinline__ void step(State<W, kCols>& st, const uint8_t* gp, int
             for (int h = 0; h < 2; ++h)
                 asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %0;" : "+r"(pf[h]));
         }
-        values<W, kCols, kMasked>(st, gp + e * CacheLayout<W>::kGroupBytes, lane, pf, left[e], nan);
+        values<W, kCols, kMasked>(st, gp + e * CacheLayout<W>::kGroupBytes, lane, pf, left[e], flags);
     }
 }
 
@@ -745,7 +748,7 @@ __global__ void __launch_bounds__(kThreads, Config<W, kCols>::kCtasPerSm)
             if (ok) where = p.c.pool + (((long long)pg * p.c.Hkv + h) * per_page + gi % per_page) * L::kGroupBytes;
             has = __ballot_sync(0xffffffffu, ok);
         };
-        uint32_t there = 0;   // which groups of the slots exist, two bits each
+        uint32_t there = 0;   // which groups of the slots exist, two bits each, and kSawNan
         auto load = [&](int i, int slot) {
             if ((i & 15) == 0) look(i);
             const int first = 2 * (i & 15);
@@ -805,7 +808,6 @@ __global__ void __launch_bounds__(kThreads, Config<W, kCols>::kCtasPerSm)
         const int whole_steps = max(0, least / kStep - g0);
         const int plain = tame ? min(n, solo ? whole_steps : (whole_steps + kWarps - 1) / kWarps) : 0;
         int slot = 0;
-        bool nan = false;   // a masked step left out blocks of V that are NaN
 #pragma unroll 1
         for (int i = 0; i < n; ++i) {
             {
@@ -825,7 +827,7 @@ __global__ void __launch_bounds__(kThreads, Config<W, kCols>::kCtasPerSm)
                 const uint8_t* gp = ring + slot * C::kSlot;
                 if (i < plain && two == 3u) {
                     const int left[2] = {kCacheGroup, kCacheGroup}, lim[2][2] = {};
-                    step<W, kCols, false>(st, gp, lane, qf, factor, left, lim, nan);
+                    step<W, kCols, false>(st, gp, lane, qf, factor, left, lim, there);
                 } else if (two) {
                     const int first = (g0 + every * i) * kStep;
                     int left[2], lim[2][2];
@@ -836,7 +838,7 @@ __global__ void __launch_bounds__(kThreads, Config<W, kCols>::kCtasPerSm)
                         lim[e][0] = here ? mylim[0] - first - e * kCacheGroup : 0;
                         lim[e][1] = here ? mylim[1] - first - e * kCacheGroup : 0;
                     }
-                    step<W, kCols, true>(st, gp, lane, qf, factor, left, lim, nan);
+                    step<W, kCols, true>(st, gp, lane, qf, factor, left, lim, there);
                 }
                 // (the products that used the slot's last bytes have been issued, so these were read)
                 __syncwarp();
@@ -849,7 +851,7 @@ __global__ void __launch_bounds__(kThreads, Config<W, kCols>::kCtasPerSm)
         }
         __syncwarp();
         // blocks of V that are NaN, for the columns that see their tokens (looked for again in the pool: hardly ever)
-        if (__any_sync(0xffffffffu, nan))
+        if (__any_sync(0xffffffffu, (there & kSawNan) != 0))
 #pragma unroll 1
             for (int k = 0; k < 2 * n; ++k) {
                 const int gi = 2 * (g0 + every * (k >> 1)) + (k & 1);
