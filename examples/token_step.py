@@ -1,7 +1,7 @@
 """A stream that is generated token by token: one block's step with its weights and its cache in four bits.
 
-Prompts go through the block first (many rows: the quantised linear, and their keys and values into the cache); then every
-step takes one token of each sequence through
+The keys and values of the prompts are made and stored first (many rows: the quantised linear; nothing else of a single block
+needs them), then every step takes one token of each sequence through
 
     h     = norm of x before the attention                          h3fp4_block_norm
     qkv   = linear of the few rows, activations as they are         h3fp4_linear_rows

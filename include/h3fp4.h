@@ -475,7 +475,8 @@ H3FP4_API h3fp4_status h3fp4_block_norm(const void* x_bf16, const void* y_bf16, 
  *     out = bf16(R + g * (s_w * (x . W_q^T) + b))  or  bf16(s_w * (x . W_q^T) + b)
  * ("H3 Blackwell Runtime" README, "Checkpoints": pre-quantised weights).  Sums are fp32; x
  * enters with an error of at most 2^-22 of the largest magnitude of its block of 16, or 2^-40
- * of its row's.
+ * of its row's.  The same call gives the same bits; how the sums of a row are divided depends
+ * on how many rows come with it, so its last bits may differ between calls of other M.
  *   x: bf16 [M][K] (a row with an infinity or a NaN gives NaN), 1 <= M <= H3FP4_ROWS_MAX; K % 64 == 0, K <= 2^16; N % 8 == 0,
  *      N <= 2^24.
  *   w_codes, w_sf, w_gscale: output of h3fp4_quantize_weight.
@@ -559,8 +560,11 @@ H3FP4_API h3fp4_status h3fp4_cache_read(const h3fp4_heads* k, const h3fp4_heads*
  * over all positions j of the row's sequence, with H3FP4_CAUSAL over those up to the
  * row's own; kv head h / (Hq / heads) for query head h.  q, out: [M][Hq][dim], Hq %
  * heads == 0, M * Hq < 2^31.  Made for few rows per sequence (single tokens): the cache is
- * read once per 16 columns (rows * Hq / heads); many rows are right, but h3fp4_cache_read
- * and h3fp4_cross_attn are faster for them.
+ * read once per 16 columns (rows * Hq / heads).  Many rows are right, but take longer than
+ * h3fp4_cache_read and h3fp4_cross_attn do where these can take their place: without
+ * H3FP4_CAUSAL (h3fp4_cross_attn has no causal order), to dim 128.  One sequence of 32768
+ * tokens, 32 heads over 8 of 128: 16 rows 51 us against 72, 64 rows 148 against 79, 1024 rows
+ * 2065 against 384.
  *   Scores, statistics and sums are fp32; keys and values enter as they are held, q
  *   unrounded (elements below 2^-31 of the largest of their row and head are rounded),
  *   the p_j rounded to fp16 for their product with V.
